@@ -318,6 +318,7 @@ class _Pool:
         out = []
         for ptr in self.pk.kv_pool_ptrs(self.handle):
             raw = Raw()
+            raw.pool = self  # the tensors keep the pool
             raw.__cuda_array_interface__ = dict(shape=shape, typestr="<f4" if dtype == torch.float32 else "<i2",
                                                 data=(ptr, False), version=3, strides=None)
             out.append(torch.as_tensor(raw, device="cuda").view(dtype))
