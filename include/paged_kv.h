@@ -42,6 +42,8 @@
  *   - Element types: KV_F32 (IEEE fp32), KV_BF16 (bfloat16) or KV_F16 (IEEE
  *     half precision).  q, k_new and v_new use the pool's type; out may be
  *     KV_F32 or the pool's type.  The cascade decode takes bf16 or fp16 pools.
+ *     A KV_I4 pool stores 4-bit codes with shared scales (see "4-bit pools");
+ *     the calls that read or write one say what type their rows have.
  *   - head_dim must be 64 or 128, block_size must be 16, num_q_heads must be
  *     a multiple of num_kv_heads with num_q_heads / num_kv_heads <= 8.
  *
@@ -72,8 +74,9 @@ typedef enum {
     KV_ERR_STATE = -7           /* call not valid in the object's current state */
 } kv_status;
 
-/* Element types: IEEE fp32, bfloat16, IEEE half precision (binary16). */
-typedef enum { KV_F32 = 0, KV_BF16 = 1, KV_F16 = 2 } kv_dtype;
+/* Element types: IEEE fp32, bfloat16, IEEE half precision (binary16); pools
+ * only: 4-bit codes with an e4m3 scale per 16 dimensions. */
+typedef enum { KV_F32 = 0, KV_BF16 = 1, KV_F16 = 2, KV_I4 = 3 } kv_dtype;
 
 /* Bits of the device error word. */
 #define KV_DEVERR_BLOCK_RANGE 0x1   /* block-table entry outside [0, num_blocks) */
@@ -83,6 +86,8 @@ typedef enum { KV_F32 = 0, KV_BF16 = 1, KV_F16 = 2 } kv_dtype;
 #define KV_DEVERR_VALUE_RANGE 0x10  /* prefill: a V value of a key below the sequence length
                                        with |v| >= 65536 or infinite; the PV product, run on
                                        fp16 operands, used +-65504 in its place */
+
+#define KV_DEVERR_POSITION 0x20     /* kv_append_rope: position outside [0, max_position) */
 
 /* Default time limit of a pipeline wait inside a kernel (nanoseconds). */
 #define KV_WAIT_LIMIT_DEFAULT_NS 2000000000ull
@@ -278,6 +283,53 @@ kv_status kv_cow_if_shared(kv_pool_t p, int32_t *block_id_inout, int *copied, vo
 kv_status kv_append(kv_pool_t p, const void *k_new, const void *v_new,
                     const int64_t *slot_mapping, int num_tokens, void *stream);
 
+/* Append with the position rotation ("PagedAttention Nedir?", "Nasil
+ * Calisir?" steps 1-3; the pages give no position encoding: the rotation is
+ * this library's packaging of the step before the append).  For token t with
+ * position pos = positions[t], the first rot_dim dimensions of every q and k head
+ * are rotated in pairs, y1 = x1 cos - x2 sin, y2 = x2 cos + x1 sin, and the k and
+ * v rows go to pool slot slot_mapping[t]; q goes to q_out.
+ *   k_new, v_new  device rows of type in_dtype, token t's num_kv_heads *
+ *                 head_dim elements from t * k_stride / v_stride on (elements; 0
+ *                 = packed), so that k and v may be slices of one projection;
+ *   in_dtype      the pool's type; for a KV_I4 pool KV_F32, KV_BF16 or KV_F16;
+ *   slot_mapping  device int64[num_tokens], as kv_append: a negative slot stores
+ *                 no k and v (q is rotated all the same), one past the pool is
+ *                 skipped and sets KV_DEVERR_SLOT_RANGE.  Two tokens naming the
+ *                 same slot: its contents are unspecified;
+ *   positions     device int32[num_tokens]; one outside [0, max_position) leaves
+ *                 the whole token out (its q_out row stays as it was) and sets
+ *                 KV_DEVERR_POSITION;
+ *   cos_sin       device fp32 [max_position][rot_dim]: for each position the
+ *                 rot_dim / 2 cosines of its pairs, then their sines;
+ *   rot_dim       rotated dimensions, a multiple of 16 up to head_dim; 0: no
+ *                 rotation (positions, cos_sin unused, q must be NULL): a plain
+ *                 append, the one that writes a KV_I4 pool;
+ *   interleaved   0: pair j is dimensions (j, j + rot_dim / 2); 1: (2j, 2j + 1);
+ *   q, q_out      device rows of num_q_heads * head_dim elements of in_dtype
+ *                 from t * q_stride / q_out_stride on (0 = packed), or NULL for
+ *                 none.  q_out may be q itself (same stride; 0 takes q's).
+ * Rotated in fp32 (two products and a sum, each rounded) and rounded once; what
+ * is not rotated is moved bit by bit.  Addresses and strides: multiples of 16
+ * bytes.  KV_ERR_ARG for a wrong size, stride, alignment, type or NULL pointer,
+ * KV_ERR_UNSUPPORTED for an in_dtype that no pool takes. */
+kv_status kv_append_rope(kv_pool_t p, const void *k_new, const void *v_new, kv_dtype in_dtype,
+                         int64_t k_stride, int64_t v_stride, const int64_t *slot_mapping,
+                         const int32_t *positions, const float *cos_sin, int max_position,
+                         int rot_dim, int interleaved, const void *q, void *q_out,
+                         int64_t q_stride, int64_t q_out_stride, int num_q_heads, int num_tokens,
+                         void *stream);
+
+/* Cached tokens as rows, the way back from an append: k_out and v_out (device
+ * [num_tokens][num_kv_heads][head_dim] of out_dtype, 16-byte aligned) receive the K
+ * and V rows of slot slots[t] (device int64).  A negative slot leaves its rows as
+ * they were; one past the pool does too and sets KV_DEVERR_SLOT_RANGE.  out_dtype:
+ * the pool's type (bits are moved); for a KV_I4 pool KV_F32, KV_BF16 or KV_F16 (the
+ * values its codes stand for, rounded once where the type cannot hold them: 16-bit
+ * types hold all of them while the pool's scales keep them in range). */
+kv_status kv_read_tokens(kv_pool_t p, const int64_t *slots, int num_tokens, void *k_out,
+                         void *v_out, kv_dtype out_dtype, void *stream);
+
 /* Copy-on-write block copies: for i < n, every head and slot of K and V of
  * block src[i] is copied to block dst[i] (device int32 arrays).  Pairs must
  * not overlap (no dst is another pair's src).  Out-of-range ids are skipped
@@ -300,6 +352,60 @@ kv_status kv_swap_out(kv_pool_t p, const int32_t *block_ids, int n, void *host_b
 kv_status kv_swap_in(kv_pool_t p, const int32_t *block_ids, int n, const void *host_buf,
                      void *stream);
 kv_status kv_swap_bytes(kv_pool_t p, int n, size_t *bytes);
+
+/* ----------------------------------------------------------------------
+ * 4-bit pools (kv_pool_create with KV_I4).  Sixteen consecutive dimensions of
+ * one (token, kv head) share an e4m3 scale s and hold integer codes c in -7..7;
+ * they stand for c * s * g, g the pool's scale of K or V: 4.5 bits a value, a
+ * 3.6th of a 16-bit pool's bytes.  s is the e4m3 nearest to max|x| / (7 g), at
+ * most 448, c the integer nearest to x / (s g); ties to even.  A NaN makes its
+ * group NaN; magnitudes past 3136 g and infinities become 3136 g.
+ *
+ * kv_append_rope writes such a pool, kv_read_tokens reads it back,
+ * paged_decode_attention_i4 and paged_prefill_attention_i4 attend over it; block
+ * management, kv_copy_blocks, kv_cow_if_shared and the swap calls move its blocks
+ * as they move others.  kv_append and the other attention calls return
+ * KV_ERR_UNSUPPORTED for it.  kv_pool_ptrs' arrays hold one tile of 9 * head_dim
+ * bytes per (block, kv head): codes, then scales.
+ * -------------------------------------------------------------------- */
+
+/* The pool's scales g of K and V: powers of two from 2^-32 to 2^32 (scaling by
+ * them never rounds), 1 at first.  Set them before the first append: what is
+ * stored is not converted.  Host only.  KV_ERR_UNSUPPORTED for other pools. */
+kv_status kv_pool_set_i4_scales(kv_pool_t p, float k_scale, float v_scale);
+
+/* num_splits for paged_decode_attention_i4 from the host-known lengths, as
+ * kv_decode_plan chooses it for 16-bit pools. */
+kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_heads,
+                            int max_blocks, int *num_splits);
+
+/* paged_decode_attention over a KV_I4 pool.  q is of type q_dtype (KV_BF16 or
+ * KV_F16), out of q_dtype or KV_F32; seq_order as in paged_append_and_decode or
+ * NULL; the workspace is kv_decode_workspace_size bytes for the same num_splits.
+ * K and V enter the tensor cores exactly (fp16 holds every c * s); q enters in
+ * fp16, scaled per head by a power of two (exact but for elements below 2^-27 of
+ * the head's largest); the softmax weights in fp16, with KV_F32 output in two fp16
+ * parts (about 22 bits). */
+kv_status paged_decode_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype,
+                                    const int32_t *block_tables, int max_blocks,
+                                    const int32_t *seq_lens, const int32_t *seq_order, int batch,
+                                    int num_q_heads, float scale, void *out, kv_dtype out_dtype,
+                                    float *lse_out, int num_splits, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/* paged_prefill_attention over a KV_I4 pool (head_dim 128, q of type q_dtype
+ * KV_BF16 or KV_F16, out of q_dtype or KV_F32).  The blocks of the batch are
+ * first expanded to 16-bit tiles in the workspace (16-byte aligned,
+ * kv_prefill_i4_workspace_size bytes for the same sizes), once for all their
+ * query tiles and heads. */
+kv_status kv_prefill_i4_workspace_size(kv_pool_t p, int batch, int num_q_heads, int max_blocks,
+                                       int max_q_len, size_t *bytes);
+kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype,
+                                     const int32_t *cu_q, int total_q, int max_q_len,
+                                     const int32_t *block_tables, int max_blocks,
+                                     const int32_t *seq_lens, int batch, int num_q_heads,
+                                     float scale, void *out, kv_dtype out_dtype, float *lse_out,
+                                     void *workspace, size_t workspace_bytes, void *stream);
 
 /* Scratch memory the decode call needs for a split plan: partial outputs
  * fp32 [batch][num_q_heads][splits][head_dim] and their log-sum-exp

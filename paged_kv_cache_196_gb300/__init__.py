@@ -15,7 +15,7 @@ import os
 from . import build as _build
 
 __all__ = [
-    "KVError", "lib", "KV_F32", "KV_BF16", "KV_F16", "kv_status_string", "kv_last_cuda_error", "kv_blocks_for_tokens",
+    "KVError", "lib", "KV_F32", "KV_BF16", "KV_F16", "KV_I4", "kv_status_string", "kv_last_cuda_error", "kv_blocks_for_tokens",
     "kv_allocator_create", "kv_allocator_destroy", "kv_allocator_set_order",
     "kv_allocator_alloc", "kv_allocator_share", "kv_allocator_free", "kv_allocator_refcount",
     "kv_allocator_num_free", "kv_prepare_append", "kv_prepare_append_batch",
@@ -32,11 +32,14 @@ __all__ = [
     "kv_contig_ptrs", "kv_contig_stats", "kv_contig_page_pool", "kv_contig_page_stats", "kv_contig_append", "contig_decode_attention",
     "contig_append_and_decode", "kv_contig_get_device_error", "kv_debug_set_wait_limit_ns", "kv_debug_fail_page_create",
     "KV_WAIT_LIMIT_DEFAULT_NS",
+    "kv_append_rope", "kv_read_tokens", "kv_pool_set_i4_scales", "kv_decode_plan_i4", "paged_decode_attention_i4",
+    "kv_prefill_i4_workspace_size", "paged_prefill_attention_i4",
 ]
 
 KV_F32 = 0
 KV_BF16 = 1
 KV_F16 = 2
+KV_I4 = 3
 KV_WAIT_LIMIT_DEFAULT_NS = 2000000000
 
 STATUS = {0: "KV_OK", -1: "KV_ERR_ARG", -2: "KV_ERR_OOM", -3: "KV_ERR_UNSUPPORTED",
@@ -114,6 +117,16 @@ _SIGS = {
                                        _sz, _vp],
     "paged_prefill_attention": [_vp, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _i32, _f32, _vp,
                                 _i32, _vp, _vp],
+    "kv_append_rope": [_vp, _vp, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _i64, _i64,
+                       _i32, _i32, _vp],
+    "kv_read_tokens": [_vp, _vp, _i32, _vp, _vp, _i32, _vp],
+    "kv_pool_set_i4_scales": [_vp, _f32, _f32],
+    "kv_decode_plan_i4": [_vp, _i32, _i32, _i32, _P(_i32)],
+    "paged_decode_attention_i4": [_vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _f32, _vp, _i32, _vp, _i32,
+                                  _vp, _sz, _vp],
+    "kv_prefill_i4_workspace_size": [_vp, _i32, _i32, _i32, _i32, _P(_sz)],
+    "paged_prefill_attention_i4": [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _i32, _f32, _vp, _i32,
+                                   _vp, _vp, _sz, _vp],
     "kv_get_device_error": [_vp, _P(_i32), _vp],
     "kv_contig_create": [_i32, _i32, _i32, _i32, _i32, _P(_vp)],
     "kv_contig_destroy": [_vp],
@@ -377,6 +390,30 @@ def kv_append(p: int, k_new, v_new, slot_mapping, num_tokens: int, stream=None):
                            _stream(stream)), "kv_append")
 
 
+def kv_append_rope(p: int, k_new, v_new, in_dtype: int, slot_mapping, num_tokens: int, k_stride: int = 0,
+                   v_stride: int = 0, positions=None, cos_sin=None, max_position: int = 0, rot_dim: int = 0,
+                   interleaved: bool = False, q=None, q_out=None, num_q_heads: int = 0, q_stride: int = 0,
+                   q_out_stride: int = 0, stream=None):
+    """Rotates q and k by their positions, writes q_out and stores k and v in
+    their slots (quantised for a KV_I4 pool); rot_dim = 0: a plain append.
+    Strides in elements between tokens, 0 = packed.  See the C header."""
+    _check(lib().kv_append_rope(p, _ptr(k_new), _ptr(v_new), in_dtype, k_stride, v_stride, _ptr(slot_mapping),
+                                _ptr(positions), _ptr(cos_sin), max_position, rot_dim, 1 if interleaved else 0,
+                                _ptr(q), _ptr(q_out), q_stride, q_out_stride, num_q_heads, num_tokens,
+                                _stream(stream)), "kv_append_rope")
+
+
+def kv_read_tokens(p: int, slots, num_tokens: int, k_out, v_out, out_dtype: int, stream=None):
+    """K and V rows of the given slots (int64) as [num_tokens][Hkv][D] of out_dtype."""
+    _check(lib().kv_read_tokens(p, _ptr(slots), num_tokens, _ptr(k_out), _ptr(v_out), out_dtype, _stream(stream)),
+           "kv_read_tokens")
+
+
+def kv_pool_set_i4_scales(p: int, k_scale: float, v_scale: float):
+    """Power-of-two scales of a KV_I4 pool's K and V."""
+    _check(lib().kv_pool_set_i4_scales(p, k_scale, v_scale), "kv_pool_set_i4_scales")
+
+
 def kv_copy_blocks(p: int, src, dst, n: int, stream=None):
     _check(lib().kv_copy_blocks(p, _ptr(src), _ptr(dst), n, _stream(stream)), "kv_copy_blocks")
 
@@ -571,6 +608,45 @@ def paged_prefill_attention(p: int, q, cu_q, total_q: int, max_q_len: int, block
                                          num_q_heads, scale, _ptr(out), out_dtype, _ptr(lse_out),
                                          _stream(stream)),
            "paged_prefill_attention")
+
+
+def kv_decode_plan_i4(host_seq_lens, num_kv_heads: int, max_blocks: int) -> int:
+    """num_splits of paged_decode_attention_i4 for these (host, int32) lengths."""
+    import numpy as _np
+    lens = _np.ascontiguousarray(host_seq_lens, dtype=_np.int32)
+    r = _i32()
+    _check(lib().kv_decode_plan_i4(_ptr(lens), len(lens), num_kv_heads, max_blocks, ctypes.byref(r)),
+           "kv_decode_plan_i4")
+    return r.value
+
+
+def paged_decode_attention_i4(p: int, q, q_dtype: int, block_tables, max_blocks: int, seq_lens, batch: int,
+                              num_q_heads: int, scale: float, out, out_dtype: int, lse_out=None,
+                              num_splits: int = 0, workspace=None, workspace_bytes: int = 0, stream=None,
+                              seq_order=None):
+    """paged_decode_attention over a KV_I4 pool; q of q_dtype (KV_BF16 or KV_F16)."""
+    _check(lib().paged_decode_attention_i4(p, _ptr(q), q_dtype, _ptr(block_tables), max_blocks, _ptr(seq_lens),
+                                           _ptr(seq_order), batch, num_q_heads, scale, _ptr(out), out_dtype,
+                                           _ptr(lse_out), num_splits, _ptr(workspace), workspace_bytes,
+                                           _stream(stream)), "paged_decode_attention_i4")
+
+
+def kv_prefill_i4_workspace_size(p: int, batch: int, num_q_heads: int, max_blocks: int, max_q_len: int) -> int:
+    r = _sz()
+    _check(lib().kv_prefill_i4_workspace_size(p, batch, num_q_heads, max_blocks, max_q_len, ctypes.byref(r)),
+           "kv_prefill_i4_workspace_size")
+    return r.value
+
+
+def paged_prefill_attention_i4(p: int, q, q_dtype: int, cu_q, total_q: int, max_q_len: int, block_tables,
+                               max_blocks: int, seq_lens, batch: int, num_q_heads: int, scale: float, out,
+                               out_dtype: int, lse_out=None, workspace=None, workspace_bytes: int = 0,
+                               stream=None):
+    """paged_prefill_attention over a KV_I4 pool; see the C header."""
+    _check(lib().paged_prefill_attention_i4(p, _ptr(q), q_dtype, _ptr(cu_q), total_q, max_q_len,
+                                            _ptr(block_tables), max_blocks, _ptr(seq_lens), batch, num_q_heads,
+                                            scale, _ptr(out), out_dtype, _ptr(lse_out), _ptr(workspace),
+                                            workspace_bytes, _stream(stream)), "paged_prefill_attention_i4")
 
 
 def kv_get_device_error(p: int, stream=None) -> int:

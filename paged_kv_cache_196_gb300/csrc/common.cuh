@@ -198,4 +198,20 @@ KV_DEVICE void store_out(void *out, size_t idx, float v, int out_type) {
         reinterpret_cast<uint16_t *>(out)[idx] = float_to_f16_rn(v);
 }
 
+// Four consecutive elements (idx a multiple of 4) as store_out, in one store.
+KV_DEVICE void store_out4(void *out, size_t idx, float4 v, int out_type) {
+    if (out_type == KV_F32) {
+        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + idx) = v;
+        return;
+    }
+    uint2 w;
+    if (out_type == KV_BF16)
+        w = make_uint2(float_to_bf16_rn(v.x) | (uint32_t)float_to_bf16_rn(v.y) << 16,
+                       float_to_bf16_rn(v.z) | (uint32_t)float_to_bf16_rn(v.w) << 16);
+    else
+        w = make_uint2(float_to_f16_rn(v.x) | (uint32_t)float_to_f16_rn(v.y) << 16,
+                       float_to_f16_rn(v.z) | (uint32_t)float_to_f16_rn(v.w) << 16);
+    *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(out) + idx) = w;
+}
+
 }  // namespace pkv

@@ -1497,6 +1497,7 @@ static kv_status launch_cc(kv_dtype dt, bool linear, int G, const DecodeKParams 
 }
 
 kv_status launch_decode(const DecodeArgs &a, bool linear) {
+    if (a.dtype == KV_I4) return KV_ERR_UNSUPPORTED;  // paged_decode_attention_i4
     if (a.batch < 0 || a.num_q_heads <= 0 || a.num_kv_heads <= 0) return KV_ERR_ARG;
     if (a.num_q_heads % a.num_kv_heads) return KV_ERR_ARG;
     const int g = a.num_q_heads / a.num_kv_heads;
@@ -2026,7 +2027,7 @@ kv_status paged_decode_attention_scheduled(kv_pool_t p, const void *q, const voi
     if (k_new && (!v_new || !slot_mapping)) return KV_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15)
         return KV_ERR_ARG;
-    if (p->dtype == KV_F32 || p->head_dim != 128) return KV_ERR_UNSUPPORTED;
+    if (p->dtype == KV_F32 || p->dtype == KV_I4 || p->head_dim != 128) return KV_ERR_UNSUPPORTED;
     if (kv_status st = pool_tensor_maps(p)) return st;
     DecodeArgs a{};
     a.q = q;

@@ -1,0 +1,772 @@
+// Decode attention over a 4-bit pool, and its form for a few query tokens.
+//
+// Maths: o = softmax(scale * q K^T) V per query head, K and V as their codes
+// stand for them (i4.cuh), with a running maximum and sum over the blocks and a
+// log-sum-exp merge of the partitions of one sequence, as the 16-bit decode.
+//
+// What bounds it.  A token's K and V take 9 D / 8 bytes per kv head against 4 D
+// in 16 bits, while every code still has to become an fp16 operand.  So the
+// kernel is written around the number of instructions per code: one logical
+// operation and one fused multiply-add make two codes into a scaled fp16 pair
+// (i4::values8: 10 instructions for 8 codes), the layout of a tile puts each
+// lane's operands of the tensor core's fragments into consecutive bytes (no
+// ldmatrix, no shuffles), and the scales of a lane's rows are two bytes a load.
+//
+// Shape.  One CTA = a run of blocks of one (sequence, kv head) for all its query
+// columns (head of the group, and query token where there are several); four
+// warps, warp w takes blocks w, w + 4, ... and keeps its own softmax state.  Each
+// warp feeds itself: lane 0 issues the two bulk copies of a tile into the warp's
+// own ring, and issues the next one into a stage as soon as the warp has it in
+// registers.  No producer warp, no barrier between warps before the end.
+//
+// Products.  S^T[16 tokens][8 columns] = K q^T and O^T[16 dims][8 columns] += V^T
+// P^T on mma.sync m16n8k16 with fp32 sums.  The contraction over dimensions may run
+// in any order, so lane (r, c) = (lane / 4, lane % 4) takes a quarter row of tokens
+// r and r + 8 as it lies in memory, and q is laid out to match once per CTA.  O's
+// rows are dimensions D/8 r + 2 f and + 1 of product f: each lane ends with D / 8
+// consecutive dimensions of two columns.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <vector>
+
+#include "common.cuh"
+#include "i4.cuh"
+#include "internal.h"
+#include "i4_attend.h"
+
+namespace pkv {
+
+constexpr int kI4Warps = 4;
+constexpr int kI4Threads = kI4Warps * 32;
+constexpr int kI4Stages = 4;   // ring stages of one warp (a power of two)
+constexpr int kI4BS = 16;
+// The weights are 2^(s - m + 10): at most 1024, so that fp16 keeps 10 more
+// binary places of the small ones before they become subnormal.
+constexpr float kI4Bias = 10.f;
+
+struct I4Params {
+    const uint16_t *q;      // rows [hq][D], bf16 or fp16
+    int q_bf16;
+    const int32_t *cu_q;    // null: one query token per sequence, row b
+    int total_q, max_t;     // rows of q and out; most query tokens of a sequence
+    const char *k_pool, *v_pool;
+    const int32_t *tables;
+    int max_blocks, num_blocks;
+    const int32_t *seq_lens, *seq_order;
+    int batch, hq, hkv, g;
+    float scale_log2;       // softmax scale * log2(e) * 4 * the pool's K scale
+    float v_mul;            // 4 * the pool's V scale
+    int part_blocks, max_splits;
+    int col_groups;         // CTAs that share a partition's columns
+    void *out;
+    int out_type;
+    float *lse;
+    float *ws_o, *ws_lse;   // [b][query token][hq][max_splits] partial results and their lse
+    int *counters;          // null: merge_i4_kernel merges
+    int *err;
+};
+
+KV_DEVICE float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Whether a phase is complete, without the suspension of mbarrier.try_wait.
+KV_DEVICE bool phase_done(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+KV_DEVICE void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8x8 transpose of a 16-bit fragment.
+KV_DEVICE uint32_t transpose8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+KV_DEVICE uint32_t half_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two e4m3 scales of a tile, a quarter of their value, as an fp16 pair.
+KV_DEVICE __half2 quarter_scales(uint32_t two) {
+    return __hmul2(i4::e4m3x2_to_half2(two), __float2half2_rn(0.25f));
+}
+
+// N words of shared memory, 16 or 8 bytes at once.
+template <int N>
+KV_DEVICE void load_words(const char *src, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(src);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(src);
+        w[0] = u.x, w[1] = u.y;
+    }
+}
+
+template <int D>
+constexpr size_t i4_ring_bytes() {
+    const size_t ring = (size_t)kI4Warps * kI4Stages * 2 * 9 * D;
+    const size_t merge = (size_t)kI4Warps * 8 * D * 4 + 4096;
+    return ((ring > merge ? ring : merge) + 127) / 128 * 128;
+}
+template <int D>
+constexpr size_t i4_smem_bytes() {
+    return i4_ring_bytes<D>() + (size_t)kI4Warps * kI4Stages * (sizeof(uint64_t) + sizeof(int));
+}
+
+// The sequence of a CTA: rows of its queries, keys, partition.  False: nothing to do.
+struct I4Work {
+    int b, q0, T, nblk, blk0, nloc, nsplit;
+    long long L;
+};
+
+// Row of a query head in q and out, and in the workspace.
+KV_DEVICE size_t out_row(const I4Params &p, const I4Work &w, int tq, int hq) { return (size_t)(w.q0 + tq) * p.hq + hq; }
+KV_DEVICE size_t ws_row(const I4Params &p, const I4Work &w, int tq, int hq) {
+    return ((size_t)w.b * p.max_t + tq) * p.hq + hq;
+}
+
+KV_DEVICE bool i4_sequence(const I4Params &p, int b, bool report, I4Work &w) {
+    w.b = b;
+    long long L = p.seq_lens[b];
+    const long long most = (long long)p.max_blocks * kI4BS;
+    if (p.cu_q) {
+        w.q0 = p.cu_q[b];
+        w.T = p.cu_q[b + 1] - w.q0;
+        if (w.T <= 0) return false;
+        if (L < w.T || L > most || w.T > p.max_t || w.q0 < 0 || (long long)w.q0 + w.T > p.total_q) {
+            if (report) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
+            return false;
+        }
+    } else {
+        w.q0 = b;
+        w.T = 1;
+        if (L > most) {
+            if (report) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
+            L = most;
+        }
+        if (L < 0) L = 0;
+    }
+    w.L = L;
+    w.nblk = (int)((L + kI4BS - 1) / kI4BS);
+    w.nsplit = max(1, (w.nblk + p.part_blocks - 1) / p.part_blocks);
+    return true;
+}
+
+// D: head dim.  NT: columns / 8 of a CTA.  EXACT: weights in two fp16 parts (fp32
+// output).  TW: waits read their limit at run time (tests).
+template <int D, int NT, bool EXACT, bool TW, int MINB>
+__global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Params p) {
+    constexpr int kTile = 9 * D;
+    constexpr int kW = D / 32;        // words of a quarter row of K, of a lane's dims of a V pair
+    constexpr int kSteps = D / 16;    // products along D
+    constexpr int kNst = kI4Stages;
+    const int split = blockIdx.x, h = blockIdx.y;
+    int b = blockIdx.z / p.col_groups;
+    const int cg = blockIdx.z % p.col_groups;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int r = lane >> 2, c = lane & 3;
+    const bool reports = tid == 0 && split == 0 && h == 0 && cg == 0;
+    if (p.seq_order) {
+        b = __ldg(p.seq_order + b);
+        if (b < 0 || b >= p.batch) {  // not a permutation of the batch
+            if (reports) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
+            return;
+        }
+    }
+    I4Work w;
+    if (!i4_sequence(p, b, reports, w)) return;
+    w.blk0 = split * p.part_blocks;
+    if (w.blk0 >= w.nblk && split > 0) return;
+    w.nloc = max(0, min(p.part_blocks, w.nblk - w.blk0));
+    const int col0 = cg * 8 * NT;                // first column of this CTA
+    const int ncols = min(8 * NT, w.T * p.g - col0);
+    if (ncols <= 0) return;
+
+    extern __shared__ __align__(128) char smem[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + i4_ring_bytes<D>()) + warp * kNst;
+    volatile int *valid = reinterpret_cast<int *>(smem + i4_ring_bytes<D>() + kI4Warps * kNst * sizeof(uint64_t)) + warp * kNst;
+    char *ring = smem + (size_t)warp * kNst * 2 * kTile;
+    __shared__ uint2 s_q[kSteps * NT * 32];
+    __shared__ float s_scale[8 * NT];
+    __shared__ float s_m[kI4Warps * 8], s_l[kI4Warps * 8];
+    __shared__ int s_last;
+
+    if (lane == 0) {
+        for (int st = 0; st < kNst; ++st) mbar_init(&full[st], 1);
+        mbar_init_fence();
+    }
+    __syncwarp();
+
+    // ---- this warp's blocks: warp, warp + 4, ... of the partition
+    const int nown = w.nloc > warp ? (w.nloc - warp + kI4Warps - 1) / kI4Warps : 0;
+    const int32_t *row = p.tables + (size_t)b * p.max_blocks + w.blk0 + warp;
+    // table entries of 32 own blocks at a time, the next 32 already under way
+    int ids = lane < nown ? __ldg(row + kI4Warps * lane) : -1;
+    int ids_next = 32 + lane < nown ? __ldg(row + kI4Warps * (32 + lane)) : -1;
+    const uint64_t policy = l2_evict_first_policy();
+    int issued = 0;
+    auto issue = [&]() {  // the copies of own block `issued`, in its turn
+        const int j = issued++;
+        if (j > 0 && (j & 31) == 0) {
+            ids = ids_next;
+            ids_next = j + 32 + lane < nown ? __ldg(row + kI4Warps * (j + 32 + lane)) : -1;
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, j & 31);
+        if (lane == 0) {
+            const int st = j % kNst;
+            const bool ok = id >= 0 && id < p.num_blocks;
+            valid[st] = ok;
+            if (ok) {
+                const size_t off = ((size_t)id * p.hkv + h) * kTile;
+                char *dst = ring + st * 2 * kTile;
+                mbar_arrive_expect_tx(&full[st], 2 * kTile);
+                bulk_g2s(dst, p.k_pool + off, kTile, &full[st], policy);
+                bulk_g2s(dst + kTile, p.v_pool + off, kTile, &full[st], policy);
+            } else {
+                atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
+                mbar_arrive(&full[st]);
+            }
+        }
+    };
+#pragma unroll 1
+    for (int j = 0; j < kNst && j < nown; ++j) issue();
+
+    // Test instantiation with a limit of 0: a tile that is not there at once is a
+    // wait that ran out (try_wait would sleep until it came).
+    bool stop = false;
+    if constexpr (TW) {
+        if (g_wait_limit_ns == 0 && nown > 0) {
+            stop = __any_sync(0xffffffffu, !phase_done(&full[0], 0));
+            if (stop && lane == 0) atomicOr(p.err, KV_DEVERR_TIMEOUT);
+        }
+    }
+
+    // ---- q of each column: largest magnitude to [2^13, 2^14) by a power of two,
+    // so that fp16 holds it, then into the order of the fragments
+    __half *qs = reinterpret_cast<__half *>(s_q);
+    for (int col = warp; col < 8 * NT; col += kI4Warps) {
+        constexpr int kPer = D / 32;
+        float x[kPer];
+        if (col < ncols) {
+            const int tq = (col0 + col) / p.g, j = (col0 + col) - tq * p.g;
+            const uint16_t *src = p.q + ((size_t)(w.q0 + tq) * p.hq + h * p.g + j) * D + lane * kPer;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                x[i] = p.q_bf16 ? bf16_to_float(src[i]) : f16x2_to_float2(src[i]).x;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) x[i] = 0.f;
+        }
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) m = fmaxf(m, fabsf(x[i]));
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+        // exponent field of the largest; 0 (all zero or below normal) and 255 are left alone
+        const int e = (int)(__float_as_uint(m) >> 23);
+        const int up = e == 0 || e == 255 ? 0 : max(-126, min(126, 127 + 13 - e));
+        const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            // dimension d: quarter cq, word wi, four bits n; pair n of half d / 4 % 2
+            const int d = lane * kPer + i, cq = d / (D / 4), in = d % (D / 4), wi = in / 8, n = in % 4, hi = in / 4 % 2;
+            const int pair = 4 * wi + n;
+            qs[((((pair >> 1) * NT + (col >> 3)) * 32 + (col & 7) * 4 + cq) * 2 + (pair & 1)) * 2 + hi] =
+                __float2half_rn(x[i] * mul);
+        }
+        if (lane == 0) s_scale[col] = p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
+    }
+    __syncthreads();
+
+    // ---- state of columns 8 nt + 2 c and + 1 (maxima replicated over r)
+    float m_run[NT][2], l_run[NT][2], o[NT][kSteps][4], sc[NT][2];
+    int lim[NT][2];  // keys that the column sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int col = 8 * nt + 2 * c + x;
+            m_run[nt][x] = -INFINITY;
+            l_run[nt][x] = 0.f;
+            sc[nt][x] = s_scale[col];
+            lim[nt][x] = (int)(w.L - w.T) + min((col0 + col) / p.g, w.T - 1) + 1;
+#pragma unroll
+            for (int f = 0; f < kSteps; ++f) o[nt][f][x] = o[nt][f][2 + x] = 0.f;
+        }
+    const int least = (int)(w.L - w.T) + col0 / p.g + 1;  // keys that every column sees
+
+    for (int j = 0; j < nown && !stop; ++j) {
+        const int st = j % kNst;
+        const bool bad = !mbar_wait<TW>(&full[st], (j / kNst) & 1, p.err);
+        if (__any_sync(0xffffffffu, bad)) break;
+        const char *kt = ring + st * 2 * kTile, *vt = kt + kTile;
+        const int tok0 = (w.blk0 + warp + kI4Warps * j) * kI4BS;
+        const int ntok = valid[st] ? min(kI4BS, (int)(w.L - tok0)) : 0;
+        // ---- operands: tokens r, r + 8 of K; token pairs c, c + 4 of V
+        uint32_t k0[kW], k1[kW], v0[kW], v1[kW];
+        load_words<kW>(kt + r * (D / 2) + c * (D / 8), k0);
+        load_words<kW>(kt + (r + 8) * (D / 2) + c * (D / 8), k1);
+        load_words<kW>(vt + c * D + r * (D / 8), v0);
+        load_words<kW>(vt + (c + 4) * D + r * (D / 8), v1);
+        uint32_t ks0, ks1, vs0, vs1;
+        if constexpr (D == 128) {
+            ks0 = *reinterpret_cast<const uint16_t *>(kt + 8 * D + r * 8 + 2 * c);
+            ks1 = *reinterpret_cast<const uint16_t *>(kt + 8 * D + (r + 8) * 8 + 2 * c);
+            vs0 = *reinterpret_cast<const uint16_t *>(vt + 8 * D + c * 16 + 2 * r);
+            vs1 = *reinterpret_cast<const uint16_t *>(vt + 8 * D + (c + 4) * 16 + 2 * r);
+        } else {
+            ks0 = *reinterpret_cast<const uint8_t *>(kt + 8 * D + r * 4 + c);
+            ks1 = *reinterpret_cast<const uint8_t *>(kt + 8 * D + (r + 8) * 4 + c);
+            vs0 = *reinterpret_cast<const uint16_t *>(vt + 8 * D + c * 8 + (r & ~1));
+            vs1 = *reinterpret_cast<const uint16_t *>(vt + 8 * D + (c + 4) * 8 + (r & ~1));
+        }
+        // ---- S^T = K q^T
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        {
+            const __half2 a = quarter_scales(ks0), e = quarter_scales(ks1);
+            i4::Scale g0, g1;
+#pragma unroll
+            for (int wi = 0; wi < kW; ++wi) {
+                if (wi == 0) {
+                    g0 = i4::make_scale(__low2half2(a));
+                    g1 = i4::make_scale(__low2half2(e));
+                } else if (D == 128 && wi == 2) {
+                    g0 = i4::make_scale(__high2half2(a));
+                    g1 = i4::make_scale(__high2half2(e));
+                }
+                uint32_t x0[4], x1[4];
+                i4::values8(k0[wi], g0, x0);
+                i4::values8(k1[wi], g1, x1);
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint2 bq = s_q[((2 * wi + f) * NT + nt) * 32 + lane];
+                        mma_16816(s[nt], x0[2 * f], x1[2 * f], x0[2 * f + 1], x1[2 * f + 1], bq.x, bq.y);
+                    }
+            }
+        }
+        // the stage is in registers: its next tile may come
+        __syncwarp();
+        if (issued < nown) issue();
+
+        // ---- softmax: s[0], s[1] token r, columns 2 c, 2 c + 1; s[2], s[3] token r + 8
+        uint32_t ph[NT][2], pl[NT][2];
+        const bool masked = tok0 + kI4BS > least || ntok < kI4BS;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[nt][x] *= sc[nt][x & 1];
+            if (masked) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int t = r + 4 * (x & 2);
+                    if (t >= ntok || tok0 + t >= lim[nt][x & 1]) s[nt][x] = -INFINITY;
+                }
+            }
+            float m0 = fmaxf(s[nt][0], s[nt][2]), m1 = fmaxf(s[nt][1], s[nt][3]);
+#pragma unroll
+            for (int x = 4; x <= 16; x <<= 1) {
+                m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, x));
+                m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, x));
+            }
+            const float n0 = fmaxf(m_run[nt][0], m0), n1 = fmaxf(m_run[nt][1], m1);
+            const float u0 = n0 == -INFINITY ? 0.f : n0 - kI4Bias, u1 = n1 == -INFINITY ? 0.f : n1 - kI4Bias;
+            if (__any_sync(0xffffffffu, n0 != m_run[nt][0] || n1 != m_run[nt][1])) {
+                // 2^(old - new); a state of -inf is empty
+                const float a0 = ex2(m_run[nt][0] - (u0 + kI4Bias)), a1 = ex2(m_run[nt][1] - (u1 + kI4Bias));
+                m_run[nt][0] = n0;
+                m_run[nt][1] = n1;
+                l_run[nt][0] *= a0;
+                l_run[nt][1] *= a1;
+#pragma unroll
+                for (int f = 0; f < kSteps; ++f) {
+                    o[nt][f][0] *= a0;
+                    o[nt][f][1] *= a1;
+                    o[nt][f][2] *= a0;
+                    o[nt][f][3] *= a1;
+                }
+            }
+            const float p0 = ex2(s[nt][0] - u0), p1 = ex2(s[nt][1] - u1);
+            const float p2 = ex2(s[nt][2] - u0), p3 = ex2(s[nt][3] - u1);
+            l_run[nt][0] += p0 + p2;
+            l_run[nt][1] += p1 + p3;
+            const uint32_t h01 = half_pair(p0, p1), h23 = half_pair(p2, p3);
+            ph[nt][0] = transpose8(h01);
+            ph[nt][1] = transpose8(h23);
+            if constexpr (EXACT) {
+                const float2 f01 = f16x2_to_float2(h01), f23 = f16x2_to_float2(h23);
+                pl[nt][0] = transpose8(half_pair(p0 - f01.x, p1 - f01.y));
+                pl[nt][1] = transpose8(half_pair(p2 - f23.x, p3 - f23.y));
+            }
+        }
+        // ---- O^T += V^T P^T.  Slots past the sequence may hold anything: a scale
+        // of zero makes their values zero (codes are finite).
+        {
+            uint32_t a = __half2_raw(quarter_scales(vs0)).x | (uint32_t)__half2_raw(quarter_scales(vs0)).y << 16;
+            uint32_t e = __half2_raw(quarter_scales(vs1)).x | (uint32_t)__half2_raw(quarter_scales(vs1)).y << 16;
+            if (ntok < kI4BS) {
+                a &= (2 * c < ntok ? 0xffffu : 0u) | (2 * c + 1 < ntok ? 0xffff0000u : 0u);
+                e &= (2 * c + 8 < ntok ? 0xffffu : 0u) | (2 * c + 9 < ntok ? 0xffff0000u : 0u);
+            }
+            const i4::Scale g0 = i4::make_scale(*reinterpret_cast<__half2 *>(&a));
+            const i4::Scale g1 = i4::make_scale(*reinterpret_cast<__half2 *>(&e));
+#pragma unroll
+            for (int wi = 0; wi < kW; ++wi) {
+                uint32_t x0[4], x1[4];
+                i4::values8(v0[wi], g0, x0);
+                i4::values8(v1[wi], g1, x1);
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_16816(o[nt][2 * wi + f], x0[2 * f], x0[2 * f + 1], x1[2 * f], x1[2 * f + 1], ph[nt][0], ph[nt][1]);
+                        if constexpr (EXACT)
+                            mma_16816(o[nt][2 * wi + f], x0[2 * f], x0[2 * f + 1], x1[2 * f], x1[2 * f + 1], pl[nt][0],
+                                      pl[nt][1]);
+                    }
+            }
+        }
+    }
+    // After a timed-out wait: no copy may still be on its way into this CTA's memory.
+    for (int j = max(0, issued - kNst); j < issued; ++j) mbar_wait_drain(&full[j % kNst], (j / kNst) & 1, p.err);
+
+    // ---- the four warps' states to this partition's result, eight columns at a time
+    float4 *sm_o = reinterpret_cast<float4 *>(smem);  // [warp][column][D / 4], see `at`
+    constexpr int kQ = D / 32;                         // float4s of one lane's dims
+    auto at = [&](int wp, int col, int rr, int i) {    // spread over the banks
+        return (wp * 8 + col) * (D / 4) + rr * kQ + (i ^ ((col >> 1) & (kQ - 1)));
+    };
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float l0 = l_run[nt][0], l1 = l_run[nt][1];
+#pragma unroll
+        for (int x = 4; x <= 16; x <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+        }
+        __syncthreads();  // the rings, or the previous columns, have been read
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int i = 0; i < kQ; ++i)
+                sm_o[at(warp, 2 * c + x, r, i)] =
+                    make_float4(o[nt][2 * i][x], o[nt][2 * i][2 + x], o[nt][2 * i + 1][x], o[nt][2 * i + 1][2 + x]);
+        if (r == 0) {
+            // the weights are relative to m - kI4Bias
+            s_m[warp * 8 + 2 * c] = m_run[nt][0] - kI4Bias;
+            s_m[warp * 8 + 2 * c + 1] = m_run[nt][1] - kI4Bias;
+            s_l[warp * 8 + 2 * c] = l0;
+            s_l[warp * 8 + 2 * c + 1] = l1;
+        }
+        __syncthreads();
+        const int live = min(8, ncols - 8 * nt);
+        for (int idx = tid; idx < live * (D / 4); idx += kI4Threads) {
+            const int col = idx / (D / 4), d4 = idx % (D / 4);
+            float M = s_m[col];
+#pragma unroll
+            for (int wp = 1; wp < kI4Warps; ++wp) M = fmaxf(M, s_m[wp * 8 + col]);
+            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+            float den = 0.f;
+#pragma unroll
+            for (int wp = 0; wp < kI4Warps; ++wp) {
+                const float lw = s_l[wp * 8 + col];
+                if (lw == 0.f) continue;  // saw no key
+                const float f = ex2(s_m[wp * 8 + col] - M);
+                const float4 v = sm_o[at(wp, col, d4 / kQ, d4 % kQ)];
+                num.x += f * v.x;
+                num.y += f * v.y;
+                num.z += f * v.z;
+                num.w += f * v.w;
+                den += f * lw;
+            }
+            const float inv = den != 0.f ? p.v_mul / den : 0.f;  // den NaN: NaN
+            const int gc = col0 + 8 * nt + col, tq = gc / p.g;
+            const int hq = h * p.g + (gc - tq * p.g);
+            const size_t orow = out_row(p, w, tq, hq);
+            const float4 v = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+            const float lse2 = den != 0.f ? M + log2f(den) : -INFINITY;
+            if (w.nsplit == 1) {
+                store_out4(p.out, orow * D + 4 * d4, v, p.out_type);
+                if (p.lse && d4 == 0) p.lse[orow] = lse2 * 0.6931471805599453f;
+            } else {
+                const size_t slot = ws_row(p, w, tq, hq) * p.max_splits + split;
+                reinterpret_cast<float4 *>(p.ws_o)[slot * (D / 4) + d4] = v;
+                if (d4 == 0) p.ws_lse[slot] = lse2;
+            }
+        }
+    }
+    if (w.nsplit == 1 || !p.counters || w.nsplit > kFuseMaxSplits) return;
+
+    // ---- the last partition to finish merges them all
+    __threadfence();
+    __syncthreads();
+    int *counter = p.counters + ((size_t)b * p.col_groups + cg) * p.hkv + h;
+    if (tid == 0) s_last = atomicAdd(counter, 1) == w.nsplit - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    float *wt = reinterpret_cast<float *>(smem);  // [8 NT][kFuseMaxSplits]
+    for (int col = warp; col < ncols; col += kI4Warps) {
+        const int gc = col0 + col, tq = gc / p.g;
+        const int hq = h * p.g + (gc - tq * p.g);
+        const size_t orow = out_row(p, w, tq, hq), wrow = ws_row(p, w, tq, hq);
+        const float x = lane < w.nsplit ? __ldcg(p.ws_lse + wrow * p.max_splits + lane) : -INFINITY;
+        float M = x;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+        const float e = x == -INFINITY ? 0.f : ex2(x - M);  // NaN stays
+        float den = e;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) den += __shfl_xor_sync(0xffffffffu, den, s);
+        wt[col * kFuseMaxSplits + lane] = den != 0.f ? e / den : 0.f;
+        if (p.lse && lane == 0) p.lse[orow] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+    }
+    __syncthreads();
+    for (int idx = tid; idx < ncols * (D / 4); idx += kI4Threads) {
+        const int col = idx / (D / 4), d4 = idx % (D / 4);
+        const int gc = col0 + col, tq = gc / p.g;
+        const int hq = h * p.g + (gc - tq * p.g);
+        const size_t orow = out_row(p, w, tq, hq);
+        const float4 *src = reinterpret_cast<const float4 *>(p.ws_o) + ws_row(p, w, tq, hq) * p.max_splits * (D / 4) + d4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = 0; s < w.nsplit; ++s) {
+            const float f = wt[col * kFuseMaxSplits + s];
+            const float4 v = __ldcg(src + (size_t)s * (D / 4));
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+        }
+        store_out4(p.out, orow * D + 4 * d4, acc, p.out_type);
+    }
+    if (tid == 0) *counter = 0;  // ready for the next call
+}
+
+// Merge of rows cut into more partitions than one CTA merges: one CTA per query
+// row, its threads in groups of D / 4 that take every group-th partition.
+template <int D>
+__global__ void __launch_bounds__(kI4Threads) merge_i4_kernel(const I4Params p, int min_splits) {
+    constexpr int kLanes = D / 4, kGroups = kI4Threads / kLanes;
+    const int tq = blockIdx.x / p.hq, hq = blockIdx.x % p.hq;
+    I4Work w;
+    if (!i4_sequence(p, blockIdx.y, false, w) || tq >= w.T || w.nsplit < min_splits) return;
+    const int tid = threadIdx.x, d4 = tid % kLanes, grp = tid / kLanes;
+    const size_t orow = out_row(p, w, tq, hq), wrow = ws_row(p, w, tq, hq);
+    const float *ls = p.ws_lse + wrow * p.max_splits;
+    __shared__ float s_red[kI4Warps * 2];
+    __shared__ float4 s_acc[kI4Threads];
+    __shared__ float s_den[kGroups];
+    float M = -INFINITY;
+    for (int s = tid; s < w.nsplit; s += kI4Threads) M = fmaxf(M, ls[s]);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+    if ((tid & 31) == 0) s_red[tid >> 5] = M;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kI4Warps; ++i) M = fmaxf(M, s_red[i]);
+    const float4 *src = reinterpret_cast<const float4 *>(p.ws_o) + wrow * p.max_splits * kLanes + d4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.f;
+#pragma unroll 4
+    for (int s = grp; s < w.nsplit; s += kGroups) {
+        const float x = ls[s], e = x == -INFINITY ? 0.f : ex2(x - M);
+        const float4 v = src[(size_t)s * kLanes];
+        acc.x += e * v.x;
+        acc.y += e * v.y;
+        acc.z += e * v.z;
+        acc.w += e * v.w;
+        den += e;
+    }
+    s_acc[tid] = acc;
+    if (d4 == 0) s_den[grp] = den;
+    __syncthreads();
+    if (grp) return;
+    den = s_den[0];
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+        const float4 v = s_acc[i * kLanes + d4];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+        den += s_den[i];
+    }
+    const float inv = den != 0.f ? 1.f / den : 0.f;
+    store_out4(p.out, orow * D + 4 * d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), p.out_type);
+    if (p.lse && d4 == 0) p.lse[orow] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+}
+
+cudaError_t set_wait_limit_decode_i4(unsigned long long ns) { return set_wait_limit_here(ns); }
+
+template <int D, int NT, int MINB>
+static kv_status launch_i4(const I4Params &p, dim3 grid, cudaStream_t s) {
+    const bool exact = p.out_type == KV_F32, tw = test_waits_enabled();
+    auto fn = exact ? (tw ? decode_i4_kernel<D, NT, true, true, MINB> : decode_i4_kernel<D, NT, true, false, MINB>)
+                    : (tw ? decode_i4_kernel<D, NT, false, true, MINB> : decode_i4_kernel<D, NT, false, false, MINB>);
+    constexpr size_t smem = i4_smem_bytes<D>();
+    if (kv_status st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
+        return st;
+    fn<<<grid, kI4Threads, smem, s>>>(p);
+    return cuda_status(cudaGetLastError());
+}
+
+kv_status attend_i4(const I4Call &a) {
+    kv_pool *pool = a.pool;
+    const int g = a.num_q_heads / pool->num_kv_heads;
+    int pb = 0, ms = 0;
+    split_plan(a.batch, pool->num_kv_heads, a.max_blocks, a.num_splits, &pb, &ms);
+    const long long rows = (long long)a.batch * a.max_q_len;
+    if (rows > INT32_MAX) return KV_ERR_UNSUPPORTED;
+    const size_t need = decode_workspace_bytes((int)rows, a.num_q_heads, pool->head_dim, ms);
+    if (need > 0 && (!a.workspace || a.workspace_bytes < need)) return KV_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(a.workspace) & 15) return KV_ERR_ARG;
+    const int cols = a.max_q_len * g;  // of one (sequence, kv head)
+    const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+    const int groups = (cols + 8 * nt - 1) / (8 * nt);
+    if (ms > 65535 || (long long)a.batch * groups > 65535 || pool->num_kv_heads > 65535) return KV_ERR_UNSUPPORTED;
+    I4Params p{};
+    p.q = static_cast<const uint16_t *>(a.q);
+    p.q_bf16 = a.q_dtype == KV_BF16;
+    p.cu_q = a.cu_q;
+    p.total_q = a.total_q;
+    p.max_t = a.max_q_len;
+    p.k_pool = static_cast<const char *>(pool->k);
+    p.v_pool = static_cast<const char *>(pool->v);
+    p.tables = a.block_tables;
+    p.max_blocks = a.max_blocks;
+    p.num_blocks = pool->num_blocks;
+    p.seq_lens = a.seq_lens;
+    p.seq_order = a.seq_order;
+    p.batch = a.batch;
+    p.hq = a.num_q_heads;
+    p.hkv = pool->num_kv_heads;
+    p.g = g;
+    p.scale_log2 = a.scale * 1.4426950408889634f * 4.f * pool->k_scale;
+    p.v_mul = 4.f * pool->v_scale;
+    p.part_blocks = pb;
+    p.max_splits = ms;
+    p.col_groups = groups;
+    p.out = a.out;
+    p.out_type = a.out_dtype;
+    p.lse = a.lse;
+    p.ws_o = static_cast<float *>(a.workspace);
+    p.ws_lse = p.ws_o ? p.ws_o + (size_t)rows * a.num_q_heads * ms * pool->head_dim : nullptr;
+    const bool fused = (long long)a.batch * groups * pool->num_kv_heads <= kv_pool::kCounterSlots;
+    p.counters = fused ? pool->counters : nullptr;
+    p.err = pool->err;
+    const dim3 grid(ms, pool->num_kv_heads, a.batch * groups);
+    kv_status st;
+    if (pool->head_dim == 64)
+        st = nt == 1 ? launch_i4<64, 1, 5>(p, grid, a.stream) : KV_ERR_UNSUPPORTED;
+    else
+        st = nt == 1   ? launch_i4<128, 1, 5>(p, grid, a.stream)
+             : nt == 2 ? launch_i4<128, 2, 3>(p, grid, a.stream)
+                       : launch_i4<128, 4, 2>(p, grid, a.stream);
+    if (st != KV_OK) return st;
+    const int min_splits = fused ? kFuseMaxSplits + 1 : 2;
+    if (ms >= min_splits) {
+        const dim3 mgrid(a.num_q_heads * a.max_q_len, a.batch);
+        if (pool->head_dim == 64)
+            merge_i4_kernel<64><<<mgrid, kI4Threads, 0, a.stream>>>(p, min_splits);
+        else
+            merge_i4_kernel<128><<<mgrid, kI4Threads, 0, a.stream>>>(p, min_splits);
+        return cuda_status(cudaGetLastError());
+    }
+    return KV_OK;
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_heads, int max_blocks,
+                            int *num_splits) {
+    if (!num_splits || batch < 0 || num_kv_heads <= 0 || max_blocks < 0 || (batch > 0 && !host_seq_lens))
+        return KV_ERR_ARG;
+    *num_splits = 1;
+    if (batch == 0 || max_blocks == 0) return KV_OK;
+    // One wave: the smallest partitions whose CTAs fit five to an SM.
+    const long long wave = 5LL * sm_count();
+    for (int s = 1; s <= 4096; ++s) {
+        int pb, ms;
+        split_plan(batch, num_kv_heads, max_blocks, s, &pb, &ms);
+        long long ctas = 0;
+        for (int b = 0; b < batch; ++b) {
+            const long long L = std::min<long long>(std::max(host_seq_lens[b], 0), (long long)max_blocks * kI4BS);
+            const long long n = (L + kI4BS - 1) / kI4BS;
+            ctas += std::max<long long>(1, (n + pb - 1) / pb);
+        }
+        if (ctas * num_kv_heads <= wave) *num_splits = s;
+        if (pb <= 2 * kI4Warps) break;
+    }
+    return KV_OK;
+}
+
+kv_status paged_decode_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype, const int32_t *block_tables,
+                                    int max_blocks, const int32_t *seq_lens, const int32_t *seq_order, int batch,
+                                    int num_q_heads, float scale, void *out, kv_dtype out_dtype, float *lse_out,
+                                    int num_splits, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!p || batch < 0 || num_q_heads <= 0 || max_blocks < 0 || num_splits < 0) return KV_ERR_ARG;
+    if (p->dtype != KV_I4 || (q_dtype != KV_BF16 && q_dtype != KV_F16) ||
+        (out_dtype != KV_F32 && out_dtype != q_dtype))
+        return KV_ERR_UNSUPPORTED;
+    if (num_q_heads % p->num_kv_heads) return KV_ERR_ARG;
+    if (num_q_heads / p->num_kv_heads > 8) return KV_ERR_UNSUPPORTED;
+    if (kv_status st = require_device(p->device)) return st;
+    if (batch == 0) return KV_OK;
+    if (!q || !seq_lens || !out || (max_blocks > 0 && !block_tables)) return KV_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return KV_ERR_ARG;
+    I4Call a{};
+    a.pool = p;
+    a.q = q;
+    a.q_dtype = q_dtype;
+    a.max_q_len = 1;
+    a.block_tables = block_tables;
+    a.max_blocks = max_blocks;
+    a.seq_lens = seq_lens;
+    a.seq_order = seq_order;
+    a.batch = batch;
+    a.num_q_heads = num_q_heads;
+    a.scale = scale;
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.lse = lse_out;
+    a.num_splits = num_splits;
+    a.workspace = workspace;
+    a.workspace_bytes = workspace_bytes;
+    a.stream = as_stream(stream);
+    return attend_i4(a);
+}
+
+}  // extern "C"

@@ -1,0 +1,118 @@
+// The 4-bit cache format (KV_I4): how a tile is laid out, how values become
+// codes and codes values.
+//
+// 16 consecutive dimensions of one (token, kv head) are a group: sixteen
+// integer codes c in -7..7 and one e4m3 scale s, standing for c * s * g with g
+// the pool's power-of-two scale of K or V.  s is the e4m3 nearest to
+// max|x| / (7 g) (at most 448), c the integer nearest to x / (s g), both ties to
+// even; a group whose s rounds to 0 holds zeros, a group with a NaN is NaN.
+// c * s has at most 7 significant bits and lies between 2^-9 and 3136: exact in
+// fp16 and bf16.
+//
+// A (block, kv head) tile of K or of V is 16 x D / 2 bytes of codes followed by
+// 16 x D / 16 scale bytes (9 D bytes; 1152 for D = 128).  A code is stored as
+// u = c + 8 in four bits.
+//   K  token t's row is D / 2 bytes in order of dimensions, dimension d in the
+//      four bits d % 8 of the row's 32-bit word d / 8; its scale of group j is
+//      byte t * D / 16 + j of the scales.  A lane of the score product loads a
+//      quarter row, 16 consecutive bytes.
+//   V  is contracted over tokens, so the two tokens of a pair (2p, 2p + 1) share
+//      words: word (p, quad) holds dimensions 4 quad .. 4 quad + 3 of token 2p in
+//      its low half and of token 2p + 1 in its high half, so that a masked word
+//      is already the pair of operands the tensor core wants.  Scales: byte
+//      p * D / 8 + 2 j + (t & 1).  A token owns whole 16-bit halves and whole scale
+//      bytes: tokens of one pair may be written at the same time.
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace pkv {
+namespace i4 {
+
+// Larger of two, NaN if either is.
+KV_DEVICE float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The e4m3 nearest to x >= 0 (at most 448; NaN for NaN) as its byte.
+KV_DEVICE uint32_t e4m3_of(float x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+    return r;
+}
+
+// Two e4m3 bytes (low byte first) as a pair of fp16 values, exact.
+KV_DEVICE __half2 e4m3x2_to_half2(uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(b));
+    return *reinterpret_cast<__half2 *>(&r);
+}
+
+KV_DEVICE float e4m3_to_float(uint32_t b) { return __low2float(e4m3x2_to_half2(b)); }
+
+// Eight values of one group half -> their eight 4-bit codes, value i in bits
+// 4i .. 4i + 3, given the group's scale s (a value of e4m3).
+//
+// c = rint(x / s) must be decided as exact arithmetic decides it: values of 16
+// bits are often exactly between two codes.  (k + 1/2) s has at most 8
+// significant bits, so the correctly rounded quotient lies on the right side of
+// (or on) each border, and a reciprocal with one correction step gives that
+// quotient: q0 = x r, q = q0 + (x - q0 s) r.  Clamping x to +-7.25 s first (exact)
+// keeps infinities and |c| > 7 out.  rint and the bias are one addition of
+// 1.5 * 2^23 + 8.
+KV_DEVICE uint32_t codes8(const float (&x)[8], float s) {
+    const float lim = 7.25f * s;
+    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+        const float y = fminf(fmaxf(x[i], -lim), lim);
+        const float q0 = __fmul_rn(y, r);
+        const float q = __fmaf_rn(__fmaf_rn(-q0, s, y), r, q0);
+        // low bits of the sum's word: rint(q) + 8, in 1..15
+        w = (w << 4) + (__float_as_uint(__fadd_rn(q, 12582920.f)) & 15u);
+    }
+    return w;
+}
+
+// Four code pairs of one word as fp16 pairs times their scales: out[n] = (low
+// half's four bits n, high half's four bits n).
+//
+// A code placed in the mantissa of 16 or 256 gives 16 + u or 256 + u with one
+// logical operation, and one fused multiply-add takes it to (u - 8) s: the
+// constants -24 s and -264 s are exact (6 and 10 bits), the product is not
+// rounded before the sum, the result has 7 bits.  s is taken a quarter so that
+// 264 s stays below 65504; the callers multiply the result's sum by 4.
+struct Scale {
+    __half2 s, m24, m264;
+};
+
+KV_DEVICE Scale make_scale(__half2 s_quarter) {
+    Scale r;
+    r.s = s_quarter;
+    r.m24 = __hmul2(s_quarter, __float2half2_rn(-24.f));
+    r.m264 = __hmul2(s_quarter, __float2half2_rn(-264.f));
+    return r;
+}
+
+KV_DEVICE uint32_t fma2(uint32_t x, __half2 s, __half2 m) {
+    const __half2 v = __hfma2(*reinterpret_cast<const __half2 *>(&x), s, m);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+KV_DEVICE void values8(uint32_t w, const Scale &k, uint32_t (&out)[4]) {
+    const uint32_t a = w << 2, b = w >> 6;
+    out[0] = fma2((a & 0x003C003Cu) | 0x5C005C00u, k.s, k.m264);
+    out[1] = fma2((a & 0x03C003C0u) | 0x4C004C00u, k.s, k.m24);
+    out[2] = fma2((b & 0x003C003Cu) | 0x5C005C00u, k.s, k.m264);
+    out[3] = fma2((b & 0x03C003C0u) | 0x4C004C00u, k.s, k.m24);
+}
+
+}  // namespace i4
+}  // namespace pkv

@@ -14,8 +14,9 @@ struct kv_pool {
     int head_dim = 0;
     kv_dtype dtype = KV_BF16;
     int device = 0;
-    void *k = nullptr;  // [num_blocks][num_kv_heads][block_size][head_dim]
+    void *k = nullptr;  // [num_blocks][num_kv_heads][block_size][head_dim]; KV_I4: tiles (i4.cuh)
     void *v = nullptr;
+    float k_scale = 1.f, v_scale = 1.f;  // KV_I4: powers of two (kv_pool_set_i4_scales)
     int *err = nullptr;  // device error word
     // arrival counters of the fused split merge, one per (sequence, kv head),
     // zero between calls (each merging CTA resets its own)
@@ -33,7 +34,20 @@ struct kv_pool {
 
 namespace pkv {
 
+// Bytes of one element of a type that stores whole elements (not KV_I4).
 inline int dtype_bytes(kv_dtype t) { return t == KV_F32 ? 4 : 2; }
+
+// Bytes of one (block, kv head) tile of the K or V pool: 16 tokens x head_dim
+// elements; KV_I4: 16 x head_dim / 2 bytes of codes, then one scale byte per
+// 16 dimensions.
+inline size_t tile_bytes(kv_dtype t, int head_dim) {
+    return t == KV_I4 ? (size_t)9 * head_dim : (size_t)16 * head_dim * dtype_bytes(t);
+}
+
+// 16-byte chunks of one block (all kv heads) of the K or V pool.
+inline int block_chunks_of(const kv_pool *p) {
+    return (int)(p->num_kv_heads * tile_bytes(p->dtype, p->head_dim) / 16);
+}
 
 inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s); }
 
@@ -52,6 +66,7 @@ kv_status require_device(int device);
 cudaError_t set_wait_limit_decode(unsigned long long ns);
 cudaError_t set_wait_limit_prefill(unsigned long long ns);
 cudaError_t set_wait_limit_cascade(unsigned long long ns);
+cudaError_t set_wait_limit_decode_i4(unsigned long long ns);
 
 // True once a test has set a pipeline-wait limit other than the default
 // (kv_debug_set_wait_limit_ns): launches then take the kernels' test
@@ -147,6 +162,28 @@ struct DecodeArgs {
     int *err;
     cudaStream_t stream;
 };
+
+// ---- prefill: the tcgen05 kernel over checked arguments and tensor maps of the
+// K and V tiles ([block][kv head][16] rows of 128 16-bit values)
+struct PrefillCall {
+    const void *q;
+    kv_dtype q_dtype;  // KV_BF16 or KV_F16: q, K and a 16-bit out
+    bool v_f16;        // V is fp16 (else bf16, as q)
+    const CUtensorMap *map_k, *map_v;
+    const int32_t *cu_q;
+    int total_q, max_q_len;
+    const int32_t *block_tables;
+    int max_blocks, num_blocks, num_kv_heads;
+    const int32_t *seq_lens;
+    int batch, num_q_heads;
+    float scale, v_mul;
+    void *out;
+    kv_dtype out_dtype;
+    float *lse;
+    int *err;
+    cudaStream_t stream;
+};
+kv_status launch_prefill(const PrefillCall &a);
 
 // Splits per (sequence, kv head) merged inside the decode kernel by the last
 // CTA of that pair; longer plans leave the merge to merge_kernel.

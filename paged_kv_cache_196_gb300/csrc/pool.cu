@@ -9,8 +9,10 @@
 // between parallel samples and branches, copied when written).
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <initializer_list>
 #include <new>
 
 #include "common.cuh"
@@ -184,7 +186,7 @@ kv_status kv_pool_create(int num_blocks, int block_size, int num_kv_heads, int h
                          kv_dtype dtype, kv_pool_t *out) {
     if (!out || num_blocks <= 0 || num_kv_heads <= 0) return KV_ERR_ARG;
     if (block_size != 16 || (head_dim != 64 && head_dim != 128) ||
-        (dtype != KV_F32 && dtype != KV_BF16 && dtype != KV_F16))
+        (dtype != KV_F32 && dtype != KV_BF16 && dtype != KV_F16 && dtype != KV_I4))
         return KV_ERR_UNSUPPORTED;
     kv_pool *p = new (std::nothrow) kv_pool();
     if (!p) return KV_ERR_OOM;
@@ -194,7 +196,7 @@ kv_status kv_pool_create(int num_blocks, int block_size, int num_kv_heads, int h
     p->head_dim = head_dim;
     p->dtype = dtype;
     cudaGetDevice(&p->device);
-    const size_t bytes = (size_t)num_blocks * num_kv_heads * block_size * head_dim * dtype_bytes(dtype);
+    const size_t bytes = (size_t)num_blocks * num_kv_heads * tile_bytes(dtype, head_dim);
     kv_status st = KV_OK;
     if (cudaMalloc(&p->k, bytes) != cudaSuccess || cudaMalloc(&p->v, bytes) != cudaSuccess ||
         cudaMalloc(&p->err, sizeof(int)) != cudaSuccess ||
@@ -244,6 +246,18 @@ kv_status kv_pool_set_launch_overlap(kv_pool_t p, int enable) {
     return KV_OK;
 }
 
+kv_status kv_pool_set_i4_scales(kv_pool_t p, float k_scale, float v_scale) {
+    if (!p) return KV_ERR_ARG;
+    if (p->dtype != KV_I4) return KV_ERR_UNSUPPORTED;
+    for (float x : {k_scale, v_scale}) {
+        int e = 0;
+        if (!(x >= 0x1p-32f && x <= 0x1p32f) || std::frexp(x, &e) != 0.5f) return KV_ERR_ARG;
+    }
+    p->k_scale = k_scale;
+    p->v_scale = v_scale;
+    return KV_OK;
+}
+
 kv_status kv_pool_allocator(kv_pool_t p, kv_allocator_t *out) {
     if (!p || !out) return KV_ERR_ARG;
     *out = p->alloc;
@@ -275,7 +289,7 @@ kv_status kv_cow_if_shared(kv_pool_t p, int32_t *block_id_inout, int *copied, vo
     if (rc == 1) return KV_OK;  // private already: write in place
     int32_t fresh = -1;
     if (kv_status st = kv_allocator_alloc(p->alloc, 1, &fresh)) return st;
-    const int block_chunks = p->num_kv_heads * p->block_size * p->head_dim * dtype_bytes(p->dtype) / 16;
+    const int block_chunks = block_chunks_of(p);
     copy_block_kernel<<<grid_for(block_chunks, 256), 256, 0, as_stream(stream)>>>(
         (uint4 *)p->k, (uint4 *)p->v, old, fresh, block_chunks);
     if (kv_status st = cuda_status(cudaGetLastError())) {
@@ -292,6 +306,7 @@ kv_status kv_append(kv_pool_t p, const void *k_new, const void *v_new,
                     const int64_t *slot_mapping, int num_tokens, void *stream) {
     if (!p || num_tokens < 0) return KV_ERR_ARG;
     if (kv_status st = require_device(p->device)) return st;
+    if (p->dtype == KV_I4) return KV_ERR_UNSUPPORTED;  // kv_append_rope says what type the rows have
     if (num_tokens == 0) return KV_OK;
     if (!k_new || !v_new || !slot_mapping) return KV_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15)
@@ -325,7 +340,7 @@ kv_status kv_copy_blocks(kv_pool_t p, const int32_t *src, const int32_t *dst, in
     if (kv_status st = require_device(p->device)) return st;
     if (n == 0) return KV_OK;
     if (!src || !dst) return KV_ERR_ARG;
-    const int block_chunks = p->num_kv_heads * p->block_size * p->head_dim * dtype_bytes(p->dtype) / 16;
+    const int block_chunks = block_chunks_of(p);
     copy_blocks_kernel<<<grid_for((long long)n * block_chunks, 256), 256, 0, as_stream(stream)>>>(
         (uint4 *)p->k, (uint4 *)p->v, src, dst, n, block_chunks, p->num_blocks, p->err);
     return cuda_status(cudaGetLastError());
@@ -336,7 +351,7 @@ static kv_status swap(kv_pool_t p, const int32_t *ids, int n, void *host, int di
     if (kv_status st = require_device(p->device)) return st;
     if (n == 0) return KV_OK;
     if (!ids || !host || (reinterpret_cast<uintptr_t>(host) & 15)) return KV_ERR_ARG;
-    const int block_chunks = p->num_kv_heads * p->block_size * p->head_dim * dtype_bytes(p->dtype) / 16;
+    const int block_chunks = block_chunks_of(p);
     const long long total = (long long)n * block_chunks;
     swap_blocks_kernel<<<grid_for(total, 256), 256, 0, as_stream(stream)>>>(
         (uint4 *)p->k, (uint4 *)p->v, (uint4 *)host, ids, n, block_chunks, p->num_blocks, dir,
@@ -355,7 +370,7 @@ kv_status kv_swap_in(kv_pool_t p, const int32_t *block_ids, int n, const void *h
 
 kv_status kv_swap_bytes(kv_pool_t p, int n, size_t *bytes) {
     if (!p || n < 0 || !bytes) return KV_ERR_ARG;
-    *bytes = (size_t)n * 2 * p->num_kv_heads * p->block_size * p->head_dim * dtype_bytes(p->dtype);
+    *bytes = (size_t)n * 2 * p->num_kv_heads * tile_bytes(p->dtype, p->head_dim);
     return KV_OK;
 }
 
@@ -363,6 +378,7 @@ kv_status kv_debug_set_wait_limit_ns(uint64_t ns) {
     cudaError_t e = set_wait_limit_decode(ns);
     if (e == cudaSuccess) e = set_wait_limit_prefill(ns);
     if (e == cudaSuccess) e = set_wait_limit_cascade(ns);
+    if (e == cudaSuccess) e = set_wait_limit_decode_i4(ns);
     if (e == cudaSuccess) g_test_waits.store(ns != KV_WAIT_LIMIT_DEFAULT_NS);
     return cuda_status(e);
 }

@@ -103,8 +103,9 @@ struct PrefillParams {
     int num_kv_heads;
     int g;
     float scale_log2;
+    float v_mul;   // factor of V (a 4-bit pool's expanded tiles), else 1
     void *out;
-    int out_type;  // kv_dtype of out: KV_F32 or the pool's type
+    int out_type;  // kv_dtype of out: KV_F32 or q's type
     float *lse;
     int *err;
 };
@@ -119,7 +120,9 @@ struct PfBars {
     int abort;
 };
 
-template <bool TW, bool F16>
+// F16: q and K are fp16 (else bf16).  VF16: V already is fp16, otherwise it is
+// bf16 and rewritten as fp16 in shared memory.
+template <bool TW, bool F16, bool VF16 = F16>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
@@ -207,9 +210,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // swizzle permutes chunks within a 128-byte row, never across rows).
         uint4 *vt = reinterpret_cast<uint4 *>(sV + s * kPfTileBytes);
         const long long valid = L - (long long)t * kPfBN;  // rows below this hold keys < L
-        if constexpr (F16) {
-            // an fp16 pool: V is already in the MMA's type; only the rows of
-            // keys at or past L are zeroed
+        if constexpr (VF16) {
+            // V is already in the MMA's type; only the rows of keys at or past L
+            // are zeroed
             if (valid < kPfBN)
                 for (int i = 32 * part + lane; i < 2048; i += 256)
                     if (((i & 1023) >> 3) >= valid) vt[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (ok) ok = mbar_wait<TW>(&bars->done, 0, p.err);
         if (!ok) *abort_flag = 1;
         tc::fence_after_sync();
-        const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
+        const float inv = l_sum > 0.f ? p.v_mul / l_sum : 0.f;
         const size_t orow = ((size_t)(q_begin + qrow) * p.num_q_heads + hq) * kPfD;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -549,6 +552,44 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 
 cudaError_t set_wait_limit_prefill(unsigned long long ns) { return set_wait_limit_here(ns); }
 
+kv_status launch_prefill(const PrefillCall &a) {
+    // The q map covers exactly total_q rows: a tile reaching past them reads
+    // zeros, and rows past a chunk or past total_q are never stored.
+    CUtensorMap tm_q;
+    if (!encode_q_map(&tm_q, a.q, a.total_q, a.num_q_heads)) return KV_ERR_CUDA;
+    PrefillParams pp{};
+    pp.cu_q = a.cu_q;
+    pp.total_q = a.total_q;
+    pp.tables = a.block_tables;
+    pp.seq_lens = a.seq_lens;
+    pp.max_blocks = a.max_blocks;
+    pp.num_blocks = a.num_blocks;
+    pp.num_q_heads = a.num_q_heads;
+    pp.num_kv_heads = a.num_kv_heads;
+    pp.g = a.num_q_heads / a.num_kv_heads;
+    pp.scale_log2 = a.scale * 1.4426950408889634f;
+    pp.v_mul = a.v_mul;
+    pp.out = a.out;
+    pp.out_type = a.out_dtype;
+    pp.lse = a.lse;
+    pp.err = a.err;
+    const bool f16 = a.q_dtype == KV_F16, vf16 = a.v_f16;
+    auto fn = test_waits_enabled() ? (f16    ? prefill_kernel<true, true>
+                                      : vf16 ? prefill_kernel<true, false, true>
+                                             : prefill_kernel<true, false>)
+                                   : (f16    ? prefill_kernel<false, true>
+                                      : vf16 ? prefill_kernel<false, false, true>
+                                             : prefill_kernel<false, false>);
+    if (kv_status st0 = cuda_status(cudaFuncSetAttribute(
+            fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kPfSmemBytes)))
+        return st0;
+    const int q_tiles = (a.max_q_len + kPfBM - 1) / kPfBM;
+    if (q_tiles > 65535) return KV_ERR_UNSUPPORTED;
+    const dim3 grid(a.num_q_heads, q_tiles, a.batch);
+    fn<<<grid, kPfThreads, kPfSmemBytes, a.stream>>>(tm_q, *a.map_k, *a.map_v, pp);
+    return cuda_status(cudaGetLastError());
+}
+
 }  // namespace pkv
 
 using namespace pkv;
@@ -561,7 +602,7 @@ extern "C" kv_status paged_prefill_attention(kv_pool_t p, const void *q, const i
     if (!p || batch < 0 || total_q < 0 || max_q_len < 0 || max_blocks < 0 || num_q_heads <= 0)
         return KV_ERR_ARG;
     if (kv_status st = require_device(p->device)) return st;
-    if (p->dtype == KV_F32 || p->head_dim != kPfD) return KV_ERR_UNSUPPORTED;
+    if (p->dtype == KV_F32 || p->dtype == KV_I4 || p->head_dim != kPfD) return KV_ERR_UNSUPPORTED;
     if (num_q_heads % p->num_kv_heads) return KV_ERR_ARG;
     if (out_dtype != KV_F32 && out_dtype != p->dtype) return KV_ERR_UNSUPPORTED;
     if (batch == 0 || max_q_len == 0 || total_q == 0) return KV_OK;
@@ -570,35 +611,28 @@ extern "C" kv_status paged_prefill_attention(kv_pool_t p, const void *q, const i
     const long long pool_rows = (long long)p->num_blocks * p->num_kv_heads * 16;
     if (pool_rows > INT32_MAX || batch > 65535) return KV_ERR_UNSUPPORTED;
     if (pool_tensor_maps(p) != KV_OK) return KV_ERR_CUDA;
-    // The q map covers exactly total_q rows: a tile reaching past them reads
-    // zeros, and rows past a chunk or past total_q are never stored.
-    CUtensorMap tm_q;
-    if (!encode_q_map(&tm_q, q, total_q, num_q_heads)) return KV_ERR_CUDA;
-    PrefillParams pp{};
-    pp.cu_q = cu_q;
-    pp.total_q = total_q;
-    pp.tables = block_tables;
-    pp.seq_lens = seq_lens;
-    pp.max_blocks = max_blocks;
-    pp.num_blocks = p->num_blocks;
-    pp.num_q_heads = num_q_heads;
-    pp.num_kv_heads = p->num_kv_heads;
-    pp.g = num_q_heads / p->num_kv_heads;
-    pp.scale_log2 = scale * 1.4426950408889634f;
-    pp.out = out;
-    pp.out_type = out_dtype;
-    pp.lse = lse_out;
-    pp.err = p->err;
-    const bool f16 = p->dtype == KV_F16;
-    auto fn = test_waits_enabled() ? (f16 ? prefill_kernel<true, true> : prefill_kernel<true, false>)
-                                   : (f16 ? prefill_kernel<false, true> : prefill_kernel<false, false>);
-    if (kv_status st0 = cuda_status(cudaFuncSetAttribute(
-            fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kPfSmemBytes)))
-        return st0;
-    const int q_tiles = (max_q_len + kPfBM - 1) / kPfBM;
-    if (q_tiles > 65535) return KV_ERR_UNSUPPORTED;
-    const dim3 grid(num_q_heads, q_tiles, batch);
-    fn<<<grid, kPfThreads, kPfSmemBytes, as_stream(stream)>>>(tm_q, p->tmap_k,
-                                                                         p->tmap_v, pp);
-    return cuda_status(cudaGetLastError());
+    PrefillCall a{};
+    a.q = q;
+    a.q_dtype = p->dtype;
+    a.v_f16 = p->dtype == KV_F16;
+    a.map_k = &p->tmap_k;
+    a.map_v = &p->tmap_v;
+    a.cu_q = cu_q;
+    a.total_q = total_q;
+    a.max_q_len = max_q_len;
+    a.block_tables = block_tables;
+    a.max_blocks = max_blocks;
+    a.num_blocks = p->num_blocks;
+    a.num_kv_heads = p->num_kv_heads;
+    a.seq_lens = seq_lens;
+    a.batch = batch;
+    a.num_q_heads = num_q_heads;
+    a.scale = scale;
+    a.v_mul = 1.f;
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.lse = lse_out;
+    a.err = p->err;
+    a.stream = as_stream(stream);
+    return launch_prefill(a);
 }

@@ -1,0 +1,449 @@
+// Append with the position rotation, and the read of cached tokens.
+//
+// Rotation.  With angle a = pos * f_j of pair j the pair (x1, x2) becomes
+// (x1 cos a - x2 sin a, x2 cos a + x1 sin a); cos and sin come from the caller's
+// fp32 table (angles of far positions need 64 bits, once per table instead of
+// once per token).  The arithmetic is fp32 -- two products and one sum, each
+// rounded, no contraction, so that every caller and every reference that follows
+// the formula gets the same bits -- and the result is rounded once, to the
+// output's type, or quantised unrounded (KV_I4).
+//
+// Work.  Memory-bound: each element is read and written once.  Eight
+// consecutive dimensions (one 16-byte chunk of 16-bit elements) are a thread's
+// share of a row; a row (one head of q, k or v) is D / 8 neighbouring lanes, a
+// warp takes 32 / (D / 8) rows at a time of one token, kRows / that many times:
+// the token's cos and sin are loaded once per thread and the rows' loads are all
+// issued before the first use.  The partner of a half-split pair sits a fixed
+// number of lanes away and comes by shuffle, so that no element is loaded twice
+// and q may be rotated in place.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "common.cuh"
+#include "i4.cuh"
+#include "internal.h"
+
+namespace pkv {
+
+constexpr int kRopeThreads = 256;
+
+struct RopeParams {
+    const char *q, *k, *v;             // input rows, heads packed within a token
+    long long q_stride, k_stride, v_stride, q_out_stride;  // bytes between tokens
+    char *q_out;
+    char *k_pool, *v_pool;
+    const int64_t *slots;
+    const int32_t *positions;
+    const float *table;                // [max_position][rot / 2 cos, rot / 2 sin]
+    int max_position;
+    int rot;                           // rotated dimensions (0: none)
+    int interleaved;
+    int hq, hkv;                       // hq = 0: no q
+    long long num_tokens, num_slots;
+    float k_inv, v_inv;                // 1 / pool scales (KV_I4)
+    int *err;
+};
+
+// Eight elements of type ET as fp32 and back.
+template <int ET>
+struct Octet {
+    static constexpr int kWords = ET == KV_F32 ? 8 : 4;
+    uint32_t w[kWords];
+    KV_DEVICE void load(const char *src) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(src);
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) {
+            const uint4 u = p[i];
+            w[4 * i] = u.x;
+            w[4 * i + 1] = u.y;
+            w[4 * i + 2] = u.z;
+            w[4 * i + 3] = u.w;
+        }
+    }
+    KV_DEVICE void store(char *dst) const {
+        uint4 *p = reinterpret_cast<uint4 *>(dst);
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) p[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    KV_DEVICE void get(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (ET == KV_F32) {
+                x[2 * i] = __uint_as_float(w[2 * i]);
+                x[2 * i + 1] = __uint_as_float(w[2 * i + 1]);
+            } else {
+                const float2 f = ET == KV_BF16 ? bf16x2_to_float2(w[i]) : f16x2_to_float2(w[i]);
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            }
+        }
+    }
+    KV_DEVICE void set(const float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (ET == KV_F32) {
+                w[2 * i] = __float_as_uint(x[2 * i]);
+                w[2 * i + 1] = __float_as_uint(x[2 * i + 1]);
+            } else if constexpr (ET == KV_BF16) {
+                w[i] = float_to_bf16_rn(x[2 * i]) | (uint32_t)float_to_bf16_rn(x[2 * i + 1]) << 16;
+            } else {
+                w[i] = float_to_f16_rn(x[2 * i]) | (uint32_t)float_to_f16_rn(x[2 * i + 1]) << 16;
+            }
+        }
+    }
+};
+
+// Quantises this lane's octet o of a K (V = false) or V row of token offset t
+// (0..15) and stores it into the tile; the two lanes of a group share its scale.
+// Every lane of the warp takes part in the shuffle, `live` lanes store.
+template <int D, bool V>
+KV_DEVICE void store_i4(char *tile, int t, int o, float (&x)[8], float inv, bool live) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] *= inv;  // a power of two
+        m = i4::max_nan(m, fabsf(x[i]));
+    }
+    m = i4::max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const uint32_t sb = i4::e4m3_of(__fdiv_rn(m, 7.f));
+    const uint32_t w = i4::codes8(x, i4::e4m3_to_float(sb));
+    if (!live) return;
+    if constexpr (V) {
+        uint16_t *c = reinterpret_cast<uint16_t *>(tile) + (t >> 1) * (D / 2) + 4 * o + (t & 1);
+        c[0] = (uint16_t)w;          // quad 2 o
+        c[2] = (uint16_t)(w >> 16);  // quad 2 o + 1
+        if (!(o & 1)) tile[8 * D + (t >> 1) * (D / 8) + o + (t & 1)] = (char)sb;
+    } else {
+        reinterpret_cast<uint32_t *>(tile)[t * (D / 8) + o] = w;
+        if (!(o & 1)) tile[8 * D + t * (D / 16) + (o >> 1)] = (char)sb;
+    }
+}
+
+// IN: type of the rows; I4: 4-bit pool, else the pool holds type IN.  R: rows
+// of a token per warp (a multiple of 32 / (D / 8)).
+template <int D, int IN, bool I4, int R>
+__global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopeParams p) {
+    constexpr int kLanes = D / 8;         // lanes of one row
+    constexpr int kAtOnce = 32 / kLanes;  // rows of one pass
+    constexpr int kPasses = R / kAtOnce;
+    constexpr int kE = IN == KV_F32 ? 4 : 2;
+    const int lane = threadIdx.x & 31, o = lane % kLanes, sub = lane / kLanes;
+    const int rows = p.hq + 2 * p.hkv;
+    const int units = (rows + R - 1) / R;
+    const long long total = p.num_tokens * units;
+    const long long stride = (long long)gridDim.x * (kRopeThreads / 32);
+    for (long long wi = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); wi < total; wi += stride) {
+        const long long tok = wi / units;
+        const int row0 = (int)(wi - tok * units) * R + sub;
+        // ---- the rows' loads
+        Octet<IN> x[kPasses];
+        int row[kPasses];
+#pragma unroll
+        for (int u = 0; u < kPasses; ++u) {
+            row[u] = row0 + u * kAtOnce;
+            const int r = row[u];
+            const char *src = nullptr;
+            if (r < p.hq)
+                src = p.q + tok * p.q_stride + (long long)r * (D * kE);
+            else if (r < p.hq + p.hkv)
+                src = p.k + tok * p.k_stride + (long long)(r - p.hq) * (D * kE);
+            else if (r < rows)
+                src = p.v + tok * p.v_stride + (long long)(r - p.hq - p.hkv) * (D * kE);
+            if (src) {
+                x[u].load(src + o * (8 * kE));
+            } else {
+#pragma unroll
+                for (int i = 0; i < Octet<IN>::kWords; ++i) x[u].w[i] = 0;
+            }
+        }
+        long long slot = __ldg(p.slots + tok);
+        if (slot >= p.num_slots) {
+            if (lane == 0 && wi == tok * units) atomicOr(p.err, KV_DEVERR_SLOT_RANGE);
+            slot = -1;
+        }
+        // ---- cos and sin of this lane's pairs
+        float c[8], s[8];
+        const bool rotates = 8 * o < p.rot;
+        if (p.rot > 0) {
+            const int pos = __ldg(p.positions + tok);
+            if (pos < 0 || pos >= p.max_position) {  // the token is left out
+                if (lane == 0 && wi == tok * units) atomicOr(p.err, KV_DEVERR_POSITION);
+                continue;
+            }
+            if (rotates) {
+                const float *cs = p.table + (long long)pos * p.rot;
+                const int half = p.rot / 2;
+                if (p.interleaved) {  // pairs 4 o .. 4 o + 3
+                    const float4 c4 = *reinterpret_cast<const float4 *>(cs + 4 * o);
+                    const float4 s4 = *reinterpret_cast<const float4 *>(cs + half + 4 * o);
+                    c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
+                    s[0] = s4.x, s[1] = s4.y, s[2] = s4.z, s[3] = s4.w;
+                } else {  // pairs j0 .. j0 + 7
+                    const int j0 = 8 * o < half ? 8 * o : 8 * o - half;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 c4 = *reinterpret_cast<const float4 *>(cs + j0 + 4 * i);
+                        const float4 s4 = *reinterpret_cast<const float4 *>(cs + half + j0 + 4 * i);
+                        c[4 * i] = c4.x, c[4 * i + 1] = c4.y, c[4 * i + 2] = c4.z, c[4 * i + 3] = c4.w;
+                        s[4 * i] = s4.x, s[4 * i + 1] = s4.y, s[4 * i + 2] = s4.z, s[4 * i + 3] = s4.w;
+                    }
+                }
+            }
+        }
+        // ---- rotate and store
+        const int step = p.rot / 16;  // lanes between the halves of a pair
+        const bool first = o < step;
+        const int partner = (lane & ~(kLanes - 1)) + (!rotates || p.interleaved ? o : first ? o + step : o - step);
+#pragma unroll
+        for (int u = 0; u < kPasses; ++u) {
+            const int r = row[u];
+            float y[8];
+            x[u].get(y);
+            bool changed = false;
+            if (p.rot > 0) {
+                const bool turn = rotates && r < p.hq + p.hkv;
+                if (p.interleaved) {
+                    if (turn) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float x1 = y[2 * i], x2 = y[2 * i + 1];
+                            y[2 * i] = __fsub_rn(__fmul_rn(x1, c[i]), __fmul_rn(x2, s[i]));
+                            y[2 * i + 1] = __fadd_rn(__fmul_rn(x2, c[i]), __fmul_rn(x1, s[i]));
+                        }
+                    }
+                } else {
+                    Octet<IN> other;
+#pragma unroll
+                    for (int i = 0; i < Octet<IN>::kWords; ++i)
+                        other.w[i] = __shfl_sync(0xffffffffu, x[u].w[i], partner);
+                    if (turn) {
+                        float z[8];
+                        other.get(z);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float a = __fmul_rn(y[i], c[i]), b = __fmul_rn(z[i], s[i]);
+                            y[i] = first ? __fsub_rn(a, b) : __fadd_rn(a, b);
+                        }
+                    }
+                }
+                changed = turn;
+            }
+            const bool is_q = r < p.hq, is_v = r >= p.hq + p.hkv;
+            if (is_q) {
+                if (changed) x[u].set(y);
+                x[u].store(p.q_out + tok * p.q_out_stride + (long long)r * (D * kE) + o * (8 * kE));
+            }
+            const int h = is_v ? r - p.hq - p.hkv : r - p.hq;
+            const bool live = !is_q && r < rows && slot >= 0;
+            if constexpr (I4) {
+                // whole warps quantise: the group's lanes exchange their maxima
+                const long long tile_id = live ? (slot >> 4) * p.hkv + h : 0;
+                const int t = (int)(slot & 15);
+                if (__any_sync(0xffffffffu, live && !is_v))
+                    store_i4<D, false>(p.k_pool + tile_id * (9 * D), t, o, y, p.k_inv, live && !is_v);
+                if (__any_sync(0xffffffffu, live && is_v)) {
+                    float z[8];
+                    x[u].get(z);
+                    store_i4<D, true>(p.v_pool + tile_id * (9 * D), t, o, z, p.v_inv, live && is_v);
+                }
+            } else if (live) {
+                if (changed) x[u].set(y);
+                const long long prow = ((slot >> 4) * p.hkv + h) * 16 + (slot & 15);
+                x[u].store((is_v ? p.v_pool : p.k_pool) + prow * (D * kE) + o * (8 * kE));
+            }
+        }
+    }
+}
+
+// Cached tokens as rows: token i's K and V rows [hkv][D] of type OUT from slot
+// slots[i].  A thread takes an octet; ET: the pool's type (KV_I4: codes).
+template <int D, int ET, int OUT>
+__global__ void __launch_bounds__(256) read_tokens_kernel(const char *__restrict__ k_pool,
+                                                          const char *__restrict__ v_pool,
+                                                          const int64_t *__restrict__ slots, long long num_tokens,
+                                                          int hkv, long long num_slots, float k_scale,
+                                                          float v_scale, char *__restrict__ k_out,
+                                                          char *__restrict__ v_out, int *err) {
+    constexpr int kLanes = D / 8;
+    constexpr int kE = OUT == KV_F32 ? 4 : 2;
+    const long long total = num_tokens * hkv * kLanes;
+    const long long stride = (long long)gridDim.x * blockDim.x;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
+        const long long row = i / kLanes;
+        const int o = (int)(i % kLanes);
+        const long long tok = row / hkv;
+        const int h = (int)(row - tok * hkv);
+        const long long slot = __ldg(slots + tok);
+        if (slot >= num_slots) {
+            if (o == 0 && h == 0) atomicOr(err, KV_DEVERR_SLOT_RANGE);
+            continue;
+        }
+        if (slot < 0) continue;
+        const int t = (int)(slot & 15);
+        const long long tile = (slot >> 4) * hkv + h;
+        Octet<OUT> ko, vo;
+        if constexpr (ET == KV_I4) {
+            const char *kt = k_pool + tile * (9 * D), *vt = v_pool + tile * (9 * D);
+            const uint32_t kw = reinterpret_cast<const uint32_t *>(kt)[t * (D / 8) + o];
+            const float ks = i4::e4m3_to_float((uint8_t)kt[8 * D + t * (D / 16) + (o >> 1)]) * k_scale;
+            const uint16_t *vc = reinterpret_cast<const uint16_t *>(vt) + (t >> 1) * (D / 2) + 4 * o + (t & 1);
+            const uint32_t vw = vc[0] | (uint32_t)vc[2] << 16;
+            const float vs = i4::e4m3_to_float((uint8_t)vt[8 * D + (t >> 1) * (D / 8) + (o & ~1) + (t & 1)]) * v_scale;
+            float a[8], b[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a[j] = (float)((int)(kw >> (4 * j) & 15u) - 8) * ks;
+                b[j] = (float)((int)(vw >> (4 * j) & 15u) - 8) * vs;
+            }
+            ko.set(a);
+            vo.set(b);
+        } else {
+            const long long at = (tile * 16 + t) * (D * kE) + o * (8 * kE);
+            ko.load(k_pool + at);
+            vo.load(v_pool + at);
+        }
+        ko.store(k_out + i * (8 * kE));
+        vo.store(v_out + i * (8 * kE));
+    }
+}
+
+template <int D, int IN, bool I4>
+static void launch_append_rope(const RopeParams &p, cudaStream_t s) {
+    constexpr int kAtOnce = 32 / (D / 8);
+    const long long rows = p.hq + 2LL * p.hkv;
+    // Rows per warp: few while that leaves SMs idle (a decode step), more when
+    // there are warps enough, so that a token's cos and sin serve more rows.
+    const int sms = sm_count();
+    auto go = [&](auto fn, int r) {
+        const long long warps = p.num_tokens * ((rows + r - 1) / r);
+        long long blocks = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+        if (blocks > (1LL << 30)) blocks = 1LL << 30;
+        fn<<<(unsigned)blocks, kRopeThreads, 0, s>>>(p);
+    };
+    if (p.num_tokens * ((rows + 4 * kAtOnce - 1) / (4 * kAtOnce)) >= 16LL * sms)
+        go(append_rope_kernel<D, IN, I4, 4 * kAtOnce>, 4 * kAtOnce);
+    else
+        go(append_rope_kernel<D, IN, I4, kAtOnce>, kAtOnce);
+}
+
+template <int D, int ET, int OUT>
+static void launch_read(kv_pool_t p, const int64_t *slots, long long n, void *k_out, void *v_out, cudaStream_t s) {
+    const long long total = n * p->num_kv_heads * (D / 8);
+    long long blocks = (total + 255) / 256;
+    if (blocks > (1LL << 30)) blocks = 1LL << 30;
+    read_tokens_kernel<D, ET, OUT><<<(unsigned)blocks, 256, 0, s>>>(
+        (const char *)p->k, (const char *)p->v, slots, n, p->num_kv_heads, (long long)p->num_blocks * 16, p->k_scale,
+        p->v_scale, (char *)k_out, (char *)v_out, p->err);
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+kv_status kv_append_rope(kv_pool_t p, const void *k_new, const void *v_new, kv_dtype in_dtype, int64_t k_stride,
+                         int64_t v_stride, const int64_t *slot_mapping, const int32_t *positions,
+                         const float *cos_sin, int max_position, int rot_dim, int interleaved, const void *q,
+                         void *q_out, int64_t q_stride, int64_t q_out_stride, int num_q_heads, int num_tokens,
+                         void *stream) {
+    if (!p || num_tokens < 0 || rot_dim < 0 || k_stride < 0 || v_stride < 0 || q_stride < 0 || q_out_stride < 0 ||
+        (interleaved != 0 && interleaved != 1))
+        return KV_ERR_ARG;
+    if (in_dtype != KV_F32 && in_dtype != KV_BF16 && in_dtype != KV_F16) return KV_ERR_UNSUPPORTED;
+    if (p->dtype != KV_I4 && in_dtype != p->dtype) return KV_ERR_ARG;
+    const int d = p->head_dim, e = dtype_bytes(in_dtype);
+    if (rot_dim > d || rot_dim % 16) return KV_ERR_ARG;
+    if (rot_dim > 0 && max_position <= 0) return KV_ERR_ARG;
+    if (q && (rot_dim == 0 || !q_out || num_q_heads <= 0)) return KV_ERR_ARG;
+    const int64_t kv_row = (int64_t)p->num_kv_heads * d, q_row = q ? (int64_t)num_q_heads * d : 0;
+    if (k_stride == 0) k_stride = kv_row;
+    if (v_stride == 0) v_stride = kv_row;
+    if (q_stride == 0) q_stride = q_row;
+    if (q_out_stride == 0) q_out_stride = q == q_out ? q_stride : q_row;
+    if (k_stride < kv_row || v_stride < kv_row || q_stride < q_row || q_out_stride < q_row) return KV_ERR_ARG;
+    if (q && q == q_out && q_stride != q_out_stride) return KV_ERR_ARG;
+    // rows move in 16-byte chunks
+    if ((k_stride * e) % 16 || (v_stride * e) % 16 || (q_stride * e) % 16 || (q_out_stride * e) % 16) return KV_ERR_ARG;
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new) |
+                           reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q ? q_out : nullptr) |
+                           reinterpret_cast<uintptr_t>(rot_dim > 0 ? cos_sin : nullptr);
+    if (bits & 15) return KV_ERR_ARG;
+    if (kv_status st = require_device(p->device)) return st;
+    if (num_tokens == 0) return KV_OK;
+    if (!k_new || !v_new || !slot_mapping || (rot_dim > 0 && (!positions || !cos_sin))) return KV_ERR_ARG;
+    RopeParams r{};
+    r.q = static_cast<const char *>(q);
+    r.k = static_cast<const char *>(k_new);
+    r.v = static_cast<const char *>(v_new);
+    r.q_stride = q_stride * e;
+    r.k_stride = k_stride * e;
+    r.v_stride = v_stride * e;
+    r.q_out_stride = q_out_stride * e;
+    r.q_out = static_cast<char *>(q_out);
+    r.k_pool = static_cast<char *>(p->k);
+    r.v_pool = static_cast<char *>(p->v);
+    r.slots = slot_mapping;
+    r.positions = positions;
+    r.table = cos_sin;
+    r.max_position = max_position;
+    r.rot = rot_dim;
+    r.interleaved = interleaved;
+    r.hq = q ? num_q_heads : 0;
+    r.hkv = p->num_kv_heads;
+    r.num_tokens = num_tokens;
+    r.num_slots = (long long)p->num_blocks * p->block_size;
+    r.k_inv = 1.f / p->k_scale;
+    r.v_inv = 1.f / p->v_scale;
+    r.err = p->err;
+    const cudaStream_t s = as_stream(stream);
+    auto by_type = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        const bool i4 = p->dtype == KV_I4;
+        if (in_dtype == KV_F32)
+            i4 ? launch_append_rope<D, KV_F32, true>(r, s) : launch_append_rope<D, KV_F32, false>(r, s);
+        else if (in_dtype == KV_BF16)
+            i4 ? launch_append_rope<D, KV_BF16, true>(r, s) : launch_append_rope<D, KV_BF16, false>(r, s);
+        else
+            i4 ? launch_append_rope<D, KV_F16, true>(r, s) : launch_append_rope<D, KV_F16, false>(r, s);
+    };
+    if (d == 128)
+        by_type(std::integral_constant<int, 128>{});
+    else
+        by_type(std::integral_constant<int, 64>{});
+    return cuda_status(cudaGetLastError());
+}
+
+kv_status kv_read_tokens(kv_pool_t p, const int64_t *slots, int num_tokens, void *k_out, void *v_out,
+                         kv_dtype out_dtype, void *stream) {
+    if (!p || num_tokens < 0) return KV_ERR_ARG;
+    if (out_dtype != KV_F32 && out_dtype != KV_BF16 && out_dtype != KV_F16) return KV_ERR_UNSUPPORTED;
+    if (p->dtype != KV_I4 && out_dtype != p->dtype) return KV_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 15) return KV_ERR_ARG;
+    if (kv_status st = require_device(p->device)) return st;
+    if (num_tokens == 0) return KV_OK;
+    if (!slots || !k_out || !v_out) return KV_ERR_ARG;
+    const cudaStream_t s = as_stream(stream);
+    auto by_type = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        if (p->dtype == KV_I4) {
+            if (out_dtype == KV_F32) launch_read<D, KV_I4, KV_F32>(p, slots, num_tokens, k_out, v_out, s);
+            if (out_dtype == KV_BF16) launch_read<D, KV_I4, KV_BF16>(p, slots, num_tokens, k_out, v_out, s);
+            if (out_dtype == KV_F16) launch_read<D, KV_I4, KV_F16>(p, slots, num_tokens, k_out, v_out, s);
+        } else if (p->dtype == KV_F32) {
+            launch_read<D, KV_F32, KV_F32>(p, slots, num_tokens, k_out, v_out, s);
+        } else {  // rows of 16 bits are moved, whatever they mean
+            launch_read<D, KV_BF16, KV_BF16>(p, slots, num_tokens, k_out, v_out, s);
+        }
+    };
+    if (p->head_dim == 128)
+        by_type(std::integral_constant<int, 128>{});
+    else
+        by_type(std::integral_constant<int, 64>{});
+    return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

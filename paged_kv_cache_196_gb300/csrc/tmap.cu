@@ -58,7 +58,7 @@ bool encode_q_map(CUtensorMap *m, const void *q, int rows, int hq) {
 
 kv_status pool_tensor_maps(kv_pool *p) {
     if (p->tmaps_ready) return KV_OK;
-    if (p->dtype == KV_F32 || p->head_dim != 128) return KV_ERR_UNSUPPORTED;
+    if (p->dtype == KV_F32 || p->dtype == KV_I4 || p->head_dim != 128) return KV_ERR_UNSUPPORTED;
     const long long rows = (long long)p->num_blocks * p->num_kv_heads * 16;
     if (rows > INT32_MAX) return KV_ERR_UNSUPPORTED;
     if (!encode_rows_map(&p->tmap_k, p->k, rows) || !encode_rows_map(&p->tmap_v, p->v, rows))
