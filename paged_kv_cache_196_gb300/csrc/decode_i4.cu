@@ -8,16 +8,18 @@
 // in 16 bits, while every code still has to become an fp16 operand.  So the
 // kernel is written around the number of instructions per code: one logical
 // operation and one fused multiply-add make two codes into a scaled fp16 pair
-// (i4::values8: 10 instructions for 8 codes), the layout of a tile puts each
+// (i4::values8: 9 instructions for 8 codes), the layout of a tile puts each
 // lane's operands of the tensor core's fragments into consecutive bytes (no
-// ldmatrix, no shuffles), and the scales of a lane's rows are two bytes a load.
+// ldmatrix, no shuffles), the scales of a lane's rows are two bytes a load, and a
+// warp takes NB blocks at a time, so that waiting, issuing, the maximum over lanes
+// and the test for a new maximum are paid once per NB blocks.
 //
 // Shape.  One CTA = a run of blocks of one (sequence, kv head) for all its query
 // columns (head of the group, and query token where there are several); four
-// warps, warp w takes blocks w, w + 4, ... and keeps its own softmax state.  Each
-// warp feeds itself: lane 0 issues the two bulk copies of a tile into the warp's
-// own ring, and issues the next one into a stage as soon as the warp has it in
-// registers.  No producer warp, no barrier between warps before the end.
+// warps, warp w takes the block groups w, w + 4, ... and keeps its own softmax state.
+// Each warp feeds itself: lane i issues the two bulk copies of block i of a group
+// into the warp's own ring, the next group into a stage as soon as the warp has the
+// old one in registers.  No producer warp, no barrier between warps before the end.
 //
 // Products.  S^T[16 tokens][8 columns] = K q^T and O^T[16 dims][8 columns] += V^T
 // P^T on mma.sync m16n8k16 with fp32 sums.  The contraction over dimensions may run
@@ -42,11 +44,12 @@ namespace pkv {
 
 constexpr int kI4Warps = 4;
 constexpr int kI4Threads = kI4Warps * 32;
-constexpr int kI4Stages = 4;   // ring stages of one warp (a power of two)
 constexpr int kI4BS = 16;
-// The weights are 2^(s - m + 10): at most 1024, so that fp16 keeps 10 more
-// binary places of the small ones before they become subnormal.
-constexpr float kI4Bias = 10.f;
+// The weights are 2^(s - m + 6) for a reference m that is renewed (and the state
+// rescaled) only when the maximum passes it by more than 2^8: rarely after the
+// first blocks, and exact mathematics, since sums and outputs share m.  They stay
+// below 2^14, in fp16's range, and the largest seen is at least 2^6.
+constexpr float kI4Bias = 6.f, kI4Renew = 8.f;
 
 struct I4Params {
     const uint16_t *q;      // rows [hq][D], bf16 or fp16
@@ -58,8 +61,8 @@ struct I4Params {
     int max_blocks, num_blocks;
     const int32_t *seq_lens, *seq_order;
     int batch, hq, hkv, g;
-    float scale_log2;       // softmax scale * log2(e) * 4 * the pool's K scale
-    float v_mul;            // 4 * the pool's V scale
+    float scale_log2;       // softmax scale * log2(e) * kScaleUnit * the pool's K scale
+    float v_mul;            // kScaleUnit * the pool's V scale
     int part_blocks, max_splits;
     int col_groups;         // CTAs that share a partition's columns
     void *out;
@@ -110,11 +113,6 @@ KV_DEVICE uint32_t half_pair(float lo, float hi) {
     return r;
 }
 
-// Two e4m3 scales of a tile, a quarter of their value, as an fp16 pair.
-KV_DEVICE __half2 quarter_scales(uint32_t two) {
-    return __hmul2(i4::e4m3x2_to_half2(two), __float2half2_rn(0.25f));
-}
-
 // N words of shared memory, 16 or 8 bytes at once.
 template <int N>
 KV_DEVICE void load_words(const char *src, uint32_t (&w)[N]) {
@@ -127,15 +125,16 @@ KV_DEVICE void load_words(const char *src, uint32_t (&w)[N]) {
     }
 }
 
-template <int D>
+// Shared memory: the warps' rings (NST stages of NB blocks), reused by the merges.
+template <int D, int NB, int NST>
 constexpr size_t i4_ring_bytes() {
-    const size_t ring = (size_t)kI4Warps * kI4Stages * 2 * 9 * D;
+    const size_t ring = (size_t)kI4Warps * NST * NB * 2 * 9 * D;
     const size_t merge = (size_t)kI4Warps * 8 * D * 4 + 4096;
     return ((ring > merge ? ring : merge) + 127) / 128 * 128;
 }
-template <int D>
+template <int D, int NB, int NST>
 constexpr size_t i4_smem_bytes() {
-    return i4_ring_bytes<D>() + (size_t)kI4Warps * kI4Stages * (sizeof(uint64_t) + sizeof(int));
+    return i4_ring_bytes<D, NB, NST>() + (size_t)kI4Warps * NST * (sizeof(uint64_t) + NB * sizeof(int));
 }
 
 // The sequence of a CTA: rows of its queries, keys, partition.  False: nothing to do.
@@ -178,13 +177,14 @@ KV_DEVICE bool i4_sequence(const I4Params &p, int b, bool report, I4Work &w) {
 }
 
 // D: head dim.  NT: columns / 8 of a CTA.  EXACT: weights in two fp16 parts (fp32
-// output).  TW: waits read their limit at run time (tests).
-template <int D, int NT, bool EXACT, bool TW, int MINB>
+// output).  TW: waits read their limit at run time (tests).  NB: blocks of a group;
+// NST: ring stages; MINB: CTAs per SM it is built for.
+template <int D, int NT, bool EXACT, bool TW, int NB, int NST, int MINB>
 __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Params p) {
     constexpr int kTile = 9 * D;
     constexpr int kW = D / 32;        // words of a quarter row of K, of a lane's dims of a V pair
     constexpr int kSteps = D / 16;    // products along D
-    constexpr int kNst = kI4Stages;
+    constexpr int kStage = NB * 2 * kTile;  // K tiles, then V tiles
     const int split = blockIdx.x, h = blockIdx.y;
     int b = blockIdx.z / p.col_groups;
     const int cg = blockIdx.z % p.col_groups;
@@ -208,53 +208,52 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
     if (ncols <= 0) return;
 
     extern __shared__ __align__(128) char smem[];
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + i4_ring_bytes<D>()) + warp * kNst;
-    volatile int *valid = reinterpret_cast<int *>(smem + i4_ring_bytes<D>() + kI4Warps * kNst * sizeof(uint64_t)) + warp * kNst;
-    char *ring = smem + (size_t)warp * kNst * 2 * kTile;
+    constexpr size_t kRing = i4_ring_bytes<D, NB, NST>();
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRing) + warp * NST;
+    volatile int *valid = reinterpret_cast<int *>(smem + kRing + kI4Warps * NST * sizeof(uint64_t)) + warp * NST * NB;
+    char *ring = smem + (size_t)warp * NST * kStage;
     __shared__ uint2 s_q[kSteps * NT * 32];
     __shared__ float s_scale[8 * NT];
     __shared__ float s_m[kI4Warps * 8], s_l[kI4Warps * 8];
     __shared__ int s_last;
 
     if (lane == 0) {
-        for (int st = 0; st < kNst; ++st) mbar_init(&full[st], 1);
+        for (int st = 0; st < NST; ++st) mbar_init(&full[st], NB);
         mbar_init_fence();
     }
     __syncwarp();
 
-    // ---- this warp's blocks: warp, warp + 4, ... of the partition
-    const int nown = w.nloc > warp ? (w.nloc - warp + kI4Warps - 1) / kI4Warps : 0;
-    const int32_t *row = p.tables + (size_t)b * p.max_blocks + w.blk0 + warp;
-    // table entries of 32 own blocks at a time, the next 32 already under way
-    int ids = lane < nown ? __ldg(row + kI4Warps * lane) : -1;
-    int ids_next = 32 + lane < nown ? __ldg(row + kI4Warps * (32 + lane)) : -1;
+    // ---- this warp's groups: NB blocks from NB (warp + 4 j) on
+    const int ngroups = (w.nloc + NB - 1) / NB;
+    const int nown = ngroups > warp ? (ngroups - warp + kI4Warps - 1) / kI4Warps : 0;
+    // lane i < NB issues block i of each group; its table entry is read one group ahead
+    int next = NB * warp + lane;  // block of the partition this lane issues next
+    const int32_t *row = p.tables + (size_t)b * p.max_blocks + w.blk0;
+    int id_next = lane < NB && next < w.nloc ? __ldg(row + next) : -1;
     const uint64_t policy = l2_evict_first_policy();
     int issued = 0;
-    auto issue = [&]() {  // the copies of own block `issued`, in its turn
-        const int j = issued++;
-        if (j > 0 && (j & 31) == 0) {
-            ids = ids_next;
-            ids_next = j + 32 + lane < nown ? __ldg(row + kI4Warps * (j + 32 + lane)) : -1;
-        }
-        const int id = __shfl_sync(0xffffffffu, ids, j & 31);
-        if (lane == 0) {
-            const int st = j % kNst;
-            const bool ok = id >= 0 && id < p.num_blocks;
-            valid[st] = ok;
+    auto issue = [&](int st) {  // the copies of own group `issued` into stage st
+        ++issued;
+        if (lane < NB) {
+            const bool ok = id_next >= 0 && id_next < p.num_blocks;
+            valid[st * NB + lane] = ok;
             if (ok) {
-                const size_t off = ((size_t)id * p.hkv + h) * kTile;
-                char *dst = ring + st * 2 * kTile;
+                const size_t off = ((size_t)id_next * p.hkv + h) * kTile;
+                char *dst = ring + st * kStage + lane * kTile;
                 mbar_arrive_expect_tx(&full[st], 2 * kTile);
                 bulk_g2s(dst, p.k_pool + off, kTile, &full[st], policy);
-                bulk_g2s(dst + kTile, p.v_pool + off, kTile, &full[st], policy);
+                bulk_g2s(dst + NB * kTile, p.v_pool + off, kTile, &full[st], policy);
             } else {
-                atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
+                if (next < w.nloc) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
                 mbar_arrive(&full[st]);
             }
+            next += NB * kI4Warps;
+            id_next = next < w.nloc ? __ldg(row + next) : -1;
         }
     };
-#pragma unroll 1
-    for (int j = 0; j < kNst && j < nown; ++j) issue();
+#pragma unroll
+    for (int j = 0; j < NST; ++j)
+        if (j < nown) issue(j);
 
     // Test instantiation with a limit of 0: a tile that is not there at once is a
     // wait that ran out (try_wait would sleep until it came).
@@ -290,7 +289,9 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         // exponent field of the largest; 0 (all zero or below normal) and 255 are left alone
         const int e = (int)(__float_as_uint(m) >> 23);
         const int up = e == 0 || e == 255 ? 0 : max(-126, min(126, 127 + 13 - e));
-        const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+        // the score's factor is made positive (its sign goes to q), so that scaling keeps
+        // the order of scores; a factor of 0 zeroes q instead
+        const float mul = copysignf(p.scale_log2 == 0.f ? 0.f : __uint_as_float((uint32_t)(127 + up) << 23), p.scale_log2);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             // dimension d: quarter cq, word wi, four bits n; pair n of half d / 4 % 2
@@ -299,7 +300,8 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             qs[((((pair >> 1) * NT + (col >> 3)) * 32 + (col & 7) * 4 + cq) * 2 + (pair & 1)) * 2 + hi] =
                 __float2half_rn(x[i] * mul);
         }
-        if (lane == 0) s_scale[col] = p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
+        if (lane == 0)
+            s_scale[col] = p.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 - up) << 23), 1e-37f);
     }
     __syncthreads();
 
@@ -320,143 +322,193 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         }
     const int least = (int)(w.L - w.T) + col0 / p.g + 1;  // keys that every column sees
 
+    int st = 0;
+    uint32_t parity = 0;
     for (int j = 0; j < nown && !stop; ++j) {
-        const int st = j % kNst;
-        const bool bad = !mbar_wait<TW>(&full[st], (j / kNst) & 1, p.err);
+        const bool bad = !mbar_wait<TW>(&full[st], parity, p.err);
         if (__any_sync(0xffffffffu, bad)) break;
-        const char *kt = ring + st * 2 * kTile, *vt = kt + kTile;
-        const int tok0 = (w.blk0 + warp + kI4Warps * j) * kI4BS;
-        const int ntok = valid[st] ? min(kI4BS, (int)(w.L - tok0)) : 0;
-        // ---- operands: tokens r, r + 8 of K; token pairs c, c + 4 of V
-        uint32_t k0[kW], k1[kW], v0[kW], v1[kW];
-        load_words<kW>(kt + r * (D / 2) + c * (D / 8), k0);
-        load_words<kW>(kt + (r + 8) * (D / 2) + c * (D / 8), k1);
-        load_words<kW>(vt + c * D + r * (D / 8), v0);
-        load_words<kW>(vt + (c + 4) * D + r * (D / 8), v1);
-        uint32_t ks0, ks1, vs0, vs1;
-        if constexpr (D == 128) {
-            ks0 = *reinterpret_cast<const uint16_t *>(kt + 8 * D + r * 8 + 2 * c);
-            ks1 = *reinterpret_cast<const uint16_t *>(kt + 8 * D + (r + 8) * 8 + 2 * c);
-            vs0 = *reinterpret_cast<const uint16_t *>(vt + 8 * D + c * 16 + 2 * r);
-            vs1 = *reinterpret_cast<const uint16_t *>(vt + 8 * D + (c + 4) * 16 + 2 * r);
-        } else {
-            ks0 = *reinterpret_cast<const uint8_t *>(kt + 8 * D + r * 4 + c);
-            ks1 = *reinterpret_cast<const uint8_t *>(kt + 8 * D + (r + 8) * 4 + c);
-            vs0 = *reinterpret_cast<const uint16_t *>(vt + 8 * D + c * 8 + (r & ~1));
-            vs1 = *reinterpret_cast<const uint16_t *>(vt + 8 * D + (c + 4) * 8 + (r & ~1));
-        }
-        // ---- S^T = K q^T
-        float s[NT][4];
+        const char *stage = ring + st * kStage;
+        const int blk = w.blk0 + NB * (warp + kI4Warps * j);
+        const int tok0 = blk * kI4BS;
+        // ---- S^T = K q^T: tokens r, r + 8 of each block
+        float s[NB][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[n][nt][0] = s[n][nt][1] = s[n][nt][2] = s[n][nt][3] = 0.f;
         {
-            const __half2 a = quarter_scales(ks0), e = quarter_scales(ks1);
-            i4::Scale g0, g1;
+            uint32_t k0[NB][kW], k1[NB][kW];
+            __half2 a0[NB], a1[NB];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const char *kt = stage + n * kTile;
+                load_words<kW>(kt + r * (D / 2) + c * (D / 8), k0[n]);
+                load_words<kW>(kt + (r + 8) * (D / 2) + c * (D / 8), k1[n]);
+                uint32_t s0, s1;
+                if constexpr (D == 128) {
+                    s0 = *reinterpret_cast<const uint16_t *>(kt + 8 * D + r * 8 + 2 * c);
+                    s1 = *reinterpret_cast<const uint16_t *>(kt + 8 * D + (r + 8) * 8 + 2 * c);
+                } else {
+                    s0 = *reinterpret_cast<const uint8_t *>(kt + 8 * D + r * 4 + c);
+                    s1 = *reinterpret_cast<const uint8_t *>(kt + 8 * D + (r + 8) * 4 + c);
+                }
+                a0[n] = i4::scale_pair(s0);
+                a1[n] = i4::scale_pair(s1);
+            }
+            i4::Scale g0[NB], g1[NB];
 #pragma unroll
             for (int wi = 0; wi < kW; ++wi) {
-                if (wi == 0) {
-                    g0 = i4::make_scale(__low2half2(a));
-                    g1 = i4::make_scale(__low2half2(e));
-                } else if (D == 128 && wi == 2) {
-                    g0 = i4::make_scale(__high2half2(a));
-                    g1 = i4::make_scale(__high2half2(e));
+                uint32_t x0[NB][4], x1[NB][4];
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    if (wi == 0) {
+                        g0[n] = i4::make_scale(__low2half2(a0[n]));
+                        g1[n] = i4::make_scale(__low2half2(a1[n]));
+                    } else if (D == 128 && wi == 2) {
+                        g0[n] = i4::make_scale(__high2half2(a0[n]));
+                        g1[n] = i4::make_scale(__high2half2(a1[n]));
+                    }
+                    i4::values8(k0[n][wi], g0[n], x0[n]);
+                    i4::values8(k1[n][wi], g1[n], x1[n]);
                 }
-                uint32_t x0[4], x1[4];
-                i4::values8(k0[wi], g0, x0);
-                i4::values8(k1[wi], g1, x1);
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const uint2 bq = s_q[((2 * wi + f) * NT + nt) * 32 + lane];
-                        mma_16816(s[nt], x0[2 * f], x1[2 * f], x0[2 * f + 1], x1[2 * f + 1], bq.x, bq.y);
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+                            mma_16816(s[n][nt], x0[n][2 * f], x1[n][2 * f], x0[n][2 * f + 1], x1[n][2 * f + 1], bq.x, bq.y);
                     }
             }
         }
-        // the stage is in registers: its next tile may come
+        // ---- V: token pairs c, c + 4 of each block, dimensions D / 8 r ..
+        uint32_t v0[NB][kW], v1[NB][kW], vs0[NB], vs1[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const char *vt = stage + (NB + n) * kTile;
+            load_words<kW>(vt + c * D + 4 * ((r * kW) ^ i4::v_swizzle<D>(c)), v0[n]);
+            load_words<kW>(vt + (c + 4) * D + 4 * ((r * kW) ^ i4::v_swizzle<D>(c + 4)), v1[n]);
+            const int gr = D == 128 ? 2 * r : (r & ~1);
+            vs0[n] = *reinterpret_cast<const uint16_t *>(vt + 8 * D + c * (D / 8) + gr);
+            vs1[n] = *reinterpret_cast<const uint16_t *>(vt + 8 * D + (c + 4) * (D / 8) + gr);
+        }
+        // tokens past the sequence or the partition, or in a block that is not there
+        const int end = (int)min((long long)(w.blk0 + w.nloc) * kI4BS, w.L);
+        bool whole = tok0 + NB * kI4BS <= end;
+        int ntok[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const int there = valid[st * NB + n];
+            whole = whole && there;
+            ntok[n] = there ? min(kI4BS, end - (tok0 + n * kI4BS)) : 0;
+        }
+        // the stage is in registers: its next group may come
         __syncwarp();
-        if (issued < nown) issue();
+        if (issued < nown) issue(st);
+        if (++st == NST) {
+            st = 0;
+            parity ^= 1;
+        }
 
         // ---- softmax: s[0], s[1] token r, columns 2 c, 2 c + 1; s[2], s[3] token r + 8
-        uint32_t ph[NT][2], pl[NT][2];
-        const bool masked = tok0 + kI4BS > least || ntok < kI4BS;
+        uint32_t ph[NB][NT][2], pl[NB][NT][2];
+        const bool masked = !whole || tok0 + NB * kI4BS > least;
+        if (masked) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int t = r + 4 * (x & 2);
+                        if (t >= ntok[n] || tok0 + n * kI4BS + t >= lim[nt][x & 1]) s[n][nt][x] = -INFINITY;
+                    }
+        }
+        bool renew = false;
+        float top[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float m = fmaxf(s[0][nt][x], s[0][nt][2 + x]);
+#pragma unroll
+                for (int n = 1; n < NB; ++n) m = fmaxf(m, fmaxf(s[n][nt][x], s[n][nt][2 + x]));
+#pragma unroll
+                for (int y = 4; y <= 16; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
+                top[nt][x] = m * sc[nt][x];
+                renew |= top[nt][x] > m_run[nt][x] + kI4Renew;
+            }
+        if (__any_sync(0xffffffffu, renew)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    // 2^(old - new); an empty state has a reference of -inf
+                    const float m = top[nt][x] > m_run[nt][x] + kI4Renew ? top[nt][x] : m_run[nt][x];
+                    const float a = m == m_run[nt][x] ? 1.f : ex2(m_run[nt][x] - m);
+                    m_run[nt][x] = m;
+                    l_run[nt][x] *= a;
+#pragma unroll
+                    for (int f = 0; f < kSteps; ++f) {
+                        o[nt][f][x] *= a;
+                        o[nt][f][2 + x] *= a;
+                    }
+                }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            const float u0 = m_run[nt][0] == -INFINITY ? 0.f : kI4Bias - m_run[nt][0];
+            const float u1 = m_run[nt][1] == -INFINITY ? 0.f : kI4Bias - m_run[nt][1];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) s[nt][x] *= sc[nt][x & 1];
-            if (masked) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int t = r + 4 * (x & 2);
-                    if (t >= ntok || tok0 + t >= lim[nt][x & 1]) s[nt][x] = -INFINITY;
+            for (int n = 0; n < NB; ++n) {
+                const float p0 = ex2(fmaf(s[n][nt][0], sc[nt][0], u0)), p1 = ex2(fmaf(s[n][nt][1], sc[nt][1], u1));
+                const float p2 = ex2(fmaf(s[n][nt][2], sc[nt][0], u0)), p3 = ex2(fmaf(s[n][nt][3], sc[nt][1], u1));
+                l_run[nt][0] += p0 + p2;
+                l_run[nt][1] += p1 + p3;
+                const uint32_t h01 = half_pair(p0, p1), h23 = half_pair(p2, p3);
+                ph[n][nt][0] = transpose8(h01);
+                ph[n][nt][1] = transpose8(h23);
+                if constexpr (EXACT) {
+                    const float2 f01 = f16x2_to_float2(h01), f23 = f16x2_to_float2(h23);
+                    pl[n][nt][0] = transpose8(half_pair(p0 - f01.x, p1 - f01.y));
+                    pl[n][nt][1] = transpose8(half_pair(p2 - f23.x, p3 - f23.y));
                 }
-            }
-            float m0 = fmaxf(s[nt][0], s[nt][2]), m1 = fmaxf(s[nt][1], s[nt][3]);
-#pragma unroll
-            for (int x = 4; x <= 16; x <<= 1) {
-                m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, x));
-                m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, x));
-            }
-            const float n0 = fmaxf(m_run[nt][0], m0), n1 = fmaxf(m_run[nt][1], m1);
-            const float u0 = n0 == -INFINITY ? 0.f : n0 - kI4Bias, u1 = n1 == -INFINITY ? 0.f : n1 - kI4Bias;
-            if (__any_sync(0xffffffffu, n0 != m_run[nt][0] || n1 != m_run[nt][1])) {
-                // 2^(old - new); a state of -inf is empty
-                const float a0 = ex2(m_run[nt][0] - (u0 + kI4Bias)), a1 = ex2(m_run[nt][1] - (u1 + kI4Bias));
-                m_run[nt][0] = n0;
-                m_run[nt][1] = n1;
-                l_run[nt][0] *= a0;
-                l_run[nt][1] *= a1;
-#pragma unroll
-                for (int f = 0; f < kSteps; ++f) {
-                    o[nt][f][0] *= a0;
-                    o[nt][f][1] *= a1;
-                    o[nt][f][2] *= a0;
-                    o[nt][f][3] *= a1;
-                }
-            }
-            const float p0 = ex2(s[nt][0] - u0), p1 = ex2(s[nt][1] - u1);
-            const float p2 = ex2(s[nt][2] - u0), p3 = ex2(s[nt][3] - u1);
-            l_run[nt][0] += p0 + p2;
-            l_run[nt][1] += p1 + p3;
-            const uint32_t h01 = half_pair(p0, p1), h23 = half_pair(p2, p3);
-            ph[nt][0] = transpose8(h01);
-            ph[nt][1] = transpose8(h23);
-            if constexpr (EXACT) {
-                const float2 f01 = f16x2_to_float2(h01), f23 = f16x2_to_float2(h23);
-                pl[nt][0] = transpose8(half_pair(p0 - f01.x, p1 - f01.y));
-                pl[nt][1] = transpose8(half_pair(p2 - f23.x, p3 - f23.y));
             }
         }
         // ---- O^T += V^T P^T.  Slots past the sequence may hold anything: a scale
         // of zero makes their values zero (codes are finite).
-        {
-            uint32_t a = __half2_raw(quarter_scales(vs0)).x | (uint32_t)__half2_raw(quarter_scales(vs0)).y << 16;
-            uint32_t e = __half2_raw(quarter_scales(vs1)).x | (uint32_t)__half2_raw(quarter_scales(vs1)).y << 16;
-            if (ntok < kI4BS) {
-                a &= (2 * c < ntok ? 0xffffu : 0u) | (2 * c + 1 < ntok ? 0xffff0000u : 0u);
-                e &= (2 * c + 8 < ntok ? 0xffffu : 0u) | (2 * c + 9 < ntok ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            __half2 a = i4::scale_pair(vs0[n]), e = i4::scale_pair(vs1[n]);
+            if (!whole) {
+                uint32_t ab = *reinterpret_cast<uint32_t *>(&a), eb = *reinterpret_cast<uint32_t *>(&e);
+                ab &= (2 * c < ntok[n] ? 0xffffu : 0u) | (2 * c + 1 < ntok[n] ? 0xffff0000u : 0u);
+                eb &= (2 * c + 8 < ntok[n] ? 0xffffu : 0u) | (2 * c + 9 < ntok[n] ? 0xffff0000u : 0u);
+                a = *reinterpret_cast<__half2 *>(&ab);
+                e = *reinterpret_cast<__half2 *>(&eb);
             }
-            const i4::Scale g0 = i4::make_scale(*reinterpret_cast<__half2 *>(&a));
-            const i4::Scale g1 = i4::make_scale(*reinterpret_cast<__half2 *>(&e));
+            const i4::Scale g0 = i4::make_scale(a), g1 = i4::make_scale(e);
 #pragma unroll
             for (int wi = 0; wi < kW; ++wi) {
                 uint32_t x0[4], x1[4];
-                i4::values8(v0[wi], g0, x0);
-                i4::values8(v1[wi], g1, x1);
+                i4::values8(v0[n][wi], g0, x0);
+                i4::values8(v1[n][wi], g1, x1);
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_16816(o[nt][2 * wi + f], x0[2 * f], x0[2 * f + 1], x1[2 * f], x1[2 * f + 1], ph[nt][0], ph[nt][1]);
+                        mma_16816(o[nt][2 * wi + f], x0[2 * f], x0[2 * f + 1], x1[2 * f], x1[2 * f + 1], ph[n][nt][0],
+                                  ph[n][nt][1]);
                         if constexpr (EXACT)
-                            mma_16816(o[nt][2 * wi + f], x0[2 * f], x0[2 * f + 1], x1[2 * f], x1[2 * f + 1], pl[nt][0],
-                                      pl[nt][1]);
+                            mma_16816(o[nt][2 * wi + f], x0[2 * f], x0[2 * f + 1], x1[2 * f], x1[2 * f + 1], pl[n][nt][0],
+                                      pl[n][nt][1]);
                     }
             }
         }
     }
     // After a timed-out wait: no copy may still be on its way into this CTA's memory.
-    for (int j = max(0, issued - kNst); j < issued; ++j) mbar_wait_drain(&full[j % kNst], (j / kNst) & 1, p.err);
+    for (int j = max(0, issued - NST); j < issued; ++j) mbar_wait_drain(&full[j % NST], (j / NST) & 1, p.err);
 
     // ---- the four warps' states to this partition's result, eight columns at a time
     float4 *sm_o = reinterpret_cast<float4 *>(smem);  // [warp][column][D / 4], see `at`
@@ -627,12 +679,14 @@ __global__ void __launch_bounds__(kI4Threads) merge_i4_kernel(const I4Params p, 
 
 cudaError_t set_wait_limit_decode_i4(unsigned long long ns) { return set_wait_limit_here(ns); }
 
-template <int D, int NT, int MINB>
+template <int D, int NT, int NB, int NST, int MINB>
 static kv_status launch_i4(const I4Params &p, dim3 grid, cudaStream_t s) {
     const bool exact = p.out_type == KV_F32, tw = test_waits_enabled();
-    auto fn = exact ? (tw ? decode_i4_kernel<D, NT, true, true, MINB> : decode_i4_kernel<D, NT, true, false, MINB>)
-                    : (tw ? decode_i4_kernel<D, NT, false, true, MINB> : decode_i4_kernel<D, NT, false, false, MINB>);
-    constexpr size_t smem = i4_smem_bytes<D>();
+    auto fn = exact ? (tw ? decode_i4_kernel<D, NT, true, true, NB, NST, MINB>
+                          : decode_i4_kernel<D, NT, true, false, NB, NST, MINB>)
+                    : (tw ? decode_i4_kernel<D, NT, false, true, NB, NST, MINB>
+                          : decode_i4_kernel<D, NT, false, false, NB, NST, MINB>);
+    constexpr size_t smem = i4_smem_bytes<D, NB, NST>();
     if (kv_status st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
         return st;
     fn<<<grid, kI4Threads, smem, s>>>(p);
@@ -650,7 +704,7 @@ kv_status attend_i4(const I4Call &a) {
     if (need > 0 && (!a.workspace || a.workspace_bytes < need)) return KV_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(a.workspace) & 15) return KV_ERR_ARG;
     const int cols = a.max_q_len * g;  // of one (sequence, kv head)
-    const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+    const int nt = std::min(4, (cols + 7) / 8);
     const int groups = (cols + 8 * nt - 1) / (8 * nt);
     if (ms > 65535 || (long long)a.batch * groups > 65535 || pool->num_kv_heads > 65535) return KV_ERR_UNSUPPORTED;
     I4Params p{};
@@ -670,8 +724,8 @@ kv_status attend_i4(const I4Call &a) {
     p.hq = a.num_q_heads;
     p.hkv = pool->num_kv_heads;
     p.g = g;
-    p.scale_log2 = a.scale * 1.4426950408889634f * 4.f * pool->k_scale;
-    p.v_mul = 4.f * pool->v_scale;
+    p.scale_log2 = a.scale * 1.4426950408889634f * i4::kScaleUnit * pool->k_scale;
+    p.v_mul = i4::kScaleUnit * pool->v_scale;
     p.part_blocks = pb;
     p.max_splits = ms;
     p.col_groups = groups;
@@ -686,11 +740,12 @@ kv_status attend_i4(const I4Call &a) {
     const dim3 grid(ms, pool->num_kv_heads, a.batch * groups);
     kv_status st;
     if (pool->head_dim == 64)
-        st = nt == 1 ? launch_i4<64, 1, 5>(p, grid, a.stream) : KV_ERR_UNSUPPORTED;
+        st = nt == 1 ? launch_i4<64, 1, 2, 3, 5>(p, grid, a.stream) : KV_ERR_UNSUPPORTED;
     else
-        st = nt == 1   ? launch_i4<128, 1, 5>(p, grid, a.stream)
-             : nt == 2 ? launch_i4<128, 2, 3>(p, grid, a.stream)
-                       : launch_i4<128, 4, 2>(p, grid, a.stream);
+        st = nt == 1   ? launch_i4<128, 1, 2, 2, 4>(p, grid, a.stream)
+             : nt == 2 ? launch_i4<128, 2, 1, 4, 3>(p, grid, a.stream)
+             : nt == 3 ? launch_i4<128, 3, 1, 4, 2>(p, grid, a.stream)
+                       : launch_i4<128, 4, 1, 4, 2>(p, grid, a.stream);
     if (st != KV_OK) return st;
     const int min_splits = fused ? kFuseMaxSplits + 1 : 2;
     if (ms >= min_splits) {

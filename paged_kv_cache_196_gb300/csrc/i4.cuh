@@ -19,9 +19,13 @@
 //   V  is contracted over tokens, so the two tokens of a pair (2p, 2p + 1) share
 //      words: word (p, quad) holds dimensions 4 quad .. 4 quad + 3 of token 2p in
 //      its low half and of token 2p + 1 in its high half, so that a masked word
-//      is already the pair of operands the tensor core wants.  Scales: byte
-//      p * D / 8 + 2 j + (t & 1).  A token owns whole 16-bit halves and whole scale
-//      bytes: tokens of one pair may be written at the same time.
+//      is already the pair of operands the tensor core wants.  A token owns whole
+//      16-bit halves and whole scale bytes: tokens of one pair may be written at the
+//      same time.  Pair p's D / 4 words lie at word p D / 4, in an order that lets
+//      the eight lanes (of four pairs) that load together hit all banks: quad q at
+//      position q ^ v_swizzle(p).  Scales: byte p * D / 8 + 2 j + (t & 1).
+//   A scale byte is the e4m3 code; NaN is 0xff, so that the byte shifted left by 7
+//   is an fp16 NaN and otherwise the fp16 value s / 256 (see scale_pair).
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -40,11 +44,11 @@ KV_DEVICE float max_nan(float a, float b) {
     return r;
 }
 
-// The e4m3 nearest to x >= 0 (at most 448; NaN for NaN) as its byte.
+// The e4m3 nearest to x >= 0 (at most 448) as its byte; 0xff for NaN.
 KV_DEVICE uint32_t e4m3_of(float x) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
-    return r;
+    return x != x ? 0xffu : r;
 }
 
 // Two e4m3 bytes (low byte first) as a pair of fp16 values, exact.
@@ -55,6 +59,12 @@ KV_DEVICE __half2 e4m3x2_to_half2(uint32_t b) {
 }
 
 KV_DEVICE float e4m3_to_float(uint32_t b) { return __low2float(e4m3x2_to_half2(b)); }
+
+// Where pair p keeps its quad q: q ^ v_swizzle<D>(p).
+template <int D>
+KV_DEVICE constexpr int v_swizzle(int p) {
+    return D == 128 ? 8 * (p & 3) : 8 * ((p >> 1) & 1);
+}
 
 // Eight values of one group half -> their eight 4-bit codes, value i in bits
 // 4i .. 4i + 3, given the group's scale s (a value of e4m3).
@@ -81,23 +91,38 @@ KV_DEVICE uint32_t codes8(const float (&x)[8], float s) {
     return w;
 }
 
-// Four code pairs of one word as fp16 pairs times their scales: out[n] = (low
-// half's four bits n, high half's four bits n).
+// Two scale bytes (low byte first) as the fp16 pair s / 256.  e4m3's exponent and
+// mantissa are the low bits of fp16's with a bias 8 smaller, so it is a shift, exact
+// for every e4m3 (subnormals become fp16 subnormals); the byte 0xff becomes a NaN.
+KV_DEVICE __half2 scale_pair(uint32_t two) {
+    const uint32_t h = __byte_perm(two, 0u, 0x1404) >> 1;
+    return *reinterpret_cast<const __half2 *>(&h);
+}
+
+// Four code pairs of one word as fp16 pairs times their scales (c s / 256): out[n]
+// = (low half's four bits n, high half's four bits n).
 //
-// A code placed in the mantissa of 16 or 256 gives 16 + u or 256 + u with one
-// logical operation, and one fused multiply-add takes it to (u - 8) s: the
-// constants -24 s and -264 s are exact (6 and 10 bits), the product is not
-// rounded before the sum, the result has 7 bits.  s is taken a quarter so that
-// 264 s stays below 65504; the callers multiply the result's sum by 4.
+// Four bits at the bottom of the mantissa of 1024, or above four zero bits in that of
+// 64, give 1024 + u or 64 + u with one logical operation, and one fused multiply-add
+// takes it to (u - 8) s: the constants -1032 s and -72 s are exact (129 and 9 times
+// the four significant bits of s fit 11), the product is not rounded before the sum,
+// and the result has 7 bits.
 struct Scale {
-    __half2 s, m24, m264;
+    __half2 s, m72, m1032;
 };
 
-KV_DEVICE Scale make_scale(__half2 s_quarter) {
+KV_DEVICE Scale make_scale(__half2 s) {
     Scale r;
-    r.s = s_quarter;
-    r.m24 = __hmul2(s_quarter, __float2half2_rn(-24.f));
-    r.m264 = __hmul2(s_quarter, __float2half2_rn(-264.f));
+    r.s = s;
+    r.m72 = __hmul2(s, __float2half2_rn(-72.f));
+    r.m1032 = __hmul2(s, __float2half2_rn(-1032.f));
+    return r;
+}
+
+// (w & mask) | bits as one instruction.
+KV_DEVICE uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
     return r;
 }
 
@@ -107,12 +132,15 @@ KV_DEVICE uint32_t fma2(uint32_t x, __half2 s, __half2 m) {
 }
 
 KV_DEVICE void values8(uint32_t w, const Scale &k, uint32_t (&out)[4]) {
-    const uint32_t a = w << 2, b = w >> 6;
-    out[0] = fma2((a & 0x003C003Cu) | 0x5C005C00u, k.s, k.m264);
-    out[1] = fma2((a & 0x03C003C0u) | 0x4C004C00u, k.s, k.m24);
-    out[2] = fma2((b & 0x003C003Cu) | 0x5C005C00u, k.s, k.m264);
-    out[3] = fma2((b & 0x03C003C0u) | 0x4C004C00u, k.s, k.m24);
+    const uint32_t b = w >> 8;
+    out[0] = fma2(and_or(w, 0x000F000Fu, 0x64006400u), k.s, k.m1032);
+    out[1] = fma2(and_or(w, 0x00F000F0u, 0x54005400u), k.s, k.m72);
+    out[2] = fma2(and_or(b, 0x000F000Fu, 0x64006400u), k.s, k.m1032);
+    out[3] = fma2(and_or(b, 0x00F000F0u, 0x54005400u), k.s, k.m72);
 }
+
+// What values8 leaves out: the callers multiply their sums by it.
+constexpr float kScaleUnit = 256.f;
 
 }  // namespace i4
 }  // namespace pkv

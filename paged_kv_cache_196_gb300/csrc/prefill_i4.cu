@@ -8,8 +8,8 @@
 // q's type, V in fp16 (no conversion in its inner loop).  For 4 chunks of 2048
 // tokens over 8192 cached ones the expansion moves 47 MB in and 336 MB out.
 //
-// A quarter of each value is stored (c s / 4: exact in both types, see i4.cuh);
-// the softmax scale and the output take the factor back, with the pool's scales.
+// c s / 256 is stored (exact in both types, see i4.cuh); the softmax scale and the
+// output take the factor back, with the pool's scales.
 //
 // A chunk of few query tokens reads the cache about once, so it takes the 4-bit
 // decode kernel with a column per (query token, head) instead.
@@ -59,27 +59,27 @@ __global__ void __launch_bounds__(256) expand_i4_kernel(const char *__restrict__
     const char *kt = k_pool + ((size_t)id * hkv + h) * kExTile, *vt = v_pool + ((size_t)id * hkv + h) * kExTile;
     uint4 *ko = reinterpret_cast<uint4 *>(k_out + (at * hkv + h) * kExOut);
     uint2 *vo = reinterpret_cast<uint2 *>(v_out + (at * hkv + h) * kExOut);
-    // word 32 j + lane: K row 2 j + lane / 16, octet lane % 16; V pair j, quad lane
+    // word 32 j + lane: K row 2 j + lane / 16, octet lane % 16; V pair j, the word
+    // of quad lane
     uint32_t kw[8], vw[8];
     uint32_t ks[8], vs[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         kw[j] = __ldg(reinterpret_cast<const uint32_t *>(kt) + 32 * j + lane);
-        vw[j] = __ldg(reinterpret_cast<const uint32_t *>(vt) + 32 * j + lane);
+        vw[j] = __ldg(reinterpret_cast<const uint32_t *>(vt) + 32 * j + (lane ^ i4::v_swizzle<kExD>(j)));
         ks[j] = __ldg(reinterpret_cast<const uint8_t *>(kt) + 8 * kExD + (2 * j + (lane >> 4)) * 8 + ((lane & 15) >> 1));
         vs[j] = __ldg(reinterpret_cast<const uint16_t *>(vt + 8 * kExD + j * 16) + (lane >> 2));
     }
-    const __half2 quarter = __float2half2_rn(0.25f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         uint32_t x[4];
-        i4::values8(kw[j], i4::make_scale(__hmul2(__low2half2(i4::e4m3x2_to_half2(ks[j])), quarter)), x);
+        i4::values8(kw[j], i4::make_scale(__low2half2(i4::scale_pair(ks[j]))), x);
         // (0, 4) (1, 5) (2, 6) (3, 7) -> (0, 1) (2, 3) (4, 5) (6, 7)
         ko[32 * j + lane] = make_uint4(to_k_type<BF16>(__byte_perm(x[0], x[1], 0x5410)),
                                        to_k_type<BF16>(__byte_perm(x[2], x[3], 0x5410)),
                                        to_k_type<BF16>(__byte_perm(x[0], x[1], 0x7632)),
                                        to_k_type<BF16>(__byte_perm(x[2], x[3], 0x7632)));
-        i4::values8(vw[j], i4::make_scale(__hmul2(i4::e4m3x2_to_half2(vs[j]), quarter)), x);
+        i4::values8(vw[j], i4::make_scale(i4::scale_pair(vs[j])), x);
         vo[64 * j + lane] = make_uint2(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
         vo[64 * j + 32 + lane] = make_uint2(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
     }
@@ -180,8 +180,8 @@ kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtyp
     a.seq_lens = seq_lens;
     a.batch = batch;
     a.num_q_heads = num_q_heads;
-    a.scale = scale * 4.f * p->k_scale;
-    a.v_mul = 4.f * p->v_scale;
+    a.scale = scale * i4::kScaleUnit * p->k_scale;
+    a.v_mul = i4::kScaleUnit * p->v_scale;
     a.out = out;
     a.out_dtype = out_dtype;
     a.lse = lse_out;

@@ -112,9 +112,11 @@ KV_DEVICE void store_i4(char *tile, int t, int o, float (&x)[8], float inv, bool
     const uint32_t w = i4::codes8(x, i4::e4m3_to_float(sb));
     if (!live) return;
     if constexpr (V) {
-        uint16_t *c = reinterpret_cast<uint16_t *>(tile) + (t >> 1) * (D / 2) + 4 * o + (t & 1);
-        c[0] = (uint16_t)w;          // quad 2 o
-        c[2] = (uint16_t)(w >> 16);  // quad 2 o + 1
+        // quads 2 o and 2 o + 1
+        uint16_t *c = reinterpret_cast<uint16_t *>(tile) + (t >> 1) * (D / 2) +
+                      2 * ((2 * o) ^ i4::v_swizzle<D>(t >> 1)) + (t & 1);
+        c[0] = (uint16_t)w;
+        c[2] = (uint16_t)(w >> 16);
         if (!(o & 1)) tile[8 * D + (t >> 1) * (D / 8) + o + (t & 1)] = (char)sb;
     } else {
         reinterpret_cast<uint32_t *>(tile)[t * (D / 8) + o] = w;
@@ -289,7 +291,8 @@ __global__ void __launch_bounds__(256) read_tokens_kernel(const char *__restrict
             const char *kt = k_pool + tile * (9 * D), *vt = v_pool + tile * (9 * D);
             const uint32_t kw = reinterpret_cast<const uint32_t *>(kt)[t * (D / 8) + o];
             const float ks = i4::e4m3_to_float((uint8_t)kt[8 * D + t * (D / 16) + (o >> 1)]) * k_scale;
-            const uint16_t *vc = reinterpret_cast<const uint16_t *>(vt) + (t >> 1) * (D / 2) + 4 * o + (t & 1);
+            const uint16_t *vc = reinterpret_cast<const uint16_t *>(vt) + (t >> 1) * (D / 2) +
+                                 2 * ((2 * o) ^ i4::v_swizzle<D>(t >> 1)) + (t & 1);
             const uint32_t vw = vc[0] | (uint32_t)vc[2] << 16;
             const float vs = i4::e4m3_to_float((uint8_t)vt[8 * D + (t >> 1) * (D / 8) + (o & ~1) + (t & 1)]) * v_scale;
             float a[8], b[8];

@@ -94,14 +94,14 @@ def attend(q, k, v, scale, seen):
     return o, lse, av, mag, np.abs(v).max(initial=0.0)
 
 
-def check_attention(out, lse, ref, scale, n_keys, out_type, weight_step, what="", floor=2.0 ** -35):
+def check_attention(out, lse, ref, scale, n_keys, out_type, weight_step, what="", floor=2.0 ** -31):
     """Bounds: a score is an fp32 sum of exact products (D + 8 roundings of at most
     2^-23 of sum |q||k|, the tensor core truncating); a weight's relative error is twice
     that times the softmax scale (numerator and denominator), 2^-21 for the
     exponential, and weight_step for its rounding; o sums n / 16 tiles in fp32; out
     is rounded once to its type.  floor: the smallest weights are fp16 subnormals,
-    whose half spacing is 2^-25 however small they are, of weights up to 2^10 (the
-    4-bit decode's; its second part is rounded alike): 2^-35 of the largest per key."""
+    whose half spacing is 2^-25 however small they are, where the largest weight is at
+    least 2^6 (the 4-bit decode's; its second part is rounded alike): 2^-31 of it per key."""
     o, ref_lse, av, mag, vmax = ref
     d = o.shape[-1]
     ds = abs(scale) * mag * (d + 8) * 2.0 ** -23

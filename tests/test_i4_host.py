@@ -42,10 +42,12 @@ def test_reference_scales_are_those_of_the_type():
 
 
 def test_stored_values_fit_sixteen_bits():
-    """Every code times every scale, a quarter of it and the kernels' constants are
-    exact in fp16 (and the values in bf16)."""
+    """Every code times every scale, a 256th of it and the kernels' constants are
+    exact in fp16 (and the values in bf16); a scale's byte shifted by 7 is its 256th."""
+    assert np.array_equal((np.arange(127, dtype=np.uint16) << 7).view(np.float16).astype(np.float64), E4M3 / 256)
+    assert np.isnan(np.array([0xff << 7], np.uint16).view(np.float16))[0]
     c = np.arange(-8, 8)[:, None] * E4M3[None]
-    for x in (c, c / 4, 24 * E4M3 / 4, 264 * E4M3 / 4, E4M3 / 4):
+    for x in (c, c / 256, 72 * E4M3 / 256, 1032 * E4M3 / 256, E4M3 / 256):
         assert np.array_equal(x.astype(np.float16).astype(np.float64), x)
     t = torch.from_numpy(c)
     assert torch.equal(t.to(torch.bfloat16).double(), t)
