@@ -14,12 +14,20 @@
 // warp takes NB blocks at a time, so that waiting, issuing, the maximum over lanes
 // and the test for a new maximum are paid once per NB blocks.
 //
-// Shape.  One CTA = a run of blocks of one (sequence, kv head) for all its query
-// columns (head of the group, and query token where there are several); four
-// warps, warp w takes the block groups w, w + 4, ... and keeps its own softmax state.
-// Each warp feeds itself: lane i issues the two bulk copies of block i of a group
-// into the warp's own ring, the next group into a stage as soon as the warp has the
-// old one in registers.  No producer warp, no barrier between warps before the end.
+// Shape.  A pair is one (sequence, kv head) with up to 8 NT of its query columns
+// (head of the group, and query token where there are several).  Its blocks are
+// taken in rounds: a round is NB blocks for each of a CTA's four warps, which keep
+// their own softmax states and meet at a pair's end.  Each warp feeds itself: lane i
+// issues the two bulk copies of block i of a group into the warp's own ring, the next
+// group into a stage as soon as the warp has the old one in registers.  No producer
+// warp, no barrier between warps within a pair.
+//
+// Balance.  The rounds of all pairs are laid end to end and cut into one equal run
+// per CTA of a single wave; every CTA finds its run from the lengths on the device
+// (a scan of the batch), so a captured graph stays balanced when the lengths change.
+// The copies run ahead across pair boundaries.  A pair cut by runs leaves a partial
+// result per CTA, which the last of them merges.  A pair counts kI4PairCost rounds
+// more than it has, for its queries and its end.
 //
 // Products.  S^T[16 tokens][8 columns] = K q^T and O^T[16 dims][8 columns] += V^T
 // P^T on mma.sync m16n8k16 with fp32 sums.  The contraction over dimensions may run
@@ -45,6 +53,9 @@ namespace pkv {
 constexpr int kI4Warps = 4;
 constexpr int kI4Threads = kI4Warps * 32;
 constexpr int kI4BS = 16;
+constexpr int kI4PairCost = 1;       // rounds
+constexpr int kI4MinRun = 2;         // shortest run: a pair's cost and a round
+constexpr int kI4ScanBatch = 4096;   // largest batch whose runs the device cuts
 // The weights are 2^(s - m + 6) for a reference m that is renewed (and the state
 // rescaled) only when the maximum passes it by more than 2^8: rarely after the
 // first blocks, and exact mathematics, since sums and outputs share m.  They stay
@@ -63,8 +74,12 @@ struct I4Params {
     int batch, hq, hkv, g;
     float scale_log2;       // softmax scale * log2(e) * kScaleUnit * the pool's K scale
     float v_mul;            // kScaleUnit * the pool's V scale
-    int part_blocks, max_splits;
-    int col_groups;         // CTAs that share a partition's columns
+    // balanced: one run per CTA, at most max_splits to a pair.  Otherwise CTA
+    // (split, kv head, (sequence, column group)) takes part_rounds rounds.
+    int balanced;
+    int part_rounds, max_splits;
+    int round_blocks, cols; // blocks of a round, columns of a pair (the kernel's own)
+    int col_groups;         // pairs that share a sequence's columns of one kv head
     void *out;
     int out_type;
     float *lse;
@@ -125,22 +140,26 @@ KV_DEVICE void load_words(const char *src, uint32_t (&w)[N]) {
     }
 }
 
-// Shared memory: the warps' rings (NST stages of NB blocks), reused by the merges.
+// Shared memory: the warps' rings (NST stages of NB blocks), the merge's outputs
+// ([warp][8 columns][D], reused for the split merge's weights), barriers.
 template <int D, int NB, int NST>
 constexpr size_t i4_ring_bytes() {
-    const size_t ring = (size_t)kI4Warps * NST * NB * 2 * 9 * D;
-    const size_t merge = (size_t)kI4Warps * 8 * D * 4 + 4096;
-    return ((ring > merge ? ring : merge) + 127) / 128 * 128;
+    return (size_t)kI4Warps * NST * NB * 2 * 9 * D;
+}
+template <int D>
+constexpr size_t i4_merge_bytes() {
+    return (size_t)kI4Warps * 8 * D * 4;
 }
 template <int D, int NB, int NST>
 constexpr size_t i4_smem_bytes() {
-    return i4_ring_bytes<D, NB, NST>() + (size_t)kI4Warps * NST * (sizeof(uint64_t) + NB * sizeof(int));
+    return i4_ring_bytes<D, NB, NST>() + i4_merge_bytes<D>() +
+           (size_t)kI4Warps * NST * (sizeof(uint64_t) + NB * sizeof(int));
 }
 
-// The sequence of a CTA: rows of its queries, keys, partition.  False: nothing to do.
+// A sequence: its query rows, keys, rounds, and the pairs it makes (0: left out).
 struct I4Work {
-    int b, q0, T, nblk, blk0, nloc, nsplit;
-    long long L;
+    int b, q0, T, nblk, rounds, pairs;
+    int L;
 };
 
 // Row of a query head in q and out, and in the workspace.
@@ -149,17 +168,19 @@ KV_DEVICE size_t ws_row(const I4Params &p, const I4Work &w, int tq, int hq) {
     return ((size_t)w.b * p.max_t + tq) * p.hq + hq;
 }
 
-KV_DEVICE bool i4_sequence(const I4Params &p, int b, bool report, I4Work &w) {
+// round_blocks: blocks of a round; cols: columns of a pair.
+KV_DEVICE I4Work i4_sequence(const I4Params &p, int b, int round_blocks, int cols, bool report) {
+    I4Work w{};
     w.b = b;
     long long L = p.seq_lens[b];
     const long long most = (long long)p.max_blocks * kI4BS;
     if (p.cu_q) {
         w.q0 = p.cu_q[b];
         w.T = p.cu_q[b + 1] - w.q0;
-        if (w.T <= 0) return false;
+        if (w.T <= 0) return w;
         if (L < w.T || L > most || w.T > p.max_t || w.q0 < 0 || (long long)w.q0 + w.T > p.total_q) {
             if (report) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
-            return false;
+            return w;
         }
     } else {
         w.q0 = b;
@@ -170,10 +191,11 @@ KV_DEVICE bool i4_sequence(const I4Params &p, int b, bool report, I4Work &w) {
         }
         if (L < 0) L = 0;
     }
-    w.L = L;
-    w.nblk = (int)((L + kI4BS - 1) / kI4BS);
-    w.nsplit = max(1, (w.nblk + p.part_blocks - 1) / p.part_blocks);
-    return true;
+    w.L = (int)L;
+    w.nblk = (w.L + kI4BS - 1) / kI4BS;
+    w.rounds = max(1, (w.nblk + round_blocks - 1) / round_blocks);
+    w.pairs = p.hkv * ((w.T * p.g + cols - 1) / cols);
+    return w;
 }
 
 // D: head dim.  NT: columns / 8 of a CTA.  EXACT: weights in two fp16 parts (fp32
@@ -185,452 +207,588 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
     constexpr int kW = D / 32;        // words of a quarter row of K, of a lane's dims of a V pair
     constexpr int kSteps = D / 16;    // products along D
     constexpr int kStage = NB * 2 * kTile;  // K tiles, then V tiles
-    const int split = blockIdx.x, h = blockIdx.y;
-    int b = blockIdx.z / p.col_groups;
-    const int cg = blockIdx.z % p.col_groups;
+    constexpr int kRound = NB * kI4Warps;   // blocks of a round
+    constexpr int kCols = 8 * NT;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
-    const bool reports = tid == 0 && split == 0 && h == 0 && cg == 0;
-    if (p.seq_order) {
-        b = __ldg(p.seq_order + b);
-        if (b < 0 || b >= p.batch) {  // not a permutation of the batch
-            if (reports) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
-            return;
-        }
-    }
-    I4Work w;
-    if (!i4_sequence(p, b, reports, w)) return;
-    w.blk0 = split * p.part_blocks;
-    if (w.blk0 >= w.nblk && split > 0) return;
-    w.nloc = max(0, min(p.part_blocks, w.nblk - w.blk0));
-    const int col0 = cg * 8 * NT;                // first column of this CTA
-    const int ncols = min(8 * NT, w.T * p.g - col0);
-    if (ncols <= 0) return;
 
     extern __shared__ __align__(128) char smem[];
-    constexpr size_t kRing = i4_ring_bytes<D, NB, NST>();
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRing) + warp * NST;
-    volatile int *valid = reinterpret_cast<int *>(smem + kRing + kI4Warps * NST * sizeof(uint64_t)) + warp * NST * NB;
+    constexpr size_t kRing = i4_ring_bytes<D, NB, NST>(), kMerge = i4_merge_bytes<D>();
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRing + kMerge) + warp * NST;
+    volatile int *valid =
+        reinterpret_cast<int *>(smem + kRing + kMerge + kI4Warps * NST * sizeof(uint64_t)) + warp * NST * NB;
     char *ring = smem + (size_t)warp * NST * kStage;
     __shared__ uint2 s_q[kSteps * NT * 32];
     __shared__ float s_scale[8 * NT];
     __shared__ float s_m[kI4Warps * 8], s_l[kI4Warps * 8];
-    __shared__ int s_last;
+    __shared__ int s_scan[kI4Warps], s_most[kI4Warps], s_start[3], s_last;
 
     if (lane == 0) {
         for (int st = 0; st < NST; ++st) mbar_init(&full[st], NB);
         mbar_init_fence();
     }
+
+    // ---- this CTA's run: `todo` units (rounds and pair costs) from unit `unit` of
+    // sequence b0 on, whose first unit is number `base` of all
+    int b0, unit, base, todo, run = 0;
+    if (p.balanced) {
+        // each thread adds up a slice of the batch, then the slices are scanned
+        const int per = (p.batch + kI4Threads - 1) / kI4Threads;
+        const int first = tid * per, past = min(p.batch, first + per);
+        int sum = 0, most = 1;
+        for (int b = first; b < past; ++b) {
+            const I4Work w = i4_sequence(p, b, kRound, kCols, blockIdx.x == 0);
+            if (w.pairs) most = max(most, w.rounds);
+            sum += w.pairs * (w.rounds + kI4PairCost);
+        }
+        int scan = sum;
+#pragma unroll
+        for (int y = 1; y < 32; y <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, y);
+            if (lane >= y) scan += v;
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, y));
+        }
+        if (lane == 31) s_scan[warp] = scan, s_most[warp] = most;
+        __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int y = 0; y < kI4Warps; ++y) {
+            if (y < warp) scan += s_scan[y];
+            total += s_scan[y];
+            most = max(most, s_most[y]);
+        }
+        // a pair of n rounds is cut into at most (n - 2) / run + 2 pieces
+        run = max((total + (int)gridDim.x - 1) / (int)gridDim.x,
+                  p.max_splits > 1 ? (most + p.max_splits - 3) / (p.max_splits - 1) : most + kI4PairCost);
+        run = max(run, kI4MinRun);
+        const long long at64 = (long long)blockIdx.x * run;
+        if (at64 >= total) return;
+        const int at = (int)at64;
+        if (at >= scan - sum && at < scan) {
+            int left = at - (scan - sum);
+            for (int b = first; b < past; ++b) {
+                const I4Work w = i4_sequence(p, b, kRound, kCols, false);
+                const int n = w.pairs * (w.rounds + kI4PairCost);
+                if (left < n) {
+                    s_start[0] = b, s_start[1] = left, s_start[2] = at - left;
+                    break;
+                }
+                left -= n;
+            }
+        }
+        __syncthreads();
+        b0 = s_start[0], unit = s_start[1], base = s_start[2];
+        todo = min(run, total - at);
+    } else {
+        const int split = blockIdx.x;
+        b0 = blockIdx.z / p.col_groups;
+        const int cg = blockIdx.z % p.col_groups;
+        const bool reports = tid == 0 && split == 0 && blockIdx.y == 0 && cg == 0;
+        if (p.seq_order) {
+            b0 = __ldg(p.seq_order + b0);
+            if (b0 < 0 || b0 >= p.batch) {  // not a permutation of the batch
+                if (reports) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
+                return;
+            }
+        }
+        const I4Work w = i4_sequence(p, b0, kRound, kCols, reports);
+        const int pair = cg * p.hkv + blockIdx.y, r0 = split * p.part_rounds;
+        if (pair >= w.pairs || r0 >= w.rounds) return;
+        base = 0;
+        unit = pair * (w.rounds + kI4PairCost) + kI4PairCost + r0;
+        todo = min(p.part_rounds, w.rounds - r0);
+    }
     __syncwarp();
 
-    // ---- this warp's groups: NB blocks from NB (warp + 4 j) on
-    const int ngroups = (w.nloc + NB - 1) / NB;
-    const int nown = ngroups > warp ? (ngroups - warp + kI4Warps - 1) / kI4Warps : 0;
-    // lane i < NB issues block i of each group; its table entry is read one group ahead
-    int next = NB * warp + lane;  // block of the partition this lane issues next
-    const int32_t *row = p.tables + (size_t)b * p.max_blocks + w.blk0;
-    int id_next = lane < NB && next < w.nloc ? __ldg(row + next) : -1;
+    // ---- the copies' place in the run
+    I4Work iw = i4_sequence(p, b0, kRound, kCols, false);
+    int i_unit = unit, i_left = todo;  // in units of sequence iw.b
+    int i_pair = 0, i_round = 0;       // the round the next issue takes
+    int id_next = -1;
     const uint64_t policy = l2_evict_first_policy();
+    // moves to the next unit that is a round; false at the run's end
+    auto place = [&]() -> bool {
+        while (i_left > 0) {
+            const int per = iw.rounds + kI4PairCost;
+            if (i_unit >= iw.pairs * per) {
+                iw = i4_sequence(p, iw.b + 1, kRound, kCols, false);
+                i_unit = 0;
+                continue;
+            }
+            i_pair = i_unit / per;
+            i_round = i_unit - i_pair * per - kI4PairCost;
+            if (i_round >= 0) return true;
+            ++i_unit;
+            --i_left;
+        }
+        return false;
+    };
+    bool more = place();
+    auto fetch = [&]() {  // the table entry of the block this lane copies next
+        if (lane < NB) {
+            const int blk = i_round * kRound + NB * warp + lane;
+            id_next = blk < iw.nblk ? __ldg(p.tables + (size_t)iw.b * p.max_blocks + blk) : -2;
+        }
+    };
+    if (more) fetch();
     int issued = 0;
-    auto issue = [&](int st) {  // the copies of own group `issued` into stage st
+    auto issue = [&](int st) {  // this warp's group of round i_round into stage st
         ++issued;
         if (lane < NB) {
             const bool ok = id_next >= 0 && id_next < p.num_blocks;
             valid[st * NB + lane] = ok;
             if (ok) {
-                const size_t off = ((size_t)id_next * p.hkv + h) * kTile;
+                const size_t off = ((size_t)id_next * p.hkv + i_pair % p.hkv) * kTile;
                 char *dst = ring + st * kStage + lane * kTile;
                 mbar_arrive_expect_tx(&full[st], 2 * kTile);
                 bulk_g2s(dst, p.k_pool + off, kTile, &full[st], policy);
                 bulk_g2s(dst + NB * kTile, p.v_pool + off, kTile, &full[st], policy);
             } else {
-                if (next < w.nloc) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
+                if (id_next != -2) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
                 mbar_arrive(&full[st]);
             }
-            next += NB * kI4Warps;
-            id_next = next < w.nloc ? __ldg(row + next) : -1;
         }
+        ++i_unit;
+        --i_left;
+        if (++i_round < iw.rounds)
+            more = i_left > 0;  // the same pair
+        else
+            more = place();
+        if (more) fetch();
     };
 #pragma unroll
     for (int j = 0; j < NST; ++j)
-        if (j < nown) issue(j);
+        if (more) issue(j);
 
+    bool stop = false;
     // Test instantiation with a limit of 0: a tile that is not there at once is a
     // wait that ran out (try_wait would sleep until it came).
-    bool stop = false;
     if constexpr (TW) {
-        if (g_wait_limit_ns == 0 && nown > 0) {
+        if (g_wait_limit_ns == 0 && issued > 0) {
             stop = __any_sync(0xffffffffu, !phase_done(&full[0], 0));
             if (stop && lane == 0) atomicOr(p.err, KV_DEVERR_TIMEOUT);
         }
     }
 
-    // ---- q of each column: largest magnitude to [2^13, 2^14) by a power of two,
-    // so that fp16 holds it, then into the order of the fragments
-    __half *qs = reinterpret_cast<__half *>(s_q);
-    for (int col = warp; col < 8 * NT; col += kI4Warps) {
-        constexpr int kPer = D / 32;
-        float x[kPer];
-        if (col < ncols) {
-            const int tq = (col0 + col) / p.g, j = (col0 + col) - tq * p.g;
-            const uint16_t *src = p.q + ((size_t)(w.q0 + tq) * p.hq + h * p.g + j) * D + lane * kPer;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                x[i] = p.q_bf16 ? bf16_to_float(src[i]) : f16x2_to_float2(src[i]).x;
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) x[i] = 0.f;
-        }
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) m = fmaxf(m, fabsf(x[i]));
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-        // exponent field of the largest; 0 (all zero or below normal) and 255 are left alone
-        const int e = (int)(__float_as_uint(m) >> 23);
-        const int up = e == 0 || e == 255 ? 0 : max(-126, min(126, 127 + 13 - e));
-        // the score's factor is made positive (its sign goes to q), so that scaling keeps
-        // the order of scores; a factor of 0 zeroes q instead
-        const float mul = copysignf(p.scale_log2 == 0.f ? 0.f : __uint_as_float((uint32_t)(127 + up) << 23), p.scale_log2);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            // dimension d: quarter cq, word wi, four bits n; pair n of half d / 4 % 2
-            const int d = lane * kPer + i, cq = d / (D / 4), in = d % (D / 4), wi = in / 8, n = in % 4, hi = in / 4 % 2;
-            const int pair = 4 * wi + n;
-            qs[((((pair >> 1) * NT + (col >> 3)) * 32 + (col & 7) * 4 + cq) * 2 + (pair & 1)) * 2 + hi] =
-                __float2half_rn(x[i] * mul);
-        }
-        if (lane == 0)
-            s_scale[col] = p.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 - up) << 23), 1e-37f);
-    }
-    __syncthreads();
-
-    // ---- state of columns 8 nt + 2 c and + 1 (maxima replicated over r)
-    float m_run[NT][2], l_run[NT][2], o[NT][kSteps][4], sc[NT][2];
-    int lim[NT][2];  // keys that the column sees
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int col = 8 * nt + 2 * c + x;
-            m_run[nt][x] = -INFINITY;
-            l_run[nt][x] = 0.f;
-            sc[nt][x] = s_scale[col];
-            lim[nt][x] = (int)(w.L - w.T) + min((col0 + col) / p.g, w.T - 1) + 1;
-#pragma unroll
-            for (int f = 0; f < kSteps; ++f) o[nt][f][x] = o[nt][f][2 + x] = 0.f;
-        }
-    const int least = (int)(w.L - w.T) + col0 / p.g + 1;  // keys that every column sees
-
+    // ---- the run's pieces
     int st = 0;
     uint32_t parity = 0;
-    for (int j = 0; j < nown && !stop; ++j) {
-        const bool bad = !mbar_wait<TW>(&full[st], parity, p.err);
-        if (__any_sync(0xffffffffu, bad)) break;
-        const char *stage = ring + st * kStage;
-        const int blk = w.blk0 + NB * (warp + kI4Warps * j);
-        const int tok0 = blk * kI4BS;
-        // ---- S^T = K q^T: tokens r, r + 8 of each block
-        float s[NB][NT][4];
+    I4Work w = i4_sequence(p, b0, kRound, kCols, false);
+    while (todo > 0) {
+        const int per = w.rounds + kI4PairCost;
+        if (unit >= w.pairs * per) {
+            base += w.pairs * per;
+            w = i4_sequence(p, w.b + 1, kRound, kCols, false);
+            unit = 0;
+            continue;
+        }
+        const int pair = unit / per, u0 = unit - pair * per;   // units u0 .. of the pair
+        const int units = min(todo, per - u0);
+        todo -= units;
+        unit += units;
+        const int round0 = max(u0 - kI4PairCost, 0), nrounds = u0 + units - kI4PairCost - round0;
+        if (nrounds <= 0) continue;  // the pair begins in this run, its rounds in the next
+        const int h = pair % p.hkv, cg = pair / p.hkv;
+        const int col0 = cg * kCols, ncols = min(kCols, w.T * p.g - col0);
+        // pieces of the pair, and which of them this is
+        int split, nsplit;
+        if (p.balanced) {
+            const int v0 = base + pair * per + kI4PairCost;  // number of the pair's first round
+            const int c0 = v0 / run, c1 = (v0 + w.rounds - 1) / run;
+            nsplit = c1 - c0 + 1;
+            split = blockIdx.x - c0;
+        } else {
+            nsplit = (w.rounds + p.part_rounds - 1) / p.part_rounds;
+            split = blockIdx.x;
+        }
+        // ---- q of each column: largest magnitude to [2^13, 2^14) by a power of two,
+        // so that fp16 holds it, then into the order of the fragments
+        __half *qs = reinterpret_cast<__half *>(s_q);
+        for (int col = warp; col < 8 * NT; col += kI4Warps) {
+            constexpr int kPer = D / 32;
+            float x[kPer];
+            if (col < ncols) {
+                const int tq = (col0 + col) / p.g, j = (col0 + col) - tq * p.g;
+                const uint16_t *src = p.q + ((size_t)(w.q0 + tq) * p.hq + h * p.g + j) * D + lane * kPer;
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+                for (int i = 0; i < kPer; ++i)
+                    x[i] = p.q_bf16 ? bf16_to_float(src[i]) : f16x2_to_float2(src[i]).x;
+            } else {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[n][nt][0] = s[n][nt][1] = s[n][nt][2] = s[n][nt][3] = 0.f;
-        {
-            uint32_t k0[NB][kW], k1[NB][kW];
-            __half2 a0[NB], a1[NB];
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const char *kt = stage + n * kTile;
-                load_words<kW>(kt + r * (D / 2) + c * (D / 8), k0[n]);
-                load_words<kW>(kt + (r + 8) * (D / 2) + c * (D / 8), k1[n]);
-                uint32_t s0, s1;
-                if constexpr (D == 128) {
-                    s0 = *reinterpret_cast<const uint16_t *>(kt + 8 * D + r * 8 + 2 * c);
-                    s1 = *reinterpret_cast<const uint16_t *>(kt + 8 * D + (r + 8) * 8 + 2 * c);
-                } else {
-                    s0 = *reinterpret_cast<const uint8_t *>(kt + 8 * D + r * 4 + c);
-                    s1 = *reinterpret_cast<const uint8_t *>(kt + 8 * D + (r + 8) * 4 + c);
-                }
-                a0[n] = i4::scale_pair(s0);
-                a1[n] = i4::scale_pair(s1);
+                for (int i = 0; i < kPer; ++i) x[i] = 0.f;
             }
-            i4::Scale g0[NB], g1[NB];
+            float m = 0.f;
 #pragma unroll
-            for (int wi = 0; wi < kW; ++wi) {
-                uint32_t x0[NB][4], x1[NB][4];
+            for (int i = 0; i < kPer; ++i) m = fmaxf(m, fabsf(x[i]));
 #pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    if (wi == 0) {
-                        g0[n] = i4::make_scale(__low2half2(a0[n]));
-                        g1[n] = i4::make_scale(__low2half2(a1[n]));
-                    } else if (D == 128 && wi == 2) {
-                        g0[n] = i4::make_scale(__high2half2(a0[n]));
-                        g1[n] = i4::make_scale(__high2half2(a1[n]));
-                    }
-                    i4::values8(k0[n][wi], g0[n], x0[n]);
-                    i4::values8(k1[n][wi], g1[n], x1[n]);
-                }
+            for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+            // exponent field of the largest; 0 (all zero or below normal) and 255 are left alone
+            const int e = (int)(__float_as_uint(m) >> 23);
+            const int up = e == 0 || e == 255 ? 0 : max(-126, min(126, 127 + 13 - e));
+            // the score's factor is made positive (its sign goes to q), so that scaling keeps
+            // the order of scores; a factor of 0 zeroes q instead
+            const float mul = copysignf(p.scale_log2 == 0.f ? 0.f : __uint_as_float((uint32_t)(127 + up) << 23), p.scale_log2);
 #pragma unroll
-                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint2 bq = s_q[((2 * wi + f) * NT + nt) * 32 + lane];
-#pragma unroll
-                        for (int n = 0; n < NB; ++n)
-                            mma_16816(s[n][nt], x0[n][2 * f], x1[n][2 * f], x0[n][2 * f + 1], x1[n][2 * f + 1], bq.x, bq.y);
-                    }
+            for (int i = 0; i < kPer; ++i) {
+                // dimension d: quarter cq, word wi, four bits n; pair n of half d / 4 % 2
+                const int d = lane * kPer + i, cq = d / (D / 4), in = d % (D / 4), wi = in / 8, n = in % 4, hi = in / 4 % 2;
+                const int pair = 4 * wi + n;
+                qs[((((pair >> 1) * NT + (col >> 3)) * 32 + (col & 7) * 4 + cq) * 2 + (pair & 1)) * 2 + hi] =
+                    __float2half_rn(x[i] * mul);
             }
+            if (lane == 0)
+                s_scale[col] = p.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 - up) << 23), 1e-37f);
         }
-        // ---- V: token pairs c, c + 4 of each block, dimensions D / 8 r ..
-        uint32_t v0[NB][kW], v1[NB][kW], vs0[NB], vs1[NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const char *vt = stage + (NB + n) * kTile;
-            load_words<kW>(vt + c * D + 4 * ((r * kW) ^ i4::v_swizzle<D>(c)), v0[n]);
-            load_words<kW>(vt + (c + 4) * D + 4 * ((r * kW) ^ i4::v_swizzle<D>(c + 4)), v1[n]);
-            const int gr = D == 128 ? 2 * r : (r & ~1);
-            vs0[n] = *reinterpret_cast<const uint16_t *>(vt + 8 * D + c * (D / 8) + gr);
-            vs1[n] = *reinterpret_cast<const uint16_t *>(vt + 8 * D + (c + 4) * (D / 8) + gr);
-        }
-        // tokens past the sequence or the partition, or in a block that is not there
-        const int end = (int)min((long long)(w.blk0 + w.nloc) * kI4BS, w.L);
-        bool whole = tok0 + NB * kI4BS <= end;
-        int ntok[NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const int there = valid[st * NB + n];
-            whole = whole && there;
-            ntok[n] = there ? min(kI4BS, end - (tok0 + n * kI4BS)) : 0;
-        }
-        // the stage is in registers: its next group may come
-        __syncwarp();
-        if (issued < nown) issue(st);
-        if (++st == NST) {
-            st = 0;
-            parity ^= 1;
-        }
+        __syncthreads();
 
-        // ---- softmax: s[0], s[1] token r, columns 2 c, 2 c + 1; s[2], s[3] token r + 8
-        uint32_t ph[NB][NT][2], pl[NB][NT][2];
-        const bool masked = !whole || tok0 + NB * kI4BS > least;
-        if (masked) {
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int t = r + 4 * (x & 2);
-                        if (t >= ntok[n] || tok0 + n * kI4BS + t >= lim[nt][x & 1]) s[n][nt][x] = -INFINITY;
-                    }
-        }
-        bool renew = false;
-        float top[NT][2];
+        // ---- state of columns 8 nt + 2 c and + 1 (maxima replicated over r)
+        float m_run[NT][2], l_run[NT][2], o[NT][kSteps][4], sc[NT][2];
+        int lim[NT][2];  // keys that the column sees
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                float m = fmaxf(s[0][nt][x], s[0][nt][2 + x]);
+                const int col = 8 * nt + 2 * c + x;
+                m_run[nt][x] = -INFINITY;
+                l_run[nt][x] = 0.f;
+                sc[nt][x] = s_scale[col];
+                lim[nt][x] = w.L - w.T + min((col0 + col) / p.g, w.T - 1) + 1;
 #pragma unroll
-                for (int n = 1; n < NB; ++n) m = fmaxf(m, fmaxf(s[n][nt][x], s[n][nt][2 + x]));
-#pragma unroll
-                for (int y = 4; y <= 16; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
-                top[nt][x] = m * sc[nt][x];
-                renew |= top[nt][x] > m_run[nt][x] + kI4Renew;
+                for (int f = 0; f < kSteps; ++f) o[nt][f][x] = o[nt][f][2 + x] = 0.f;
             }
-        if (__any_sync(0xffffffffu, renew)) {
+        const int least = w.L - w.T + col0 / p.g + 1;  // keys that every column sees
+
+        for (int j = 0; j < nrounds && !stop; ++j) {
+            const bool bad = !mbar_wait<TW>(&full[st], parity, p.err);
+            stop = __any_sync(0xffffffffu, bad);
+            if (stop) break;
+            const char *stage = ring + st * kStage;
+            const int tok0 = ((round0 + j) * kRound + NB * warp) * kI4BS;
+            // ---- S^T = K q^T: tokens r, r + 8 of each block
+            float s[NB][NT][4];
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[n][nt][0] = s[n][nt][1] = s[n][nt][2] = s[n][nt][3] = 0.f;
+            {
+                uint32_t k0[NB][kW], k1[NB][kW];
+                __half2 a0[NB], a1[NB];
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const char *kt = stage + n * kTile;
+                    load_words<kW>(kt + r * (D / 2) + c * (D / 8), k0[n]);
+                    load_words<kW>(kt + (r + 8) * (D / 2) + c * (D / 8), k1[n]);
+                    uint32_t s0, s1;
+                    if constexpr (D == 128) {
+                        s0 = *reinterpret_cast<const uint16_t *>(kt + 8 * D + r * 8 + 2 * c);
+                        s1 = *reinterpret_cast<const uint16_t *>(kt + 8 * D + (r + 8) * 8 + 2 * c);
+                    } else {
+                        s0 = *reinterpret_cast<const uint8_t *>(kt + 8 * D + r * 4 + c);
+                        s1 = *reinterpret_cast<const uint8_t *>(kt + 8 * D + (r + 8) * 4 + c);
+                    }
+                    a0[n] = i4::scale_pair(s0);
+                    a1[n] = i4::scale_pair(s1);
+                }
+                i4::Scale g0[NB], g1[NB];
+#pragma unroll
+                for (int wi = 0; wi < kW; ++wi) {
+                    uint32_t x0[NB][4], x1[NB][4];
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        if (wi == 0) {
+                            g0[n] = i4::make_scale(__low2half2(a0[n]));
+                            g1[n] = i4::make_scale(__low2half2(a1[n]));
+                        } else if (D == 128 && wi == 2) {
+                            g0[n] = i4::make_scale(__high2half2(a0[n]));
+                            g1[n] = i4::make_scale(__high2half2(a1[n]));
+                        }
+                        i4::values8(k0[n][wi], g0[n], x0[n]);
+                        i4::values8(k1[n][wi], g1[n], x1[n]);
+                    }
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint2 bq = s_q[((2 * wi + f) * NT + nt) * 32 + lane];
+#pragma unroll
+                            for (int n = 0; n < NB; ++n)
+                                mma_16816(s[n][nt], x0[n][2 * f], x1[n][2 * f], x0[n][2 * f + 1], x1[n][2 * f + 1], bq.x, bq.y);
+                        }
+                }
+            }
+            // ---- V: token pairs c, c + 4 of each block, dimensions D / 8 r ..
+            uint32_t v0[NB][kW], v1[NB][kW], vs0[NB], vs1[NB];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const char *vt = stage + (NB + n) * kTile;
+                load_words<kW>(vt + c * D + 4 * ((r * kW) ^ i4::v_swizzle<D>(c)), v0[n]);
+                load_words<kW>(vt + (c + 4) * D + 4 * ((r * kW) ^ i4::v_swizzle<D>(c + 4)), v1[n]);
+                const int gr = D == 128 ? 2 * r : (r & ~1);
+                vs0[n] = *reinterpret_cast<const uint16_t *>(vt + 8 * D + c * (D / 8) + gr);
+                vs1[n] = *reinterpret_cast<const uint16_t *>(vt + 8 * D + (c + 4) * (D / 8) + gr);
+            }
+            // tokens past the sequence, or in a block that is not there
+            bool whole = tok0 + NB * kI4BS <= w.L;
+            int ntok[NB];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const int there = valid[st * NB + n];
+                whole = whole && there;
+                ntok[n] = there ? min(kI4BS, w.L - (tok0 + n * kI4BS)) : 0;
+            }
+            // the stage is in registers: its next group may come
+            __syncwarp();
+            if (more) issue(st);
+            if (++st == NST) {
+                st = 0;
+                parity ^= 1;
+            }
+
+            // ---- softmax: s[0], s[1] token r, columns 2 c, 2 c + 1; s[2], s[3] token r + 8
+            uint32_t ph[NB][NT][2], pl[NB][NT][2];
+            const bool masked = !whole || tok0 + NB * kI4BS > least;
+            if (masked) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int t = r + 4 * (x & 2);
+                            if (t >= ntok[n] || tok0 + n * kI4BS + t >= lim[nt][x & 1]) s[n][nt][x] = -INFINITY;
+                        }
+            }
+            bool renew = false;
+            float top[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    // 2^(old - new); an empty state has a reference of -inf
-                    const float m = top[nt][x] > m_run[nt][x] + kI4Renew ? top[nt][x] : m_run[nt][x];
-                    const float a = m == m_run[nt][x] ? 1.f : ex2(m_run[nt][x] - m);
-                    m_run[nt][x] = m;
-                    l_run[nt][x] *= a;
+                    float m = fmaxf(s[0][nt][x], s[0][nt][2 + x]);
 #pragma unroll
-                    for (int f = 0; f < kSteps; ++f) {
-                        o[nt][f][x] *= a;
-                        o[nt][f][2 + x] *= a;
+                    for (int n = 1; n < NB; ++n) m = fmaxf(m, fmaxf(s[n][nt][x], s[n][nt][2 + x]));
+#pragma unroll
+                    for (int y = 4; y <= 16; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
+                    top[nt][x] = m * sc[nt][x];
+                    renew |= top[nt][x] > m_run[nt][x] + kI4Renew;
+                }
+            if (__any_sync(0xffffffffu, renew)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        // 2^(old - new); an empty state has a reference of -inf
+                        const float m = top[nt][x] > m_run[nt][x] + kI4Renew ? top[nt][x] : m_run[nt][x];
+                        const float a = m == m_run[nt][x] ? 1.f : ex2(m_run[nt][x] - m);
+                        m_run[nt][x] = m;
+                        l_run[nt][x] *= a;
+#pragma unroll
+                        for (int f = 0; f < kSteps; ++f) {
+                            o[nt][f][x] *= a;
+                            o[nt][f][2 + x] *= a;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float u0 = m_run[nt][0] == -INFINITY ? 0.f : kI4Bias - m_run[nt][0];
+                const float u1 = m_run[nt][1] == -INFINITY ? 0.f : kI4Bias - m_run[nt][1];
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const float p0 = ex2(fmaf(s[n][nt][0], sc[nt][0], u0)), p1 = ex2(fmaf(s[n][nt][1], sc[nt][1], u1));
+                    const float p2 = ex2(fmaf(s[n][nt][2], sc[nt][0], u0)), p3 = ex2(fmaf(s[n][nt][3], sc[nt][1], u1));
+                    l_run[nt][0] += p0 + p2;
+                    l_run[nt][1] += p1 + p3;
+                    const uint32_t h01 = half_pair(p0, p1), h23 = half_pair(p2, p3);
+                    ph[n][nt][0] = transpose8(h01);
+                    ph[n][nt][1] = transpose8(h23);
+                    if constexpr (EXACT) {
+                        const float2 f01 = f16x2_to_float2(h01), f23 = f16x2_to_float2(h23);
+                        pl[n][nt][0] = transpose8(half_pair(p0 - f01.x, p1 - f01.y));
+                        pl[n][nt][1] = transpose8(half_pair(p2 - f23.x, p3 - f23.y));
                     }
                 }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const float u0 = m_run[nt][0] == -INFINITY ? 0.f : kI4Bias - m_run[nt][0];
-            const float u1 = m_run[nt][1] == -INFINITY ? 0.f : kI4Bias - m_run[nt][1];
+            }
+            // ---- O^T += V^T P^T.  Slots past the sequence may hold anything: a scale
+            // of zero makes their values zero (codes are finite).
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const float p0 = ex2(fmaf(s[n][nt][0], sc[nt][0], u0)), p1 = ex2(fmaf(s[n][nt][1], sc[nt][1], u1));
-                const float p2 = ex2(fmaf(s[n][nt][2], sc[nt][0], u0)), p3 = ex2(fmaf(s[n][nt][3], sc[nt][1], u1));
-                l_run[nt][0] += p0 + p2;
-                l_run[nt][1] += p1 + p3;
-                const uint32_t h01 = half_pair(p0, p1), h23 = half_pair(p2, p3);
-                ph[n][nt][0] = transpose8(h01);
-                ph[n][nt][1] = transpose8(h23);
-                if constexpr (EXACT) {
-                    const float2 f01 = f16x2_to_float2(h01), f23 = f16x2_to_float2(h23);
-                    pl[n][nt][0] = transpose8(half_pair(p0 - f01.x, p1 - f01.y));
-                    pl[n][nt][1] = transpose8(half_pair(p2 - f23.x, p3 - f23.y));
+                __half2 a = i4::scale_pair(vs0[n]), e = i4::scale_pair(vs1[n]);
+                if (!whole) {
+                    uint32_t ab = *reinterpret_cast<uint32_t *>(&a), eb = *reinterpret_cast<uint32_t *>(&e);
+                    ab &= (2 * c < ntok[n] ? 0xffffu : 0u) | (2 * c + 1 < ntok[n] ? 0xffff0000u : 0u);
+                    eb &= (2 * c + 8 < ntok[n] ? 0xffffu : 0u) | (2 * c + 9 < ntok[n] ? 0xffff0000u : 0u);
+                    a = *reinterpret_cast<__half2 *>(&ab);
+                    e = *reinterpret_cast<__half2 *>(&eb);
+                }
+                const i4::Scale g0 = i4::make_scale(a), g1 = i4::make_scale(e);
+#pragma unroll
+                for (int wi = 0; wi < kW; ++wi) {
+                    uint32_t x0[4], x1[4];
+                    i4::values8(v0[n][wi], g0, x0);
+                    i4::values8(v1[n][wi], g1, x1);
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_16816(o[nt][2 * wi + f], x0[2 * f], x0[2 * f + 1], x1[2 * f], x1[2 * f + 1], ph[n][nt][0],
+                                      ph[n][nt][1]);
+                            if constexpr (EXACT)
+                                mma_16816(o[nt][2 * wi + f], x0[2 * f], x0[2 * f + 1], x1[2 * f], x1[2 * f + 1], pl[n][nt][0],
+                                          pl[n][nt][1]);
+                        }
                 }
             }
         }
-        // ---- O^T += V^T P^T.  Slots past the sequence may hold anything: a scale
-        // of zero makes their values zero (codes are finite).
+
+        // ---- the four warps' states to this piece's result, eight columns at a time
+        float4 *sm_o = reinterpret_cast<float4 *>(smem + kRing);  // [warp][column][D / 4], see `at`
+        constexpr int kQ = D / 32;                         // float4s of one lane's dims
+        auto at = [&](int wp, int col, int rr, int i) {    // spread over the banks
+            return (wp * 8 + col) * (D / 4) + rr * kQ + (i ^ ((col >> 1) & (kQ - 1)));
+        };
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            __half2 a = i4::scale_pair(vs0[n]), e = i4::scale_pair(vs1[n]);
-            if (!whole) {
-                uint32_t ab = *reinterpret_cast<uint32_t *>(&a), eb = *reinterpret_cast<uint32_t *>(&e);
-                ab &= (2 * c < ntok[n] ? 0xffffu : 0u) | (2 * c + 1 < ntok[n] ? 0xffff0000u : 0u);
-                eb &= (2 * c + 8 < ntok[n] ? 0xffffu : 0u) | (2 * c + 9 < ntok[n] ? 0xffff0000u : 0u);
-                a = *reinterpret_cast<__half2 *>(&ab);
-                e = *reinterpret_cast<__half2 *>(&eb);
+        for (int nt = 0; nt < NT; ++nt) {
+            float l0 = l_run[nt][0], l1 = l_run[nt][1];
+#pragma unroll
+            for (int x = 4; x <= 16; x <<= 1) {
+                l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+                l1 += __shfl_xor_sync(0xffffffffu, l1, x);
             }
-            const i4::Scale g0 = i4::make_scale(a), g1 = i4::make_scale(e);
+            if (nt > 0) __syncthreads();  // the previous columns have been read
 #pragma unroll
-            for (int wi = 0; wi < kW; ++wi) {
-                uint32_t x0[4], x1[4];
-                i4::values8(v0[n][wi], g0, x0);
-                i4::values8(v1[n][wi], g1, x1);
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int f = 0; f < 2; ++f)
+                for (int i = 0; i < kQ; ++i)
+                    sm_o[at(warp, 2 * c + x, r, i)] =
+                        make_float4(o[nt][2 * i][x], o[nt][2 * i][2 + x], o[nt][2 * i + 1][x], o[nt][2 * i + 1][2 + x]);
+            if (r == 0) {
+                // the weights are relative to m - kI4Bias
+                s_m[warp * 8 + 2 * c] = m_run[nt][0] - kI4Bias;
+                s_m[warp * 8 + 2 * c + 1] = m_run[nt][1] - kI4Bias;
+                s_l[warp * 8 + 2 * c] = l0;
+                s_l[warp * 8 + 2 * c + 1] = l1;
+            }
+            __syncthreads();
+            const int live = min(8, ncols - 8 * nt);
+            for (int idx = tid; idx < live * (D / 4); idx += kI4Threads) {
+                const int col = idx / (D / 4), d4 = idx % (D / 4);
+                float M = s_m[col];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_16816(o[nt][2 * wi + f], x0[2 * f], x0[2 * f + 1], x1[2 * f], x1[2 * f + 1], ph[n][nt][0],
-                                  ph[n][nt][1]);
-                        if constexpr (EXACT)
-                            mma_16816(o[nt][2 * wi + f], x0[2 * f], x0[2 * f + 1], x1[2 * f], x1[2 * f + 1], pl[n][nt][0],
-                                      pl[n][nt][1]);
-                    }
+                for (int wp = 1; wp < kI4Warps; ++wp) M = fmaxf(M, s_m[wp * 8 + col]);
+                float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+                float den = 0.f;
+#pragma unroll
+                for (int wp = 0; wp < kI4Warps; ++wp) {
+                    const float lw = s_l[wp * 8 + col];
+                    if (lw == 0.f) continue;  // saw no key
+                    const float f = ex2(s_m[wp * 8 + col] - M);
+                    const float4 v = sm_o[at(wp, col, d4 / kQ, d4 % kQ)];
+                    num.x += f * v.x;
+                    num.y += f * v.y;
+                    num.z += f * v.z;
+                    num.w += f * v.w;
+                    den += f * lw;
+                }
+                const float inv = den != 0.f ? p.v_mul / den : 0.f;  // den NaN: NaN
+                const int gc = col0 + 8 * nt + col, tq = gc / p.g;
+                const int hq = h * p.g + (gc - tq * p.g);
+                const size_t orow = out_row(p, w, tq, hq);
+                const float4 v = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+                const float lse2 = den != 0.f ? M + log2f(den) : -INFINITY;
+                if (nsplit == 1) {
+                    store_out4(p.out, orow * D + 4 * d4, v, p.out_type);
+                    if (p.lse && d4 == 0) p.lse[orow] = lse2 * 0.6931471805599453f;
+                } else {
+                    const size_t slot = ws_row(p, w, tq, hq) * p.max_splits + split;
+                    reinterpret_cast<float4 *>(p.ws_o)[slot * (D / 4) + d4] = v;
+                    if (d4 == 0) p.ws_lse[slot] = lse2;
+                }
             }
         }
+        if (nsplit == 1 || !p.counters) continue;
+        int *counter = p.counters + ((size_t)w.b * p.col_groups + cg) * p.hkv + h;
+        if (nsplit > kFuseMaxSplits) {  // for merge_i4_kernel
+            if (split == 0 && tid == 0) *counter = nsplit;
+            continue;
+        }
+        // ---- the last piece to finish merges them all
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) s_last = atomicAdd(counter, 1) == nsplit - 1;
+        __syncthreads();
+        if (!s_last) continue;
+        __threadfence();
+        float *wt = reinterpret_cast<float *>(smem + kRing);  // [8 NT][kFuseMaxSplits]
+        for (int col = warp; col < ncols; col += kI4Warps) {
+            const int gc = col0 + col, tq = gc / p.g;
+            const int hq = h * p.g + (gc - tq * p.g);
+            const size_t orow = out_row(p, w, tq, hq), wrow = ws_row(p, w, tq, hq);
+            const float x = lane < nsplit ? __ldcg(p.ws_lse + wrow * p.max_splits + lane) : -INFINITY;
+            float M = x;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+            const float e = x == -INFINITY ? 0.f : ex2(x - M);  // NaN stays
+            float den = e;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) den += __shfl_xor_sync(0xffffffffu, den, s);
+            wt[col * kFuseMaxSplits + lane] = den != 0.f ? e / den : 0.f;
+            if (p.lse && lane == 0) p.lse[orow] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+        }
+        __syncthreads();
+        for (int idx = tid; idx < ncols * (D / 4); idx += kI4Threads) {
+            const int col = idx / (D / 4), d4 = idx % (D / 4);
+            const int gc = col0 + col, tq = gc / p.g;
+            const int hq = h * p.g + (gc - tq * p.g);
+            const size_t orow = out_row(p, w, tq, hq);
+            const float4 *src = reinterpret_cast<const float4 *>(p.ws_o) + ws_row(p, w, tq, hq) * p.max_splits * (D / 4) + d4;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int s = 0; s < nsplit; ++s) {
+                const float f = wt[col * kFuseMaxSplits + s];
+                const float4 v = __ldcg(src + (size_t)s * (D / 4));
+                acc.x += f * v.x;
+                acc.y += f * v.y;
+                acc.z += f * v.z;
+                acc.w += f * v.w;
+            }
+            store_out4(p.out, orow * D + 4 * d4, acc, p.out_type);
+        }
+        if (tid == 0) *counter = 0;  // ready for the next call
     }
     // After a timed-out wait: no copy may still be on its way into this CTA's memory.
     for (int j = max(0, issued - NST); j < issued; ++j) mbar_wait_drain(&full[j % NST], (j / NST) & 1, p.err);
-
-    // ---- the four warps' states to this partition's result, eight columns at a time
-    float4 *sm_o = reinterpret_cast<float4 *>(smem);  // [warp][column][D / 4], see `at`
-    constexpr int kQ = D / 32;                         // float4s of one lane's dims
-    auto at = [&](int wp, int col, int rr, int i) {    // spread over the banks
-        return (wp * 8 + col) * (D / 4) + rr * kQ + (i ^ ((col >> 1) & (kQ - 1)));
-    };
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float l0 = l_run[nt][0], l1 = l_run[nt][1];
-#pragma unroll
-        for (int x = 4; x <= 16; x <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-        }
-        __syncthreads();  // the rings, or the previous columns, have been read
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int i = 0; i < kQ; ++i)
-                sm_o[at(warp, 2 * c + x, r, i)] =
-                    make_float4(o[nt][2 * i][x], o[nt][2 * i][2 + x], o[nt][2 * i + 1][x], o[nt][2 * i + 1][2 + x]);
-        if (r == 0) {
-            // the weights are relative to m - kI4Bias
-            s_m[warp * 8 + 2 * c] = m_run[nt][0] - kI4Bias;
-            s_m[warp * 8 + 2 * c + 1] = m_run[nt][1] - kI4Bias;
-            s_l[warp * 8 + 2 * c] = l0;
-            s_l[warp * 8 + 2 * c + 1] = l1;
-        }
-        __syncthreads();
-        const int live = min(8, ncols - 8 * nt);
-        for (int idx = tid; idx < live * (D / 4); idx += kI4Threads) {
-            const int col = idx / (D / 4), d4 = idx % (D / 4);
-            float M = s_m[col];
-#pragma unroll
-            for (int wp = 1; wp < kI4Warps; ++wp) M = fmaxf(M, s_m[wp * 8 + col]);
-            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-            float den = 0.f;
-#pragma unroll
-            for (int wp = 0; wp < kI4Warps; ++wp) {
-                const float lw = s_l[wp * 8 + col];
-                if (lw == 0.f) continue;  // saw no key
-                const float f = ex2(s_m[wp * 8 + col] - M);
-                const float4 v = sm_o[at(wp, col, d4 / kQ, d4 % kQ)];
-                num.x += f * v.x;
-                num.y += f * v.y;
-                num.z += f * v.z;
-                num.w += f * v.w;
-                den += f * lw;
-            }
-            const float inv = den != 0.f ? p.v_mul / den : 0.f;  // den NaN: NaN
-            const int gc = col0 + 8 * nt + col, tq = gc / p.g;
-            const int hq = h * p.g + (gc - tq * p.g);
-            const size_t orow = out_row(p, w, tq, hq);
-            const float4 v = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-            const float lse2 = den != 0.f ? M + log2f(den) : -INFINITY;
-            if (w.nsplit == 1) {
-                store_out4(p.out, orow * D + 4 * d4, v, p.out_type);
-                if (p.lse && d4 == 0) p.lse[orow] = lse2 * 0.6931471805599453f;
-            } else {
-                const size_t slot = ws_row(p, w, tq, hq) * p.max_splits + split;
-                reinterpret_cast<float4 *>(p.ws_o)[slot * (D / 4) + d4] = v;
-                if (d4 == 0) p.ws_lse[slot] = lse2;
-            }
-        }
-    }
-    if (w.nsplit == 1 || !p.counters || w.nsplit > kFuseMaxSplits) return;
-
-    // ---- the last partition to finish merges them all
-    __threadfence();
-    __syncthreads();
-    int *counter = p.counters + ((size_t)b * p.col_groups + cg) * p.hkv + h;
-    if (tid == 0) s_last = atomicAdd(counter, 1) == w.nsplit - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    float *wt = reinterpret_cast<float *>(smem);  // [8 NT][kFuseMaxSplits]
-    for (int col = warp; col < ncols; col += kI4Warps) {
-        const int gc = col0 + col, tq = gc / p.g;
-        const int hq = h * p.g + (gc - tq * p.g);
-        const size_t orow = out_row(p, w, tq, hq), wrow = ws_row(p, w, tq, hq);
-        const float x = lane < w.nsplit ? __ldcg(p.ws_lse + wrow * p.max_splits + lane) : -INFINITY;
-        float M = x;
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-        const float e = x == -INFINITY ? 0.f : ex2(x - M);  // NaN stays
-        float den = e;
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) den += __shfl_xor_sync(0xffffffffu, den, s);
-        wt[col * kFuseMaxSplits + lane] = den != 0.f ? e / den : 0.f;
-        if (p.lse && lane == 0) p.lse[orow] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
-    }
-    __syncthreads();
-    for (int idx = tid; idx < ncols * (D / 4); idx += kI4Threads) {
-        const int col = idx / (D / 4), d4 = idx % (D / 4);
-        const int gc = col0 + col, tq = gc / p.g;
-        const int hq = h * p.g + (gc - tq * p.g);
-        const size_t orow = out_row(p, w, tq, hq);
-        const float4 *src = reinterpret_cast<const float4 *>(p.ws_o) + ws_row(p, w, tq, hq) * p.max_splits * (D / 4) + d4;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int s = 0; s < w.nsplit; ++s) {
-            const float f = wt[col * kFuseMaxSplits + s];
-            const float4 v = __ldcg(src + (size_t)s * (D / 4));
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
-        }
-        store_out4(p.out, orow * D + 4 * d4, acc, p.out_type);
-    }
-    if (tid == 0) *counter = 0;  // ready for the next call
 }
 
 // Merge of rows cut into more partitions than one CTA merges: one CTA per query
 // row, its threads in groups of D / 4 that take every group-th partition.
 template <int D>
-__global__ void __launch_bounds__(kI4Threads) merge_i4_kernel(const I4Params p, int min_splits) {
+__global__ void __launch_bounds__(kI4Threads) merge_i4_kernel(const I4Params p) {
     constexpr int kLanes = D / 4, kGroups = kI4Threads / kLanes;
     const int tq = blockIdx.x / p.hq, hq = blockIdx.x % p.hq;
-    I4Work w;
-    if (!i4_sequence(p, blockIdx.y, false, w) || tq >= w.T || w.nsplit < min_splits) return;
+    const I4Work w = i4_sequence(p, blockIdx.y, p.round_blocks, p.cols, false);
+    if (!w.pairs || tq >= w.T) return;
+    const int gc = tq * p.g + hq % p.g;  // its column
+    int nsplit;
+    if (p.counters) {  // what the pair's first piece left, if it is for this kernel
+        // Each row of the pair takes it with an arrival in the upper half; the last
+        // leaves the counter at 0.
+        int *counter = p.counters + ((size_t)w.b * p.col_groups + gc / p.cols) * p.hkv + hq / p.g;
+        __shared__ int s_n;
+        if (threadIdx.x == 0) {
+            s_n = 0;
+            if (*counter) {
+                const unsigned x = (unsigned)atomicAdd(counter, 1 << 16);
+                s_n = (int)(x & 0xffffu);
+                if ((int)(x >> 16) == min(p.cols, w.T * p.g - gc / p.cols * p.cols) - 1) *counter = 0;
+            }
+        }
+        __syncthreads();
+        nsplit = s_n;
+    } else {
+        nsplit = (w.rounds + p.part_rounds - 1) / p.part_rounds;
+    }
+    if (nsplit < 2) return;
     const int tid = threadIdx.x, d4 = tid % kLanes, grp = tid / kLanes;
     const size_t orow = out_row(p, w, tq, hq), wrow = ws_row(p, w, tq, hq);
     const float *ls = p.ws_lse + wrow * p.max_splits;
@@ -638,7 +796,7 @@ __global__ void __launch_bounds__(kI4Threads) merge_i4_kernel(const I4Params p, 
     __shared__ float4 s_acc[kI4Threads];
     __shared__ float s_den[kGroups];
     float M = -INFINITY;
-    for (int s = tid; s < w.nsplit; s += kI4Threads) M = fmaxf(M, ls[s]);
+    for (int s = tid; s < nsplit; s += kI4Threads) M = fmaxf(M, ls[s]);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
     if ((tid & 31) == 0) s_red[tid >> 5] = M;
@@ -649,7 +807,7 @@ __global__ void __launch_bounds__(kI4Threads) merge_i4_kernel(const I4Params p, 
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f;
 #pragma unroll 4
-    for (int s = grp; s < w.nsplit; s += kGroups) {
+    for (int s = grp; s < nsplit; s += kGroups) {
         const float x = ls[s], e = x == -INFINITY ? 0.f : ex2(x - M);
         const float4 v = src[(size_t)s * kLanes];
         acc.x += e * v.x;
@@ -680,7 +838,7 @@ __global__ void __launch_bounds__(kI4Threads) merge_i4_kernel(const I4Params p, 
 cudaError_t set_wait_limit_decode_i4(unsigned long long ns) { return set_wait_limit_here(ns); }
 
 template <int D, int NT, int NB, int NST, int MINB>
-static kv_status launch_i4(const I4Params &p, dim3 grid, cudaStream_t s) {
+static kv_status launch_i4(I4Params &p, int part_blocks, cudaStream_t s) {
     const bool exact = p.out_type == KV_F32, tw = test_waits_enabled();
     auto fn = exact ? (tw ? decode_i4_kernel<D, NT, true, true, NB, NST, MINB>
                           : decode_i4_kernel<D, NT, true, false, NB, NST, MINB>)
@@ -689,6 +847,14 @@ static kv_status launch_i4(const I4Params &p, dim3 grid, cudaStream_t s) {
     constexpr size_t smem = i4_smem_bytes<D, NB, NST>();
     if (kv_status st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
         return st;
+    p.round_blocks = NB * kI4Warps;
+    p.cols = 8 * NT;
+    p.part_rounds = (part_blocks + p.round_blocks - 1) / p.round_blocks;
+    const long long pairs = (long long)p.batch * p.col_groups * p.hkv;
+    const long long units = pairs * (p.max_blocks / p.round_blocks + 1 + kI4PairCost);
+    p.balanced = p.max_splits > 1 && p.counters && p.batch <= kI4ScanBatch && units < (1 << 30);
+    dim3 grid(p.max_splits, p.hkv, p.batch * p.col_groups);
+    if (p.balanced) grid = dim3((unsigned)std::min<long long>((long long)MINB * sm_count(), units));
     fn<<<grid, kI4Threads, smem, s>>>(p);
     return cuda_status(cudaGetLastError());
 }
@@ -726,7 +892,6 @@ kv_status attend_i4(const I4Call &a) {
     p.g = g;
     p.scale_log2 = a.scale * 1.4426950408889634f * i4::kScaleUnit * pool->k_scale;
     p.v_mul = i4::kScaleUnit * pool->v_scale;
-    p.part_blocks = pb;
     p.max_splits = ms;
     p.col_groups = groups;
     p.out = a.out;
@@ -734,29 +899,24 @@ kv_status attend_i4(const I4Call &a) {
     p.lse = a.lse;
     p.ws_o = static_cast<float *>(a.workspace);
     p.ws_lse = p.ws_o ? p.ws_o + (size_t)rows * a.num_q_heads * ms * pool->head_dim : nullptr;
-    const bool fused = (long long)a.batch * groups * pool->num_kv_heads <= kv_pool::kCounterSlots;
-    p.counters = fused ? pool->counters : nullptr;
+    const bool counted = (long long)a.batch * groups * pool->num_kv_heads <= kv_pool::kCounterSlots;
+    p.counters = counted ? pool->counters : nullptr;
     p.err = pool->err;
-    const dim3 grid(ms, pool->num_kv_heads, a.batch * groups);
     kv_status st;
     if (pool->head_dim == 64)
-        st = nt == 1 ? launch_i4<64, 1, 2, 3, 5>(p, grid, a.stream) : KV_ERR_UNSUPPORTED;
+        st = nt == 1 ? launch_i4<64, 1, 2, 3, 5>(p, pb, a.stream) : KV_ERR_UNSUPPORTED;
     else
-        st = nt == 1   ? launch_i4<128, 1, 2, 2, 4>(p, grid, a.stream)
-             : nt == 2 ? launch_i4<128, 2, 1, 4, 3>(p, grid, a.stream)
-             : nt == 3 ? launch_i4<128, 3, 1, 4, 2>(p, grid, a.stream)
-                       : launch_i4<128, 4, 1, 4, 2>(p, grid, a.stream);
-    if (st != KV_OK) return st;
-    const int min_splits = fused ? kFuseMaxSplits + 1 : 2;
-    if (ms >= min_splits) {
-        const dim3 mgrid(a.num_q_heads * a.max_q_len, a.batch);
-        if (pool->head_dim == 64)
-            merge_i4_kernel<64><<<mgrid, kI4Threads, 0, a.stream>>>(p, min_splits);
-        else
-            merge_i4_kernel<128><<<mgrid, kI4Threads, 0, a.stream>>>(p, min_splits);
-        return cuda_status(cudaGetLastError());
-    }
-    return KV_OK;
+        st = nt == 1   ? launch_i4<128, 1, 2, 2, 4>(p, pb, a.stream)
+             : nt == 2 ? launch_i4<128, 2, 1, 4, 3>(p, pb, a.stream)
+             : nt == 3 ? launch_i4<128, 3, 1, 4, 2>(p, pb, a.stream)
+                       : launch_i4<128, 4, 1, 4, 2>(p, pb, a.stream);
+    if (st != KV_OK || ms < (counted ? kFuseMaxSplits + 1 : 2)) return st;
+    const dim3 mgrid(a.num_q_heads * a.max_q_len, a.batch);
+    if (pool->head_dim == 64)
+        merge_i4_kernel<64><<<mgrid, kI4Threads, 0, a.stream>>>(p);
+    else
+        merge_i4_kernel<128><<<mgrid, kI4Threads, 0, a.stream>>>(p);
+    return cuda_status(cudaGetLastError());
 }
 
 }  // namespace pkv
@@ -771,19 +931,26 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
         return KV_ERR_ARG;
     *num_splits = 1;
     if (batch == 0 || max_blocks == 0) return KV_OK;
-    // One wave: the smallest partitions whose CTAs fit five to an SM.
-    const long long wave = 5LL * sm_count();
-    for (int s = 1; s <= 4096; ++s) {
+    // The pieces that the longest pair is cut into by equal runs of one wave (the
+    // kernel's own arithmetic: rounds of 8 blocks, four CTAs per SM).
+    constexpr int kRound = 8;
+    long long units = 0, most = 1;
+    for (int b = 0; b < batch; ++b) {
+        const long long L = std::min<long long>(std::max(host_seq_lens[b], 0), (long long)max_blocks * kI4BS);
+        const long long n = std::max<long long>(1, (L + kRound * kI4BS - 1) / (kRound * kI4BS));
+        units += num_kv_heads * (n + kI4PairCost);
+        most = std::max(most, n);
+    }
+    const long long wave = 4LL * sm_count(), run = std::max<long long>(kI4MinRun, (units + wave - 1) / wave);
+    if (most < 2) return KV_OK;
+    const long long pieces = (most - 2) / run + 2;
+    // split_plan's partitions are whole multiples of four blocks: the split count that
+    // gives at least as many
+    for (int s = (int)std::min<long long>(pieces, max_blocks);; ++s) {
         int pb, ms;
         split_plan(batch, num_kv_heads, max_blocks, s, &pb, &ms);
-        long long ctas = 0;
-        for (int b = 0; b < batch; ++b) {
-            const long long L = std::min<long long>(std::max(host_seq_lens[b], 0), (long long)max_blocks * kI4BS);
-            const long long n = (L + kI4BS - 1) / kI4BS;
-            ctas += std::max<long long>(1, (n + pb - 1) / pb);
-        }
-        if (ctas * num_kv_heads <= wave) *num_splits = s;
-        if (pb <= 2 * kI4Warps) break;
+        *num_splits = s;
+        if (ms >= pieces || pb <= kI4Warps || s >= max_blocks) break;
     }
     return KV_OK;
 }
