@@ -365,8 +365,10 @@ kv_status kv_swap_bytes(kv_pool_t p, int n, size_t *bytes);
  * paged_decode_attention_i4 and paged_prefill_attention_i4 attend over it; block
  * management, kv_copy_blocks, kv_cow_if_shared and the swap calls move its blocks
  * as they move others.  kv_append and the other attention calls return
- * KV_ERR_UNSUPPORTED for it.  kv_pool_ptrs' arrays hold one tile of 9 * head_dim
- * bytes per (block, kv head): codes, then scales.
+ * KV_ERR_UNSUPPORTED for it.  Its memory is one array of tiles of 9 * head_dim bytes
+ * (codes, then scales): for each (block, kv head) the K tile, then the V tile;
+ * kv_pool_ptrs gives the first of each.  kv_swap_out's layout of a block is its bytes
+ * in this order.
  * -------------------------------------------------------------------- */
 
 /* The pool's scales g of K and V: powers of two from 2^-32 to 2^32 (scaling by

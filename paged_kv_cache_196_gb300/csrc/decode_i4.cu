@@ -10,17 +10,18 @@
 // operation and one fused multiply-add make two codes into a scaled fp16 pair
 // (i4::values8: 9 instructions for 8 codes), the layout of a tile puts each
 // lane's operands of the tensor core's fragments into consecutive bytes (no
-// ldmatrix, no shuffles), the scales of a lane's rows are two bytes a load, and a
-// warp takes NB blocks at a time, so that waiting, issuing, the maximum over lanes
-// and the test for a new maximum are paid once per NB blocks.
+// ldmatrix, no shuffles), the scales of a lane's rows are two bytes a load, a
+// warp takes NB blocks at a time, so that waiting, the maximum over lanes and the
+// test for a new maximum are paid once per NB blocks, and a warp of its own does
+// all that copying needs.
 //
 // Shape.  A pair is one (sequence, kv head) with up to 8 NT of its query columns
 // (head of the group, and query token where there are several).  Its blocks are
-// taken in rounds: a round is NB blocks for each of a CTA's four warps, which keep
-// their own softmax states and meet at a pair's end.  Each warp feeds itself: lane i
-// issues the two bulk copies of block i of a group into the warp's own ring, the next
-// group into a stage as soon as the warp has the old one in registers.  No producer
-// warp, no barrier between warps within a pair.
+// taken in rounds: a round is NB blocks for each of a CTA's seven attending warps,
+// which keep their own softmax states and meet at a pair's end.  The eighth warp
+// copies a round per ring stage and reads the table a round ahead.
+// (Eight warps in all: the register file is split in four, so a ninth warp would
+// cost every warp a fifth of its registers.)
 //
 // Balance.  The rounds of all pairs are laid end to end and cut into one equal run
 // per CTA of a single wave; every CTA finds its run from the lengths on the device
@@ -50,8 +51,10 @@
 
 namespace pkv {
 
-constexpr int kI4Warps = 4;
-constexpr int kI4Threads = kI4Warps * 32;
+constexpr int kI4Warps = 7;                      // attending warps of a CTA
+constexpr int kI4Attend = kI4Warps * 32;
+constexpr int kI4Threads = kI4Attend + 32;       // and the copying warp
+constexpr int kI4MergeThreads = 128;             // of merge_i4_kernel
 constexpr int kI4BS = 16;
 constexpr int kI4PairCost = 1;       // rounds
 constexpr int kI4MinRun = 2;         // shortest run: a pair's cost and a round
@@ -67,7 +70,7 @@ struct I4Params {
     int q_bf16;
     const int32_t *cu_q;    // null: one query token per sequence, row b
     int total_q, max_t;     // rows of q and out; most query tokens of a sequence
-    const char *k_pool, *v_pool;
+    const char *pool;
     const int32_t *tables;
     int max_blocks, num_blocks;
     const int32_t *seq_lens, *seq_order;
@@ -94,16 +97,15 @@ KV_DEVICE float ex2(float x) {
     return y;
 }
 
-// Whether a phase is complete, without the suspension of mbarrier.try_wait.
-KV_DEVICE bool phase_done(uint64_t *bar, uint32_t parity) {
+// One lane of a converged warp, in the form that lets the compiler issue copies from
+// uniform registers (under an ordinary lane test it loops over the lanes).
+KV_DEVICE bool elect_one() {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
+        : "=r"(ok));
     return ok != 0;
 }
 
@@ -140,20 +142,19 @@ KV_DEVICE void load_words(const char *src, uint32_t (&w)[N]) {
     }
 }
 
-// Shared memory: the warps' rings (NST stages of NB blocks), the merge's outputs
-// ([warp][8 columns][D], reused for the split merge's weights), barriers.
+// Shared memory: the ring (a stage: a round's blocks), the merge's outputs ([warp][4 columns][D], reused for the split merge's
+// weights), barriers and the stages' masks of missing blocks.
 template <int D, int NB, int NST>
 constexpr size_t i4_ring_bytes() {
-    return (size_t)kI4Warps * NST * NB * 2 * 9 * D;
+    return (size_t)NST * kI4Warps * NB * 2 * 9 * D;
 }
 template <int D>
 constexpr size_t i4_merge_bytes() {
-    return (size_t)kI4Warps * 8 * D * 4;
+    return (size_t)kI4Warps * 4 * D * 4;
 }
 template <int D, int NB, int NST>
 constexpr size_t i4_smem_bytes() {
-    return i4_ring_bytes<D, NB, NST>() + i4_merge_bytes<D>() +
-           (size_t)kI4Warps * NST * (sizeof(uint64_t) + NB * sizeof(int));
+    return i4_ring_bytes<D, NB, NST>() + i4_merge_bytes<D>() + (size_t)NST * (2 * sizeof(uint64_t) + sizeof(int));
 }
 
 // A sequence: its query rows, keys, rounds, and the pairs it makes (0: left out).
@@ -199,33 +200,36 @@ KV_DEVICE I4Work i4_sequence(const I4Params &p, int b, int round_blocks, int col
 }
 
 // D: head dim.  NT: columns / 8 of a CTA.  EXACT: weights in two fp16 parts (fp32
-// output).  TW: waits read their limit at run time (tests).  NB: blocks of a group;
-// NST: ring stages; MINB: CTAs per SM it is built for.
+// output).  TW: waits read their limit at run time (tests).  NB: blocks of a warp's
+// share of a round; NST: ring stages; MINB: CTAs per SM it is built for.
 template <int D, int NT, bool EXACT, bool TW, int NB, int NST, int MINB>
 __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Params p) {
     constexpr int kTile = 9 * D;
     constexpr int kW = D / 32;        // words of a quarter row of K, of a lane's dims of a V pair
     constexpr int kSteps = D / 16;    // products along D
-    constexpr int kStage = NB * 2 * kTile;  // K tiles, then V tiles
     constexpr int kRound = NB * kI4Warps;   // blocks of a round
+    constexpr int kStage = kRound * 2 * kTile;
     constexpr int kCols = 8 * NT;
+    static_assert(kRound <= 32, "a lane looks after one block of a round");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int r = lane >> 2, c = lane & 3;
 
     extern __shared__ __align__(128) char smem[];
     constexpr size_t kRing = i4_ring_bytes<D, NB, NST>(), kMerge = i4_merge_bytes<D>();
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRing + kMerge) + warp * NST;
-    volatile int *valid =
-        reinterpret_cast<int *>(smem + kRing + kMerge + kI4Warps * NST * sizeof(uint64_t)) + warp * NST * NB;
-    char *ring = smem + (size_t)warp * NST * kStage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRing + kMerge), *empty = full + NST;
+    volatile int *missing = reinterpret_cast<int *>(empty + NST);  // bit i: block i of the round is not there
     __shared__ uint2 s_q[kSteps * NT * 32];
     __shared__ float s_scale[8 * NT];
     __shared__ float s_m[kI4Warps * 8], s_l[kI4Warps * 8];
-    __shared__ int s_scan[kI4Warps], s_most[kI4Warps], s_start[3], s_last;
+    __shared__ int s_scan[kI4Warps + 1], s_most[kI4Warps + 1], s_start[3], s_last;
+    __shared__ volatile int s_abort;  // a wait ran out
 
-    if (lane == 0) {
-        for (int st = 0; st < NST; ++st) mbar_init(&full[st], NB);
+    if (tid == 0) {
+        for (int st = 0; st < NST; ++st) {
+            mbar_init(&full[st], 1);
+            mbar_init(&empty[st], kI4Warps);
+        }
         mbar_init_fence();
+        s_abort = 0;
     }
 
     // ---- this CTA's run: `todo` units (rounds and pair costs) from unit `unit` of
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         __syncthreads();
         int total = 0;
 #pragma unroll
-        for (int y = 0; y < kI4Warps; ++y) {
+        for (int y = 0; y <= kI4Warps; ++y) {
             if (y < warp) scan += s_scan[y];
             total += s_scan[y];
             most = max(most, s_most[y]);
@@ -298,81 +302,101 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         unit = pair * (w.rounds + kI4PairCost) + kI4PairCost + r0;
         todo = min(p.part_rounds, w.rounds - r0);
     }
-    __syncwarp();
+    __syncthreads();
 
-    // ---- the copies' place in the run
-    I4Work iw = i4_sequence(p, b0, kRound, kCols, false);
-    int i_unit = unit, i_left = todo;  // in units of sequence iw.b
-    int i_pair = 0, i_round = 0;       // the round the next issue takes
-    int id_next = -1;
-    const uint64_t policy = l2_evict_first_policy();
-    // moves to the next unit that is a round; false at the run's end
-    auto place = [&]() -> bool {
-        while (i_left > 0) {
-            const int per = iw.rounds + kI4PairCost;
-            if (i_unit >= iw.pairs * per) {
-                iw = i4_sequence(p, iw.b + 1, kRound, kCols, false);
-                i_unit = 0;
-                continue;
+    if (warp == kI4Warps) {
+        // ================================================== the copying warp
+        // Lane i looks after block i of a round; one lane issues every copy.
+        I4Work w = i4_sequence(p, b0, kRound, kCols, false);
+        const uint64_t policy = l2_evict_first_policy();
+        int pair = 0, round = 0;
+        // Moves to the next unit that is a round; false at the run's end.
+        auto place = [&]() -> bool {
+            while (todo > 0) {
+                const int per = w.rounds + kI4PairCost;
+                if (unit >= w.pairs * per) {
+                    w = i4_sequence(p, w.b + 1, kRound, kCols, false);
+                    unit = 0;
+                    continue;
+                }
+                pair = unit / per;
+                round = unit - pair * per - kI4PairCost;
+                if (round >= 0) return true;
+                ++unit;
+                --todo;
             }
-            i_pair = i_unit / per;
-            i_round = i_unit - i_pair * per - kI4PairCost;
-            if (i_round >= 0) return true;
-            ++i_unit;
-            --i_left;
-        }
-        return false;
-    };
-    bool more = place();
-    auto fetch = [&]() {  // the table entry of the block this lane copies next
-        if (lane < NB) {
-            const int blk = i_round * kRound + NB * warp + lane;
-            id_next = blk < iw.nblk ? __ldg(p.tables + (size_t)iw.b * p.max_blocks + blk) : -2;
-        }
-    };
-    if (more) fetch();
-    int issued = 0;
-    auto issue = [&](int st) {  // this warp's group of round i_round into stage st
-        ++issued;
-        if (lane < NB) {
-            const bool ok = id_next >= 0 && id_next < p.num_blocks;
-            valid[st * NB + lane] = ok;
-            if (ok) {
-                const size_t off = ((size_t)id_next * p.hkv + i_pair % p.hkv) * kTile;
-                char *dst = ring + st * kStage + lane * kTile;
-                mbar_arrive_expect_tx(&full[st], 2 * kTile);
-                bulk_g2s(dst, p.k_pool + off, kTile, &full[st], policy);
-                bulk_g2s(dst + NB * kTile, p.v_pool + off, kTile, &full[st], policy);
-            } else {
-                if (id_next != -2) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
-                mbar_arrive(&full[st]);
+            return false;
+        };
+        int id_next = -1;      // table entry of this lane's next block
+        bool in_next = false;  // that block is one of the sequence's
+        auto entry = [&]() {
+            const int blk = round * kRound + lane;
+            in_next = lane < kRound && blk < w.nblk;
+            if (in_next) id_next = __ldg(p.tables + (size_t)w.b * p.max_blocks + blk);
+        };
+        bool more = place();
+        if (more) entry();
+        int issued = 0;
+        while (more) {
+            const int id = id_next, h = pair % p.hkv, st = issued % NST;
+            const bool inside = in_next;
+            // the next round's entries are on their way while this round is copied
+            ++unit;
+            --todo;
+            ++round;
+            more = round < w.rounds ? todo > 0 : place();
+            if (more) entry();
+            bool bad = false;
+            if (lane == 0) {
+                // the ring is full most of the time: look now and then, not in every free slot
+                for (int i = 0; i < 256 && issued >= NST && !mbar_try_wait(&empty[st], (issued / NST - 1) & 1); ++i)
+                    __nanosleep(50);
+                bad = s_abort || (issued >= NST && !mbar_wait<TW>(&empty[st], (issued / NST - 1) & 1, p.err));
             }
-        }
-        ++i_unit;
-        --i_left;
-        if (++i_round < iw.rounds)
-            more = i_left > 0;  // the same pair
-        else
-            more = place();
-        if (more) fetch();
-    };
+            if (__shfl_sync(0xffffffffu, bad, 0)) {
+                if (lane == 0) s_abort = 1;
+                break;
+            }
+            const bool ok = inside && id >= 0 && id < p.num_blocks;
+            const uint32_t there = __ballot_sync(0xffffffffu, ok);
+            const uint32_t gone = __ballot_sync(0xffffffffu, inside && !ok);
+            if (gone && lane == 0) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
+            const long long off = ((long long)id * p.hkv + h) * (2 * kTile);
+            const bool leader = elect_one();
+            if (leader) {
+                missing[st] = (int)gone;
+                if (there)
+                    mbar_arrive_expect_tx(&full[st], 2 * __popc(there) * kTile);
+                else
+                    mbar_arrive(&full[st]);
+            }
+            char *dst = smem + st * kStage;
 #pragma unroll
-    for (int j = 0; j < NST; ++j)
-        if (more) issue(j);
-
-    bool stop = false;
-    // Test instantiation with a limit of 0: a tile that is not there at once is a
-    // wait that ran out (try_wait would sleep until it came).
-    if constexpr (TW) {
-        if (g_wait_limit_ns == 0 && issued > 0) {
-            stop = __any_sync(0xffffffffu, !phase_done(&full[0], 0));
-            if (stop && lane == 0) atomicOr(p.err, KV_DEVERR_TIMEOUT);
+            for (int i = 0; i < kRound; ++i) {
+                const long long at = __shfl_sync(0xffffffffu, off, i);
+                if ((there >> i & 1) && leader) {
+                    bulk_g2s(dst + 2 * i * kTile, p.pool + at, 2 * kTile, &full[st], policy);
+                }
+            }
+            ++issued;
         }
+        // Never leave while a copy into this CTA's shared memory may be in flight.
+        if (lane == 0)
+            for (int k = max(0, issued - NST); k < issued; ++k) mbar_wait_drain(&full[k % NST], (k / NST) & 1, p.err);
+        return;
     }
 
-    // ---- the run's pieces
+    // ====================================================== attending warps
+    const int r = lane >> 2, c = lane & 3;
+    // columns without a query hold zeros (later pieces may leave old ones: a column's
+    // values reach no other column)
+    for (int i = tid; i < kSteps * NT * 32; i += kI4Attend) s_q[i] = make_uint2(0u, 0u);
+    for (int i = tid; i < 8 * NT; i += kI4Attend) s_scale[i] = 1.f;
+    named_bar_sync(1, kI4Attend);
+
     int st = 0;
     uint32_t parity = 0;
+    bool stop = false;
     I4Work w = i4_sequence(p, b0, kRound, kCols, false);
     while (todo > 0) {
         const int per = w.rounds + kI4PairCost;
@@ -404,18 +428,22 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         // ---- q of each column: largest magnitude to [2^13, 2^14) by a power of two,
         // so that fp16 holds it, then into the order of the fragments
         __half *qs = reinterpret_cast<__half *>(s_q);
-        for (int col = warp; col < 8 * NT; col += kI4Warps) {
+        for (int col = warp; col < ncols; col += kI4Warps) {
             constexpr int kPer = D / 32;
+            const int tq = w.T == 1 ? 0 : (col0 + col) / p.g, hq = h * p.g + (col0 + col) - tq * p.g;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + out_row(p, w, tq, hq) * D + lane * kPer);
             float x[kPer];
-            if (col < ncols) {
-                const int tq = (col0 + col) / p.g, j = (col0 + col) - tq * p.g;
-                const uint16_t *src = p.q + ((size_t)(w.q0 + tq) * p.hq + h * p.g + j) * D + lane * kPer;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    x[i] = p.q_bf16 ? bf16_to_float(src[i]) : f16x2_to_float2(src[i]).x;
+            uint32_t two[kPer / 2];
+            if constexpr (kPer == 4) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
+                two[0] = u.x, two[1] = u.y;
             } else {
+                two[0] = __ldg(src);
+            }
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) x[i] = 0.f;
+            for (int i = 0; i < kPer / 2; ++i) {
+                const float2 f = p.q_bf16 ? bf16x2_to_float2(two[i]) : f16x2_to_float2(two[i]);
+                x[2 * i] = f.x, x[2 * i + 1] = f.y;
             }
             float m = 0.f;
 #pragma unroll
@@ -439,7 +467,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             if (lane == 0)
                 s_scale[col] = p.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 - up) << 23), 1e-37f);
         }
-        __syncthreads();
+        named_bar_sync(1, kI4Attend);
 
         // ---- state of columns 8 nt + 2 c and + 1 (maxima replicated over r)
         float m_run[NT][2], l_run[NT][2], o[NT][kSteps][4], sc[NT][2];
@@ -452,17 +480,20 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 m_run[nt][x] = -INFINITY;
                 l_run[nt][x] = 0.f;
                 sc[nt][x] = s_scale[col];
-                lim[nt][x] = w.L - w.T + min((col0 + col) / p.g, w.T - 1) + 1;
+                lim[nt][x] = w.L - w.T + (w.T == 1 ? 1 : min((col0 + col) / p.g, w.T - 1) + 1);
 #pragma unroll
                 for (int f = 0; f < kSteps; ++f) o[nt][f][x] = o[nt][f][2 + x] = 0.f;
             }
-        const int least = w.L - w.T + col0 / p.g + 1;  // keys that every column sees
+        const int least = w.L - w.T + (w.T == 1 ? 0 : col0 / p.g) + 1;  // keys that every column sees
 
         for (int j = 0; j < nrounds && !stop; ++j) {
             const bool bad = !mbar_wait<TW>(&full[st], parity, p.err);
             stop = __any_sync(0xffffffffu, bad);
-            if (stop) break;
-            const char *stage = ring + st * kStage;
+            if (stop) {
+                if (lane == 0) s_abort = 1;
+                break;
+            }
+            const char *stage = smem + st * kStage + NB * warp * 2 * kTile;
             const int tok0 = ((round0 + j) * kRound + NB * warp) * kI4BS;
             // ---- S^T = K q^T: tokens r, r + 8 of each block
             float s[NB][NT][4];
@@ -475,7 +506,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 __half2 a0[NB], a1[NB];
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    const char *kt = stage + n * kTile;
+                    const char *kt = stage + 2 * n * kTile;
                     load_words<kW>(kt + r * (D / 2) + c * (D / 8), k0[n]);
                     load_words<kW>(kt + (r + 8) * (D / 2) + c * (D / 8), k1[n]);
                     uint32_t s0, s1;
@@ -520,7 +551,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             uint32_t v0[NB][kW], v1[NB][kW], vs0[NB], vs1[NB];
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const char *vt = stage + (NB + n) * kTile;
+                const char *vt = stage + (2 * n + 1) * kTile;
                 load_words<kW>(vt + c * D + 4 * ((r * kW) ^ i4::v_swizzle<D>(c)), v0[n]);
                 load_words<kW>(vt + (c + 4) * D + 4 * ((r * kW) ^ i4::v_swizzle<D>(c + 4)), v1[n]);
                 const int gr = D == 128 ? 2 * r : (r & ~1);
@@ -528,21 +559,16 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 vs1[n] = *reinterpret_cast<const uint16_t *>(vt + 8 * D + (c + 4) * (D / 8) + gr);
             }
             // tokens past the sequence, or in a block that is not there
-            bool whole = tok0 + NB * kI4BS <= w.L;
-            int ntok[NB];
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const int there = valid[st * NB + n];
-                whole = whole && there;
-                ntok[n] = there ? min(kI4BS, w.L - (tok0 + n * kI4BS)) : 0;
-            }
-            // the stage is in registers: its next group may come
+            const int gone = missing[st] >> (NB * warp) & ((1 << NB) - 1);
+            const bool whole = !gone && tok0 + NB * kI4BS <= w.L;
+            // the stage is in registers: its next round may come
             __syncwarp();
-            if (more) issue(st);
+            if (lane == 0) mbar_arrive(&empty[st]);
             if (++st == NST) {
                 st = 0;
                 parity ^= 1;
             }
+            auto tokens = [&](int n) { return gone >> n & 1 ? 0 : min(kI4BS, w.L - (tok0 + n * kI4BS)); };
 
             // ---- softmax: s[0], s[1] token r, columns 2 c, 2 c + 1; s[2], s[3] token r + 8
             uint32_t ph[NB][NT][2], pl[NB][NT][2];
@@ -555,7 +581,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             const int t = r + 4 * (x & 2);
-                            if (t >= ntok[n] || tok0 + n * kI4BS + t >= lim[nt][x & 1]) s[n][nt][x] = -INFINITY;
+                            if (t >= tokens(n) || tok0 + n * kI4BS + t >= lim[nt][x & 1]) s[n][nt][x] = -INFINITY;
                         }
             }
             bool renew = false;
@@ -616,8 +642,9 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 __half2 a = i4::scale_pair(vs0[n]), e = i4::scale_pair(vs1[n]);
                 if (!whole) {
                     uint32_t ab = *reinterpret_cast<uint32_t *>(&a), eb = *reinterpret_cast<uint32_t *>(&e);
-                    ab &= (2 * c < ntok[n] ? 0xffffu : 0u) | (2 * c + 1 < ntok[n] ? 0xffff0000u : 0u);
-                    eb &= (2 * c + 8 < ntok[n] ? 0xffffu : 0u) | (2 * c + 9 < ntok[n] ? 0xffff0000u : 0u);
+                    const int ntok = tokens(n);
+                    ab &= (2 * c < ntok ? 0xffffu : 0u) | (2 * c + 1 < ntok ? 0xffff0000u : 0u);
+                    eb &= (2 * c + 8 < ntok ? 0xffffu : 0u) | (2 * c + 9 < ntok ? 0xffff0000u : 0u);
                     a = *reinterpret_cast<__half2 *>(&ab);
                     e = *reinterpret_cast<__half2 *>(&eb);
                 }
@@ -641,11 +668,11 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             }
         }
 
-        // ---- the four warps' states to this piece's result, eight columns at a time
+        // ---- the warps' states to this piece's result, four columns at a time
         float4 *sm_o = reinterpret_cast<float4 *>(smem + kRing);  // [warp][column][D / 4], see `at`
-        constexpr int kQ = D / 32;                         // float4s of one lane's dims
-        auto at = [&](int wp, int col, int rr, int i) {    // spread over the banks
-            return (wp * 8 + col) * (D / 4) + rr * kQ + (i ^ ((col >> 1) & (kQ - 1)));
+        constexpr int kQ = D / 32;                                 // float4s of one lane's dims
+        auto at = [&](int wp, int col, int rr, int i) {            // spread over the banks
+            return (wp * 4 + col) * (D / 4) + rr * kQ + (i ^ ((col >> 1) & (kQ - 1)) ^ (rr & (kQ - 1)));
         };
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -655,54 +682,60 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 l0 += __shfl_xor_sync(0xffffffffu, l0, x);
                 l1 += __shfl_xor_sync(0xffffffffu, l1, x);
             }
-            if (nt > 0) __syncthreads();  // the previous columns have been read
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int half = 0; half < 2; ++half) {
+                const int live = min(4, ncols - 8 * nt - 4 * half);
+                if (live <= 0) break;
+                if (nt > 0 || half > 0) named_bar_sync(1, kI4Attend);  // the previous columns have been read
+                if ((c >> 1) == half) {
+                    const int c4 = 2 * (c & 1);
 #pragma unroll
-                for (int i = 0; i < kQ; ++i)
-                    sm_o[at(warp, 2 * c + x, r, i)] =
-                        make_float4(o[nt][2 * i][x], o[nt][2 * i][2 + x], o[nt][2 * i + 1][x], o[nt][2 * i + 1][2 + x]);
-            if (r == 0) {
-                // the weights are relative to m - kI4Bias
-                s_m[warp * 8 + 2 * c] = m_run[nt][0] - kI4Bias;
-                s_m[warp * 8 + 2 * c + 1] = m_run[nt][1] - kI4Bias;
-                s_l[warp * 8 + 2 * c] = l0;
-                s_l[warp * 8 + 2 * c + 1] = l1;
-            }
-            __syncthreads();
-            const int live = min(8, ncols - 8 * nt);
-            for (int idx = tid; idx < live * (D / 4); idx += kI4Threads) {
-                const int col = idx / (D / 4), d4 = idx % (D / 4);
-                float M = s_m[col];
+                    for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int wp = 1; wp < kI4Warps; ++wp) M = fmaxf(M, s_m[wp * 8 + col]);
-                float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-                float den = 0.f;
-#pragma unroll
-                for (int wp = 0; wp < kI4Warps; ++wp) {
-                    const float lw = s_l[wp * 8 + col];
-                    if (lw == 0.f) continue;  // saw no key
-                    const float f = ex2(s_m[wp * 8 + col] - M);
-                    const float4 v = sm_o[at(wp, col, d4 / kQ, d4 % kQ)];
-                    num.x += f * v.x;
-                    num.y += f * v.y;
-                    num.z += f * v.z;
-                    num.w += f * v.w;
-                    den += f * lw;
+                        for (int i = 0; i < kQ; ++i)
+                            sm_o[at(warp, c4 + x, r, i)] = make_float4(o[nt][2 * i][x], o[nt][2 * i][2 + x],
+                                                                       o[nt][2 * i + 1][x], o[nt][2 * i + 1][2 + x]);
+                    if (r == 0) {
+                        // the weights are relative to m - kI4Bias
+                        s_m[warp * 4 + c4] = m_run[nt][0] - kI4Bias;
+                        s_m[warp * 4 + c4 + 1] = m_run[nt][1] - kI4Bias;
+                        s_l[warp * 4 + c4] = l0;
+                        s_l[warp * 4 + c4 + 1] = l1;
+                    }
                 }
-                const float inv = den != 0.f ? p.v_mul / den : 0.f;  // den NaN: NaN
-                const int gc = col0 + 8 * nt + col, tq = gc / p.g;
-                const int hq = h * p.g + (gc - tq * p.g);
-                const size_t orow = out_row(p, w, tq, hq);
-                const float4 v = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-                const float lse2 = den != 0.f ? M + log2f(den) : -INFINITY;
-                if (nsplit == 1) {
-                    store_out4(p.out, orow * D + 4 * d4, v, p.out_type);
-                    if (p.lse && d4 == 0) p.lse[orow] = lse2 * 0.6931471805599453f;
-                } else {
-                    const size_t slot = ws_row(p, w, tq, hq) * p.max_splits + split;
-                    reinterpret_cast<float4 *>(p.ws_o)[slot * (D / 4) + d4] = v;
-                    if (d4 == 0) p.ws_lse[slot] = lse2;
+                named_bar_sync(1, kI4Attend);
+                if (tid < live * (D / 4)) {
+                    const int col = tid / (D / 4), d4 = tid % (D / 4);
+                    float M = s_m[col];
+#pragma unroll
+                    for (int wp = 1; wp < kI4Warps; ++wp) M = fmaxf(M, s_m[wp * 4 + col]);
+                    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float den = 0.f;
+#pragma unroll
+                    for (int wp = 0; wp < kI4Warps; ++wp) {
+                        const float lw = s_l[wp * 4 + col];
+                        const float f = lw == 0.f ? 0.f : ex2(s_m[wp * 4 + col] - M);  // 0: saw no key
+                        const float4 v = sm_o[at(wp, col, d4 / kQ, d4 % kQ)];
+                        num.x += f * v.x;
+                        num.y += f * v.y;
+                        num.z += f * v.z;
+                        num.w += f * v.w;
+                        den += f * lw;
+                    }
+                    const float inv = den != 0.f ? p.v_mul / den : 0.f;  // den NaN: NaN
+                    const int gc = col0 + 8 * nt + 4 * half + col, tq = w.T == 1 ? 0 : gc / p.g;
+                    const int hq = h * p.g + (gc - tq * p.g);
+                    const size_t orow = out_row(p, w, tq, hq);
+                    const float4 v = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+                    const float lse2 = den != 0.f ? M + log2f(den) : -INFINITY;
+                    if (nsplit == 1) {
+                        store_out4(p.out, orow * D + 4 * d4, v, p.out_type);
+                        if (p.lse && d4 == 0) p.lse[orow] = lse2 * 0.6931471805599453f;
+                    } else {
+                        const size_t slot = ws_row(p, w, tq, hq) * p.max_splits + split;
+                        reinterpret_cast<float4 *>(p.ws_o)[slot * (D / 4) + d4] = v;
+                        if (d4 == 0) p.ws_lse[slot] = lse2;
+                    }
                 }
             }
         }
@@ -714,14 +747,14 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         }
         // ---- the last piece to finish merges them all
         __threadfence();
-        __syncthreads();
+        named_bar_sync(1, kI4Attend);
         if (tid == 0) s_last = atomicAdd(counter, 1) == nsplit - 1;
-        __syncthreads();
+        named_bar_sync(1, kI4Attend);
         if (!s_last) continue;
         __threadfence();
         float *wt = reinterpret_cast<float *>(smem + kRing);  // [8 NT][kFuseMaxSplits]
         for (int col = warp; col < ncols; col += kI4Warps) {
-            const int gc = col0 + col, tq = gc / p.g;
+            const int gc = col0 + col, tq = w.T == 1 ? 0 : gc / p.g;
             const int hq = h * p.g + (gc - tq * p.g);
             const size_t orow = out_row(p, w, tq, hq), wrow = ws_row(p, w, tq, hq);
             const float x = lane < nsplit ? __ldcg(p.ws_lse + wrow * p.max_splits + lane) : -INFINITY;
@@ -735,10 +768,10 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             wt[col * kFuseMaxSplits + lane] = den != 0.f ? e / den : 0.f;
             if (p.lse && lane == 0) p.lse[orow] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
         }
-        __syncthreads();
-        for (int idx = tid; idx < ncols * (D / 4); idx += kI4Threads) {
+        named_bar_sync(1, kI4Attend);
+        for (int idx = tid; idx < ncols * (D / 4); idx += kI4Attend) {
             const int col = idx / (D / 4), d4 = idx % (D / 4);
-            const int gc = col0 + col, tq = gc / p.g;
+            const int gc = col0 + col, tq = w.T == 1 ? 0 : gc / p.g;
             const int hq = h * p.g + (gc - tq * p.g);
             const size_t orow = out_row(p, w, tq, hq);
             const float4 *src = reinterpret_cast<const float4 *>(p.ws_o) + ws_row(p, w, tq, hq) * p.max_splits * (D / 4) + d4;
@@ -756,15 +789,13 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         }
         if (tid == 0) *counter = 0;  // ready for the next call
     }
-    // After a timed-out wait: no copy may still be on its way into this CTA's memory.
-    for (int j = max(0, issued - NST); j < issued; ++j) mbar_wait_drain(&full[j % NST], (j / NST) & 1, p.err);
 }
 
 // Merge of rows cut into more partitions than one CTA merges: one CTA per query
 // row, its threads in groups of D / 4 that take every group-th partition.
 template <int D>
-__global__ void __launch_bounds__(kI4Threads) merge_i4_kernel(const I4Params p) {
-    constexpr int kLanes = D / 4, kGroups = kI4Threads / kLanes;
+__global__ void __launch_bounds__(kI4MergeThreads) merge_i4_kernel(const I4Params p) {
+    constexpr int kLanes = D / 4, kGroups = kI4MergeThreads / kLanes;
     const int tq = blockIdx.x / p.hq, hq = blockIdx.x % p.hq;
     const I4Work w = i4_sequence(p, blockIdx.y, p.round_blocks, p.cols, false);
     if (!w.pairs || tq >= w.T) return;
@@ -792,17 +823,17 @@ __global__ void __launch_bounds__(kI4Threads) merge_i4_kernel(const I4Params p) 
     const int tid = threadIdx.x, d4 = tid % kLanes, grp = tid / kLanes;
     const size_t orow = out_row(p, w, tq, hq), wrow = ws_row(p, w, tq, hq);
     const float *ls = p.ws_lse + wrow * p.max_splits;
-    __shared__ float s_red[kI4Warps * 2];
-    __shared__ float4 s_acc[kI4Threads];
+    __shared__ float s_red[kI4MergeThreads / 32];
+    __shared__ float4 s_acc[kI4MergeThreads];
     __shared__ float s_den[kGroups];
     float M = -INFINITY;
-    for (int s = tid; s < nsplit; s += kI4Threads) M = fmaxf(M, ls[s]);
+    for (int s = tid; s < nsplit; s += kI4MergeThreads) M = fmaxf(M, ls[s]);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
     if ((tid & 31) == 0) s_red[tid >> 5] = M;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kI4Warps; ++i) M = fmaxf(M, s_red[i]);
+    for (int i = 0; i < kI4MergeThreads / 32; ++i) M = fmaxf(M, s_red[i]);
     const float4 *src = reinterpret_cast<const float4 *>(p.ws_o) + wrow * p.max_splits * kLanes + d4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f;
@@ -870,7 +901,7 @@ kv_status attend_i4(const I4Call &a) {
     if (need > 0 && (!a.workspace || a.workspace_bytes < need)) return KV_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(a.workspace) & 15) return KV_ERR_ARG;
     const int cols = a.max_q_len * g;  // of one (sequence, kv head)
-    const int nt = std::min(4, (cols + 7) / 8);
+    const int nt = cols <= 24 ? (cols + 7) / 8 : 2;  // more: groups of 16 (a fourth tile of eight does not fit)
     const int groups = (cols + 8 * nt - 1) / (8 * nt);
     if (ms > 65535 || (long long)a.batch * groups > 65535 || pool->num_kv_heads > 65535) return KV_ERR_UNSUPPORTED;
     I4Params p{};
@@ -879,8 +910,7 @@ kv_status attend_i4(const I4Call &a) {
     p.cu_q = a.cu_q;
     p.total_q = a.total_q;
     p.max_t = a.max_q_len;
-    p.k_pool = static_cast<const char *>(pool->k);
-    p.v_pool = static_cast<const char *>(pool->v);
+    p.pool = static_cast<const char *>(pool->k);
     p.tables = a.block_tables;
     p.max_blocks = a.max_blocks;
     p.num_blocks = pool->num_blocks;
@@ -904,18 +934,17 @@ kv_status attend_i4(const I4Call &a) {
     p.err = pool->err;
     kv_status st;
     if (pool->head_dim == 64)
-        st = nt == 1 ? launch_i4<64, 1, 2, 3, 5>(p, pb, a.stream) : KV_ERR_UNSUPPORTED;
+        st = nt == 1 ? launch_i4<64, 1, 2, 4, 2>(p, pb, a.stream) : KV_ERR_UNSUPPORTED;
     else
-        st = nt == 1   ? launch_i4<128, 1, 2, 2, 4>(p, pb, a.stream)
-             : nt == 2 ? launch_i4<128, 2, 1, 4, 3>(p, pb, a.stream)
-             : nt == 3 ? launch_i4<128, 3, 1, 4, 2>(p, pb, a.stream)
-                       : launch_i4<128, 4, 1, 4, 2>(p, pb, a.stream);
+        st = nt == 1   ? launch_i4<128, 1, 2, 3, 2>(p, pb, a.stream)
+             : nt == 2 ? launch_i4<128, 2, 1, 6, 1>(p, pb, a.stream)
+                       : launch_i4<128, 3, 1, 6, 1>(p, pb, a.stream);
     if (st != KV_OK || ms < (counted ? kFuseMaxSplits + 1 : 2)) return st;
     const dim3 mgrid(a.num_q_heads * a.max_q_len, a.batch);
     if (pool->head_dim == 64)
-        merge_i4_kernel<64><<<mgrid, kI4Threads, 0, a.stream>>>(p);
+        merge_i4_kernel<64><<<mgrid, kI4MergeThreads, 0, a.stream>>>(p);
     else
-        merge_i4_kernel<128><<<mgrid, kI4Threads, 0, a.stream>>>(p);
+        merge_i4_kernel<128><<<mgrid, kI4MergeThreads, 0, a.stream>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
@@ -932,8 +961,8 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
     *num_splits = 1;
     if (batch == 0 || max_blocks == 0) return KV_OK;
     // The pieces that the longest pair is cut into by equal runs of one wave (the
-    // kernel's own arithmetic: rounds of 8 blocks, four CTAs per SM).
-    constexpr int kRound = 8;
+    // kernel's own arithmetic: rounds of 14 blocks, two CTAs per SM).
+    constexpr int kRound = 2 * kI4Warps;
     long long units = 0, most = 1;
     for (int b = 0; b < batch; ++b) {
         const long long L = std::min<long long>(std::max(host_seq_lens[b], 0), (long long)max_blocks * kI4BS);
@@ -941,7 +970,7 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
         units += num_kv_heads * (n + kI4PairCost);
         most = std::max(most, n);
     }
-    const long long wave = 4LL * sm_count(), run = std::max<long long>(kI4MinRun, (units + wave - 1) / wave);
+    const long long wave = 2LL * sm_count(), run = std::max<long long>(kI4MinRun, (units + wave - 1) / wave);
     if (most < 2) return KV_OK;
     const long long pieces = (most - 2) / run + 2;
     // split_plan's partitions are whole multiples of four blocks: the split count that
@@ -950,7 +979,7 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
         int pb, ms;
         split_plan(batch, num_kv_heads, max_blocks, s, &pb, &ms);
         *num_splits = s;
-        if (ms >= pieces || pb <= kI4Warps || s >= max_blocks) break;
+        if (ms >= pieces || pb <= 4 || s >= max_blocks) break;
     }
     return KV_OK;
 }

@@ -10,8 +10,9 @@
 // fp16 and bf16.
 //
 // A (block, kv head) tile of K or of V is 16 x D / 2 bytes of codes followed by
-// 16 x D / 16 scale bytes (9 D bytes; 1152 for D = 128).  A code is stored as
-// u = c + 8 in four bits.
+// 16 x D / 16 scale bytes (9 D bytes; 1152 for D = 128).  A K tile is followed by its V
+// tile, so that one copy of 18 D bytes brings both.  A code is stored as u = c + 8 in
+// four bits.
 //   K  token t's row is D / 2 bytes in order of dimensions, dimension d in the
 //      four bits d % 8 of the row's 32-bit word d / 8; its scale of group j is
 //      byte t * D / 16 + j of the scales.  A lane of the score product loads a

@@ -14,8 +14,8 @@ struct kv_pool {
     int head_dim = 0;
     kv_dtype dtype = KV_BF16;
     int device = 0;
-    void *k = nullptr;  // [num_blocks][num_kv_heads][block_size][head_dim]; KV_I4: tiles (i4.cuh)
-    void *v = nullptr;
+    void *k = nullptr;  // [num_blocks][num_kv_heads][block_size][head_dim]
+    void *v = nullptr;  // KV_I4: tiles (i4.cuh), each K tile followed by its V tile; v = k + a tile
     float k_scale = 1.f, v_scale = 1.f;  // KV_I4: powers of two (kv_pool_set_i4_scales)
     int *err = nullptr;  // device error word
     // arrival counters of the fused split merge, one per (sequence, kv head),
@@ -44,9 +44,19 @@ inline size_t tile_bytes(kv_dtype t, int head_dim) {
     return t == KV_I4 ? (size_t)9 * head_dim : (size_t)16 * head_dim * dtype_bytes(t);
 }
 
-// 16-byte chunks of one block (all kv heads) of the K or V pool.
-inline int block_chunks_of(const kv_pool *p) {
-    return (int)(p->num_kv_heads * tile_bytes(p->dtype, p->head_dim) / 16);
+// A block as two parts of `chunks` 16-byte chunks each, `stride` chunks from one
+// block to the next: its K and its V (all kv heads), or, where they alternate
+// (KV_I4), its two halves.
+struct BlockParts {
+    char *a, *b;
+    int chunks;
+    long long stride;
+};
+inline BlockParts block_parts(const kv_pool *p) {
+    const size_t bytes = p->num_kv_heads * tile_bytes(p->dtype, p->head_dim);
+    char *k = static_cast<char *>(p->k);
+    if (p->dtype == KV_I4) return {k, k + bytes, (int)(bytes / 16), (long long)(2 * bytes / 16)};
+    return {k, static_cast<char *>(p->v), (int)(bytes / 16), (long long)(bytes / 16)};
 }
 
 inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s); }

@@ -101,13 +101,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(uint4 *__restric
 }
 
 // Copies whole blocks (all heads and slots) of K and V: pair p moves block
-// src[p] to block dst[p].  block_chunks = 16-byte chunks per block per pool.
+// src[p] to block dst[p].  block_chunks = 16-byte chunks per block per pool,
+// stride = chunks between blocks.
 __global__ void __launch_bounds__(256) copy_blocks_kernel(uint4 *__restrict__ k_pool,
                                                           uint4 *__restrict__ v_pool,
                                                           const int32_t *__restrict__ src,
                                                           const int32_t *__restrict__ dst,
-                                                          int n, int block_chunks, int num_blocks,
-                                                          int *err) {
+                                                          int n, int block_chunks, long long stride,
+                                                          int num_blocks, int *err) {
     const long long total = (long long)n * block_chunks;
     for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
          i += (long long)gridDim.x * blockDim.x) {
@@ -118,8 +119,8 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(uint4 *__restrict__ k_
             if (c == 0) atomicOr(err, KV_DEVERR_BLOCK_RANGE);
             continue;
         }
-        k_pool[(long long)d * block_chunks + c] = k_pool[(long long)s * block_chunks + c];
-        v_pool[(long long)d * block_chunks + c] = v_pool[(long long)s * block_chunks + c];
+        k_pool[d * stride + c] = k_pool[s * stride + c];
+        v_pool[d * stride + c] = v_pool[s * stride + c];
     }
 }
 
@@ -127,10 +128,11 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(uint4 *__restrict__ k_
 // host checked both ids.
 __global__ void __launch_bounds__(256) copy_block_kernel(uint4 *__restrict__ k_pool,
                                                          uint4 *__restrict__ v_pool, int src,
-                                                         int dst, int block_chunks) {
+                                                         int dst, int block_chunks,
+                                                         long long stride) {
     for (int c = blockIdx.x * blockDim.x + threadIdx.x; c < block_chunks; c += gridDim.x * blockDim.x) {
-        k_pool[(long long)dst * block_chunks + c] = k_pool[(long long)src * block_chunks + c];
-        v_pool[(long long)dst * block_chunks + c] = v_pool[(long long)src * block_chunks + c];
+        k_pool[dst * stride + c] = k_pool[src * stride + c];
+        v_pool[dst * stride + c] = v_pool[src * stride + c];
     }
 }
 
@@ -142,8 +144,8 @@ __global__ void __launch_bounds__(256) swap_blocks_kernel(uint4 *__restrict__ k_
                                                           uint4 *__restrict__ v_pool,
                                                           uint4 *__restrict__ host,
                                                           const int32_t *__restrict__ ids, int n,
-                                                          int block_chunks, int num_blocks, int dir,
-                                                          int *err) {
+                                                          int block_chunks, long long stride,
+                                                          int num_blocks, int dir, int *err) {
     const long long total = (long long)n * block_chunks;
     for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
          i += (long long)gridDim.x * blockDim.x) {
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(256) swap_blocks_kernel(uint4 *__restrict__ k_
         }
         uint4 *hk = host + (2LL * p) * block_chunks + c;
         uint4 *hv = hk + block_chunks;
-        const long long pc = (long long)id * block_chunks + c;
+        const long long pc = id * stride + c;
         if (dir == 0) {
             *hk = k_pool[pc];
             *hv = v_pool[pc];
@@ -198,7 +200,9 @@ kv_status kv_pool_create(int num_blocks, int block_size, int num_kv_heads, int h
     cudaGetDevice(&p->device);
     const size_t bytes = (size_t)num_blocks * num_kv_heads * tile_bytes(dtype, head_dim);
     kv_status st = KV_OK;
-    if (cudaMalloc(&p->k, bytes) != cudaSuccess || cudaMalloc(&p->v, bytes) != cudaSuccess ||
+    const bool one = dtype == KV_I4;  // K and V tiles alternate in one array
+    if (cudaMalloc(&p->k, one ? 2 * bytes : bytes) != cudaSuccess ||
+        (!one && cudaMalloc(&p->v, bytes) != cudaSuccess) ||
         cudaMalloc(&p->err, sizeof(int)) != cudaSuccess ||
         cudaMalloc(&p->counters, sizeof(int) * kv_pool::kCounterSlots) != cudaSuccess) {
         cudaGetLastError();
@@ -207,6 +211,7 @@ kv_status kv_pool_create(int num_blocks, int block_size, int num_kv_heads, int h
                cudaMemset(p->counters, 0, sizeof(int) * kv_pool::kCounterSlots) != cudaSuccess) {
         st = KV_ERR_CUDA;
     } else {
+        if (one) p->v = static_cast<char *>(p->k) + tile_bytes(dtype, head_dim);
         st = kv_allocator_create(num_blocks, &p->alloc);
     }
     if (st != KV_OK) {
@@ -224,7 +229,7 @@ kv_status kv_pool_destroy(kv_pool_t p) {
     const bool switched = cudaGetDevice(&cur) == cudaSuccess && cur != p->device &&
                           cudaSetDevice(p->device) == cudaSuccess;
     if (p->k) cudaFree(p->k);
-    if (p->v) cudaFree(p->v);
+    if (p->v && p->dtype != KV_I4) cudaFree(p->v);
     if (p->err) cudaFree(p->err);
     if (p->counters) cudaFree(p->counters);
     if (switched) cudaSetDevice(cur);
@@ -289,9 +294,9 @@ kv_status kv_cow_if_shared(kv_pool_t p, int32_t *block_id_inout, int *copied, vo
     if (rc == 1) return KV_OK;  // private already: write in place
     int32_t fresh = -1;
     if (kv_status st = kv_allocator_alloc(p->alloc, 1, &fresh)) return st;
-    const int block_chunks = block_chunks_of(p);
-    copy_block_kernel<<<grid_for(block_chunks, 256), 256, 0, as_stream(stream)>>>(
-        (uint4 *)p->k, (uint4 *)p->v, old, fresh, block_chunks);
+    const BlockParts b = block_parts(p);
+    copy_block_kernel<<<grid_for(b.chunks, 256), 256, 0, as_stream(stream)>>>(
+        (uint4 *)b.a, (uint4 *)b.b, old, fresh, b.chunks, b.stride);
     if (kv_status st = cuda_status(cudaGetLastError())) {
         kv_allocator_free(p->alloc, 1, &fresh);
         return st;
@@ -340,9 +345,9 @@ kv_status kv_copy_blocks(kv_pool_t p, const int32_t *src, const int32_t *dst, in
     if (kv_status st = require_device(p->device)) return st;
     if (n == 0) return KV_OK;
     if (!src || !dst) return KV_ERR_ARG;
-    const int block_chunks = block_chunks_of(p);
-    copy_blocks_kernel<<<grid_for((long long)n * block_chunks, 256), 256, 0, as_stream(stream)>>>(
-        (uint4 *)p->k, (uint4 *)p->v, src, dst, n, block_chunks, p->num_blocks, p->err);
+    const BlockParts b = block_parts(p);
+    copy_blocks_kernel<<<grid_for((long long)n * b.chunks, 256), 256, 0, as_stream(stream)>>>(
+        (uint4 *)b.a, (uint4 *)b.b, src, dst, n, b.chunks, b.stride, p->num_blocks, p->err);
     return cuda_status(cudaGetLastError());
 }
 
@@ -351,10 +356,10 @@ static kv_status swap(kv_pool_t p, const int32_t *ids, int n, void *host, int di
     if (kv_status st = require_device(p->device)) return st;
     if (n == 0) return KV_OK;
     if (!ids || !host || (reinterpret_cast<uintptr_t>(host) & 15)) return KV_ERR_ARG;
-    const int block_chunks = block_chunks_of(p);
-    const long long total = (long long)n * block_chunks;
+    const BlockParts b = block_parts(p);
+    const long long total = (long long)n * b.chunks;
     swap_blocks_kernel<<<grid_for(total, 256), 256, 0, as_stream(stream)>>>(
-        (uint4 *)p->k, (uint4 *)p->v, (uint4 *)host, ids, n, block_chunks, p->num_blocks, dir,
+        (uint4 *)b.a, (uint4 *)b.b, (uint4 *)host, ids, n, b.chunks, b.stride, p->num_blocks, dir,
         p->err);
     return cuda_status(cudaGetLastError());
 }

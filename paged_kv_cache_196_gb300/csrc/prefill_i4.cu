@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(256) expand_i4_kernel(const char *__restrict__
     const bool ok = id >= 0 && id < num_blocks;
     if (h == 0 && lane == 0) new_table[at] = ok ? (int32_t)at : -1;
     if (!ok) return;  // the prefill reports it and reads zeros
-    const char *kt = k_pool + ((size_t)id * hkv + h) * kExTile, *vt = v_pool + ((size_t)id * hkv + h) * kExTile;
+    const size_t tile = ((size_t)id * hkv + h) * 2 * kExTile;
+    const char *kt = k_pool + tile, *vt = v_pool + tile;
     uint4 *ko = reinterpret_cast<uint4 *>(k_out + (at * hkv + h) * kExOut);
     uint2 *vo = reinterpret_cast<uint2 *>(v_out + (at * hkv + h) * kExOut);
     // word 32 j + lane: K row 2 j + lane / 16, octet lane % 16; V pair j, the word

@@ -245,11 +245,11 @@ __global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopePar
                 const long long tile_id = live ? (slot >> 4) * p.hkv + h : 0;
                 const int t = (int)(slot & 15);
                 if (__any_sync(0xffffffffu, live && !is_v))
-                    store_i4<D, false>(p.k_pool + tile_id * (9 * D), t, o, y, p.k_inv, live && !is_v);
+                    store_i4<D, false>(p.k_pool + tile_id * (18 * D), t, o, y, p.k_inv, live && !is_v);
                 if (__any_sync(0xffffffffu, live && is_v)) {
                     float z[8];
                     x[u].get(z);
-                    store_i4<D, true>(p.v_pool + tile_id * (9 * D), t, o, z, p.v_inv, live && is_v);
+                    store_i4<D, true>(p.v_pool + tile_id * (18 * D), t, o, z, p.v_inv, live && is_v);
                 }
             } else if (live) {
                 if (changed) x[u].set(y);
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(256) read_tokens_kernel(const char *__restrict
         const long long tile = (slot >> 4) * hkv + h;
         Octet<OUT> ko, vo;
         if constexpr (ET == KV_I4) {
-            const char *kt = k_pool + tile * (9 * D), *vt = v_pool + tile * (9 * D);
+            const char *kt = k_pool + tile * (18 * D), *vt = v_pool + tile * (18 * D);
             const uint32_t kw = reinterpret_cast<const uint32_t *>(kt)[t * (D / 8) + o];
             const float ks = i4::e4m3_to_float((uint8_t)kt[8 * D + t * (D / 16) + (o >> 1)]) * k_scale;
             const uint16_t *vc = reinterpret_cast<const uint16_t *>(vt) + (t >> 1) * (D / 2) +

@@ -138,8 +138,7 @@ class Cache:
         self.pool = pk.kv_pool_create(self.nb, 16, hkv, d, pk.KV_I4)
         pk.kv_pool_set_i4_scales(self.pool, k_scale, v_scale)
         if poison:  # every byte 0xff: codes of 7, scales that are NaN
-            for ptr in pk.kv_pool_ptrs(self.pool):
-                raw_bytes(ptr, self.nb * hkv * 9 * d).fill_(255)
+            raw_bytes(pk.kv_pool_ptrs(self.pool)[0], self.nb * hkv * 18 * d).fill_(255)
         rows = [torch.from_numpy(rng.standard_normal((max(int(n), 1), hkv, d)).astype(np.float32))[:int(n)] for n in lens]
         self.k = [(x * torch.from_numpy(np.exp(0.5 * rng.standard_normal((1, hkv, d))).astype(np.float32))).to(TORCH[dtype])
                   for x in rows]

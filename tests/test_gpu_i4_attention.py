@@ -82,11 +82,12 @@ def test_decode_placement_and_order_do_not_matter():
     b.close()
 
 
-def test_decode_bad_blocks_are_skipped_and_flagged():
+@pytest.mark.parametrize("bad", [-1, -2, -2 ** 31, 2 ** 31 - 1])
+def test_decode_bad_blocks_are_skipped_and_flagged(bad):
     c = Cache([100, 64], 2, 128, seed=9)
     q = c.queries(2, 4, "bf16")
     tables = c.tables.copy()
-    tables[0, 2], tables[1, 0] = c.nb, -5
+    tables[0, 2], tables[1, 0] = c.nb, bad
     out, lse = c.decode(q, "bf16", "f32", 2, tables=torch.from_numpy(tables).cuda(), expect=0x1)
     c.kv = [np.delete(c.kv[0], np.s_[32:48], 0), c.kv[1][16:]]
     c.vv = [np.delete(c.vv[0], np.s_[32:48], 0), c.vv[1][16:]]
@@ -153,8 +154,7 @@ def test_decode_past_32_bit_offsets():
 def test_decode_wait_limit():
     """A wait that runs out is reported; the pool works again afterwards."""
     c = Cache([3000, 800], 8, 128, seed=5, num_blocks=16384, poison=False)
-    for ptr in pk.kv_pool_ptrs(c.pool):  # the other blocks: codes of 0
-        raw_bytes(ptr, (c.nb - c.width - 50) * 8 * 9 * 128).fill_(0)
+    raw_bytes(pk.kv_pool_ptrs(c.pool)[0], (c.nb - c.width - 50) * 8 * 18 * 128).fill_(0)  # the other blocks: zeros
     # more bytes than L2 holds: some first copy is not there when it is looked for
     B, width = 64, 250
     tables = torch.arange(B * width, dtype=torch.int32, device="cuda").view(B, width)

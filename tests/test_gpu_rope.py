@@ -110,8 +110,10 @@ def test_bad_slots_and_positions_are_left_out_and_flagged(pool_type):
     pos[1], pos[3] = -1, 300
     slots[2] = nb * 16
     pool = pk.kv_pool_create(nb, 16, hkv, d, pk.KV_BF16 if pool_type == "bf16" else pk.KV_I4)
-    size = nb * hkv * (16 * d * 2 if pool_type == "bf16" else 9 * d)
-    views = [raw_bytes(ptr, size) for ptr in pk.kv_pool_ptrs(pool)]
+    if pool_type == "bf16":
+        views = [raw_bytes(ptr, nb * hkv * 16 * d * 2) for ptr in pk.kv_pool_ptrs(pool)]
+    else:  # K and V tiles alternate in one array
+        views = [raw_bytes(pk.kv_pool_ptrs(pool)[0], nb * hkv * 18 * d)]
     for x in views:
         x.fill_(0x35)
     q_out = torch.zeros(T, hq, d, dtype=torch.bfloat16, device="cuda").fill_(9)
