@@ -198,6 +198,19 @@ KV_DEVICE void store_out(void *out, size_t idx, float v, int out_type) {
         reinterpret_cast<uint16_t *>(out)[idx] = float_to_f16_rn(v);
 }
 
+// Two fp32 values as a pair of bf16 or fp16 (nearest even), low half first: one
+// instruction, where single conversions go through a slower unit.
+KV_DEVICE uint32_t float2_to_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+KV_DEVICE uint32_t float2_to_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Four consecutive elements (idx a multiple of 4) as store_out, in one store.
 KV_DEVICE void store_out4(void *out, size_t idx, float4 v, int out_type) {
     if (out_type == KV_F32) {
@@ -206,11 +219,9 @@ KV_DEVICE void store_out4(void *out, size_t idx, float4 v, int out_type) {
     }
     uint2 w;
     if (out_type == KV_BF16)
-        w = make_uint2(float_to_bf16_rn(v.x) | (uint32_t)float_to_bf16_rn(v.y) << 16,
-                       float_to_bf16_rn(v.z) | (uint32_t)float_to_bf16_rn(v.w) << 16);
+        w = make_uint2(float2_to_bf16x2(v.x, v.y), float2_to_bf16x2(v.z, v.w));
     else
-        w = make_uint2(float_to_f16_rn(v.x) | (uint32_t)float_to_f16_rn(v.y) << 16,
-                       float_to_f16_rn(v.z) | (uint32_t)float_to_f16_rn(v.w) << 16);
+        w = make_uint2(float2_to_f16x2(v.x, v.y), float2_to_f16x2(v.z, v.w));
     *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(out) + idx) = w;
 }
 

@@ -97,6 +97,19 @@ KV_DEVICE float ex2(float x) {
     return y;
 }
 
+// Whether a phase is complete, without the suspension of mbarrier.try_wait.
+KV_DEVICE bool phase_done(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // One lane of a converged warp, in the form that lets the compiler issue copies from
 // uniform registers (under an ordinary lane test it loops over the lanes).
 KV_DEVICE bool elect_one() {
@@ -122,12 +135,6 @@ KV_DEVICE uint32_t transpose8(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
-}
-
-KV_DEVICE uint32_t half_pair(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 // N words of shared memory, 16 or 8 bytes at once.
@@ -397,6 +404,17 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
     int st = 0;
     uint32_t parity = 0;
     bool stop = false;
+    // Test instantiation with a limit of 0: a round that is not there at once is a
+    // wait that ran out (try_wait would sleep until it came).
+    if constexpr (TW) {
+        if (g_wait_limit_ns == 0) {
+            stop = __any_sync(0xffffffffu, !phase_done(&full[0], 0));
+            if (stop && lane == 0) {
+                atomicOr(p.err, KV_DEVERR_TIMEOUT);
+                s_abort = 1;
+            }
+        }
+    }
     I4Work w = i4_sequence(p, b0, kRound, kCols, false);
     while (todo > 0) {
         const int per = w.rounds + kI4PairCost;
@@ -625,13 +643,13 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                     const float p2 = ex2(fmaf(s[n][nt][2], sc[nt][0], u0)), p3 = ex2(fmaf(s[n][nt][3], sc[nt][1], u1));
                     l_run[nt][0] += p0 + p2;
                     l_run[nt][1] += p1 + p3;
-                    const uint32_t h01 = half_pair(p0, p1), h23 = half_pair(p2, p3);
+                    const uint32_t h01 = float2_to_f16x2(p0, p1), h23 = float2_to_f16x2(p2, p3);
                     ph[n][nt][0] = transpose8(h01);
                     ph[n][nt][1] = transpose8(h23);
                     if constexpr (EXACT) {
                         const float2 f01 = f16x2_to_float2(h01), f23 = f16x2_to_float2(h23);
-                        pl[n][nt][0] = transpose8(half_pair(p0 - f01.x, p1 - f01.y));
-                        pl[n][nt][1] = transpose8(half_pair(p2 - f23.x, p3 - f23.y));
+                        pl[n][nt][0] = transpose8(float2_to_f16x2(p0 - f01.x, p1 - f01.y));
+                        pl[n][nt][1] = transpose8(float2_to_f16x2(p2 - f23.x, p3 - f23.y));
                     }
                 }
             }

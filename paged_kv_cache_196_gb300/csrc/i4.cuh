@@ -67,29 +67,49 @@ KV_DEVICE constexpr int v_swizzle(int p) {
     return D == 128 ? 8 * (p & 3) : 8 * ((p >> 1) & 1);
 }
 
+// x / d by its reciprocal r (to an ulp or so) and one correction step, the usual
+// division by iteration: the quotient's error before the last rounding is of the order
+// of 2^-46.
+KV_DEVICE float divide(float x, float d, float r) {
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+}
+
+KV_DEVICE float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The scale byte of a group with largest magnitude m.  The e4m3 borders times 7 have
+// at most 8 significant bits: m / 7, rounded correctly, lies on the right side of (or
+// on) each of them, as for codes8.
+KV_DEVICE uint32_t scale_byte(float m) {
+    m = m > 1e30f ? 1e30f : m;  // an infinity would leave NaN; NaN stays
+    return e4m3_of(divide(m, 7.f, 1.f / 7.f));
+}
+
 // Eight values of one group half -> their eight 4-bit codes, value i in bits
 // 4i .. 4i + 3, given the group's scale s (a value of e4m3).
 //
 // c = rint(x / s) must be decided as exact arithmetic decides it: values of 16
-// bits are often exactly between two codes.  (k + 1/2) s has at most 8
-// significant bits, so the correctly rounded quotient lies on the right side of
-// (or on) each border, and a reciprocal with one correction step gives that
-// quotient: q0 = x r, q = q0 + (x - q0 s) r.  Clamping x to +-7.25 s first (exact)
-// keeps infinities and |c| > 7 out.  rint and the bias are one addition of
-// 1.5 * 2^23 + 8.
+// bits are often exactly between two codes.  A border (k + 1/2) s has at most 8
+// significant bits; a quotient that is one of them comes out exactly, and any other
+// fp32 x is further from it than half an ulp of the quotient.  Clamping x to +-7.25 s
+// first (exact) keeps infinities and |c| > 7 out.  rint and the bias are one addition
+// of 1.5 * 2^23 + 8.
 KV_DEVICE uint32_t codes8(const float (&x)[8], float s) {
     const float lim = 7.25f * s;
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+    const float r = s > 0.f ? reciprocal(s) : 0.f;
     uint32_t w = 0;
 #pragma unroll
     for (int i = 7; i >= 0; --i) {
-        const float y = fminf(fmaxf(x[i], -lim), lim);
-        const float q0 = __fmul_rn(y, r);
-        const float q = __fmaf_rn(__fmaf_rn(-q0, s, y), r, q0);
-        // low bits of the sum's word: rint(q) + 8, in 1..15
-        w = (w << 4) + (__float_as_uint(__fadd_rn(q, 12582920.f)) & 15u);
+        const float q = divide(fminf(fmaxf(x[i], -lim), lim), s, r);
+        // low bits of the sum's word: rint(q) + 8, in 1..15; the rest is the same in
+        // each and subtracted once
+        w = w * 16u + __float_as_uint(__fadd_rn(q, 12582920.f));
     }
-    return w;
+    return w - 0x4B400000u * 0x11111111u;
 }
 
 // Two scale bytes (low byte first) as the fp16 pair s / 256.  e4m3's exponent and

@@ -35,7 +35,7 @@ template <bool BF16>
 KV_DEVICE uint32_t to_k_type(uint32_t h2) {
     if constexpr (!BF16) return h2;
     const float2 f = f16x2_to_float2(h2);
-    return float_to_bf16_rn(f.x) | (uint32_t)float_to_bf16_rn(f.y) << 16;  // exact
+    return float2_to_bf16x2(f.x, f.y);  // exact
 }
 
 // One warp expands the K and V tiles of one (sequence, block, kv head) and writes

@@ -10,12 +10,12 @@
 //
 // Work.  Memory-bound: each element is read and written once.  Eight
 // consecutive dimensions (one 16-byte chunk of 16-bit elements) are a thread's
-// share of a row; a row (one head of q, k or v) is D / 8 neighbouring lanes, a
-// warp takes 32 / (D / 8) rows at a time of one token, kRows / that many times:
-// the token's cos and sin are loaded once per thread and the rows' loads are all
-// issued before the first use.  The partner of a half-split pair sits a fixed
-// number of lanes away and comes by shuffle, so that no element is loaded twice
-// and q may be rotated in place.
+// share of a row; a row (one head of q, k or v) is D / 8 neighbouring lanes.  A
+// warp takes 32 / (D / 8) rows of one token at a time, P times, all of q, of k or of v:
+// the token's cos and sin are loaded once per thread, the rows' loads are all issued
+// before the first use, and nothing branches within a warp.  The partner of a
+// half-split pair sits a fixed number of lanes away and comes by shuffle, so that no
+// element is loaded twice and q may be rotated in place.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -28,7 +28,8 @@
 
 namespace pkv {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = 8;
+constexpr int kRopeThreads = kRopeWarps * 32;
 
 struct RopeParams {
     const char *q, *k, *v;             // input rows, heads packed within a token
@@ -88,9 +89,9 @@ struct Octet {
                 w[2 * i] = __float_as_uint(x[2 * i]);
                 w[2 * i + 1] = __float_as_uint(x[2 * i + 1]);
             } else if constexpr (ET == KV_BF16) {
-                w[i] = float_to_bf16_rn(x[2 * i]) | (uint32_t)float_to_bf16_rn(x[2 * i + 1]) << 16;
+                w[i] = float2_to_bf16x2(x[2 * i], x[2 * i + 1]);
             } else {
-                w[i] = float_to_f16_rn(x[2 * i]) | (uint32_t)float_to_f16_rn(x[2 * i + 1]) << 16;
+                w[i] = float2_to_f16x2(x[2 * i], x[2 * i + 1]);
             }
         }
     }
@@ -108,7 +109,7 @@ KV_DEVICE void store_i4(char *tile, int t, int o, float (&x)[8], float inv, bool
         m = i4::max_nan(m, fabsf(x[i]));
     }
     m = i4::max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    const uint32_t sb = i4::e4m3_of(__fdiv_rn(m, 7.f));
+    const uint32_t sb = i4::scale_byte(m);
     const uint32_t w = i4::codes8(x, i4::e4m3_to_float(sb));
     if (!live) return;
     if constexpr (V) {
@@ -124,177 +125,187 @@ KV_DEVICE void store_i4(char *tile, int t, int o, float (&x)[8], float inv, bool
     }
 }
 
-// IN: type of the rows; I4: 4-bit pool, else the pool holds type IN.  R: rows
-// of a token per warp (a multiple of 32 / (D / 8)).
-template <int D, int IN, bool I4, int R>
+// y[i] = x[i] c[i] + z[i] s[i] for eight values: two products and their sum, each
+// rounded.  The products run on pairs; the sums do not, since a packed product and a
+// packed sum come back contracted to one rounding.
+KV_DEVICE void rotate8(const float (&x)[8], const float (&z)[8], const float (&c)[8], const float (&s)[8],
+                       float (&y)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 a = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(c[i], c[i + 1]));
+        const float2 b = __fmul2_rn(make_float2(z[i], z[i + 1]), make_float2(s[i], s[i + 1]));
+        y[i] = __fadd_rn(a.x, b.x);
+        y[i + 1] = __fadd_rn(a.y, b.y);
+    }
+}
+
+// IN: type of the rows; I4: 4-bit pool, else the pool holds type IN.  P: passes of a
+// warp, 32 / (D / 8) rows each.  blockIdx.y: a warp's rows, first those of q, then of
+// k, then of v; blockIdx.x: kRopeWarps tokens.
+template <int D, int IN, bool I4, int P>
 __global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopeParams p) {
     constexpr int kLanes = D / 8;         // lanes of one row
     constexpr int kAtOnce = 32 / kLanes;  // rows of one pass
-    constexpr int kPasses = R / kAtOnce;
     constexpr int kE = IN == KV_F32 ? 4 : 2;
-    const int lane = threadIdx.x & 31, o = lane % kLanes, sub = lane / kLanes;
-    const int rows = p.hq + 2 * p.hkv;
-    const int units = (rows + R - 1) / R;
-    const long long total = p.num_tokens * units;
-    const long long stride = (long long)gridDim.x * (kRopeThreads / 32);
-    for (long long wi = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); wi < total; wi += stride) {
-        const long long tok = wi / units;
-        const int row0 = (int)(wi - tok * units) * R + sub;
-        // ---- the rows' loads
-        Octet<IN> x[kPasses];
-        int row[kPasses];
+    constexpr int kRowBytes = D * kE;
+    const long long tok = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+    if (tok >= p.num_tokens) return;
+    const int lane = threadIdx.x & 31, o = lane % kLanes;
+    // ---- whose rows
+    const int uq = (p.hq + P * kAtOnce - 1) / (P * kAtOnce), ukv = (p.hkv + P * kAtOnce - 1) / (P * kAtOnce);
+    const int unit = blockIdx.y;
+    const bool is_q = unit < uq, is_v = unit >= uq + ukv;
+    const int heads = is_q ? p.hq : p.hkv;
+    const int h0 = (is_q ? unit : is_v ? unit - uq - ukv : unit - uq) * (P * kAtOnce) + lane / kLanes;
+    const char *src = is_q ? p.q + tok * p.q_stride : is_v ? p.v + tok * p.v_stride : p.k + tok * p.k_stride;
+    src += (long long)h0 * kRowBytes + o * (8 * kE);
+    Octet<IN> x[P];
 #pragma unroll
-        for (int u = 0; u < kPasses; ++u) {
-            row[u] = row0 + u * kAtOnce;
-            const int r = row[u];
-            const char *src = nullptr;
-            if (r < p.hq)
-                src = p.q + tok * p.q_stride + (long long)r * (D * kE);
-            else if (r < p.hq + p.hkv)
-                src = p.k + tok * p.k_stride + (long long)(r - p.hq) * (D * kE);
-            else if (r < rows)
-                src = p.v + tok * p.v_stride + (long long)(r - p.hq - p.hkv) * (D * kE);
-            if (src) {
-                x[u].load(src + o * (8 * kE));
-            } else {
+    for (int u = 0; u < P; ++u) {
+        if (h0 + u * kAtOnce < heads) {
+            x[u].load(src + u * (kAtOnce * kRowBytes));
+        } else {
 #pragma unroll
-                for (int i = 0; i < Octet<IN>::kWords; ++i) x[u].w[i] = 0;
+            for (int i = 0; i < Octet<IN>::kWords; ++i) x[u].w[i] = 0;
+        }
+    }
+    // ---- the token's place
+    int pos = 0;
+    if (p.rot > 0) {
+        pos = __ldg(p.positions + tok);
+        if (pos < 0 || pos >= p.max_position) {  // the token is left out
+            if (unit == 0 && lane == 0) atomicOr(p.err, KV_DEVERR_POSITION);
+            return;
+        }
+    }
+    char *dst;
+    int t = 0;  // the token's place in its block
+    if (is_q) {
+        dst = p.q_out + tok * p.q_out_stride + (long long)h0 * kRowBytes + o * (8 * kE);
+    } else {
+        const long long slot = __ldg(p.slots + tok);
+        if (slot < 0 || slot >= p.num_slots) {
+            if (slot >= 0 && unit == uq && lane == 0) atomicOr(p.err, KV_DEVERR_SLOT_RANGE);
+            return;
+        }
+        t = (int)(slot & 15);
+        const long long tile = (slot >> 4) * p.hkv + h0;
+        dst = is_v ? p.v_pool : p.k_pool;
+        if constexpr (I4)
+            dst += tile * (18 * D);
+        else
+            dst += (tile * 16 + t) * kRowBytes + o * (8 * kE);
+        if constexpr (I4) {
+            if (is_v) {
+#pragma unroll
+                for (int u = 0; u < P; ++u) {
+                    float y[8];
+                    x[u].get(y);
+                    store_i4<D, true>(dst + (long long)u * kAtOnce * (18 * D), t, o, y, p.v_inv, h0 + u * kAtOnce < heads);
+                }
+                return;
             }
         }
-        long long slot = __ldg(p.slots + tok);
-        if (slot >= p.num_slots) {
-            if (lane == 0 && wi == tok * units) atomicOr(p.err, KV_DEVERR_SLOT_RANGE);
-            slot = -1;
+    }
+    const long long step_dst = is_q ? (long long)kAtOnce * kRowBytes : (long long)kAtOnce * (I4 ? 18 * D : 16 * kRowBytes);
+    // ---- cos and sin of this lane's pairs, the sign of the formula in sin; a lane
+    // that rotates nothing takes 1 and 0
+    float c[8], s[8];
+    const bool rotates = !is_v && 8 * o < p.rot;
+    const int half = p.rot / 2;
+    const bool first = 8 * o < half;
+    if (rotates) {
+        const float *cs = p.table + (long long)pos * p.rot;
+        if (p.interleaved) {  // pairs 4 o .. 4 o + 3
+            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(cs + 4 * o));
+            const float4 s4 = __ldg(reinterpret_cast<const float4 *>(cs + half + 4 * o));
+            c[0] = c[1] = c4.x, c[2] = c[3] = c4.y, c[4] = c[5] = c4.z, c[6] = c[7] = c4.w;
+            s[0] = -s4.x, s[1] = s4.x, s[2] = -s4.y, s[3] = s4.y;
+            s[4] = -s4.z, s[5] = s4.z, s[6] = -s4.w, s[7] = s4.w;
+        } else {  // pairs j0 .. j0 + 7
+            const int j0 = first ? 8 * o : 8 * o - half;
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                const float4 c4 = __ldg(reinterpret_cast<const float4 *>(cs + j0 + i));
+                const float4 s4 = __ldg(reinterpret_cast<const float4 *>(cs + half + j0 + i));
+                c[i] = c4.x, c[i + 1] = c4.y, c[i + 2] = c4.z, c[i + 3] = c4.w;
+                s[i] = first ? -s4.x : s4.x, s[i + 1] = first ? -s4.y : s4.y;
+                s[i + 2] = first ? -s4.z : s4.z, s[i + 3] = first ? -s4.w : s4.w;
+            }
         }
-        // ---- cos and sin of this lane's pairs
-        float c[8], s[8];
-        const bool rotates = 8 * o < p.rot;
-        if (p.rot > 0) {
-            const int pos = __ldg(p.positions + tok);
-            if (pos < 0 || pos >= p.max_position) {  // the token is left out
-                if (lane == 0 && wi == tok * units) atomicOr(p.err, KV_DEVERR_POSITION);
+    }
+    // the lane that holds the other halves of this lane's half-split pairs
+    const int across = half / 8;
+    const int partner = !rotates || p.interleaved ? lane : first ? lane + across : lane - across;
+    const bool swaps = p.rot > 0 && !p.interleaved && !is_v;
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+        const bool live = h0 + u * kAtOnce < heads;
+        Octet<IN> other = x[u];
+        if (swaps) {
+#pragma unroll
+            for (int i = 0; i < Octet<IN>::kWords; ++i) other.w[i] = __shfl_sync(0xffffffffu, x[u].w[i], partner);
+        }
+        float y[8];
+        if (rotates) {
+            float a[8], z[8];
+            x[u].get(a);
+            other.get(z);
+            if (p.interleaved) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) z[i] = a[i + 1], z[i + 1] = a[i];
+            }
+            rotate8(a, z, c, s, y);
+            if (!I4 || is_q) x[u].set(y);
+        } else if (I4) {
+            x[u].get(y);
+        }
+        if constexpr (I4) {
+            if (!is_q) {  // a K row; the group's lanes exchange their maxima
+                store_i4<D, false>(dst + u * step_dst, t, o, y, p.k_inv, live);
                 continue;
             }
-            if (rotates) {
-                const float *cs = p.table + (long long)pos * p.rot;
-                const int half = p.rot / 2;
-                if (p.interleaved) {  // pairs 4 o .. 4 o + 3
-                    const float4 c4 = *reinterpret_cast<const float4 *>(cs + 4 * o);
-                    const float4 s4 = *reinterpret_cast<const float4 *>(cs + half + 4 * o);
-                    c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
-                    s[0] = s4.x, s[1] = s4.y, s[2] = s4.z, s[3] = s4.w;
-                } else {  // pairs j0 .. j0 + 7
-                    const int j0 = 8 * o < half ? 8 * o : 8 * o - half;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float4 c4 = *reinterpret_cast<const float4 *>(cs + j0 + 4 * i);
-                        const float4 s4 = *reinterpret_cast<const float4 *>(cs + half + j0 + 4 * i);
-                        c[4 * i] = c4.x, c[4 * i + 1] = c4.y, c[4 * i + 2] = c4.z, c[4 * i + 3] = c4.w;
-                        s[4 * i] = s4.x, s[4 * i + 1] = s4.y, s[4 * i + 2] = s4.z, s[4 * i + 3] = s4.w;
-                    }
-                }
-            }
         }
-        // ---- rotate and store
-        const int step = p.rot / 16;  // lanes between the halves of a pair
-        const bool first = o < step;
-        const int partner = (lane & ~(kLanes - 1)) + (!rotates || p.interleaved ? o : first ? o + step : o - step);
-#pragma unroll
-        for (int u = 0; u < kPasses; ++u) {
-            const int r = row[u];
-            float y[8];
-            x[u].get(y);
-            bool changed = false;
-            if (p.rot > 0) {
-                const bool turn = rotates && r < p.hq + p.hkv;
-                if (p.interleaved) {
-                    if (turn) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float x1 = y[2 * i], x2 = y[2 * i + 1];
-                            y[2 * i] = __fsub_rn(__fmul_rn(x1, c[i]), __fmul_rn(x2, s[i]));
-                            y[2 * i + 1] = __fadd_rn(__fmul_rn(x2, c[i]), __fmul_rn(x1, s[i]));
-                        }
-                    }
-                } else {
-                    Octet<IN> other;
-#pragma unroll
-                    for (int i = 0; i < Octet<IN>::kWords; ++i)
-                        other.w[i] = __shfl_sync(0xffffffffu, x[u].w[i], partner);
-                    if (turn) {
-                        float z[8];
-                        other.get(z);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float a = __fmul_rn(y[i], c[i]), b = __fmul_rn(z[i], s[i]);
-                            y[i] = first ? __fsub_rn(a, b) : __fadd_rn(a, b);
-                        }
-                    }
-                }
-                changed = turn;
-            }
-            const bool is_q = r < p.hq, is_v = r >= p.hq + p.hkv;
-            if (is_q) {
-                if (changed) x[u].set(y);
-                x[u].store(p.q_out + tok * p.q_out_stride + (long long)r * (D * kE) + o * (8 * kE));
-            }
-            const int h = is_v ? r - p.hq - p.hkv : r - p.hq;
-            const bool live = !is_q && r < rows && slot >= 0;
-            if constexpr (I4) {
-                // whole warps quantise: the group's lanes exchange their maxima
-                const long long tile_id = live ? (slot >> 4) * p.hkv + h : 0;
-                const int t = (int)(slot & 15);
-                if (__any_sync(0xffffffffu, live && !is_v))
-                    store_i4<D, false>(p.k_pool + tile_id * (18 * D), t, o, y, p.k_inv, live && !is_v);
-                if (__any_sync(0xffffffffu, live && is_v)) {
-                    float z[8];
-                    x[u].get(z);
-                    store_i4<D, true>(p.v_pool + tile_id * (18 * D), t, o, z, p.v_inv, live && is_v);
-                }
-            } else if (live) {
-                if (changed) x[u].set(y);
-                const long long prow = ((slot >> 4) * p.hkv + h) * 16 + (slot & 15);
-                x[u].store((is_v ? p.v_pool : p.k_pool) + prow * (D * kE) + o * (8 * kE));
-            }
-        }
+        if (live) x[u].store(dst + u * step_dst);  // what is not rotated: bit by bit
     }
 }
 
 // Cached tokens as rows: token i's K and V rows [hkv][D] of type OUT from slot
-// slots[i].  A thread takes an octet; ET: the pool's type (KV_I4: codes).
+// slots[i].  ET: the pool's type (KV_I4: codes).  A warp takes the rows of
+// 32 / (D / 8) heads of a token at a time, an octet a lane.
 template <int D, int ET, int OUT>
-__global__ void __launch_bounds__(256) read_tokens_kernel(const char *__restrict__ k_pool,
-                                                          const char *__restrict__ v_pool,
-                                                          const int64_t *__restrict__ slots, long long num_tokens,
-                                                          int hkv, long long num_slots, float k_scale,
-                                                          float v_scale, char *__restrict__ k_out,
-                                                          char *__restrict__ v_out, int *err) {
-    constexpr int kLanes = D / 8;
+__global__ void __launch_bounds__(kRopeThreads) read_tokens_kernel(const char *__restrict__ k_pool,
+                                                                   const char *__restrict__ v_pool,
+                                                                   const int64_t *__restrict__ slots,
+                                                                   long long num_tokens, int hkv, long long num_slots,
+                                                                   float k_scale, float v_scale,
+                                                                   char *__restrict__ k_out,
+                                                                   char *__restrict__ v_out, int *err) {
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
     constexpr int kE = OUT == KV_F32 ? 4 : 2;
-    const long long total = num_tokens * hkv * kLanes;
-    const long long stride = (long long)gridDim.x * blockDim.x;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
-        const long long row = i / kLanes;
-        const int o = (int)(i % kLanes);
-        const long long tok = row / hkv;
-        const int h = (int)(row - tok * hkv);
-        const long long slot = __ldg(slots + tok);
-        if (slot >= num_slots) {
-            if (o == 0 && h == 0) atomicOr(err, KV_DEVERR_SLOT_RANGE);
-            continue;
-        }
-        if (slot < 0) continue;
-        const int t = (int)(slot & 15);
+    const long long tok = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+    if (tok >= num_tokens) return;
+    const int lane = threadIdx.x & 31, o = lane % kLanes;
+    const long long slot = __ldg(slots + tok);
+    if (slot < 0 || slot >= num_slots) {
+        if (slot >= 0 && lane == 0) atomicOr(err, KV_DEVERR_SLOT_RANGE);
+        return;
+    }
+    const int t = (int)(slot & 15);
+#pragma unroll 4
+    for (int h = lane / kLanes; h < hkv; h += kAtOnce) {
         const long long tile = (slot >> 4) * hkv + h;
         Octet<OUT> ko, vo;
         if constexpr (ET == KV_I4) {
             const char *kt = k_pool + tile * (18 * D), *vt = v_pool + tile * (18 * D);
-            const uint32_t kw = reinterpret_cast<const uint32_t *>(kt)[t * (D / 8) + o];
-            const float ks = i4::e4m3_to_float((uint8_t)kt[8 * D + t * (D / 16) + (o >> 1)]) * k_scale;
-            const uint16_t *vc = reinterpret_cast<const uint16_t *>(vt) + (t >> 1) * (D / 2) +
-                                 2 * ((2 * o) ^ i4::v_swizzle<D>(t >> 1)) + (t & 1);
-            const uint32_t vw = vc[0] | (uint32_t)vc[2] << 16;
-            const float vs = i4::e4m3_to_float((uint8_t)vt[8 * D + (t >> 1) * (D / 8) + (o & ~1) + (t & 1)]) * v_scale;
+            const uint32_t kw = __ldg(reinterpret_cast<const uint32_t *>(kt) + t * (D / 8) + o);
+            const uint32_t kb = __ldg(reinterpret_cast<const uint8_t *>(kt) + 8 * D + t * (D / 16) + (o >> 1));
+            // both tokens' words of quads 2 o and 2 o + 1
+            const uint2 vq = __ldg(reinterpret_cast<const uint2 *>(
+                reinterpret_cast<const uint32_t *>(vt) + (t >> 1) * (D / 4) + ((2 * o) ^ i4::v_swizzle<D>(t >> 1))));
+            const uint32_t vw = __byte_perm(vq.x, vq.y, t & 1 ? 0x7632 : 0x5410);
+            const uint32_t vb = __ldg(reinterpret_cast<const uint8_t *>(vt) + 8 * D + (t >> 1) * (D / 8) + (o & ~1) + (t & 1));
+            const float ks = i4::e4m3_to_float(kb) * k_scale, vs = i4::e4m3_to_float(vb) * v_scale;
             float a[8], b[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -308,36 +319,32 @@ __global__ void __launch_bounds__(256) read_tokens_kernel(const char *__restrict
             ko.load(k_pool + at);
             vo.load(v_pool + at);
         }
-        ko.store(k_out + i * (8 * kE));
-        vo.store(v_out + i * (8 * kE));
+        const long long at = (tok * hkv + h) * (long long)(D * kE) + o * (8 * kE);
+        ko.store(k_out + at);
+        vo.store(v_out + at);
     }
 }
 
 template <int D, int IN, bool I4>
-static void launch_append_rope(const RopeParams &p, cudaStream_t s) {
+static kv_status launch_append_rope(const RopeParams &p, cudaStream_t s) {
     constexpr int kAtOnce = 32 / (D / 8);
-    const long long rows = p.hq + 2LL * p.hkv;
-    // Rows per warp: few while that leaves SMs idle (a decode step), more when
+    // Passes per warp: one while that leaves SMs idle (a decode step), more when
     // there are warps enough, so that a token's cos and sin serve more rows.
-    const int sms = sm_count();
+    auto units = [&](int r) { return (p.hq + r - 1) / r + 2LL * ((p.hkv + r - 1) / r); };
     auto go = [&](auto fn, int r) {
-        const long long warps = p.num_tokens * ((rows + r - 1) / r);
-        long long blocks = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-        if (blocks > (1LL << 30)) blocks = 1LL << 30;
-        fn<<<(unsigned)blocks, kRopeThreads, 0, s>>>(p);
+        if (units(r) > 65535) return KV_ERR_UNSUPPORTED;
+        const dim3 grid((unsigned)((p.num_tokens + kRopeWarps - 1) / kRopeWarps), (unsigned)units(r));
+        fn<<<grid, kRopeThreads, 0, s>>>(p);
+        return cuda_status(cudaGetLastError());
     };
-    if (p.num_tokens * ((rows + 4 * kAtOnce - 1) / (4 * kAtOnce)) >= 16LL * sms)
-        go(append_rope_kernel<D, IN, I4, 4 * kAtOnce>, 4 * kAtOnce);
-    else
-        go(append_rope_kernel<D, IN, I4, kAtOnce>, kAtOnce);
+    if (p.num_tokens * units(4 * kAtOnce) >= 16LL * sm_count())
+        return go(append_rope_kernel<D, IN, I4, 4>, 4 * kAtOnce);
+    return go(append_rope_kernel<D, IN, I4, 1>, kAtOnce);
 }
 
 template <int D, int ET, int OUT>
 static void launch_read(kv_pool_t p, const int64_t *slots, long long n, void *k_out, void *v_out, cudaStream_t s) {
-    const long long total = n * p->num_kv_heads * (D / 8);
-    long long blocks = (total + 255) / 256;
-    if (blocks > (1LL << 30)) blocks = 1LL << 30;
-    read_tokens_kernel<D, ET, OUT><<<(unsigned)blocks, 256, 0, s>>>(
+    read_tokens_kernel<D, ET, OUT><<<(unsigned)((n + kRopeWarps - 1) / kRopeWarps), kRopeThreads, 0, s>>>(
         (const char *)p->k, (const char *)p->v, slots, n, p->num_kv_heads, (long long)p->num_blocks * 16, p->k_scale,
         p->v_scale, (char *)k_out, (char *)v_out, p->err);
 }
@@ -407,17 +414,12 @@ kv_status kv_append_rope(kv_pool_t p, const void *k_new, const void *v_new, kv_d
         constexpr int D = decltype(dim)::value;
         const bool i4 = p->dtype == KV_I4;
         if (in_dtype == KV_F32)
-            i4 ? launch_append_rope<D, KV_F32, true>(r, s) : launch_append_rope<D, KV_F32, false>(r, s);
-        else if (in_dtype == KV_BF16)
-            i4 ? launch_append_rope<D, KV_BF16, true>(r, s) : launch_append_rope<D, KV_BF16, false>(r, s);
-        else
-            i4 ? launch_append_rope<D, KV_F16, true>(r, s) : launch_append_rope<D, KV_F16, false>(r, s);
+            return i4 ? launch_append_rope<D, KV_F32, true>(r, s) : launch_append_rope<D, KV_F32, false>(r, s);
+        if (in_dtype == KV_BF16)
+            return i4 ? launch_append_rope<D, KV_BF16, true>(r, s) : launch_append_rope<D, KV_BF16, false>(r, s);
+        return i4 ? launch_append_rope<D, KV_F16, true>(r, s) : launch_append_rope<D, KV_F16, false>(r, s);
     };
-    if (d == 128)
-        by_type(std::integral_constant<int, 128>{});
-    else
-        by_type(std::integral_constant<int, 64>{});
-    return cuda_status(cudaGetLastError());
+    return d == 128 ? by_type(std::integral_constant<int, 128>{}) : by_type(std::integral_constant<int, 64>{});
 }
 
 kv_status kv_read_tokens(kv_pool_t p, const int64_t *slots, int num_tokens, void *k_out, void *v_out,

@@ -204,7 +204,8 @@ def test_i4_stores_the_rotated_key(dtype, d, rot, interleaved):
     np.testing.assert_array_equal(f64(vo), stored(f64(qkv[:, hq + hkv:])))
     # the same rotation as a 16/32-bit pool's append gives q
     ref = torch.from_numpy(rotate32(qkv[:, :hq].float().cpu().numpy(), table[pos], rot, interleaved)).to(TORCH[dtype])
-    assert torch.equal(q_out.cpu(), ref)
+    bad = (q_out.cpu() != ref).nonzero()
+    assert not len(bad), (len(bad), bad[:4], q_out.cpu()[tuple(bad[0])], ref[tuple(bad[0])])
     pk.kv_pool_destroy(pool)
 
 
