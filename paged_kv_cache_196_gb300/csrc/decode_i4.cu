@@ -19,7 +19,8 @@
 // (head of the group, and query token where there are several).  Its blocks are
 // taken in rounds: a round is NB blocks for each of a CTA's seven attending warps,
 // which keep their own softmax states and meet at a pair's end.  The eighth warp
-// copies a round per ring stage and reads the table a round ahead.
+// copies a round per ring stage, reads the table a round ahead and lays out the next
+// pair's queries.
 // (Eight warps in all: the register file is split in four, so a ninth warp would
 // cost every warp a fifth of its registers.)
 //
@@ -57,6 +58,7 @@ constexpr int kI4Threads = kI4Attend + 32;       // and the copying warp
 constexpr int kI4MergeThreads = 128;             // of merge_i4_kernel
 constexpr int kI4BS = 16;
 constexpr int kI4PairCost = 1;       // rounds
+constexpr int kI4AloneSplits = 4;    // pieces that one warp merges
 constexpr int kI4MinRun = 2;         // shortest run: a pair's cost and a round
 constexpr int kI4ScanBatch = 4096;   // largest batch whose runs the device cuts
 // The weights are 2^(s - m + 6) for a reference m that is renewed (and the state
@@ -90,6 +92,16 @@ struct I4Params {
     int *counters;          // null: merge_i4_kernel merges
     int *err;
 };
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// One more arrival; what the arriving CTA's threads wrote before a barrier is visible to
+// whoever sees the count (and the other way round).
+KV_DEVICE int count_arrival(int *counter) {
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+    return old;
+}
 
 KV_DEVICE float ex2(float x) {
     float y;
@@ -149,19 +161,22 @@ KV_DEVICE void load_words(const char *src, uint32_t (&w)[N]) {
     }
 }
 
-// Shared memory: the ring (a stage: a round's blocks), the merge's outputs ([warp][4 columns][D], reused for the split merge's
+// Shared memory: the ring (a stage: a round's blocks), the merge's outputs ([warp][column][D], reused for the split merge's
 // weights), barriers and the stages' masks of missing blocks.
 template <int D, int NB, int NST>
 constexpr size_t i4_ring_bytes() {
     return (size_t)NST * kI4Warps * NB * 2 * 9 * D;
 }
-template <int D>
+// Columns that are merged at once: with one tile of eight the shared memory of a second
+// CTA per SM leaves room for four.
+constexpr int i4_merge_cols(int NT) { return NT == 1 ? 4 : 8 * NT; }
+template <int D, int NT>
 constexpr size_t i4_merge_bytes() {
-    return (size_t)kI4Warps * 4 * D * 4;
+    return (size_t)kI4Warps * i4_merge_cols(NT) * D * 4;
 }
-template <int D, int NB, int NST>
+template <int D, int NT, int NB, int NST>
 constexpr size_t i4_smem_bytes() {
-    return i4_ring_bytes<D, NB, NST>() + i4_merge_bytes<D>() + (size_t)NST * (2 * sizeof(uint64_t) + sizeof(int));
+    return i4_ring_bytes<D, NB, NST>() + i4_merge_bytes<D, NT>() + (size_t)NST * (2 * sizeof(uint64_t) + sizeof(int));
 }
 
 // A sequence: its query rows, keys, rounds, and the pairs it makes (0: left out).
@@ -206,6 +221,53 @@ KV_DEVICE I4Work i4_sequence(const I4Params &p, int b, int round_blocks, int col
     return w;
 }
 
+// The D / 32 elements of column gc's query that this lane lays out.
+template <int D>
+KV_DEVICE void load_query(const I4Params &p, const I4Work &w, int h, int gc, int lane, uint32_t (&two)[D / 64]) {
+    const int tq = w.T == 1 ? 0 : gc / p.g;
+    const uint16_t *src = p.q + out_row(p, w, tq, h * p.g + gc - tq * p.g) * D + lane * (D / 32);
+    if constexpr (D == 128) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
+        two[0] = u.x, two[1] = u.y;
+    } else {
+        two[0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+    }
+}
+
+// A warp lays out the query of a column: its largest magnitude to [2^13, 2^14) by a
+// power of two, so that fp16 holds it, then into the order of the fragments.
+template <int D, int NT>
+KV_DEVICE void put_query(const I4Params &p, const uint32_t (&two)[D / 64], int col, int lane, uint2 *fragments,
+                         float *scale) {
+    constexpr int kPer = D / 32;
+    __half *qs = reinterpret_cast<__half *>(fragments);
+    float x[kPer], m = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+        const float2 f = p.q_bf16 ? bf16x2_to_float2(two[i / 2]) : f16x2_to_float2(two[i / 2]);
+        x[i] = f.x, x[i + 1] = f.y;
+        m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    // exponent field of the largest; 0 (all zero or below normal) and 255 are left alone
+    const int e = (int)(__float_as_uint(m) >> 23);
+    const int up = e == 0 || e == 255 ? 0 : max(-126, min(126, 127 + 13 - e));
+    // the score's factor is made positive (its sign goes to q), so that scaling keeps the
+    // order of scores; a factor of 0 zeroes q instead
+    const bool zero = p.scale_log2 == 0.f;
+    const float mul = copysignf(zero ? 0.f : __uint_as_float((uint32_t)(127 + up) << 23), p.scale_log2);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        // dimension d: quarter cq, word in / 8, four bits in % 4 of half in / 4 % 2
+        const int d = lane * kPer + i, cq = d / (D / 4), in = d % (D / 4);
+        const int to = 4 * (in / 8) + in % 4, hi = in / 4 % 2;
+        qs[((((to >> 1) * NT + (col >> 3)) * 32 + (col & 7) * 4 + cq) * 2 + (to & 1)) * 2 + hi] = __float2half_rn(x[i] * mul);
+    }
+    if (lane == 0)
+        scale[col] = zero ? 1.f : fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 - up) << 23), 1e-37f);
+}
+
 // D: head dim.  NT: columns / 8 of a CTA.  EXACT: weights in two fp16 parts (fp32
 // output).  TW: waits read their limit at run time (tests).  NB: blocks of a warp's
 // share of a round; NST: ring stages; MINB: CTAs per SM it is built for.
@@ -221,19 +283,29 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     extern __shared__ __align__(128) char smem[];
-    constexpr size_t kRing = i4_ring_bytes<D, NB, NST>(), kMerge = i4_merge_bytes<D>();
+    constexpr size_t kRing = i4_ring_bytes<D, NB, NST>(), kMerge = i4_merge_bytes<D, NT>();
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRing + kMerge), *empty = full + NST;
     volatile int *missing = reinterpret_cast<int *>(empty + NST);  // bit i: block i of the round is not there
-    __shared__ uint2 s_q[kSteps * NT * 32];
-    __shared__ float s_scale[8 * NT];
-    __shared__ float s_m[kI4Warps * 8], s_l[kI4Warps * 8];
-    __shared__ int s_scan[kI4Warps + 1], s_most[kI4Warps + 1], s_start[3], s_last;
+    constexpr int kMC = i4_merge_cols(NT);
+    __shared__ uint2 s_q[2][kSteps * NT * 32];  // fragments of two pieces' queries
+    __shared__ float s_scale[2][8 * NT];
+    __shared__ uint64_t s_qfull[2], s_qempty[2];
+    __shared__ float s_m[kI4Warps * kMC], s_l[kI4Warps * kMC];
+    __shared__ int s_last;
+    // of the scan of the batch, over before the merges' are used (two CTAs fill the
+    // SM's shared memory to the last bytes)
+    int *s_scan = reinterpret_cast<int *>(s_m), *s_most = s_scan + kI4Warps + 1;
+    int *s_start = reinterpret_cast<int *>(s_l);
     __shared__ volatile int s_abort;  // a wait ran out
 
     if (tid == 0) {
         for (int st = 0; st < NST; ++st) {
             mbar_init(&full[st], 1);
             mbar_init(&empty[st], kI4Warps);
+        }
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&s_qfull[k], 1);
+            mbar_init(&s_qempty[k], kI4Warps);
         }
         mbar_init_fence();
         s_abort = 0;
@@ -341,17 +413,39 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             in_next = lane < kRound && blk < w.nblk;
             if (in_next) id_next = __ldg(p.tables + (size_t)w.b * p.max_blocks + blk);
         };
-        bool more = place();
+        // The queries of the second and later pieces (the attending warps lay out the
+        // first one's).  False if the buffer did not come free.
+        auto stage = [&](const I4Work &w, int pair, int piece) -> bool {
+            constexpr int kAhead = 4;
+            const int buf = piece & 1, h = pair % p.hkv, col0 = pair / p.hkv * kCols;
+            const int ncols = min(kCols, w.T * p.g - col0);
+            const bool bad = lane == 0 && !mbar_wait<TW>(&s_qempty[buf], ((piece - !buf * 2) >> 1) & 1, p.err);
+            if (__shfl_sync(0xffffffffu, bad, 0)) return false;
+            for (int first = 0; first < ncols; first += kAhead) {
+                uint32_t two[kAhead][D / 64];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) load_query<D>(p, w, h, col0 + min(first + k, ncols - 1), lane, two[k]);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (first + k < ncols) put_query<D, NT>(p, two[k], first + k, lane, s_q[buf], s_scale[buf]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_qfull[buf]);
+            return true;
+        };
+        bool more = place(), fresh = true;  // fresh: the round begins a piece
         if (more) entry();
-        int issued = 0;
+        int issued = 0, pieces = 0;
         while (more) {
-            const int id = id_next, h = pair % p.hkv, st = issued % NST;
-            const bool inside = in_next;
+            const I4Work cw = w;
+            const int id = id_next, cpair = pair, h = pair % p.hkv, st = issued % NST;
+            const bool inside = in_next, starts = fresh;
             // the next round's entries are on their way while this round is copied
             ++unit;
             --todo;
             ++round;
-            more = round < w.rounds ? todo > 0 : place();
+            fresh = round >= w.rounds;
+            more = fresh ? place() : todo > 0;
             if (more) entry();
             bool bad = false;
             if (lane == 0) {
@@ -386,6 +480,10 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 }
             }
             ++issued;
+            if (starts && pieces++ > 0 && !stage(cw, cpair, pieces - 1)) {
+                if (lane == 0) s_abort = 1;
+                break;
+            }
         }
         // Never leave while a copy into this CTA's shared memory may be in flight.
         if (lane == 0)
@@ -397,11 +495,12 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
     const int r = lane >> 2, c = lane & 3;
     // columns without a query hold zeros (later pieces may leave old ones: a column's
     // values reach no other column)
-    for (int i = tid; i < kSteps * NT * 32; i += kI4Attend) s_q[i] = make_uint2(0u, 0u);
-    for (int i = tid; i < 8 * NT; i += kI4Attend) s_scale[i] = 1.f;
+    for (int i = tid; i < 2 * kSteps * NT * 32; i += kI4Attend) s_q[0][i] = make_uint2(0u, 0u);
+    for (int i = tid; i < 2 * 8 * NT; i += kI4Attend) s_scale[0][i] = 1.f;
     named_bar_sync(1, kI4Attend);
+    if (lane == 0) mbar_arrive(&s_qempty[1]);  // the second piece's buffer is free
 
-    int st = 0;
+    int st = 0, piece = 0;
     uint32_t parity = 0;
     bool stop = false;
     // Test instantiation with a limit of 0: a round that is not there at once is a
@@ -443,61 +542,34 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             nsplit = (w.rounds + p.part_rounds - 1) / p.part_rounds;
             split = blockIdx.x;
         }
-        // ---- q of each column: largest magnitude to [2^13, 2^14) by a power of two,
-        // so that fp16 holds it, then into the order of the fragments
-        __half *qs = reinterpret_cast<__half *>(s_q);
-        for (int col = warp; col < ncols; col += kI4Warps) {
-            constexpr int kPer = D / 32;
-            const int tq = w.T == 1 ? 0 : (col0 + col) / p.g, hq = h * p.g + (col0 + col) - tq * p.g;
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + out_row(p, w, tq, hq) * D + lane * kPer);
-            float x[kPer];
-            uint32_t two[kPer / 2];
-            if constexpr (kPer == 4) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
-                two[0] = u.x, two[1] = u.y;
-            } else {
-                two[0] = __ldg(src);
+        // ---- its queries
+        const int buf = piece & 1;
+        if (piece == 0) {
+            for (int col = warp; col < ncols; col += kI4Warps) {
+                uint32_t two[D / 64];
+                load_query<D>(p, w, h, col0 + col, lane, two);
+                put_query<D, NT>(p, two, col, lane, s_q[0], s_scale[0]);
             }
-#pragma unroll
-            for (int i = 0; i < kPer / 2; ++i) {
-                const float2 f = p.q_bf16 ? bf16x2_to_float2(two[i]) : f16x2_to_float2(two[i]);
-                x[2 * i] = f.x, x[2 * i + 1] = f.y;
-            }
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) m = fmaxf(m, fabsf(x[i]));
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-            // exponent field of the largest; 0 (all zero or below normal) and 255 are left alone
-            const int e = (int)(__float_as_uint(m) >> 23);
-            const int up = e == 0 || e == 255 ? 0 : max(-126, min(126, 127 + 13 - e));
-            // the score's factor is made positive (its sign goes to q), so that scaling keeps
-            // the order of scores; a factor of 0 zeroes q instead
-            const float mul = copysignf(p.scale_log2 == 0.f ? 0.f : __uint_as_float((uint32_t)(127 + up) << 23), p.scale_log2);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                // dimension d: quarter cq, word wi, four bits n; pair n of half d / 4 % 2
-                const int d = lane * kPer + i, cq = d / (D / 4), in = d % (D / 4), wi = in / 8, n = in % 4, hi = in / 4 % 2;
-                const int pair = 4 * wi + n;
-                qs[((((pair >> 1) * NT + (col >> 3)) * 32 + (col & 7) * 4 + cq) * 2 + (pair & 1)) * 2 + hi] =
-                    __float2half_rn(x[i] * mul);
-            }
-            if (lane == 0)
-                s_scale[col] = p.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 - up) << 23), 1e-37f);
+            named_bar_sync(1, kI4Attend);
+        } else if (!stop) {
+            const bool bad = !mbar_wait<TW>(&s_qfull[buf], ((piece - !buf * 2) >> 1) & 1, p.err);
+            stop = __any_sync(0xffffffffu, bad);
+            if (stop && lane == 0) s_abort = 1;
         }
-        named_bar_sync(1, kI4Attend);
+        ++piece;
 
         // ---- state of columns 8 nt + 2 c and + 1 (maxima replicated over r)
-        float m_run[NT][2], l_run[NT][2], o[NT][kSteps][4], sc[NT][2];
+        // past: the raw score that renews the reference m_run; less: kI4Bias - m_run
+        float m_run[NT][2], l_run[NT][2], o[NT][kSteps][4], sc[NT][2], past[NT][2], less[NT][2];
         int lim[NT][2];  // keys that the column sees
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int col = 8 * nt + 2 * c + x;
-                m_run[nt][x] = -INFINITY;
-                l_run[nt][x] = 0.f;
-                sc[nt][x] = s_scale[col];
+                m_run[nt][x] = past[nt][x] = -INFINITY;
+                l_run[nt][x] = less[nt][x] = 0.f;
+                sc[nt][x] = s_scale[buf][col];
                 lim[nt][x] = w.L - w.T + (w.T == 1 ? 1 : min((col0 + col) / p.g, w.T - 1) + 1);
 #pragma unroll
                 for (int f = 0; f < kSteps; ++f) o[nt][f][x] = o[nt][f][2 + x] = 0.f;
@@ -558,7 +630,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                     for (int f = 0; f < 2; ++f)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const uint2 bq = s_q[((2 * wi + f) * NT + nt) * 32 + lane];
+                            const uint2 bq = s_q[buf][((2 * wi + f) * NT + nt) * 32 + lane];
 #pragma unroll
                             for (int n = 0; n < NB; ++n)
                                 mma_16816(s[n][nt], x0[n][2 * f], x1[n][2 * f], x0[n][2 * f + 1], x1[n][2 * f + 1], bq.x, bq.y);
@@ -602,8 +674,9 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                             if (t >= tokens(n) || tok0 + n * kI4BS + t >= lim[nt][x & 1]) s[n][nt][x] = -INFINITY;
                         }
             }
+            // a score past a column's limit renews its reference: looked at per lane, the
+            // maximum over lanes is taken only then
             bool renew = false;
-            float top[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -611,20 +684,24 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                     float m = fmaxf(s[0][nt][x], s[0][nt][2 + x]);
 #pragma unroll
                     for (int n = 1; n < NB; ++n) m = fmaxf(m, fmaxf(s[n][nt][x], s[n][nt][2 + x]));
-#pragma unroll
-                    for (int y = 4; y <= 16; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
-                    top[nt][x] = m * sc[nt][x];
-                    renew |= top[nt][x] > m_run[nt][x] + kI4Renew;
+                    renew |= m > past[nt][x];
                 }
             if (__any_sync(0xffffffffu, renew)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
+                        float m = fmaxf(s[0][nt][x], s[0][nt][2 + x]);
+#pragma unroll
+                        for (int n = 1; n < NB; ++n) m = fmaxf(m, fmaxf(s[n][nt][x], s[n][nt][2 + x]));
+#pragma unroll
+                        for (int y = 4; y <= 16; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
+                        m = fmaxf(m * sc[nt][x], m_run[nt][x]);
                         // 2^(old - new); an empty state has a reference of -inf
-                        const float m = top[nt][x] > m_run[nt][x] + kI4Renew ? top[nt][x] : m_run[nt][x];
                         const float a = m == m_run[nt][x] ? 1.f : ex2(m_run[nt][x] - m);
                         m_run[nt][x] = m;
+                        past[nt][x] = m == -INFINITY ? -INFINITY : (m + kI4Renew) / sc[nt][x];
+                        less[nt][x] = m == -INFINITY ? 0.f : kI4Bias - m;
                         l_run[nt][x] *= a;
 #pragma unroll
                         for (int f = 0; f < kSteps; ++f) {
@@ -635,12 +712,10 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float u0 = m_run[nt][0] == -INFINITY ? 0.f : kI4Bias - m_run[nt][0];
-                const float u1 = m_run[nt][1] == -INFINITY ? 0.f : kI4Bias - m_run[nt][1];
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    const float p0 = ex2(fmaf(s[n][nt][0], sc[nt][0], u0)), p1 = ex2(fmaf(s[n][nt][1], sc[nt][1], u1));
-                    const float p2 = ex2(fmaf(s[n][nt][2], sc[nt][0], u0)), p3 = ex2(fmaf(s[n][nt][3], sc[nt][1], u1));
+                    const float p0 = ex2(fmaf(s[n][nt][0], sc[nt][0], less[nt][0])), p1 = ex2(fmaf(s[n][nt][1], sc[nt][1], less[nt][1]));
+                    const float p2 = ex2(fmaf(s[n][nt][2], sc[nt][0], less[nt][0])), p3 = ex2(fmaf(s[n][nt][3], sc[nt][1], less[nt][1]));
                     l_run[nt][0] += p0 + p2;
                     l_run[nt][1] += p1 + p3;
                     const uint32_t h01 = float2_to_f16x2(p0, p1), h23 = float2_to_f16x2(p2, p3);
@@ -686,74 +761,76 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             }
         }
 
-        // ---- the warps' states to this piece's result, four columns at a time
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_qempty[buf]);
+
+        // ---- the warps' states to this piece's result, kMC columns at a time
         float4 *sm_o = reinterpret_cast<float4 *>(smem + kRing);  // [warp][column][D / 4], see `at`
         constexpr int kQ = D / 32;                                 // float4s of one lane's dims
         auto at = [&](int wp, int col, int rr, int i) {            // spread over the banks
-            return (wp * 4 + col) * (D / 4) + rr * kQ + (i ^ ((col >> 1) & (kQ - 1)) ^ (rr & (kQ - 1)));
+            return (wp * kMC + col) * (D / 4) + rr * kQ + (i ^ ((col >> 1) & (kQ - 1)) ^ (rr & (kQ - 1)));
         };
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float l0 = l_run[nt][0], l1 = l_run[nt][1];
+        for (int pass = 0; pass < kCols / kMC; ++pass) {
+            const int live = min(kMC, ncols - kMC * pass);
+            if (live <= 0) break;
+            named_bar_sync(1, kI4Attend);  // the previous piece or columns have been read
 #pragma unroll
-            for (int x = 4; x <= 16; x <<= 1) {
-                l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-                l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-            }
+            for (int nt = 0; nt < NT; ++nt) {
+                float l0 = l_run[nt][0], l1 = l_run[nt][1];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int live = min(4, ncols - 8 * nt - 4 * half);
-                if (live <= 0) break;
-                if (nt > 0 || half > 0) named_bar_sync(1, kI4Attend);  // the previous columns have been read
-                if ((c >> 1) == half) {
-                    const int c4 = 2 * (c & 1);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int i = 0; i < kQ; ++i)
-                            sm_o[at(warp, c4 + x, r, i)] = make_float4(o[nt][2 * i][x], o[nt][2 * i][2 + x],
-                                                                       o[nt][2 * i + 1][x], o[nt][2 * i + 1][2 + x]);
-                    if (r == 0) {
-                        // the weights are relative to m - kI4Bias
-                        s_m[warp * 4 + c4] = m_run[nt][0] - kI4Bias;
-                        s_m[warp * 4 + c4 + 1] = m_run[nt][1] - kI4Bias;
-                        s_l[warp * 4 + c4] = l0;
-                        s_l[warp * 4 + c4 + 1] = l1;
-                    }
+                for (int x = 4; x <= 16; x <<= 1) {
+                    l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+                    l1 += __shfl_xor_sync(0xffffffffu, l1, x);
                 }
-                named_bar_sync(1, kI4Attend);
-                if (tid < live * (D / 4)) {
-                    const int col = tid / (D / 4), d4 = tid % (D / 4);
-                    float M = s_m[col];
+                const int col = 8 * nt + 2 * c - kMC * pass;
+                if (col < 0 || col >= live) continue;  // (an odd last column brings a spare one)
 #pragma unroll
-                    for (int wp = 1; wp < kI4Warps; ++wp) M = fmaxf(M, s_m[wp * 4 + col]);
-                    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float den = 0.f;
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int wp = 0; wp < kI4Warps; ++wp) {
-                        const float lw = s_l[wp * 4 + col];
-                        const float f = lw == 0.f ? 0.f : ex2(s_m[wp * 4 + col] - M);  // 0: saw no key
-                        const float4 v = sm_o[at(wp, col, d4 / kQ, d4 % kQ)];
-                        num.x += f * v.x;
-                        num.y += f * v.y;
-                        num.z += f * v.z;
-                        num.w += f * v.w;
-                        den += f * lw;
-                    }
-                    const float inv = den != 0.f ? p.v_mul / den : 0.f;  // den NaN: NaN
-                    const int gc = col0 + 8 * nt + 4 * half + col, tq = w.T == 1 ? 0 : gc / p.g;
-                    const int hq = h * p.g + (gc - tq * p.g);
-                    const size_t orow = out_row(p, w, tq, hq);
-                    const float4 v = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-                    const float lse2 = den != 0.f ? M + log2f(den) : -INFINITY;
-                    if (nsplit == 1) {
-                        store_out4(p.out, orow * D + 4 * d4, v, p.out_type);
-                        if (p.lse && d4 == 0) p.lse[orow] = lse2 * 0.6931471805599453f;
-                    } else {
-                        const size_t slot = ws_row(p, w, tq, hq) * p.max_splits + split;
-                        reinterpret_cast<float4 *>(p.ws_o)[slot * (D / 4) + d4] = v;
-                        if (d4 == 0) p.ws_lse[slot] = lse2;
-                    }
+                    for (int i = 0; i < kQ; ++i)
+                        sm_o[at(warp, col + x, r, i)] = make_float4(o[nt][2 * i][x], o[nt][2 * i][2 + x],
+                                                                    o[nt][2 * i + 1][x], o[nt][2 * i + 1][2 + x]);
+                if (r == 0) {
+                    // the weights are relative to m - kI4Bias
+                    s_m[warp * kMC + col] = m_run[nt][0] - kI4Bias;
+                    s_m[warp * kMC + col + 1] = m_run[nt][1] - kI4Bias;
+                    s_l[warp * kMC + col] = l0;
+                    s_l[warp * kMC + col + 1] = l1;
+                }
+            }
+            named_bar_sync(1, kI4Attend);
+            for (int idx = tid; idx < live * (D / 4); idx += kI4Attend) {
+                const int col = idx / (D / 4), d4 = idx % (D / 4);
+                float M = s_m[col];
+#pragma unroll
+                for (int wp = 1; wp < kI4Warps; ++wp) M = fmaxf(M, s_m[wp * kMC + col]);
+                float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+                float den = 0.f;
+#pragma unroll
+                for (int wp = 0; wp < kI4Warps; ++wp) {
+                    const float lw = s_l[wp * kMC + col];
+                    const float f = lw == 0.f ? 0.f : ex2(s_m[wp * kMC + col] - M);  // 0: saw no key
+                    const float4 v = sm_o[at(wp, col, d4 / kQ, d4 % kQ)];
+                    num.x += f * v.x;
+                    num.y += f * v.y;
+                    num.z += f * v.z;
+                    num.w += f * v.w;
+                    den += f * lw;
+                }
+                const float inv = den != 0.f ? p.v_mul / den : 0.f;  // den NaN: NaN
+                const int gc = col0 + kMC * pass + col, tq = w.T == 1 ? 0 : gc / p.g;
+                const int hq = h * p.g + (gc - tq * p.g);
+                const size_t orow = out_row(p, w, tq, hq);
+                const float4 v = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+                const float lse2 = den != 0.f ? M + log2f(den) : -INFINITY;
+                if (nsplit == 1) {
+                    store_out4(p.out, orow * D + 4 * d4, v, p.out_type);
+                    if (p.lse && d4 == 0) p.lse[orow] = lse2 * kLn2;
+                } else {
+                    const size_t slot = ws_row(p, w, tq, hq) * p.max_splits + split;
+                    reinterpret_cast<float4 *>(p.ws_o)[slot * (D / 4) + d4] = v;
+                    if (d4 == 0) p.ws_lse[slot] = lse2;
                 }
             }
         }
@@ -763,49 +840,61 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             if (split == 0 && tid == 0) *counter = nsplit;
             continue;
         }
-        // ---- the last piece to finish merges them all
-        __threadfence();
-        named_bar_sync(1, kI4Attend);
-        if (tid == 0) s_last = atomicAdd(counter, 1) == nsplit - 1;
-        named_bar_sync(1, kI4Attend);
+        // ---- the last piece to finish merges them all: one warp does where that is
+        // little and the others have more of the run before them
+        named_bar_sync(1, kI4Attend);  // every thread's part is written
+        const bool alone = NT == 1 && todo > 0 && nsplit <= kI4AloneSplits;
+        if (alone && warp != kI4Warps - 1) continue;
+        if (alone ? lane == 0 : tid == 0) s_last = count_arrival(counter) == nsplit - 1;
+        if (alone)
+            __syncwarp();
+        else
+            named_bar_sync(1, kI4Attend);
         if (!s_last) continue;
-        __threadfence();
-        float *wt = reinterpret_cast<float *>(smem + kRing);  // [8 NT][kFuseMaxSplits]
-        for (int col = warp; col < ncols; col += kI4Warps) {
-            const int gc = col0 + col, tq = w.T == 1 ? 0 : gc / p.g;
-            const int hq = h * p.g + (gc - tq * p.g);
-            const size_t orow = out_row(p, w, tq, hq), wrow = ws_row(p, w, tq, hq);
-            const float x = lane < nsplit ? __ldcg(p.ws_lse + wrow * p.max_splits + lane) : -INFINITY;
-            float M = x;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-            const float e = x == -INFINITY ? 0.f : ex2(x - M);  // NaN stays
-            float den = e;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) den += __shfl_xor_sync(0xffffffffu, den, s);
-            wt[col * kFuseMaxSplits + lane] = den != 0.f ? e / den : 0.f;
-            if (p.lse && lane == 0) p.lse[orow] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
-        }
-        named_bar_sync(1, kI4Attend);
-        for (int idx = tid; idx < ncols * (D / 4); idx += kI4Attend) {
+        const int me = alone ? lane : tid, all = alone ? 32 : kI4Attend;
+        for (int idx = me; idx < ncols * (D / 4); idx += all) {
             const int col = idx / (D / 4), d4 = idx % (D / 4);
             const int gc = col0 + col, tq = w.T == 1 ? 0 : gc / p.g;
             const int hq = h * p.g + (gc - tq * p.g);
-            const size_t orow = out_row(p, w, tq, hq);
-            const float4 *src = reinterpret_cast<const float4 *>(p.ws_o) + ws_row(p, w, tq, hq) * p.max_splits * (D / 4) + d4;
+            const size_t orow = out_row(p, w, tq, hq), wrow = ws_row(p, w, tq, hq) * p.max_splits;
+            const float *ls = p.ws_lse + wrow;
+            const float4 *src = reinterpret_cast<const float4 *>(p.ws_o) + wrow * (D / 4) + d4;
+            // a running maximum over the pieces, kAhead loads at a time
+            constexpr int kAhead = 4;
+            float M = -INFINITY, den = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int s = 0; s < nsplit; ++s) {
-                const float f = wt[col * kFuseMaxSplits + s];
-                const float4 v = __ldcg(src + (size_t)s * (D / 4));
-                acc.x += f * v.x;
-                acc.y += f * v.y;
-                acc.z += f * v.z;
-                acc.w += f * v.w;
+            for (int s = 0; s < nsplit; s += kAhead) {
+                float x[kAhead];
+                float4 v[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int sk = min(s + k, nsplit - 1);
+                    x[k] = __ldcg(ls + sk);
+                    v[k] = __ldcg(src + (size_t)sk * (D / 4));
+                }
+                float top = M;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) top = fmaxf(top, x[k]);
+                if (top != -INFINITY) {
+                    const float a = ex2(M - top);  // of nothing: 0
+                    acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a, den *= a;
+                }
+                M = top;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const float e = s + k >= nsplit || x[k] == -INFINITY ? 0.f : ex2(x[k] - M);  // NaN stays
+                    acc.x += e * v[k].x;
+                    acc.y += e * v[k].y;
+                    acc.z += e * v[k].z;
+                    acc.w += e * v[k].w;
+                    den += e;
+                }
             }
-            store_out4(p.out, orow * D + 4 * d4, acc, p.out_type);
+            const float inv = den != 0.f ? 1.f / den : 0.f;
+            store_out4(p.out, orow * D + 4 * d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), p.out_type);
+            if (p.lse && d4 == 0) p.lse[orow] = den != 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
         }
-        if (tid == 0) *counter = 0;  // ready for the next call
+        if (me == 0) *counter = 0;  // ready for the next call
     }
 }
 
@@ -881,7 +970,7 @@ __global__ void __launch_bounds__(kI4MergeThreads) merge_i4_kernel(const I4Param
     }
     const float inv = den != 0.f ? 1.f / den : 0.f;
     store_out4(p.out, orow * D + 4 * d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), p.out_type);
-    if (p.lse && d4 == 0) p.lse[orow] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+    if (p.lse && d4 == 0) p.lse[orow] = den != 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
 }
 
 cudaError_t set_wait_limit_decode_i4(unsigned long long ns) { return set_wait_limit_here(ns); }
@@ -893,7 +982,7 @@ static kv_status launch_i4(I4Params &p, int part_blocks, cudaStream_t s) {
                           : decode_i4_kernel<D, NT, true, false, NB, NST, MINB>)
                     : (tw ? decode_i4_kernel<D, NT, false, true, NB, NST, MINB>
                           : decode_i4_kernel<D, NT, false, false, NB, NST, MINB>);
-    constexpr size_t smem = i4_smem_bytes<D, NB, NST>();
+    constexpr size_t smem = i4_smem_bytes<D, NT, NB, NST>();
     if (kv_status st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
         return st;
     p.round_blocks = NB * kI4Warps;
