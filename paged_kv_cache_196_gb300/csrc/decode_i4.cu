@@ -161,8 +161,9 @@ KV_DEVICE void load_words(const char *src, uint32_t (&w)[N]) {
     }
 }
 
-// Shared memory: the ring (a stage: a round's blocks), the merge's outputs ([warp][column][D], reused for the split merge's
-// weights), barriers and the stages' masks of missing blocks.
+// Shared memory asked for at launch: the ring (a stage: a round's blocks) and the
+// merge's outputs ([warp][column][D]).  With the kernel's own variables, two CTAs of
+// the D = 128 decode fill an SM's to the last hundred bytes.
 template <int D, int NB, int NST>
 constexpr size_t i4_ring_bytes() {
     return (size_t)NST * kI4Warps * NB * 2 * 9 * D;
@@ -176,7 +177,7 @@ constexpr size_t i4_merge_bytes() {
 }
 template <int D, int NT, int NB, int NST>
 constexpr size_t i4_smem_bytes() {
-    return i4_ring_bytes<D, NB, NST>() + i4_merge_bytes<D, NT>() + (size_t)NST * (2 * sizeof(uint64_t) + sizeof(int));
+    return i4_ring_bytes<D, NB, NST>() + i4_merge_bytes<D, NT>();
 }
 
 // A sequence: its query rows, keys, rounds, and the pairs it makes (0: left out).
@@ -185,10 +186,19 @@ struct I4Work {
     int L;
 };
 
+// A CTA's share of a pair, which the copying warp hands to the attending ones.
+struct I4Piece {
+    int b, q0, T, L;         // its sequence
+    int h, cg;               // kv head, column group
+    int round0, rounds;      // rounds: 0 ends the run
+    int split, nsplit;       // which of the pair's pieces
+    int more;                // the run goes on behind it
+};
+
 // Row of a query head in q and out, and in the workspace.
-KV_DEVICE size_t out_row(const I4Params &p, const I4Work &w, int tq, int hq) { return (size_t)(w.q0 + tq) * p.hq + hq; }
-KV_DEVICE size_t ws_row(const I4Params &p, const I4Work &w, int tq, int hq) {
-    return ((size_t)w.b * p.max_t + tq) * p.hq + hq;
+KV_DEVICE size_t out_row(const I4Params &p, int q0, int tq, int hq) { return (size_t)(q0 + tq) * p.hq + hq; }
+KV_DEVICE size_t ws_row(const I4Params &p, int b, int tq, int hq) {
+    return ((size_t)b * p.max_t + tq) * p.hq + hq;
 }
 
 // round_blocks: blocks of a round; cols: columns of a pair.
@@ -223,9 +233,9 @@ KV_DEVICE I4Work i4_sequence(const I4Params &p, int b, int round_blocks, int col
 
 // The D / 32 elements of column gc's query that this lane lays out.
 template <int D>
-KV_DEVICE void load_query(const I4Params &p, const I4Work &w, int h, int gc, int lane, uint32_t (&two)[D / 64]) {
-    const int tq = w.T == 1 ? 0 : gc / p.g;
-    const uint16_t *src = p.q + out_row(p, w, tq, h * p.g + gc - tq * p.g) * D + lane * (D / 32);
+KV_DEVICE void load_query(const I4Params &p, int q0, int T, int h, int gc, int lane, uint32_t (&two)[D / 64]) {
+    const int tq = T == 1 ? 0 : gc / p.g;
+    const uint16_t *src = p.q + out_row(p, q0, tq, h * p.g + gc - tq * p.g) * D + lane * (D / 32);
     if constexpr (D == 128) {
         const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
         two[0] = u.x, two[1] = u.y;
@@ -283,17 +293,17 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     extern __shared__ __align__(128) char smem[];
-    constexpr size_t kRing = i4_ring_bytes<D, NB, NST>(), kMerge = i4_merge_bytes<D, NT>();
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRing + kMerge), *empty = full + NST;
-    volatile int *missing = reinterpret_cast<int *>(empty + NST);  // bit i: block i of the round is not there
+    constexpr size_t kRing = i4_ring_bytes<D, NB, NST>();
+    __shared__ uint64_t full[NST], empty[NST];
+    __shared__ volatile int missing[NST];  // bit i: block i of the round is not there
     constexpr int kMC = i4_merge_cols(NT);
     __shared__ uint2 s_q[2][kSteps * NT * 32];  // fragments of two pieces' queries
     __shared__ float s_scale[2][8 * NT];
-    __shared__ uint64_t s_qfull[2], s_qempty[2];
+    __shared__ I4Piece s_piece[2];
+    __shared__ uint64_t s_qfull[2], s_qempty[2];  // of a piece's description and queries
     __shared__ float s_m[kI4Warps * kMC], s_l[kI4Warps * kMC];
     __shared__ int s_last;
-    // of the scan of the batch, over before the merges' are used (two CTAs fill the
-    // SM's shared memory to the last bytes)
+    // of the scan of the batch, over before the merges' are used
     int *s_scan = reinterpret_cast<int *>(s_m), *s_most = s_scan + kI4Warps + 1;
     int *s_start = reinterpret_cast<int *>(s_l);
     __shared__ volatile int s_abort;  // a wait ran out
@@ -394,6 +404,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             while (todo > 0) {
                 const int per = w.rounds + kI4PairCost;
                 if (unit >= w.pairs * per) {
+                    base += w.pairs * per;
                     w = i4_sequence(p, w.b + 1, kRound, kCols, false);
                     unit = 0;
                     continue;
@@ -406,6 +417,25 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             }
             return false;
         };
+        // The piece that begins at this place.
+        auto describe = [&]() {
+            I4Piece d{};
+            d.b = w.b, d.q0 = w.q0, d.T = w.T, d.L = w.L;
+            d.h = pair % p.hkv, d.cg = pair / p.hkv;
+            d.round0 = round;
+            d.rounds = min(w.rounds - round, todo);
+            d.more = todo > d.rounds;
+            if (p.balanced) {
+                const int v0 = base + pair * (w.rounds + kI4PairCost) + kI4PairCost;  // the pair's first round
+                const int c0 = v0 / run, c1 = (v0 + w.rounds - 1) / run;
+                d.nsplit = c1 - c0 + 1;
+                d.split = blockIdx.x - c0;
+            } else {
+                d.nsplit = (w.rounds + p.part_rounds - 1) / p.part_rounds;
+                d.split = blockIdx.x;
+            }
+            return d;
+        };
         int id_next = -1;      // table entry of this lane's next block
         bool in_next = false;  // that block is one of the sequence's
         auto entry = [&]() {
@@ -413,18 +443,22 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             in_next = lane < kRound && blk < w.nblk;
             if (in_next) id_next = __ldg(p.tables + (size_t)w.b * p.max_blocks + blk);
         };
-        // The queries of the second and later pieces (the attending warps lay out the
-        // first one's).  False if the buffer did not come free.
-        auto stage = [&](const I4Work &w, int pair, int piece) -> bool {
+        // Hands piece number `piece` over: its description and, but for the first one's
+        // (the attending warps lay that out), its queries.  False if the buffer did not
+        // come free.
+        auto hand = [&](const I4Piece &d, int piece) -> bool {
             constexpr int kAhead = 4;
-            const int buf = piece & 1, h = pair % p.hkv, col0 = pair / p.hkv * kCols;
-            const int ncols = min(kCols, w.T * p.g - col0);
-            const bool bad = lane == 0 && !mbar_wait<TW>(&s_qempty[buf], ((piece - !buf * 2) >> 1) & 1, p.err);
-            if (__shfl_sync(0xffffffffu, bad, 0)) return false;
-            for (int first = 0; first < ncols; first += kAhead) {
+            const int buf = piece & 1, col0 = d.cg * kCols, ncols = min(kCols, d.T * p.g - col0);
+            if (piece > 0) {
+                const bool bad = lane == 0 && !mbar_wait<TW>(&s_qempty[buf], ((piece - !buf * 2) >> 1) & 1, p.err);
+                if (__shfl_sync(0xffffffffu, bad, 0)) return false;
+            }
+            if (lane == 0) s_piece[buf] = d;
+            for (int first = 0; piece > 0 && d.rounds > 0 && first < ncols; first += kAhead) {
                 uint32_t two[kAhead][D / 64];
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) load_query<D>(p, w, h, col0 + min(first + k, ncols - 1), lane, two[k]);
+                for (int k = 0; k < kAhead; ++k)
+                    load_query<D>(p, d.q0, d.T, d.h, col0 + min(first + k, ncols - 1), lane, two[k]);
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k)
                     if (first + k < ncols) put_query<D, NT>(p, two[k], first + k, lane, s_q[buf], s_scale[buf]);
@@ -433,19 +467,23 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             if (lane == 0) mbar_arrive(&s_qfull[buf]);
             return true;
         };
-        bool more = place(), fresh = true;  // fresh: the round begins a piece
+        bool more = place(), starts = true;  // starts: the round begins a piece
         if (more) entry();
         int issued = 0, pieces = 0;
+        I4Piece d{};
+        if (more) {
+            d = describe();
+            hand(d, pieces++);
+        }
         while (more) {
-            const I4Work cw = w;
-            const int id = id_next, cpair = pair, h = pair % p.hkv, st = issued % NST;
-            const bool inside = in_next, starts = fresh;
+            const int id = id_next, h = d.h, st = issued % NST;
+            const bool inside = in_next;
             // the next round's entries are on their way while this round is copied
             ++unit;
             --todo;
             ++round;
-            fresh = round >= w.rounds;
-            more = fresh ? place() : todo > 0;
+            starts = round >= w.rounds;
+            more = starts ? place() : todo > 0;
             if (more) entry();
             bool bad = false;
             if (lane == 0) {
@@ -480,10 +518,17 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 }
             }
             ++issued;
-            if (starts && pieces++ > 0 && !stage(cw, cpair, pieces - 1)) {
-                if (lane == 0) s_abort = 1;
-                break;
+            if (more && starts) {
+                d = describe();
+                if (!hand(d, pieces++)) {
+                    if (lane == 0) s_abort = 1;
+                    break;
+                }
             }
+        }
+        if (!more) {  // the end of the run, as a piece of no rounds
+            d.rounds = 0;
+            if (!hand(d, pieces) && lane == 0) s_abort = 1;
         }
         // Never leave while a copy into this CTA's shared memory may be in flight.
         if (lane == 0)
@@ -500,7 +545,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
     named_bar_sync(1, kI4Attend);
     if (lane == 0) mbar_arrive(&s_qempty[1]);  // the second piece's buffer is free
 
-    int st = 0, piece = 0;
+    int st = 0;
     uint32_t parity = 0;
     bool stop = false;
     // Test instantiation with a limit of 0: a round that is not there at once is a
@@ -514,49 +559,25 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             }
         }
     }
-    I4Work w = i4_sequence(p, b0, kRound, kCols, false);
-    while (todo > 0) {
-        const int per = w.rounds + kI4PairCost;
-        if (unit >= w.pairs * per) {
-            base += w.pairs * per;
-            w = i4_sequence(p, w.b + 1, kRound, kCols, false);
-            unit = 0;
-            continue;
-        }
-        const int pair = unit / per, u0 = unit - pair * per;   // units u0 .. of the pair
-        const int units = min(todo, per - u0);
-        todo -= units;
-        unit += units;
-        const int round0 = max(u0 - kI4PairCost, 0), nrounds = u0 + units - kI4PairCost - round0;
-        if (nrounds <= 0) continue;  // the pair begins in this run, its rounds in the next
-        const int h = pair % p.hkv, cg = pair / p.hkv;
-        const int col0 = cg * kCols, ncols = min(kCols, w.T * p.g - col0);
-        // pieces of the pair, and which of them this is
-        int split, nsplit;
-        if (p.balanced) {
-            const int v0 = base + pair * per + kI4PairCost;  // number of the pair's first round
-            const int c0 = v0 / run, c1 = (v0 + w.rounds - 1) / run;
-            nsplit = c1 - c0 + 1;
-            split = blockIdx.x - c0;
-        } else {
-            nsplit = (w.rounds + p.part_rounds - 1) / p.part_rounds;
-            split = blockIdx.x;
-        }
-        // ---- its queries
+    for (int piece = 0;; ++piece) {
         const int buf = piece & 1;
+        if (!stop) stop = __any_sync(0xffffffffu, !mbar_wait<TW>(&s_qfull[buf], (piece >> 1) & 1, p.err));
+        if (stop && lane == 0) s_abort = 1;
+        // All warps go on or none; and the previous piece's results have been read.
+        if (named_bar_or(1, kI4Attend, stop)) break;
+        const volatile I4Piece &d = s_piece[buf];
+        const int nrounds = d.rounds;
+        if (nrounds == 0) break;
+        const int round0 = d.round0, L = d.L, T = d.T, col0 = d.cg * kCols, ncols = min(kCols, T * p.g - col0);
         if (piece == 0) {
+            const int q0 = d.q0, h = d.h;
             for (int col = warp; col < ncols; col += kI4Warps) {
                 uint32_t two[D / 64];
-                load_query<D>(p, w, h, col0 + col, lane, two);
+                load_query<D>(p, q0, T, h, col0 + col, lane, two);
                 put_query<D, NT>(p, two, col, lane, s_q[0], s_scale[0]);
             }
             named_bar_sync(1, kI4Attend);
-        } else if (!stop) {
-            const bool bad = !mbar_wait<TW>(&s_qfull[buf], ((piece - !buf * 2) >> 1) & 1, p.err);
-            stop = __any_sync(0xffffffffu, bad);
-            if (stop && lane == 0) s_abort = 1;
         }
-        ++piece;
 
         // ---- state of columns 8 nt + 2 c and + 1 (maxima replicated over r)
         // past: the raw score that renews the reference m_run; less: kI4Bias - m_run
@@ -570,11 +591,11 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 m_run[nt][x] = past[nt][x] = -INFINITY;
                 l_run[nt][x] = less[nt][x] = 0.f;
                 sc[nt][x] = s_scale[buf][col];
-                lim[nt][x] = w.L - w.T + (w.T == 1 ? 1 : min((col0 + col) / p.g, w.T - 1) + 1);
+                lim[nt][x] = L - T + (T == 1 ? 1 : min((col0 + col) / p.g, T - 1) + 1);
 #pragma unroll
                 for (int f = 0; f < kSteps; ++f) o[nt][f][x] = o[nt][f][2 + x] = 0.f;
             }
-        const int least = w.L - w.T + (w.T == 1 ? 0 : col0 / p.g) + 1;  // keys that every column sees
+        const int least = L - T + (T == 1 ? 0 : col0 / p.g) + 1;  // keys that every column sees
 
         for (int j = 0; j < nrounds && !stop; ++j) {
             const bool bad = !mbar_wait<TW>(&full[st], parity, p.err);
@@ -650,7 +671,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             }
             // tokens past the sequence, or in a block that is not there
             const int gone = missing[st] >> (NB * warp) & ((1 << NB) - 1);
-            const bool whole = !gone && tok0 + NB * kI4BS <= w.L;
+            const bool whole = !gone && tok0 + NB * kI4BS <= L;
             // the stage is in registers: its next round may come
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
@@ -658,7 +679,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 st = 0;
                 parity ^= 1;
             }
-            auto tokens = [&](int n) { return gone >> n & 1 ? 0 : min(kI4BS, w.L - (tok0 + n * kI4BS)); };
+            auto tokens = [&](int n) { return gone >> n & 1 ? 0 : min(kI4BS, L - (tok0 + n * kI4BS)); };
 
             // ---- softmax: s[0], s[1] token r, columns 2 c, 2 c + 1; s[2], s[3] token r + 8
             uint32_t ph[NB][NT][2], pl[NB][NT][2];
@@ -761,9 +782,9 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             }
         }
 
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_qempty[buf]);
-
+        // what the loop had no need of
+        const int b = d.b, q0 = d.q0, h = d.h, split = d.split, nsplit = d.nsplit;
+        const bool goes_on = d.more;
         // ---- the warps' states to this piece's result, kMC columns at a time
         float4 *sm_o = reinterpret_cast<float4 *>(smem + kRing);  // [warp][column][D / 4], see `at`
         constexpr int kQ = D / 32;                                 // float4s of one lane's dims
@@ -774,7 +795,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         for (int pass = 0; pass < kCols / kMC; ++pass) {
             const int live = min(kMC, ncols - kMC * pass);
             if (live <= 0) break;
-            named_bar_sync(1, kI4Attend);  // the previous piece or columns have been read
+            if (pass > 0) named_bar_sync(1, kI4Attend);  // the previous columns have been read
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float l0 = l_run[nt][0], l1 = l_run[nt][1];
@@ -819,23 +840,26 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                     den += f * lw;
                 }
                 const float inv = den != 0.f ? p.v_mul / den : 0.f;  // den NaN: NaN
-                const int gc = col0 + kMC * pass + col, tq = w.T == 1 ? 0 : gc / p.g;
+                const int gc = col0 + kMC * pass + col, tq = T == 1 ? 0 : gc / p.g;
                 const int hq = h * p.g + (gc - tq * p.g);
-                const size_t orow = out_row(p, w, tq, hq);
+                const size_t orow = out_row(p, q0, tq, hq);
                 const float4 v = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
                 const float lse2 = den != 0.f ? M + log2f(den) : -INFINITY;
                 if (nsplit == 1) {
                     store_out4(p.out, orow * D + 4 * d4, v, p.out_type);
                     if (p.lse && d4 == 0) p.lse[orow] = lse2 * kLn2;
                 } else {
-                    const size_t slot = ws_row(p, w, tq, hq) * p.max_splits + split;
+                    const size_t slot = ws_row(p, b, tq, hq) * p.max_splits + split;
                     reinterpret_cast<float4 *>(p.ws_o)[slot * (D / 4) + d4] = v;
                     if (d4 == 0) p.ws_lse[slot] = lse2;
                 }
             }
         }
+        // the description and the queries may be replaced
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_qempty[buf]);
         if (nsplit == 1 || !p.counters) continue;
-        int *counter = p.counters + ((size_t)w.b * p.col_groups + cg) * p.hkv + h;
+        int *counter = p.counters + ((size_t)b * p.col_groups + col0 / kCols) * p.hkv + h;
         if (nsplit > kFuseMaxSplits) {  // for merge_i4_kernel
             if (split == 0 && tid == 0) *counter = nsplit;
             continue;
@@ -843,7 +867,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         // ---- the last piece to finish merges them all: one warp does where that is
         // little and the others have more of the run before them
         named_bar_sync(1, kI4Attend);  // every thread's part is written
-        const bool alone = NT == 1 && todo > 0 && nsplit <= kI4AloneSplits;
+        const bool alone = NT == 1 && goes_on && nsplit <= kI4AloneSplits;
         if (alone && warp != kI4Warps - 1) continue;
         if (alone ? lane == 0 : tid == 0) s_last = count_arrival(counter) == nsplit - 1;
         if (alone)
@@ -854,9 +878,9 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         const int me = alone ? lane : tid, all = alone ? 32 : kI4Attend;
         for (int idx = me; idx < ncols * (D / 4); idx += all) {
             const int col = idx / (D / 4), d4 = idx % (D / 4);
-            const int gc = col0 + col, tq = w.T == 1 ? 0 : gc / p.g;
+            const int gc = col0 + col, tq = T == 1 ? 0 : gc / p.g;
             const int hq = h * p.g + (gc - tq * p.g);
-            const size_t orow = out_row(p, w, tq, hq), wrow = ws_row(p, w, tq, hq) * p.max_splits;
+            const size_t orow = out_row(p, q0, tq, hq), wrow = ws_row(p, b, tq, hq) * p.max_splits;
             const float *ls = p.ws_lse + wrow;
             const float4 *src = reinterpret_cast<const float4 *>(p.ws_o) + wrow * (D / 4) + d4;
             // a running maximum over the pieces, kAhead loads at a time
@@ -928,7 +952,7 @@ __global__ void __launch_bounds__(kI4MergeThreads) merge_i4_kernel(const I4Param
     }
     if (nsplit < 2) return;
     const int tid = threadIdx.x, d4 = tid % kLanes, grp = tid / kLanes;
-    const size_t orow = out_row(p, w, tq, hq), wrow = ws_row(p, w, tq, hq);
+    const size_t orow = out_row(p, w.q0, tq, hq), wrow = ws_row(p, w.b, tq, hq);
     const float *ls = p.ws_lse + wrow * p.max_splits;
     __shared__ float s_red[kI4MergeThreads / 32];
     __shared__ float4 s_acc[kI4MergeThreads];
