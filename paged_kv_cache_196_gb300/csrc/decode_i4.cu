@@ -28,8 +28,8 @@
 // per CTA of a single wave; every CTA finds its run from the lengths on the device
 // (a scan of the batch), so a captured graph stays balanced when the lengths change.
 // The copies run ahead across pair boundaries.  A pair cut by runs leaves a partial
-// result per CTA, which the last of them merges.  A pair counts kI4PairCost rounds
-// more than it has, for its queries and its end.
+// result per CTA, which the last of them merges.  A pair counts i4_pair_cost
+// rounds more than it has, for its queries and its end.
 //
 // Products.  S^T[16 tokens][8 columns] = K q^T and O^T[16 dims][8 columns] += V^T
 // P^T on mma.sync m16n8k16 with fp32 sums.  The contraction over dimensions may run
@@ -57,8 +57,10 @@ constexpr int kI4Attend = kI4Warps * 32;
 constexpr int kI4Threads = kI4Attend + 32;       // and the copying warp
 constexpr int kI4MergeThreads = 128;             // of merge_i4_kernel
 constexpr int kI4BS = 16;
-constexpr int kI4PairCost = 1;       // rounds
-constexpr int kI4AloneSplits = 4;    // pieces that one warp merges
+// Rounds that a pair costs besides its own (its queries and its end), for rounds of NB
+// blocks a warp.  Measured with 0, 1, 2, 3: decode of 64 sequences 48.4, 45.0, 46.1,
+// 47.6 us (NB = 2); five drafted tokens of 16 sequences 65.5, 60.7, 55.6, 55.2 us (NB = 1).
+constexpr int i4_pair_cost(int NB) { return NB > 1 ? 1 : 2; }
 constexpr int kI4MinRun = 2;         // shortest run: a pair's cost and a round
 constexpr int kI4ScanBatch = 4096;   // largest batch whose runs the device cuts
 // The weights are 2^(s - m + 6) for a reference m that is renewed (and the state
@@ -192,7 +194,6 @@ struct I4Piece {
     int h, cg;               // kv head, column group
     int round0, rounds;      // rounds: 0 ends the run
     int split, nsplit;       // which of the pair's pieces
-    int more;                // the run goes on behind it
 };
 
 // Row of a query head in q and out, and in the workspace.
@@ -289,6 +290,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
     constexpr int kRound = NB * kI4Warps;   // blocks of a round
     constexpr int kStage = kRound * 2 * kTile;
     constexpr int kCols = 8 * NT;
+    constexpr int kPairCost = i4_pair_cost(NB);
     static_assert(kRound <= 32, "a lane looks after one block of a round");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         for (int b = first; b < past; ++b) {
             const I4Work w = i4_sequence(p, b, kRound, kCols, blockIdx.x == 0);
             if (w.pairs) most = max(most, w.rounds);
-            sum += w.pairs * (w.rounds + kI4PairCost);
+            sum += w.pairs * (w.rounds + kPairCost);
         }
         int scan = sum;
 #pragma unroll
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         }
         // a pair of n rounds is cut into at most (n - 2) / run + 2 pieces
         run = max((total + (int)gridDim.x - 1) / (int)gridDim.x,
-                  p.max_splits > 1 ? (most + p.max_splits - 3) / (p.max_splits - 1) : most + kI4PairCost);
+                  p.max_splits > 1 ? (most + p.max_splits - 3) / (p.max_splits - 1) : most + kPairCost);
         run = max(run, kI4MinRun);
         const long long at64 = (long long)blockIdx.x * run;
         if (at64 >= total) return;
@@ -361,7 +363,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             int left = at - (scan - sum);
             for (int b = first; b < past; ++b) {
                 const I4Work w = i4_sequence(p, b, kRound, kCols, false);
-                const int n = w.pairs * (w.rounds + kI4PairCost);
+                const int n = w.pairs * (w.rounds + kPairCost);
                 if (left < n) {
                     s_start[0] = b, s_start[1] = left, s_start[2] = at - left;
                     break;
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         const int pair = cg * p.hkv + blockIdx.y, r0 = split * p.part_rounds;
         if (pair >= w.pairs || r0 >= w.rounds) return;
         base = 0;
-        unit = pair * (w.rounds + kI4PairCost) + kI4PairCost + r0;
+        unit = pair * (w.rounds + kPairCost) + kPairCost + r0;
         todo = min(p.part_rounds, w.rounds - r0);
     }
     __syncthreads();
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         // Moves to the next unit that is a round; false at the run's end.
         auto place = [&]() -> bool {
             while (todo > 0) {
-                const int per = w.rounds + kI4PairCost;
+                const int per = w.rounds + kPairCost;
                 if (unit >= w.pairs * per) {
                     base += w.pairs * per;
                     w = i4_sequence(p, w.b + 1, kRound, kCols, false);
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                     continue;
                 }
                 pair = unit / per;
-                round = unit - pair * per - kI4PairCost;
+                round = unit - pair * per - kPairCost;
                 if (round >= 0) return true;
                 ++unit;
                 --todo;
@@ -424,9 +426,8 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             d.h = pair % p.hkv, d.cg = pair / p.hkv;
             d.round0 = round;
             d.rounds = min(w.rounds - round, todo);
-            d.more = todo > d.rounds;
             if (p.balanced) {
-                const int v0 = base + pair * (w.rounds + kI4PairCost) + kI4PairCost;  // the pair's first round
+                const int v0 = base + pair * (w.rounds + kPairCost) + kPairCost;  // the pair's first round
                 const int c0 = v0 / run, c1 = (v0 + w.rounds - 1) / run;
                 d.nsplit = c1 - c0 + 1;
                 d.split = blockIdx.x - c0;
@@ -784,7 +785,6 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
 
         // what the loop had no need of
         const int b = d.b, q0 = d.q0, h = d.h, split = d.split, nsplit = d.nsplit;
-        const bool goes_on = d.more;
         // ---- the warps' states to this piece's result, kMC columns at a time
         float4 *sm_o = reinterpret_cast<float4 *>(smem + kRing);  // [warp][column][D / 4], see `at`
         constexpr int kQ = D / 32;                                 // float4s of one lane's dims
@@ -864,19 +864,12 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             if (split == 0 && tid == 0) *counter = nsplit;
             continue;
         }
-        // ---- the last piece to finish merges them all: one warp does where that is
-        // little and the others have more of the run before them
+        // ---- the last piece to finish merges them all
         named_bar_sync(1, kI4Attend);  // every thread's part is written
-        const bool alone = NT == 1 && goes_on && nsplit <= kI4AloneSplits;
-        if (alone && warp != kI4Warps - 1) continue;
-        if (alone ? lane == 0 : tid == 0) s_last = count_arrival(counter) == nsplit - 1;
-        if (alone)
-            __syncwarp();
-        else
-            named_bar_sync(1, kI4Attend);
+        if (tid == 0) s_last = count_arrival(counter) == nsplit - 1;
+        named_bar_sync(1, kI4Attend);
         if (!s_last) continue;
-        const int me = alone ? lane : tid, all = alone ? 32 : kI4Attend;
-        for (int idx = me; idx < ncols * (D / 4); idx += all) {
+        for (int idx = tid; idx < ncols * (D / 4); idx += kI4Attend) {
             const int col = idx / (D / 4), d4 = idx % (D / 4);
             const int gc = col0 + col, tq = T == 1 ? 0 : gc / p.g;
             const int hq = h * p.g + (gc - tq * p.g);
@@ -918,7 +911,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             store_out4(p.out, orow * D + 4 * d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), p.out_type);
             if (p.lse && d4 == 0) p.lse[orow] = den != 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
         }
-        if (me == 0) *counter = 0;  // ready for the next call
+        if (tid == 0) *counter = 0;  // ready for the next call
     }
 }
 
@@ -1013,7 +1006,7 @@ static kv_status launch_i4(I4Params &p, int part_blocks, cudaStream_t s) {
     p.cols = 8 * NT;
     p.part_rounds = (part_blocks + p.round_blocks - 1) / p.round_blocks;
     const long long pairs = (long long)p.batch * p.col_groups * p.hkv;
-    const long long units = pairs * (p.max_blocks / p.round_blocks + 1 + kI4PairCost);
+    const long long units = pairs * (p.max_blocks / p.round_blocks + 1 + i4_pair_cost(NB));
     p.balanced = p.max_splits > 1 && p.counters && p.batch <= kI4ScanBatch && units < (1 << 30);
     dim3 grid(p.max_splits, p.hkv, p.batch * p.col_groups);
     if (p.balanced) grid = dim3((unsigned)std::min<long long>((long long)MINB * sm_count(), units));
@@ -1098,7 +1091,7 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
     for (int b = 0; b < batch; ++b) {
         const long long L = std::min<long long>(std::max(host_seq_lens[b], 0), (long long)max_blocks * kI4BS);
         const long long n = std::max<long long>(1, (L + kRound * kI4BS - 1) / (kRound * kI4BS));
-        units += num_kv_heads * (n + kI4PairCost);
+        units += num_kv_heads * (n + i4_pair_cost(2));
         most = std::max(most, n);
     }
     const long long wave = 2LL * sm_count(), run = std::max<long long>(kI4MinRun, (units + wave - 1) / wave);
