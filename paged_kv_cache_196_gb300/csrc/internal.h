@@ -106,7 +106,8 @@ int sm_count();
 
 // tiled-TMA maps (tmap.cu): bf16 rows of 128 values, boxes 16 x 64, 128B swizzle
 bool encode_rows_map(CUtensorMap *m, void *base, long long rows);
-bool encode_q_map(CUtensorMap *m, const void *q, int rows, int hq);
+// queries [rows][hq][128]: boxes of box_rows rows x box_heads heads x 64 values
+bool encode_q_map(CUtensorMap *m, const void *q, int rows, int hq, int box_heads, int box_rows);
 kv_status pool_tensor_maps(kv_pool *p);
 
 // ---- decode (shared by the paged and contiguous paths) ----
@@ -178,7 +179,8 @@ struct DecodeArgs {
 struct PrefillCall {
     const void *q;
     kv_dtype q_dtype;  // KV_BF16 or KV_F16: q, K and a 16-bit out
-    bool v_f16;        // V is fp16 (else bf16, as q)
+    // a tile's rows: all heads of a group, and V in fp16 whatever q's type
+    bool packed;
     const CUtensorMap *map_k, *map_v;
     const int32_t *cu_q;
     int total_q, max_q_len;

@@ -50,6 +50,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -121,8 +122,10 @@ struct PfBars {
 };
 
 // F16: q and K are fp16 (else bf16).  VF16: V already is fp16, otherwise it is
-// bf16 and rewritten as fp16 in shared memory.
-template <bool TW, bool F16, bool VF16 = F16>
+// bf16 and rewritten as fp16 in shared memory.  PACK: a tile's 128 rows are 128 / g
+// query tokens of all g heads of a kv head (row = token * g + head) instead of 128
+// tokens of one head: a short chunk fills its tiles, and a tile ends at fewer keys.
+template <bool TW, bool F16, bool VF16 = F16, bool PACK = false>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
@@ -130,11 +133,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // chunk sees more keys, so the grid's last wave holds light CTAs.  The
     // sequences stay in order, so the CTAs running at one time share one
     // sequence's K/V in L2.
-    const int hq = blockIdx.x, qt = gridDim.y - 1 - blockIdx.y, b = blockIdx.z;
+    const int qt = gridDim.y - 1 - blockIdx.y, b = blockIdx.z;
+    const int tokens = PACK ? 128 / p.g : 128;       // query tokens of a tile
+    const int hq = PACK ? blockIdx.x * p.g : blockIdx.x;  // (first) query head
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q_begin = p.cu_q[b];
     const int T = p.cu_q[b + 1] - q_begin;
-    const int q0 = qt * kPfBM;
+    const int q0 = qt * (2 * tokens);
     if (q0 >= T) return;  // uniform: this sequence's chunk has no tile here
     long long L = p.seq_lens[b];
     const long long c = L - T;
@@ -143,7 +148,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         return;
     }
     const int h = hq / p.g;
-    const long long kv_end = c + min(q0 + kPfBM, T);  // keys any row of this CTA can see
+    const long long kv_end = c + min(q0 + 2 * tokens, T);  // keys any row of this CTA can see
     const int n = (int)((kv_end + kPfBN - 1) / kPfBN);
     const int nblk = (int)((L + 15) / 16);
 
@@ -258,12 +263,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (lane == 0) {
             tc::prefetch_tensormap(&tm_q);
             tc::prefetch_tensormap(&tm_k);
-            mbar_arrive_expect_tx(&bars->qfull, 2 * kPfTileBytes);
+            // (packed rows past tokens * g hold anything: no row reaches another one)
+            mbar_arrive_expect_tx(&bars->qfull, PACK ? 4 * tokens * p.g * 128 : 2 * kPfTileBytes);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                tc::tma_load_3d(sQ + x * kPfTileBytes, &tm_q, 0, hq, q_begin + q0 + 128 * x, &bars->qfull);
+                tc::tma_load_3d(sQ + x * kPfTileBytes, &tm_q, 0, hq, q_begin + q0 + tokens * x, &bars->qfull);
                 tc::tma_load_3d(sQ + x * kPfTileBytes + kPfHalfBytes, &tm_q, 64, hq,
-                                q_begin + q0 + 128 * x, &bars->qfull);
+                                q_begin + q0 + tokens * x, &bars->qfull);
             }
         }
         int issued = 0;
@@ -401,8 +407,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int x = warp >> 2;       // query tile
         const int r = tid & 127;       // query row within the tile = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const int qrow = q0 + 128 * x + r;
-        const bool row_valid = qrow < T;
+        const int at = PACK ? r / p.g : r;                 // token of the tile
+        const int head = PACK ? hq + r - at * p.g : hq;    // query head
+        const int qrow = q0 + tokens * x + at;
+        const bool row_valid = qrow < T && (!PACK || at < tokens);
         // Invalid rows (past the chunk) see every key; they are never stored.
         const long long qpos = row_valid ? c + qrow : L - 1;
         float m_used = -INFINITY, l_sum = 0.f;
@@ -513,7 +521,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (!ok) *abort_flag = 1;
         tc::fence_after_sync();
         const float inv = l_sum > 0.f ? p.v_mul / l_sum : 0.f;
-        const size_t orow = ((size_t)(q_begin + qrow) * p.num_q_heads + hq) * kPfD;
+        const size_t orow = ((size_t)(q_begin + qrow) * p.num_q_heads + head) * kPfD;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t v[32];
@@ -539,7 +547,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
         }
         if (row_valid && ok && p.lse)
-            p.lse[(size_t)(q_begin + qrow) * p.num_q_heads + hq] =
+            p.lse[(size_t)(q_begin + qrow) * p.num_q_heads + head] =
                 l_sum > 0.f ? (m_used + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
     }
     tc::fence_before_sync();
@@ -556,7 +564,9 @@ kv_status launch_prefill(const PrefillCall &a) {
     // The q map covers exactly total_q rows: a tile reaching past them reads
     // zeros, and rows past a chunk or past total_q are never stored.
     CUtensorMap tm_q;
-    if (!encode_q_map(&tm_q, a.q, a.total_q, a.num_q_heads)) return KV_ERR_CUDA;
+    const int g = a.num_q_heads / a.num_kv_heads;
+    if (!encode_q_map(&tm_q, a.q, a.total_q, a.num_q_heads, a.packed ? g : 1, a.packed ? 128 / g : 128))
+        return KV_ERR_CUDA;
     PrefillParams pp{};
     pp.cu_q = a.cu_q;
     pp.total_q = a.total_q;
@@ -566,26 +576,27 @@ kv_status launch_prefill(const PrefillCall &a) {
     pp.num_blocks = a.num_blocks;
     pp.num_q_heads = a.num_q_heads;
     pp.num_kv_heads = a.num_kv_heads;
-    pp.g = a.num_q_heads / a.num_kv_heads;
+    pp.g = g;
     pp.scale_log2 = a.scale * 1.4426950408889634f;
     pp.v_mul = a.v_mul;
     pp.out = a.out;
     pp.out_type = a.out_dtype;
     pp.lse = a.lse;
     pp.err = a.err;
-    const bool f16 = a.q_dtype == KV_F16, vf16 = a.v_f16;
-    auto fn = test_waits_enabled() ? (f16    ? prefill_kernel<true, true>
-                                      : vf16 ? prefill_kernel<true, false, true>
-                                             : prefill_kernel<true, false>)
-                                   : (f16    ? prefill_kernel<false, true>
-                                      : vf16 ? prefill_kernel<false, false, true>
-                                             : prefill_kernel<false, false>);
+    const bool f16 = a.q_dtype == KV_F16;
+    auto pick = [&](auto tw) {
+        constexpr bool TW = decltype(tw)::value;
+        if (a.packed) return f16 ? prefill_kernel<TW, true, true, true> : prefill_kernel<TW, false, true, true>;
+        return f16 ? prefill_kernel<TW, true> : prefill_kernel<TW, false>;
+    };
+    auto fn = test_waits_enabled() ? pick(std::true_type{}) : pick(std::false_type{});
     if (kv_status st0 = cuda_status(cudaFuncSetAttribute(
             fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kPfSmemBytes)))
         return st0;
-    const int q_tiles = (a.max_q_len + kPfBM - 1) / kPfBM;
+    const int span = a.packed ? 2 * (128 / g) : kPfBM;  // query tokens of a CTA
+    const int q_tiles = (a.max_q_len + span - 1) / span;
     if (q_tiles > 65535) return KV_ERR_UNSUPPORTED;
-    const dim3 grid(a.num_q_heads, q_tiles, a.batch);
+    const dim3 grid(a.packed ? a.num_kv_heads : a.num_q_heads, q_tiles, a.batch);
     fn<<<grid, kPfThreads, kPfSmemBytes, a.stream>>>(tm_q, *a.map_k, *a.map_v, pp);
     return cuda_status(cudaGetLastError());
 }
@@ -614,7 +625,6 @@ extern "C" kv_status paged_prefill_attention(kv_pool_t p, const void *q, const i
     PrefillCall a{};
     a.q = q;
     a.q_dtype = p->dtype;
-    a.v_f16 = p->dtype == KV_F16;
     a.map_k = &p->tmap_k;
     a.map_v = &p->tmap_v;
     a.cu_q = cu_q;

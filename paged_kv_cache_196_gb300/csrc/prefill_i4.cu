@@ -102,6 +102,7 @@ kv_status kv_prefill_i4_workspace_size(kv_pool_t p, int batch, int num_q_heads, 
     if (!p || !bytes || batch < 0 || num_q_heads <= 0 || max_blocks < 0 || max_q_len < 0) return KV_ERR_ARG;
     if (p->dtype != KV_I4 || p->head_dim != kExD) return KV_ERR_UNSUPPORTED;
     if (num_q_heads % p->num_kv_heads) return KV_ERR_ARG;
+    if (num_q_heads / p->num_kv_heads > 8) return KV_ERR_UNSUPPORTED;
     if ((long long)max_q_len * (num_q_heads / p->num_kv_heads) <= kFewColumns) {
         int pb, ms;
         split_plan(batch, p->num_kv_heads, max_blocks, 0, &pb, &ms);
@@ -122,6 +123,7 @@ kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtyp
         (out_dtype != KV_F32 && out_dtype != q_dtype))
         return KV_ERR_UNSUPPORTED;
     if (num_q_heads % p->num_kv_heads) return KV_ERR_ARG;
+    if (num_q_heads / p->num_kv_heads > 8) return KV_ERR_UNSUPPORTED;
     if (kv_status st = require_device(p->device)) return st;
     if (batch == 0 || max_q_len == 0 || total_q == 0) return KV_OK;
     if (!q || !cu_q || !block_tables || !seq_lens || !out) return KV_ERR_ARG;
@@ -168,7 +170,7 @@ kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtyp
     PrefillCall a{};
     a.q = q;
     a.q_dtype = q_dtype;
-    a.v_f16 = true;
+    a.packed = true;
     a.map_k = &map_k;
     a.map_v = &map_v;
     a.cu_q = cu_q;
