@@ -179,8 +179,10 @@ struct DecodeArgs {
 struct PrefillCall {
     const void *q;
     kv_dtype q_dtype;  // KV_BF16 or KV_F16: q, K and a 16-bit out
-    // a tile's rows: all heads of a group, and V in fp16 whatever q's type
+    // a tile's rows: all heads of a group, and V in fp16 whatever q's type; launched
+    // while the previous kernel (the expansion of the tiles) still runs
     bool packed;
+    const int32_t *order;  // device permutation of the batch (packed only), or null
     const CUtensorMap *map_k, *map_v;
     const int32_t *cu_q;
     int total_q, max_q_len;

@@ -95,6 +95,7 @@ KV_DEVICE constexpr uint32_t colO(int x) { return x ? 384u : 256u; }
 
 struct PrefillParams {
     const int32_t *cu_q;
+    const int32_t *order;  // PACK: the order in which the grid takes the sequences, or null
     int total_q;
     const int32_t *tables;
     const int32_t *seq_lens;
@@ -133,7 +134,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // chunk sees more keys, so the grid's last wave holds light CTAs.  The
     // sequences stay in order, so the CTAs running at one time share one
     // sequence's K/V in L2.
-    const int qt = gridDim.y - 1 - blockIdx.y, b = blockIdx.z;
+    const int qt = gridDim.y - 1 - blockIdx.y;
+    int b = blockIdx.z;
+    if constexpr (PACK) {
+        // Launched to overlap the expansion of the tiles, which writes all that is read
+        // from here on but q.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (p.order) b = p.order[b];
+    }
     const int tokens = PACK ? 128 / p.g : 128;       // query tokens of a tile
     const int hq = PACK ? blockIdx.x * p.g : blockIdx.x;  // (first) query head
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -569,6 +577,7 @@ kv_status launch_prefill(const PrefillCall &a) {
         return KV_ERR_CUDA;
     PrefillParams pp{};
     pp.cu_q = a.cu_q;
+    pp.order = a.order;
     pp.total_q = a.total_q;
     pp.tables = a.block_tables;
     pp.seq_lens = a.seq_lens;
@@ -597,6 +606,19 @@ kv_status launch_prefill(const PrefillCall &a) {
     const int q_tiles = (a.max_q_len + span - 1) / span;
     if (q_tiles > 65535) return KV_ERR_UNSUPPORTED;
     const dim3 grid(a.packed ? a.num_kv_heads : a.num_q_heads, q_tiles, a.batch);
+    if (a.packed) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(kPfThreads);
+        cfg.dynamicSmemBytes = kPfSmemBytes;
+        cfg.stream = a.stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cuda_status(cudaLaunchKernelEx(&cfg, fn, tm_q, *a.map_k, *a.map_v, pp));
+    }
     fn<<<grid, kPfThreads, kPfSmemBytes, a.stream>>>(tm_q, *a.map_k, *a.map_v, pp);
     return cuda_status(cudaGetLastError());
 }

@@ -38,15 +38,38 @@ KV_DEVICE uint32_t to_k_type(uint32_t h2) {
     return float2_to_bf16x2(f.x, f.y);  // exact
 }
 
+// Largest batch that is put in order; its work grows with the square.
+constexpr int kOrderBatch = 1024;
+
 // One warp expands the K and V tiles of one (sequence, block, kv head) and writes
-// the block's entry of the expanded tiles' table.
+// the block's entry of the expanded tiles' table.  The grid's last rows (blockIdx.x at
+// `order_at`, first head) rank the sequences, most keys first: a prefill whose longest
+// tiles start last ends with a few CTAs at work.
 template <bool BF16>
 __global__ void __launch_bounds__(256) expand_i4_kernel(const char *__restrict__ k_pool,
                                                         const char *__restrict__ v_pool,
                                                         const int32_t *__restrict__ tables,
                                                         const int32_t *__restrict__ seq_lens, int max_blocks,
                                                         int num_blocks, int hkv, int32_t *__restrict__ new_table,
-                                                        char *__restrict__ k_out, char *__restrict__ v_out) {
+                                                        char *__restrict__ k_out, char *__restrict__ v_out,
+                                                        int32_t *__restrict__ order, int order_at) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the prefill waits for this grid's end
+    if ((int)blockIdx.x == order_at) {
+        if (blockIdx.y) return;
+        const int mine = seq_lens[blockIdx.z];
+        int before = 0;
+        for (int o = threadIdx.x; o < (int)gridDim.z; o += blockDim.x) {
+            const int L = seq_lens[o];
+            before += L > mine || (L == mine && o < (int)blockIdx.z);
+        }
+        __shared__ int s_before;
+        if (threadIdx.x == 0) s_before = 0;
+        __syncthreads();
+        atomicAdd(&s_before, before);
+        __syncthreads();
+        if (threadIdx.x == 0) order[s_before] = blockIdx.z;
+        return;
+    }
     const int lane = threadIdx.x & 31;
     const int b = blockIdx.z, h = blockIdx.y, i = blockIdx.x * 8 + (threadIdx.x >> 5);
     const long long L = seq_lens[b];
@@ -86,9 +109,9 @@ __global__ void __launch_bounds__(256) expand_i4_kernel(const char *__restrict__
     }
 }
 
-// Workspace of the expanding path: table, K tiles, V tiles.
+// Workspace of the expanding path: order of the batch and table, K tiles, V tiles.
 static size_t expand_table_bytes(int batch, int max_blocks) {
-    return ((size_t)batch * max_blocks * sizeof(int32_t) + 1023) / 1024 * 1024;
+    return ((size_t)batch * (max_blocks + 1) * sizeof(int32_t) + 1023) / 1024 * 1024;
 }
 
 }  // namespace pkv
@@ -157,20 +180,24 @@ kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtyp
     }
     const long long rows = (long long)batch * max_blocks * p->num_kv_heads * 16;
     if (rows > INT32_MAX || p->num_kv_heads > 65535) return KV_ERR_UNSUPPORTED;
-    int32_t *table = static_cast<int32_t *>(workspace);
+    int32_t *order = static_cast<int32_t *>(workspace), *table = order + batch;
     char *k_tiles = static_cast<char *>(workspace) + expand_table_bytes(batch, max_blocks);
     char *v_tiles = k_tiles + (size_t)batch * max_blocks * p->num_kv_heads * kExOut;
     CUtensorMap map_k, map_v;
     if (!encode_rows_map(&map_k, k_tiles, rows) || !encode_rows_map(&map_v, v_tiles, rows)) return KV_ERR_CUDA;
-    const dim3 grid((max_blocks + 7) / 8, p->num_kv_heads, batch);
+    const bool ordered = batch > 1 && batch <= kOrderBatch;
+    const int columns = (max_blocks + 7) / 8;
+    const dim3 grid(columns + ordered, p->num_kv_heads, batch);
     auto fn = q_dtype == KV_BF16 ? expand_i4_kernel<true> : expand_i4_kernel<false>;
     fn<<<grid, 256, 0, as_stream(stream)>>>((const char *)p->k, (const char *)p->v, block_tables, seq_lens, max_blocks,
-                                            p->num_blocks, p->num_kv_heads, table, k_tiles, v_tiles);
+                                            p->num_blocks, p->num_kv_heads, table, k_tiles, v_tiles, order,
+                                            ordered ? columns : -1);
     if (kv_status st = cuda_status(cudaGetLastError())) return st;
     PrefillCall a{};
     a.q = q;
     a.q_dtype = q_dtype;
     a.packed = true;
+    a.order = ordered ? order : nullptr;
     a.map_k = &map_k;
     a.map_v = &map_v;
     a.cu_q = cu_q;
