@@ -11,8 +11,8 @@
 // (i4::values8: 9 instructions for 8 codes), the layout of a tile puts each
 // lane's operands of the tensor core's fragments into consecutive bytes (no
 // ldmatrix, no shuffles), the scales of a lane's rows are two bytes a load, a
-// warp takes NB blocks at a time, so that waiting, the maximum over lanes and the
-// test for a new maximum are paid once per NB blocks, and a warp of its own does
+// warp takes two blocks (NB) at a time, so that waiting, the maximum over lanes and the
+// test for a new maximum are paid once per pair of blocks, and a warp of its own does
 // all that copying needs.
 //
 // Shape.  A pair is one (sequence, kv head) with up to 8 NT of its query columns
@@ -57,10 +57,13 @@ constexpr int kI4Attend = kI4Warps * 32;
 constexpr int kI4Threads = kI4Attend + 32;       // and the copying warp
 constexpr int kI4MergeThreads = 128;             // of merge_i4_kernel
 constexpr int kI4BS = 16;
-// Rounds that a pair costs besides its own (its queries and its end), for rounds of NB
-// blocks a warp.  Measured with 0, 1, 2, 3: decode of 64 sequences 48.4, 45.0, 46.1,
-// 47.6 us (NB = 2); five drafted tokens of 16 sequences 65.5, 60.7, 55.6, 55.2 us (NB = 1).
-constexpr int i4_pair_cost(int NB) { return NB > 1 ? 1 : 2; }
+constexpr int NB = 2;                 // blocks of a warp's share of a round
+constexpr int kI4Round = NB * kI4Warps;  // blocks of a round
+// Rounds that a pair costs besides its own (its queries and its end), for 8 NT columns.
+// Measured with 0, 1, 2, 3: decode of 64 sequences 48.4, 45.0, 46.1, 47.6 us (NT = 1);
+// with 1 .. 5 and 7: five drafted tokens of 16 sequences 51.8, 46.9, 44.2, 43.2, 43.6,
+// 46.0 us (NT = 3).
+constexpr int i4_pair_cost(int NT) { return NT == 1 ? 1 : 4; }
 constexpr int kI4MinRun = 2;         // shortest run: a pair's cost and a round
 constexpr int kI4ScanBatch = 4096;   // largest batch whose runs the device cuts
 // The weights are 2^(s - m + 6) for a reference m that is renewed (and the state
@@ -85,7 +88,7 @@ struct I4Params {
     // (split, kv head, (sequence, column group)) takes part_rounds rounds.
     int balanced;
     int part_rounds, max_splits;
-    int round_blocks, cols; // blocks of a round, columns of a pair (the kernel's own)
+    int cols;               // columns of a pair (the kernel's own)
     int col_groups;         // pairs that share a sequence's columns of one kv head
     void *out;
     int out_type;
@@ -166,9 +169,9 @@ KV_DEVICE void load_words(const char *src, uint32_t (&w)[N]) {
 // Shared memory asked for at launch: the ring (a stage: a round's blocks) and the
 // merge's outputs ([warp][column][D]).  With the kernel's own variables, two CTAs of
 // the D = 128 decode fill an SM's to the last hundred bytes.
-template <int D, int NB, int NST>
+template <int D, int NST>
 constexpr size_t i4_ring_bytes() {
-    return (size_t)NST * kI4Warps * NB * 2 * 9 * D;
+    return (size_t)NST * kI4Round * 2 * 9 * D;
 }
 // Columns that are merged at once: with one tile of eight the shared memory of a second
 // CTA per SM leaves room for four.
@@ -177,9 +180,9 @@ template <int D, int NT>
 constexpr size_t i4_merge_bytes() {
     return (size_t)kI4Warps * i4_merge_cols(NT) * D * 4;
 }
-template <int D, int NT, int NB, int NST>
+template <int D, int NT, int NST>
 constexpr size_t i4_smem_bytes() {
-    return i4_ring_bytes<D, NB, NST>() + i4_merge_bytes<D, NT>();
+    return i4_ring_bytes<D, NST>() + i4_merge_bytes<D, NT>();
 }
 
 // A sequence: its query rows, keys, rounds, and the pairs it makes (0: left out).
@@ -280,22 +283,22 @@ KV_DEVICE void put_query(const I4Params &p, const uint32_t (&two)[D / 64], int c
 }
 
 // D: head dim.  NT: columns / 8 of a CTA.  EXACT: weights in two fp16 parts (fp32
-// output).  TW: waits read their limit at run time (tests).  NB: blocks of a warp's
-// share of a round; NST: ring stages; MINB: CTAs per SM it is built for.
-template <int D, int NT, bool EXACT, bool TW, int NB, int NST, int MINB>
+// output).  TW: waits read their limit at run time (tests).  NST: ring stages; MINB:
+// CTAs per SM it is built for.
+template <int D, int NT, bool EXACT, bool TW, int NST, int MINB>
 __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Params p) {
     constexpr int kTile = 9 * D;
     constexpr int kW = D / 32;        // words of a quarter row of K, of a lane's dims of a V pair
     constexpr int kSteps = D / 16;    // products along D
-    constexpr int kRound = NB * kI4Warps;   // blocks of a round
+    constexpr int kRound = kI4Round;
     constexpr int kStage = kRound * 2 * kTile;
     constexpr int kCols = 8 * NT;
-    constexpr int kPairCost = i4_pair_cost(NB);
+    constexpr int kPairCost = i4_pair_cost(NT);
     static_assert(kRound <= 32, "a lane looks after one block of a round");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     extern __shared__ __align__(128) char smem[];
-    constexpr size_t kRing = i4_ring_bytes<D, NB, NST>();
+    constexpr size_t kRing = i4_ring_bytes<D, NST>();
     __shared__ uint64_t full[NST], empty[NST];
     __shared__ volatile int missing[NST];  // bit i: block i of the round is not there
     constexpr int kMC = i4_merge_cols(NT);
@@ -921,7 +924,7 @@ template <int D>
 __global__ void __launch_bounds__(kI4MergeThreads) merge_i4_kernel(const I4Params p) {
     constexpr int kLanes = D / 4, kGroups = kI4MergeThreads / kLanes;
     const int tq = blockIdx.x / p.hq, hq = blockIdx.x % p.hq;
-    const I4Work w = i4_sequence(p, blockIdx.y, p.round_blocks, p.cols, false);
+    const I4Work w = i4_sequence(p, blockIdx.y, kI4Round, p.cols, false);
     if (!w.pairs || tq >= w.T) return;
     const int gc = tq * p.g + hq % p.g;  // its column
     int nsplit;
@@ -992,21 +995,20 @@ __global__ void __launch_bounds__(kI4MergeThreads) merge_i4_kernel(const I4Param
 
 cudaError_t set_wait_limit_decode_i4(unsigned long long ns) { return set_wait_limit_here(ns); }
 
-template <int D, int NT, int NB, int NST, int MINB>
+template <int D, int NT, int NST, int MINB>
 static kv_status launch_i4(I4Params &p, int part_blocks, cudaStream_t s) {
     const bool exact = p.out_type == KV_F32, tw = test_waits_enabled();
-    auto fn = exact ? (tw ? decode_i4_kernel<D, NT, true, true, NB, NST, MINB>
-                          : decode_i4_kernel<D, NT, true, false, NB, NST, MINB>)
-                    : (tw ? decode_i4_kernel<D, NT, false, true, NB, NST, MINB>
-                          : decode_i4_kernel<D, NT, false, false, NB, NST, MINB>);
-    constexpr size_t smem = i4_smem_bytes<D, NT, NB, NST>();
+    auto fn = exact ? (tw ? decode_i4_kernel<D, NT, true, true, NST, MINB>
+                          : decode_i4_kernel<D, NT, true, false, NST, MINB>)
+                    : (tw ? decode_i4_kernel<D, NT, false, true, NST, MINB>
+                          : decode_i4_kernel<D, NT, false, false, NST, MINB>);
+    constexpr size_t smem = i4_smem_bytes<D, NT, NST>();
     if (kv_status st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
         return st;
-    p.round_blocks = NB * kI4Warps;
     p.cols = 8 * NT;
-    p.part_rounds = (part_blocks + p.round_blocks - 1) / p.round_blocks;
+    p.part_rounds = (part_blocks + kI4Round - 1) / kI4Round;
     const long long pairs = (long long)p.batch * p.col_groups * p.hkv;
-    const long long units = pairs * (p.max_blocks / p.round_blocks + 1 + i4_pair_cost(NB));
+    const long long units = pairs * (p.max_blocks / kI4Round + 1 + i4_pair_cost(NT));
     p.balanced = p.max_splits > 1 && p.counters && p.batch <= kI4ScanBatch && units < (1 << 30);
     dim3 grid(p.max_splits, p.hkv, p.batch * p.col_groups);
     if (p.balanced) grid = dim3((unsigned)std::min<long long>((long long)MINB * sm_count(), units));
@@ -1058,11 +1060,11 @@ kv_status attend_i4(const I4Call &a) {
     p.err = pool->err;
     kv_status st;
     if (pool->head_dim == 64)
-        st = nt == 1 ? launch_i4<64, 1, 2, 4, 2>(p, pb, a.stream) : KV_ERR_UNSUPPORTED;
+        st = nt == 1 ? launch_i4<64, 1, 4, 2>(p, pb, a.stream) : KV_ERR_UNSUPPORTED;
     else
-        st = nt == 1   ? launch_i4<128, 1, 2, 3, 2>(p, pb, a.stream)
-             : nt == 2 ? launch_i4<128, 2, 1, 6, 1>(p, pb, a.stream)
-                       : launch_i4<128, 3, 1, 6, 1>(p, pb, a.stream);
+        st = nt == 1   ? launch_i4<128, 1, 3, 2>(p, pb, a.stream)
+             : nt == 2 ? launch_i4<128, 2, 3, 1>(p, pb, a.stream)
+                       : launch_i4<128, 3, 3, 1>(p, pb, a.stream);
     if (st != KV_OK || ms < (counted ? kFuseMaxSplits + 1 : 2)) return st;
     const dim3 mgrid(a.num_q_heads * a.max_q_len, a.batch);
     if (pool->head_dim == 64)
@@ -1086,12 +1088,11 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
     if (batch == 0 || max_blocks == 0) return KV_OK;
     // The pieces that the longest pair is cut into by equal runs of one wave (the
     // kernel's own arithmetic: rounds of 14 blocks, two CTAs per SM).
-    constexpr int kRound = 2 * kI4Warps;
     long long units = 0, most = 1;
     for (int b = 0; b < batch; ++b) {
         const long long L = std::min<long long>(std::max(host_seq_lens[b], 0), (long long)max_blocks * kI4BS);
-        const long long n = std::max<long long>(1, (L + kRound * kI4BS - 1) / (kRound * kI4BS));
-        units += num_kv_heads * (n + i4_pair_cost(2));
+        const long long n = std::max<long long>(1, (L + kI4Round * kI4BS - 1) / (kI4Round * kI4BS));
+        units += num_kv_heads * (n + i4_pair_cost(1));
         most = std::max(most, n);
     }
     const long long wave = 2LL * sm_count(), run = std::max<long long>(kI4MinRun, (units + wave - 1) / wave);
