@@ -28,8 +28,18 @@ namespace pkv {
 constexpr int kExD = 128;            // head dim of the tcgen05 prefill
 constexpr int kExTile = 9 * kExD;    // bytes of a 4-bit tile
 constexpr int kExOut = 16 * kExD * 2;  // of an expanded one
-// Query columns (tokens x heads of a group) up to which the decode kernel runs.
-constexpr int kFewColumns = 32;
+
+// Whether the decode kernel with a column per (query token, head) runs instead.  It
+// turns the cache's codes into operands once per 16 columns and cuts each sequence
+// over the whole GPU; the expanding path does so once, writes and reads 16-bit tiles,
+// and has a CTA per (kv head, 256 rows).  Measured with 8 kv heads, 4 query heads each,
+// columns against expanding: 16 sequences of 1000 to 8000 tokens 88 / 164 us at 48
+// columns, 114 / 165 at 64, 167 / 165 at 96; 2 sequences of 500 to 2000 tokens 19 / 35 at
+// 96; 64 sequences of 200 to 1500 tokens (512 pairs of sequence and kv head, several for
+// every SM) 88 / 112 at 32, 127 / 112 at 48.
+static bool few_columns(int batch, int hkv, int max_q_len, int g) {
+    return (long long)max_q_len * g <= ((long long)batch * hkv < 2LL * sm_count() ? 96 : 32);
+}
 
 template <bool BF16>
 KV_DEVICE uint32_t to_k_type(uint32_t h2) {
@@ -126,7 +136,7 @@ kv_status kv_prefill_i4_workspace_size(kv_pool_t p, int batch, int num_q_heads, 
     if (p->dtype != KV_I4 || p->head_dim != kExD) return KV_ERR_UNSUPPORTED;
     if (num_q_heads % p->num_kv_heads) return KV_ERR_ARG;
     if (num_q_heads / p->num_kv_heads > 8) return KV_ERR_UNSUPPORTED;
-    if ((long long)max_q_len * (num_q_heads / p->num_kv_heads) <= kFewColumns) {
+    if (few_columns(batch, p->num_kv_heads, max_q_len, num_q_heads / p->num_kv_heads)) {
         int pb, ms;
         split_plan(batch, p->num_kv_heads, max_blocks, 0, &pb, &ms);
         *bytes = decode_workspace_bytes(batch * max_q_len, num_q_heads, kExD, ms);
@@ -156,7 +166,7 @@ kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtyp
     size_t need = 0;
     if (kv_status st = kv_prefill_i4_workspace_size(p, batch, num_q_heads, max_blocks, max_q_len, &need)) return st;
     if (need > 0 && (!workspace || workspace_bytes < need)) return KV_ERR_ARG;
-    if ((long long)max_q_len * (num_q_heads / p->num_kv_heads) <= kFewColumns) {
+    if (few_columns(batch, p->num_kv_heads, max_q_len, num_q_heads / p->num_kv_heads)) {
         I4Call a{};
         a.pool = p;
         a.q = q;

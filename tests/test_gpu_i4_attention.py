@@ -200,6 +200,7 @@ def check_prefill(c, q, out, lse, cu, out_type, what=""):
     ([200, 33], [8, 4]),
     ([300, 129, 45], [50, 129, 33]),           # expanded tiles, one chunk that starts its sequence
     ([400], [300]),
+    ([40, 300, 97], [20, 11, 1]),              # between the two: by columns, or expanded
 ])
 def test_prefill(q_dtype, out_type, g, hkv, lens, chunks):
     c = Cache(lens, hkv, 128, seed=sum(lens) + g)
@@ -211,7 +212,7 @@ def test_prefill(q_dtype, out_type, g, hkv, lens, chunks):
     c.close()
 
 
-@pytest.mark.parametrize("columns", [8, 9, 16, 17, 24, 32])
+@pytest.mark.parametrize("columns", [8, 9, 16, 17, 24, 32, 48, 96])
 def test_prefill_few_columns_long_context(columns):
     """Each width of the column form, cut into partitions that are merged."""
     c = Cache([6000, 700, 16 * 40], 1, 128, seed=columns)
@@ -222,12 +223,12 @@ def test_prefill_few_columns_long_context(columns):
     out, lse = c.prefill(q, "bf16", "bf16", cu, T)
     check_prefill(c, q, out, lse, cu, "bf16")
     # the same rows through the expanding path: equal within the two forms' bounds
-    out2, _ = c.prefill(q, "bf16", "f32", cu, 64)
+    out2, _ = c.prefill(q, "bf16", "f32", cu, 97)
     check_prefill(c, q, out2, lse, cu, "f32")
     c.close()
 
 
-@pytest.mark.parametrize("T", [4, 40])
+@pytest.mark.parametrize("T", [4, 40, 60])
 def test_prefill_flags_bad_blocks_and_lengths(T):
     c = Cache([100, 90], 2, 128, seed=9)
     q = c.queries(2 * T, 4, "bf16")
@@ -265,7 +266,7 @@ def test_refusals():
                          (-3, dec(B=70000))):
         refused(status, *case[0], **case[1])
 
-    def pre(pool=c.pool, q=t, qt=pk.KV_BF16, cu=i, rows=1, most=40, tab=i, mb=3, lens=i, B=1, hq=4, out=t, ot=pk.KV_F32, ws=t, n=1 << 16):
+    def pre(pool=c.pool, q=t, qt=pk.KV_BF16, cu=i, rows=1, most=400, tab=i, mb=3, lens=i, B=1, hq=4, out=t, ot=pk.KV_F32, ws=t, n=1 << 16):
         return pk.paged_prefill_attention_i4, pool, q, qt, cu, rows, most, tab, mb, lens, B, hq, 1.0, out, ot, None, ws, n
 
     for status, case in ((-3, pre(pool=bf)), (-3, pre(pool=d64.pool)), (-3, pre(qt=pk.KV_F32)), (-3, pre(ot=pk.KV_F16)),
