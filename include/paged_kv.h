@@ -310,7 +310,9 @@ kv_status kv_append(kv_pool_t p, const void *k_new, const void *v_new,
  *                 from t * q_stride / q_out_stride on (0 = packed), or NULL for
  *                 none.  q_out may be q itself (same stride; 0 takes q's).
  * Rotated in fp32 (two products and a sum, each rounded) and rounded once; what
- * is not rotated is moved bit by bit.  Addresses and strides: multiples of 16
+ * is not rotated is moved bit by bit.  With kv_pool_set_launch_overlap on, a call
+ * that writes q_out keeps the next launch from overlapping it (a decode would read
+ * q_out early).  Addresses and strides: multiples of 16
  * bytes.  KV_ERR_ARG for a wrong size, stride, alignment, type or NULL pointer,
  * KV_ERR_UNSUPPORTED for an in_dtype that no pool takes. */
 kv_status kv_append_rope(kv_pool_t p, const void *k_new, const void *v_new, kv_dtype in_dtype,
@@ -377,17 +379,26 @@ kv_status kv_swap_bytes(kv_pool_t p, int n, size_t *bytes);
 kv_status kv_pool_set_i4_scales(kv_pool_t p, float k_scale, float v_scale);
 
 /* num_splits for paged_decode_attention_i4 from the host-known lengths, as
- * kv_decode_plan chooses it for 16-bit pools. */
+ * kv_decode_plan chooses it for 16-bit pools: the pieces into which the longest
+ * sequence is cut when the work of the batch is spread evenly over one wave of CTAs. */
 kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_heads,
                             int max_blocks, int *num_splits);
 
 /* paged_decode_attention over a KV_I4 pool.  q is of type q_dtype (KV_BF16 or
- * KV_F16), out of q_dtype or KV_F32; seq_order as in paged_append_and_decode or
- * NULL; the workspace is kv_decode_workspace_size bytes for the same num_splits.
+ * KV_F16), out of q_dtype or KV_F32, both 16-byte aligned; seq_order as in
+ * paged_append_and_decode or NULL; the workspace is kv_decode_workspace_size bytes
+ * for the same num_splits (16-byte aligned).  With num_splits = 1 every (sequence, kv
+ * head) is one CTA's.  Otherwise, for batches up to 4096 with at most 65536 (sequence,
+ * kv head) pairs, the kernel itself cuts the batch into equal runs of 224 tokens from
+ * the lengths on the device, a sequence into no more pieces than kv_decode_split_plan
+ * gives for num_splits (seq_order has no part in it); larger ones are cut as that plan
+ * says.  So results depend, within rounding, on the batch's lengths; they do not depend
+ * on where the blocks sit, and are the same from call to call.
  * K and V enter the tensor cores exactly (fp16 holds every c * s); q enters in
  * fp16, scaled per head by a power of two (exact but for elements below 2^-27 of
  * the head's largest); the softmax weights in fp16, with KV_F32 output in two fp16
- * parts (about 22 bits). */
+ * parts (about 22 bits).  Attention calls (decode and prefill) over one KV_I4 pool
+ * must not run concurrently on the GPU: order them on one stream. */
 kv_status paged_decode_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype,
                                     const int32_t *block_tables, int max_blocks,
                                     const int32_t *seq_lens, const int32_t *seq_order, int batch,
@@ -396,10 +407,13 @@ kv_status paged_decode_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype
                                     size_t workspace_bytes, void *stream);
 
 /* paged_prefill_attention over a KV_I4 pool (head_dim 128, q of type q_dtype
- * KV_BF16 or KV_F16, out of q_dtype or KV_F32).  The blocks of the batch are
- * first expanded to 16-bit tiles in the workspace (16-byte aligned,
- * kv_prefill_i4_workspace_size bytes for the same sizes), once for all their
- * query tiles and heads. */
+ * KV_BF16 or KV_F16, out of q_dtype or KV_F32, q and out 16-byte aligned).  Few query
+ * tokens per sequence (a step over drafted tokens) run on the decode's kernel with a
+ * column per (query token, head); a sequence with more than max_q_len of them is then
+ * left out and sets KV_DEVERR_BLOCK_RANGE.  Otherwise the blocks of the batch are first
+ * expanded to 16-bit tiles in the workspace, once for all their query tiles and heads:
+ * pass tables no wider than the longest sequence needs.  workspace: 16-byte aligned,
+ * kv_prefill_i4_workspace_size bytes for the same sizes. */
 kv_status kv_prefill_i4_workspace_size(kv_pool_t p, int batch, int num_q_heads, int max_blocks,
                                        int max_q_len, size_t *bytes);
 kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype,

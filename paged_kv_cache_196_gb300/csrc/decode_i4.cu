@@ -1029,7 +1029,9 @@ kv_status attend_i4(const I4Call &a) {
     const int cols = a.max_q_len * g;  // of one (sequence, kv head)
     const int nt = cols <= 24 ? (cols + 7) / 8 : 2;  // more: groups of 16 (a fourth tile of eight does not fit)
     const int groups = (cols + 8 * nt - 1) / (8 * nt);
-    if (ms > 65535 || (long long)a.batch * groups > 65535 || pool->num_kv_heads > 65535) return KV_ERR_UNSUPPORTED;
+    if (ms > 65535 || (long long)a.batch * groups > 65535 || pool->num_kv_heads > 65535 ||
+        a.max_blocks > INT32_MAX / kI4BS)
+        return KV_ERR_UNSUPPORTED;
     I4Params p{};
     p.q = static_cast<const uint16_t *>(a.q);
     p.q_bf16 = a.q_dtype == KV_BF16;

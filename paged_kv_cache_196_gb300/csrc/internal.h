@@ -17,7 +17,7 @@ struct kv_pool {
     void *k = nullptr;  // [num_blocks][num_kv_heads][block_size][head_dim]
     void *v = nullptr;  // KV_I4: tiles (i4.cuh), each K tile followed by its V tile; v = k + a tile
     float k_scale = 1.f, v_scale = 1.f;  // KV_I4: powers of two (kv_pool_set_i4_scales)
-    int *err = nullptr;  // device error word
+    int *err = nullptr;  // device error word, and a word nothing reads
     // arrival counters of the fused split merge, one per (sequence, kv head),
     // zero between calls (each merging CTA resets its own)
     static constexpr int kCounterSlots = 65536;

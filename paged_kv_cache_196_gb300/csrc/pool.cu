@@ -203,7 +203,7 @@ kv_status kv_pool_create(int num_blocks, int block_size, int num_kv_heads, int h
     const bool one = dtype == KV_I4;  // K and V tiles alternate in one array
     if (cudaMalloc(&p->k, one ? 2 * bytes : bytes) != cudaSuccess ||
         (!one && cudaMalloc(&p->v, bytes) != cudaSuccess) ||
-        cudaMalloc(&p->err, sizeof(int)) != cudaSuccess ||
+        cudaMalloc(&p->err, 2 * sizeof(int)) != cudaSuccess ||
         cudaMalloc(&p->counters, sizeof(int) * kv_pool::kCounterSlots) != cudaSuccess) {
         cudaGetLastError();
         st = KV_ERR_OOM;

@@ -419,7 +419,12 @@ kv_status kv_append_rope(kv_pool_t p, const void *k_new, const void *v_new, kv_d
             return i4 ? launch_append_rope<D, KV_BF16, true>(r, s) : launch_append_rope<D, KV_BF16, false>(r, s);
         return i4 ? launch_append_rope<D, KV_F16, true>(r, s) : launch_append_rope<D, KV_F16, false>(r, s);
     };
-    return d == 128 ? by_type(std::integral_constant<int, 128>{}) : by_type(std::integral_constant<int, 64>{});
+    const kv_status st =
+        d == 128 ? by_type(std::integral_constant<int, 128>{}) : by_type(std::integral_constant<int, 64>{});
+    // A decode launched to overlap the kernel before it reads q early; q is what was
+    // just written.  Anything but a kernel between the two ends the overlap.
+    if (st == KV_OK && q && p->launch_overlap) return cuda_status(cudaMemsetAsync(p->err + 1, 0, sizeof(int), s));
+    return st;
 }
 
 kv_status kv_read_tokens(kv_pool_t p, const int64_t *slots, int num_tokens, void *k_out, void *v_out,

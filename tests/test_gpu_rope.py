@@ -335,3 +335,61 @@ def test_append_and_read_captured_in_a_graph():
     np.testing.assert_array_equal(f64(ko), stored(rotate32(qkv[:, 8:10].float().cpu().numpy(), table.cpu().numpy()[pos], 128, False)))
     np.testing.assert_array_equal(f64(vo), stored(f64(qkv[:, 10:])))
     pk.kv_pool_destroy(pool)
+
+
+def test_rotated_queries_reach_an_overlapping_decode():
+    """With launch overlap on, a 16-bit decode reads its queries before the previous
+    kernel has ended; it must see the ones this call wrote all the same."""
+    require_cuda()
+    B, hq, hkv, d, L = 64, 32, 8, 128, 900
+    rng = np.random.default_rng(3)
+    width = -(-(L + 1) // 16)
+    pool = pk.kv_pool_create(B * width, 16, hkv, d, pk.KV_BF16)
+    table, tables = torch.from_numpy(rope_table(L + 1, d)).cuda(), torch.arange(B * width, dtype=torch.int32).view(B, width).cuda()
+    rows = torch.randn(B * L, hkv, d, device="cuda").to(torch.bfloat16)
+    j = torch.arange(L)
+    slots = (tables.cpu().long()[:, j // 16] * 16 + j % 16).reshape(-1).cuda()
+    pk.kv_append_rope(pool, rows, rows, pk.KV_BF16, slots, B * L)
+    lens = torch.full((B,), L + 1, dtype=torch.int32, device="cuda")
+    new = (tables.long()[:, L // 16] * 16 + L % 16).contiguous()
+    pos = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    n = pk.kv_decode_workspace_size(B, hq, hkv, d, width, 2)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    qkvs = [torch.from_numpy(rng.standard_normal((B, hq + 2 * hkv, d)).astype(np.float32)).to(torch.bfloat16).cuda() for _ in range(8)]
+    row = (hq + 2 * hkv) * d
+
+    def steps(overlap):
+        pk.kv_pool_set_launch_overlap(pool, overlap)
+        q = torch.zeros(B, hq, d, dtype=torch.bfloat16, device="cuda")
+        outs = [torch.empty(B, hq, d, device="cuda") for _ in qkvs]
+        for qkv, out in zip(qkvs, outs):  # one query buffer, rewritten by each step
+            pk.kv_append_rope(pool, qkv[:, hq:], qkv[:, hq + hkv:], pk.KV_BF16, new, B, row, row, pos, table, L + 1, d, False, qkv, q,
+                              hq, row)
+            pk.paged_decode_attention(pool, q, tables, width, lens, B, hq, d ** -0.5, out, pk.KV_F32, None, 2, ws, n)
+        torch.cuda.synchronize()
+        assert pk.kv_get_device_error(pool) == 0
+        return outs
+
+    plain = steps(False)
+    for _ in range(5):
+        for a, b in zip(plain, steps(True)):
+            assert torch.equal(a, b)
+    pk.kv_pool_destroy(pool)
+
+
+def test_on_a_stream_of_its_own():
+    require_cuda()
+    qkv, pos, slots, nb = _inputs(65, 8, 2, 128, "f16", 13)
+    pool = pk.kv_pool_create(nb, 16, 2, 128, pk.KV_I4)
+    t_slots = torch.from_numpy(slots).cuda()
+    k, v = qkv[:, 8:10].contiguous(), qkv[:, 10:].contiguous()
+    ko, vo = (torch.empty(65, 2, 128, device="cuda") for _ in "kv")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    pk.kv_append_rope(pool, k, v, pk.KV_F16, t_slots, 65, stream=s)          # given
+    with torch.cuda.stream(s):
+        pk.kv_read_tokens(pool, t_slots, 65, ko, vo, pk.KV_F32)              # current
+    s.synchronize()
+    np.testing.assert_array_equal(f64(ko), stored(f64(k)))
+    np.testing.assert_array_equal(f64(vo), stored(f64(v)))
+    pk.kv_pool_destroy(pool)
