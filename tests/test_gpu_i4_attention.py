@@ -179,6 +179,72 @@ def test_decode_wait_limit():
     c.close()
 
 
+def test_two_graphs_share_a_workspace():
+    """Two captured steps over one pool and one workspace, replayed in turn, and a
+    length that changes between replays: the cut is made on the device."""
+    a, lens2 = Cache([900, 40, 2000, 333], 2, 128, seed=21), [500, 40, 1200, 16]
+    q1, q2 = a.queries(4, 8, "bf16", seed=1), a.queries(4, 8, "bf16", seed=2)
+    lens = a.t_lens.clone()
+    outs = [torch.empty(4, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    lses = [torch.empty(4, 8, device="cuda") for _ in range(2)]
+    n = pk.kv_decode_workspace_size(4, 8, 2, 128, a.width, 8)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for q, out, lse in zip((q1, q2), outs, lses):
+        def step():
+            pk.paged_decode_attention_i4(a.pool, q, pk.KV_BF16, a.t_tables, a.width, lens, 4, 8, 128 ** -0.5, out, pk.KV_BF16, lse, 8,
+                                         ws, n)
+        step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        graphs.append(g)
+    for now in (a.lens, np.array(lens2, np.int32), a.lens):
+        lens.copy_(torch.from_numpy(now))
+        for _ in range(3):
+            for g in graphs:
+                g.replay()
+        torch.cuda.synchronize()
+        for q, out, lse in zip((q1, q2), outs, lses):
+            for b, m in enumerate(now):
+                ref = attend(f64(q)[b:b + 1], a.kv[b][:m], a.vv[b][:m], 128 ** -0.5, [int(m)])
+                check_attention(f64(out)[b:b + 1], f64(lse)[b:b + 1], ref, 128 ** -0.5, int(m), "bf16", STEP["bf16"])
+    assert pk.kv_get_device_error(a.pool) == 0
+    a.close()
+
+
+@pytest.mark.parametrize("batch", [255, 257, 1100, 4096, 4097])
+def test_decode_many_sequences(batch):
+    """Batches around the scan's slices and past the largest that it takes."""
+    lens = [(i * 37) % 40 for i in range(batch)]
+    lens[batch // 2] = 700
+    one = Cache([700], 1, 64, seed=8)
+    tables = one.t_tables.expand(batch, -1).contiguous()
+    t_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = one.queries(batch, 2, "f16")
+    for splits in (1, 3):
+        out, lse = one.decode(q, "f16", "f32", splits, tables=tables, lens=t_lens)
+        o64, l64, q64 = f64(out), f64(lse), f64(q)
+        for b in list(range(0, batch, 41)) + [batch // 2, batch - 1]:
+            ref = attend(q64[b:b + 1], one.kv[0][:lens[b]], one.vv[0][:lens[b]], 64 ** -0.5, [lens[b]])
+            check_attention(o64[b:b + 1], l64[b:b + 1], ref, 64 ** -0.5, lens[b], "f32", STEP["f32"], f"seq {b}")
+    one.close()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+def test_decode_scale_of_zero_and_below(scale):
+    c = Cache([100, 33], 2, 128, seed=14)
+    q = c.queries(2, 4, "bf16")
+    out = torch.empty(2, 4, 128, device="cuda")
+    lse = torch.empty(2, 4, device="cuda")
+    pk.paged_decode_attention_i4(c.pool, q, pk.KV_BF16, c.t_tables, c.width, c.t_lens, 2, 4, scale, out, pk.KV_F32, lse, 1)
+    for b, n in enumerate(c.lens):
+        ref = attend(f64(q)[b:b + 1], c.kv[b], c.vv[b], scale, [int(n)])
+        check_attention(f64(out)[b:b + 1], f64(lse)[b:b + 1], ref, scale, int(n), "f32", STEP["f32"])
+    c.close()
+
+
 # ------------------------------------------------------------------ prefill
 def check_prefill(c, q, out, lse, cu, out_type, what=""):
     q64, o64, l64 = f64(q), f64(out), f64(lse)
