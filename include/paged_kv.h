@@ -86,7 +86,6 @@ typedef enum { KV_F32 = 0, KV_BF16 = 1, KV_F16 = 2, KV_I4 = 3 } kv_dtype;
 #define KV_DEVERR_VALUE_RANGE 0x10  /* prefill: a V value of a key below the sequence length
                                        with |v| >= 65536 or infinite; the PV product, run on
                                        fp16 operands, used +-65504 in its place */
-
 #define KV_DEVERR_POSITION 0x20     /* kv_append_rope: position outside [0, max_position) */
 
 /* Default time limit of a pipeline wait inside a kernel (nanoseconds). */
@@ -312,9 +311,9 @@ kv_status kv_append(kv_pool_t p, const void *k_new, const void *v_new,
  * Rotated in fp32 (two products and a sum, each rounded) and rounded once; what
  * is not rotated is moved bit by bit.  With kv_pool_set_launch_overlap on, a call
  * that writes q_out keeps the next launch from overlapping it (a decode would read
- * q_out early).  Addresses and strides: multiples of 16
- * bytes.  KV_ERR_ARG for a wrong size, stride, alignment, type or NULL pointer,
- * KV_ERR_UNSUPPORTED for an in_dtype that no pool takes. */
+ * q_out early).  Addresses and strides: multiples of 16 bytes.  KV_ERR_ARG for a
+ * wrong size, stride, alignment, type or NULL pointer, KV_ERR_UNSUPPORTED for an
+ * in_dtype that no pool takes. */
 kv_status kv_append_rope(kv_pool_t p, const void *k_new, const void *v_new, kv_dtype in_dtype,
                          int64_t k_stride, int64_t v_stride, const int64_t *slot_mapping,
                          const int32_t *positions, const float *cos_sin, int max_position,

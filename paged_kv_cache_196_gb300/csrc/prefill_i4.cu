@@ -16,6 +16,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "common.cuh"
@@ -135,13 +136,15 @@ kv_status kv_prefill_i4_workspace_size(kv_pool_t p, int batch, int num_q_heads, 
     if (!p || !bytes || batch < 0 || num_q_heads <= 0 || max_blocks < 0 || max_q_len < 0) return KV_ERR_ARG;
     if (p->dtype != KV_I4 || p->head_dim != kExD) return KV_ERR_UNSUPPORTED;
     if (num_q_heads % p->num_kv_heads) return KV_ERR_ARG;
-    if (num_q_heads / p->num_kv_heads > 8) return KV_ERR_UNSUPPORTED;
+    if (num_q_heads / p->num_kv_heads > 8 || batch > 65535) return KV_ERR_UNSUPPORTED;
     if (few_columns(batch, p->num_kv_heads, max_q_len, num_q_heads / p->num_kv_heads)) {
         int pb, ms;
         split_plan(batch, p->num_kv_heads, max_blocks, 0, &pb, &ms);
         *bytes = decode_workspace_bytes(batch * max_q_len, num_q_heads, kExD, ms);
     } else {
-        *bytes = expand_table_bytes(batch, max_blocks) + 2 * (size_t)batch * max_blocks * p->num_kv_heads * kExOut;
+        // a tensor map has at least one row, so a table without columns takes a block
+        *bytes = expand_table_bytes(batch, max_blocks) +
+                 2 * (size_t)batch * std::max(max_blocks, 1) * p->num_kv_heads * kExOut;
     }
     return KV_OK;
 }
@@ -188,16 +191,16 @@ kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtyp
         a.stream = as_stream(stream);
         return attend_i4(a);
     }
-    const long long rows = (long long)batch * max_blocks * p->num_kv_heads * 16;
+    const long long blocks = (long long)batch * std::max(max_blocks, 1), rows = blocks * p->num_kv_heads * 16;
     if (rows > INT32_MAX || p->num_kv_heads > 65535) return KV_ERR_UNSUPPORTED;
     int32_t *order = static_cast<int32_t *>(workspace), *table = order + batch;
     char *k_tiles = static_cast<char *>(workspace) + expand_table_bytes(batch, max_blocks);
-    char *v_tiles = k_tiles + (size_t)batch * max_blocks * p->num_kv_heads * kExOut;
+    char *v_tiles = k_tiles + (size_t)blocks * p->num_kv_heads * kExOut;
     CUtensorMap map_k, map_v;
     if (!encode_rows_map(&map_k, k_tiles, rows) || !encode_rows_map(&map_v, v_tiles, rows)) return KV_ERR_CUDA;
     const bool ordered = batch > 1 && batch <= kOrderBatch;
     const int columns = (max_blocks + 7) / 8;
-    const dim3 grid(columns + ordered, p->num_kv_heads, batch);
+    const dim3 grid(std::max(columns + (int)ordered, 1), p->num_kv_heads, batch);
     auto fn = q_dtype == KV_BF16 ? expand_i4_kernel<true> : expand_i4_kernel<false>;
     fn<<<grid, 256, 0, as_stream(stream)>>>((const char *)p->k, (const char *)p->v, block_tables, seq_lens, max_blocks,
                                             p->num_blocks, p->num_kv_heads, table, k_tiles, v_tiles, order,
@@ -215,7 +218,7 @@ kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtyp
     a.max_q_len = max_q_len;
     a.block_tables = table;
     a.max_blocks = max_blocks;
-    a.num_blocks = (int)(rows / 16 / p->num_kv_heads);
+    a.num_blocks = (int)blocks;
     a.num_kv_heads = p->num_kv_heads;
     a.seq_lens = seq_lens;
     a.batch = batch;

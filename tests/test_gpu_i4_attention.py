@@ -310,6 +310,23 @@ def test_prefill_flags_bad_blocks_and_lengths(T):
     c.close()
 
 
+@pytest.mark.parametrize("T", [4, 400])
+def test_prefill_without_a_table_column(T):
+    """No sequence can have a key: each with a query is left out and flagged."""
+    c = Cache([20], 2, 128, seed=2)
+    n = pk.kv_prefill_i4_workspace_size(c.pool, 1, 4, 0, T)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    q = c.queries(T, 4, "bf16")
+    out = torch.full_like(q, 7)
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    for length in (0, T):
+        lens = torch.tensor([length], dtype=torch.int32, device="cuda")
+        pk.paged_prefill_attention_i4(c.pool, q, pk.KV_BF16, cu, T, T, c.t_tables, 0, lens, 1, 4, 1.0, out, pk.KV_BF16, None, ws, n)
+        assert pk.kv_get_device_error(c.pool) == 0x1
+        assert torch.all(out == 7)
+    c.close()
+
+
 def test_refusals():
     c = Cache([40], 2, 128, seed=1)
     d64 = Cache([40], 2, 64, seed=1)
@@ -343,6 +360,7 @@ def test_refusals():
     refused(-3, pk.kv_prefill_i4_workspace_size, bf, 1, 4, 3, 40)
     refused(-3, pk.kv_prefill_i4_workspace_size, d64.pool, 1, 4, 3, 40)
     refused(-1, pk.kv_prefill_i4_workspace_size, c.pool, 1, 3, 3, 40)
+    refused(-3, pk.kv_prefill_i4_workspace_size, c.pool, 70000, 4, 3, 40)
     pk.paged_decode_attention_i4(c.pool, None, pk.KV_BF16, None, 3, None, 0, 4, 1.0, None, pk.KV_F32)  # nothing to do
     assert pk.kv_get_device_error(c.pool) == 0
     for x in (c, d64):
