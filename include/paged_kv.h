@@ -406,13 +406,16 @@ kv_status paged_decode_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype
                                     size_t workspace_bytes, void *stream);
 
 /* paged_prefill_attention over a KV_I4 pool (head_dim 128, q of type q_dtype
- * KV_BF16 or KV_F16, out of q_dtype or KV_F32, q and out 16-byte aligned).  Few query
- * tokens per sequence (a step over drafted tokens) run on the decode's kernel with a
- * column per (query token, head); a sequence with more than max_q_len of them is then
- * left out and sets KV_DEVERR_BLOCK_RANGE.  Otherwise the blocks of the batch are first
- * expanded to 16-bit tiles in the workspace, once for all their query tiles and heads:
- * pass tables no wider than the longest sequence needs.  workspace: 16-byte aligned,
- * kv_prefill_i4_workspace_size bytes for the same sizes. */
+ * KV_BF16 or KV_F16, out of q_dtype or KV_F32, q and out 16-byte aligned, scale > 0).
+ * Few query tokens per sequence (a step over drafted tokens) run on the decode's kernel
+ * with a column per (query token, head).  Otherwise the blocks of the batch are first
+ * expanded to 16-bit tiles in the workspace, once for all their query tiles and heads
+ * (pass tables no wider than the longest sequence needs), and where query tiles alone
+ * would leave SMs idle their keys are cut too, by the lengths on the device: results
+ * then depend, within rounding, on the batch's lengths, and are the same from call to
+ * call.  A sequence with more than max_q_len query tokens is left out and sets
+ * KV_DEVERR_BLOCK_RANGE.  workspace: 16-byte aligned, kv_prefill_i4_workspace_size bytes
+ * for the same sizes. */
 kv_status kv_prefill_i4_workspace_size(kv_pool_t p, int batch, int num_q_heads, int max_blocks,
                                        int max_q_len, size_t *bytes);
 kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype,

@@ -176,13 +176,32 @@ struct DecodeArgs {
 
 // ---- prefill: the tcgen05 kernel over checked arguments and tensor maps of the
 // K and V tiles ([block][kv head][16] rows of 128 16-bit values)
+// A packed prefill's share of one CTA per kv head: query tile qt of sequence b over its
+// key tiles j0 .. j1 - 1 (of 128 keys).  nsplit > 1: one of that many pieces of the
+// query tile's keys, whose partial results lie in slots slot0 .. slot0 + nsplit - 1.
+struct PrefillItem {
+    int b, qt, j0, j1;
+    int split, nsplit, slot0, unused;
+};
+// Floats of a slot per kv head: 256 rows of O, and each row's reference and sum.
+constexpr int kPrefillSlot = 256 * (128 + 2);
+
+struct PrefillCounts {
+    int items, cuts;  // entries of both lists
+};
+
 struct PrefillCall {
     const void *q;
     kv_dtype q_dtype;  // KV_BF16 or KV_F16: q, K and a 16-bit out
     // a tile's rows: all heads of a group, and V in fp16 whatever q's type; launched
     // while the previous kernel (the expansion of the tiles) still runs
     bool packed;
-    const int32_t *order;  // device permutation of the batch (packed only), or null
+    // packed: the CTAs' shares, how many there are (device), and at most
+    const PrefillItem *items;
+    const PrefillCounts *counts;
+    int max_items;
+    const int *cuts;  // first items of the cut query tiles; null: none are cut
+    float *partial;   // slots [slot][kv head][kPrefillSlot]
     const CUtensorMap *map_k, *map_v;
     const int32_t *cu_q;
     int total_q, max_q_len;

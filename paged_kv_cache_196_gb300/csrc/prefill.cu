@@ -95,7 +95,10 @@ KV_DEVICE constexpr uint32_t colO(int x) { return x ? 384u : 256u; }
 
 struct PrefillParams {
     const int32_t *cu_q;
-    const int32_t *order;  // PACK: the order in which the grid takes the sequences, or null
+    const PrefillItem *items;  // PACK (see PrefillCall)
+    const PrefillCounts *counts;
+    const int *cuts;
+    float *partial;
     int total_q;
     const int32_t *tables;
     const int32_t *seq_lens;
@@ -134,30 +137,44 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // chunk sees more keys, so the grid's last wave holds light CTAs.  The
     // sequences stay in order, so the CTAs running at one time share one
     // sequence's K/V in L2.
-    const int qt = gridDim.y - 1 - blockIdx.y;
-    int b = blockIdx.z;
+    int qt = gridDim.y - 1 - blockIdx.y, b = blockIdx.z;
+    int hq = blockIdx.x;  // (first) query head
+    int j0 = 0, j1 = 0;      // PACK: key tiles
     if constexpr (PACK) {
         // Launched to overlap the expansion of the tiles, which writes all that is read
         // from here on but q.
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (p.order) b = p.order[b];
+        const int i = blockIdx.x / p.num_kv_heads;
+        const int num_items = p.counts->items;
+        const int4 item = *reinterpret_cast<const int4 *>(p.items + i);
+        if (i >= num_items) return;
+        b = item.x;
+        qt = item.y;
+        j0 = item.z;
+        j1 = item.w;
+        hq = (blockIdx.x - i * p.num_kv_heads) * p.g;
     }
     const int tokens = PACK ? 128 / p.g : 128;       // query tokens of a tile
-    const int hq = PACK ? blockIdx.x * p.g : blockIdx.x;  // (first) query head
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q_begin = p.cu_q[b];
     const int T = p.cu_q[b + 1] - q_begin;
     const int q0 = qt * (2 * tokens);
     if (q0 >= T) return;  // uniform: this sequence's chunk has no tile here
     long long L = p.seq_lens[b];
-    const long long c = L - T;
+    long long c = L - T;
     if (c < 0 || L > (long long)p.max_blocks * 16 || q_begin < 0 || q_begin + T > p.total_q) {
         if (tid == 0) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
         return;
     }
     const int h = hq / p.g;
     const long long kv_end = c + min(q0 + 2 * tokens, T);  // keys any row of this CTA can see
-    const int n = (int)((kv_end + kPfBN - 1) / kPfBN);
+    const int n = PACK ? j1 - j0 : (int)((kv_end + kPfBN - 1) / kPfBN);
+    const int32_t *table_row = p.tables + (size_t)b * p.max_blocks;
+    if constexpr (PACK) {  // from here on the sequence begins at the piece's first key
+        L -= (long long)j0 * kPfBN;
+        c -= (long long)j0 * kPfBN;
+        table_row += j0 * (kPfBN / 16);
+    }
     const int nblk = (int)((L + 15) / 16);
 
     extern __shared__ __align__(1024) char smem_raw[];
@@ -194,7 +211,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const uint32_t tmem = bars->tmem_slot;
     volatile int *abort_flag = &bars->abort;
 
-    const int32_t *table_row = p.tables + (size_t)b * p.max_blocks;
     // Tensor row of block (8*jj + lane) of this sequence and head for lanes
     // 0-7; rows -16..-1 lie outside the tensor and read as zeros.
     auto fetch = [&](int jj, bool flag_bad) {
@@ -467,7 +483,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             float alpha = 1.f;
             bool rescale = false;
             if (j == 0) {
-                m_used = mrow;
+                // a piece may start past all keys of a row: its reference stays finite
+                m_used = PACK ? fmaxf(mrow, -1e30f) : mrow;
             } else if (mrow > m_used + kRescaleThreshold) {
                 alpha = ex2_approx(m_used - mrow);
                 m_used = mrow;
@@ -528,6 +545,26 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (ok) ok = mbar_wait<TW>(&bars->done, 0, p.err);
         if (!ok) *abort_flag = 1;
         tc::fence_after_sync();
+        if constexpr (PACK) {
+            const int4 cut = reinterpret_cast<const int4 *>(p.items + blockIdx.x / p.num_kv_heads)[1];
+            if (cut.y > 1) {  // the whole CTA's: a piece leaves O, reference and sum
+                float4 *part = reinterpret_cast<float4 *>(
+                    p.partial + ((size_t)(cut.z + cut.x) * p.num_kv_heads + blockIdx.x % p.num_kv_heads) * kPrefillSlot);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t v[32];
+                    tc::tmem_ld32(tmem + lane_base + colO(x) + 32 * i, v);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        part[(8 * i + k) * kPfBM + tid] =
+                            make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                        __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+                }
+                reinterpret_cast<float2 *>(part + 32 * kPfBM)[tid] = make_float2(m_used, l_sum);
+                ok = false;  // nothing else to store
+            }
+        }
         const float inv = l_sum > 0.f ? p.v_mul / l_sum : 0.f;
         const size_t orow = ((size_t)(q_begin + qrow) * p.num_q_heads + head) * kPfD;
 #pragma unroll
@@ -566,6 +603,48 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
 }
 
+// Adds up the pieces of cut query tiles: O = sum of 2^(m - M) O_piece over the sum of
+// 2^(m - M) l_piece.  A CTA of a single wave takes 16 rows of a (tile, kv head) at a
+// time; lane = (dims / 4 % 2, row), so that a warp reads runs of 256 bytes.
+constexpr int kPfMergeThreads = 256, kPfMergeRows = 16;
+__global__ void __launch_bounds__(kPfMergeThreads) merge_prefill_kernel(const PrefillParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kGroups = kPfBM / kPfMergeRows;
+    const int tokens = 128 / p.g;
+    const int units = p.counts->cuts * p.num_kv_heads * kGroups;
+    const int r = threadIdx.x % kPfMergeRows, dq = threadIdx.x / kPfMergeRows;  // dims 4 dq ..  and 64 + 4 dq ..
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const int row = u % kGroups * kPfMergeRows + r, h = u / kGroups % p.num_kv_heads;
+        const PrefillItem item = p.items[p.cuts[u / kGroups / p.num_kv_heads]];
+        const int q_begin = p.cu_q[item.b], T = p.cu_q[item.b + 1] - q_begin;
+        const int x = row >> 7, at = (row & 127) / p.g, head = h * p.g + (row & 127) - at * p.g;
+        const int qrow = item.qt * (2 * tokens) + tokens * x + at;
+        if (qrow >= T || at >= tokens || item.nsplit < 2) continue;
+        const float *part = p.partial + ((size_t)item.slot0 * p.num_kv_heads + h) * kPrefillSlot;
+        const size_t step = (size_t)p.num_kv_heads * kPrefillSlot;
+        float M = -1e30f, den = 0.f;
+        for (int s = 0; s < item.nsplit; ++s)
+            M = fmaxf(M, __ldg(reinterpret_cast<const float2 *>(part + s * step + 128 * kPfBM) + row).x);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
+#pragma unroll 4
+        for (int s = 0; s < item.nsplit; ++s) {
+            const float *from = part + s * step;
+            const float2 ml = __ldg(reinterpret_cast<const float2 *>(from + 128 * kPfBM) + row);
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(from) + dq * kPfBM + row);
+            const float4 w = __ldg(reinterpret_cast<const float4 *>(from) + (dq + 16) * kPfBM + row);
+            const float e = ex2_approx(ml.x - M);
+            den += e * ml.y;
+            a.x += e * v.x, a.y += e * v.y, a.z += e * v.z, a.w += e * v.w;
+            c.x += e * w.x, c.y += e * w.y, c.z += e * w.z, c.w += e * w.w;
+        }
+        const float inv = den > 0.f ? p.v_mul / den : 0.f;
+        const size_t orow = (size_t)(q_begin + qrow) * p.num_q_heads + head;
+        store_out4(p.out, orow * kPfD + 4 * dq, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), p.out_type);
+        store_out4(p.out, orow * kPfD + 64 + 4 * dq, make_float4(c.x * inv, c.y * inv, c.z * inv, c.w * inv), p.out_type);
+        if (p.lse && dq == 0) p.lse[orow] = den > 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
 cudaError_t set_wait_limit_prefill(unsigned long long ns) { return set_wait_limit_here(ns); }
 
 kv_status launch_prefill(const PrefillCall &a) {
@@ -577,7 +656,10 @@ kv_status launch_prefill(const PrefillCall &a) {
         return KV_ERR_CUDA;
     PrefillParams pp{};
     pp.cu_q = a.cu_q;
-    pp.order = a.order;
+    pp.items = a.items;
+    pp.counts = a.counts;
+    pp.cuts = a.cuts;
+    pp.partial = a.partial;
     pp.total_q = a.total_q;
     pp.tables = a.block_tables;
     pp.seq_lens = a.seq_lens;
@@ -602,13 +684,9 @@ kv_status launch_prefill(const PrefillCall &a) {
     if (kv_status st0 = cuda_status(cudaFuncSetAttribute(
             fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kPfSmemBytes)))
         return st0;
-    const int span = a.packed ? 2 * (128 / g) : kPfBM;  // query tokens of a CTA
-    const int q_tiles = (a.max_q_len + span - 1) / span;
-    if (q_tiles > 65535) return KV_ERR_UNSUPPORTED;
-    const dim3 grid(a.packed ? a.num_kv_heads : a.num_q_heads, q_tiles, a.batch);
     if (a.packed) {
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = grid;
+        cfg.gridDim = dim3((unsigned)a.max_items * (unsigned)a.num_kv_heads);
         cfg.blockDim = dim3(kPfThreads);
         cfg.dynamicSmemBytes = kPfSmemBytes;
         cfg.stream = a.stream;
@@ -617,8 +695,16 @@ kv_status launch_prefill(const PrefillCall &a) {
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        return cuda_status(cudaLaunchKernelEx(&cfg, fn, tm_q, *a.map_k, *a.map_v, pp));
+        if (kv_status st = cuda_status(cudaLaunchKernelEx(&cfg, fn, tm_q, *a.map_k, *a.map_v, pp))) return st;
+        if (!a.cuts) return KV_OK;
+        cfg.gridDim = dim3(2u * (unsigned)sm_count());
+        cfg.blockDim = dim3(kPfMergeThreads);
+        cfg.dynamicSmemBytes = 0;
+        return cuda_status(cudaLaunchKernelEx(&cfg, merge_prefill_kernel, pp));
     }
+    const int q_tiles = (a.max_q_len + kPfBM - 1) / kPfBM;
+    if (q_tiles > 65535) return KV_ERR_UNSUPPORTED;
+    const dim3 grid(a.num_q_heads, q_tiles, a.batch);
     fn<<<grid, kPfThreads, kPfSmemBytes, a.stream>>>(tm_q, *a.map_k, *a.map_v, pp);
     return cuda_status(cudaGetLastError());
 }

@@ -310,6 +310,52 @@ def test_prefill_flags_bad_blocks_and_lengths(T):
     c.close()
 
 
+@pytest.mark.parametrize("out_type", ["bf16", "f32"])
+@pytest.mark.parametrize("hkv,g,lens,chunks", [
+    (1, 1, [9000], [300]),                 # two query tiles, their keys cut into many pieces
+    (1, 8, [5000, 700, 130, 4100], [40, 700, 129, 33]),
+    (2, 4, [8000, 20, 0, 3000], [130, 20, 0, 41]),
+    (1, 3, [3000, 600], [2600, 90]),       # rows that see none of a piece's keys
+])
+def test_prefill_keys_cut(hkv, g, lens, chunks, out_type):
+    c = Cache(lens, hkv, 128, seed=sum(lens) + g)
+    cu = np.concatenate([[0], np.cumsum(chunks)])
+    q = c.queries(int(cu[-1]), g * hkv, "bf16")
+    out, lse = c.prefill(q, "bf16", out_type, cu, max(chunks))
+    check_prefill(c, q, out, lse, cu, out_type)
+    for _ in range(3):  # the last piece to arrive differs, the result does not
+        again, lse2 = c.prefill(q, "bf16", out_type, cu, max(chunks))
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+    c.close()
+
+
+def test_prefill_more_sequences_than_are_ordered_at_once():
+    B = 600
+    one = Cache([1500], 1, 128, seed=6)
+    lens = torch.tensor([1500 if b % 199 == 7 else 33 + b % 90 for b in range(B)], dtype=torch.int32)
+    T = [0 if b % 11 == 3 else 33 if b % 199 == 7 else 1 + b % 33 for b in range(B)]
+    cu = np.concatenate([[0], np.cumsum(T)])
+    q = one.queries(int(cu[-1]), 1, "f16")
+    out, lse = one.prefill(q, "f16", "f16", cu, 33, tables=one.t_tables.expand(B, -1).contiguous(), lens=lens.cuda())
+    q64, o64, l64 = f64(q), f64(out), f64(lse)
+    for b in list(range(0, B, 37)) + [7, 206, B - 1]:
+        n, rows = int(lens[b]), slice(cu[b], cu[b + 1])
+        ref = attend(q64[rows], one.kv[0][:n], one.vv[0][:n], 128 ** -0.5, [n - T[b] + i + 1 for i in range(T[b])])
+        check_attention(o64[rows], l64[rows], ref, 128 ** -0.5, n, "f16", 2.0 ** -11, f"seq {b}", floor=2.0 ** -24)
+    one.close()
+
+
+def test_prefill_longer_than_announced_is_left_out():
+    c = Cache([300, 200], 1, 128, seed=3)
+    cu = [0, 120, 220]
+    q = c.queries(220, 4, "bf16")
+    out, _ = c.prefill(q, "bf16", "bf16", cu, 100, expect=0x1)
+    good, _ = c.prefill(q, "bf16", "bf16", cu, 120)
+    assert torch.all(out[:120] == 7) and torch.all(torch.isfinite(out[120:]))
+    assert torch.equal(out[120:], good[120:])
+    c.close()
+
+
 @pytest.mark.parametrize("T", [4, 400])
 def test_prefill_without_a_table_column(T):
     """No sequence can have a key: each with a query is left out and flagged."""
@@ -349,13 +395,15 @@ def test_refusals():
                          (-3, dec(B=70000))):
         refused(status, *case[0], **case[1])
 
-    def pre(pool=c.pool, q=t, qt=pk.KV_BF16, cu=i, rows=1, most=400, tab=i, mb=3, lens=i, B=1, hq=4, out=t, ot=pk.KV_F32, ws=t, n=1 << 16):
-        return pk.paged_prefill_attention_i4, pool, q, qt, cu, rows, most, tab, mb, lens, B, hq, 1.0, out, ot, None, ws, n
+    def pre(pool=c.pool, q=t, qt=pk.KV_BF16, cu=i, rows=1, most=400, tab=i, mb=3, lens=i, B=1, hq=4, out=t, ot=pk.KV_F32, ws=t,
+            n=1 << 16, scale=1.0):
+        return pk.paged_prefill_attention_i4, pool, q, qt, cu, rows, most, tab, mb, lens, B, hq, scale, out, ot, None, ws, n
 
     for status, case in ((-3, pre(pool=bf)), (-3, pre(pool=d64.pool)), (-3, pre(qt=pk.KV_F32)), (-3, pre(ot=pk.KV_F16)),
                          (-1, pre(hq=3)), (-1, pre(q=None)), (-1, pre(cu=None)), (-1, pre(tab=None)), (-1, pre(lens=None)),
                          (-1, pre(out=None)), (-1, pre(ws=None)), (-1, pre(n=1000)), (-1, pre(rows=-1)), (-1, pre(most=-1)),
-                         (-1, pre(ws=t.data_ptr() + 8)), (-3, pre(B=70000))):
+                         (-1, pre(ws=t.data_ptr() + 8)), (-3, pre(B=70000)), (-1, pre(scale=0.0)), (-1, pre(scale=-1.0)),
+                         (-1, pre(scale=float("nan")))):
         refused(status, *case)
     refused(-3, pk.kv_prefill_i4_workspace_size, bf, 1, 4, 3, 40)
     refused(-3, pk.kv_prefill_i4_workspace_size, d64.pool, 1, 4, 3, 40)
