@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         auto at = [&](int wp, int col, int rr, int i) {            // spread over the banks
             return (wp * kMC + col) * (D / 4) + rr * kQ + (i ^ ((col >> 1) & (kQ - 1)) ^ (rr & (kQ - 1)));
         };
-#pragma unroll
+#pragma unroll 1
         for (int pass = 0; pass < kCols / kMC; ++pass) {
             const int live = min(kMC, ncols - kMC * pass);
             if (live <= 0) break;
