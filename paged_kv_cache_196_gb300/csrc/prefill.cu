@@ -605,7 +605,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 
 // Adds up the pieces of cut query tiles: O = sum of 2^(m - M) O_piece over the sum of
 // 2^(m - M) l_piece.  A CTA of a single wave takes 16 rows of a (tile, kv head) at a
-// time; lane = (dims / 4 % 2, row), so that a warp reads runs of 256 bytes.
+// time; a warp covers 16 rows of two quads of dimensions, so that it reads runs of 256
+// bytes.  Bound by the latency of L2 (a cut tile's pieces were written just before).
 constexpr int kPfMergeThreads = 256, kPfMergeRows = 16;
 __global__ void __launch_bounds__(kPfMergeThreads) merge_prefill_kernel(const PrefillParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");

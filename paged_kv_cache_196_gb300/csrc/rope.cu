@@ -141,7 +141,14 @@ KV_DEVICE void rotate8(const float (&x)[8], const float (&z)[8], const float (&c
 
 // IN: type of the rows; I4: 4-bit pool, else the pool holds type IN.  P: passes of a
 // warp, 32 / (D / 8) rows each.  blockIdx.y: a warp's rows, first those of q, then of
-// k, then of v; blockIdx.x: kRopeWarps tokens.
+// k, then of v; blockIdx.x: kRopeWarps tokens.  (Rows of one token in consecutive
+// CTAs instead: 55.0 us for the chunk below.  k and v first: 49.6, but 56.1 into a 4-bit
+// pool.)
+//
+// Bound by memory: a chunk of 8192 tokens (56 q, 8 kv heads of 128 dims, bf16) moves
+// 306 MB in 50.1 us, 6100 GB/s (0.90 of a device copy); into a 4-bit pool 282 MB in
+// 54.2 us, 5200 GB/s, the integer pipe busy for 54% of the time.  A step of 64 tokens (32 q, 8 kv heads): 2.5 and 2.9 us, a launch's
+// length.
 template <int D, int IN, bool I4, int P>
 __global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopeParams p) {
     constexpr int kLanes = D / 8;         // lanes of one row
@@ -272,7 +279,10 @@ __global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopePar
 
 // Cached tokens as rows: token i's K and V rows [hkv][D] of type OUT from slot
 // slots[i].  ET: the pool's type (KV_I4: codes).  A warp takes the rows of
-// 32 / (D / 8) heads of a token at a time, an octet a lane.
+// 32 / (D / 8) heads of a token at a time, an octet a lane: the inverse of the
+// store's lanes, so that a row is written in one piece.  8192 tokens of 8 kv heads of 128
+// dims from a 4-bit pool as bf16: 43 MB in 9.0 us, 4800 GB/s with the rows' lines still
+// in L2; the conversions keep the integer pipe at 58%.
 template <int D, int ET, int OUT>
 __global__ void __launch_bounds__(kRopeThreads) read_tokens_kernel(const char *__restrict__ k_pool,
                                                                    const char *__restrict__ v_pool,
@@ -328,8 +338,12 @@ __global__ void __launch_bounds__(kRopeThreads) read_tokens_kernel(const char *_
 template <int D, int IN, bool I4>
 static kv_status launch_append_rope(const RopeParams &p, cudaStream_t s) {
     constexpr int kAtOnce = 32 / (D / 8);
-    // Passes per warp: one while that leaves SMs idle (a decode step), more when
-    // there are warps enough, so that a token's cos and sin serve more rows.
+    // Passes per warp: one while that leaves SMs idle (a decode step), four when there
+    // are warps enough, so that a token's cos and sin serve more rows.  With 32 q and 8
+    // kv heads, one / four passes: 64 tokens 2.3 / 2.5 us (4-bit 2.7 / 3.5), 256 tokens
+    // 3.3 / 3.1 (3.4 / 3.9), 512 tokens 4.6 / 3.7 (4.8 / 4.4), 4096 tokens 26.7 / 19.0
+    // (28.5 / 20.9).  Two and eight passes cost the 8192-token chunk below 58.7 and 55.0
+    // us.
     auto units = [&](int r) { return (p.hq + r - 1) / r + 2LL * ((p.hkv + r - 1) / r); };
     auto go = [&](auto fn, int r) {
         if (units(r) > 65535) return KV_ERR_UNSUPPORTED;
