@@ -53,7 +53,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <vector>
 
 #include "common.cuh"
 #include "i4.cuh"

@@ -356,6 +356,95 @@ def test_prefill_longer_than_announced_is_left_out():
     c.close()
 
 
+@pytest.mark.parametrize("T", [5, 60])
+def test_prefill_nan_stays_in_its_rows(T):
+    c = Cache([200, 90], 2, 128, seed=4)
+    cu = [0, T, 2 * T]
+    q = c.queries(2 * T, 4, "bf16")
+    ref, lref = c.prefill(q, "bf16", "bf16", cu, T)
+    bad = q.clone()
+    bad[2, 1, 7] = float("nan")
+    out, lse = c.prefill(bad, "bf16", "bf16", cu, T)
+    assert torch.isnan(out[2, 1]).all()
+    keep = torch.ones(2 * T, 4, dtype=torch.bool, device="cuda")
+    keep[2, 1] = False
+    assert torch.equal(out[keep], ref[keep]) and torch.equal(lse[keep], lref[keep])
+    # a key inside the chunk: the rows before it do not see it
+    at = 200 - T + 3
+    k = c.k[0][at:at + 1].clone()
+    k[0, 1, 3] = float("nan")
+    pk.kv_append_rope(c.pool, k.cuda(), c.v[0][at:at + 1].cuda(), pk.KV_BF16, torch.from_numpy(c.slots[0][at:at + 1]).cuda(), 1)
+    out, lse = c.prefill(q, "bf16", "bf16", cu, T)
+    assert torch.isnan(out[3:T, 2:]).all()
+    keep = torch.ones(2 * T, 4, dtype=torch.bool, device="cuda")
+    keep[3:T, 2:] = False
+    assert torch.equal(out[keep], ref[keep]) and torch.equal(lse[keep], lref[keep])
+    c.close()
+
+
+@pytest.mark.parametrize("T", [8, 64])
+def test_prefill_captured_while_lengths_change(T):
+    """The columns' runs and the list of items are made on the device: a replayed graph
+    follows the lengths and the chunks' bounds as a new call would."""
+    c = Cache([4000, 300, 900], 2, 128, seed=12)
+    q = c.queries(3 * T, 8, "bf16")
+    cu, lens = torch.tensor([0, T, 2 * T, 3 * T], dtype=torch.int32, device="cuda"), c.t_lens.clone()
+    out, lse = torch.empty_like(q), torch.empty(3 * T, 8, device="cuda")
+    n = pk.kv_prefill_i4_workspace_size(c.pool, 3, 8, c.width, T)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def step(o, l):
+        pk.paged_prefill_attention_i4(c.pool, q, pk.KV_BF16, cu, 3 * T, T, c.t_tables, c.width, lens, 3, 8, 128 ** -0.5, o, pk.KV_BF16, l,
+                                      ws, n)
+
+    step(out, lse)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(out, lse)
+    for now, bounds in (([4000, 300, 900], [0, T, 2 * T, 3 * T]), ([T, 300, 70], [0, T, T + 1, 2 * T + 1]),
+                        ([3000, 0, 900], [0, 3, 3, 3 + T]), ([4000, 300, 900], [0, T, 2 * T, 3 * T])):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        cu.copy_(torch.tensor(bounds, dtype=torch.int32))
+        out.fill_(7)
+        lse.fill_(7)
+        g.replay()
+        again, lse2 = torch.full_like(out, 7), torch.full_like(lse, 7)
+        step(again, lse2)
+        torch.cuda.synchronize()
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+        for b, m in enumerate(now):
+            rows = slice(bounds[b], bounds[b + 1])
+            t = bounds[b + 1] - bounds[b]
+            if t:
+                ref = attend(f64(q)[rows], c.kv[b][:m], c.vv[b][:m], 128 ** -0.5, [m - t + i + 1 for i in range(t)])
+                check_attention(f64(out)[rows], f64(lse)[rows], ref, 128 ** -0.5, m, "bf16", 2.0 ** -11, f"seq {b}", floor=2.0 ** -24)
+    assert pk.kv_get_device_error(c.pool) == 0
+    c.close()
+
+
+def test_prefill_past_32_bit_offsets():
+    """Expanded tiles past 2^32 bytes: a wide table, mostly unused."""
+    c = Cache([700], 8, 128, seed=5)
+    width = 48000
+    tables = torch.full((3, width), -1, dtype=torch.int32, device="cuda")
+    tables[0, :c.width] = tables[2, :c.width] = c.t_tables[0]
+    lens = torch.tensor([700, 0, 650], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 30, 30, 130], dtype=torch.int32, device="cuda")
+    q = c.queries(130, 8, "f16")
+    out, lse = torch.empty(130, 8, 128, device="cuda"), torch.empty(130, 8, device="cuda")
+    n = pk.kv_prefill_i4_workspace_size(c.pool, 3, 8, width, 100)
+    assert n > 2 * 2 ** 32
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    pk.paged_prefill_attention_i4(c.pool, q, pk.KV_F16, cu, 130, 100, tables, width, lens, 3, 8, 128 ** -0.5, out, pk.KV_F32, lse, ws, n)
+    for rows, m in ((slice(0, 30), 700), (slice(30, 130), 650)):
+        t = rows.stop - rows.start
+        ref = attend(f64(q)[rows], c.kv[0][:m], c.vv[0][:m], 128 ** -0.5, [m - t + i + 1 for i in range(t)])
+        check_attention(f64(out)[rows], f64(lse)[rows], ref, 128 ** -0.5, m, "f32", 2.0 ** -11, floor=2.0 ** -24)
+    assert pk.kv_get_device_error(c.pool) == 0
+    c.close()
+
+
 @pytest.mark.parametrize("T", [4, 400])
 def test_prefill_without_a_table_column(T):
     """No sequence can have a key: each with a query is left out and flagged."""
