@@ -382,6 +382,33 @@ def test_prefill_nan_stays_in_its_rows(T):
     c.close()
 
 
+@pytest.mark.parametrize("lens,T", [([3000, 200], 60), ([400, 300], 300)])
+def test_prefill_wait_limit(lens, T):
+    """As for the decode, with keys cut and whole: a wait that runs out is reported, the
+    next call is right."""
+    c = Cache(lens, 2, 128, seed=15)
+    cu = [0, T, 2 * T]
+    q = c.queries(2 * T, 8, "bf16")
+    n = pk.kv_prefill_i4_workspace_size(c.pool, 2, 8, c.width, T)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    t_cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    pk.kv_debug_set_wait_limit_ns(0)
+    try:
+        seen = 0
+        for _ in range(3):
+            pk.paged_prefill_attention_i4(c.pool, q, pk.KV_BF16, t_cu, 2 * T, T, c.t_tables, c.width, c.t_lens, 2, 8, 0.1, out,
+                                          pk.KV_BF16, None, ws, n)
+            torch.cuda.synchronize()
+            seen |= pk.kv_get_device_error(c.pool)
+        assert seen == 0x4
+    finally:
+        pk.kv_debug_set_wait_limit_ns(pk.KV_WAIT_LIMIT_DEFAULT_NS)
+    got, lse = c.prefill(q, "bf16", "bf16", cu, T)
+    check_prefill(c, q, got, lse, cu, "bf16")
+    c.close()
+
+
 @pytest.mark.parametrize("T", [8, 64])
 def test_prefill_captured_while_lengths_change(T):
     """The columns' runs and the list of items are made on the device: a replayed graph
