@@ -36,13 +36,16 @@ constexpr int kExOut = 16 * kExD * 2;  // of an expanded one
 // Whether the decode kernel with a column per (query token, head) runs instead.  It
 // turns the cache's codes into operands once per 16 columns and cuts each sequence
 // over the whole GPU; the expanding path does so once, writes and reads 16-bit tiles,
-// and has a CTA per (kv head, 256 rows).  Measured with 8 kv heads, 4 query heads each,
-// columns against expanding: 16 sequences of 1000 to 8000 tokens 88 / 164 us at 48
-// columns, 114 / 165 at 64, 167 / 165 at 96; 2 sequences of 500 to 2000 tokens 19 / 35 at
-// 96; 64 sequences of 200 to 1500 tokens (512 pairs of sequence and kv head, several for
-// every SM) 88 / 112 at 32, 127 / 112 at 48.
+// and has a CTA per (kv head, 256 rows).  So few columns go by columns, and up to 96 while
+// the pairs of sequence and kv head leave the expanding path's CTAs badly spread.
+// Measured, columns / expanding, us: 16 pairs of 500 to 2000 tokens 20 / 23 at 96
+// columns; 64 of 2000 39 / 58 at 64, 57 / 58 at 96; 128 of 1000 to 8000 113 / 155 at 64,
+// 166 / 155 at 96, of 500 31 / 23 at 48; 192 of 300 to 3000 68 / 102 at 48, 131 / 103 at 96;
+// 256 of 300 to 3000 64 / 102 at 32, 92 / 99 at 48, 118 / 100 at 64; 512 of 200 to 1500
+// 88 / 111 at 32, 127 / 113 at 48.
 static bool few_columns(int batch, int hkv, int max_q_len, int g) {
-    return (long long)max_q_len * g <= ((long long)batch * hkv < 2LL * sm_count() ? 96 : 32);
+    const long long columns = (long long)max_q_len * g;
+    return columns <= 32 || (columns <= 96 && columns * batch * hkv <= 80LL * sm_count());
 }
 
 template <bool BF16>
