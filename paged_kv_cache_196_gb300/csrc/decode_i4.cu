@@ -44,7 +44,8 @@
 // 3.6 times the bytes at 0.92 and 0.96.  Not memory but instructions bound it: about 300
 // per warp and 16 tokens, the schedulers issuing in 55 to 60% of cycles from four warps
 // each; stalls are spread over fixed latencies, busy pipes and instruction fetch.  Short
-// sequences lose the rest at the pieces' ends (queries, merge).  Tried and slower: one
+// sequences lose the rest at the pieces' ends (queries, merge): 2048 pairs of 1 to 64 tokens
+// take 29.3 us, a pair 3.7 us of a CTA's, whose rounds are mostly empty.  Tried and slower: one
 // or three blocks a warp; 3, 5, 9 or 11 warps; four warps that copy for themselves;
 // other ring depths; the products rolled into loops (89 to 95 us for the long ones).
 #include <cuda.h>
@@ -75,6 +76,11 @@ constexpr int kI4Round = NB * kI4Warps;  // blocks of a round
 constexpr int i4_pair_cost(int NT) { return NT == 1 ? 1 : 4; }
 constexpr int kI4MinRun = 2;         // shortest run: a pair's cost and a round
 constexpr int kI4ScanBatch = 4096;   // largest batch whose runs the device cuts
+// Pairs per CTA of a wave beyond which runs of whole pairs (the ring and the queries carry
+// over from pair to pair) replace a CTA for each: 2048 pairs of 1 to 64 tokens 39.0 us by a
+// CTA each, 29.3 by runs; 2000 of 20 to 200 38.8 / 30.4; 2048 of 256 55.7 / 43.6.
+constexpr int kI4UncutPairs = 2;
+constexpr int kI4ShortPair = 8;      // rounds of a pair that may better stay whole
 // The weights are 2^(s - m + 6) for a reference m that is renewed (and the state
 // rescaled) only when the maximum passes it by more than 2^8: rarely after the
 // first blocks, and exact mathematics, since sums and outputs share m.  They stay
@@ -93,9 +99,10 @@ struct I4Params {
     int batch, hq, hkv, g;
     float scale_log2;       // softmax scale * log2(e) * kScaleUnit * the pool's K scale
     float v_mul;            // kScaleUnit * the pool's V scale
-    // balanced: one run per CTA, at most max_splits to a pair.  Otherwise CTA
-    // (split, kv head, (sequence, column group)) takes part_rounds rounds.
-    int balanced;
+    // balanced: one run per CTA, at most max_splits to a pair; uncut: a run takes the
+    // pairs that begin in it whole.  Otherwise CTA (split, kv head, (sequence, column
+    // group)) takes part_rounds rounds.
+    int balanced, uncut;
     int part_rounds, max_splits;
     int cols;               // columns of a pair (the kernel's own)
     int col_groups;         // pairs that share a sequence's columns of one kv head
@@ -365,8 +372,8 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             most = max(most, s_most[y]);
         }
         // a pair of n rounds is cut into at most (n - 2) / run + 2 pieces
-        run = max((total + (int)gridDim.x - 1) / (int)gridDim.x,
-                  p.max_splits > 1 ? (most + p.max_splits - 3) / (p.max_splits - 1) : most + kPairCost);
+        run = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+        if (!p.uncut) run = max(run, (most + p.max_splits - 3) / (p.max_splits - 1));
         run = max(run, kI4MinRun);
         const long long at64 = (long long)blockIdx.x * run;
         if (at64 >= total) return;
@@ -386,6 +393,12 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
         __syncthreads();
         b0 = s_start[0], unit = s_start[1], base = s_start[2];
         todo = min(run, total - at);
+        if (p.uncut) {  // on to the first pair that begins in the run; none: todo <= 0
+            const int per_pair = i4_sequence(p, b0, kRound, kCols, false).rounds + kPairCost, in = unit % per_pair;
+            const int skip = in ? per_pair - in : 0;
+            unit += skip;
+            todo -= skip;
+        }
     } else {
         const int split = blockIdx.x;
         b0 = blockIdx.z / p.col_groups;
@@ -426,6 +439,12 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 pair = unit / per;
                 round = unit - pair * per - kPairCost;
                 if (round >= 0) return true;
+                if (p.uncut) {  // begun in this run: its rounds are this CTA's too
+                    unit -= round;
+                    todo += round;
+                    round = 0;
+                    return true;
+                }
                 ++unit;
                 --todo;
             }
@@ -437,8 +456,10 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             d.b = w.b, d.q0 = w.q0, d.T = w.T, d.L = w.L;
             d.h = pair % p.hkv, d.cg = pair / p.hkv;
             d.round0 = round;
-            d.rounds = min(w.rounds - round, todo);
-            if (p.balanced) {
+            d.rounds = p.uncut ? w.rounds : min(w.rounds - round, todo);
+            if (p.uncut) {
+                d.nsplit = 1;
+            } else if (p.balanced) {
                 const int v0 = base + pair * (w.rounds + kPairCost) + kPairCost;  // the pair's first round
                 const int c0 = v0 / run, c1 = (v0 + w.rounds - 1) / run;
                 d.nsplit = c1 - c0 + 1;
@@ -496,7 +517,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             --todo;
             ++round;
             starts = round >= w.rounds;
-            more = starts ? place() : todo > 0;
+            more = starts ? place() : p.uncut || todo > 0;
             if (more) entry();
             bool bad = false;
             if (lane == 0) {
@@ -1019,9 +1040,12 @@ static kv_status launch_i4(I4Params &p, int part_blocks, cudaStream_t s) {
     p.part_rounds = (part_blocks + kI4Round - 1) / kI4Round;
     const long long pairs = (long long)p.batch * p.col_groups * p.hkv;
     const long long units = pairs * (p.max_blocks / kI4Round + 1 + i4_pair_cost(NT));
-    p.balanced = p.max_splits > 1 && p.counters && p.batch <= kI4ScanBatch && units < (1 << 30);
+    const long long wave = (long long)MINB * sm_count();
+    p.uncut = p.max_splits == 1 && pairs > kI4UncutPairs * wave;
+    p.balanced = ((p.max_splits > 1 && p.counters) || p.uncut) && p.batch <= kI4ScanBatch && units < (1 << 30);
+    p.uncut = p.uncut && p.balanced;
     dim3 grid(p.max_splits, p.hkv, p.batch * p.col_groups);
-    if (p.balanced) grid = dim3((unsigned)std::min<long long>((long long)MINB * sm_count(), units));
+    if (p.balanced) grid = dim3((unsigned)std::min(wave, units));
     fn<<<grid, kI4Threads, smem, s>>>(p);
     return cuda_status(cudaGetLastError());
 }
@@ -1108,7 +1132,10 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
         most = std::max(most, n);
     }
     const long long wave = 2LL * sm_count(), run = std::max<long long>(kI4MinRun, (units + wave - 1) / wave);
-    if (most < 2) return KV_OK;
+    // Short pairs stay whole: cutting them costs a merge each and shortens little.  Cut /
+    // whole: 211 pairs of 83 to 1204 tokens 15.8 / 12.5 us, 500 of 1 to 508 17.2 / 15.2;
+    // but 512 of 512 to 4096 43.7 / 44.0.
+    if (most < 2 || (most <= kI4ShortPair && most <= run + 3)) return KV_OK;
     const long long pieces = (most - 2) / run + 2;
     // split_plan's partitions are whole multiples of four blocks: the split count that
     // gives at least as many

@@ -232,6 +232,28 @@ def test_decode_many_sequences(batch):
     one.close()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_runs_of_whole_sequences(d):
+    """One split and more (sequence, kv head) pairs than two for every CTA: a CTA takes
+    several pairs in turn, and each result equals that of its own CTA bit for bit."""
+    c = Cache([2500], 2, d, seed=16)
+    B = 700
+    lens = torch.tensor([(i * 911) % 2500 if i % 5 == 0 else (i * 37) % 60 for i in range(B)], dtype=torch.int32, device="cuda")
+    tables = c.t_tables.expand(B, -1).contiguous()
+    q = c.queries(B, 8, "bf16")
+    out, lse = c.decode(q, "bf16", "bf16", 1, tables=tables, lens=lens)
+    for at in range(0, B, 70):
+        part = slice(at, at + 70)
+        o, l = c.decode(q[part].contiguous(), "bf16", "bf16", 1, tables=tables[part].contiguous(), lens=lens[part].contiguous())
+        assert torch.equal(out[part], o) and torch.equal(lse[part], l)
+    bad = lens.clone()
+    bad[333] = 16 * c.width + 1  # read as far as the table goes
+    out2, _ = c.decode(q, "bf16", "bf16", 1, tables=tables, lens=bad, expect=0x1)
+    keep = torch.arange(B, device="cuda") != 333
+    assert torch.equal(out2[keep], out[keep])
+    c.close()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2])
 def test_decode_scale_of_zero_and_below(scale):
     c = Cache([100, 33], 2, 128, seed=14)
