@@ -379,7 +379,9 @@ kv_status kv_pool_set_i4_scales(kv_pool_t p, float k_scale, float v_scale);
 
 /* num_splits for paged_decode_attention_i4 from the host-known lengths, as
  * kv_decode_plan chooses it for 16-bit pools: the pieces into which the longest
- * sequence is cut when the work of the batch is spread evenly over one wave of CTAs. */
+ * sequence is cut when the work of the batch is spread evenly over one wave of CTAs, 1
+ * where sequences are short.  A captured step whose sequences grow is planned for the
+ * longest that it will see: the kernel cuts by the lengths it finds, up to the plan. */
 kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_heads,
                             int max_blocks, int *num_splits);
 
