@@ -290,8 +290,10 @@ struct ExpandLayout {
     size_t items, cuts, table, k_tiles, v_tiles, partial, bytes;
     ExpandLayout(int batch, int hkv, int g, int max_blocks, int max_q_len) {
         const int span = 2 * (128 / g), sms = sm_count();
-        const long long tiles = (long long)batch * ((max_q_len + span - 1) / span);
-        const long long extra = extra_pieces(hkv, sms), most = (max_blocks + 7) / 8;  // key tiles of a sequence
+        // a chunk is at most as long as its sequence (max_q_len may be any upper bound)
+        const long long longest = std::min<long long>(max_q_len, std::max(16LL * max_blocks, 1LL));
+        const long long tiles = batch * ((longest + span - 1) / span);
+        const long long extra = extra_pieces(hkv, sms), most = (max_blocks + 7LL) / 8;  // key tiles of a sequence
         if (most > kMinPiece) max_slots = std::min(2 * extra, tiles * ((most + kMinPiece - 1) / kMinPiece));
         max_items = tiles + (max_slots ? extra : 0);
         // a tensor map has at least one row, so a table without columns takes a block

@@ -1,0 +1,34 @@
+"""Sizes at the ends of the 4-bit calls' ranges, and inputs whose results must not
+depend on which kernel a call takes."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_196_gb300 as pk
+from _gpu import require_cuda
+from _i4 import Cache, attend, check_attention, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def test_prefill_workspace_with_an_unbounded_chunk_length():
+    """Any upper bound of the chunks' lengths may be given, the largest int too: the
+    workspace is the one for chunks as long as the table."""
+    require_cuda()
+    pool = pk.kv_pool_create(4, 16, 8, 128, pk.KV_I4)
+    for width in (1, 40, 16384):
+        size = [pk.kv_prefill_i4_workspace_size(pool, 1, 16, width, m) for m in (16 * width, 2 ** 30, 2 ** 31 - 1)]
+        assert size[1] == size[2] and (width < 40 or size[0] == size[1])
+        assert size[2] > 2 * width * 8 * 16 * 128 * 2  # the K and V tiles alone
+    pk.kv_pool_destroy(pool)
+
+
+def test_prefill_with_an_unbounded_chunk_length():
+    """The same results as with the chunks' own longest length."""
+    c = Cache([300, 129, 45], 2, 128, seed=31)
+    cu = np.array([0, 60, 189, 222])
+    q = c.queries(222, 8, "bf16")
+    out, lse = c.prefill(q, "bf16", "bf16", cu, 2 ** 31 - 1)
+    good, lse2 = c.prefill(q, "bf16", "bf16", cu, 129)
+    assert torch.equal(out, good) and torch.equal(lse, lse2)
+    c.close()
