@@ -418,7 +418,8 @@ kv_status paged_decode_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype
  * call.  A sequence with more than max_q_len query tokens is left out and sets
  * KV_DEVERR_BLOCK_RANGE.  A NaN in V of a key inside a chunk reaches the chunk's earlier
  * rows of its kv head too (a weight of zero times NaN), as in paged_prefill_attention; a
- * NaN in K or q does not.  workspace: 16-byte aligned, kv_prefill_i4_workspace_size bytes
+ * NaN in K or q does not: the rows that see it, and no others, are NaN, their lse too.
+ * workspace: 16-byte aligned, kv_prefill_i4_workspace_size bytes
  * for the same sizes. */
 kv_status kv_prefill_i4_workspace_size(kv_pool_t p, int batch, int num_q_heads, int max_blocks,
                                        int max_q_len, size_t *bytes);

@@ -565,7 +565,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 ok = false;  // nothing else to store
             }
         }
-        const float inv = l_sum > 0.f ? p.v_mul / l_sum : 0.f;
+        // PACK: only a row that saw no key has a sum of 0; one with a NaN score stays NaN,
+        // its log-sum-exp too
+        const bool seen = PACK ? l_sum != 0.f : l_sum > 0.f;
+        const float inv = seen ? p.v_mul / l_sum : 0.f;
         const size_t orow = ((size_t)(q_begin + qrow) * p.num_q_heads + head) * kPfD;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -593,7 +596,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         if (row_valid && ok && p.lse)
             p.lse[(size_t)(q_begin + qrow) * p.num_q_heads + head] =
-                l_sum > 0.f ? (m_used + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+                seen ? (m_used + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -638,11 +641,12 @@ __global__ void __launch_bounds__(kPfMergeThreads) merge_prefill_kernel(const Pr
             a.x += e * v.x, a.y += e * v.y, a.z += e * v.z, a.w += e * v.w;
             c.x += e * w.x, c.y += e * w.y, c.z += e * w.z, c.w += e * w.w;
         }
-        const float inv = den > 0.f ? p.v_mul / den : 0.f;
+        const bool seen = den != 0.f;  // NaN: stays
+        const float inv = seen ? p.v_mul / den : 0.f;
         const size_t orow = (size_t)(q_begin + qrow) * p.num_q_heads + head;
         store_out4(p.out, orow * kPfD + 4 * dq, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), p.out_type);
         store_out4(p.out, orow * kPfD + 64 + 4 * dq, make_float4(c.x * inv, c.y * inv, c.z * inv, c.w * inv), p.out_type);
-        if (p.lse && dq == 0) p.lse[orow] = den > 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+        if (p.lse && dq == 0) p.lse[orow] = seen ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
     }
 }
 

@@ -32,3 +32,34 @@ def test_prefill_with_an_unbounded_chunk_length():
     good, lse2 = c.prefill(q, "bf16", "bf16", cu, 129)
     assert torch.equal(out, good) and torch.equal(lse, lse2)
     c.close()
+
+
+@pytest.mark.parametrize("lens,g,T", [
+    ([200, 90], 2, 5),        # by columns
+    ([200, 90], 2, 60),       # expanded tiles
+    ([9000], 1, 300),         # expanded tiles, their keys cut into pieces
+])
+def test_prefill_lse_of_a_nan_row_is_nan(lens, g, T):
+    """A NaN in q or in a key: the rows that meet it have a NaN log-sum-exp beside their NaN
+    output, on every path; -inf would say that they saw no key."""
+    c = Cache(lens, 2, 128, seed=14)
+    cu = np.arange(len(lens) + 1) * T
+    q = c.queries(int(cu[-1]), 2 * g, "bf16")
+    ref, lref = c.prefill(q, "bf16", "bf16", cu, T)
+    bad = q.clone()
+    bad[2, 1, 7] = float("nan")
+    out, lse = c.prefill(bad, "bf16", "bf16", cu, T)
+    hit = torch.zeros(int(cu[-1]), 2 * g, dtype=torch.bool, device="cuda")
+    hit[2, 1] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], ref[~hit]) and torch.equal(lse[~hit], lref[~hit])
+    at = lens[0] - T + 3  # a key of the chunk
+    k = c.k[0][at:at + 1].clone()
+    k[0, 1, 3] = float("nan")
+    pk.kv_append_rope(c.pool, k.cuda(), c.v[0][at:at + 1].cuda(), pk.KV_BF16, torch.from_numpy(c.slots[0][at:at + 1]).cuda(), 1)
+    out, lse = c.prefill(q, "bf16", "bf16", cu, T)
+    hit.zero_()
+    hit[3:T, g:] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], ref[~hit]) and torch.equal(lse[~hit], lref[~hit])
+    c.close()
