@@ -416,7 +416,8 @@ kv_status paged_decode_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype
  * would leave SMs idle their keys are cut too, by the lengths on the device: results
  * then depend, within rounding, on the batch's lengths, and are the same from call to
  * call.  A sequence with more than max_q_len query tokens is left out and sets
- * KV_DEVERR_BLOCK_RANGE.  A NaN in V of a key inside a chunk reaches the chunk's earlier
+ * KV_DEVERR_BLOCK_RANGE; so does an out-of-range block id, whose keys are left out (in
+ * the decode too; a row with no key left has out = 0, lse = -inf).  A NaN in V of a key inside a chunk reaches the chunk's earlier
  * rows of its kv head too (a weight of zero times NaN), as in paged_prefill_attention; a
  * NaN in K or q does not: the rows that see it, and no others, are NaN, their lse too.
  * workspace: 16-byte aligned, kv_prefill_i4_workspace_size bytes

@@ -123,6 +123,7 @@ struct PfBars {
     uint64_t done;                // all MMAs complete
     uint32_t tmem_slot;
     int abort;
+    uint32_t gone[kPfVStages];    // PACK: bit i: block i of the V stage's tile is not there
 };
 
 // F16: q and K are fp16 (else bf16).  VF16: V already is fp16, otherwise it is
@@ -344,6 +345,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         !mbar_wait<TW>(&bars->vempty[s], ((t - kPfVStages) / kPfVStages) & 1, p.err));
             if (__shfl_sync(0xffffffffu, stop, 0)) break;
             char *dst = sV + s * kPfTileBytes;
+            if constexpr (PACK) {
+                // read by the softmax warps between their wait for this copy and their
+                // arrival for P V(t), which the stage's next tile waits for
+                const uint32_t gone = __ballot_sync(0xffffffffu, lane < 8 && 8 * t + lane < nblk && y_cur < 0);
+                if (lane == 0) bars->gone[s] = gone;
+            }
             if (lane == 0) mbar_arrive_expect_tx(&bars->vland[s], kPfTileBytes);
             __syncwarp();
             if (lane < 8) {
@@ -441,6 +448,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         bool ok = convert(0, warp);
         if (!ok) *abort_flag = 1;
         for (int j = 0; ok && j < n; ++j) {
+            const uint32_t gone = PACK ? bars->gone[j % kPfVStages] : 0u;
             // Exits are warp-uniform: the warp arrives on pfull as one.
             bool bad = *abort_flag != 0;
             if (!bad) bad = !mbar_wait<TW>(&bars->sfull[x], j & 1, p.err);
@@ -458,12 +466,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             // k <= lim.  Only tiles on the diagonal need it; the branch is
             // warp-uniform so interior tiles pay nothing.
             const int lim = (int)max(-1LL, min(127LL, qpos - key0));
-            if (__any_sync(0xffffffffu, lim < 127)) {
+            // (PACK: nor the keys of blocks that are not there, as in the 4-bit decode)
+            if (__any_sync(0xffffffffu, lim < 127 || gone)) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         if (32 * i + k > lim) sv[i][k] = __float_as_uint(-INFINITY);
+                if (gone) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (gone >> ((32 * i + k) / 16) & 1) sv[i][k] = __float_as_uint(-INFINITY);
+                }
             }
             // raw row maximum (scale > 0, so max(scale*s) = scale*max(s)),
             // eight independent chains of three-input maxima

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(256, 6) expand_i4_kernel(const char *__restric
     const int id = __ldg(tables + at);
     const bool ok = id >= 0 && id < num_blocks;
     if (h == 0 && lane == 0) new_table[at] = ok ? (int32_t)at : -1;
-    if (!ok) return;  // the prefill reports it and reads zeros
+    if (!ok) return;  // the prefill reports it and leaves its keys out
     const size_t tile = ((size_t)id * hkv + h) * 2 * kExTile;
     const char *kt = k_pool + tile, *vt = v_pool + tile;
     uint4 *ko = reinterpret_cast<uint4 *>(k_out + (at * hkv + h) * kExOut);

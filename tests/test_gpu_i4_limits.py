@@ -63,3 +63,43 @@ def test_prefill_lse_of_a_nan_row_is_nan(lens, g, T):
     assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
     assert torch.equal(out[~hit], ref[~hit]) and torch.equal(lse[~hit], lref[~hit])
     c.close()
+
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 2 ** 31 - 1, "past"])
+@pytest.mark.parametrize("lens,hkv,g,T", [
+    ([100, 90], 2, 2, 4),        # by columns
+    ([100, 90], 2, 2, 60),       # expanded tiles
+    ([700, 300], 1, 4, 260),     # several key tiles
+    ([9000], 1, 2, 260),         # keys cut into pieces, some without a block that is not there
+])
+def test_prefill_leaves_out_the_keys_of_bad_blocks(lens, hkv, g, T, bad):
+    """A block id out of range: its keys have no weight, on every path. Blocks of the cached
+    part, of the chunk and a whole key tile are missing."""
+    c = Cache(lens, hkv, 128, seed=16)
+    cu = np.arange(len(lens) + 1) * T
+    q = c.queries(int(cu[-1]), hkv * g, "bf16")
+    tables = c.tables.copy()
+    gone = [0, (lens[0] - T // 2) // 16] + (list(range(8, 16)) if lens[0] > 400 else [])
+    tables[0, gone] = c.nb if bad == "past" else bad
+    out, lse = c.prefill(q, "bf16", "f32", cu, T, tables=torch.from_numpy(tables).cuda(), expect=0x1)
+    o64, l64, q64 = f64(out), f64(lse), f64(q)
+    for b, n in enumerate(lens):
+        there = np.ones(n, bool)
+        if b == 0:
+            for i in gone:
+                there[16 * i:16 * i + 16] = False
+        rows = slice(cu[b], cu[b + 1])
+        seen = [int(there[:n - T + i + 1].sum()) for i in range(T)]
+        ref = attend(q64[rows], c.kv[b][there], c.vv[b][there], 128 ** -0.5, seen)
+        check_attention(o64[rows], l64[rows], ref, 128 ** -0.5, n, "f32", 2.0 ** -11, f"seq {b}", floor=2.0 ** -24)
+    c.close()
+
+
+@pytest.mark.parametrize("T", [4, 60])
+def test_prefill_without_a_block_that_is_there(T):
+    """No key left: rows of zeros and a log-sum-exp of -inf, as an empty sequence's."""
+    c = Cache([60], 2, 128, seed=17)
+    q = c.queries(T, 4, "f16")
+    out, lse = c.prefill(q, "f16", "f16", [0, T], T, tables=torch.full_like(c.t_tables, -1), expect=0x1)
+    assert torch.all(out == 0) and torch.isneginf(lse).all()
+    c.close()
