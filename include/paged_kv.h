@@ -388,13 +388,15 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
 /* paged_decode_attention over a KV_I4 pool.  q is of type q_dtype (KV_BF16 or
  * KV_F16), out of q_dtype or KV_F32, both 16-byte aligned; seq_order as in
  * paged_append_and_decode or NULL; the workspace is kv_decode_workspace_size bytes
- * for the same num_splits (16-byte aligned).  With num_splits = 1 every (sequence, kv
- * head) is one CTA's.  Otherwise, for batches up to 4096 with at most 65536 (sequence,
- * kv head) pairs, the kernel itself cuts the batch into equal runs of 224 tokens from
- * the lengths on the device, a sequence into no more pieces than kv_decode_split_plan
- * gives for num_splits (seq_order has no part in it); larger ones are cut as that plan
- * says.  So results depend, within rounding, on the batch's lengths; they do not depend
- * on where the blocks sit, and are the same from call to call.
+ * for the same num_splits (16-byte aligned; never less than the call takes).
+ * num_splits = n plans partitions of ceil(max_blocks / n) blocks, rounded up to a multiple of
+ * four, 0 those of kv_decode_split_plan.  With n = 1 no (sequence, kv head) is cut, whatever
+ * the table's width, and no workspace is needed.  Otherwise, for batches up to 4096 with at
+ * most 65536 (sequence, kv head) pairs, the kernel itself cuts the batch into equal runs of
+ * 224 tokens from the lengths on the device, a sequence into no more pieces than a table row
+ * has partitions (seq_order has no part in it); larger ones are cut into the partitions.
+ * So results depend, within rounding, on the batch's lengths; they do not depend on where
+ * the blocks sit, and are the same from call to call.
  * K and V enter the tensor cores exactly (fp16 holds every c * s); q enters in
  * fp16, scaled per head by a power of two (exact but for elements below 2^-27 of
  * the head's largest); the softmax weights in fp16, with KV_F32 output in two fp16

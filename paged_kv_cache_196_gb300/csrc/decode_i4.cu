@@ -1024,6 +1024,23 @@ __global__ void __launch_bounds__(kI4MergeThreads) merge_i4_kernel(const I4Param
     if (p.lse && d4 == 0) p.lse[orow] = den != 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
 }
 
+// The split plan of an explicit num_splits: as split_plan, without the longest partition
+// that the 16-bit kernels' table slice in shared memory allows (this kernel reads the table
+// as it goes), so that 1 means whole sequences however wide the table is.  Never more
+// partitions than split_plan's, whose workspace serves.  Under a table of 8192 columns, with
+// that limit / without: 256 sequences of 1 to 64 tokens (8 kv heads of 4) 31.3 / 29.1 us, 500
+// of 1 to 508 (2 of 3) 26.9 / 25.8.
+static void i4_split_plan(int batch, int num_kv_heads, int max_blocks, int num_splits, int *part_blocks,
+                          int *max_splits) {
+    if (num_splits <= 0 || max_blocks <= 0) {
+        split_plan(batch, num_kv_heads, max_blocks, num_splits, part_blocks, max_splits);
+        return;
+    }
+    const long long pb = ((long long)max_blocks + num_splits - 1) / num_splits;
+    *part_blocks = (int)((pb + 3) / 4 * 4);
+    *max_splits = (int)(((long long)max_blocks + *part_blocks - 1) / *part_blocks);
+}
+
 cudaError_t set_wait_limit_decode_i4(unsigned long long ns) { return set_wait_limit_here(ns); }
 
 template <int D, int NT, int NST, int MINB>
@@ -1054,7 +1071,7 @@ kv_status attend_i4(const I4Call &a) {
     kv_pool *pool = a.pool;
     const int g = a.num_q_heads / pool->num_kv_heads;
     int pb = 0, ms = 0;
-    split_plan(a.batch, pool->num_kv_heads, a.max_blocks, a.num_splits, &pb, &ms);
+    i4_split_plan(a.batch, pool->num_kv_heads, a.max_blocks, a.num_splits, &pb, &ms);
     const long long rows = (long long)a.batch * a.max_q_len;
     if (rows > INT32_MAX) return KV_ERR_UNSUPPORTED;
     const size_t need = decode_workspace_bytes((int)rows, a.num_q_heads, pool->head_dim, ms);
@@ -1137,11 +1154,11 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
     // but 512 of 512 to 4096 43.7 / 44.0.
     if (most < 2 || (most <= kI4ShortPair && most <= run + 3)) return KV_OK;
     const long long pieces = (most - 2) / run + 2;
-    // split_plan's partitions are whole multiples of four blocks: the split count that
+    // i4_split_plan's partitions are whole multiples of four blocks: the split count that
     // gives at least as many
     for (int s = (int)std::min<long long>(pieces, max_blocks);; ++s) {
         int pb, ms;
-        split_plan(batch, num_kv_heads, max_blocks, s, &pb, &ms);
+        i4_split_plan(batch, num_kv_heads, max_blocks, s, &pb, &ms);
         *num_splits = s;
         if (ms >= pieces || pb <= 4 || s >= max_blocks) break;
     }

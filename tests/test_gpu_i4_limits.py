@@ -103,3 +103,48 @@ def test_prefill_without_a_block_that_is_there(T):
     out, lse = c.prefill(q, "f16", "f16", [0, T], T, tables=torch.full_like(c.t_tables, -1), expect=0x1)
     assert torch.all(out == 0) and torch.isneginf(lse).all()
     c.close()
+
+
+@pytest.mark.parametrize("batch", [40, 400, 4100])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_of_one_split_under_a_wide_table(batch, d):
+    """One split means whole sequences, without a workspace, for a table of a long-context
+    model's width too: the bits of the narrow table's call, below and above the number of
+    pairs that one wave takes and past the batch that the device cuts."""
+    c = Cache([500], 2, d, seed=18)
+    lens = torch.tensor([(37 * b) % 501 for b in range(batch)], dtype=torch.int32, device="cuda")
+    q = c.queries(batch, 8, "bf16")
+    outs = []
+    for width in (c.width, 8192):
+        tables = torch.full((batch, width), -1, dtype=torch.int32, device="cuda")
+        tables[:, :c.width] = c.t_tables[0]
+        out, lse = torch.empty_like(q), torch.empty(batch, 8, device="cuda")
+        pk.paged_decode_attention_i4(c.pool, q, pk.KV_BF16, tables, width, lens, batch, 8, d ** -0.5, out, pk.KV_BF16, lse, 1)
+        assert pk.kv_get_device_error(c.pool) == 0
+        outs.append((out, lse))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    for b in range(0, batch, max(1, batch // 12)):
+        n = int(lens[b])
+        ref = attend(f64(q[b:b + 1]), c.kv[0][:n], c.vv[0][:n], d ** -0.5, [n])
+        check_attention(f64(outs[1][0][b:b + 1]), f64(outs[1][1][b:b + 1]), ref, d ** -0.5, n, "bf16", 2.0 ** -11, f"seq {b}")
+    c.close()
+
+
+@pytest.mark.parametrize("splits", [2, 5, 40])
+def test_decode_of_long_sequences_under_a_wide_table(splits):
+    """More splits than one: planned over the table's width, within the workspace of the
+    general rule."""
+    c = Cache([20000, 33, 0, 4100], 1, 128, seed=19)
+    width = 16384
+    tables = torch.full((4, width), -1, dtype=torch.int32, device="cuda")
+    tables[:, :c.width] = c.t_tables
+    q = c.queries(4, 4, "bf16")
+    out, lse = torch.empty(4, 4, 128, device="cuda"), torch.empty(4, 4, device="cuda")
+    n = pk.kv_decode_workspace_size(4, 4, 1, 128, width, splits)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    pk.paged_decode_attention_i4(c.pool, q, pk.KV_BF16, tables, width, c.t_lens, 4, 4, 128 ** -0.5, out, pk.KV_F32, lse, splits, ws, n)
+    assert pk.kv_get_device_error(c.pool) == 0
+    for b, m in enumerate(c.lens):
+        ref = attend(f64(q)[b:b + 1], c.kv[b], c.vv[b], 128 ** -0.5, [int(m)])
+        check_attention(f64(out)[b:b + 1], f64(lse)[b:b + 1], ref, 128 ** -0.5, int(m), "f32", 2.0 ** -21, f"seq {b}")
+    c.close()
