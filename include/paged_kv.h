@@ -396,7 +396,9 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
  * 224 tokens from the lengths on the device, a sequence into no more pieces than a table row
  * has partitions (seq_order has no part in it); larger ones are cut into the partitions.
  * So results depend, within rounding, on the batch's lengths; they do not depend on where
- * the blocks sit, and are the same from call to call.
+ * the blocks sit, and are the same from call to call.  KV_ERR_UNSUPPORTED for batch or kv
+ * heads > 65535, more than 65535 partitions, max_blocks > 2^27 - 1 and more than 2^31 - 1
+ * (sequence, kv head, partition).
  * K and V enter the tensor cores exactly (fp16 holds every c * s); q enters in
  * fp16, scaled per head by a power of two (exact but for elements below 2^-27 of
  * the head's largest); the softmax weights in fp16, with KV_F32 output in two fp16
@@ -422,8 +424,11 @@ kv_status paged_decode_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype
  * the decode too; a row with no key left has out = 0, lse = -inf).  A NaN in V of a key inside a chunk reaches the chunk's earlier
  * rows of its kv head too (a weight of zero times NaN), as in paged_prefill_attention; a
  * NaN in K or q does not: the rows that see it, and no others, are NaN, their lse too.
- * workspace: 16-byte aligned, kv_prefill_i4_workspace_size bytes
- * for the same sizes. */
+ * workspace: 16-byte aligned, kv_prefill_i4_workspace_size bytes for the same sizes.
+ * Both calls return KV_ERR_UNSUPPORTED for the same sizes: batch or kv heads > 65535, more
+ * than 8 query heads per kv head, and, where tiles are expanded, a batch * max_blocks * kv
+ * heads * 16 of more than 2^31 - 1 (by columns, max_blocks > 2^27 - 1 or a grid of as many
+ * CTAs). */
 kv_status kv_prefill_i4_workspace_size(kv_pool_t p, int batch, int num_q_heads, int max_blocks,
                                        int max_q_len, size_t *bytes);
 kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype,

@@ -100,8 +100,8 @@ struct I4Params {
     float scale_log2;       // softmax scale * log2(e) * kScaleUnit * the pool's K scale
     float v_mul;            // kScaleUnit * the pool's V scale
     // balanced: one run per CTA, at most max_splits to a pair; uncut: a run takes the
-    // pairs that begin in it whole.  Otherwise CTA (split, kv head, (sequence, column
-    // group)) takes part_rounds rounds.
+    // pairs that begin in it whole.  Otherwise CTA ((sequence, column group), kv head,
+    // split), splits next to each other, takes part_rounds rounds.
     int balanced, uncut;
     int part_rounds, max_splits;
     int cols;               // columns of a pair (the kernel's own)
@@ -400,10 +400,11 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             todo -= skip;
         }
     } else {
-        const int split = blockIdx.x;
-        b0 = blockIdx.z / p.col_groups;
-        const int cg = blockIdx.z % p.col_groups;
-        const bool reports = tid == 0 && split == 0 && blockIdx.y == 0 && cg == 0;
+        const int at = blockIdx.x / p.max_splits, split = blockIdx.x - at * p.max_splits;
+        const int row = at / p.hkv, h = at - row * p.hkv;
+        b0 = row / p.col_groups;
+        const int cg = row - b0 * p.col_groups;
+        const bool reports = tid == 0 && split == 0 && h == 0 && cg == 0;
         if (p.seq_order) {
             b0 = __ldg(p.seq_order + b0);
             if (b0 < 0 || b0 >= p.batch) {  // not a permutation of the batch
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             }
         }
         const I4Work w = i4_sequence(p, b0, kRound, kCols, reports);
-        const int pair = cg * p.hkv + blockIdx.y, r0 = split * p.part_rounds;
+        const int pair = cg * p.hkv + h, r0 = split * p.part_rounds;
         if (pair >= w.pairs || r0 >= w.rounds) return;
         base = 0;
         unit = pair * (w.rounds + kPairCost) + kPairCost + r0;
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 d.split = blockIdx.x - c0;
             } else {
                 d.nsplit = (w.rounds + p.part_rounds - 1) / p.part_rounds;
-                d.split = blockIdx.x;
+                d.split = round / p.part_rounds;
             }
             return d;
         };
@@ -1061,10 +1062,25 @@ static kv_status launch_i4(I4Params &p, int part_blocks, cudaStream_t s) {
     p.uncut = p.max_splits == 1 && pairs > kI4UncutPairs * wave;
     p.balanced = ((p.max_splits > 1 && p.counters) || p.uncut) && p.batch <= kI4ScanBatch && units < (1 << 30);
     p.uncut = p.uncut && p.balanced;
-    dim3 grid(p.max_splits, p.hkv, p.batch * p.col_groups);
-    if (p.balanced) grid = dim3((unsigned)std::min(wave, units));
-    fn<<<grid, kI4Threads, smem, s>>>(p);
+    const long long grid = p.balanced ? std::min(wave, units) : pairs * p.max_splits;
+    fn<<<(unsigned)grid, kI4Threads, smem, s>>>(p);
     return cuda_status(cudaGetLastError());
+}
+
+// Tiles of eight columns of a pair and pairs of one (sequence, kv head) for its columns.
+static void i4_columns(int cols, int *nt, int *groups) {
+    *nt = cols <= 24 ? (cols + 7) / 8 : 2;  // more: groups of 16 (a fourth tile of eight does not fit)
+    *groups = (cols + 8 * *nt - 1) / (8 * *nt);
+}
+
+kv_status attend_i4_limits(int batch, int num_kv_heads, int cols, int max_blocks, int max_splits) {
+    int nt, groups;
+    i4_columns(cols, &nt, &groups);
+    // the merge's grid; a count of pieces in 16 bits; keys; the grid of CTAs per partition
+    if (batch > 65535 || max_splits > 65535 || num_kv_heads > 65535 || max_blocks > INT32_MAX / kI4BS ||
+        (long long)batch * groups * num_kv_heads > INT32_MAX / max_splits)
+        return KV_ERR_UNSUPPORTED;
+    return KV_OK;
 }
 
 kv_status attend_i4(const I4Call &a) {
@@ -1078,11 +1094,9 @@ kv_status attend_i4(const I4Call &a) {
     if (need > 0 && (!a.workspace || a.workspace_bytes < need)) return KV_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(a.workspace) & 15) return KV_ERR_ARG;
     const int cols = a.max_q_len * g;  // of one (sequence, kv head)
-    const int nt = cols <= 24 ? (cols + 7) / 8 : 2;  // more: groups of 16 (a fourth tile of eight does not fit)
-    const int groups = (cols + 8 * nt - 1) / (8 * nt);
-    if (ms > 65535 || (long long)a.batch * groups > 65535 || pool->num_kv_heads > 65535 ||
-        a.max_blocks > INT32_MAX / kI4BS)
-        return KV_ERR_UNSUPPORTED;
+    int nt, groups;
+    i4_columns(cols, &nt, &groups);
+    if (kv_status st = attend_i4_limits(a.batch, pool->num_kv_heads, cols, a.max_blocks, ms)) return st;
     I4Params p{};
     p.q = static_cast<const uint16_t *>(a.q);
     p.q_bf16 = a.q_dtype == KV_BF16;

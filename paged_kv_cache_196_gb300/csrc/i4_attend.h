@@ -25,8 +25,12 @@ struct I4Call {
     cudaStream_t stream;
 };
 
+// KV_ERR_UNSUPPORTED: sizes past a limit of the launch.  cols: query tokens x heads of a
+// (sequence, kv head); max_splits: partitions of a table row.
+kv_status attend_i4_limits(int batch, int num_kv_heads, int cols, int max_blocks, int max_splits);
+
 // Launches the attention of checked arguments; KV_ERR_ARG: the workspace is too
-// small, KV_ERR_UNSUPPORTED: a grid limit.
+// small, KV_ERR_UNSUPPORTED: attend_i4_limits.
 kv_status attend_i4(const I4Call &a);
 
 }  // namespace pkv

@@ -320,13 +320,18 @@ kv_status kv_prefill_i4_workspace_size(kv_pool_t p, int batch, int num_q_heads, 
     if (!p || !bytes || batch < 0 || num_q_heads <= 0 || max_blocks < 0 || max_q_len < 0) return KV_ERR_ARG;
     if (p->dtype != KV_I4 || p->head_dim != kExD) return KV_ERR_UNSUPPORTED;
     if (num_q_heads % p->num_kv_heads) return KV_ERR_ARG;
-    if (num_q_heads / p->num_kv_heads > 8 || batch > 65535) return KV_ERR_UNSUPPORTED;
-    if (few_columns(batch, p->num_kv_heads, max_q_len, num_q_heads / p->num_kv_heads)) {
+    const int hkv = p->num_kv_heads, g = num_q_heads / hkv;
+    // what the call refuses (it asks here too)
+    if (g > 8 || batch > 65535 || hkv > 65535) return KV_ERR_UNSUPPORTED;
+    if (few_columns(batch, hkv, max_q_len, g)) {
         int pb, ms;
-        split_plan(batch, p->num_kv_heads, max_blocks, 0, &pb, &ms);
+        split_plan(batch, hkv, max_blocks, 0, &pb, &ms);
+        if (kv_status st = attend_i4_limits(batch, hkv, max_q_len * g, max_blocks, ms)) return st;
         *bytes = decode_workspace_bytes(batch * max_q_len, num_q_heads, kExD, ms);
     } else {
-        *bytes = ExpandLayout(batch, p->num_kv_heads, num_q_heads / p->num_kv_heads, max_blocks, max_q_len).bytes;
+        const ExpandLayout at(batch, hkv, g, max_blocks, max_q_len);
+        if (at.blocks > INT32_MAX / 16 / hkv) return KV_ERR_UNSUPPORTED;  // a tensor map's rows; bounds the items too
+        *bytes = at.bytes;
     }
     return KV_OK;
 }
@@ -348,7 +353,6 @@ kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtyp
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(workspace)) & 15)
         return KV_ERR_ARG;
     if (!(scale > 0.f)) return KV_ERR_ARG;
-    if (batch > 65535) return KV_ERR_UNSUPPORTED;
     size_t need = 0;
     if (kv_status st = kv_prefill_i4_workspace_size(p, batch, num_q_heads, max_blocks, max_q_len, &need)) return st;
     if (need > 0 && (!workspace || workspace_bytes < need)) return KV_ERR_ARG;
@@ -383,7 +387,6 @@ kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtyp
     const bool cut = at.max_slots > 0 && tiles * hkv < (batch == 1 ? 1LL : 2LL) * sm_count();
     const long long max_items = std::min(at.max_items, tiles + (cut ? extra_pieces(hkv, sm_count()) : 0));
     const long long rows = at.blocks * hkv * 16;
-    if (rows > INT32_MAX || hkv > 65535 || max_items * hkv > INT32_MAX) return KV_ERR_UNSUPPORTED;
     char *ws = static_cast<char *>(workspace);
     PrefillCounts *counts = reinterpret_cast<PrefillCounts *>(ws);
     int *cuts = reinterpret_cast<int *>(ws + at.cuts);

@@ -148,3 +148,50 @@ def test_decode_of_long_sequences_under_a_wide_table(splits):
         ref = attend(f64(q)[b:b + 1], c.kv[b], c.vv[b], 128 ** -0.5, [int(m)])
         check_attention(f64(out)[b:b + 1], f64(lse)[b:b + 1], ref, 128 ** -0.5, int(m), "f32", 2.0 ** -21, f"seq {b}")
     c.close()
+
+
+def test_prefill_of_many_drafts():
+    """40000 sequences of up to 4 drafted tokens with 8 heads per kv head: two groups of
+    columns each, more (sequence, group) pairs than a grid's second dimensions hold."""
+    c = Cache([60], 1, 128, seed=20)
+    B, T = 40000, 4
+    t = np.array([(b % 5) for b in range(B)])
+    t[[0, B - 1]] = T
+    cu = np.concatenate([[0], np.cumsum(t)])
+    lens = np.array([4 + (7 * b) % 57 for b in range(B)], np.int32)
+    q = c.queries(1, 8, "bf16").expand(int(cu[-1]), -1, -1).contiguous()
+    q *= torch.linspace(0.5, 1.5, q.shape[0], device="cuda")[:, None, None].to(q.dtype)
+    out, lse = c.prefill(q, "bf16", "f32", cu, T, tables=c.t_tables.expand(B, -1).contiguous(), lens=torch.from_numpy(lens).cuda())
+    for b in list(range(0, B, 1999)) + [32767, 32768, 32769, B - 2, B - 1]:
+        n, rows = int(lens[b]), slice(int(cu[b]), int(cu[b + 1]))
+        if not t[b]:
+            continue
+        ref = attend(f64(q[rows]), c.kv[0][:n], c.vv[0][:n], 128 ** -0.5, [n - t[b] + i + 1 for i in range(t[b])])
+        check_attention(f64(out[rows]), f64(lse[rows]), ref, 128 ** -0.5, n, "f32", 2.0 ** -11, f"seq {b}", floor=2.0 ** -24)
+    c.close()
+
+
+def test_prefill_size_and_call_refuse_the_same():
+    """What the call cannot do its workspace query refuses too."""
+    require_cuda()
+    pool = pk.kv_pool_create(4, 16, 8, 128, pk.KV_I4)
+    t = torch.zeros(1 << 14, dtype=torch.float32, device="cuda")
+    i = torch.zeros(64, dtype=torch.int32, device="cuda")
+
+    def both(batch, hq, width, most):
+        with pytest.raises(pk.KVError) as e:
+            pk.kv_prefill_i4_workspace_size(pool, batch, hq, width, most)
+        assert e.value.status == -3
+        with pytest.raises(pk.KVError) as e:
+            pk.paged_prefill_attention_i4(pool, t, pk.KV_BF16, i, 1, most, i, width, i, batch, hq, 1.0, t, pk.KV_F32, None, t, 2 ** 62)
+        assert e.value.status == -3
+
+    both(3, 8, 6_000_000, 400)              # expanded: rows of the tiles past 2^31
+    both(65535, 8, 2 ** 31 - 1, 2 ** 31 - 1)
+    both(1, 8, 2 ** 27, 4)                  # by columns: keys past 2^31
+    both(65535, 64, 2 ** 27 - 1, 4)         # a grid of as many CTAs
+    both(65536, 8, 3, 4)
+    both(1, 72, 3, 4)
+    assert pk.kv_prefill_i4_workspace_size(pool, 3, 8, 5_000_000, 400) > 3 * 5_000_000 * 8 * 8192
+    assert pk.kv_get_device_error(pool) == 0
+    pk.kv_pool_destroy(pool)
