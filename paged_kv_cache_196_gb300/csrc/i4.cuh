@@ -67,9 +67,14 @@ KV_DEVICE constexpr int v_swizzle(int p) {
     return D == 128 ? 8 * (p & 3) : 8 * ((p >> 1) & 1);
 }
 
-// x / d by its reciprocal r (to an ulp or so) and one correction step, the usual
-// division by iteration: the quotient's error before the last rounding is of the order
-// of 2^-46.
+// x / d from an approximate reciprocal r of d: a first quotient q = x r, its residual
+// x - q d, and the correction q + (x - q d) r, Newton's step for the quotient in the form
+// that a fused multiply-add allows (P. Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", IBM J. Res. Dev. 34, 1990).
+// Error: with r = (1 + e) / d, |e| <= 2^-22, q is x / d (1 + e') with |e'| <= |e| + 2^-24;
+// the residual is exact (both terms are multiples of q's last place times d's, and their
+// difference is small) and the correction leaves x / d (1 - e e'), so the result is the
+// rounding of a number within 2^-43 of the quotient, relatively.
 KV_DEVICE float divide(float x, float d, float r) {
     const float q = __fmul_rn(x, r);
     return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
@@ -81,9 +86,10 @@ KV_DEVICE float reciprocal(float x) {
     return r;
 }
 
-// The scale byte of a group with largest magnitude m.  The e4m3 borders times 7 have
-// at most 8 significant bits: m / 7, rounded correctly, lies on the right side of (or
-// on) each of them, as for codes8.
+// The scale byte of a group with largest magnitude m.  A border b between two e4m3
+// values has 5 significant bits, 7 b at most 8: m = 7 b comes out as b exactly, and an m
+// one last place away is at least 4 / 7 of b's last place from b after the division
+// (ulp(7 b) is 4 or 8 times ulp(b)), so it does not round to b.
 KV_DEVICE uint32_t scale_byte(float m) {
     m = m > 1e30f ? 1e30f : m;  // an infinity would leave NaN; NaN stays
     return e4m3_of(divide(m, 7.f, 1.f / 7.f));
@@ -94,8 +100,10 @@ KV_DEVICE uint32_t scale_byte(float m) {
 //
 // c = rint(x / s) must be decided as exact arithmetic decides it: values of 16
 // bits are often exactly between two codes.  A border (k + 1/2) s has at most 8
-// significant bits; a quotient that is one of them comes out exactly, and any other
-// fp32 x is further from it than half an ulp of the quotient.  Clamping x to +-7.25 s
+// significant bits: x on it gives k + 1/2 exactly.  An x one last place away is at
+// least 8 / 15 of the quotient's last place from it after the division (s's mantissa is
+// at most 15 / 8; a border that is a power of two has s a power of two, an exact
+// division), so it does not round to it.  Clamping x to +-7.25 s
 // first (exact) keeps infinities and |c| > 7 out.  rint and the bias are one addition
 // of 1.5 * 2^23 + 8.
 KV_DEVICE uint32_t codes8(const float (&x)[8], float s) {
