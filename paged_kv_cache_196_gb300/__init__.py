@@ -177,9 +177,11 @@ def _ptr(x):
     if x is None:
         return None
     try:
-        return x.data_ptr()  # a tensor: the case of every hot call
+        data_ptr = x.data_ptr  # a tensor: the case of every hot call
     except AttributeError:
         pass
+    else:
+        return data_ptr()  # what it raises is the caller's to see
     if isinstance(x, int):
         return x
     if hasattr(x, "ctypes"):
