@@ -398,7 +398,8 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
  * So results depend, within rounding, on the batch's lengths; they do not depend on where
  * the blocks sit, and are the same from call to call.  KV_ERR_UNSUPPORTED for batch or kv
  * heads > 65535, more than 65535 partitions, max_blocks > 2^27 - 1 and more than 2^31 - 1
- * (sequence, kv head, partition).
+ * (sequence, kv head, partition).  A scale that is no finite number makes every row with a
+ * key NaN.
  * K and V enter the tensor cores exactly (fp16 holds every c * s); q enters in
  * fp16, scaled per head by a power of two (exact but for elements below 2^-27 of
  * the head's largest); the softmax weights in fp16, with KV_F32 output in two fp16
@@ -412,7 +413,8 @@ kv_status paged_decode_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype
                                     size_t workspace_bytes, void *stream);
 
 /* paged_prefill_attention over a KV_I4 pool (head_dim 128, q of type q_dtype
- * KV_BF16 or KV_F16, out of q_dtype or KV_F32, q and out 16-byte aligned, scale > 0).
+ * KV_BF16 or KV_F16, out of q_dtype or KV_F32, q and out 16-byte aligned, scale > 0 and
+ * finite, times the pool's scale of K too).
  * Few query tokens per sequence (a step over drafted tokens) run on the decode's kernel
  * with a column per (query token, head).  Otherwise the blocks of the batch are first
  * expanded to 16-bit tiles in the workspace, once for all their query tiles and heads

@@ -284,9 +284,10 @@ KV_DEVICE void put_query(const I4Params &p, const uint32_t (&two)[D / 64], int c
     const int e = (int)(__float_as_uint(m) >> 23);
     const int up = e == 0 || e == 255 ? 0 : max(-126, min(126, 127 + 13 - e));
     // the score's factor is made positive (its sign goes to q), so that scaling keeps the
-    // order of scores; a factor of 0 zeroes q instead
-    const bool zero = p.scale_log2 == 0.f;
-    const float mul = copysignf(zero ? 0.f : __uint_as_float((uint32_t)(127 + up) << 23), p.scale_log2);
+    // order of scores; a factor of 0 zeroes q instead, and one that is no number makes it
+    // NaN (a score's factor of NaN would reach masked keys too)
+    const bool zero = p.scale_log2 == 0.f, finite = fabsf(p.scale_log2) < INFINITY;
+    const float mul = finite ? copysignf(zero ? 0.f : __uint_as_float((uint32_t)(127 + up) << 23), p.scale_log2) : NAN;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         // dimension d: quarter cq, word in / 8, four bits in % 4 of half in / 4 % 2
@@ -295,7 +296,7 @@ KV_DEVICE void put_query(const I4Params &p, const uint32_t (&two)[D / 64], int c
         qs[((((to >> 1) * NT + (col >> 3)) * 32 + (col & 7) * 4 + cq) * 2 + (to & 1)) * 2 + hi] = __float2half_rn(x[i] * mul);
     }
     if (lane == 0)
-        scale[col] = zero ? 1.f : fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 - up) << 23), 1e-37f);
+        scale[col] = zero || !finite ? 1.f : fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 - up) << 23), 1e-37f);
 }
 
 // D: head dim.  NT: columns / 8 of a CTA.  EXACT: weights in two fp16 parts (fp32

@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "common.cuh"
@@ -352,7 +353,8 @@ kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtyp
     if (!q || !cu_q || !block_tables || !seq_lens || !out) return KV_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(workspace)) & 15)
         return KV_ERR_ARG;
-    if (!(scale > 0.f)) return KV_ERR_ARG;
+    // what the kernels multiply scores by has to be a number above 0
+    if (!(scale > 0.f) || !std::isfinite(scale * i4::kScaleUnit * p->k_scale * 1.4426950408889634f)) return KV_ERR_ARG;
     size_t need = 0;
     if (kv_status st = kv_prefill_i4_workspace_size(p, batch, num_q_heads, max_blocks, max_q_len, &need)) return st;
     if (need > 0 && (!workspace || workspace_bytes < need)) return KV_ERR_ARG;

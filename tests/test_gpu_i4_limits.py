@@ -195,3 +195,30 @@ def test_prefill_size_and_call_refuse_the_same():
     assert pk.kv_prefill_i4_workspace_size(pool, 3, 8, 5_000_000, 400) > 3 * 5_000_000 * 8 * 8192
     assert pk.kv_get_device_error(pool) == 0
     pk.kv_pool_destroy(pool)
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_scale_that_is_no_number(scale, d):
+    """Every row with a key is NaN, as the formula has it; an empty sequence keeps its 0."""
+    c = Cache([700, 0, 33], 2, d, seed=22)
+    q = c.queries(3, 4, "bf16")
+    for splits in (1, 3):
+        out, lse = c.decode(q, "bf16", "f32", splits, scale=scale)
+        assert torch.isnan(out[[0, 2]]).all() and torch.isnan(lse[[0, 2]]).all()
+        assert torch.all(out[1] == 0) and torch.isneginf(lse[1]).all()
+    c.close()
+
+
+@pytest.mark.parametrize("most", [4, 400])
+def test_prefill_refuses_a_scale_that_is_no_number(most):
+    require_cuda()
+    pool = pk.kv_pool_create(4, 16, 2, 128, pk.KV_I4)
+    pk.kv_pool_set_i4_scales(pool, 2.0 ** 20, 1.0)
+    t = torch.zeros(1 << 14, dtype=torch.float32, device="cuda")
+    i = torch.zeros(64, dtype=torch.int32, device="cuda")
+    for scale in (float("nan"), float("inf"), 3e38, 2e30):  # the last: times the pool's scale past fp32
+        with pytest.raises(pk.KVError) as e:
+            pk.paged_prefill_attention_i4(pool, t, pk.KV_BF16, i, 1, most, i, 3, i, 1, 4, scale, t, pk.KV_F32, None, t, 2 ** 62)
+        assert e.value.status == -1
+    pk.kv_pool_destroy(pool)
