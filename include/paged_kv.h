@@ -398,7 +398,7 @@ kv_status kv_decode_plan_i4(const int32_t *host_seq_lens, int batch, int num_kv_
  * So results depend, within rounding, on the batch's lengths; they do not depend on where
  * the blocks sit, and are the same from call to call.  KV_ERR_UNSUPPORTED for batch or kv
  * heads > 65535, more than 65535 partitions, max_blocks > 2^27 - 1 and more than 2^31 - 1
- * (sequence, kv head, partition).  A scale that is no finite number makes every row with a
+ * (sequence, partition).  A scale that is no finite number makes every row with a
  * key NaN.
  * K and V enter the tensor cores exactly (fp16 holds every c * s); q enters in
  * fp16, scaled per head by a power of two (exact but for elements below 2^-27 of

@@ -80,6 +80,7 @@ constexpr int kI4ScanBatch = 4096;   // largest batch whose runs the device cuts
 // over from pair to pair) replace a CTA for each: 2048 pairs of 1 to 64 tokens 39.0 us by a
 // CTA each, 29.3 by runs; 2000 of 20 to 200 38.8 / 30.4; 2048 of 256 55.7 / 43.6.
 constexpr int kI4UncutPairs = 2;
+constexpr int kI4MaxRows = 65535;    // of a grid's third dimension
 constexpr int kI4ShortPair = 8;      // rounds of a pair that may better stay whole
 // The weights are 2^(s - m + 6) for a reference m that is renewed (and the state
 // rescaled) only when the maximum passes it by more than 2^8: rarely after the
@@ -100,8 +101,9 @@ struct I4Params {
     float scale_log2;       // softmax scale * log2(e) * kScaleUnit * the pool's K scale
     float v_mul;            // kScaleUnit * the pool's V scale
     // balanced: one run per CTA, at most max_splits to a pair; uncut: a run takes the
-    // pairs that begin in it whole.  Otherwise CTA ((sequence, column group), kv head,
-    // split), splits next to each other, takes part_rounds rounds.
+    // pairs that begin in it whole.  Otherwise CTA (split, kv head, (sequence, column
+    // group)) takes part_rounds rounds; what the grid's third dimension does not hold of
+    // the last follows in the first, max_splits further each time.
     int balanced, uncut;
     int part_rounds, max_splits;
     int cols;               // columns of a pair (the kernel's own)
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
 
     // ---- this CTA's run: `todo` units (rounds and pair costs) from unit `unit` of
     // sequence b0 on, whose first unit is number `base` of all
-    int b0, unit, base, todo, run = 0;
+    int b0, unit, base, todo, run = 0, split = 0;
     if (p.balanced) {
         // each thread adds up a slice of the batch, then the slices are scanned
         const int per = (p.batch + kI4Threads - 1) / kI4Threads;
@@ -401,11 +403,13 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             todo -= skip;
         }
     } else {
-        const int at = blockIdx.x / p.max_splits, split = blockIdx.x - at * p.max_splits;
-        const int row = at / p.hkv, h = at - row * p.hkv;
+        int row = blockIdx.z;
+        split = blockIdx.x;
+        for (; split >= p.max_splits; split -= p.max_splits) row += gridDim.z;
         b0 = row / p.col_groups;
-        const int cg = row - b0 * p.col_groups;
-        const bool reports = tid == 0 && split == 0 && h == 0 && cg == 0;
+        const int cg = row % p.col_groups;
+        if (b0 >= p.batch) return;
+        const bool reports = tid == 0 && split == 0 && blockIdx.y == 0 && cg == 0;
         if (p.seq_order) {
             b0 = __ldg(p.seq_order + b0);
             if (b0 < 0 || b0 >= p.batch) {  // not a permutation of the batch
@@ -414,7 +418,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
             }
         }
         const I4Work w = i4_sequence(p, b0, kRound, kCols, reports);
-        const int pair = cg * p.hkv + h, r0 = split * p.part_rounds;
+        const int pair = cg * p.hkv + blockIdx.y, r0 = split * p.part_rounds;
         if (pair >= w.pairs || r0 >= w.rounds) return;
         base = 0;
         unit = pair * (w.rounds + kPairCost) + kPairCost + r0;
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(kI4Threads, MINB) decode_i4_kernel(const I4Par
                 d.split = blockIdx.x - c0;
             } else {
                 d.nsplit = (w.rounds + p.part_rounds - 1) / p.part_rounds;
-                d.split = round / p.part_rounds;
+                d.split = split;
             }
             return d;
         };
@@ -1063,8 +1067,10 @@ static kv_status launch_i4(I4Params &p, int part_blocks, cudaStream_t s) {
     p.uncut = p.max_splits == 1 && pairs > kI4UncutPairs * wave;
     p.balanced = ((p.max_splits > 1 && p.counters) || p.uncut) && p.batch <= kI4ScanBatch && units < (1 << 30);
     p.uncut = p.uncut && p.balanced;
-    const long long grid = p.balanced ? std::min(wave, units) : pairs * p.max_splits;
-    fn<<<(unsigned)grid, kI4Threads, smem, s>>>(p);
+    const int rows = p.batch * p.col_groups, slabs = (rows + kI4MaxRows - 1) / kI4MaxRows;
+    dim3 grid(p.max_splits * slabs, p.hkv, std::min(rows, kI4MaxRows));
+    if (p.balanced) grid = dim3((unsigned)std::min(wave, units));
+    fn<<<grid, kI4Threads, smem, s>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
@@ -1079,7 +1085,7 @@ kv_status attend_i4_limits(int batch, int num_kv_heads, int cols, int max_blocks
     i4_columns(cols, &nt, &groups);
     // the merge's grid; a count of pieces in 16 bits; keys; the grid of CTAs per partition
     if (batch > 65535 || max_splits > 65535 || num_kv_heads > 65535 || max_blocks > INT32_MAX / kI4BS ||
-        (long long)batch * groups * num_kv_heads > INT32_MAX / max_splits)
+        (long long)batch * groups > INT32_MAX / max_splits)
         return KV_ERR_UNSUPPORTED;
     return KV_OK;
 }
