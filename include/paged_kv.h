@@ -414,23 +414,31 @@ kv_status paged_decode_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype
 
 /* paged_prefill_attention over a KV_I4 pool (head_dim 128, q of type q_dtype
  * KV_BF16 or KV_F16, out of q_dtype or KV_F32, q and out 16-byte aligned, scale > 0 and
- * finite, times the pool's scale of K too).
- * Few query tokens per sequence (a step over drafted tokens) run on the decode's kernel
- * with a column per (query token, head).  Otherwise the blocks of the batch are first
- * expanded to 16-bit tiles in the workspace, once for all their query tiles and heads
- * (pass tables no wider than the longest sequence needs), and where query tiles alone
- * would leave SMs idle their keys are cut too, by the lengths on the device: results
- * then depend, within rounding, on the batch's lengths, and are the same from call to
- * call.  A sequence with more than max_q_len query tokens is left out and sets
- * KV_DEVERR_BLOCK_RANGE; so does an out-of-range block id, whose keys are left out (in
- * the decode too; a row with no key left has out = 0, lse = -inf).  A NaN in V of a key inside a chunk reaches the chunk's earlier
- * rows of its kv head too (a weight of zero times NaN), as in paged_prefill_attention; a
- * NaN in K or q does not: the rows that see it, and no others, are NaN, their lse too.
- * workspace: 16-byte aligned, kv_prefill_i4_workspace_size bytes for the same sizes.
+ * finite, times the pool's scale of K too).  Few query tokens per sequence (a step over
+ * drafted tokens) run on the decode's kernel with a column per (query token, head of a
+ * group): up to 32 columns for max_q_len, and up to 96 where columns * batch * kv heads is
+ * at most 80 per SM.  Otherwise the blocks of the batch are first expanded to 16-bit tiles
+ * in the workspace, once for all their query tiles and heads, and where query tiles alone
+ * would leave SMs idle their keys are cut too, by the lengths on the device: results then
+ * depend, within rounding, on the batch's lengths, and are the same from call to call.
+ * A sequence with more than max_q_len query tokens is left out and sets
+ * KV_DEVERR_BLOCK_RANGE; so does an out-of-range block id, whose keys are left out (in the
+ * decode too; a row with no key left has out = 0, lse = -inf).  A NaN in V of a key inside
+ * a chunk reaches the chunk's earlier rows of its kv head too (a weight of zero times NaN),
+ * as in paged_prefill_attention; a NaN in K or q does not: the rows that see it, and no
+ * others, are NaN, their lse too.
+ * Precision: by columns as the decode above (fp32 output: weights in two fp16 parts); over
+ * expanded tiles q as it is and the softmax weights in one fp16 part (11 bits) for every
+ * out_dtype, as in paged_prefill_attention.
+ * workspace: 16-byte aligned, kv_prefill_i4_workspace_size bytes for the same sizes.  Where
+ * tiles are expanded that is 8192 bytes and more per (sequence, table column, kv head)
+ * whether a sequence reaches the column or not, 3.6 times a full table's cache: pass tables
+ * no wider than the longest sequence needs, and chunks over sequences of very unlike
+ * lengths in calls of like ones, which may use one workspace in turn.
  * Both calls return KV_ERR_UNSUPPORTED for the same sizes: batch or kv heads > 65535, more
- * than 8 query heads per kv head, and, where tiles are expanded, a batch * max_blocks * kv
- * heads * 16 of more than 2^31 - 1 (by columns, max_blocks > 2^27 - 1 or a grid of as many
- * CTAs). */
+ * than 8 query heads per kv head, and, where tiles are expanded, more than 2^31 - 1 rows
+ * batch * max_blocks * kv heads * 16 (by columns max_blocks > 2^27 - 1, or more than
+ * 2^31 - 1 partitions of groups of 16 columns). */
 kv_status kv_prefill_i4_workspace_size(kv_pool_t p, int batch, int num_q_heads, int max_blocks,
                                        int max_q_len, size_t *bytes);
 kv_status paged_prefill_attention_i4(kv_pool_t p, const void *q, kv_dtype q_dtype,

@@ -11,6 +11,11 @@
 // large bf16 matrix product), bound as in the 16-bit prefill by the softmax between the
 // tensor core's two products (its pipe is busy for 65% of the time).
 //
+// The weights enter the second product as one fp16 number each for every output type (the
+// tensor core takes 16-bit operands, and a second part would be a third product; error
+// against 64 bits over mixed fp16 chunks 2.62e-4, of 24-bit weights 2.06e-4); few query
+// tokens, by the decode kernel, keep two parts for fp32 output.
+//
 // c s / 256 is stored (exact in both types, see i4.cuh); the softmax scale and the
 // output take the factor back, with the pool's scales.
 //

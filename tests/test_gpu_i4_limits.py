@@ -222,3 +222,24 @@ def test_prefill_refuses_a_scale_that_is_no_number(most):
             pk.paged_prefill_attention_i4(pool, t, pk.KV_BF16, i, 1, most, i, 3, i, 1, 4, scale, t, pk.KV_F32, None, t, 2 ** 62)
         assert e.value.status == -1
     pk.kv_pool_destroy(pool)
+
+
+@pytest.mark.parametrize("q_dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("columns", [8, 21, 24, 32, 96])
+def test_prefill_by_columns_has_the_decodes_weights(columns, q_dtype):
+    """fp32 output by columns keeps weights of two fp16 parts, 2^-21, at every width; the
+    same rows over expanded tiles weights of one, and the log-sum-exp of the decode's bound."""
+    c = Cache([6000, 33, 700], 1, 128, seed=columns + 1)
+    g = 8 if columns % 8 == 0 else 7
+    T = columns // g
+    cu = np.array([0, T, T, 2 * T])
+    q = c.queries(2 * T, g, q_dtype)
+    for most, step, floor in ((T, 2.0 ** -21, 2.0 ** -31), (97, 2.0 ** -11, 2.0 ** -24)):
+        out, lse = c.prefill(q, q_dtype, "f32", cu, most)
+        for b, n in enumerate(c.lens):
+            t, rows = int(cu[b + 1] - cu[b]), slice(int(cu[b]), int(cu[b + 1]))
+            if t:
+                ref = attend(f64(q[rows]), c.kv[b], c.vv[b], 128 ** -0.5, [int(n) - t + i + 1 for i in range(t)])
+                check_attention(f64(out[rows]), f64(lse[rows]), ref, 128 ** -0.5, int(n), "f32", step, f"most {most} seq {b}",
+                                floor=floor)
+    c.close()
