@@ -1080,7 +1080,7 @@ static kv_status launch_i4(I4Params &p, int part_blocks, cudaStream_t s) {
 
 // Tiles of eight columns of a pair and pairs of one (sequence, kv head) for its columns.
 static void i4_columns(int cols, int *nt, int *groups) {
-    *nt = cols <= 24 ? (cols + 7) / 8 : 2;  // more: groups of 16 (a fourth tile of eight does not fit)
+    *nt = cols <= 24 ? std::max(1, (cols + 7) / 8) : 2;  // more: groups of 16 (a fourth tile of eight does not fit)
     *groups = (cols + 8 * *nt - 1) / (8 * *nt);
 }
 

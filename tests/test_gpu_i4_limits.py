@@ -243,3 +243,19 @@ def test_prefill_by_columns_has_the_decodes_weights(columns, q_dtype):
                 check_attention(f64(out[rows]), f64(lse[rows]), ref, 128 ** -0.5, int(n), "f32", step, f"most {most} seq {b}",
                                 floor=floor)
     c.close()
+
+
+def test_prefill_workspace_of_nothing():
+    """No sequence, no query token or no table column: an answer, and a call without work."""
+    require_cuda()
+    pool = pk.kv_pool_create(4, 16, 2, 128, pk.KV_I4)
+    for batch, width, most in ((0, 3, 4), (0, 3, 400), (2, 3, 0), (0, 0, 0), (2, 0, 0), (2, 0, 4)):
+        n = pk.kv_prefill_i4_workspace_size(pool, batch, 8, width, most)
+        assert n == 0 or most > 96 // 4
+    t = torch.zeros(1 << 12, dtype=torch.float32, device="cuda")
+    i = torch.zeros(8, dtype=torch.int32, device="cuda")
+    for batch, rows, most in ((0, 0, 0), (0, 5, 5), (2, 0, 0), (2, 0, 5), (2, 5, 0)):
+        pk.paged_prefill_attention_i4(pool, t, pk.KV_BF16, i, rows, most, i, 3, i, batch, 8, 1.0, t, pk.KV_F32)
+    torch.cuda.synchronize()
+    assert pk.kv_get_device_error(pool) == 0 and torch.all(t == 0)
+    pk.kv_pool_destroy(pool)
