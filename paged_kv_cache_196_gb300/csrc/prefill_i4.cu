@@ -7,7 +7,7 @@
 // workspace laid out as a 16-bit pool's, and the tcgen05 prefill runs over them: K in
 // q's type, V in fp16 (no conversion in its inner loop).  For 4 chunks of 2048
 // tokens over 8192 cached ones (8 kv heads of 7, bf16) the expansion moves 47 MB in and
-// 168 MB out in 35 us of the call's 1468: the products run at 1474 TFLOP/s (0.77 of a
+// 168 MB out in 35 us of the call's 1471: the products run at 1472 TFLOP/s (0.77 of a
 // large bf16 matrix product), bound as in the 16-bit prefill by the softmax between the
 // tensor core's two products (its pipe is busy for 65% of the time).
 //
