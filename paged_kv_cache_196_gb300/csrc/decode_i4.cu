@@ -86,8 +86,8 @@ constexpr int kI4ShortPair = 8;      // rounds of a pair that may better stay wh
 // rescaled) only when the maximum passes it by more than 2^8: rarely after the
 // first blocks, and exact mathematics, since sums and outputs share m.  They stay
 // below 2^14, in fp16's range, and the largest seen is at least 2^6.
-// With 16-bit output a weight is one fp16 number (half a step: 2^-12 of it), with fp32
-// output two, which doubles the products with V: a bf16 output is 16 times coarser than
+// With 16-bit output a weight is one fp16 number (off by at most 2^-11 of it), with fp32
+// output two, which doubles the products with V: the rounding to a bf16 output is 8 times
 // that, and the error of 64 sequences' outputs against 64 bits is 1.656e-3 where weights of
 // 24 bits leave 1.646e-3 (drafted tokens in fp16: 2.30e-4, 2.07e-4).
 constexpr float kI4Bias = 6.f, kI4Renew = 8.f;
@@ -1047,7 +1047,7 @@ static void i4_split_plan(int batch, int num_kv_heads, int max_blocks, int num_s
         return;
     }
     const long long pb = ((long long)max_blocks + num_splits - 1) / num_splits;
-    *part_blocks = (int)((pb + 3) / 4 * 4);
+    *part_blocks = (int)std::min<long long>((pb + 3) / 4 * 4, INT32_MAX);
     *max_splits = (int)(((long long)max_blocks + *part_blocks - 1) / *part_blocks);
 }
 
