@@ -87,6 +87,8 @@ typedef enum { KV_F32 = 0, KV_BF16 = 1, KV_F16 = 2, KV_I4 = 3 } kv_dtype;
                                        with |v| >= 65536 or infinite; the PV product, run on
                                        fp16 operands, used +-65504 in its place */
 #define KV_DEVERR_POSITION 0x20     /* kv_append_rope: position outside [0, max_position) */
+#define KV_DEVERR_TREE 0x40         /* a parent that does not come before its node, a drafted token
+                                       past the vocabulary, an accepted path that does not rise */
 
 /* Default time limit of a pipeline wait inside a kernel (nanoseconds). */
 #define KV_WAIT_LIMIT_DEFAULT_NS 2000000000ull
@@ -708,6 +710,111 @@ kv_status paged_prefill_attention(kv_pool_t p, const void *q, const int32_t *cu_
                                   const int32_t *seq_lens, int batch, int num_q_heads,
                                   float scale, void *out, kv_dtype out_dtype, float *lse_out,
                                   void *stream);
+
+/* ----------------------------------------------------------------------
+ * Drafted tokens.  A step that checks several guesses at once appends a tree of
+ * tokens to each sequence (kv_append or kv_append_rope, a node's position being that
+ * of its parent plus one), attends with all of them, and keeps one path of the tree.
+ *
+ * Sequence b's tree has T_b = cu_q[b+1] - cu_q[b] nodes, 0 to 256 of them; they are the last
+ * T_b of its seq_lens[b] cached tokens, node i at place seq_lens[b] - T_b + i.  parents
+ * (device int32[total_q]) holds each node's parent by its index in the tree, which is below
+ * the node's own, or -1; NULL: every tree is a chain, each node's parent the one before.
+ * Node 0 is the token that the step before emitted, the others are drafts (nodes with
+ * parent -1 beside node 0 are attended with, never accepted).
+ * -------------------------------------------------------------------- */
+
+/* Attention of the trees: query row cu_q[b] + i (of every head) attends the
+ * seq_lens[b] - T_b tokens before the tree, node i and the nodes above it.
+ *   q, out      device rows [total_q][num_q_heads][head_dim] of the pool's type; out of
+ *               that type or KV_F32; both 16-byte aligned; rows of no tree are left as
+ *               they were;
+ *   cu_q        device int32[batch + 1], rising from 0 or more, cu_q[batch] <= total_q;
+ *   max_q_len   host: the most nodes of a tree, at most 256;
+ *   scale       positive and finite;
+ *   lse_out     device fp32[total_q][num_q_heads] or NULL;
+ *   workspace   16-byte aligned, kv_tree_workspace_size bytes for the same sizes.  Nothing in
+ *               it has to start at zero; calls that may run at the same time need one each.
+ * Other arguments as paged_prefill_attention; pools of KV_F32, KV_BF16 and KV_F16, head_dim
+ * 64 and 128.  Sums and softmax statistics are fp32.  fp32 pools: products in fp32.  16-bit
+ * pools: products on the tensor cores, softmax weights in two parts of the pool's type (16
+ * significant bits with bf16, 22 with fp16).
+ * The kernel cuts the batch by the lengths on the device, so a captured call stays balanced
+ * as they change; results depend, within rounding, on the batch's lengths, and are the same
+ * from call to call.  A tree that is longer than max_q_len or its sequence, a sequence
+ * longer than its table or rows past total_q leave that sequence out and set
+ * KV_DEVERR_BLOCK_RANGE; so does an out-of-range block id, whose keys are left out (a row
+ * with no key left has out = 0, lse = -inf).  A parent that does not come before its node
+ * sets KV_DEVERR_TREE; the node is attended as if it had none.  What K and V hold in keys
+ * that a row does not attend, NaN and infinities too, does not reach the row; a NaN in an
+ * attended key, or an infinity in its V, makes it NaN or infinite.
+ * KV_ERR_UNSUPPORTED: KV_I4 pools, an out_dtype as above, more than 8 query heads per kv
+ * head, max_q_len > 256, max_blocks > 2^27 - 1, 16-bit pools of more than 2^31 - 1 (block,
+ * kv head, token) rows. */
+kv_status kv_tree_workspace_size(kv_pool_t p, int batch, int num_q_heads, int max_blocks, int max_q_len,
+                                 size_t *bytes);
+kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, int total_q, int max_q_len,
+                               const int32_t *parents, const int32_t *block_tables, int max_blocks,
+                               const int32_t *seq_lens, int batch, int num_q_heads, float scale, void *out,
+                               kv_dtype out_dtype, float *lse_out, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* Which drafts stay: a walk from node 0 of each tree.  At a node, its children are tried in
+ * order.  With p the target's probabilities after the node, q those that its children were
+ * drawn from (independently) and u = accept_uniform of the child, the child's token x is
+ * accepted if u q(x) < p(x); otherwise p becomes max(p - q, 0), divided by its sum, for the
+ * next child.  When no child is accepted, or max_path nodes are, the next token is drawn from
+ * what p is by then: the first whose running sum of p passes sample_uniform times the sum
+ * of all.  So what is emitted is distributed as the target's own samples.
+ *   target_probs  device [total_q][vocab] of probs_dtype (KV_F32, KV_BF16 or KV_F16), row
+ *                 cu_q[b] + i from i * target_stride elements on (0: vocab): after node i;
+ *   draft_probs   the same for the distribution that node i's children were drawn from (rows
+ *                 of leaves are not read), or NULL: drafts were chosen, not drawn (the
+ *                 draft's likeliest tokens, say), and q counts as one at x;
+ *   tokens        device int32[total_q], each node's token (node 0's is not read); a negative
+ *                 one is no draft: it is passed over;
+ *   accept_uniform, sample_uniform  device fp32 [total_q] and [batch], random numbers of
+ *                 [0, 1) (node 0's accept_uniform is not read);
+ *   max_path      host: most drafts that are accepted, 0 to 255;
+ *   num_accepted  device int32[batch];
+ *   path          device int32[batch][max_path]: the accepted nodes from the top, -1 behind
+ *                 them (may be NULL if max_path is 0);
+ *   out_tokens    device int32[batch][max_path + 1]: their tokens, the next token, then -1.
+ * Rows need not sum to one (a draw divides by their sum, a first acceptance takes p and q
+ * as they are); entries that are negative or NaN count as 0, above one as 1.  If nothing of
+ * p is left after the rejections, the draw is from p as it was before them; a row without any
+ * positive entry gives the token -1.  For a sequence that samples greedily p is one at its
+ * token.  Sums are exact (whole numbers of 2^-42 or finer), so that a draw does not depend on
+ * the order of additions.  Rows of nodes that the walk does not reach are not read, but for
+ * the entries of their drafts.  A sequence without nodes, or whose cu_q is out of
+ * range (KV_DEVERR_BLOCK_RANGE), accepts nothing and emits -1; a token past the vocabulary or
+ * a parent that does not come before its node sets KV_DEVERR_TREE, the draft is passed over.
+ * p: any pool of the device, for its error word.  KV_ERR_UNSUPPORTED: vocab > 2^20,
+ * max_q_len > 256, max_path > 255, batch > 2^27, another probs_dtype. */
+kv_status kv_verify_tree(kv_pool_t p, const void *target_probs, int64_t target_stride, const void *draft_probs,
+                         int64_t draft_stride, kv_dtype probs_dtype, int vocab, const int32_t *cu_q, int total_q,
+                         int max_q_len, const int32_t *parents, const int32_t *tokens, const float *accept_uniform,
+                         const float *sample_uniform, int batch, int max_path, int32_t *num_accepted, int32_t *path,
+                         int32_t *out_tokens, void *stream);
+
+/* Leaves the accepted nodes in the cache: the K and V rows of node path[b][i] move to place
+ * seq_lens[b] - T_b + 1 + i, behind node 0, for i < num_accepted[b], and new_seq_lens[b]
+ * (device int32[batch], not overlapping seq_lens) becomes seq_lens[b] - T_b + 1 +
+ * num_accepted[b]: what the next append goes on from.  (Blocks behind it stay in the
+ * tables; the host frees or refills them.)  A sequence without nodes keeps its length.
+ *   pools     host array of num_pools distinct pools of one size, type and device, one per
+ *             layer, which share tables and lengths: one launch moves up to 128 of them;
+ *   path, num_accepted, max_path  as kv_verify_tree leaves them; a path rises.
+ * Blocks that rows move into must be held by their sequence alone, as for an append.  A path
+ * that does not rise or leaves the tree sets KV_DEVERR_TREE, sizes out of range set
+ * KV_DEVERR_BLOCK_RANGE (in every pool's word): the sequence stays as it was, with its
+ * length.  An out-of-range block id leaves that row out and sets KV_DEVERR_BLOCK_RANGE.
+ * KV_ERR_UNSUPPORTED: KV_I4 pools, max_q_len > 256, max_path > 255, max_blocks > 2^27 - 1,
+ * batch > 2^24 - 1. */
+kv_status kv_keep_path(const kv_pool_t *pools, int num_pools, const int32_t *cu_q, int max_q_len,
+                       const int32_t *path, int max_path, const int32_t *num_accepted,
+                       const int32_t *block_tables, int max_blocks, const int32_t *seq_lens, int batch,
+                       int32_t *new_seq_lens, void *stream);
 
 /* Synchronises `stream`, returns the device error word in *code (0 = none)
  * and clears it.  Returns KV_ERR_TIMEOUT if the timeout bit is set, else

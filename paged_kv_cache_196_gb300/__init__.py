@@ -34,6 +34,7 @@ __all__ = [
     "KV_WAIT_LIMIT_DEFAULT_NS",
     "kv_append_rope", "kv_read_tokens", "kv_pool_set_i4_scales", "kv_decode_plan_i4", "paged_decode_attention_i4",
     "kv_prefill_i4_workspace_size", "paged_prefill_attention_i4",
+    "kv_tree_workspace_size", "paged_tree_attention", "kv_verify_tree", "kv_keep_path",
 ]
 
 KV_F32 = 0
@@ -127,6 +128,12 @@ _SIGS = {
     "kv_prefill_i4_workspace_size": [_vp, _i32, _i32, _i32, _i32, _P(_sz)],
     "paged_prefill_attention_i4": [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _i32, _f32, _vp, _i32,
                                    _vp, _vp, _sz, _vp],
+    "kv_tree_workspace_size": [_vp, _i32, _i32, _i32, _i32, _P(_sz)],
+    "paged_tree_attention": [_vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _f32, _vp, _i32, _vp, _vp, _sz,
+                             _vp],
+    "kv_verify_tree": [_vp, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp,
+                       _vp, _vp],
+    "kv_keep_path": [_vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp],
     "kv_get_device_error": [_vp, _P(_i32), _vp],
     "kv_contig_create": [_i32, _i32, _i32, _i32, _i32, _P(_vp)],
     "kv_contig_destroy": [_vp],
@@ -658,6 +665,46 @@ def paged_prefill_attention_i4(p: int, q, q_dtype: int, cu_q, total_q: int, max_
                                             _ptr(block_tables), max_blocks, _ptr(seq_lens), batch, num_q_heads,
                                             scale, _ptr(out), out_dtype, _ptr(lse_out), _ptr(workspace),
                                             workspace_bytes, _stream(stream)), "paged_prefill_attention_i4")
+
+
+def kv_tree_workspace_size(p: int, batch: int, num_q_heads: int, max_blocks: int, max_q_len: int) -> int:
+    r = _sz()
+    _check(lib().kv_tree_workspace_size(p, batch, num_q_heads, max_blocks, max_q_len, ctypes.byref(r)),
+           "kv_tree_workspace_size")
+    return r.value
+
+
+def paged_tree_attention(p: int, q, cu_q, total_q: int, max_q_len: int, parents, block_tables, max_blocks: int,
+                         seq_lens, batch: int, num_q_heads: int, scale: float, out, out_dtype: int, lse_out=None,
+                         workspace=None, workspace_bytes: int = 0, stream=None):
+    """Attention of a tree of drafted tokens per sequence over its cache; parents (int32, by index
+    within the tree, -1 = none) or None for chains.  See the C header."""
+    _check(lib().paged_tree_attention(p, _ptr(q), _ptr(cu_q), total_q, max_q_len, _ptr(parents), _ptr(block_tables),
+                                      max_blocks, _ptr(seq_lens), batch, num_q_heads, scale, _ptr(out), out_dtype,
+                                      _ptr(lse_out), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "paged_tree_attention")
+
+
+def kv_verify_tree(p: int, target_probs, draft_probs, probs_dtype: int, vocab: int, cu_q, total_q: int, max_q_len: int,
+                   parents, tokens, accept_uniform, sample_uniform, batch: int, max_path: int, num_accepted, path,
+                   out_tokens, target_stride: int = 0, draft_stride: int = 0, stream=None):
+    """Which drafts of each tree the target accepts, from given random numbers, and the token after
+    them; draft_probs None: the drafts were chosen, not drawn.  Strides in elements between
+    rows, 0 = packed.  See the C header."""
+    _check(lib().kv_verify_tree(p, _ptr(target_probs), target_stride, _ptr(draft_probs), draft_stride, probs_dtype,
+                                vocab, _ptr(cu_q), total_q, max_q_len, _ptr(parents), _ptr(tokens),
+                                _ptr(accept_uniform), _ptr(sample_uniform), batch, max_path, _ptr(num_accepted),
+                                _ptr(path), _ptr(out_tokens), _stream(stream)), "kv_verify_tree")
+
+
+def kv_keep_path(pools, cu_q, max_q_len: int, path, max_path: int, num_accepted, block_tables, max_blocks: int,
+                 seq_lens, batch: int, new_seq_lens, stream=None):
+    """Moves the rows of the accepted nodes behind their roots in every pool of the list (one per
+    layer) and writes the sequences' new lengths.  See the C header."""
+    handles = (_vp * len(pools))(*pools)
+    _check(lib().kv_keep_path(handles, len(pools), _ptr(cu_q), max_q_len, _ptr(path), max_path, _ptr(num_accepted),
+                              _ptr(block_tables), max_blocks, _ptr(seq_lens), batch, _ptr(new_seq_lens),
+                              _stream(stream)), "kv_keep_path")
 
 
 def kv_get_device_error(p: int, stream=None) -> int:

@@ -1,0 +1,369 @@
+// Attention of a tree of drafted tokens over a paged cache.
+//
+// Maths.  Sequence b holds L tokens, the last T of them the nodes of a tree, node i
+// below parent[i] < i.  With S_i the L - T tokens before the tree, node i and the nodes
+// above it:  o_i = sum_{j in S_i} exp(scale q_i.k_j) v_j / sum_{j in S_i} exp(scale q_i.k_j),
+// in one pass over the keys with a running reference and sum per row.  A row is a
+// (node, query head); the rows of a kv head and of as many nodes as fit are one matrix
+// product with each tile of its keys, so a key is read once for all of them.
+//
+// The keys before the tree need no mask.  Those of the tree get one bit per (node, key),
+// from a walk up the parents: S_i's bits are the row's mask of the last tiles.
+//
+// The work is spread over one wave of CTAs by tree_plan.cuh; a second kernel adds up the
+// pairs that were cut: with m_s, l_s, O_s a piece's reference, sum and output,
+//   o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tree.h"
+#include "tree_plan.cuh"
+
+namespace pkv {
+namespace tree {
+
+KV_DEVICE float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---------------------------------------------------------------- fp32 arithmetic
+// 32 rows of a pair against 32 keys at a time, products by fp32 multiply-adds: thread
+// (ty, tx) holds rows 2 ty, 2 ty + 1, scores keys tx + 8 j and sums dimensions
+// 4 tx + 32 i.  A warp owns eight rows, so their statistics and weights need no barrier.
+constexpr int kSimpleRows = 32, kSimpleKeys = 32, kSimpleThreads = 128;
+
+template <int D>
+struct SimpleShared {
+    float q[kSimpleRows][D + 4], k[kSimpleKeys][D + 4], v[kSimpleKeys][D + 4];
+    float p[kSimpleRows][kSimpleKeys + 1];
+    uint32_t anc[kSimpleRows][kMaxNodes / 32];
+    uint32_t there;  // bit j: key j of the tile is in the pool
+    PlaceScratch<kSimpleThreads> scratch;
+};
+
+template <typename T>
+KV_DEVICE float4 load4(const void *base, size_t idx);
+template <>
+KV_DEVICE float4 load4<float>(const void *base, size_t idx) {
+    return __ldg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + idx));
+}
+struct Bf16 {};
+struct F16 {};
+template <>
+KV_DEVICE float4 load4<Bf16>(const void *base, size_t idx) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(base) + idx));
+    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+template <>
+KV_DEVICE float4 load4<F16>(const void *base, size_t idx) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(base) + idx));
+    const float2 a = f16x2_to_float2(w.x), b = f16x2_to_float2(w.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeParams p) {
+    extern __shared__ __align__(16) char raw[];
+    auto &sm = *reinterpret_cast<SimpleShared<D> *>(raw);
+    const int tid = threadIdx.x, ty = tid / 8, tx = tid % 8;
+    const Place at = place(p.plan, blockIdx.x, sm.scratch, blockIdx.x == 0 ? p.err : nullptr);
+    Pieces pieces;
+    pieces.start(p.plan, at, blockIdx.x);
+    Piece pc;
+    while (pieces.next(p.plan, pc)) {
+        const int node0 = pc.grp * p.plan.group_nodes;
+        const int rows = min(p.plan.group_nodes, pc.seq.nodes - node0) * p.g;
+        const int before = pc.seq.len - pc.seq.nodes;  // tokens before the tree
+        const int32_t *table = p.tables + (size_t)pc.b * p.plan.max_blocks;
+        __syncthreads();  // the piece before is done with what follows
+        for (int i = tid; i < kSimpleRows * D / 4; i += kSimpleThreads) {
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows)
+                x = load4<T>(p.q, ((size_t)(pc.seq.q0 + node0 + r / p.g) * p.hq + pc.h * p.g + r % p.g) * D + d);
+            *reinterpret_cast<float4 *>(&sm.q[r][d]) = x;
+        }
+        if (tid < kSimpleRows) {
+            for (int w = 0; w < kMaxNodes / 32; ++w) sm.anc[tid][w] = 0;
+            if (tid < rows)
+                walk_up(p.parents ? p.parents + pc.seq.q0 : nullptr, node0 + tid / p.g, p.err,
+                        [&](int i) { sm.anc[tid][i >> 5] |= 1u << (i & 31); });
+        }
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float4 o[2][D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[0][i] = o[1][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int key1 = min(pc.t1 * kTile, pc.seq.len);
+        for (int key0 = pc.t0 * kTile; key0 < key1; key0 += kSimpleKeys) {
+            __syncthreads();
+            if (tid < kSimpleKeys) {
+                const int key = key0 + tid;
+                const int id = key < key1 ? __ldg(table + key / 16) : 0;
+                const bool in = id >= 0 && id < p.num_blocks;
+                if (!in) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
+                const uint32_t there = __ballot_sync(0xffffffffu, in && key < key1);
+                if (tid == 0) sm.there = there;
+            }
+            for (int i = tid; i < kSimpleKeys * D / 4; i += kSimpleThreads) {
+                const int r = i / (D / 4), d = i % (D / 4) * 4, key = key0 + r;
+                const int id = key < key1 ? __ldg(table + key / 16) : -1;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+                if (id >= 0 && id < p.num_blocks) {
+                    const size_t at0 = (((size_t)id * p.plan.hkv + pc.h) * 16 + key % 16) * D + d;
+                    x = load4<T>(p.k, at0);
+                    y = load4<T>(p.v, at0);
+                }
+                *reinterpret_cast<float4 *>(&sm.k[r][d]) = x;
+                *reinterpret_cast<float4 *>(&sm.v[r][d]) = y;
+            }
+            __syncthreads();
+            float s[2][4] = {};
+#pragma unroll 4
+            for (int d = 0; d < D; d += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(&sm.q[2 * ty][d]);
+                const float4 c = *reinterpret_cast<const float4 *>(&sm.q[2 * ty + 1][d]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 b = *reinterpret_cast<const float4 *>(&sm.k[tx + 8 * j][d]);
+                    s[0][j] += a.x * b.x, s[0][j] += a.y * b.y, s[0][j] += a.z * b.z, s[0][j] += a.w * b.w;
+                    s[1][j] += c.x * b.x, s[1][j] += c.y * b.y, s[1][j] += c.z * b.z, s[1][j] += c.w * b.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = 2 * ty + i;
+                const uint32_t bits = key_bits(sm.anc[row], key0 - before) & sm.there;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = bits >> (tx + 8 * j) & 1 ? s[i][j] * p.scale_log2 : -INFINITY;
+                    mx = fmaxf(mx, s[i][j]);
+                }
+#pragma unroll
+                for (int off = 4; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                const float up = fmaxf(m[i], mx);
+                const float ref = up == -INFINITY ? 0.f : up;
+                const float alpha = ex2(m[i] - ref);
+                m[i] = up;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float e = ex2(s[i][j] - ref);
+                    sum += e;
+                    sm.p[row][tx + 8 * j] = e;
+                }
+#pragma unroll
+                for (int off = 4; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                l[i] = l[i] * alpha + sum;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                    o[i][k].x *= alpha, o[i][k].y *= alpha, o[i][k].z *= alpha, o[i][k].w *= alpha;
+            }
+            __syncwarp();
+            // a weight of zero leaves its key out: what lies in a masked one reaches no row
+#pragma unroll 4
+            for (int j = 0; j < kSimpleKeys; ++j) {
+                const float e0 = sm.p[2 * ty][j], e1 = sm.p[2 * ty + 1][j];
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&sm.v[j][4 * tx + 32 * k]);
+                    if (e0 != 0.f)
+                        o[0][k].x += e0 * v.x, o[0][k].y += e0 * v.y, o[0][k].z += e0 * v.z, o[0][k].w += e0 * v.w;
+                    if (e1 != 0.f)
+                        o[1][k].x += e1 * v.x, o[1][k].y += e1 * v.y, o[1][k].z += e1 * v.z, o[1][k].w += e1 * v.w;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = 2 * ty + i;
+            if (row >= rows) continue;
+            if (pc.slot >= 0) {
+                float *part = p.partial + (size_t)pc.slot * kSimpleRows * (D + 2);
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                    reinterpret_cast<float4 *>(part)[(tx + 8 * k) * kSimpleRows + row] = o[i][k];
+                if (tx == 0) reinterpret_cast<float2 *>(part + kSimpleRows * D)[row] = make_float2(m[i], l[i]);
+                continue;
+            }
+            const size_t orow = (size_t)(pc.seq.q0 + node0 + row / p.g) * p.hq + pc.h * p.g + row % p.g;
+            const bool seen = l[i] != 0.f;  // a row with a NaN score stays NaN
+            const float inv = seen ? 1.f / l[i] : 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+                store_out4(p.out, orow * D + 4 * tx + 32 * k,
+                           make_float4(o[i][k].x * inv, o[i][k].y * inv, o[i][k].z * inv, o[i][k].w * inv), p.out_type);
+            if (p.lse && tx == 0)
+                p.lse[orow] = seen ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- cut pairs
+// CTA x > 0 looks at the end of run x - 1: if it lies among the tiles of a pair, the pair
+// is cut, and this CTA takes one share of its rows, one share per cut.
+constexpr int kMergeThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p, int slot_rows) {
+    __shared__ PlaceScratch<kMergeThreads> scratch;
+    const int r = blockIdx.x + 1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Place at = place(p.plan, r, scratch, nullptr);
+    if (at.b >= p.plan.batch) return;
+    const Seq seq = load_seq(p.plan, at.b, nullptr);
+    const long long cost = seq.pair_units();
+    const int pair = (int)((r * at.per - at.base) / cost);
+    const long long first = at.base + pair * cost;
+    const int r0 = (int)((first + kTreePairCost) / at.per);  // the run that has the first tile
+    const int r1 = (int)((first + cost - 1) / at.per);       // and the last
+    if (r <= r0 || r > r1) return;
+    const int h = pair / seq.groups, node0 = (pair - h * seq.groups) * p.plan.group_nodes;
+    const int rows = min(p.plan.group_nodes, seq.nodes - node0) * p.g;
+    const int shares = (r1 - r0) * gridDim.y, share = (r - r0 - 1) * gridDim.y + blockIdx.y;
+    const int row0 = (int)((long long)rows * share / shares), row1 = (int)((long long)rows * (share + 1) / shares);
+    const size_t step = (size_t)slot_rows * (D + 2);
+    const int slot0 = 2 * r0 + (first < r0 * at.per ? 0 : 1);
+    for (int i = threadIdx.x; i < (row1 - row0) * (D / 4); i += kMergeThreads) {
+        const int dq = i / (row1 - row0), row = row0 + i - dq * (row1 - row0);
+        float M = -INFINITY;
+        for (int s = r0; s <= r1; ++s) {
+            const float *part = p.partial + (s == r0 ? slot0 : 2 * s) * step;
+            M = fmaxf(M, reinterpret_cast<const float2 *>(part + (size_t)slot_rows * D)[row].x);
+        }
+        const float ref = M == -INFINITY ? 0.f : M;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = 0.f;
+#pragma unroll 4
+        for (int s = r0; s <= r1; ++s) {
+            const float *part = p.partial + (s == r0 ? slot0 : 2 * s) * step;
+            const float2 ml = reinterpret_cast<const float2 *>(part + (size_t)slot_rows * D)[row];
+            const float4 v = reinterpret_cast<const float4 *>(part)[(size_t)dq * slot_rows + row];
+            const float e = ex2(ml.x - ref);
+            // (a piece without a key of the row has nothing to add, whatever its reference)
+            den += ml.y == 0.f ? 0.f : e * ml.y;
+            if (ml.y != 0.f) a.x += e * v.x, a.y += e * v.y, a.z += e * v.z, a.w += e * v.w;
+        }
+        const bool seen = den != 0.f;
+        const float inv = seen ? 1.f / den : 0.f;
+        const size_t orow = (size_t)(seq.q0 + node0 + row / p.g) * p.hq + h * p.g + row % p.g;
+        store_out4(p.out, orow * D + 4 * dq, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), p.out_type);
+        if (p.lse && dq == 0) p.lse[orow] = seen ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
+namespace {
+
+constexpr int kSimplePerSm = 3;  // CTAs
+
+size_t slot_bytes(int rows, int d) { return (size_t)rows * (d + 2) * sizeof(float); }
+
+kv_status launch_simple(const TreeParams &pp, kv_dtype t, int d, cudaStream_t stream) {
+    auto fn = d == 64 ? (t == KV_F32 ? tree_simple_kernel<float, 64>
+                                     : t == KV_BF16 ? tree_simple_kernel<Bf16, 64> : tree_simple_kernel<F16, 64>)
+                      : (t == KV_F32 ? tree_simple_kernel<float, 128>
+                                     : t == KV_BF16 ? tree_simple_kernel<Bf16, 128> : tree_simple_kernel<F16, 128>);
+    const int smem = d == 64 ? (int)sizeof(SimpleShared<64>) : (int)sizeof(SimpleShared<128>);
+    if (kv_status st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+        return st;
+    fn<<<pp.plan.runs, kSimpleThreads, smem, stream>>>(pp);
+    return cuda_status(cudaGetLastError());
+}
+
+kv_status launch_merge(const TreeParams &pp, int d, int slot_rows, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)pp.plan.runs - 1, 2);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, d == 64 ? tree_merge_kernel<64> : tree_merge_kernel<128>, pp, slot_rows));
+}
+
+// How a call runs: what the workspace query and the call have to agree on.
+struct Shape {
+    int rows;  // query rows of a group, and of a slot
+    int runs, min_run;
+};
+Shape shape_of(const kv_pool *, int, int) {
+    return {kSimpleRows, kSimplePerSm * sm_count(), 2 + kTreePairCost};
+}
+
+// Arguments that the query and the call refuse alike.
+kv_status check(kv_pool_t p, int batch, int num_q_heads, int max_blocks, int max_q_len) {
+    if (!p || batch < 0 || max_q_len < 0 || max_blocks < 0 || num_q_heads <= 0) return KV_ERR_ARG;
+    if (kv_status st = require_device(p->device)) return st;
+    if (p->dtype == KV_I4) return KV_ERR_UNSUPPORTED;
+    if (num_q_heads % p->num_kv_heads) return KV_ERR_ARG;
+    if (num_q_heads / p->num_kv_heads > 8 || max_q_len > kMaxNodes || max_blocks > (1 << 27) - 1)
+        return KV_ERR_UNSUPPORTED;
+    return KV_OK;
+}
+
+}  // namespace
+}  // namespace tree
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+kv_status kv_tree_workspace_size(kv_pool_t p, int batch, int num_q_heads, int max_blocks, int max_q_len,
+                                 size_t *bytes) {
+    if (!bytes) return KV_ERR_ARG;
+    if (kv_status st = tree::check(p, batch, num_q_heads, max_blocks, max_q_len)) return st;
+    *bytes = 0;
+    if (batch == 0 || max_q_len == 0) return KV_OK;
+    const tree::Shape s = tree::shape_of(p, num_q_heads / p->num_kv_heads, max_q_len);
+    *bytes = 2 * (size_t)s.runs * tree::slot_bytes(s.rows, p->head_dim);
+    return KV_OK;
+}
+
+kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, int total_q, int max_q_len,
+                               const int32_t *parents, const int32_t *block_tables, int max_blocks,
+                               const int32_t *seq_lens, int batch, int num_q_heads, float scale, void *out,
+                               kv_dtype out_dtype, float *lse_out, void *workspace, size_t workspace_bytes,
+                               void *stream) {
+    if (total_q < 0) return KV_ERR_ARG;
+    if (kv_status st = tree::check(p, batch, num_q_heads, max_blocks, max_q_len)) return st;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return KV_ERR_ARG;
+    if (out_dtype != KV_F32 && out_dtype != p->dtype) return KV_ERR_UNSUPPORTED;
+    if (batch == 0 || max_q_len == 0 || total_q == 0) return KV_OK;
+    if (!q || !cu_q || !block_tables || !seq_lens || !out || !workspace) return KV_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(workspace)) & 15)
+        return KV_ERR_ARG;
+    const int g = num_q_heads / p->num_kv_heads;
+    const tree::Shape s = tree::shape_of(p, g, max_q_len);
+    if (workspace_bytes < 2 * (size_t)s.runs * tree::slot_bytes(s.rows, p->head_dim)) return KV_ERR_ARG;
+    tree::TreeParams pp{};
+    pp.plan = {cu_q, seq_lens, batch, total_q, max_q_len, max_blocks, p->num_kv_heads, s.rows / g, s.runs, s.min_run, 0};
+    pp.q = q;
+    pp.k = p->k;
+    pp.v = p->v;
+    pp.tables = block_tables;
+    pp.parents = parents;
+    pp.num_blocks = p->num_blocks;
+    pp.hq = num_q_heads;
+    pp.g = g;
+    pp.scale_log2 = scale * 1.4426950408889634f;
+    pp.out = out;
+    pp.out_type = out_dtype;
+    pp.lse = lse_out;
+    pp.partial = static_cast<float *>(workspace);
+    pp.err = p->err;
+    if (kv_status st = tree::launch_simple(pp, p->dtype, p->head_dim, as_stream(stream))) return st;
+    return tree::launch_merge(pp, p->head_dim, s.rows, as_stream(stream));
+}
+
+}  // extern "C"

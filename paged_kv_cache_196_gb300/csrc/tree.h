@@ -1,0 +1,29 @@
+// Tree attention: what its kernels share.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "tree_plan.cuh"
+
+namespace pkv {
+namespace tree {
+
+struct TreeParams {
+    Plan plan;
+    const void *q;           // rows [total_q][hq][D], the pool's type
+    const void *k, *v;       // the pool's arrays
+    const int32_t *tables;   // [batch][max_blocks]
+    const int32_t *parents;  // [total_q]: index within the tree, -1: none; null: chains
+    int num_blocks;
+    int hq, g;
+    float scale_log2;        // softmax scale * log2(e)
+    void *out;
+    int out_type;
+    float *lse;
+    float *partial;          // slots of [D / 4][rows] float4 and [rows] (reference, sum)
+    int *err;
+};
+
+}  // namespace tree
+}  // namespace pkv

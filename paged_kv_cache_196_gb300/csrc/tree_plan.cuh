@@ -1,0 +1,206 @@
+// How tree attention spreads a ragged batch over one wave of CTAs, from the lengths
+// it finds on the device (a captured step stays balanced as its sequences grow).
+//
+// A sequence of L tokens and T nodes is kv heads x groups pairs: a group is as many
+// whole nodes as the kernel takes query rows (all heads of a kv head, row = node of
+// the group * g + head), so a pair is what one pass over the keys of a kv head serves.
+// A pair counts kTreePairCost units (its queries and its end) and one per key tile of
+// 128.  The units of all pairs are laid end to end, sequence by sequence, and cut into
+// equal runs, one per CTA.  What a run holds of a pair is a piece: a range of its key
+// tiles, empty where the run's end falls among the pair's first kTreePairCost units.
+// A pair of more than one piece leaves partial results: a run that begins inside a pair
+// has its piece of it in slot 2 run, the one that it begins and does not end in slot
+// 2 run + 1.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace pkv {
+namespace tree {
+
+constexpr int kTile = 128;  // keys
+constexpr int kTreePairCost = 1;
+
+struct Plan {
+    const int32_t *cu_q, *seq_lens;
+    int batch, total_q, max_q_len, max_blocks;
+    int hkv, group_nodes;  // kv heads; nodes of a group
+    int runs;              // CTAs
+    int min_run;           // units of the shortest run
+    int whole;             // a run takes the pairs that begin in it whole: none is cut
+};
+
+struct Seq {
+    int q0, nodes, len, tiles, groups;
+    KV_DEVICE long long pair_units() const { return tiles + kTreePairCost; }
+};
+
+// Sequence b; without nodes where there are none or what describes it is out of range.
+KV_DEVICE Seq load_seq(const Plan &p, int b, int *err) {
+    const long long q0 = __ldg(p.cu_q + b), t = __ldg(p.cu_q + b + 1) - q0, len = __ldg(p.seq_lens + b);
+    Seq s{0, 0, 0, 0, 0};
+    if (t == 0) return s;
+    if (t < 0 || t > p.max_q_len || q0 < 0 || q0 + t > p.total_q || len < t || len > (long long)p.max_blocks * 16) {
+        if (err) atomicOr(err, KV_DEVERR_BLOCK_RANGE);
+        return s;
+    }
+    s.q0 = (int)q0;
+    s.nodes = (int)t;
+    s.len = (int)len;
+    s.tiles = (int)((len + kTile - 1) / kTile);
+    s.groups = (s.nodes + p.group_nodes - 1) / p.group_nodes;
+    return s;
+}
+
+KV_DEVICE long long seq_units(const Plan &p, const Seq &s) {
+    return s.nodes ? (long long)p.hkv * s.groups * s.pair_units() : 0;
+}
+
+// What a CTA knows after place(): units of a run, all units, and the sequence that holds
+// the unit it asked for (batch: none) with the first unit of that sequence.
+struct Place {
+    long long per, total, base;
+    int b;
+};
+
+template <int kThreads>
+struct PlaceScratch {
+    long long sums[kThreads / 32];
+    Place at;
+};
+
+// All threads of the CTA: the place of unit run * per.
+template <int kThreads>
+KV_DEVICE Place place(const Plan &p, int run, PlaceScratch<kThreads> &s, int *err) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int chunk = (p.batch + kThreads - 1) / kThreads;
+    const int b0 = min(p.batch, tid * chunk), b1 = min(p.batch, b0 + chunk);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += seq_units(p, load_seq(p, b, err));
+    long long upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += v;
+    }
+    if (lane == 31) s.sums[warp] = upto;
+    __syncthreads();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) before = total;
+        total += s.sums[w];
+    }
+    upto += before;
+    const long long per = max((long long)p.min_run, (total + p.runs - 1) / p.runs);
+    const long long unit = run * per;
+    if (tid == 0 && unit >= total) s.at = Place{per, total, total, p.batch};
+    if (unit < upto && unit >= upto - mine) {
+        long long base = upto - mine;
+        for (int b = b0; b < b1; ++b) {
+            const long long n = seq_units(p, load_seq(p, b, nullptr));
+            if (unit < base + n) {
+                s.at = Place{per, total, base, b};
+                break;
+            }
+            base += n;
+        }
+    }
+    __syncthreads();
+    return s.at;
+}
+
+// A piece: key tiles t0 .. t1 - 1 of the pair of sequence b, kv head h and node group grp.
+struct Piece {
+    int b, h, grp, t0, t1;
+    int slot;  // of its partial results; -1: the pair is whole
+    Seq seq;
+};
+
+// The pieces of a run, in order.
+struct Pieces {
+    long long unit, end, base;
+    int b, run;
+    Seq seq, ahead;  // of sequences b and b + 1
+
+    KV_DEVICE void start(const Plan &p, const Place &at, int r) {
+        run = r;
+        unit = r * at.per;
+        end = min(at.total, unit + at.per);
+        base = at.base;
+        b = at.b;
+        if (b < p.batch) {
+            seq = load_seq(p, b, nullptr);
+            ahead = b + 1 < p.batch ? load_seq(p, b + 1, nullptr) : Seq{0, 0, 0, 0, 0};
+        }
+    }
+    KV_DEVICE bool next(const Plan &p, Piece &out) {
+        while (unit < end && b < p.batch) {
+            const long long all = seq_units(p, seq);
+            if (unit >= base + all) {
+                base += all;
+                ++b;
+                seq = ahead;
+                ahead = b + 1 < p.batch ? load_seq(p, b + 1, nullptr) : Seq{0, 0, 0, 0, 0};
+                continue;
+            }
+            const long long cost = seq.pair_units();
+            const int pair = (int)((unit - base) / cost);
+            const long long first = base + pair * cost;
+            const long long from = unit - first;
+            const long long to = p.whole ? cost : min(end - first, cost);
+            unit = first + cost;
+            if (p.whole && from > 0) continue;  // the run before has it
+            out.t0 = (int)max(0LL, from - kTreePairCost);
+            out.t1 = (int)max(0LL, to - kTreePairCost);
+            if (out.t0 >= out.t1) continue;
+            out.b = b;
+            out.h = pair / seq.groups;
+            out.grp = pair - out.h * seq.groups;
+            out.slot = out.t0 == 0 && out.t1 == seq.tiles ? -1 : 2 * run + (from > 0 ? 0 : 1);
+            out.seq = seq;
+            return true;
+        }
+        return false;
+    }
+};
+
+// ---------------------------------------------------------------- the tree
+// Ancestors of the nodes, 32 of them a word.
+constexpr int kMaxNodes = 256;
+
+// The bits of node i and of every node above it into out[0 .. kMaxNodes / 32); a parent
+// that does not come before its node ends the walk (it has at most T steps) and is
+// reported.  parents: the tree's (shared memory or global), null: each node's is the one
+// before it.
+template <typename Set>
+KV_DEVICE void walk_up(const int32_t *parents, int i, int *err, Set set) {
+    while (true) {
+        set(i);
+        const int up = parents ? parents[i] : i - 1;
+        if (up >= i || up < -1) {
+            atomicOr(err, KV_DEVERR_TREE);
+            return;
+        }
+        if (up < 0) return;
+        i = up;
+    }
+}
+
+// Bits of 32 keys from key on (a position relative to the tree's first token) that a row
+// with these ancestors attends: all before the tree, none behind it (bits of nodes that
+// are not there are zero).
+KV_DEVICE uint32_t key_bits(const uint32_t *anc, int key) {
+    if (key <= -32) return 0xffffffffu;
+    if (key < 0) return (0xffffffffu >> (32 + key)) | (anc[0] << -key);
+    const int w = key >> 5, s = key & 31;
+    if (w >= kMaxNodes / 32) return 0u;
+    const uint32_t hi = w + 1 < kMaxNodes / 32 ? anc[w + 1] : 0u;
+    return __funnelshift_r(anc[w], hi, s);
+}
+
+}  // namespace tree
+}  // namespace pkv
