@@ -27,6 +27,7 @@ struct kv_pool {
     CUtensorMap tmap_k;
     CUtensorMap tmap_v;
     bool tmaps_ready = false;
+    bool tmaps_64_ready = false;  // head_dim 64 (tree attention)
     // decode launches may overlap the previous kernel in the stream
     // (kv_pool_set_launch_overlap)
     bool launch_overlap = false;
@@ -77,6 +78,7 @@ cudaError_t set_wait_limit_decode(unsigned long long ns);
 cudaError_t set_wait_limit_prefill(unsigned long long ns);
 cudaError_t set_wait_limit_cascade(unsigned long long ns);
 cudaError_t set_wait_limit_decode_i4(unsigned long long ns);
+cudaError_t set_wait_limit_tree(unsigned long long ns);
 
 // True once a test has set a pipeline-wait limit other than the default
 // (kv_debug_set_wait_limit_ns): launches then take the kernels' test
@@ -104,11 +106,12 @@ inline kv_status device_error_status(int code) {
 
 int sm_count();
 
-// tiled-TMA maps (tmap.cu): bf16 rows of 128 values, boxes 16 x 64, 128B swizzle
-bool encode_rows_map(CUtensorMap *m, void *base, long long rows);
+// tiled-TMA maps (tmap.cu): 16-bit rows of `dim` values, boxes 16 x 64, 128B swizzle
+bool encode_rows_map(CUtensorMap *m, void *base, long long rows, int dim = 128);
 // queries [rows][hq][128]: boxes of box_rows rows x box_heads heads x 64 values
 bool encode_q_map(CUtensorMap *m, const void *q, int rows, int hq, int box_heads, int box_rows);
-kv_status pool_tensor_maps(kv_pool *p);
+kv_status pool_tensor_maps(kv_pool *p);     // of a pool with head_dim 128
+kv_status pool_tensor_maps_64(kv_pool *p);  // 64
 
 // ---- decode (shared by the paged and contiguous paths) ----
 struct DecodeArgs {

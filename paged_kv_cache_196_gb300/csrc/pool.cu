@@ -384,6 +384,7 @@ kv_status kv_debug_set_wait_limit_ns(uint64_t ns) {
     if (e == cudaSuccess) e = set_wait_limit_prefill(ns);
     if (e == cudaSuccess) e = set_wait_limit_cascade(ns);
     if (e == cudaSuccess) e = set_wait_limit_decode_i4(ns);
+    if (e == cudaSuccess) e = set_wait_limit_tree(ns);
     if (e == cudaSuccess) g_test_waits.store(ns != KV_WAIT_LIMIT_DEFAULT_NS);
     return cuda_status(e);
 }

@@ -1,5 +1,5 @@
 // Tiled-TMA tensor maps (CUtensorMap) for the pools, per-request contiguous
-// regions and prefill queries.  Every map describes rows of 128 16-bit values
+// regions and prefill queries.  Every map describes rows of 128 (or 64) 16-bit values
 // (bf16 or fp16: the copies move bits, so one data type serves both) read as
 // boxes of 16 rows x 64 values with 128-byte swizzle (the layout both the
 // tcgen05 descriptors and the ldmatrix address math expect).
@@ -32,11 +32,11 @@ static EncodeTiledFn encode_fn() {
     return fn;
 }
 
-bool encode_rows_map(CUtensorMap *m, void *base, long long rows) {
+bool encode_rows_map(CUtensorMap *m, void *base, long long rows, int dim) {
     EncodeTiledFn enc = encode_fn();
     if (!enc || rows <= 0) return false;
-    cuuint64_t dims[2] = {128, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {128 * 2};
+    cuuint64_t dims[2] = {(cuuint64_t)dim, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)dim * 2};
     cuuint32_t box[2] = {64, 16};
     cuuint32_t estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
@@ -64,6 +64,17 @@ kv_status pool_tensor_maps(kv_pool *p) {
     if (!encode_rows_map(&p->tmap_k, p->k, rows) || !encode_rows_map(&p->tmap_v, p->v, rows))
         return KV_ERR_CUDA;
     p->tmaps_ready = true;
+    return KV_OK;
+}
+
+kv_status pool_tensor_maps_64(kv_pool *p) {
+    if (p->tmaps_64_ready) return KV_OK;
+    if (p->dtype == KV_F32 || p->dtype == KV_I4 || p->head_dim != 64) return KV_ERR_UNSUPPORTED;
+    const long long rows = (long long)p->num_blocks * p->num_kv_heads * 16;
+    if (rows > INT32_MAX) return KV_ERR_UNSUPPORTED;
+    if (!encode_rows_map(&p->tmap_k, p->k, rows, 64) || !encode_rows_map(&p->tmap_v, p->v, rows, 64))
+        return KV_ERR_CUDA;
+    p->tmaps_64_ready = true;
     return KV_OK;
 }
 

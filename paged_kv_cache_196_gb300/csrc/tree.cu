@@ -48,28 +48,7 @@ struct SimpleShared {
     PlaceScratch<kSimpleThreads> scratch;
 };
 
-template <typename T>
-KV_DEVICE float4 load4(const void *base, size_t idx);
-template <>
-KV_DEVICE float4 load4<float>(const void *base, size_t idx) {
-    return __ldg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + idx));
-}
-struct Bf16 {};
-struct F16 {};
-template <>
-KV_DEVICE float4 load4<Bf16>(const void *base, size_t idx) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(base) + idx));
-    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-template <>
-KV_DEVICE float4 load4<F16>(const void *base, size_t idx) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(base) + idx));
-    const float2 a = f16x2_to_float2(w.x), b = f16x2_to_float2(w.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeParams p) {
     extern __shared__ __align__(16) char raw[];
     auto &sm = *reinterpret_cast<SimpleShared<D> *>(raw);
@@ -88,7 +67,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
             const int r = i / (D / 4), d = i % (D / 4) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows)
-                x = load4<T>(p.q, ((size_t)(pc.seq.q0 + node0 + r / p.g) * p.hq + pc.h * p.g + r % p.g) * D + d);
+                x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + ((size_t)(pc.seq.q0 + node0 + r / p.g) * p.hq + pc.h * p.g + r % p.g) * D + d));
             *reinterpret_cast<float4 *>(&sm.q[r][d]) = x;
         }
         if (tid < kSimpleRows) {
@@ -118,8 +97,8 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
                 if (id >= 0 && id < p.num_blocks) {
                     const size_t at0 = (((size_t)id * p.plan.hkv + pc.h) * 16 + key % 16) * D + d;
-                    x = load4<T>(p.k, at0);
-                    y = load4<T>(p.v, at0);
+                    x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.k) + at0));
+                    y = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.v) + at0));
                 }
                 *reinterpret_cast<float4 *>(&sm.k[r][d]) = x;
                 *reinterpret_cast<float4 *>(&sm.v[r][d]) = y;
@@ -266,11 +245,8 @@ constexpr int kSimplePerSm = 3;  // CTAs
 
 size_t slot_bytes(int rows, int d) { return (size_t)rows * (d + 2) * sizeof(float); }
 
-kv_status launch_simple(const TreeParams &pp, kv_dtype t, int d, cudaStream_t stream) {
-    auto fn = d == 64 ? (t == KV_F32 ? tree_simple_kernel<float, 64>
-                                     : t == KV_BF16 ? tree_simple_kernel<Bf16, 64> : tree_simple_kernel<F16, 64>)
-                      : (t == KV_F32 ? tree_simple_kernel<float, 128>
-                                     : t == KV_BF16 ? tree_simple_kernel<Bf16, 128> : tree_simple_kernel<F16, 128>);
+kv_status launch_simple(const TreeParams &pp, int d, cudaStream_t stream) {
+    auto fn = d == 64 ? tree_simple_kernel<64> : tree_simple_kernel<128>;
     const int smem = d == 64 ? (int)sizeof(SimpleShared<64>) : (int)sizeof(SimpleShared<128>);
     if (kv_status st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
         return st;
@@ -296,8 +272,9 @@ struct Shape {
     int rows;  // query rows of a group, and of a slot
     int runs, min_run;
 };
-Shape shape_of(const kv_pool *, int, int) {
-    return {kSimpleRows, kSimplePerSm * sm_count(), 2 + kTreePairCost};
+Shape shape_of(const kv_pool *p, int g, int max_q_len) {
+    if (p->dtype == KV_F32) return {kSimpleRows, kSimplePerSm * sm_count(), 2 + kTreePairCost};
+    return {max_q_len * g > 128 ? 256 : 128, sm_count(), 2 + kTreePairCost};
 }
 
 // Arguments that the query and the call refuse alike.
@@ -306,7 +283,8 @@ kv_status check(kv_pool_t p, int batch, int num_q_heads, int max_blocks, int max
     if (kv_status st = require_device(p->device)) return st;
     if (p->dtype == KV_I4) return KV_ERR_UNSUPPORTED;
     if (num_q_heads % p->num_kv_heads) return KV_ERR_ARG;
-    if (num_q_heads / p->num_kv_heads > 8 || max_q_len > kMaxNodes || max_blocks > (1 << 27) - 1)
+    if (num_q_heads / p->num_kv_heads > 8 || max_q_len > kMaxNodes || max_blocks > (1 << 27) - 1 ||
+        (p->dtype != KV_F32 && (long long)p->num_blocks * p->num_kv_heads * 16 > INT32_MAX))
         return KV_ERR_UNSUPPORTED;
     return KV_OK;
 }
@@ -362,7 +340,14 @@ kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, 
     pp.lse = lse_out;
     pp.partial = static_cast<float *>(workspace);
     pp.err = p->err;
-    if (kv_status st = tree::launch_simple(pp, p->dtype, p->head_dim, as_stream(stream))) return st;
+    if (p->dtype == KV_F32) {
+        if (kv_status st = tree::launch_simple(pp, p->head_dim, as_stream(stream))) return st;
+    } else {
+        if (kv_status st = p->head_dim == 128 ? pool_tensor_maps(p) : pool_tensor_maps_64(p)) return st;
+        if (kv_status st = tree::launch_tc(pp, p->head_dim, s.rows, p->dtype == KV_F16, p->tmap_k, p->tmap_v,
+                                           as_stream(stream)))
+            return st;
+    }
     return tree::launch_merge(pp, p->head_dim, s.rows, as_stream(stream));
 }
 

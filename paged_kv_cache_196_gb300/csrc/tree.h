@@ -1,5 +1,6 @@
 // Tree attention: what its kernels share.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -24,6 +25,11 @@ struct TreeParams {
     float *partial;          // slots of [D / 4][rows] float4 and [rows] (reference, sum)
     int *err;
 };
+
+// tree_tc.cu: 16-bit pools; groups of `rows` (128 or 256) query rows, tensor maps of the pool's
+// K and V rows.
+kv_status launch_tc(const TreeParams &pp, int d, int rows, bool f16, const CUtensorMap &tk, const CUtensorMap &tv,
+                    cudaStream_t stream);
 
 }  // namespace tree
 }  // namespace pkv

@@ -1,0 +1,830 @@
+// Tree attention on the tcgen05 tensor cores: pools of 16-bit types.
+//
+// A CTA takes a run of pieces (tree_plan.cuh): key tiles of 128 keys (8 blocks) against
+// the query rows of a group, 128 of them (MT = 1) or 256 (MT = 2: two row tiles, which
+// share every key tile).  Per key tile
+//   S = Q K^T      (M = 128 rows, N = 128 keys, fp32 in tensor memory)
+//   softmax warps  S -> P, written over S: of every 32 keys' columns the first 16 hold
+//                  P_hi = t(P) in the pool's type t, the others P_lo = t(P - P_hi), so the
+//                  weights keep 16 significant bits with bf16, 22 with fp16 (a bf16
+//                  weight alone would be off by 2^-8 of itself, as much as a bf16 output)
+//   O += P_hi V + P_lo V   (P from tensor memory)
+// Roles: softmax warps (a thread = a row = a tensor-memory lane), a warp that copies K and V
+// tiles into one ring by TMA (each block-table entry becomes a box of 16 rows per 64
+// dimensions), a thread that issues the products, a warp that copies the rows of the next
+// group's queries.  The ring runs on across pieces.
+//
+// MT = 1: S is double-buffered, so the next tile's scores are computed while the softmax
+// warps work on this one's; so are Q and O, so a piece's end overlaps the next piece's
+// beginning.  A tile that a group does not fill is filled with copies of its rows (DUP: two of
+// up to 64 rows, four of up to 32): the tensor core computes all of S at the same cost, and
+// each copy's warps take their own keys of the tile and leave zeros as the others' weights,
+// so that all four schedulers share the exponentials; the copies' sums meet at the
+// piece's end.  MT = 2: each row tile has one S and one O, and the softmax of one
+// overlaps the products of the other.
+//
+// Tensor memory (512 columns): MT = 1: S at 0 and 128, O at 256 and 384, by tile and by piece
+// in turn; MT = 2: S_A, S_B, O_A, O_B.
+//
+// Only tiles that reach into the tree are masked, by the bits of each row's node and of
+// those above it.  Their V rows are looked over before the product: a weight of zero does
+// not keep out a NaN, so rows behind the sequence become zeros, and so do the
+// infinities and NaN of the tree's own rows, which are added at the end to the rows that
+// attend them.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc.cuh"
+#include "tree.h"
+
+namespace pkv {
+namespace tree {
+
+constexpr float kRenew = 8.0f;  // log2 units by which a maximum passes the reference before sums are scaled
+constexpr uint32_t kColO0 = 256;
+
+template <int D, int MT>
+struct Layout {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalfBytes = 128 * 128;  // 128 rows x 64 values
+    static constexpr int kTileBytes = kHalves * kHalfBytes;
+    static constexpr int kSlots = D == 128 ? 5 : 8;
+    static constexpr int kQBufs = MT == 1 ? 2 : 1;  // of MT tiles
+    static constexpr int kRing = 2 * kTileBytes;
+    static constexpr int kBars = kRing + kSlots * kTileBytes;
+    static constexpr int kSoftmax = 128 * MT;       // threads
+    static constexpr int kCopyWarp = 4 * MT, kMmaWarp = kCopyWarp + 1, kQWarp = kCopyWarp + 2;
+    static constexpr int kThreads = kSoftmax + 96;
+};
+
+template <int D, int MT>
+struct Shared {
+    uint64_t full[Layout<D, MT>::kSlots], empty[Layout<D, MT>::kSlots];
+    uint64_t qfull[2], qempty[2];
+    uint64_t sfull[2], pfull[2];   // MT = 1: by tile in turn; MT = 2: of a row tile
+    uint64_t odone[2];             // a phase per key tile; MT = 2: of a row tile
+    uint64_t oempty[2];            // MT = 1: by piece in turn; MT = 2: of a row tile
+    uint64_t done;
+    uint32_t tmem;
+    int abort;
+    uint32_t gone[8];              // by tile in turn: bit i: block i is not there
+    int nonfinite[2];              // by piece in turn: number of a piece whose tree holds some in V
+    float2 ml[128];                // DUP: reference and sum of each row copy
+    PlaceScratch<Layout<D, MT>::kThreads> scratch;
+};
+
+KV_DEVICE float tc_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+KV_DEVICE float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+KV_DEVICE void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Two weights as a pair of the 16-bit type and the pair of what that leaves of them.
+template <bool F16>
+KV_DEVICE void split(float x, float y, uint32_t &hi, uint32_t &lo) {
+    if constexpr (F16) {
+        hi = tc::pack_f16x2(x, y);
+        const float2 h = f16x2_to_float2(hi);
+        lo = tc::pack_f16x2(x - h.x, y - h.y);
+    } else {
+        hi = tc::pack_bf16x2(x, y);
+        const float2 h = bf16x2_to_float2(hi);
+        lo = tc::pack_bf16x2(x - h.x, y - h.y);
+    }
+}
+
+// D (+)= P B over 128 keys: P at p_tmem in steps of 16 keys, 8 columns each, two steps of every
+// 32 columns; B as in tc::mma_ts_k128.
+KV_DEVICE void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc_first) {
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 t, %5, %5;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+        "add.u32 x, %1, 32;\n\tadd.u32 y, %2, 256;\n\tmov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+        "add.u32 x, %1, 40;\n\tadd.u32 y, %2, 384;\n\tmov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+        "add.u32 x, %1, 64;\n\tadd.u32 y, %2, 512;\n\tmov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+        "add.u32 x, %1, 72;\n\tadd.u32 y, %2, 640;\n\tmov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+        "add.u32 x, %1, 96;\n\tadd.u32 y, %2, 768;\n\tmov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+        "add.u32 x, %1, 104;\n\tadd.u32 y, %2, 896;\n\tmov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t}" ::"r"(d_tmem),
+        "r"(p_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc_first)
+        : "memory");
+}
+
+// D = A B^T over 64 dimensions, as tc::mma_ss_k128 over 128.
+KV_DEVICE void mma_ss_k64(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.u32 p, %4, %4;\n\tsetp.eq.u32 t, %4, %4;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc)
+        : "memory");
+}
+
+// The rows of a piece, the same for every role.
+struct Rows {
+    int node0, rows, copies;  // copies of each row in a tile
+    int before;               // tokens before the tree
+    KV_DEVICE Rows(const TreeParams &p, const Piece &pc, int mt) {
+        node0 = pc.grp * p.plan.group_nodes;
+        rows = min(p.plan.group_nodes, pc.seq.nodes - node0) * p.g;
+        copies = mt == 2 || rows > 64 ? 1 : rows > 32 ? 2 : 4;
+        before = pc.seq.len - pc.seq.nodes;
+    }
+};
+
+// Bits of a row's node and of those above it, 32 nodes a word.
+struct Ancestors {
+    uint32_t w[kMaxNodes / 32];
+
+    // All lanes of a warp: each walks up from its node (a negative one: none).  Lane l holds the
+    // parents of nodes 8 l .. 8 l + 7 as bytes, 255 for none.
+    KV_DEVICE void walk(const int32_t *parents, int nodes, int node, int *err) {
+        const int lane = threadIdx.x & 31;
+        uint32_t lo = 0xffffffffu, hi = 0xffffffffu;
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = 8 * lane + k;
+            int up = -1;
+            if (i < nodes) {
+                up = parents ? __ldg(parents + i) : i - 1;
+                if (up < -1 || up >= i) {
+                    bad = true;
+                    up = -1;
+                }
+            }
+            const uint32_t byte = (uint32_t)up & 255u;
+            if (k < 4)
+                lo = (lo & ~(255u << (8 * k))) | (byte << (8 * k));
+            else
+                hi = (hi & ~(255u << (8 * k - 32))) | (byte << (8 * k - 32));
+        }
+        if (bad) atomicOr(err, KV_DEVERR_TREE);
+#pragma unroll
+        for (int k = 0; k < kMaxNodes / 32; ++k) w[k] = 0;
+        int i = node;
+        while (__any_sync(0xffffffffu, i >= 0)) {
+            const int at = i >= 0 ? i : 0;
+            const uint32_t a = __shfl_sync(0xffffffffu, lo, at >> 3), b = __shfl_sync(0xffffffffu, hi, at >> 3);
+            if (i >= 0) {
+#pragma unroll
+                for (int k = 0; k < kMaxNodes / 32; ++k) w[k] |= (i >> 5) == k ? 1u << (i & 31) : 0u;
+                const uint32_t up = ((i & 4 ? b : a) >> (8 * (i & 3))) & 255u;
+                i = up == 255u ? -1 : (int)up;
+            }
+        }
+    }
+    KV_DEVICE uint32_t word(int at) const {
+        uint32_t x = 0;
+#pragma unroll
+        for (int k = 0; k < kMaxNodes / 32; ++k) x = at == k ? w[k] : x;
+        return x;
+    }
+    // As key_bits: bits of 32 keys from `key` on, counted from the tree's first token.
+    KV_DEVICE uint32_t keys(int key) const {
+        if (key <= -32) return 0xffffffffu;
+        if (key < 0) return (0xffffffffu >> (32 + key)) | (w[0] << -key);
+        return __funnelshift_r(word(key >> 5), word((key >> 5) + 1), key & 31);
+    }
+};
+
+template <int D, bool F16, int MT, bool TW>
+__global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const TreeParams p) {
+    using L = Layout<D, MT>;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    extern __shared__ __align__(1024) char smem_raw[];
+    char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    char *sQ = smem, *ring = smem + L::kRing;
+    auto &sm = *reinterpret_cast<Shared<D, MT> *>(smem + L::kBars);
+
+    if (warp == L::kMmaWarp) {
+        tc::tmem_alloc(&sm.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int s = 0; s < L::kSlots; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sm.qfull[s], 1);
+            mbar_init(&sm.qempty[s], MT == 1 ? 4 : 1);
+            mbar_init(&sm.sfull[s], 1);
+            mbar_init(&sm.pfull[s], 4);
+            mbar_init(&sm.odone[s], 1);
+            mbar_init(&sm.oempty[s], 4);
+            sm.nonfinite[s] = -1;
+        }
+        mbar_init(&sm.done, 1);
+        sm.abort = 0;
+        mbar_init_fence();
+    }
+    const Place at = place(p.plan, blockIdx.x, sm.scratch, blockIdx.x == 0 ? p.err : nullptr);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sm.tmem;
+    volatile int *abort_flag = &sm.abort;
+    Pieces pieces;
+    pieces.start(p.plan, at, blockIdx.x);
+    Piece pc;
+
+    if (warp == L::kCopyWarp) {
+        // ================================================== K and V tiles
+        if (lane == 0) {
+            tc::prefetch_tensormap(&tm_k);
+            tc::prefetch_tensormap(&tm_v);
+        }
+        int slot = 0, phase = 0, turn = 0;
+        unsigned issued = 0;
+        bool stop = false;
+        while (!stop && pieces.next(p.plan, pc)) {
+            const int32_t *table = p.tables + (size_t)pc.b * p.plan.max_blocks;
+            const int blocks = (pc.seq.len + 15) / 16;
+            auto fetch = [&](int t) {  // lanes 0-7: the table's entry; -1: none
+                const int i = t * 8 + lane;
+                return lane < 8 && t < pc.t1 && i < blocks ? __ldg(table + i) : -1;
+            };
+            int id = fetch(pc.t0), id_next = fetch(pc.t0 + 1);
+            for (int t = pc.t0; t < pc.t1; ++t) {
+                const int id_later = fetch(t + 2);
+                const bool want = lane < 8 && t * 8 + lane < blocks;
+                const bool there = id >= 0 && id < p.num_blocks;
+                if (want && !there) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
+                const uint32_t gone = __ballot_sync(0xffffffffu, want && !there) & 255u;
+                // rows -16 .. -1 lie outside the tensor and read as zeros
+                const int y = want && there ? (id * p.plan.hkv + pc.h) * 16 : -16;
+#pragma unroll
+                for (int is_v = 0; is_v < 2; ++is_v) {
+                    if (lane == 0)
+                        stop = *abort_flag || (issued >= L::kSlots && !mbar_wait<TW>(&sm.empty[slot], phase ^ 1, p.err));
+                    stop = __shfl_sync(0xffffffffu, stop, 0);
+                    if (stop) break;
+                    char *dst = ring + slot * L::kTileBytes;
+                    if (lane == 0) {
+                        if (!is_v) sm.gone[turn & 7] = gone;
+                        mbar_arrive_expect_tx(&sm.full[slot], L::kTileBytes);
+                    }
+                    __syncwarp();
+                    if (lane < 8) {
+#pragma unroll
+                        for (int h = 0; h < L::kHalves; ++h)
+                            tc::tma_load_2d(dst + h * L::kHalfBytes + lane * 2048, is_v ? &tm_v : &tm_k, 64 * h, y,
+                                            &sm.full[slot]);
+                    }
+                    ++issued;
+                    if (++slot == L::kSlots) slot = 0, phase ^= 1;
+                }
+                if (stop) break;
+                ++turn;
+                id = id_next;
+                id_next = id_later;
+            }
+        }
+        if (lane == 0) {
+            if (stop) *abort_flag = 1;
+            // no copy may be in flight into this CTA's shared memory when it ends
+            for (int i = 0; i < L::kSlots && i < issued; ++i) {
+                if (--slot < 0) slot = L::kSlots - 1, phase ^= 1;
+                mbar_wait_drain(&sm.full[slot], phase, p.err);
+            }
+        }
+    } else if (warp == L::kQWarp) {
+        // ================================================== query rows
+        // Stored K-major with 128-byte swizzle, as the products read them; rows past the
+        // group's last hold anything (no row reaches another one).
+        int n = 0;
+        bool ok = true;
+        while (ok && pieces.next(p.plan, pc)) {
+            const Rows r(p, pc, MT);
+            const int buf = n % L::kQBufs;
+            if (lane == 0)
+                ok = !*abort_flag &&
+                     (n < L::kQBufs || mbar_wait<TW>(&sm.qempty[buf], (n / L::kQBufs - 1) & 1, p.err));
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            const uint32_t dst = smem_addr(sQ) + buf * L::kTileBytes;
+            const int per_copy = 128 / r.copies;
+            const uint16_t *src = static_cast<const uint16_t *>(p.q) +
+                                  ((size_t)(pc.seq.q0 + r.node0) * p.hq + pc.h * p.g) * D;
+            constexpr int kChunks = D / 8;  // 16-byte parts of a row
+            for (int i = lane; i < r.rows * kChunks; i += 32) {
+                const int row = i / kChunks, c = i % kChunks;
+                const uint16_t *from = src + ((size_t)(row / p.g) * p.hq + row % p.g) * D + 8 * c;
+                for (int copy = 0; copy < r.copies; ++copy) {
+                    const int at_row = row + copy * per_copy;
+                    cp_async16(dst + (at_row >> 7) * L::kTileBytes + (c >> 3) * L::kHalfBytes + (at_row & 127) * 128 +
+                                   (((c & 7) ^ (at_row & 7)) << 4),
+                               from);
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.qfull[buf]);
+            ++n;
+        }
+        if (!ok && lane == 0) *abort_flag = 1;
+    } else if (warp == L::kMmaWarp) {
+        // ================================================== products
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = F16 ? tc::idesc_f16_f32(128, 128, false, false)
+                                              : tc::idesc_bf16_f32(128, 128, false, false);
+            constexpr uint32_t idesc_pv = F16 ? tc::idesc_f16_f32(128, D, false, true)
+                                              : tc::idesc_bf16_f32(128, D, false, true);
+            const uint32_t d_hi = tc::smem_desc_sw128_hi(1024);
+            const uint32_t q_lo = tc::smem_desc_sw128_lo(smem_addr(sQ), 16);
+            const uint32_t k_lo = tc::smem_desc_sw128_lo(smem_addr(ring), 16);
+            const uint32_t v_lo = tc::smem_desc_sw128_lo(smem_addr(ring), L::kHalfBytes);
+            auto issue_s = [&](uint32_t col, int q_tile, int slot) {
+                const uint32_t a = q_lo + ((q_tile * L::kTileBytes) >> 4), b = k_lo + ((slot * L::kTileBytes) >> 4);
+                if constexpr (D == 128)
+                    tc::mma_ss_k128(tmem + col, a, b, d_hi, idesc_qk, 0);
+                else
+                    mma_ss_k64(tmem + col, a, b, d_hi, idesc_qk);
+            };
+            auto issue_pv = [&](uint32_t col_o, uint32_t col_p, int slot, bool first) {
+                const uint32_t b = v_lo + ((slot * L::kTileBytes) >> 4);
+                mma_pv(tmem + col_o, tmem + col_p, b, d_hi, idesc_pv, !first);
+                mma_pv(tmem + col_o, tmem + col_p + 16, b, d_hi, idesc_pv, 1);
+            };
+            bool ok = true;
+            // tile t of the run: K in ring position 2 t, V in 2 t + 1
+            auto wait_full = [&](unsigned pos) {
+                return mbar_wait<TW>(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1, p.err);
+            };
+            if constexpr (MT == 1) {
+                // S(t + 1) is issued before PV(t), across pieces too.
+                unsigned t = 0;       // next PV
+                int n = 0;            // its piece
+                int t_left = 0;       // tiles of it that are left
+                unsigned s = 0;       // next S
+                int sn = -1, s_left = 0;
+                bool more = true;
+                auto next_s = [&]() {  // issues S(s) if there is one
+                    if (s_left == 0) {
+                        if (!more || !(more = pieces.next(p.plan, pc))) return true;
+                        s_left = pc.t1 - pc.t0;
+                        ++sn;
+                        if (!mbar_wait<TW>(&sm.qfull[sn & 1], (sn >> 1) & 1, p.err)) return false;
+                    }
+                    if (!wait_full(2 * s)) return false;
+                    tc::fence_after_sync();
+                    issue_s((s & 1) * 128, sn & 1, (int)(2 * s % L::kSlots));
+                    tc::mma_commit(&sm.sfull[s & 1]);
+                    tc::mma_commit(&sm.empty[2 * s % L::kSlots]);
+                    --s_left;
+                    ++s;
+                    return true;
+                };
+                // lengths of the pieces whose S is issued and whose PV is not: two at most
+                int len[2] = {0, 0};
+                ok = next_s();
+                if (sn >= 0) len[0] = pc.t1 - pc.t0;
+                t_left = len[0];
+                bool first = true;
+                while (ok && t < s) {
+                    const int sn_was = sn;
+                    if (!(ok = next_s())) break;
+                    if (sn != sn_was) len[sn & 1] = pc.t1 - pc.t0;
+                    if (first && n >= 2 && !mbar_wait<TW>(&sm.oempty[n & 1], ((n >> 1) - 1) & 1, p.err)) ok = false;
+                    if (!ok || !mbar_wait<TW>(&sm.pfull[t & 1], (t >> 1) & 1, p.err) || !wait_full(2 * t + 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    issue_pv(kColO0 + 128 * (n & 1), (t & 1) * 128, (int)((2 * t + 1) % L::kSlots), first);
+                    tc::mma_commit(&sm.empty[(2 * t + 1) % L::kSlots]);
+                    tc::mma_commit(&sm.odone[0]);
+                    ++t;
+                    first = --t_left == 0;
+                    if (first) {
+                        ++n;
+                        t_left = len[n & 1];
+                    }
+                }
+            } else {
+                unsigned t = 0;
+                int n = 0, used[2] = {0, 0};  // pieces, and tiles of each row tile, so far
+                int pieces_of[2] = {0, 0};
+                while (ok && pieces.next(p.plan, pc)) {
+                    const Rows r(p, pc, MT);
+                    const int row_tiles = r.rows > 128 ? 2 : 1;
+                    ok = mbar_wait<TW>(&sm.qfull[0], n & 1, p.err) && wait_full(2 * t);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const int tiles = pc.t1 - pc.t0;
+                    for (int x = 0; x < row_tiles; ++x) {
+                        issue_s(128 * x, x, (int)(2 * t % L::kSlots));
+                        tc::mma_commit(&sm.sfull[x]);
+                    }
+                    tc::mma_commit(&sm.empty[2 * t % L::kSlots]);
+                    if (tiles == 1) tc::mma_commit(&sm.qempty[0]);
+                    for (int j = 0; ok && j < tiles; ++j, ++t) {
+                        for (int x = 0; x < row_tiles; ++x) {
+                            if (j == 0 && pieces_of[x] > 0 &&
+                                !mbar_wait<TW>(&sm.oempty[x], (pieces_of[x] - 1) & 1, p.err))
+                                ok = false;
+                            if (!ok || !mbar_wait<TW>(&sm.pfull[x], used[x] & 1, p.err) ||
+                                (x == 0 && !wait_full(2 * t + 1)) ||
+                                (x == 0 && j + 1 < tiles && !wait_full(2 * t + 2))) {
+                                ok = false;
+                                break;
+                            }
+                            tc::fence_after_sync();
+                            issue_pv(kColO0 + 128 * x, 128 * x, (int)((2 * t + 1) % L::kSlots), j == 0);
+                            tc::mma_commit(&sm.odone[x]);
+                            ++used[x];
+                            if (j + 1 < tiles) {
+                                issue_s(128 * x, x, (int)((2 * t + 2) % L::kSlots));
+                                tc::mma_commit(&sm.sfull[x]);
+                            }
+                        }
+                        if (!ok) break;
+                        tc::mma_commit(&sm.empty[(2 * t + 1) % L::kSlots]);
+                        if (j + 1 < tiles) {
+                            tc::mma_commit(&sm.empty[(2 * t + 2) % L::kSlots]);
+                            if (j + 2 == tiles) tc::mma_commit(&sm.qempty[0]);
+                        }
+                    }
+                    for (int x = 0; x < row_tiles; ++x) ++pieces_of[x];
+                    ++n;
+                }
+            }
+            tc::mma_commit(&sm.done);
+            if (!ok) *abort_flag = 1;
+            // no product may still write tensor memory when it is freed
+            mbar_wait_drain(&sm.done, 0, p.err);
+        }
+    } else {
+        // ================================================== softmax
+        const int x = MT == 2 ? warp >> 2 : 0;  // row tile
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const int lane_row = tid & 127;
+        unsigned t = 0;      // tiles of this row tile so far (MT = 1: of the run)
+        unsigned run_t = 0;  // tiles of the run so far
+        int n = 0;         // pieces
+        bool ok = true;
+        while (ok && pieces.next(p.plan, pc)) {
+            const Rows r(p, pc, MT);
+            const int tiles = pc.t1 - pc.t0;
+            if (MT == 2 && x == 1 && r.rows <= 128) {
+                run_t += tiles;
+                ++n;
+                continue;
+            }
+            const int per_copy = 128 / r.copies;
+            const int copy = r.copies == 1 ? 0 : lane_row / per_copy;
+            const int row = 128 * x + (r.copies == 1 ? lane_row : lane_row % per_copy);
+            const bool valid = row < r.rows;
+            const int node = valid ? r.node0 + row / p.g : -1;
+            const bool idle = __all_sync(0xffffffffu, !valid);  // rows of no query
+            Ancestors anc;
+            if (!idle && pc.t1 * kTile > r.before)
+                anc.walk(p.parents ? p.parents + pc.seq.q0 : nullptr, pc.seq.nodes, node, p.err);
+            float m_used = -INFINITY, l_sum = 0.f;
+            for (int j = 0; j < tiles; ++j, ++t, ++run_t) {
+                const int buf = MT == 1 ? (int)(t & 1) : x;
+                const uint32_t phase = MT == 1 ? (t >> 1) & 1 : t & 1;
+                bool bad = *abort_flag != 0;
+                if (!bad) bad = !mbar_wait<TW>(&sm.sfull[buf], phase, p.err);
+                if (__any_sync(0xffffffffu, bad)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+                const int key0 = (pc.t0 + j) * kTile;
+                const bool tail = key0 + kTile > r.before;
+                const uint32_t gone = sm.gone[run_t & 7];
+                const uint32_t scol = tmem + lane_base + 128 * buf;
+                bool rescale = false;
+                float alpha = 1.f;
+                // kCount chunks of 32 keys from chunk c0 on
+                auto weigh = [&](auto count, int c0) {
+                    constexpr int kCount = decltype(count)::value;
+                    uint32_t sv[kCount][32];
+#pragma unroll
+                    for (int i = 0; i < kCount; ++i) tc::tmem_ld32(scol + 32 * (c0 + i), sv[i]);
+                    tc::tmem_wait_ld();
+                    if (tail || gone) {
+#pragma unroll
+                        for (int i = 0; i < kCount; ++i) {
+                            const int c = c0 + i;
+                            uint32_t bits = tail ? anc.keys(key0 + 32 * c - r.before) : 0xffffffffu;
+                            if (gone >> (2 * c) & 1) bits &= 0xffff0000u;
+                            if (gone >> (2 * c + 1) & 1) bits &= 0x0000ffffu;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!(bits >> k & 1)) sv[i][k] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                    float mx[2 * kCount];
+#pragma unroll
+                    for (int c = 0; c < 2 * kCount; ++c) {
+                        const uint32_t *v = &sv[c >> 1][16 * (c & 1)];
+                        float m = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+#pragma unroll
+                        for (int k = 3; k < 15; k += 2) m = max3(m, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                        mx[c] = fmaxf(m, __uint_as_float(v[15]));
+                    }
+#pragma unroll
+                    for (int c = 1; c < 2 * kCount; ++c) mx[0] = fmaxf(mx[0], mx[c]);
+                    const float mrow = mx[0] * p.scale_log2;  // scale > 0
+                    if (m_used == -INFINITY) {
+                        m_used = mrow;
+                    } else if (mrow > m_used + kRenew) {
+                        alpha = tc_ex2(m_used - mrow);
+                        m_used = mrow;
+                        l_sum *= alpha;
+                        rescale = true;
+                    }
+                    const float ref = m_used == -INFINITY ? 0.f : m_used;
+                    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-ref, -ref);
+                    float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                     make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int i = 0; i < kCount; ++i) {
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 xx = __ffma2_rn(make_float2(__uint_as_float(sv[i][2 * k]),
+                                                                     __uint_as_float(sv[i][2 * k + 1])),
+                                                         sc2, nm2);
+                            const float2 e = make_float2(tc_ex2(xx.x), tc_ex2(xx.y));
+                            acc[k & 3] = __fadd2_rn(acc[k & 3], e);
+                            split<F16>(e.x, e.y, hi[k], lo[k]);
+                        }
+                        tc::tmem_st16(scol + 32 * (c0 + i), hi);
+                        tc::tmem_st16(scol + 32 * (c0 + i) + 16, lo);
+                    }
+                    l_sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) + (acc[2].x + acc[2].y) +
+                             (acc[3].x + acc[3].y);
+                    if constexpr (kCount < 4) {  // the other copies' keys
+                        uint32_t zero[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) zero[k] = 0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (c < c0 || c >= c0 + kCount) tc::tmem_st32(scol + 32 * c, zero);
+                    }
+                };
+                if (!idle) {
+                    if (MT == 2 || r.copies == 1)
+                        weigh(std::integral_constant<int, 4>{}, 0);
+                    else if (r.copies == 2)
+                        weigh(std::integral_constant<int, 2>{}, 2 * copy);
+                    else
+                        weigh(std::integral_constant<int, 1>{}, copy);
+                    if (__any_sync(0xffffffffu, rescale)) {
+                        // O holds the products up to the tile before once that one's are done
+                        if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.odone[x], (t - 1) & 1, p.err))) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+                        const uint32_t ocol = tmem + lane_base + kColO0 + 128 * (MT == 1 ? n & 1 : x);
+#pragma unroll 1
+                        for (int i = 0; i < D / 16; ++i) {
+                            uint32_t v[16];
+                            tc::tmem_ld16(ocol + 16 * i, v);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                            tc::tmem_st16(ocol + 16 * i, v);
+                        }
+                    }
+                }
+                if (tail && x == 0) {
+                    // the rows of V that lie in the tree or behind it, one per thread (in an order of
+                    // 16-byte parts that lets eight rows' lie in different banks)
+                    const unsigned pos = 2 * run_t + 1;
+                    if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1, p.err))) {
+                        ok = false;
+                        break;
+                    }
+                    char *vrow = ring + (int)(pos % L::kSlots) * L::kTileBytes + lane_row * 128;
+                    const int key = key0 + lane_row;
+                    if (key >= pc.seq.len) {
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<uint4 *>(vrow + (c >> 3) * L::kHalfBytes + (((c ^ lane) & 7) << 4)) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    } else if (key >= r.before) {
+                        constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
+                        bool some = false;
+#pragma unroll 4
+                        for (int c = 0; c < D / 8; ++c) {
+                            uint4 *at4 = reinterpret_cast<uint4 *>(vrow + (c >> 3) * L::kHalfBytes + (((c ^ lane) & 7) << 4));
+                            uint4 v = *at4;
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            bool here = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if ((w[k] & top) == top) w[k] &= 0xffff0000u, here = true;
+                                if ((w[k] >> 16 & top) == top) w[k] &= 0x0000ffffu, here = true;
+                            }
+                            if (here) *at4 = make_uint4(w[0], w[1], w[2], w[3]);
+                            some |= here;
+                        }
+                        if (some) sm.nonfinite[n & 1] = n;
+                    }
+                    tc::fence_proxy_async_smem();  // before the tensor core reads them
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.pfull[buf]);
+            }
+            // ---- the piece's end
+            if (ok) {
+                // (MT = 1: the last S says that the products up to three tiles back are done, so
+                // the wait for the last one's phase comes after that for the one before it)
+                bool bad = MT == 1 && t >= 2 && !mbar_wait<TW>(&sm.odone[x], t & 1, p.err);
+                bad = bad || !mbar_wait<TW>(&sm.odone[x], (t - 1) & 1, p.err);
+                ok = !__any_sync(0xffffffffu, bad);
+            }
+            // all warps of the CTA stay or leave together (only then may they meet again)
+            if constexpr (MT == 1) {
+                sm.ml[lane_row] = make_float2(m_used, l_sum);
+                ok = !named_bar_or(1, L::kSoftmax, !ok);
+            }
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint32_t ocol = tmem + lane_base + kColO0 + 128 * (MT == 1 ? n & 1 : x);
+            const bool nonfinite = *reinterpret_cast<volatile int *>(&sm.nonfinite[n & 1]) == n;
+            float factor = 1.f;
+            if (MT == 1 && r.copies > 1) {
+                // the copies of a row share a reference from here on
+                float M = -INFINITY;
+                for (int c = 0; c < r.copies; ++c) M = fmaxf(M, sm.ml[lane_row % per_copy + c * per_copy].x);
+                const float ref = M == -INFINITY ? 0.f : M;
+                float l = 0.f;
+                for (int c = 0; c < r.copies; ++c) {
+                    const float2 ml = sm.ml[lane_row % per_copy + c * per_copy];
+                    l += tc_ex2(ml.x - ref) * ml.y;
+                }
+                factor = tc_ex2(m_used - ref);
+                m_used = M;
+                l_sum = l;
+            }
+            const bool stores = valid && copy == 0;
+            const size_t orow = valid ? (size_t)(pc.seq.q0 + node) * p.hq + pc.h * p.g + row % p.g : 0;
+            const bool seen = l_sum != 0.f;  // a row with a NaN score stays NaN
+            const float inv = pc.slot >= 0 ? 1.f : seen ? 1.f / l_sum : 0.f;
+            float *part = p.partial + (size_t)max(pc.slot, 0) * (128 * MT) * (D + 2);
+            // 32 columns at a time, so that what copies exchange fits their Q buffer (free by now)
+            float4 *box = reinterpret_cast<float4 *>(sQ + (MT == 1 ? (n & 1) * L::kTileBytes : 0));
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+                uint32_t v[32];
+                tc::tmem_ld32(ocol + 32 * i, v);
+                tc::tmem_wait_ld();
+                float o[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(v[k]);
+                if (MT == 1 && r.copies > 1) {
+                    // (box: [8][rows of the copies behind the first] float4)
+                    if (i > 0) named_bar_sync(2, L::kSoftmax);  // the columns before were read
+                    if (copy > 0) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            box[k * 128 + lane_row] = make_float4(o[4 * k] * factor, o[4 * k + 1] * factor,
+                                                                  o[4 * k + 2] * factor, o[4 * k + 3] * factor);
+                    }
+                    named_bar_sync(2, L::kSoftmax);
+                    if (copy == 0) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] *= factor;
+                        for (int c = 1; c < r.copies; ++c) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float4 y = box[k * 128 + lane_row + c * per_copy];
+                                o[4 * k] += y.x, o[4 * k + 1] += y.y, o[4 * k + 2] += y.z, o[4 * k + 3] += y.w;
+                            }
+                        }
+                    }
+                }
+                if (nonfinite && stores) {
+                    // what was kept out of the products, for the rows that attend it
+                    const int32_t *table = p.tables + (size_t)pc.b * p.plan.max_blocks;
+                    for (int k = 0; k < pc.seq.nodes; ++k) {
+                        const int key = r.before + k;
+                        if (!(anc.word(k >> 5) >> (k & 31) & 1) || key < pc.t0 * kTile || key >= pc.t1 * kTile) continue;
+                        const int id = __ldg(table + key / 16);
+                        if (id < 0 || id >= p.num_blocks) continue;
+                        const uint16_t *from = static_cast<const uint16_t *>(p.v) +
+                                               (((size_t)id * p.plan.hkv + pc.h) * 16 + key % 16) * D + 32 * i;
+#pragma unroll
+                        for (int d = 0; d < 32; ++d) {
+                            const float y = F16 ? f16x2_to_float2(from[d]).x : bf16_to_float(from[d]);
+                            if (!(fabsf(y) < INFINITY)) o[d] += y;
+                        }
+                    }
+                }
+                if (!stores) continue;
+                if (pc.slot >= 0) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        reinterpret_cast<float4 *>(part)[(8 * i + k) * (128 * MT) + row] =
+                            make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                } else if (p.out_type == KV_F32) {
+                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + orow * D + 32 * i);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + orow * D + 32 * i);
+                    auto pack = [&](int k) {
+                        return F16 ? tc::pack_f16x2(o[k] * inv, o[k + 1] * inv) : tc::pack_bf16x2(o[k] * inv, o[k + 1] * inv);
+                    };
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        dst[k] = make_uint4(pack(8 * k), pack(8 * k + 2), pack(8 * k + 4), pack(8 * k + 6));
+                }
+            }
+            if (stores) {
+                if (pc.slot >= 0)
+                    reinterpret_cast<float2 *>(part + (size_t)128 * MT * D)[row] = make_float2(m_used, l_sum);
+                else if (p.lse)
+                    p.lse[orow] = seen ? (m_used + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm.oempty[MT == 1 ? n & 1 : x]);
+                if (MT == 1) mbar_arrive(&sm.qempty[n & 1]);
+            }
+            ++n;
+        }
+        if (!ok) *abort_flag = 1;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == L::kMmaWarp) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+namespace {
+
+template <int D, int MT>
+kv_status launch(const TreeParams &pp, bool f16, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t stream) {
+    using L = Layout<D, MT>;
+    constexpr int smem = L::kBars + (int)sizeof(Shared<D, MT>) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    auto fn = test_waits_enabled() ? (f16 ? tree_tc_kernel<D, true, MT, true> : tree_tc_kernel<D, false, MT, true>)
+                                   : (f16 ? tree_tc_kernel<D, true, MT, false> : tree_tc_kernel<D, false, MT, false>);
+    if (kv_status st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+        return st;
+    fn<<<pp.plan.runs, L::kThreads, smem, stream>>>(tk, tv, pp);
+    return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
+kv_status launch_tc(const TreeParams &pp, int d, int rows, bool f16, const CUtensorMap &tk, const CUtensorMap &tv,
+                    cudaStream_t stream) {
+    if (d == 128)
+        return rows == 128 ? launch<128, 1>(pp, f16, tk, tv, stream) : launch<128, 2>(pp, f16, tk, tv, stream);
+    return rows == 128 ? launch<64, 1>(pp, f16, tk, tv, stream) : launch<64, 2>(pp, f16, tk, tv, stream);
+}
+
+}  // namespace tree
+
+cudaError_t set_wait_limit_tree(unsigned long long ns) { return set_wait_limit_here(ns); }
+
+}  // namespace pkv

@@ -245,6 +245,27 @@ def test_two_graphs_share_a_workspace():
         two.close()
 
 
+@pytest.mark.parametrize("d,nodes", [(64, 9), (128, 9), (128, 30), (128, 70), (64, 70)])
+def test_waits_that_run_out(d, nodes):
+    case = TreeCase("bf16", d, 2, 4, [2000, 40], [nodes, 3], seed=8)
+    try:
+        a = case.args("f32")
+        case.call(a)
+        case.check(a)
+        pk.kv_debug_set_wait_limit_ns(0)
+        try:
+            case.call(a)
+            torch.cuda.synchronize()
+            assert pk.kv_get_device_error(case.pool) & 0x4
+        finally:
+            pk.kv_debug_set_wait_limit_ns(pk.KV_WAIT_LIMIT_DEFAULT_NS)
+        a["out"].fill_(777)
+        case.call(a)
+        case.check(a)
+    finally:
+        case.close()
+
+
 def test_on_a_stream_of_its_own():
     case = TreeCase("f16", 128, 2, 4, [700, 20], [9, 3])
     try:
