@@ -27,7 +27,8 @@ struct kv_pool {
     CUtensorMap tmap_k;
     CUtensorMap tmap_v;
     bool tmaps_ready = false;
-    bool tmaps_64_ready = false;  // head_dim 64 (tree attention)
+    CUtensorMap gmap_k, gmap_v;  // of groups of 8 rows (built on first tree attention)
+    bool gmaps_ready = false;
     // decode launches may overlap the previous kernel in the stream
     // (kv_pool_set_launch_overlap)
     bool launch_overlap = false;
@@ -106,12 +107,15 @@ inline kv_status device_error_status(int code) {
 
 int sm_count();
 
-// tiled-TMA maps (tmap.cu): 16-bit rows of `dim` values, boxes 16 x 64, 128B swizzle
-bool encode_rows_map(CUtensorMap *m, void *base, long long rows, int dim = 128);
+// tiled-TMA maps (tmap.cu): bf16 rows of 128 values, boxes 16 x 64, 128B swizzle
+bool encode_rows_map(CUtensorMap *m, void *base, long long rows);
+// 16-bit rows of `dim` (64 or 128) values in groups of 8: {64 values, 8 rows, dim / 64, groups},
+// boxes of two whole groups (a block), 128B swizzle
+bool encode_groups_map(CUtensorMap *m, void *base, long long rows, int dim);
 // queries [rows][hq][128]: boxes of box_rows rows x box_heads heads x 64 values
 bool encode_q_map(CUtensorMap *m, const void *q, int rows, int hq, int box_heads, int box_rows);
-kv_status pool_tensor_maps(kv_pool *p);     // of a pool with head_dim 128
-kv_status pool_tensor_maps_64(kv_pool *p);  // 64
+kv_status pool_tensor_maps(kv_pool *p);  // of a pool with head_dim 128
+kv_status pool_group_maps(kv_pool *p);
 
 // ---- decode (shared by the paged and contiguous paths) ----
 struct DecodeArgs {

@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
     extern __shared__ __align__(16) char raw[];
     auto &sm = *reinterpret_cast<SimpleShared<D> *>(raw);
     const int tid = threadIdx.x, ty = tid / 8, tx = tid % 8;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this kernel's end
     const Place at = place(p.plan, blockIdx.x, sm.scratch, blockIdx.x == 0 ? p.err : nullptr);
     Pieces pieces;
     pieces.start(p.plan, at, blockIdx.x);
@@ -187,49 +188,66 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
 }
 
 // ---------------------------------------------------------------- cut pairs
-// CTA x > 0 looks at the end of run x - 1: if it lies among the tiles of a pair, the pair
-// is cut, and this CTA takes one share of its rows, one share per cut.
-constexpr int kMergeThreads = 256;
+// CTA x looks at the end of run x: if it lies among the tiles of a pair, the pair is cut,
+// and this CTA (with those of other y) takes one share of its rows, one share per cut.  A
+// warp takes 8 rows of 16 dimensions, so that it reads lines and writes sectors whole.
+// Launched while the attention kernel runs, so that finding the place costs nothing.
+constexpr int kMergeThreads = 256, kMergeShares = 8, kMergeAhead = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p, int slot_rows) {
     __shared__ PlaceScratch<kMergeThreads> scratch;
     const int r = blockIdx.x + 1;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const Place at = place(p.plan, r, scratch, nullptr);
     if (at.b >= p.plan.batch) return;
     const Seq seq = load_seq(p.plan, at.b, nullptr);
-    const long long cost = seq.pair_units();
-    const int pair = (int)((r * at.per - at.base) / cost);
-    const long long first = at.base + pair * cost;
-    const int r0 = (int)((first + kTreePairCost) / at.per);  // the run that has the first tile
-    const int r1 = (int)((first + cost - 1) / at.per);       // and the last
+    const int cost = seq.tiles + kTreePairCost;
+    const int r0 = (int)((at.first + kTreePairCost) / at.per);  // the run that has the pair's first tile
+    const int r1 = (int)((at.first + cost - 1) / at.per);       // and the last
     if (r <= r0 || r > r1) return;
-    const int h = pair / seq.groups, node0 = (pair - h * seq.groups) * p.plan.group_nodes;
+    const int h = at.pair / seq.groups, node0 = (at.pair - h * seq.groups) * p.plan.group_nodes;
     const int rows = min(p.plan.group_nodes, seq.nodes - node0) * p.g;
-    const int shares = (r1 - r0) * gridDim.y, share = (r - r0 - 1) * gridDim.y + blockIdx.y;
+    const int shares = (r1 - r0) * kMergeShares, share = (r - r0 - 1) * kMergeShares + blockIdx.y;
     const int row0 = (int)((long long)rows * share / shares), row1 = (int)((long long)rows * (share + 1) / shares);
     const size_t step = (size_t)slot_rows * (D + 2);
-    const int slot0 = 2 * r0 + (first < r0 * at.per ? 0 : 1);
-    for (int i = threadIdx.x; i < (row1 - row0) * (D / 4); i += kMergeThreads) {
-        const int dq = i / (row1 - row0), row = row0 + i - dq * (row1 - row0);
-        float M = -INFINITY;
-        for (int s = r0; s <= r1; ++s) {
-            const float *part = p.partial + (s == r0 ? slot0 : 2 * s) * step;
-            M = fmaxf(M, reinterpret_cast<const float2 *>(part + (size_t)slot_rows * D)[row].x);
-        }
-        const float ref = M == -INFINITY ? 0.f : M;
+    const int slot0 = 2 * r0 + (at.first < r0 * at.per ? 0 : 1);
+    const int lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kWide = D / 16;  // warps' worth of dimensions
+    for (int w = threadIdx.x >> 5; w < (row1 - row0 + 7) / 8 * kWide; w += kMergeThreads / 32) {
+        const int row = row0 + w / kWide * 8 + (lane & 7), dq = w % kWide * 4 + (lane >> 3);
+        if (row >= row1) continue;
+        float M = -INFINITY, den = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        float den = 0.f;
-#pragma unroll 4
-        for (int s = r0; s <= r1; ++s) {
-            const float *part = p.partial + (s == r0 ? slot0 : 2 * s) * step;
-            const float2 ml = reinterpret_cast<const float2 *>(part + (size_t)slot_rows * D)[row];
-            const float4 v = reinterpret_cast<const float4 *>(part)[(size_t)dq * slot_rows + row];
-            const float e = ex2(ml.x - ref);
-            // (a piece without a key of the row has nothing to add, whatever its reference)
-            den += ml.y == 0.f ? 0.f : e * ml.y;
-            if (ml.y != 0.f) a.x += e * v.x, a.y += e * v.y, a.z += e * v.z, a.w += e * v.w;
+        for (int s0 = r0; s0 <= r1; s0 += kMergeAhead) {
+            float2 ml[kMergeAhead];
+            float4 v[kMergeAhead];
+#pragma unroll
+            for (int i = 0; i < kMergeAhead; ++i) {
+                const int s = s0 + i;
+                ml[i] = make_float2(-INFINITY, 0.f);
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (s <= r1) {
+                    const float *part = p.partial + (s == r0 ? slot0 : 2 * s) * step;
+                    ml[i] = reinterpret_cast<const float2 *>(part + (size_t)slot_rows * D)[row];
+                    v[i] = reinterpret_cast<const float4 *>(part)[(size_t)dq * slot_rows + row];
+                }
+            }
+            float up = M;
+#pragma unroll
+            for (int i = 0; i < kMergeAhead; ++i) up = fmaxf(up, ml[i].x);
+            const float ref = up == -INFINITY ? 0.f : up;
+            const float alpha = ex2(M - ref);
+            M = up;
+            den *= alpha;
+            a.x *= alpha, a.y *= alpha, a.z *= alpha, a.w *= alpha;
+#pragma unroll
+            for (int i = 0; i < kMergeAhead; ++i) {
+                if (ml[i].y == 0.f) continue;  // a piece without a key of the row has nothing to add
+                const float e = ex2(ml[i].x - ref);
+                den += e * ml[i].y;
+                a.x += e * v[i].x, a.y += e * v[i].y, a.z += e * v[i].z, a.w += e * v[i].w;
+            }
         }
         const bool seen = den != 0.f;
         const float inv = seen ? 1.f / den : 0.f;
@@ -256,7 +274,7 @@ kv_status launch_simple(const TreeParams &pp, int d, cudaStream_t stream) {
 
 kv_status launch_merge(const TreeParams &pp, int d, int slot_rows, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)pp.plan.runs - 1, 2);
+    cfg.gridDim = dim3((unsigned)pp.plan.runs - 1, kMergeShares);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -343,8 +361,8 @@ kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, 
     if (p->dtype == KV_F32) {
         if (kv_status st = tree::launch_simple(pp, p->head_dim, as_stream(stream))) return st;
     } else {
-        if (kv_status st = p->head_dim == 128 ? pool_tensor_maps(p) : pool_tensor_maps_64(p)) return st;
-        if (kv_status st = tree::launch_tc(pp, p->head_dim, s.rows, p->dtype == KV_F16, p->tmap_k, p->tmap_v,
+        if (kv_status st = pool_group_maps(p)) return st;
+        if (kv_status st = tree::launch_tc(pp, p->head_dim, s.rows, p->dtype == KV_F16, p->gmap_k, p->gmap_v,
                                            as_stream(stream)))
             return st;
     }

@@ -59,11 +59,11 @@ KV_DEVICE long long seq_units(const Plan &p, const Seq &s) {
     return s.nodes ? (long long)p.hkv * s.groups * s.pair_units() : 0;
 }
 
-// What a CTA knows after place(): units of a run, all units, and the sequence that holds
-// the unit it asked for (batch: none) with the first unit of that sequence.
+// What a CTA knows after place(): units of a run, all units, and of the unit it asked for
+// the sequence (batch: none), the pair of it and that pair's first unit.
 struct Place {
-    long long per, total, base;
-    int b;
+    long long per, total, first;
+    int b, pair;
 };
 
 template <int kThreads>
@@ -97,13 +97,15 @@ KV_DEVICE Place place(const Plan &p, int run, PlaceScratch<kThreads> &s, int *er
     upto += before;
     const long long per = max((long long)p.min_run, (total + p.runs - 1) / p.runs);
     const long long unit = run * per;
-    if (tid == 0 && unit >= total) s.at = Place{per, total, total, p.batch};
+    if (tid == 0 && unit >= total) s.at = Place{per, total, total, p.batch, 0};
     if (unit < upto && unit >= upto - mine) {
         long long base = upto - mine;
         for (int b = b0; b < b1; ++b) {
-            const long long n = seq_units(p, load_seq(p, b, nullptr));
+            const Seq q = load_seq(p, b, nullptr);
+            const long long n = seq_units(p, q);
             if (unit < base + n) {
-                s.at = Place{per, total, base, b};
+                const int pair = (int)((unit - base) / q.pair_units());
+                s.at = Place{per, total, base + pair * q.pair_units(), b, pair};
                 break;
             }
             base += n;
@@ -122,44 +124,47 @@ struct Piece {
 
 // The pieces of a run, in order.
 struct Pieces {
-    long long unit, end, base;
-    int b, run;
+    long long unit, end, first;  // first: of the pair
+    int b, pair, run;
     Seq seq, ahead;  // of sequences b and b + 1
 
     KV_DEVICE void start(const Plan &p, const Place &at, int r) {
         run = r;
         unit = r * at.per;
         end = min(at.total, unit + at.per);
-        base = at.base;
+        first = at.first;
         b = at.b;
-        if (b < p.batch) {
-            seq = load_seq(p, b, nullptr);
-            ahead = b + 1 < p.batch ? load_seq(p, b + 1, nullptr) : Seq{0, 0, 0, 0, 0};
-        }
+        pair = at.pair;
+        if (unit >= end) return;
+        seq = load_seq(p, b, nullptr);
+        load_ahead(p);
+    }
+    KV_DEVICE void load_ahead(const Plan &p) {
+        ahead = Seq{0, 0, 0, 0, 0};
+        if (b + 1 < p.batch) ahead = load_seq(p, b + 1, nullptr);
     }
     KV_DEVICE bool next(const Plan &p, Piece &out) {
-        while (unit < end && b < p.batch) {
-            const long long all = seq_units(p, seq);
-            if (unit >= base + all) {
-                base += all;
+        while (unit < end) {
+            if (pair == p.hkv * seq.groups) {  // (a sequence without nodes has no pairs)
+                pair = 0;
                 ++b;
                 seq = ahead;
-                ahead = b + 1 < p.batch ? load_seq(p, b + 1, nullptr) : Seq{0, 0, 0, 0, 0};
+                load_ahead(p);
                 continue;
             }
-            const long long cost = seq.pair_units();
-            const int pair = (int)((unit - base) / cost);
-            const long long first = base + pair * cost;
-            const long long from = unit - first;
-            const long long to = p.whole ? cost : min(end - first, cost);
-            unit = first + cost;
+            const int cost = seq.tiles + kTreePairCost;
+            const int from = (int)(unit - first);
+            const int to = p.whole ? cost : (int)min(end - first, (long long)cost);
+            const int now = pair++;
+            first += cost;
+            unit = first;
             if (p.whole && from > 0) continue;  // the run before has it
-            out.t0 = (int)max(0LL, from - kTreePairCost);
-            out.t1 = (int)max(0LL, to - kTreePairCost);
+            out.t0 = max(0, from - kTreePairCost);
+            out.t1 = max(0, to - kTreePairCost);
             if (out.t0 >= out.t1) continue;
             out.b = b;
-            out.h = pair / seq.groups;
-            out.grp = pair - out.h * seq.groups;
+            out.h = seq.groups == 1 ? now : now / seq.groups;
+            out.grp = now - out.h * seq.groups;
             out.slot = out.t0 == 0 && out.t1 == seq.tiles ? -1 : 2 * run + (from > 0 ? 0 : 1);
             out.seq = seq;
             return true;

@@ -50,9 +50,11 @@ constexpr uint32_t kColO0 = 256;
 
 template <int D, int MT>
 struct Layout {
+    // A tile is 128 rows, in groups of 8 rows: 64 dimensions of them (a swizzle atom of
+    // 1 KiB), then the other 64.  So a block is one box of one copy.
     static constexpr int kHalves = D / 64;
-    static constexpr int kHalfBytes = 128 * 128;  // 128 rows x 64 values
-    static constexpr int kTileBytes = kHalves * kHalfBytes;
+    static constexpr int kGroupBytes = 1024 * kHalves;
+    static constexpr int kTileBytes = 16 * kGroupBytes;
     static constexpr int kSlots = D == 128 ? 5 : 8;
     static constexpr int kQBufs = MT == 1 ? 2 : 1;  // of MT tiles
     static constexpr int kRing = 2 * kTileBytes;
@@ -61,6 +63,12 @@ struct Layout {
     static constexpr int kCopyWarp = 4 * MT, kMmaWarp = kCopyWarp + 1, kQWarp = kCopyWarp + 2;
     static constexpr int kThreads = kSoftmax + 96;
 };
+
+// Where 16-byte part c of a row lies in its tile.
+template <int D>
+KV_DEVICE int tile_offset(int row, int c) {
+    return (row >> 3) * (1024 * (D / 64)) + (c >> 3) * 1024 + (row & 7) * 128 + (((c ^ row) & 7) << 4);
+}
 
 template <int D, int MT>
 struct Shared {
@@ -90,6 +98,15 @@ KV_DEVICE float max3(float a, float b, float c) {
     return r;
 }
 
+// A block's rows: all of the first three dimensions, two groups of 8 rows from `group` on.
+KV_DEVICE void tma_load_4d(void *dst, const CUtensorMap *map, int group, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(0), "r"(group), "r"(smem_addr(bar))
+        : "memory");
+}
+
 KV_DEVICE void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -109,36 +126,37 @@ KV_DEVICE void split(float x, float y, uint32_t &hi, uint32_t &lo) {
 }
 
 // D (+)= P B over 128 keys: P at p_tmem in steps of 16 keys, 8 columns each, two steps of every
-// 32 columns; B as in tc::mma_ts_k128.
-KV_DEVICE void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc_first) {
+// 32 columns; B (V, MN-major) advances by `step` 16-byte units per 16 keys.
+KV_DEVICE void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc_first,
+                      uint32_t step) {
     asm volatile(
         "{\n\t.reg .pred p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
         "setp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 t, %5, %5;\n\t"
         "mov.b64 b, {%2, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t"
-        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 32;\n\tadd.u32 y, %2, 256;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, 32;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 40;\n\tadd.u32 y, %2, 384;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, 40;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 64;\n\tadd.u32 y, %2, 512;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, 64;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 72;\n\tadd.u32 y, %2, 640;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, 72;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 96;\n\tadd.u32 y, %2, 768;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, 96;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 104;\n\tadd.u32 y, %2, 896;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, 104;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t}" ::"r"(d_tmem),
-        "r"(p_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc_first)
+        "r"(p_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc_first), "r"(step)
         : "memory");
 }
 
-// D = A B^T over 64 dimensions, as tc::mma_ss_k128 over 128.
-KV_DEVICE void mma_ss_k64(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc) {
+// D (+)= A B^T over 64 dimensions, both K-major.
+KV_DEVICE void mma_ss_k64(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc_first) {
     asm volatile(
         "{\n\t.reg .pred p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.u32 p, %4, %4;\n\tsetp.eq.u32 t, %4, %4;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 t, %5, %5;\n\t"
         "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t"
         "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
@@ -147,7 +165,7 @@ KV_DEVICE void mma_ss_k64(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_
         "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
         "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc)
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc_first)
         : "memory");
 }
 
@@ -225,6 +243,8 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                    const TreeParams p) {
     using L = Layout<D, MT>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the kernel that adds up cut pairs may start beside this one; it waits for its end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) char smem_raw[];
     char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     char *sQ = smem, *ring = smem + L::kRing;
@@ -285,8 +305,8 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 const bool there = id >= 0 && id < p.num_blocks;
                 if (want && !there) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
                 const uint32_t gone = __ballot_sync(0xffffffffu, want && !there) & 255u;
-                // rows -16 .. -1 lie outside the tensor and read as zeros
-                const int y = want && there ? (id * p.plan.hkv + pc.h) * 16 : -16;
+                // groups of 8 rows: -2 and -1 lie outside the tensor and read as zeros
+                const int y = want && there ? (id * p.plan.hkv + pc.h) * 2 : -2;
 #pragma unroll
                 for (int is_v = 0; is_v < 2; ++is_v) {
                     if (lane == 0)
@@ -299,12 +319,8 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         mbar_arrive_expect_tx(&sm.full[slot], L::kTileBytes);
                     }
                     __syncwarp();
-                    if (lane < 8) {
-#pragma unroll
-                        for (int h = 0; h < L::kHalves; ++h)
-                            tc::tma_load_2d(dst + h * L::kHalfBytes + lane * 2048, is_v ? &tm_v : &tm_k, 64 * h, y,
-                                            &sm.full[slot]);
-                    }
+                    if (lane < 8)
+                        tma_load_4d(dst + lane * 2 * L::kGroupBytes, is_v ? &tm_v : &tm_k, y, &sm.full[slot]);
                     ++issued;
                     if (++slot == L::kSlots) slot = 0, phase ^= 1;
                 }
@@ -346,9 +362,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 const uint16_t *from = src + ((size_t)(row / p.g) * p.hq + row % p.g) * D + 8 * c;
                 for (int copy = 0; copy < r.copies; ++copy) {
                     const int at_row = row + copy * per_copy;
-                    cp_async16(dst + (at_row >> 7) * L::kTileBytes + (c >> 3) * L::kHalfBytes + (at_row & 127) * 128 +
-                                   (((c & 7) ^ (at_row & 7)) << 4),
-                               from);
+                    cp_async16(dst + (at_row >> 7) * L::kTileBytes + tile_offset<D>(at_row & 127, c), from);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -365,21 +379,21 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                                               : tc::idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t idesc_pv = F16 ? tc::idesc_f16_f32(128, D, false, true)
                                               : tc::idesc_bf16_f32(128, D, false, true);
-            const uint32_t d_hi = tc::smem_desc_sw128_hi(1024);
+            const uint32_t d_hi = tc::smem_desc_sw128_hi(L::kGroupBytes);
             const uint32_t q_lo = tc::smem_desc_sw128_lo(smem_addr(sQ), 16);
             const uint32_t k_lo = tc::smem_desc_sw128_lo(smem_addr(ring), 16);
-            const uint32_t v_lo = tc::smem_desc_sw128_lo(smem_addr(ring), L::kHalfBytes);
+            const uint32_t v_lo = tc::smem_desc_sw128_lo(smem_addr(ring), 1024);  // (the other 64 dimensions)
             auto issue_s = [&](uint32_t col, int q_tile, int slot) {
                 const uint32_t a = q_lo + ((q_tile * L::kTileBytes) >> 4), b = k_lo + ((slot * L::kTileBytes) >> 4);
-                if constexpr (D == 128)
-                    tc::mma_ss_k128(tmem + col, a, b, d_hi, idesc_qk, 0);
-                else
-                    mma_ss_k64(tmem + col, a, b, d_hi, idesc_qk);
+#pragma unroll
+                for (int h = 0; h < L::kHalves; ++h)
+                    mma_ss_k64(tmem + col, a + 64 * h, b + 64 * h, d_hi, idesc_qk, h);
             };
             auto issue_pv = [&](uint32_t col_o, uint32_t col_p, int slot, bool first) {
                 const uint32_t b = v_lo + ((slot * L::kTileBytes) >> 4);
-                mma_pv(tmem + col_o, tmem + col_p, b, d_hi, idesc_pv, !first);
-                mma_pv(tmem + col_o, tmem + col_p + 16, b, d_hi, idesc_pv, 1);
+                constexpr uint32_t step = 2 * L::kGroupBytes / 16;
+                mma_pv(tmem + col_o, tmem + col_p, b, d_hi, idesc_pv, !first, step);
+                mma_pv(tmem + col_o, tmem + col_p + 16, b, d_hi, idesc_pv, 1, step);
             };
             bool ok = true;
             // tile t of the run: K in ring position 2 t, V in 2 t + 1
@@ -512,6 +526,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             const bool valid = row < r.rows;
             const int node = valid ? r.node0 + row / p.g : -1;
             const bool idle = __all_sync(0xffffffffu, !valid);  // rows of no query
+            const int chunks = 4 / r.copies, c0 = copy * chunks;  // of 32 keys of a tile, this copy's
             Ancestors anc;
             if (!idle && pc.t1 * kTile > r.before)
                 anc.walk(p.parents ? p.parents + pc.seq.q0 : nullptr, pc.seq.nodes, node, p.err);
@@ -532,37 +547,44 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 const uint32_t scol = tmem + lane_base + 128 * buf;
                 bool rescale = false;
                 float alpha = 1.f;
-                // kCount chunks of 32 keys from chunk c0 on
-                auto weigh = [&](auto count, int c0) {
-                    constexpr int kCount = decltype(count)::value;
-                    uint32_t sv[kCount][32];
-#pragma unroll
-                    for (int i = 0; i < kCount; ++i) tc::tmem_ld32(scol + 32 * (c0 + i), sv[i]);
-                    tc::tmem_wait_ld();
+                if (!idle) {
+                    // Loops over chunks of 32 keys are not unrolled, and scores are read twice:
+                    // the code of a tile has to stay in the instruction caches.
+                    const int c1 = c0 + chunks;
                     if (tail || gone) {
-#pragma unroll
-                        for (int i = 0; i < kCount; ++i) {
-                            const int c = c0 + i;
+#pragma unroll 1
+                        for (int c = c0; c < c1; ++c) {
                             uint32_t bits = tail ? anc.keys(key0 + 32 * c - r.before) : 0xffffffffu;
                             if (gone >> (2 * c) & 1) bits &= 0xffff0000u;
                             if (gone >> (2 * c + 1) & 1) bits &= 0x0000ffffu;
+                            uint32_t v[32];
+                            tc::tmem_ld32(scol + 32 * c, v);
+                            tc::tmem_wait_ld();
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if (!(bits >> k & 1)) sv[i][k] = __float_as_uint(-INFINITY);
+                                if (!(bits >> k & 1)) v[k] = __float_as_uint(-INFINITY);
+                            tc::tmem_st32(scol + 32 * c, v);
                         }
+                        tc::tmem_wait_st();
                     }
-                    float mx[2 * kCount];
+                    float mrow = -INFINITY;
+#pragma unroll 1
+                    for (int c = c0; c < c1; ++c) {
+                        uint32_t v[32];
+                        tc::tmem_ld32(scol + 32 * c, v);
+                        tc::tmem_wait_ld();
+                        float m[4];
 #pragma unroll
-                    for (int c = 0; c < 2 * kCount; ++c) {
-                        const uint32_t *v = &sv[c >> 1][16 * (c & 1)];
-                        float m = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-#pragma unroll
-                        for (int k = 3; k < 15; k += 2) m = max3(m, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                        mx[c] = fmaxf(m, __uint_as_float(v[15]));
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t *w = &v[8 * i];
+                            m[i] = max3(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]));
+                            m[i] = max3(m[i], __uint_as_float(w[3]), __uint_as_float(w[4]));
+                            m[i] = max3(m[i], __uint_as_float(w[5]), __uint_as_float(w[6]));
+                            m[i] = fmaxf(m[i], __uint_as_float(w[7]));
+                        }
+                        mrow = max3(mrow, max3(m[0], m[1], m[2]), m[3]);
                     }
-#pragma unroll
-                    for (int c = 1; c < 2 * kCount; ++c) mx[0] = fmaxf(mx[0], mx[c]);
-                    const float mrow = mx[0] * p.scale_log2;  // scale > 0
+                    mrow *= p.scale_log2;  // scale > 0
                     if (m_used == -INFINITY) {
                         m_used = mrow;
                     } else if (mrow > m_used + kRenew) {
@@ -573,41 +595,31 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                     const float ref = m_used == -INFINITY ? 0.f : m_used;
                     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-ref, -ref);
-                    float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                                     make_float2(0.f, 0.f)};
-#pragma unroll
-                    for (int i = 0; i < kCount; ++i) {
-                        uint32_t hi[16], lo[16];
+                    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                    for (int c = c0; c < c1; ++c) {
+                        uint32_t v[32], w[32];
+                        tc::tmem_ld32(scol + 32 * c, v);
+                        tc::tmem_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const float2 xx = __ffma2_rn(make_float2(__uint_as_float(sv[i][2 * k]),
-                                                                     __uint_as_float(sv[i][2 * k + 1])),
-                                                         sc2, nm2);
+                            const float2 xx = __ffma2_rn(
+                                make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sc2, nm2);
                             const float2 e = make_float2(tc_ex2(xx.x), tc_ex2(xx.y));
-                            acc[k & 3] = __fadd2_rn(acc[k & 3], e);
-                            split<F16>(e.x, e.y, hi[k], lo[k]);
+                            acc[k & 1] = __fadd2_rn(acc[k & 1], e);
+                            split<F16>(e.x, e.y, w[k], w[16 + k]);
                         }
-                        tc::tmem_st16(scol + 32 * (c0 + i), hi);
-                        tc::tmem_st16(scol + 32 * (c0 + i) + 16, lo);
+                        tc::tmem_st32(scol + 32 * c, w);
                     }
-                    l_sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) + (acc[2].x + acc[2].y) +
-                             (acc[3].x + acc[3].y);
-                    if constexpr (kCount < 4) {  // the other copies' keys
+                    l_sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                    if (chunks < 4) {  // the other copies' keys
                         uint32_t zero[32];
 #pragma unroll
                         for (int k = 0; k < 32; ++k) zero[k] = 0;
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < 4; ++c)
-                            if (c < c0 || c >= c0 + kCount) tc::tmem_st32(scol + 32 * c, zero);
+                            if (c < c0 || c >= c1) tc::tmem_st32(scol + 32 * c, zero);
                     }
-                };
-                if (!idle) {
-                    if (MT == 2 || r.copies == 1)
-                        weigh(std::integral_constant<int, 4>{}, 0);
-                    else if (r.copies == 2)
-                        weigh(std::integral_constant<int, 2>{}, 2 * copy);
-                    else
-                        weigh(std::integral_constant<int, 1>{}, copy);
                     if (__any_sync(0xffffffffu, rescale)) {
                         // O holds the products up to the tile before once that one's are done
                         if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.odone[x], (t - 1) & 1, p.err))) {
@@ -628,26 +640,24 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                 }
                 if (tail && x == 0) {
-                    // the rows of V that lie in the tree or behind it, one per thread (in an order of
-                    // 16-byte parts that lets eight rows' lie in different banks)
+                    // the rows of V that lie in the tree or behind it, one per thread
                     const unsigned pos = 2 * run_t + 1;
                     if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1, p.err))) {
                         ok = false;
                         break;
                     }
-                    char *vrow = ring + (int)(pos % L::kSlots) * L::kTileBytes + lane_row * 128;
+                    char *vt = ring + (int)(pos % L::kSlots) * L::kTileBytes;
                     const int key = key0 + lane_row;
                     if (key >= pc.seq.len) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D / 8; ++c)
-                            *reinterpret_cast<uint4 *>(vrow + (c >> 3) * L::kHalfBytes + (((c ^ lane) & 7) << 4)) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4 *>(vt + tile_offset<D>(lane_row, c)) = make_uint4(0u, 0u, 0u, 0u);
                     } else if (key >= r.before) {
                         constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
                         bool some = false;
-#pragma unroll 4
+#pragma unroll 2
                         for (int c = 0; c < D / 8; ++c) {
-                            uint4 *at4 = reinterpret_cast<uint4 *>(vrow + (c >> 3) * L::kHalfBytes + (((c ^ lane) & 7) << 4));
+                            uint4 *at4 = reinterpret_cast<uint4 *>(vt + tile_offset<D>(lane_row, c));
                             uint4 v = *at4;
                             uint32_t w[4] = {v.x, v.y, v.z, v.w};
                             bool here = false;
@@ -689,97 +699,113 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             if (MT == 1 && r.copies > 1) {
                 // the copies of a row share a reference from here on
                 float M = -INFINITY;
-                for (int c = 0; c < r.copies; ++c) M = fmaxf(M, sm.ml[lane_row % per_copy + c * per_copy].x);
+                for (int c = 0; c < r.copies; ++c) M = fmaxf(M, sm.ml[row + c * per_copy].x);
                 const float ref = M == -INFINITY ? 0.f : M;
                 float l = 0.f;
                 for (int c = 0; c < r.copies; ++c) {
-                    const float2 ml = sm.ml[lane_row % per_copy + c * per_copy];
+                    const float2 ml = sm.ml[row + c * per_copy];
                     l += tc_ex2(ml.x - ref) * ml.y;
                 }
                 factor = tc_ex2(m_used - ref);
                 m_used = M;
                 l_sum = l;
             }
-            const bool stores = valid && copy == 0;
             const size_t orow = valid ? (size_t)(pc.seq.q0 + node) * p.hq + pc.h * p.g + row % p.g : 0;
             const bool seen = l_sum != 0.f;  // a row with a NaN score stays NaN
-            const float inv = pc.slot >= 0 ? 1.f : seen ? 1.f / l_sum : 0.f;
+            if (pc.slot < 0) factor *= seen ? 1.f / l_sum : 0.f;
             float *part = p.partial + (size_t)max(pc.slot, 0) * (128 * MT) * (D + 2);
-            // 32 columns at a time, so that what copies exchange fits their Q buffer (free by now)
-            float4 *box = reinterpret_cast<float4 *>(sQ + (MT == 1 ? (n & 1) * L::kTileBytes : 0));
+            auto store4 = [&](int q4, float4 o) {  // dimensions 4 q4 .. 4 q4 + 3 of the row
+                if (pc.slot >= 0)
+                    reinterpret_cast<float4 *>(part)[q4 * (128 * MT) + row] = o;
+                else
+                    store_out4(p.out, orow * D + 4 * q4, o, p.out_type);
+            };
+            if (MT == 2 || r.copies == 1) {
 #pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) {
-                uint32_t v[32];
-                tc::tmem_ld32(ocol + 32 * i, v);
-                tc::tmem_wait_ld();
-                float o[32];
+                for (int i = 0; i < D / 16; ++i) {
+                    uint32_t v[16];
+                    tc::tmem_ld16(ocol + 16 * i, v);
+                    tc::tmem_wait_ld();
+                    if (valid) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(v[k]);
-                if (MT == 1 && r.copies > 1) {
-                    // (box: [8][rows of the copies behind the first] float4)
-                    if (i > 0) named_bar_sync(2, L::kSoftmax);  // the columns before were read
-                    if (copy > 0) {
+                        for (int k = 0; k < 4; ++k)
+                            store4(4 * i + k, make_float4(__uint_as_float(v[4 * k]) * factor, __uint_as_float(v[4 * k + 1]) * factor,
+                                                          __uint_as_float(v[4 * k + 2]) * factor,
+                                                          __uint_as_float(v[4 * k + 3]) * factor));
+                    }
+                }
+            } else {
+                // Half of the columns at a time, in strips of 16: copy c sums and stores every
+                // strip c, c + copies, ..; the others' go through the Q buffer, free by now:
+                // box[strip][4][row of the tile] float4.
+                float4 *box = reinterpret_cast<float4 *>(sQ + (n & 1) * L::kTileBytes);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (half) named_bar_sync(2, L::kSoftmax);  // the first half was read
+#pragma unroll 1
+                    for (int i = 0; i < D / 32; ++i) {
+                        if (i % r.copies == copy) continue;
+                        uint32_t v[16];
+                        tc::tmem_ld16(ocol + half * (D / 2) + 16 * i, v);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            box[k * 128 + lane_row] = make_float4(o[4 * k] * factor, o[4 * k + 1] * factor,
-                                                                  o[4 * k + 2] * factor, o[4 * k + 3] * factor);
+                        for (int k = 0; k < 4; ++k)
+                            box[(4 * i + k) * 128 + lane_row] =
+                                make_float4(__uint_as_float(v[4 * k]) * factor, __uint_as_float(v[4 * k + 1]) * factor,
+                                            __uint_as_float(v[4 * k + 2]) * factor, __uint_as_float(v[4 * k + 3]) * factor);
                     }
                     named_bar_sync(2, L::kSoftmax);
-                    if (copy == 0) {
+#pragma unroll 1
+                    for (int i = copy; i < D / 32; i += r.copies) {
+                        uint32_t v[16];
+                        tc::tmem_ld16(ocol + half * (D / 2) + 16 * i, v);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= factor;
-                        for (int c = 1; c < r.copies; ++c) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float4 y = box[k * 128 + lane_row + c * per_copy];
-                                o[4 * k] += y.x, o[4 * k + 1] += y.y, o[4 * k + 2] += y.z, o[4 * k + 3] += y.w;
+                        for (int k = 0; k < 4; ++k) {
+                            float4 o = make_float4(__uint_as_float(v[4 * k]) * factor, __uint_as_float(v[4 * k + 1]) * factor,
+                                                   __uint_as_float(v[4 * k + 2]) * factor, __uint_as_float(v[4 * k + 3]) * factor);
+#pragma unroll 1
+                            for (int c = 1; c < r.copies; ++c) {
+                                const float4 y = box[(4 * i + k) * 128 + ((lane_row + c * per_copy) & 127)];
+                                o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
                             }
+                            if (valid) store4(half * (D / 8) + 4 * i + k, o);
                         }
                     }
-                }
-                if (nonfinite && stores) {
-                    // what was kept out of the products, for the rows that attend it
-                    const int32_t *table = p.tables + (size_t)pc.b * p.plan.max_blocks;
-                    for (int k = 0; k < pc.seq.nodes; ++k) {
-                        const int key = r.before + k;
-                        if (!(anc.word(k >> 5) >> (k & 31) & 1) || key < pc.t0 * kTile || key >= pc.t1 * kTile) continue;
-                        const int id = __ldg(table + key / 16);
-                        if (id < 0 || id >= p.num_blocks) continue;
-                        const uint16_t *from = static_cast<const uint16_t *>(p.v) +
-                                               (((size_t)id * p.plan.hkv + pc.h) * 16 + key % 16) * D + 32 * i;
-#pragma unroll
-                        for (int d = 0; d < 32; ++d) {
-                            const float y = F16 ? f16x2_to_float2(from[d]).x : bf16_to_float(from[d]);
-                            if (!(fabsf(y) < INFINITY)) o[d] += y;
-                        }
-                    }
-                }
-                if (!stores) continue;
-                if (pc.slot >= 0) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        reinterpret_cast<float4 *>(part)[(8 * i + k) * (128 * MT) + row] =
-                            make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                } else if (p.out_type == KV_F32) {
-                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + orow * D + 32 * i);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + orow * D + 32 * i);
-                    auto pack = [&](int k) {
-                        return F16 ? tc::pack_f16x2(o[k] * inv, o[k + 1] * inv) : tc::pack_bf16x2(o[k] * inv, o[k + 1] * inv);
-                    };
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        dst[k] = make_uint4(pack(8 * k), pack(8 * k + 2), pack(8 * k + 4), pack(8 * k + 6));
                 }
             }
-            if (stores) {
+            if (valid && copy == 0) {
                 if (pc.slot >= 0)
                     reinterpret_cast<float2 *>(part + (size_t)128 * MT * D)[row] = make_float2(m_used, l_sum);
                 else if (p.lse)
                     p.lse[orow] = seen ? (m_used + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+            }
+            // (uniform over the CTA: every warp reads the same word)
+            if (MT == 1 && nonfinite) named_bar_sync(2, L::kSoftmax);  // the other copies' stores
+            if (nonfinite && valid && copy == 0) {
+                // what was kept out of the products, for the rows that attend it
+                const int32_t *table = p.tables + (size_t)pc.b * p.plan.max_blocks;
+                for (int k = 0; k < pc.seq.nodes; ++k) {
+                    const int key = r.before + k;
+                    if (!(anc.word(k >> 5) >> (k & 31) & 1) || key < pc.t0 * kTile || key >= pc.t1 * kTile) continue;
+                    const int id = __ldg(table + key / 16);
+                    if (id < 0 || id >= p.num_blocks) continue;
+                    const uint16_t *from = static_cast<const uint16_t *>(p.v) +
+                                           (((size_t)id * p.plan.hkv + pc.h) * 16 + key % 16) * D;
+#pragma unroll 1
+                    for (int d = 0; d < D; ++d) {
+                        const float y = F16 ? f16x2_to_float2(from[d]).x : bf16_to_float(from[d]);
+                        if (fabsf(y) < INFINITY) continue;
+                        if (pc.slot >= 0) {
+                            part[((size_t)(d >> 2) * (128 * MT) + row) * 4 + (d & 3)] += y;
+                        } else if (p.out_type == KV_F32) {
+                            static_cast<float *>(p.out)[orow * D + d] += y;
+                        } else {
+                            uint16_t *o = static_cast<uint16_t *>(p.out) + orow * D + d;
+                            *o = F16 ? float_to_f16_rn(f16x2_to_float2(*o).x + y) : float_to_bf16_rn(bf16_to_float(*o) + y);
+                        }
+                    }
+                }
             }
             tc::fence_before_sync();
             __syncwarp();
