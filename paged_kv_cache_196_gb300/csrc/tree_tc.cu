@@ -82,7 +82,9 @@ struct Shared {
     int abort;
     uint32_t gone[8];              // by tile in turn: bit i: block i is not there
     int nonfinite[2];              // by piece in turn: number of a piece whose tree holds some in V
-    float2 ml[128];                // DUP: reference and sum of each row copy
+    float2 ml[128];                // MT = 1: reference and sum of each row copy
+    Piece piece[2];                // by Q buffer: the piece whose queries it holds; t1 = 0: no more
+    uint2 parents[2][32];          // of the piece's tree, 8 nodes a lane (Ancestors)
     PlaceScratch<Layout<D, MT>::kThreads> scratch;
 };
 
@@ -105,6 +107,18 @@ KV_DEVICE void tma_load_4d(void *dst, const CUtensorMap *map, int group, uint64_
         " [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(smem_addr(dst)),
         "l"(map), "r"(0), "r"(group), "r"(smem_addr(bar))
         : "memory");
+}
+
+// 32 bytes in one store where they are a sector.
+KV_DEVICE void store_sector(void *dst, const uint32_t (&y)[8], bool aligned) {
+    if (aligned) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+                     "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
 }
 
 KV_DEVICE void cp_async16(uint32_t dst, const void *src) {
@@ -185,36 +199,38 @@ struct Rows {
 struct Ancestors {
     uint32_t w[kMaxNodes / 32];
 
-    // All lanes of a warp: each walks up from its node (a negative one: none).  Lane l holds the
-    // parents of nodes 8 l .. 8 l + 7 as bytes, 255 for none.
-    KV_DEVICE void walk(const int32_t *parents, int nodes, int node, int *err) {
+    // All lanes of a warp: lane l's parents, of nodes 8 l .. 8 l + 7, as bytes, 255 for none.
+    static KV_DEVICE uint2 pack(const int32_t *parents, int nodes, int *err) {
         const int lane = threadIdx.x & 31;
-        uint32_t lo = 0xffffffffu, hi = 0xffffffffu;
+        uint32_t x[2] = {0xffffffffu, 0xffffffffu};
         bool bad = false;
+        int up[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int i = 8 * lane + k;
-            int up = -1;
-            if (i < nodes) {
-                up = parents ? __ldg(parents + i) : i - 1;
-                if (up < -1 || up >= i) {
-                    bad = true;
-                    up = -1;
-                }
+            up[k] = i >= nodes ? -1 : parents ? __ldg(parents + i) : i - 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = 8 * lane + k;
+            if (i < nodes && (up[k] < -1 || up[k] >= i)) {
+                bad = true;
+                up[k] = -1;
             }
-            const uint32_t byte = (uint32_t)up & 255u;
-            if (k < 4)
-                lo = (lo & ~(255u << (8 * k))) | (byte << (8 * k));
-            else
-                hi = (hi & ~(255u << (8 * k - 32))) | (byte << (8 * k - 32));
+            x[k >> 2] = (x[k >> 2] & ~(255u << (8 * (k & 3)))) | (((uint32_t)up[k] & 255u) << (8 * (k & 3)));
         }
         if (bad) atomicOr(err, KV_DEVERR_TREE);
+        return make_uint2(x[0], x[1]);
+    }
+    // All lanes of a warp: each walks up from its node (a negative one: none), with the lanes' parents.
+    KV_DEVICE void walk(uint2 parents, int node) {
 #pragma unroll
         for (int k = 0; k < kMaxNodes / 32; ++k) w[k] = 0;
         int i = node;
         while (__any_sync(0xffffffffu, i >= 0)) {
             const int at = i >= 0 ? i : 0;
-            const uint32_t a = __shfl_sync(0xffffffffu, lo, at >> 3), b = __shfl_sync(0xffffffffu, hi, at >> 3);
+            const uint32_t a = __shfl_sync(0xffffffffu, parents.x, at >> 3);
+            const uint32_t b = __shfl_sync(0xffffffffu, parents.y, at >> 3);
             if (i >= 0) {
 #pragma unroll
                 for (int k = 0; k < kMaxNodes / 32; ++k) w[k] |= (i >> 5) == k ? 1u << (i & 31) : 0u;
@@ -261,7 +277,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.qfull[s], 1);
-            mbar_init(&sm.qempty[s], MT == 1 ? 4 : 1);
+            mbar_init(&sm.qempty[s], MT == 1 ? 4 : 9);  // MT = 2: the last S, and each softmax warp
             mbar_init(&sm.sfull[s], 1);
             mbar_init(&sm.pfull[s], 4);
             mbar_init(&sm.odone[s], 1);
@@ -278,9 +294,6 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem;
     volatile int *abort_flag = &sm.abort;
-    Pieces pieces;
-    pieces.start(p.plan, at, blockIdx.x);
-    Piece pc;
 
     if (warp == L::kCopyWarp) {
         // ================================================== K and V tiles
@@ -291,6 +304,9 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         int slot = 0, phase = 0, turn = 0;
         unsigned issued = 0;
         bool stop = false;
+        Pieces pieces;
+        pieces.start(p.plan, at, blockIdx.x);
+        Piece pc;
         while (!stop && pieces.next(p.plan, pc)) {
             const int32_t *table = p.tables + (size_t)pc.b * p.plan.max_blocks;
             const int blocks = (pc.seq.len + 15) / 16;
@@ -339,37 +355,50 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             }
         }
     } else if (warp == L::kQWarp) {
-        // ================================================== query rows
-        // Stored K-major with 128-byte swizzle, as the products read them; rows past the
-        // group's last hold anything (no row reaches another one).
-        int n = 0;
-        bool ok = true;
-        while (ok && pieces.next(p.plan, pc)) {
-            const Rows r(p, pc, MT);
+        // ================================================== pieces and their query rows
+        // What a piece is, its tree and its queries, for the other warps: theirs would be
+        // round trips to memory at every piece's beginning.  Queries are stored K-major with
+        // 128-byte swizzle, as the products read them; rows past the group's last hold
+        // anything (no row reaches another one).
+        Pieces pieces;
+        pieces.start(p.plan, at, blockIdx.x);
+        Piece pc;
+        bool ok = true, more = true;
+        for (int n = 0; more; ++n) {
+            more = pieces.next(p.plan, pc);
             const int buf = n % L::kQBufs;
             if (lane == 0)
                 ok = !*abort_flag &&
                      (n < L::kQBufs || mbar_wait<TW>(&sm.qempty[buf], (n / L::kQBufs - 1) & 1, p.err));
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
-            const uint32_t dst = smem_addr(sQ) + buf * L::kTileBytes;
-            const int per_copy = 128 / r.copies;
-            const uint16_t *src = static_cast<const uint16_t *>(p.q) +
-                                  ((size_t)(pc.seq.q0 + r.node0) * p.hq + pc.h * p.g) * D;
-            constexpr int kChunks = D / 8;  // 16-byte parts of a row
-            for (int i = lane; i < r.rows * kChunks; i += 32) {
-                const int row = i / kChunks, c = i % kChunks;
-                const uint16_t *from = src + ((size_t)(row / p.g) * p.hq + row % p.g) * D + 8 * c;
-                for (int copy = 0; copy < r.copies; ++copy) {
-                    const int at_row = row + copy * per_copy;
-                    cp_async16(dst + (at_row >> 7) * L::kTileBytes + tile_offset<D>(at_row & 127, c), from);
+            if (more) {
+                const Rows r(p, pc, MT);
+                const uint32_t dst = smem_addr(sQ) + buf * L::kTileBytes;
+                const int per_copy = 128 / r.copies;
+                constexpr int kChunks = D / 8, kStep = 32 / kChunks;  // 16-byte parts of a row; rows at a time
+                const int c = lane % kChunks;
+                const uint16_t *src = static_cast<const uint16_t *>(p.q) +
+                                      ((size_t)(pc.seq.q0 + r.node0) * p.hq + pc.h * p.g) * D + 8 * c;
+                int row = lane / kChunks, node = row / p.g, head = row - node * p.g;
+#pragma unroll 2
+                for (; row < r.rows; row += kStep) {
+                    const uint16_t *from = src + ((size_t)node * p.hq + head) * D;
+                    for (int at_row = row; at_row < (MT == 1 ? 128 : 256); at_row += per_copy) {
+                        cp_async16(dst + (at_row >> 7) * L::kTileBytes + tile_offset<D>(at_row & 127, c), from);
+                        if (r.copies == 1) break;
+                    }
+                    for (head += kStep; head >= p.g; head -= p.g) ++node;
                 }
+                sm.parents[buf][lane] = Ancestors::pack(p.parents ? p.parents + pc.seq.q0 : nullptr, pc.seq.nodes, p.err);
+            } else {
+                pc.t0 = pc.t1 = 0;
             }
+            if (lane == 0) sm.piece[buf] = pc;
             asm volatile("cp.async.wait_all;" ::: "memory");
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.qfull[buf]);
-            ++n;
         }
         if (!ok && lane == 0) *abort_flag = 1;
     } else if (warp == L::kMmaWarp) {
@@ -408,12 +437,14 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 unsigned s = 0;       // next S
                 int sn = -1, s_left = 0;
                 bool more = true;
+                int len[2] = {0, 0};  // tiles of the pieces whose S has begun and whose PV has not ended
                 auto next_s = [&]() {  // issues S(s) if there is one
                     if (s_left == 0) {
-                        if (!more || !(more = pieces.next(p.plan, pc))) return true;
-                        s_left = pc.t1 - pc.t0;
+                        if (!more) return true;
                         ++sn;
                         if (!mbar_wait<TW>(&sm.qfull[sn & 1], (sn >> 1) & 1, p.err)) return false;
+                        s_left = len[sn & 1] = sm.piece[sn & 1].t1 - sm.piece[sn & 1].t0;
+                        if (!(more = s_left > 0)) return true;
                     }
                     if (!wait_full(2 * s)) return false;
                     tc::fence_after_sync();
@@ -424,16 +455,11 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     ++s;
                     return true;
                 };
-                // lengths of the pieces whose S is issued and whose PV is not: two at most
-                int len[2] = {0, 0};
                 ok = next_s();
-                if (sn >= 0) len[0] = pc.t1 - pc.t0;
                 t_left = len[0];
                 bool first = true;
                 while (ok && t < s) {
-                    const int sn_was = sn;
                     if (!(ok = next_s())) break;
-                    if (sn != sn_was) len[sn & 1] = pc.t1 - pc.t0;
                     if (first && n >= 2 && !mbar_wait<TW>(&sm.oempty[n & 1], ((n >> 1) - 1) & 1, p.err)) ok = false;
                     if (!ok || !mbar_wait<TW>(&sm.pfull[t & 1], (t >> 1) & 1, p.err) || !wait_full(2 * t + 1)) {
                         ok = false;
@@ -454,13 +480,16 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 unsigned t = 0;
                 int n = 0, used[2] = {0, 0};  // pieces, and tiles of each row tile, so far
                 int pieces_of[2] = {0, 0};
-                while (ok && pieces.next(p.plan, pc)) {
-                    const Rows r(p, pc, MT);
-                    const int row_tiles = r.rows > 128 ? 2 : 1;
-                    ok = mbar_wait<TW>(&sm.qfull[0], n & 1, p.err) && wait_full(2 * t);
+                while (ok) {
+                    ok = mbar_wait<TW>(&sm.qfull[0], n & 1, p.err);
+                    if (!ok) break;
+                    const Piece pc = sm.piece[0];
+                    const int row_tiles = Rows(p, pc, MT).rows > 128 ? 2 : 1;
+                    const int tiles = pc.t1 - pc.t0;
+                    if (tiles == 0) break;
+                    ok = wait_full(2 * t);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const int tiles = pc.t1 - pc.t0;
                     for (int x = 0; x < row_tiles; ++x) {
                         issue_s(128 * x, x, (int)(2 * t % L::kSlots));
                         tc::mma_commit(&sm.sfull[x]);
@@ -512,10 +541,22 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         unsigned run_t = 0;  // tiles of the run so far
         int n = 0;         // pieces
         bool ok = true;
-        while (ok && pieces.next(p.plan, pc)) {
+        while (true) {
+            ok = mbar_wait<TW>(&sm.qfull[n % L::kQBufs], (n / L::kQBufs) & 1, p.err);
+            ok = !__any_sync(0xffffffffu, !ok);
+            Piece pc{};
+            uint2 parents = make_uint2(0, 0);
+            if (ok) {
+                pc = sm.piece[n % L::kQBufs];
+                parents = sm.parents[n % L::kQBufs][lane];
+                if constexpr (MT == 2) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.qempty[0]);
+                }
+            }
             const Rows r(p, pc, MT);
             const int tiles = pc.t1 - pc.t0;
-            if (MT == 2 && x == 1 && r.rows <= 128) {
+            if (MT == 2 && tiles > 0 && x == 1 && r.rows <= 128) {
                 run_t += tiles;
                 ++n;
                 continue;
@@ -523,13 +564,12 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             const int per_copy = 128 / r.copies;
             const int copy = r.copies == 1 ? 0 : lane_row / per_copy;
             const int row = 128 * x + (r.copies == 1 ? lane_row : lane_row % per_copy);
-            const bool valid = row < r.rows;
+            const bool valid = tiles > 0 && row < r.rows;
             const int node = valid ? r.node0 + row / p.g : -1;
             const bool idle = __all_sync(0xffffffffu, !valid);  // rows of no query
             const int chunks = 4 / r.copies, c0 = copy * chunks;  // of 32 keys of a tile, this copy's
             Ancestors anc;
-            if (!idle && pc.t1 * kTile > r.before)
-                anc.walk(p.parents ? p.parents + pc.seq.q0 : nullptr, pc.seq.nodes, node, p.err);
+            if (!idle && pc.t1 * kTile > r.before) anc.walk(parents, node);
             float m_used = -INFINITY, l_sum = 0.f;
             for (int j = 0; j < tiles; ++j, ++t, ++run_t) {
                 const int buf = MT == 1 ? (int)(t & 1) : x;
@@ -640,36 +680,31 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                 }
                 if (tail && x == 0) {
-                    // the rows of V that lie in the tree or behind it, one per thread
+                    // the rows of V that lie in the tree or behind it
                     const unsigned pos = 2 * run_t + 1;
                     if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1, p.err))) {
                         ok = false;
                         break;
                     }
                     char *vt = ring + (int)(pos % L::kSlots) * L::kTileBytes;
-                    const int key = key0 + lane_row;
-                    if (key >= pc.seq.len) {
-#pragma unroll 1
-                        for (int c = 0; c < D / 8; ++c)
-                            *reinterpret_cast<uint4 *>(vt + tile_offset<D>(lane_row, c)) = make_uint4(0u, 0u, 0u, 0u);
-                    } else if (key >= r.before) {
-                        constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
-                        bool some = false;
+                    const int row0 = max(0, r.before - key0);
+                    constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
 #pragma unroll 2
-                        for (int c = 0; c < D / 8; ++c) {
-                            uint4 *at4 = reinterpret_cast<uint4 *>(vt + tile_offset<D>(lane_row, c));
-                            uint4 v = *at4;
-                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                            bool here = false;
+                    for (int i = row0 * (D / 8) + lane_row; i < 128 * (D / 8); i += 128) {
+                        const int at_row = i / (D / 8);
+                        uint4 *at4 = reinterpret_cast<uint4 *>(vt + tile_offset<D>(at_row, i % (D / 8)));
+                        const uint4 v = *at4;
+                        uint32_t y[4] = {v.x, v.y, v.z, v.w};
+                        bool here = false;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if ((w[k] & top) == top) w[k] &= 0xffff0000u, here = true;
-                                if ((w[k] >> 16 & top) == top) w[k] &= 0x0000ffffu, here = true;
-                            }
-                            if (here) *at4 = make_uint4(w[0], w[1], w[2], w[3]);
-                            some |= here;
+                        for (int k = 0; k < 4; ++k) {
+                            if ((y[k] & top) == top) y[k] &= 0xffff0000u, here = true;
+                            if ((y[k] >> 16 & top) == top) y[k] &= 0x0000ffffu, here = true;
                         }
-                        if (some) sm.nonfinite[n & 1] = n;
+                        if (key0 + at_row >= pc.seq.len)
+                            *at4 = make_uint4(0u, 0u, 0u, 0u);
+                        else if (here)
+                            *at4 = make_uint4(y[0], y[1], y[2], y[3]), sm.nonfinite[n & 1] = n;
                     }
                     tc::fence_proxy_async_smem();  // before the tensor core reads them
                 }
@@ -679,19 +714,19 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&sm.pfull[buf]);
             }
             // ---- the piece's end
-            if (ok) {
+            if (ok && tiles > 0) {
                 // (MT = 1: the last S says that the products up to three tiles back are done, so
                 // the wait for the last one's phase comes after that for the one before it)
                 bool bad = MT == 1 && t >= 2 && !mbar_wait<TW>(&sm.odone[x], t & 1, p.err);
                 bad = bad || !mbar_wait<TW>(&sm.odone[x], (t - 1) & 1, p.err);
                 ok = !__any_sync(0xffffffffu, bad);
             }
-            // all warps of the CTA stay or leave together (only then may they meet again)
+            // all warps stay or leave together: they meet once for every piece and for the end
             if constexpr (MT == 1) {
                 sm.ml[lane_row] = make_float2(m_used, l_sum);
                 ok = !named_bar_or(1, L::kSoftmax, !ok);
             }
-            if (!ok) break;
+            if (!ok || tiles == 0) break;
             tc::fence_after_sync();
             const uint32_t ocol = tmem + lane_base + kColO0 + 128 * (MT == 1 ? n & 1 : x);
             const bool nonfinite = *reinterpret_cast<volatile int *>(&sm.nonfinite[n & 1]) == n;
@@ -714,11 +749,29 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             const bool seen = l_sum != 0.f;  // a row with a NaN score stays NaN
             if (pc.slot < 0) factor *= seen ? 1.f / l_sum : 0.f;
             float *part = p.partial + (size_t)max(pc.slot, 0) * (128 * MT) * (D + 2);
-            auto store4 = [&](int q4, float4 o) {  // dimensions 4 q4 .. 4 q4 + 3 of the row
-                if (pc.slot >= 0)
-                    reinterpret_cast<float4 *>(part)[q4 * (128 * MT) + row] = o;
-                else
-                    store_out4(p.out, orow * D + 4 * q4, o, p.out_type);
+            const bool aligned32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+            auto store = [&](int strip, const float (&o)[16]) {  // dimensions 16 strip .. 16 strip + 15 of the row
+                if (pc.slot >= 0) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        reinterpret_cast<float4 *>(part)[(4 * strip + k) * (128 * MT) + row] =
+                            make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                } else if (p.out_type == KV_F32) {
+                    float *dst = static_cast<float *>(p.out) + orow * D + 16 * strip;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(o[8 * k + i]);
+                        store_sector(dst + 8 * k, y, aligned32);
+                    }
+                } else {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        y[i] = F16 ? tc::pack_f16x2(o[2 * i], o[2 * i + 1]) : tc::pack_bf16x2(o[2 * i], o[2 * i + 1]);
+                    store_sector(static_cast<uint16_t *>(p.out) + orow * D + 16 * strip, y, aligned32);
+                }
             };
             if (MT == 2 || r.copies == 1) {
 #pragma unroll 1
@@ -726,13 +779,10 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     uint32_t v[16];
                     tc::tmem_ld16(ocol + 16 * i, v);
                     tc::tmem_wait_ld();
-                    if (valid) {
+                    float o[16];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            store4(4 * i + k, make_float4(__uint_as_float(v[4 * k]) * factor, __uint_as_float(v[4 * k + 1]) * factor,
-                                                          __uint_as_float(v[4 * k + 2]) * factor,
-                                                          __uint_as_float(v[4 * k + 3]) * factor));
-                    }
+                    for (int k = 0; k < 16; ++k) o[k] = __uint_as_float(v[k]) * factor;
+                    if (valid) store(i, o);
                 }
             } else {
                 // Half of the columns at a time, in strips of 16: copy c sums and stores every
@@ -760,17 +810,18 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         uint32_t v[16];
                         tc::tmem_ld16(ocol + half * (D / 2) + 16 * i, v);
                         tc::tmem_wait_ld();
+                        float o[16];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float4 o = make_float4(__uint_as_float(v[4 * k]) * factor, __uint_as_float(v[4 * k + 1]) * factor,
-                                                   __uint_as_float(v[4 * k + 2]) * factor, __uint_as_float(v[4 * k + 3]) * factor);
+                        for (int k = 0; k < 16; ++k) o[k] = __uint_as_float(v[k]) * factor;
 #pragma unroll 1
-                            for (int c = 1; c < r.copies; ++c) {
+                        for (int c = 1; c < r.copies; ++c) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
                                 const float4 y = box[(4 * i + k) * 128 + ((lane_row + c * per_copy) & 127)];
-                                o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+                                o[4 * k] += y.x, o[4 * k + 1] += y.y, o[4 * k + 2] += y.z, o[4 * k + 3] += y.w;
                             }
-                            if (valid) store4(half * (D / 8) + 4 * i + k, o);
                         }
+                        if (valid) store(half * (D / 32) + i, o);
                     }
                 }
             }
