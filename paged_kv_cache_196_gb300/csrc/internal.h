@@ -112,8 +112,8 @@ bool encode_rows_map(CUtensorMap *m, void *base, long long rows);
 // 16-bit rows of `dim` (64 or 128) values in groups of 8: {64 values, 8 rows, dim / 64, groups},
 // boxes of two whole groups (a block), 128B swizzle
 bool encode_groups_map(CUtensorMap *m, void *base, long long rows, int dim);
-// queries [rows][hq][128]: boxes of box_rows rows x box_heads heads x 64 values
-bool encode_q_map(CUtensorMap *m, const void *q, int rows, int hq, int box_heads, int box_rows);
+// queries [rows][hq][dim]: boxes of box_rows rows x box_heads heads x 64 values
+bool encode_q_map(CUtensorMap *m, const void *q, int rows, int hq, int box_heads, int box_rows, int dim = 128);
 kv_status pool_tensor_maps(kv_pool *p);  // of a pool with head_dim 128
 kv_status pool_group_maps(kv_pool *p);
 

@@ -57,11 +57,11 @@ bool encode_groups_map(CUtensorMap *m, void *base, long long rows, int dim) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_q_map(CUtensorMap *m, const void *q, int rows, int hq, int box_heads, int box_rows) {
+bool encode_q_map(CUtensorMap *m, const void *q, int rows, int hq, int box_heads, int box_rows, int dim) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
-    cuuint64_t dims[3] = {128, (cuuint64_t)hq, (cuuint64_t)rows};
-    cuuint64_t strides[2] = {128 * 2, (cuuint64_t)hq * 128 * 2};
+    cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)hq, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)hq * dim * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
     cuuint32_t estr[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,

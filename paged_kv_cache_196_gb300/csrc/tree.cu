@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
     const int r = blockIdx.x + 1;
     const Place at = place(p.plan, r, scratch, nullptr);
     if (at.b >= p.plan.batch) return;
-    const Seq seq = load_seq(p.plan, at.b, nullptr);
+    const Seq seq = at.seq;
     const int cost = seq.tiles + kTreePairCost;
     const int r0 = (int)((at.first + kTreePairCost) / at.per);  // the run that has the pair's first tile
     const int r1 = (int)((at.first + cost - 1) / at.per);       // and the last
@@ -217,6 +217,8 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
     for (int w = threadIdx.x >> 5; w < (row1 - row0 + 7) / 8 * kWide; w += kMergeThreads / 32) {
         const int row = row0 + w / kWide * 8 + (lane & 7), dq = w % kWide * 4 + (lane >> 3);
         if (row >= row1) continue;
+        const int node = row / p.g, x = node / p.plan.tile_nodes;
+        const int at_row = x * 128 + row - x * p.plan.tile_nodes * p.g;  // of the slot
         float M = -INFINITY, den = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s0 = r0; s0 <= r1; s0 += kMergeAhead) {
@@ -229,8 +231,8 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
                 v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (s <= r1) {
                     const float *part = p.partial + (s == r0 ? slot0 : 2 * s) * step;
-                    ml[i] = reinterpret_cast<const float2 *>(part + (size_t)slot_rows * D)[row];
-                    v[i] = reinterpret_cast<const float4 *>(part)[(size_t)dq * slot_rows + row];
+                    ml[i] = reinterpret_cast<const float2 *>(part + (size_t)slot_rows * D)[at_row];
+                    v[i] = reinterpret_cast<const float4 *>(part)[(size_t)dq * slot_rows + at_row];
                 }
             }
             float up = M;
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
         }
         const bool seen = den != 0.f;
         const float inv = seen ? 1.f / den : 0.f;
-        const size_t orow = (size_t)(seq.q0 + node0 + row / p.g) * p.hq + h * p.g + row % p.g;
+        const size_t orow = (size_t)(seq.q0 + node0 + node) * p.hq + h * p.g + row - node * p.g;
         store_out4(p.out, orow * D + 4 * dq, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), p.out_type);
         if (p.lse && dq == 0) p.lse[orow] = seen ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
     }
@@ -287,12 +289,23 @@ kv_status launch_merge(const TreeParams &pp, int d, int slot_rows, cudaStream_t 
 
 // How a call runs: what the workspace query and the call have to agree on.
 struct Shape {
-    int rows;  // query rows of a group, and of a slot
+    int slot_rows;                // rows of a slot of partial results
+    int tile_nodes, group_nodes;  // nodes of a row tile and of a group
+    int copies;                   // of each row in its tile
     int runs, min_run;
 };
 Shape shape_of(const kv_pool *p, int g, int max_q_len) {
-    if (p->dtype == KV_F32) return {kSimpleRows, kSimplePerSm * sm_count(), 2 + kTreePairCost};
-    return {max_q_len * g > 128 ? 256 : 128, sm_count(), 2 + kTreePairCost};
+    if (p->dtype == KV_F32)
+        return {kSimpleRows, kSimpleRows / g, kSimpleRows / g, 1, kSimplePerSm * sm_count(), 2 + kTreePairCost};
+    Shape s{128, 128 / g, 128 / g, 1, sm_count(), 2 + kTreePairCost};
+    if (max_q_len <= 64 / g) {
+        s.copies = max_q_len <= 32 / g ? 4 : 2;
+        s.tile_nodes = s.group_nodes = 128 / s.copies / g;
+    } else if (max_q_len > s.tile_nodes) {
+        s.slot_rows = 256;
+        s.group_nodes = 2 * s.tile_nodes;
+    }
+    return s;
 }
 
 // Arguments that the query and the call refuse alike.
@@ -322,7 +335,7 @@ kv_status kv_tree_workspace_size(kv_pool_t p, int batch, int num_q_heads, int ma
     *bytes = 0;
     if (batch == 0 || max_q_len == 0) return KV_OK;
     const tree::Shape s = tree::shape_of(p, num_q_heads / p->num_kv_heads, max_q_len);
-    *bytes = 2 * (size_t)s.runs * tree::slot_bytes(s.rows, p->head_dim);
+    *bytes = 2 * (size_t)s.runs * tree::slot_bytes(s.slot_rows, p->head_dim);
     return KV_OK;
 }
 
@@ -341,9 +354,12 @@ kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, 
         return KV_ERR_ARG;
     const int g = num_q_heads / p->num_kv_heads;
     const tree::Shape s = tree::shape_of(p, g, max_q_len);
-    if (workspace_bytes < 2 * (size_t)s.runs * tree::slot_bytes(s.rows, p->head_dim)) return KV_ERR_ARG;
+    if (workspace_bytes < 2 * (size_t)s.runs * tree::slot_bytes(s.slot_rows, p->head_dim)) return KV_ERR_ARG;
     tree::TreeParams pp{};
-    pp.plan = {cu_q, seq_lens, batch, total_q, max_q_len, max_blocks, p->num_kv_heads, s.rows / g, s.runs, s.min_run, 0};
+    pp.plan = {cu_q, seq_lens, batch, total_q, max_q_len, max_blocks, p->num_kv_heads, s.group_nodes,
+               s.tile_nodes, s.runs, s.min_run, 0};
+    pp.copies = s.copies;
+    pp.total_q = total_q;
     pp.q = q;
     pp.k = p->k;
     pp.v = p->v;
@@ -362,11 +378,11 @@ kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, 
         if (kv_status st = tree::launch_simple(pp, p->head_dim, as_stream(stream))) return st;
     } else {
         if (kv_status st = pool_group_maps(p)) return st;
-        if (kv_status st = tree::launch_tc(pp, p->head_dim, s.rows, p->dtype == KV_F16, p->gmap_k, p->gmap_v,
+        if (kv_status st = tree::launch_tc(pp, p->head_dim, s.slot_rows, p->dtype == KV_F16, p->gmap_k, p->gmap_v,
                                            as_stream(stream)))
             return st;
     }
-    return tree::launch_merge(pp, p->head_dim, s.rows, as_stream(stream));
+    return tree::launch_merge(pp, p->head_dim, s.slot_rows, as_stream(stream));
 }
 
 }  // extern "C"

@@ -18,6 +18,8 @@ struct TreeParams {
     const int32_t *parents;  // [total_q]: index within the tree, -1: none; null: chains
     int num_blocks;
     int hq, g;
+    int copies;              // of each row in its tile (16-bit pools)
+    int total_q;             // rows of q
     float scale_log2;        // softmax scale * log2(e)
     void *out;
     int out_type;
@@ -26,8 +28,8 @@ struct TreeParams {
     int *err;
 };
 
-// tree_tc.cu: 16-bit pools; groups of `rows` (128 or 256) query rows, tensor maps of the pool's
-// K and V rows.
+// tree_tc.cu: 16-bit pools; one or two row tiles (`rows` = 128 or 256), tensor maps of the
+// pool's K and V in groups of rows.
 kv_status launch_tc(const TreeParams &pp, int d, int rows, bool f16, const CUtensorMap &tk, const CUtensorMap &tv,
                     cudaStream_t stream);
 

@@ -2,8 +2,8 @@
 // it finds on the device (a captured step stays balanced as its sequences grow).
 //
 // A sequence of L tokens and T nodes is kv heads x groups pairs: a group is as many
-// whole nodes as the kernel takes query rows (all heads of a kv head, row = node of
-// the group * g + head), so a pair is what one pass over the keys of a kv head serves.
+// whole nodes as the kernel takes query rows (all heads of a kv head, row = node *
+// g + head within a row tile), so a pair is what one pass over the keys of a kv head serves.
 // A pair counts kTreePairCost units (its queries and its end) and one per key tile of
 // 128.  The units of all pairs are laid end to end, sequence by sequence, and cut into
 // equal runs, one per CTA.  What a run holds of a pair is a piece: a range of its key
@@ -28,6 +28,7 @@ struct Plan {
     const int32_t *cu_q, *seq_lens;
     int batch, total_q, max_q_len, max_blocks;
     int hkv, group_nodes;  // kv heads; nodes of a group
+    int tile_nodes;        // of a row tile: row of the group = node / tile_nodes * 128 + node % tile_nodes * g + head
     int runs;              // CTAs
     int min_run;           // units of the shortest run
     int whole;             // a run takes the pairs that begin in it whole: none is cut
@@ -64,6 +65,7 @@ KV_DEVICE long long seq_units(const Plan &p, const Seq &s) {
 struct Place {
     long long per, total, first;
     int b, pair;
+    Seq seq;
 };
 
 template <int kThreads>
@@ -97,7 +99,7 @@ KV_DEVICE Place place(const Plan &p, int run, PlaceScratch<kThreads> &s, int *er
     upto += before;
     const long long per = max((long long)p.min_run, (total + p.runs - 1) / p.runs);
     const long long unit = run * per;
-    if (tid == 0 && unit >= total) s.at = Place{per, total, total, p.batch, 0};
+    if (tid == 0 && unit >= total) s.at = Place{per, total, total, p.batch, 0, {}};
     if (unit < upto && unit >= upto - mine) {
         long long base = upto - mine;
         for (int b = b0; b < b1; ++b) {
@@ -105,7 +107,7 @@ KV_DEVICE Place place(const Plan &p, int run, PlaceScratch<kThreads> &s, int *er
             const long long n = seq_units(p, q);
             if (unit < base + n) {
                 const int pair = (int)((unit - base) / q.pair_units());
-                s.at = Place{per, total, base + pair * q.pair_units(), b, pair};
+                s.at = Place{per, total, base + pair * q.pair_units(), b, pair, q};
                 break;
             }
             base += n;
@@ -135,9 +137,8 @@ struct Pieces {
         first = at.first;
         b = at.b;
         pair = at.pair;
-        if (unit >= end) return;
-        seq = load_seq(p, b, nullptr);
-        load_ahead(p);
+        seq = at.seq;
+        if (unit < end) load_ahead(p);
     }
     KV_DEVICE void load_ahead(const Plan &p) {
         ahead = Seq{0, 0, 0, 0, 0};

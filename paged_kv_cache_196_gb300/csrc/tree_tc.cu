@@ -55,12 +55,14 @@ struct Layout {
     static constexpr int kHalves = D / 64;
     static constexpr int kGroupBytes = 1024 * kHalves;
     static constexpr int kTileBytes = 16 * kGroupBytes;
-    static constexpr int kSlots = D == 128 ? 5 : 8;
+    static constexpr int kSlots = D == 64 ? 8 : MT == 1 ? 5 : 4;
     static constexpr int kQBufs = MT == 1 ? 2 : 1;  // of MT tiles
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kBars = kRing + kSlots * kTileBytes;
-    static constexpr int kSoftmax = 128 * MT;       // threads
-    static constexpr int kCopyWarp = 4 * MT, kMmaWarp = kCopyWarp + 1, kQWarp = kCopyWarp + 2;
+    static constexpr int kRowThreads = MT;          // threads of a row, each with its part of the keys
+    static constexpr int kRowWarps = 4 * kRowThreads;  // softmax warps of a row tile
+    static constexpr int kSoftmax = 32 * kRowWarps * MT;  // threads
+    static constexpr int kCopyWarp = kRowWarps * MT, kMmaWarp = kCopyWarp + 1, kQWarp = kCopyWarp + 2;
     static constexpr int kThreads = kSoftmax + 96;
 };
 
@@ -82,7 +84,8 @@ struct Shared {
     int abort;
     uint32_t gone[8];              // by tile in turn: bit i: block i is not there
     int nonfinite[2];              // by piece in turn: number of a piece whose tree holds some in V
-    float2 ml[128];                // MT = 1: reference and sum of each row copy
+    float2 ml[128 * MT * MT];      // MT = 1: reference and sum of each row copy; MT = 2: sums of a row's threads
+    float top[MT == 1 ? 1 : 2][MT][MT][MT == 1 ? 1 : 128];  // MT = 2: maxima, by tile in turn, of a row tile's rows' threads
     Piece piece[2];                // by Q buffer: the piece whose queries it holds; t1 = 0: no more
     uint2 parents[2][32];          // of the piece's tree, 8 nodes a lane (Ancestors)
     PlaceScratch<Layout<D, MT>::kThreads> scratch;
@@ -119,10 +122,6 @@ KV_DEVICE void store_sector(void *dst, const uint32_t (&y)[8], bool aligned) {
         reinterpret_cast<uint4 *>(dst)[0] = make_uint4(y[0], y[1], y[2], y[3]);
         reinterpret_cast<uint4 *>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
     }
-}
-
-KV_DEVICE void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // Two weights as a pair of the 16-bit type and the pair of what that leaves of them.
@@ -167,30 +166,30 @@ KV_DEVICE void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t b_lo, uint32_t 
 }
 
 // D (+)= A B^T over 64 dimensions, both K-major.
-KV_DEVICE void mma_ss_k64(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc_first) {
+KV_DEVICE void mma_ss_k64(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                          uint32_t acc_first) {
     asm volatile(
         "{\n\t.reg .pred p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 t, %5, %5;\n\t"
-        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t"
-        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
-        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
-        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc_first)
+        "setp.ne.u32 p, %6, 0;\n\tsetp.eq.u32 t, %6, %6;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %3, 2;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %3, 4;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %3, 6;\n\tmov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc_first)
         : "memory");
 }
 
 // The rows of a piece, the same for every role.
 struct Rows {
-    int node0, rows, copies;  // copies of each row in a tile
-    int before;               // tokens before the tree
-    KV_DEVICE Rows(const TreeParams &p, const Piece &pc, int mt) {
+    int node0, nodes;  // of the group
+    int before;        // tokens before the tree
+    KV_DEVICE Rows(const TreeParams &p, const Piece &pc) {
         node0 = pc.grp * p.plan.group_nodes;
-        rows = min(p.plan.group_nodes, pc.seq.nodes - node0) * p.g;
-        copies = mt == 2 || rows > 64 ? 1 : rows > 32 ? 2 : 4;
+        nodes = min(p.plan.group_nodes, pc.seq.nodes - node0);
         before = pc.seq.len - pc.seq.nodes;
     }
 };
@@ -255,8 +254,8 @@ struct Ancestors {
 
 template <int D, bool F16, int MT, bool TW>
 __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
-    tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const TreeParams p) {
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
     using L = Layout<D, MT>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // the kernel that adds up cut pairs may start beside this one; it waits for its end
@@ -277,11 +276,12 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.qfull[s], 1);
-            mbar_init(&sm.qempty[s], MT == 1 ? 4 : 9);  // MT = 2: the last S, and each softmax warp
+            // MT = 2: the last S, and each softmax warp once it has read what the piece is
+            mbar_init(&sm.qempty[s], MT == 1 ? 4 : 1 + L::kRowWarps * MT);
             mbar_init(&sm.sfull[s], 1);
-            mbar_init(&sm.pfull[s], 4);
+            mbar_init(&sm.pfull[s], L::kRowWarps);
             mbar_init(&sm.odone[s], 1);
-            mbar_init(&sm.oempty[s], 4);
+            mbar_init(&sm.oempty[s], L::kRowWarps);
             sm.nonfinite[s] = -1;
         }
         mbar_init(&sm.done, 1);
@@ -357,9 +357,11 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
     } else if (warp == L::kQWarp) {
         // ================================================== pieces and their query rows
         // What a piece is, its tree and its queries, for the other warps: theirs would be
-        // round trips to memory at every piece's beginning.  Queries are stored K-major with
-        // 128-byte swizzle, as the products read them; rows past the group's last hold
-        // anything (no row reaches another one).
+        // round trips to memory at every piece's beginning.  A box holds 64 dimensions of all
+        // heads of tile_nodes nodes; rows past the group's last hold anything (no row
+        // reaches another one).
+        if (lane == 0) tc::prefetch_tensormap(&tm_q);
+        int copied = 0;  // pieces whose queries were asked for
         Pieces pieces;
         pieces.start(p.plan, at, blockIdx.x);
         Piece pc;
@@ -372,34 +374,37 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                      (n < L::kQBufs || mbar_wait<TW>(&sm.qempty[buf], (n / L::kQBufs - 1) & 1, p.err));
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
-            if (more) {
-                const Rows r(p, pc, MT);
-                const uint32_t dst = smem_addr(sQ) + buf * L::kTileBytes;
-                const int per_copy = 128 / r.copies;
-                constexpr int kChunks = D / 8, kStep = 32 / kChunks;  // 16-byte parts of a row; rows at a time
-                const int c = lane % kChunks;
-                const uint16_t *src = static_cast<const uint16_t *>(p.q) +
-                                      ((size_t)(pc.seq.q0 + r.node0) * p.hq + pc.h * p.g) * D + 8 * c;
-                int row = lane / kChunks, node = row / p.g, head = row - node * p.g;
-#pragma unroll 2
-                for (; row < r.rows; row += kStep) {
-                    const uint16_t *from = src + ((size_t)node * p.hq + head) * D;
-                    for (int at_row = row; at_row < (MT == 1 ? 128 : 256); at_row += per_copy) {
-                        cp_async16(dst + (at_row >> 7) * L::kTileBytes + tile_offset<D>(at_row & 127, c), from);
-                        if (r.copies == 1) break;
-                    }
-                    for (head += kStep; head >= p.g; head -= p.g) ++node;
-                }
+            if (more)
                 sm.parents[buf][lane] = Ancestors::pack(p.parents ? p.parents + pc.seq.q0 : nullptr, pc.seq.nodes, p.err);
-            } else {
+            else
                 pc.t0 = pc.t1 = 0;
-            }
-            if (lane == 0) sm.piece[buf] = pc;
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.qfull[buf]);
+            if (lane == 0) {
+                sm.piece[buf] = pc;
+                if (more) {
+                    const Rows r(p, pc);
+                    const int per_copy = 128 / p.copies;
+                    const int boxes = MT == 2 ? (r.nodes > p.plan.tile_nodes ? 2 : 1) : p.copies;
+                    mbar_arrive_expect_tx(&sm.qfull[buf], boxes * L::kHalves * p.plan.tile_nodes * p.g * 128);
+                    for (int i = 0; i < boxes; ++i) {
+                        char *dst = sQ + buf * L::kTileBytes + (MT == 2 ? i * L::kTileBytes : i * per_copy * 128);
+                        const int y = pc.seq.q0 + r.node0 + (MT == 2 ? i * p.plan.tile_nodes : 0);
+#pragma unroll
+                        for (int h = 0; h < L::kHalves; ++h)
+                            tc::tma_load_3d(dst + h * (128 * 128), &tm_q, 64 * h, pc.h * p.g, y, &sm.qfull[buf]);
+                    }
+                    ++copied;
+                } else {
+                    mbar_arrive(&sm.qfull[buf]);
+                }
+            }
+            __syncwarp();
         }
+        // No copy may be in flight when the CTA ends.  (A buffer that was given anew had its
+        // queries read; the end, once told, is in the one after the last piece's.)
+        if (lane == 0)
+            for (int i = max(0, copied + (ok ? 1 : 0) - L::kQBufs); i < copied; ++i)
+                mbar_wait_drain(&sm.qfull[i % L::kQBufs], (i / L::kQBufs) & 1, p.err);
         if (!ok && lane == 0) *abort_flag = 1;
     } else if (warp == L::kMmaWarp) {
         // ================================================== products
@@ -409,6 +414,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             constexpr uint32_t idesc_pv = F16 ? tc::idesc_f16_f32(128, D, false, true)
                                               : tc::idesc_bf16_f32(128, D, false, true);
             const uint32_t d_hi = tc::smem_desc_sw128_hi(L::kGroupBytes);
+            const uint32_t q_hi = tc::smem_desc_sw128_hi(1024);  // (Q: 128 rows of 64 dimensions, then the others)
             const uint32_t q_lo = tc::smem_desc_sw128_lo(smem_addr(sQ), 16);
             const uint32_t k_lo = tc::smem_desc_sw128_lo(smem_addr(ring), 16);
             const uint32_t v_lo = tc::smem_desc_sw128_lo(smem_addr(ring), 1024);  // (the other 64 dimensions)
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 const uint32_t a = q_lo + ((q_tile * L::kTileBytes) >> 4), b = k_lo + ((slot * L::kTileBytes) >> 4);
 #pragma unroll
                 for (int h = 0; h < L::kHalves; ++h)
-                    mma_ss_k64(tmem + col, a + 64 * h, b + 64 * h, d_hi, idesc_qk, h);
+                    mma_ss_k64(tmem + col, a + 1024 * h, q_hi, b + 64 * h, d_hi, idesc_qk, h);
             };
             auto issue_pv = [&](uint32_t col_o, uint32_t col_p, int slot, bool first) {
                 const uint32_t b = v_lo + ((slot * L::kTileBytes) >> 4);
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     ok = mbar_wait<TW>(&sm.qfull[0], n & 1, p.err);
                     if (!ok) break;
                     const Piece pc = sm.piece[0];
-                    const int row_tiles = Rows(p, pc, MT).rows > 128 ? 2 : 1;
+                    const int row_tiles = Rows(p, pc).nodes > p.plan.tile_nodes ? 2 : 1;
                     const int tiles = pc.t1 - pc.t0;
                     if (tiles == 0) break;
                     ok = wait_full(2 * t);
@@ -534,16 +540,30 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         }
     } else {
         // ================================================== softmax
-        const int x = MT == 2 ? warp >> 2 : 0;  // row tile
+        const int x = MT == 2 ? warp / L::kRowWarps : 0;      // row tile
+        const int part_of = MT == 2 ? (warp >> 2) & 1 : 0;    // MT = 2: which half of the keys is this thread's
+        const int pair_bar = 1 + (MT == 2 ? 4 * x + (warp & 3) : 0);  // MT = 2: of the two warps that share rows
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const int lane_row = tid & 127;
+        const int per_copy = 128 / p.copies;
+        const int copy = MT == 1 ? lane_row / per_copy : 0;
+        const int row = lane_row - copy * per_copy;
+        const int row_node = row / p.g, row_head = row - row_node * p.g;
+        const int chunks = MT == 2 ? 2 : 4 / p.copies;         // of 32 keys of a tile, this thread's
+        const int c0 = (MT == 2 ? part_of : copy) * chunks, c1 = c0 + chunks;
         unsigned t = 0;      // tiles of this row tile so far (MT = 1: of the run)
         unsigned run_t = 0;  // tiles of the run so far
-        int n = 0;         // pieces
+        int n = 0;           // pieces
         bool ok = true;
         while (true) {
             ok = mbar_wait<TW>(&sm.qfull[n % L::kQBufs], (n / L::kQBufs) & 1, p.err);
-            ok = !__any_sync(0xffffffffu, !ok);
+            // (warps that meet at barriers stay or leave together: MT = 2 here, and at every tile
+            // and end of a piece; MT = 1 at the end of every piece and of the run)
+            if constexpr (MT == 2)
+                ok = !named_bar_or(pair_bar, 64, !ok);
+            else
+                ok = !__any_sync(0xffffffffu, !ok);
+            if (MT == 2 && !ok) break;
             Piece pc{};
             uint2 parents = make_uint2(0, 0);
             if (ok) {
@@ -554,29 +574,27 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     if (lane == 0) mbar_arrive(&sm.qempty[0]);
                 }
             }
-            const Rows r(p, pc, MT);
+            const Rows r(p, pc);
             const int tiles = pc.t1 - pc.t0;
-            if (MT == 2 && tiles > 0 && x == 1 && r.rows <= 128) {
+            if (MT == 2 && tiles > 0 && x == 1 && r.nodes <= p.plan.tile_nodes) {
                 run_t += tiles;
                 ++n;
                 continue;
             }
-            const int per_copy = 128 / r.copies;
-            const int copy = r.copies == 1 ? 0 : lane_row / per_copy;
-            const int row = 128 * x + (r.copies == 1 ? lane_row : lane_row % per_copy);
-            const bool valid = tiles > 0 && row < r.rows;
-            const int node = valid ? r.node0 + row / p.g : -1;
+            const int at_node = x * p.plan.tile_nodes + row_node;  // of the group
+            const bool valid = tiles > 0 && row_node < p.plan.tile_nodes && at_node < r.nodes;
+            const int node = valid ? r.node0 + at_node : -1;
             const bool idle = __all_sync(0xffffffffu, !valid);  // rows of no query
-            const int chunks = 4 / r.copies, c0 = copy * chunks;  // of 32 keys of a tile, this copy's
             Ancestors anc;
             if (!idle && pc.t1 * kTile > r.before) anc.walk(parents, node);
             float m_used = -INFINITY, l_sum = 0.f;
             for (int j = 0; j < tiles; ++j, ++t, ++run_t) {
                 const int buf = MT == 1 ? (int)(t & 1) : x;
                 const uint32_t phase = MT == 1 ? (t >> 1) & 1 : t & 1;
-                bool bad = *abort_flag != 0;
+                bool bad = !ok || *abort_flag != 0;
                 if (!bad) bad = !mbar_wait<TW>(&sm.sfull[buf], phase, p.err);
                 if (__any_sync(0xffffffffu, bad)) {
+                    if (MT == 2 && !idle) named_bar_or(pair_bar, 64, true);  // where the other warp waits
                     ok = false;
                     break;
                 }
@@ -590,7 +608,6 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 if (!idle) {
                     // Loops over chunks of 32 keys are not unrolled, and scores are read twice:
                     // the code of a tile has to stay in the instruction caches.
-                    const int c1 = c0 + chunks;
                     if (tail || gone) {
 #pragma unroll 1
                         for (int c = c0; c < c1; ++c) {
@@ -624,6 +641,14 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         }
                         mrow = max3(mrow, max3(m[0], m[1], m[2]), m[3]);
                     }
+                    if constexpr (MT == 2) {  // the row's other thread has the other keys
+                        sm.top[t & 1][x][part_of][lane_row] = mrow;
+                        if (named_bar_or(pair_bar, 64, false)) {
+                            ok = false;
+                            break;
+                        }
+                        mrow = fmaxf(mrow, sm.top[t & 1][x][part_of ^ 1][lane_row]);
+                    }
                     mrow *= p.scale_log2;  // scale > 0
                     if (m_used == -INFINITY) {
                         m_used = mrow;
@@ -652,7 +677,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         tc::tmem_st32(scol + 32 * c, w);
                     }
                     l_sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-                    if (chunks < 4) {  // the other copies' keys
+                    if (MT == 1 && chunks < 4) {  // the other copies' keys
                         uint32_t zero[32];
 #pragma unroll
                         for (int k = 0; k < 32; ++k) zero[k] = 0;
@@ -664,12 +689,14 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         // O holds the products up to the tile before once that one's are done
                         if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.odone[x], (t - 1) & 1, p.err))) {
                             ok = false;
-                            break;
+                            if (MT == 1) break;
+                            continue;  // MT = 2: the warps leave at the next barrier
                         }
                         tc::fence_after_sync();
                         const uint32_t ocol = tmem + lane_base + kColO0 + 128 * (MT == 1 ? n & 1 : x);
+                        constexpr int kStrips = D / 16 / L::kRowThreads;  // a row's threads share its columns
 #pragma unroll 1
-                        for (int i = 0; i < D / 16; ++i) {
+                        for (int i = part_of * kStrips; i < (part_of + 1) * kStrips; ++i) {
                             uint32_t v[16];
                             tc::tmem_ld16(ocol + 16 * i, v);
                             tc::tmem_wait_ld();
@@ -684,13 +711,14 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     const unsigned pos = 2 * run_t + 1;
                     if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1, p.err))) {
                         ok = false;
-                        break;
+                        if (MT == 1) break;
+                        continue;
                     }
                     char *vt = ring + (int)(pos % L::kSlots) * L::kTileBytes;
                     const int row0 = max(0, r.before - key0);
                     constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
 #pragma unroll 2
-                    for (int i = row0 * (D / 8) + lane_row; i < 128 * (D / 8); i += 128) {
+                    for (int i = row0 * (D / 8) + tid; i < 128 * (D / 8); i += 32 * L::kRowWarps) {
                         const int at_row = i / (D / 8);
                         uint4 *at4 = reinterpret_cast<uint4 *>(vt + tile_offset<D>(at_row, i % (D / 8)));
                         const uint4 v = *at4;
@@ -721,23 +749,26 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 bad = bad || !mbar_wait<TW>(&sm.odone[x], (t - 1) & 1, p.err);
                 ok = !__any_sync(0xffffffffu, bad);
             }
-            // all warps stay or leave together: they meet once for every piece and for the end
             if constexpr (MT == 1) {
                 sm.ml[lane_row] = make_float2(m_used, l_sum);
                 ok = !named_bar_or(1, L::kSoftmax, !ok);
+            } else {
+                sm.ml[(2 * x + part_of) * 128 + lane_row].y = l_sum;
+                ok = !named_bar_or(pair_bar, 64, !ok);
+                if (ok) l_sum += sm.ml[(2 * x + (part_of ^ 1)) * 128 + lane_row].y;
             }
             if (!ok || tiles == 0) break;
             tc::fence_after_sync();
             const uint32_t ocol = tmem + lane_base + kColO0 + 128 * (MT == 1 ? n & 1 : x);
             const bool nonfinite = *reinterpret_cast<volatile int *>(&sm.nonfinite[n & 1]) == n;
             float factor = 1.f;
-            if (MT == 1 && r.copies > 1) {
+            if (MT == 1 && p.copies > 1) {
                 // the copies of a row share a reference from here on
                 float M = -INFINITY;
-                for (int c = 0; c < r.copies; ++c) M = fmaxf(M, sm.ml[row + c * per_copy].x);
+                for (int c = 0; c < p.copies; ++c) M = fmaxf(M, sm.ml[row + c * per_copy].x);
                 const float ref = M == -INFINITY ? 0.f : M;
                 float l = 0.f;
-                for (int c = 0; c < r.copies; ++c) {
+                for (int c = 0; c < p.copies; ++c) {
                     const float2 ml = sm.ml[row + c * per_copy];
                     l += tc_ex2(ml.x - ref) * ml.y;
                 }
@@ -745,7 +776,8 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 m_used = M;
                 l_sum = l;
             }
-            const size_t orow = valid ? (size_t)(pc.seq.q0 + node) * p.hq + pc.h * p.g + row % p.g : 0;
+            const size_t orow = valid ? (size_t)(pc.seq.q0 + node) * p.hq + pc.h * p.g + row_head : 0;
+            const int slot_row = 128 * x + row;
             const bool seen = l_sum != 0.f;  // a row with a NaN score stays NaN
             if (pc.slot < 0) factor *= seen ? 1.f / l_sum : 0.f;
             float *part = p.partial + (size_t)max(pc.slot, 0) * (128 * MT) * (D + 2);
@@ -754,7 +786,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 if (pc.slot >= 0) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        reinterpret_cast<float4 *>(part)[(4 * strip + k) * (128 * MT) + row] =
+                        reinterpret_cast<float4 *>(part)[(4 * strip + k) * (128 * MT) + slot_row] =
                             make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 } else if (p.out_type == KV_F32) {
                     float *dst = static_cast<float *>(p.out) + orow * D + 16 * strip;
@@ -773,9 +805,9 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     store_sector(static_cast<uint16_t *>(p.out) + orow * D + 16 * strip, y, aligned32);
                 }
             };
-            if (MT == 2 || r.copies == 1) {
+            if (MT == 2 || p.copies == 1) {
 #pragma unroll 1
-                for (int i = 0; i < D / 16; ++i) {
+                for (int i = part_of * (D / 16 / L::kRowThreads); i < (part_of + 1) * (D / 16 / L::kRowThreads); ++i) {
                     uint32_t v[16];
                     tc::tmem_ld16(ocol + 16 * i, v);
                     tc::tmem_wait_ld();
@@ -794,7 +826,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     if (half) named_bar_sync(2, L::kSoftmax);  // the first half was read
 #pragma unroll 1
                     for (int i = 0; i < D / 32; ++i) {
-                        if (i % r.copies == copy) continue;
+                        if (i % p.copies == copy) continue;
                         uint32_t v[16];
                         tc::tmem_ld16(ocol + half * (D / 2) + 16 * i, v);
                         tc::tmem_wait_ld();
@@ -806,7 +838,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                     named_bar_sync(2, L::kSoftmax);
 #pragma unroll 1
-                    for (int i = copy; i < D / 32; i += r.copies) {
+                    for (int i = copy; i < D / 32; i += p.copies) {
                         uint32_t v[16];
                         tc::tmem_ld16(ocol + half * (D / 2) + 16 * i, v);
                         tc::tmem_wait_ld();
@@ -814,7 +846,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 16; ++k) o[k] = __uint_as_float(v[k]) * factor;
 #pragma unroll 1
-                        for (int c = 1; c < r.copies; ++c) {
+                        for (int c = 1; c < p.copies; ++c) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const float4 y = box[(4 * i + k) * 128 + ((lane_row + c * per_copy) & 127)];
@@ -825,15 +857,15 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                 }
             }
-            if (valid && copy == 0) {
+            if (valid && copy == 0 && part_of == 0) {
                 if (pc.slot >= 0)
-                    reinterpret_cast<float2 *>(part + (size_t)128 * MT * D)[row] = make_float2(m_used, l_sum);
+                    reinterpret_cast<float2 *>(part + (size_t)128 * MT * D)[slot_row] = make_float2(m_used, l_sum);
                 else if (p.lse)
                     p.lse[orow] = seen ? (m_used + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
             }
             // (uniform over the CTA: every warp reads the same word)
-            if (MT == 1 && nonfinite) named_bar_sync(2, L::kSoftmax);  // the other copies' stores
-            if (nonfinite && valid && copy == 0) {
+            if (nonfinite) named_bar_sync(MT == 1 ? 2 : pair_bar, MT == 1 ? L::kSoftmax : 64);  // the row's other stores
+            if (nonfinite && valid && copy == 0 && part_of == 0) {
                 // what was kept out of the products, for the rows that attend it
                 const int32_t *table = p.tables + (size_t)pc.b * p.plan.max_blocks;
                 for (int k = 0; k < pc.seq.nodes; ++k) {
@@ -848,7 +880,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         const float y = F16 ? f16x2_to_float2(from[d]).x : bf16_to_float(from[d]);
                         if (fabsf(y) < INFINITY) continue;
                         if (pc.slot >= 0) {
-                            part[((size_t)(d >> 2) * (128 * MT) + row) * 4 + (d & 3)] += y;
+                            part[((size_t)(d >> 2) * (128 * MT) + slot_row) * 4 + (d & 3)] += y;
                         } else if (p.out_type == KV_F32) {
                             static_cast<float *>(p.out)[orow * D + d] += y;
                         } else {
@@ -881,13 +913,15 @@ namespace {
 template <int D, int MT>
 kv_status launch(const TreeParams &pp, bool f16, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t stream) {
     using L = Layout<D, MT>;
+    CUtensorMap tq;
+    if (!encode_q_map(&tq, pp.q, pp.total_q, pp.hq, pp.g, pp.plan.tile_nodes, D)) return KV_ERR_CUDA;
     constexpr int smem = L::kBars + (int)sizeof(Shared<D, MT>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     auto fn = test_waits_enabled() ? (f16 ? tree_tc_kernel<D, true, MT, true> : tree_tc_kernel<D, false, MT, true>)
                                    : (f16 ? tree_tc_kernel<D, true, MT, false> : tree_tc_kernel<D, false, MT, false>);
     if (kv_status st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
         return st;
-    fn<<<pp.plan.runs, L::kThreads, smem, stream>>>(tk, tv, pp);
+    fn<<<pp.plan.runs, L::kThreads, smem, stream>>>(tq, tk, tv, pp);
     return cuda_status(cudaGetLastError());
 }
 
