@@ -55,14 +55,12 @@ struct Layout {
     static constexpr int kHalves = D / 64;
     static constexpr int kGroupBytes = 1024 * kHalves;
     static constexpr int kTileBytes = 16 * kGroupBytes;
-    static constexpr int kSlots = D == 64 ? 8 : MT == 1 ? 5 : 4;
+    static constexpr int kSlots = D == 64 ? 8 : 5;
     static constexpr int kQBufs = MT == 1 ? 2 : 1;  // of MT tiles
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kBars = kRing + kSlots * kTileBytes;
-    static constexpr int kRowThreads = MT;          // threads of a row, each with its part of the keys
-    static constexpr int kRowWarps = 4 * kRowThreads;  // softmax warps of a row tile
-    static constexpr int kSoftmax = 32 * kRowWarps * MT;  // threads
-    static constexpr int kCopyWarp = kRowWarps * MT, kMmaWarp = kCopyWarp + 1, kQWarp = kCopyWarp + 2;
+    static constexpr int kSoftmax = 128 * MT;       // threads
+    static constexpr int kCopyWarp = 4 * MT, kMmaWarp = kCopyWarp + 1, kQWarp = kCopyWarp + 2;
     static constexpr int kThreads = kSoftmax + 96;
 };
 
@@ -84,8 +82,7 @@ struct Shared {
     int abort;
     uint32_t gone[8];              // by tile in turn: bit i: block i is not there
     int nonfinite[2];              // by piece in turn: number of a piece whose tree holds some in V
-    float2 ml[128 * MT * MT];      // MT = 1: reference and sum of each row copy; MT = 2: sums of a row's threads
-    float top[MT == 1 ? 1 : 2][MT][MT][MT == 1 ? 1 : 128];  // MT = 2: maxima, by tile in turn, of a row tile's rows' threads
+    float2 ml[MT == 1 ? 128 : 1];  // MT = 1: reference and sum of each row copy
     Piece piece[2];                // by Q buffer: the piece whose queries it holds; t1 = 0: no more
     uint2 parents[2][32];          // of the piece's tree, 8 nodes a lane (Ancestors)
     PlaceScratch<Layout<D, MT>::kThreads> scratch;
@@ -124,18 +121,21 @@ KV_DEVICE void store_sector(void *dst, const uint32_t (&y)[8], bool aligned) {
     }
 }
 
-// Two weights as a pair of the 16-bit type and the pair of what that leaves of them.
+// Two weights as a pair of the 16-bit type and the pair of what that leaves of them.  bf16 is
+// cut off (the upper halves of the two words), which leaves up to 2^-7 of a weight and so
+// an error of 2^-15 once the rest is rounded; fp16 is rounded: 2^-22.
 template <bool F16>
-KV_DEVICE void split(float x, float y, uint32_t &hi, uint32_t &lo) {
+KV_DEVICE void split(float2 e, uint32_t &hi, uint32_t &lo) {
+    float2 h;
     if constexpr (F16) {
-        hi = tc::pack_f16x2(x, y);
-        const float2 h = f16x2_to_float2(hi);
-        lo = tc::pack_f16x2(x - h.x, y - h.y);
+        hi = tc::pack_f16x2(e.x, e.y);
+        h = f16x2_to_float2(hi);
     } else {
-        hi = tc::pack_bf16x2(x, y);
-        const float2 h = bf16x2_to_float2(hi);
-        lo = tc::pack_bf16x2(x - h.x, y - h.y);
+        hi = __byte_perm(__float_as_uint(e.x), __float_as_uint(e.y), 0x7632);
+        h = make_float2(__uint_as_float(__float_as_uint(e.x) & 0xffff0000u), __uint_as_float(__float_as_uint(e.y) & 0xffff0000u));
     }
+    const float2 rest = __ffma2_rn(h, make_float2(-1.f, -1.f), e);
+    lo = F16 ? tc::pack_f16x2(rest.x, rest.y) : tc::pack_bf16x2(rest.x, rest.y);
 }
 
 // D (+)= P B over 128 keys: P at p_tmem in steps of 16 keys, 8 columns each, two steps of every
@@ -277,11 +277,11 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.qfull[s], 1);
             // MT = 2: the last S, and each softmax warp once it has read what the piece is
-            mbar_init(&sm.qempty[s], MT == 1 ? 4 : 1 + L::kRowWarps * MT);
+            mbar_init(&sm.qempty[s], MT == 1 ? 4 : 1 + 8);
             mbar_init(&sm.sfull[s], 1);
-            mbar_init(&sm.pfull[s], L::kRowWarps);
+            mbar_init(&sm.pfull[s], 4);
             mbar_init(&sm.odone[s], 1);
-            mbar_init(&sm.oempty[s], L::kRowWarps);
+            mbar_init(&sm.oempty[s], 4);
             sm.nonfinite[s] = -1;
         }
         mbar_init(&sm.done, 1);
@@ -540,30 +540,21 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         }
     } else {
         // ================================================== softmax
-        const int x = MT == 2 ? warp / L::kRowWarps : 0;      // row tile
-        const int part_of = MT == 2 ? (warp >> 2) & 1 : 0;    // MT = 2: which half of the keys is this thread's
-        const int pair_bar = 1 + (MT == 2 ? 4 * x + (warp & 3) : 0);  // MT = 2: of the two warps that share rows
+        const int x = MT == 2 ? warp >> 2 : 0;  // row tile
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const int lane_row = tid & 127;
         const int per_copy = 128 / p.copies;
         const int copy = MT == 1 ? lane_row / per_copy : 0;
         const int row = lane_row - copy * per_copy;
         const int row_node = row / p.g, row_head = row - row_node * p.g;
-        const int chunks = MT == 2 ? 2 : 4 / p.copies;         // of 32 keys of a tile, this thread's
-        const int c0 = (MT == 2 ? part_of : copy) * chunks, c1 = c0 + chunks;
+        const int chunks = 4 / p.copies, c0 = copy * chunks, c1 = c0 + chunks;  // of 32 keys of a tile, this copy's
         unsigned t = 0;      // tiles of this row tile so far (MT = 1: of the run)
         unsigned run_t = 0;  // tiles of the run so far
         int n = 0;           // pieces
         bool ok = true;
         while (true) {
             ok = mbar_wait<TW>(&sm.qfull[n % L::kQBufs], (n / L::kQBufs) & 1, p.err);
-            // (warps that meet at barriers stay or leave together: MT = 2 here, and at every tile
-            // and end of a piece; MT = 1 at the end of every piece and of the run)
-            if constexpr (MT == 2)
-                ok = !named_bar_or(pair_bar, 64, !ok);
-            else
-                ok = !__any_sync(0xffffffffu, !ok);
-            if (MT == 2 && !ok) break;
+            ok = !__any_sync(0xffffffffu, !ok);
             Piece pc{};
             uint2 parents = make_uint2(0, 0);
             if (ok) {
@@ -591,10 +582,9 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             for (int j = 0; j < tiles; ++j, ++t, ++run_t) {
                 const int buf = MT == 1 ? (int)(t & 1) : x;
                 const uint32_t phase = MT == 1 ? (t >> 1) & 1 : t & 1;
-                bool bad = !ok || *abort_flag != 0;
+                bool bad = *abort_flag != 0;
                 if (!bad) bad = !mbar_wait<TW>(&sm.sfull[buf], phase, p.err);
                 if (__any_sync(0xffffffffu, bad)) {
-                    if (MT == 2 && !idle) named_bar_or(pair_bar, 64, true);  // where the other warp waits
                     ok = false;
                     break;
                 }
@@ -624,32 +614,31 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         }
                         tc::tmem_wait_st();
                     }
+                    // Scores are read twice, for the maximum and for the weights, two chunks of 32 at
+                    // a time: all of them in registers at once would unroll into more code than the
+                    // instruction caches next to the schedulers hold.
                     float mrow = -INFINITY;
 #pragma unroll 1
-                    for (int c = c0; c < c1; ++c) {
-                        uint32_t v[32];
-                        tc::tmem_ld32(scol + 32 * c, v);
+                    for (int c = c0; c < c1; c += 2) {
+                        uint32_t v[2][32];
+                        tc::tmem_ld32(scol + 32 * c, v[0]);
+                        tc::tmem_ld32(scol + 32 * min(c + 1, c1 - 1), v[1]);
                         tc::tmem_wait_ld();
                         float m[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint32_t *w = &v[8 * i];
+                            const uint32_t *w = &v[i >> 1][16 * (i & 1)];
                             m[i] = max3(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]));
-                            m[i] = max3(m[i], __uint_as_float(w[3]), __uint_as_float(w[4]));
-                            m[i] = max3(m[i], __uint_as_float(w[5]), __uint_as_float(w[6]));
-                            m[i] = fmaxf(m[i], __uint_as_float(w[7]));
+#pragma unroll
+                            for (int k = 3; k < 15; k += 2)
+                                m[i] = max3(m[i], __uint_as_float(w[k]), __uint_as_float(w[k + 1]));
+                            m[i] = fmaxf(m[i], __uint_as_float(w[15]));
                         }
                         mrow = max3(mrow, max3(m[0], m[1], m[2]), m[3]);
                     }
-                    if constexpr (MT == 2) {  // the row's other thread has the other keys
-                        sm.top[t & 1][x][part_of][lane_row] = mrow;
-                        if (named_bar_or(pair_bar, 64, false)) {
-                            ok = false;
-                            break;
-                        }
-                        mrow = fmaxf(mrow, sm.top[t & 1][x][part_of ^ 1][lane_row]);
-                    }
                     mrow *= p.scale_log2;  // scale > 0
+                    uint32_t va[32], vb[32];
+                    tc::tmem_ld32(scol + 32 * c0, va);
                     if (m_used == -INFINITY) {
                         m_used = mrow;
                     } else if (mrow > m_used + kRenew) {
@@ -661,23 +650,31 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     const float ref = m_used == -INFINITY ? 0.f : m_used;
                     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-ref, -ref);
                     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-                    for (int c = c0; c < c1; ++c) {
-                        uint32_t v[32], w[32];
-                        tc::tmem_ld32(scol + 32 * c, v);
-                        tc::tmem_wait_ld();
+                    auto weigh = [&](uint32_t (&v)[32], int c) {
+                        uint32_t w[32];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             const float2 xx = __ffma2_rn(
                                 make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sc2, nm2);
                             const float2 e = make_float2(tc_ex2(xx.x), tc_ex2(xx.y));
                             acc[k & 1] = __fadd2_rn(acc[k & 1], e);
-                            split<F16>(e.x, e.y, w[k], w[16 + k]);
+                            split<F16>(e, w[k], w[16 + k]);
                         }
                         tc::tmem_st32(scol + 32 * c, w);
+                    };
+                    tc::tmem_wait_ld();
+#pragma unroll 1
+                    for (int c = c0; c < c1; c += 2) {
+                        if (c + 1 < c1) tc::tmem_ld32(scol + 32 * (c + 1), vb);
+                        weigh(va, c);
+                        if (c + 1 == c1) break;
+                        tc::tmem_wait_ld();
+                        if (c + 2 < c1) tc::tmem_ld32(scol + 32 * (c + 2), va);
+                        weigh(vb, c + 1);
+                        tc::tmem_wait_ld();
                     }
                     l_sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-                    if (MT == 1 && chunks < 4) {  // the other copies' keys
+                    if (chunks < 4) {  // the other copies' keys
                         uint32_t zero[32];
 #pragma unroll
                         for (int k = 0; k < 32; ++k) zero[k] = 0;
@@ -689,14 +686,12 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         // O holds the products up to the tile before once that one's are done
                         if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.odone[x], (t - 1) & 1, p.err))) {
                             ok = false;
-                            if (MT == 1) break;
-                            continue;  // MT = 2: the warps leave at the next barrier
+                            break;
                         }
                         tc::fence_after_sync();
                         const uint32_t ocol = tmem + lane_base + kColO0 + 128 * (MT == 1 ? n & 1 : x);
-                        constexpr int kStrips = D / 16 / L::kRowThreads;  // a row's threads share its columns
 #pragma unroll 1
-                        for (int i = part_of * kStrips; i < (part_of + 1) * kStrips; ++i) {
+                        for (int i = 0; i < D / 16; ++i) {
                             uint32_t v[16];
                             tc::tmem_ld16(ocol + 16 * i, v);
                             tc::tmem_wait_ld();
@@ -711,14 +706,13 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     const unsigned pos = 2 * run_t + 1;
                     if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1, p.err))) {
                         ok = false;
-                        if (MT == 1) break;
-                        continue;
+                        break;
                     }
                     char *vt = ring + (int)(pos % L::kSlots) * L::kTileBytes;
                     const int row0 = max(0, r.before - key0);
                     constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
 #pragma unroll 2
-                    for (int i = row0 * (D / 8) + tid; i < 128 * (D / 8); i += 32 * L::kRowWarps) {
+                    for (int i = row0 * (D / 8) + tid; i < 128 * (D / 8); i += 128) {
                         const int at_row = i / (D / 8);
                         uint4 *at4 = reinterpret_cast<uint4 *>(vt + tile_offset<D>(at_row, i % (D / 8)));
                         const uint4 v = *at4;
@@ -749,13 +743,10 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 bad = bad || !mbar_wait<TW>(&sm.odone[x], (t - 1) & 1, p.err);
                 ok = !__any_sync(0xffffffffu, bad);
             }
+            // MT = 1: all warps stay or leave together; they meet once for every piece and for the end
             if constexpr (MT == 1) {
                 sm.ml[lane_row] = make_float2(m_used, l_sum);
                 ok = !named_bar_or(1, L::kSoftmax, !ok);
-            } else {
-                sm.ml[(2 * x + part_of) * 128 + lane_row].y = l_sum;
-                ok = !named_bar_or(pair_bar, 64, !ok);
-                if (ok) l_sum += sm.ml[(2 * x + (part_of ^ 1)) * 128 + lane_row].y;
             }
             if (!ok || tiles == 0) break;
             tc::fence_after_sync();
@@ -807,7 +798,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             };
             if (MT == 2 || p.copies == 1) {
 #pragma unroll 1
-                for (int i = part_of * (D / 16 / L::kRowThreads); i < (part_of + 1) * (D / 16 / L::kRowThreads); ++i) {
+                for (int i = 0; i < D / 16; ++i) {
                     uint32_t v[16];
                     tc::tmem_ld16(ocol + 16 * i, v);
                     tc::tmem_wait_ld();
@@ -857,15 +848,15 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                 }
             }
-            if (valid && copy == 0 && part_of == 0) {
+            if (valid && copy == 0) {
                 if (pc.slot >= 0)
                     reinterpret_cast<float2 *>(part + (size_t)128 * MT * D)[slot_row] = make_float2(m_used, l_sum);
                 else if (p.lse)
                     p.lse[orow] = seen ? (m_used + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
             }
             // (uniform over the CTA: every warp reads the same word)
-            if (nonfinite) named_bar_sync(MT == 1 ? 2 : pair_bar, MT == 1 ? L::kSoftmax : 64);  // the row's other stores
-            if (nonfinite && valid && copy == 0 && part_of == 0) {
+            if (MT == 1 && nonfinite) named_bar_sync(2, L::kSoftmax);  // the other copies' stores
+            if (nonfinite && valid && copy == 0) {
                 // what was kept out of the products, for the rows that attend it
                 const int32_t *table = p.tables + (size_t)pc.b * p.plan.max_blocks;
                 for (int k = 0; k < pc.seq.nodes; ++k) {
