@@ -121,6 +121,25 @@ KV_DEVICE void store_sector(void *dst, const uint32_t (&y)[8], bool aligned) {
     }
 }
 
+// The largest of kCols columns of this thread's tensor-memory lane (NaN left out), found on the way
+// out of tensor memory.
+template <int kCols>
+KV_DEVICE float tmem_max(uint32_t taddr) {
+    uint32_t r[kCols];
+    float m;
+    if constexpr (kCols == 32) {
+        asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+                     : "=r"(r[0]),"=r"(r[1]),"=r"(r[2]),"=r"(r[3]),"=r"(r[4]),"=r"(r[5]),"=r"(r[6]),"=r"(r[7]),"=r"(r[8]),"=r"(r[9]),"=r"(r[10]),"=r"(r[11]),"=r"(r[12]),"=r"(r[13]),"=r"(r[14]),"=r"(r[15]),"=r"(r[16]),"=r"(r[17]),"=r"(r[18]),"=r"(r[19]),"=r"(r[20]),"=r"(r[21]),"=r"(r[22]),"=r"(r[23]),"=r"(r[24]),"=r"(r[25]),"=r"(r[26]),"=r"(r[27]),"=r"(r[28]),"=r"(r[29]),"=r"(r[30]),"=r"(r[31]), "=f"(m)
+                     : "r"(taddr));
+    } else {
+        asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x64.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, %64, [%65];"
+                     : "=r"(r[0]),"=r"(r[1]),"=r"(r[2]),"=r"(r[3]),"=r"(r[4]),"=r"(r[5]),"=r"(r[6]),"=r"(r[7]),"=r"(r[8]),"=r"(r[9]),"=r"(r[10]),"=r"(r[11]),"=r"(r[12]),"=r"(r[13]),"=r"(r[14]),"=r"(r[15]),"=r"(r[16]),"=r"(r[17]),"=r"(r[18]),"=r"(r[19]),"=r"(r[20]),"=r"(r[21]),"=r"(r[22]),"=r"(r[23]),"=r"(r[24]),"=r"(r[25]),"=r"(r[26]),"=r"(r[27]),"=r"(r[28]),"=r"(r[29]),"=r"(r[30]),"=r"(r[31]),"=r"(r[32]),"=r"(r[33]),"=r"(r[34]),"=r"(r[35]),"=r"(r[36]),"=r"(r[37]),"=r"(r[38]),"=r"(r[39]),"=r"(r[40]),"=r"(r[41]),"=r"(r[42]),"=r"(r[43]),"=r"(r[44]),"=r"(r[45]),"=r"(r[46]),"=r"(r[47]),"=r"(r[48]),"=r"(r[49]),"=r"(r[50]),"=r"(r[51]),"=r"(r[52]),"=r"(r[53]),"=r"(r[54]),"=r"(r[55]),"=r"(r[56]),"=r"(r[57]),"=r"(r[58]),"=r"(r[59]),"=r"(r[60]),"=r"(r[61]),"=r"(r[62]),"=r"(r[63]), "=f"(m)
+                     : "r"(taddr));
+    }
+    tc::tmem_wait_ld();
+    return m;
+}
+
 // Two weights as a pair of the 16-bit type and the pair of what that leaves of them.  bf16 is
 // cut off (the upper halves of the two words), which leaves up to 2^-7 of a weight and so
 // an error of 2^-15 once the rest is rounded; fp16 is rounded: 2^-22.
@@ -466,14 +485,16 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 bool first = true;
                 while (ok && t < s) {
                     if (!(ok = next_s())) break;
-                    if (first && n >= 2 && !mbar_wait<TW>(&sm.oempty[n & 1], ((n >> 1) - 1) & 1, p.err)) ok = false;
-                    if (!ok || !mbar_wait<TW>(&sm.pfull[t & 1], (t >> 1) & 1, p.err) || !wait_full(2 * t + 1)) {
+                    // (the weights last: between their arrival and their product nothing is left to do)
+                    const int slot = (int)((2 * t + 1) % L::kSlots);
+                    if ((first && n >= 2 && !mbar_wait<TW>(&sm.oempty[n & 1], ((n >> 1) - 1) & 1, p.err)) ||
+                        !wait_full(2 * t + 1) || !mbar_wait<TW>(&sm.pfull[t & 1], (t >> 1) & 1, p.err)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
-                    issue_pv(kColO0 + 128 * (n & 1), (t & 1) * 128, (int)((2 * t + 1) % L::kSlots), first);
-                    tc::mma_commit(&sm.empty[(2 * t + 1) % L::kSlots]);
+                    issue_pv(kColO0 + 128 * (n & 1), (t & 1) * 128, slot, first);
+                    tc::mma_commit(&sm.empty[slot]);
                     tc::mma_commit(&sm.odone[0]);
                     ++t;
                     first = --t_left == 0;
@@ -503,29 +524,30 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     tc::mma_commit(&sm.empty[2 * t % L::kSlots]);
                     if (tiles == 1) tc::mma_commit(&sm.qempty[0]);
                     for (int j = 0; ok && j < tiles; ++j, ++t) {
-                        for (int x = 0; x < row_tiles; ++x) {
-                            if (j == 0 && pieces_of[x] > 0 &&
-                                !mbar_wait<TW>(&sm.oempty[x], (pieces_of[x] - 1) & 1, p.err))
-                                ok = false;
-                            if (!ok || !mbar_wait<TW>(&sm.pfull[x], used[x] & 1, p.err) ||
-                                (x == 0 && !wait_full(2 * t + 1)) ||
-                                (x == 0 && j + 1 < tiles && !wait_full(2 * t + 2))) {
+                        // (the weights last: between their arrival and their product nothing is left to do)
+                        const int vslot = (int)((2 * t + 1) % L::kSlots), kslot = (int)((2 * t + 2) % L::kSlots);
+                        const bool more = j + 1 < tiles;
+                        ok = wait_full(2 * t + 1) && (!more || wait_full(2 * t + 2));
+                        for (int x = 0; ok && x < row_tiles; ++x) {
+                            if ((j == 0 && pieces_of[x] > 0 &&
+                                 !mbar_wait<TW>(&sm.oempty[x], (pieces_of[x] - 1) & 1, p.err)) ||
+                                !mbar_wait<TW>(&sm.pfull[x], used[x] & 1, p.err)) {
                                 ok = false;
                                 break;
                             }
                             tc::fence_after_sync();
-                            issue_pv(kColO0 + 128 * x, 128 * x, (int)((2 * t + 1) % L::kSlots), j == 0);
+                            issue_pv(kColO0 + 128 * x, 128 * x, vslot, j == 0);
                             tc::mma_commit(&sm.odone[x]);
-                            ++used[x];
-                            if (j + 1 < tiles) {
-                                issue_s(128 * x, x, (int)((2 * t + 2) % L::kSlots));
+                            if (more) {
+                                issue_s(128 * x, x, kslot);
                                 tc::mma_commit(&sm.sfull[x]);
                             }
+                            ++used[x];
                         }
                         if (!ok) break;
-                        tc::mma_commit(&sm.empty[(2 * t + 1) % L::kSlots]);
-                        if (j + 1 < tiles) {
-                            tc::mma_commit(&sm.empty[(2 * t + 2) % L::kSlots]);
+                        tc::mma_commit(&sm.empty[vslot]);
+                        if (more) {
+                            tc::mma_commit(&sm.empty[kslot]);
                             if (j + 2 == tiles) tc::mma_commit(&sm.qempty[0]);
                         }
                     }
@@ -614,28 +636,11 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         }
                         tc::tmem_wait_st();
                     }
-                    // Scores are read twice, for the maximum and for the weights, two chunks of 32 at
-                    // a time: all of them in registers at once would unroll into more code than the
-                    // instruction caches next to the schedulers hold.
-                    float mrow = -INFINITY;
-#pragma unroll 1
-                    for (int c = c0; c < c1; c += 2) {
-                        uint32_t v[2][32];
-                        tc::tmem_ld32(scol + 32 * c, v[0]);
-                        tc::tmem_ld32(scol + 32 * min(c + 1, c1 - 1), v[1]);
-                        tc::tmem_wait_ld();
-                        float m[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t *w = &v[i >> 1][16 * (i & 1)];
-                            m[i] = max3(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]));
-#pragma unroll
-                            for (int k = 3; k < 15; k += 2)
-                                m[i] = max3(m[i], __uint_as_float(w[k]), __uint_as_float(w[k + 1]));
-                            m[i] = fmaxf(m[i], __uint_as_float(w[15]));
-                        }
-                        mrow = max3(mrow, max3(m[0], m[1], m[2]), m[3]);
-                    }
+                    // Scores are read twice, for the maximum (which tensor memory finds) and for the weights,
+                    // 32 at a time: all of them in registers at once would unroll into more code than
+                    // the instruction caches next to the schedulers hold.
+                    float mrow = chunks == 1 ? tmem_max<32>(scol + 32 * c0) : tmem_max<64>(scol + 32 * c0);
+                    if (chunks == 4) mrow = fmaxf(mrow, tmem_max<64>(scol + 64));
                     mrow *= p.scale_log2;  // scale > 0
                     uint32_t va[32], vb[32];
                     tc::tmem_ld32(scol + 32 * c0, va);
