@@ -10,21 +10,21 @@
 //                  weight alone would be off by 2^-8 of itself, as much as a bf16 output)
 //   O += P_hi V + P_lo V   (P from tensor memory)
 // Roles: softmax warps (a thread = a row = a tensor-memory lane), a warp that copies K and V
-// tiles into one ring by TMA (each block-table entry becomes a box of 16 rows per 64
-// dimensions), a thread that issues the products, a warp that copies the rows of the next
-// group's queries.  The ring runs on across pieces.
+// tiles into one ring by TMA (each block-table entry becomes one box), a thread per row tile
+// that issues its products, a warp that describes the next piece and copies its queries.  The ring runs on across pieces.
 //
-// MT = 1: S is double-buffered, so the next tile's scores are computed while the softmax
-// warps work on this one's; so are Q and O, so a piece's end overlaps the next piece's
-// beginning.  A tile that a group does not fill is filled with copies of its rows (DUP: two of
-// up to 64 rows, four of up to 32): the tensor core computes all of S at the same cost, and
-// each copy's warps take their own keys of the tile and leave zeros as the others' weights,
-// so that all four schedulers share the exponentials; the copies' sums meet at the
-// piece's end.  MT = 2: each row tile has one S and one O, and the softmax of one
-// overlaps the products of the other.
+// S is double-buffered, so the next tile's scores are computed while the softmax warps work
+// on this one's.  MT = 1: Q and O are too, so a piece's end overlaps the next piece's
+// beginning.  A tile that a call's largest group does not fill is filled with copies of its
+// rows (two of up to 64 rows, four of up to 32): the tensor core computes all of S at the same
+// cost, and each copy's warps take their own keys of the tile and leave zeros as the others'
+// weights, so that all four schedulers share the exponentials; the copies' sums meet at
+// the piece's end.  MT = 2: scores of half a key tile at a time, so that two of them per row
+// tile fit; a thread of its own issues each row tile's products, since a thread takes
+// hundreds of cycles from one product to the next.
 //
 // Tensor memory (512 columns): MT = 1: S at 0 and 128, O at 256 and 384, by tile and by piece
-// in turn; MT = 2: S_A, S_B, O_A, O_B.
+// in turn; MT = 2: S_A at 0 and 64, S_B at 128 and 192, O_A, O_B.
 //
 // Only tiles that reach into the tree are masked, by the bits of each row's node and of
 // those above it.  Their V rows are looked over before the product: a weight of zero does
@@ -59,9 +59,10 @@ struct Layout {
     static constexpr int kQBufs = MT == 1 ? 2 : 1;  // of MT tiles
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kBars = kRing + kSlots * kTileBytes;
+    static constexpr int kKeys = 128 / MT;          // of a score tile; MT = 2: half a key tile
     static constexpr int kSoftmax = 128 * MT;       // threads
-    static constexpr int kCopyWarp = 4 * MT, kMmaWarp = kCopyWarp + 1, kQWarp = kCopyWarp + 2;
-    static constexpr int kThreads = kSoftmax + 96;
+    static constexpr int kCopyWarp = 4 * MT, kQWarp = kCopyWarp + 1, kMmaWarp = kCopyWarp + 2;  // one per row tile
+    static constexpr int kThreads = kSoftmax + 64 + 32 * MT;
 };
 
 // Where 16-byte part c of a row lies in its tile.
@@ -74,9 +75,10 @@ template <int D, int MT>
 struct Shared {
     uint64_t full[Layout<D, MT>::kSlots], empty[Layout<D, MT>::kSlots];
     uint64_t qfull[2], qempty[2];
-    uint64_t sfull[2], pfull[2];   // MT = 1: by tile in turn; MT = 2: of a row tile
-    uint64_t odone[2];             // a phase per key tile; MT = 2: of a row tile
+    uint64_t sfull[MT][2], pfull[MT][2];  // of a row tile: by score tile in turn
+    uint64_t odone[MT][2];         // as sfull: the product of those weights and V is done
     uint64_t oempty[2];            // MT = 1: by piece in turn; MT = 2: of a row tile
+    uint64_t vclean[8];            // MT = 2: by score tile that reaches into the tree, in turn
     uint64_t done;
     uint32_t tmem;
     int abort;
@@ -157,7 +159,7 @@ KV_DEVICE void split(float2 e, uint32_t &hi, uint32_t &lo) {
     lo = F16 ? tc::pack_f16x2(rest.x, rest.y) : tc::pack_bf16x2(rest.x, rest.y);
 }
 
-// D (+)= P B over 128 keys: P at p_tmem in steps of 16 keys, 8 columns each, two steps of every
+// D (+)= P B over 64 keys: P at p_tmem in steps of 16 keys, 8 columns each, two steps of every
 // 32 columns; B (V, MN-major) advances by `step` 16-byte units per 16 keys.
 KV_DEVICE void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc_first,
                       uint32_t step) {
@@ -171,14 +173,6 @@ KV_DEVICE void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t b_lo, uint32_t 
         "add.u32 x, %1, 32;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
         "add.u32 x, %1, 40;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 64;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 72;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 96;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 104;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t}" ::"r"(d_tmem),
         "r"(p_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc_first), "r"(step)
         : "memory");
@@ -291,19 +285,22 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < L::kSlots; ++s) {
             mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], 1);
+            mbar_init(&sm.empty[s], MT);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.qfull[s], 1);
-            // MT = 2: the last S, and each softmax warp once it has read what the piece is
-            mbar_init(&sm.qempty[s], MT == 1 ? 4 : 1 + 8);
-            mbar_init(&sm.sfull[s], 1);
-            mbar_init(&sm.pfull[s], 4);
-            mbar_init(&sm.odone[s], 1);
+            // MT = 2: each row tile's last S, and each softmax warp once it has read what the piece is
+            mbar_init(&sm.qempty[s], MT == 1 ? 4 : 2 + 8);
+            for (int x = 0; x < MT; ++x) {
+                mbar_init(&sm.sfull[x][s], 1);
+                mbar_init(&sm.pfull[x][s], 4);
+                mbar_init(&sm.odone[x][s], 1);
+            }
             mbar_init(&sm.oempty[s], 4);
             sm.nonfinite[s] = -1;
         }
-        mbar_init(&sm.done, 1);
+        for (int s = 0; s < 8; ++s) mbar_init(&sm.vclean[s], 4);
+        mbar_init(&sm.done, MT);
         sm.abort = 0;
         mbar_init_fence();
     }
@@ -425,11 +422,11 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             for (int i = max(0, copied + (ok ? 1 : 0) - L::kQBufs); i < copied; ++i)
                 mbar_wait_drain(&sm.qfull[i % L::kQBufs], (i / L::kQBufs) & 1, p.err);
         if (!ok && lane == 0) *abort_flag = 1;
-    } else if (warp == L::kMmaWarp) {
+    } else if (warp >= L::kMmaWarp) {
         // ================================================== products
         if (lane == 0) {
-            constexpr uint32_t idesc_qk = F16 ? tc::idesc_f16_f32(128, 128, false, false)
-                                              : tc::idesc_bf16_f32(128, 128, false, false);
+            constexpr uint32_t idesc_qk = F16 ? tc::idesc_f16_f32(128, L::kKeys, false, false)
+                                              : tc::idesc_bf16_f32(128, L::kKeys, false, false);
             constexpr uint32_t idesc_pv = F16 ? tc::idesc_f16_f32(128, D, false, true)
                                               : tc::idesc_bf16_f32(128, D, false, true);
             const uint32_t d_hi = tc::smem_desc_sw128_hi(L::kGroupBytes);
@@ -437,17 +434,22 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             const uint32_t q_lo = tc::smem_desc_sw128_lo(smem_addr(sQ), 16);
             const uint32_t k_lo = tc::smem_desc_sw128_lo(smem_addr(ring), 16);
             const uint32_t v_lo = tc::smem_desc_sw128_lo(smem_addr(ring), 1024);  // (the other 64 dimensions)
-            auto issue_s = [&](uint32_t col, int q_tile, int slot) {
-                const uint32_t a = q_lo + ((q_tile * L::kTileBytes) >> 4), b = k_lo + ((slot * L::kTileBytes) >> 4);
+            // `half` (MT = 2): which 64 keys of the key tile
+            auto issue_s = [&](uint32_t col, int q_tile, int slot, int half) {
+                const uint32_t a = q_lo + ((q_tile * L::kTileBytes) >> 4);
+                const uint32_t b = k_lo + ((slot * L::kTileBytes + half * (L::kTileBytes / 2)) >> 4);
 #pragma unroll
                 for (int h = 0; h < L::kHalves; ++h)
                     mma_ss_k64(tmem + col, a + 1024 * h, q_hi, b + 64 * h, d_hi, idesc_qk, h);
             };
-            auto issue_pv = [&](uint32_t col_o, uint32_t col_p, int slot, bool first) {
-                const uint32_t b = v_lo + ((slot * L::kTileBytes) >> 4);
+            auto issue_pv = [&](uint32_t col_o, uint32_t col_p, int slot, int half, bool first) {
+                const uint32_t b = v_lo + ((slot * L::kTileBytes + half * (L::kTileBytes / 2)) >> 4);
                 constexpr uint32_t step = 2 * L::kGroupBytes / 16;
-                mma_pv(tmem + col_o, tmem + col_p, b, d_hi, idesc_pv, !first, step);
-                mma_pv(tmem + col_o, tmem + col_p + 16, b, d_hi, idesc_pv, 1, step);
+#pragma unroll
+                for (int i = 0; i < L::kKeys / 64; ++i) {
+                    mma_pv(tmem + col_o, tmem + col_p + 64 * i, b + 4 * step * i, d_hi, idesc_pv, i || !first, step);
+                    mma_pv(tmem + col_o, tmem + col_p + 64 * i + 16, b + 4 * step * i, d_hi, idesc_pv, 1, step);
+                }
             };
             bool ok = true;
             // tile t of the run: K in ring position 2 t, V in 2 t + 1
@@ -473,8 +475,8 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                     if (!wait_full(2 * s)) return false;
                     tc::fence_after_sync();
-                    issue_s((s & 1) * 128, sn & 1, (int)(2 * s % L::kSlots));
-                    tc::mma_commit(&sm.sfull[s & 1]);
+                    issue_s((s & 1) * 128, sn & 1, (int)(2 * s % L::kSlots), 0);
+                    tc::mma_commit(&sm.sfull[0][s & 1]);
                     tc::mma_commit(&sm.empty[2 * s % L::kSlots]);
                     --s_left;
                     ++s;
@@ -488,14 +490,14 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     // (the weights last: between their arrival and their product nothing is left to do)
                     const int slot = (int)((2 * t + 1) % L::kSlots);
                     if ((first && n >= 2 && !mbar_wait<TW>(&sm.oempty[n & 1], ((n >> 1) - 1) & 1, p.err)) ||
-                        !wait_full(2 * t + 1) || !mbar_wait<TW>(&sm.pfull[t & 1], (t >> 1) & 1, p.err)) {
+                        !wait_full(2 * t + 1) || !mbar_wait<TW>(&sm.pfull[0][t & 1], (t >> 1) & 1, p.err)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
-                    issue_pv(kColO0 + 128 * (n & 1), (t & 1) * 128, slot, first);
+                    issue_pv(kColO0 + 128 * (n & 1), (t & 1) * 128, slot, 0, first);
                     tc::mma_commit(&sm.empty[slot]);
-                    tc::mma_commit(&sm.odone[0]);
+                    tc::mma_commit(&sm.odone[0][t & 1]);
                     ++t;
                     first = --t_left == 0;
                     if (first) {
@@ -504,55 +506,61 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                 }
             } else {
-                unsigned t = 0;
-                int n = 0, used[2] = {0, 0};  // pieces, and tiles of each row tile, so far
-                int pieces_of[2] = {0, 0};
-                while (ok) {
-                    ok = mbar_wait<TW>(&sm.qfull[0], n & 1, p.err);
-                    if (!ok) break;
+                // A thread per row tile; S(u + 1) is issued before PV(u) is, S(u + 2) behind it.
+                const int x = warp - L::kMmaWarp;
+                unsigned t = 0, u = 0;       // key tiles of the run so far; score tiles of the row tile
+                unsigned dirty = 0;          // score tiles of the run so far that reached into a tree
+                int worked = 0;              // pieces of the row tile
+                for (int n = 0; ok; ++n) {
+                    if (!(ok = mbar_wait<TW>(&sm.qfull[0], n & 1, p.err))) break;
                     const Piece pc = sm.piece[0];
-                    const int row_tiles = Rows(p, pc).nodes > p.plan.tile_nodes ? 2 : 1;
-                    const int tiles = pc.t1 - pc.t0;
+                    const int tiles = pc.t1 - pc.t0, all = 2 * tiles;
                     if (tiles == 0) break;
-                    ok = wait_full(2 * t);
-                    if (!ok) break;
+                    const Rows r(p, pc);
+                    const int clean = max(0, (r.before - pc.t0 * kTile) / L::kKeys);  // score tiles before the tree's
+                    if (x == 1 && r.nodes <= p.plan.tile_nodes) {
+                        mbar_arrive(&sm.qempty[0]);
+                        for (int i = 0; i < all; ++i) {
+                            if (!(ok = wait_full(2 * t + i))) break;
+                            mbar_arrive(&sm.empty[(2 * t + i) % L::kSlots]);
+                        }
+                        t += tiles;
+                        dirty += max(0, all - clean);
+                        continue;
+                    }
+                    auto next_s = [&](int j, unsigned s) {  // score tile j of the piece, s of the row tile
+                        const int slot = (int)((2 * (t + (j >> 1))) % L::kSlots);
+                        issue_s(128 * x + 64 * (s & 1), x, slot, j & 1);
+                        tc::mma_commit(&sm.sfull[x][s & 1]);
+                        if (j & 1) tc::mma_commit(&sm.empty[slot]);
+                        if (j + 1 == all) tc::mma_commit(&sm.qempty[0]);
+                    };
+                    if (!(ok = wait_full(2 * t))) break;
                     tc::fence_after_sync();
-                    for (int x = 0; x < row_tiles; ++x) {
-                        issue_s(128 * x, x, (int)(2 * t % L::kSlots));
-                        tc::mma_commit(&sm.sfull[x]);
-                    }
-                    tc::mma_commit(&sm.empty[2 * t % L::kSlots]);
-                    if (tiles == 1) tc::mma_commit(&sm.qempty[0]);
-                    for (int j = 0; ok && j < tiles; ++j, ++t) {
+                    next_s(0, u);
+                    next_s(1, u + 1);
+                    for (int j = 0; j < all; ++j, ++u) {
                         // (the weights last: between their arrival and their product nothing is left to do)
-                        const int vslot = (int)((2 * t + 1) % L::kSlots), kslot = (int)((2 * t + 2) % L::kSlots);
-                        const bool more = j + 1 < tiles;
-                        ok = wait_full(2 * t + 1) && (!more || wait_full(2 * t + 2));
-                        for (int x = 0; ok && x < row_tiles; ++x) {
-                            if ((j == 0 && pieces_of[x] > 0 &&
-                                 !mbar_wait<TW>(&sm.oempty[x], (pieces_of[x] - 1) & 1, p.err)) ||
-                                !mbar_wait<TW>(&sm.pfull[x], used[x] & 1, p.err)) {
-                                ok = false;
-                                break;
-                            }
-                            tc::fence_after_sync();
-                            issue_pv(kColO0 + 128 * x, 128 * x, vslot, j == 0);
-                            tc::mma_commit(&sm.odone[x]);
-                            if (more) {
-                                issue_s(128 * x, x, kslot);
-                                tc::mma_commit(&sm.sfull[x]);
-                            }
-                            ++used[x];
+                        const int slot = (int)((2 * (t + (j >> 1)) + 1) % L::kSlots);
+                        if ((j & 1) == 0)
+                            ok = wait_full(2 * (t + (j >> 1)) + 1) && (j + 2 >= all || wait_full(2 * (t + (j >> 1)) + 2)) &&
+                                 (j > 0 || worked == 0 || mbar_wait<TW>(&sm.oempty[x], (worked - 1) & 1, p.err));
+                        if (ok && j >= clean) {
+                            ok = mbar_wait<TW>(&sm.vclean[dirty & 7], (dirty >> 3) & 1, p.err);
+                            ++dirty;
                         }
-                        if (!ok) break;
-                        tc::mma_commit(&sm.empty[vslot]);
-                        if (more) {
-                            tc::mma_commit(&sm.empty[kslot]);
-                            if (j + 2 == tiles) tc::mma_commit(&sm.qempty[0]);
+                        if (!ok || !mbar_wait<TW>(&sm.pfull[x][u & 1], (u >> 1) & 1, p.err)) {
+                            ok = false;
+                            break;
                         }
+                        tc::fence_after_sync();
+                        issue_pv(kColO0 + 128 * x, 128 * x + 64 * (u & 1), slot, j & 1, j == 0);
+                        tc::mma_commit(&sm.odone[x][u & 1]);
+                        if (j & 1) tc::mma_commit(&sm.empty[slot]);
+                        if (j + 2 < all) next_s(j + 2, u + 2);
                     }
-                    for (int x = 0; x < row_tiles; ++x) ++pieces_of[x];
-                    ++n;
+                    t += tiles;
+                    ++worked;
                 }
             }
             tc::mma_commit(&sm.done);
@@ -569,9 +577,10 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         const int copy = MT == 1 ? lane_row / per_copy : 0;
         const int row = lane_row - copy * per_copy;
         const int row_node = row / p.g, row_head = row - row_node * p.g;
-        const int chunks = 4 / p.copies, c0 = copy * chunks, c1 = c0 + chunks;  // of 32 keys of a tile, this copy's
-        unsigned t = 0;      // tiles of this row tile so far (MT = 1: of the run)
-        unsigned run_t = 0;  // tiles of the run so far
+        const int chunks = L::kKeys / 32 / p.copies, c0 = copy * chunks, c1 = c0 + chunks;  // of 32 keys, this copy's
+        unsigned t = 0;      // score tiles of this row tile so far
+        unsigned run_t = 0;  // key tiles of the run so far
+        unsigned dirty = 0;  // MT = 2: score tiles of the run so far that reached into a tree
         int n = 0;           // pieces
         bool ok = true;
         while (true) {
@@ -592,7 +601,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             if (MT == 2 && tiles > 0 && x == 1 && r.nodes <= p.plan.tile_nodes) {
                 run_t += tiles;
                 ++n;
-                continue;
+                continue;  // (the tree's rows of V are the first row tile's work)
             }
             const int at_node = x * p.plan.tile_nodes + row_node;  // of the group
             const bool valid = tiles > 0 && row_node < p.plan.tile_nodes && at_node < r.nodes;
@@ -601,20 +610,20 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             Ancestors anc;
             if (!idle && pc.t1 * kTile > r.before) anc.walk(parents, node);
             float m_used = -INFINITY, l_sum = 0.f;
-            for (int j = 0; j < tiles; ++j, ++t, ++run_t) {
-                const int buf = MT == 1 ? (int)(t & 1) : x;
-                const uint32_t phase = MT == 1 ? (t >> 1) & 1 : t & 1;
+            for (int j = 0; j < tiles * MT; ++j, ++t, run_t += MT == 1 || (j & 1) == 0) {
+                const int buf = (int)(t & 1);
                 bool bad = *abort_flag != 0;
-                if (!bad) bad = !mbar_wait<TW>(&sm.sfull[buf], phase, p.err);
+                if (!bad) bad = !mbar_wait<TW>(&sm.sfull[x][buf], (t >> 1) & 1, p.err);
                 if (__any_sync(0xffffffffu, bad)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
-                const int key0 = (pc.t0 + j) * kTile;
-                const bool tail = key0 + kTile > r.before;
-                const uint32_t gone = sm.gone[run_t & 7];
-                const uint32_t scol = tmem + lane_base + 128 * buf;
+                const int half = MT == 1 ? 0 : j & 1;
+                const int key0 = pc.t0 * kTile + j * L::kKeys;
+                const bool tail = key0 + L::kKeys > r.before;
+                const uint32_t gone = (sm.gone[run_t & 7] >> (4 * half)) & (MT == 1 ? 255u : 15u);
+                const uint32_t scol = tmem + lane_base + 128 * x + L::kKeys * buf;
                 bool rescale = false;
                 float alpha = 1.f;
                 if (!idle) {
@@ -639,8 +648,8 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     // Scores are read twice, for the maximum (which tensor memory finds) and for the weights,
                     // 32 at a time: all of them in registers at once would unroll into more code than
                     // the instruction caches next to the schedulers hold.
-                    float mrow = chunks == 1 ? tmem_max<32>(scol + 32 * c0) : tmem_max<64>(scol + 32 * c0);
-                    if (chunks == 4) mrow = fmaxf(mrow, tmem_max<64>(scol + 64));
+                    float mrow = MT == 1 && chunks == 1 ? tmem_max<32>(scol + 32 * c0) : tmem_max<64>(scol + 32 * c0);
+                    if (MT == 1 && chunks == 4) mrow = fmaxf(mrow, tmem_max<64>(scol + 64));
                     mrow *= p.scale_log2;  // scale > 0
                     uint32_t va[32], vb[32];
                     tc::tmem_ld32(scol + 32 * c0, va);
@@ -679,7 +688,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         tc::tmem_wait_ld();
                     }
                     l_sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-                    if (chunks < 4) {  // the other copies' keys
+                    if (MT == 1 && chunks < 4) {  // the other copies' keys
                         uint32_t zero[32];
 #pragma unroll
                         for (int k = 0; k < 32; ++k) zero[k] = 0;
@@ -689,7 +698,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                     if (__any_sync(0xffffffffu, rescale)) {
                         // O holds the products up to the tile before once that one's are done
-                        if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.odone[x], (t - 1) & 1, p.err))) {
+                        if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.odone[x][buf ^ 1], ((t - 1) >> 1) & 1, p.err))) {
                             ok = false;
                             break;
                         }
@@ -714,10 +723,10 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         break;
                     }
                     char *vt = ring + (int)(pos % L::kSlots) * L::kTileBytes;
-                    const int row0 = max(0, r.before - key0);
+                    const int row0 = 64 * half + max(0, r.before - key0);
                     constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
 #pragma unroll 2
-                    for (int i = row0 * (D / 8) + tid; i < 128 * (D / 8); i += 128) {
+                    for (int i = row0 * (D / 8) + tid; i < (64 * half + L::kKeys) * (D / 8); i += 128) {
                         const int at_row = i / (D / 8);
                         uint4 *at4 = reinterpret_cast<uint4 *>(vt + tile_offset<D>(at_row, i % (D / 8)));
                         const uint4 v = *at4;
@@ -728,24 +737,26 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                             if ((y[k] & top) == top) y[k] &= 0xffff0000u, here = true;
                             if ((y[k] >> 16 & top) == top) y[k] &= 0x0000ffffu, here = true;
                         }
-                        if (key0 + at_row >= pc.seq.len)
+                        if (key0 - 64 * half + at_row >= pc.seq.len)
                             *at4 = make_uint4(0u, 0u, 0u, 0u);
                         else if (here)
                             *at4 = make_uint4(y[0], y[1], y[2], y[3]), sm.nonfinite[n & 1] = n;
                     }
                     tc::fence_proxy_async_smem();  // before the tensor core reads them
+                    if constexpr (MT == 2) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.vclean[dirty & 7]);
+                        ++dirty;
+                    }
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.pfull[buf]);
+                if (lane == 0) mbar_arrive(&sm.pfull[x][buf]);
             }
             // ---- the piece's end
             if (ok && tiles > 0) {
-                // (MT = 1: the last S says that the products up to three tiles back are done, so
-                // the wait for the last one's phase comes after that for the one before it)
-                bool bad = MT == 1 && t >= 2 && !mbar_wait<TW>(&sm.odone[x], t & 1, p.err);
-                bad = bad || !mbar_wait<TW>(&sm.odone[x], (t - 1) & 1, p.err);
+                const bool bad = !mbar_wait<TW>(&sm.odone[x][(t - 1) & 1], ((t - 1) >> 1) & 1, p.err);
                 ok = !__any_sync(0xffffffffu, bad);
             }
             // MT = 1: all warps stay or leave together; they meet once for every piece and for the end
