@@ -13,18 +13,18 @@
 // tiles into one ring by TMA (each block-table entry becomes one box), a thread per row tile
 // that issues its products, a warp that describes the next piece and copies its queries.  The ring runs on across pieces.
 //
-// S is double-buffered, so the next tile's scores are computed while the softmax warps work
-// on this one's.  MT = 1: Q and O are too, so a piece's end overlaps the next piece's
-// beginning.  A tile that a call's largest group does not fill is filled with copies of its
-// rows (two of up to 64 rows, four of up to 32): the tensor core computes all of S at the same
-// cost, and each copy's warps take their own keys of the tile and leave zeros as the others'
-// weights, so that all four schedulers share the exponentials; the copies' sums meet at
-// the piece's end.  MT = 2: scores of half a key tile at a time, so that two of them per row
-// tile fit; a thread of its own issues each row tile's products, since a thread takes
-// hundreds of cycles from one product to the next.
+// MT = 1: S is double-buffered, so the next tile's scores are computed while the softmax warps
+// work on this one's; Q and O are too, so a piece's end overlaps the next piece's beginning.
+// A tile that a call's largest group does not fill is filled with copies of its rows (two
+// of up to 64 rows, four of up to 32): the tensor core computes all of S at the same cost, and
+// each copy's warps take their own keys of the tile and leave zeros as the others' weights,
+// so that all four schedulers share the exponentials; the copies' sums meet at the piece's
+// end.  MT = 2: each row tile has one S and one O, and works while the other's products run; a
+// thread of its own issues each row tile's products, since a thread takes hundreds of cycles
+// from one wait to the next, and the product of half the weights begins while the other half is made.
 //
 // Tensor memory (512 columns): MT = 1: S at 0 and 128, O at 256 and 384, by tile and by piece
-// in turn; MT = 2: S_A at 0 and 64, S_B at 128 and 192, O_A, O_B.
+// in turn; MT = 2: S_A, S_B, O_A, O_B.
 //
 // Only tiles that reach into the tree are masked, by the bits of each row's node and of
 // those above it.  Their V rows are looked over before the product: a weight of zero does
@@ -59,7 +59,6 @@ struct Layout {
     static constexpr int kQBufs = MT == 1 ? 2 : 1;  // of MT tiles
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kBars = kRing + kSlots * kTileBytes;
-    static constexpr int kKeys = 128 / MT;          // of a score tile; MT = 2: half a key tile
     static constexpr int kSoftmax = 128 * MT;       // threads
     static constexpr int kCopyWarp = 4 * MT, kQWarp = kCopyWarp + 1, kMmaWarp = kCopyWarp + 2;  // one per row tile
     static constexpr int kThreads = kSoftmax + 64 + 32 * MT;
@@ -75,10 +74,11 @@ template <int D, int MT>
 struct Shared {
     uint64_t full[Layout<D, MT>::kSlots], empty[Layout<D, MT>::kSlots];
     uint64_t qfull[2], qempty[2];
-    uint64_t sfull[MT][2], pfull[MT][2];  // of a row tile: by score tile in turn
-    uint64_t odone[MT][2];         // as sfull: the product of those weights and V is done
+    uint64_t sfull[2];             // MT = 1: by tile in turn; MT = 2: of a row tile
+    uint64_t pfull[MT][2];         // MT = 1: by tile in turn; MT = 2: of a row tile, half the keys each
+    uint64_t odone[MT][2];         // of a row tile, by tile in turn: the product of its weights and V is done
     uint64_t oempty[2];            // MT = 1: by piece in turn; MT = 2: of a row tile
-    uint64_t vclean[8];            // MT = 2: by score tile that reaches into the tree, in turn
+    uint64_t vclean[8];            // MT = 2: by key tile that reaches into the tree, in turn
     uint64_t done;
     uint32_t tmem;
     int abort;
@@ -292,10 +292,10 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             // MT = 2: each row tile's last S, and each softmax warp once it has read what the piece is
             mbar_init(&sm.qempty[s], MT == 1 ? 4 : 2 + 8);
             for (int x = 0; x < MT; ++x) {
-                mbar_init(&sm.sfull[x][s], 1);
                 mbar_init(&sm.pfull[x][s], 4);
                 mbar_init(&sm.odone[x][s], 1);
             }
+            mbar_init(&sm.sfull[s], 1);
             mbar_init(&sm.oempty[s], 4);
             sm.nonfinite[s] = -1;
         }
@@ -425,8 +425,8 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
     } else if (warp >= L::kMmaWarp) {
         // ================================================== products
         if (lane == 0) {
-            constexpr uint32_t idesc_qk = F16 ? tc::idesc_f16_f32(128, L::kKeys, false, false)
-                                              : tc::idesc_bf16_f32(128, L::kKeys, false, false);
+            constexpr uint32_t idesc_qk = F16 ? tc::idesc_f16_f32(128, 128, false, false)
+                                              : tc::idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t idesc_pv = F16 ? tc::idesc_f16_f32(128, D, false, true)
                                               : tc::idesc_bf16_f32(128, D, false, true);
             const uint32_t d_hi = tc::smem_desc_sw128_hi(L::kGroupBytes);
@@ -434,22 +434,17 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             const uint32_t q_lo = tc::smem_desc_sw128_lo(smem_addr(sQ), 16);
             const uint32_t k_lo = tc::smem_desc_sw128_lo(smem_addr(ring), 16);
             const uint32_t v_lo = tc::smem_desc_sw128_lo(smem_addr(ring), 1024);  // (the other 64 dimensions)
-            // `half` (MT = 2): which 64 keys of the key tile
-            auto issue_s = [&](uint32_t col, int q_tile, int slot, int half) {
-                const uint32_t a = q_lo + ((q_tile * L::kTileBytes) >> 4);
-                const uint32_t b = k_lo + ((slot * L::kTileBytes + half * (L::kTileBytes / 2)) >> 4);
+            auto issue_s = [&](uint32_t col, int q_tile, int slot) {
+                const uint32_t a = q_lo + ((q_tile * L::kTileBytes) >> 4), b = k_lo + ((slot * L::kTileBytes) >> 4);
 #pragma unroll
                 for (int h = 0; h < L::kHalves; ++h)
                     mma_ss_k64(tmem + col, a + 1024 * h, q_hi, b + 64 * h, d_hi, idesc_qk, h);
             };
-            auto issue_pv = [&](uint32_t col_o, uint32_t col_p, int slot, int half, bool first) {
-                const uint32_t b = v_lo + ((slot * L::kTileBytes + half * (L::kTileBytes / 2)) >> 4);
+            auto issue_pv = [&](uint32_t col_o, uint32_t col_p, int slot, int half, bool first) {  // 64 keys
                 constexpr uint32_t step = 2 * L::kGroupBytes / 16;
-#pragma unroll
-                for (int i = 0; i < L::kKeys / 64; ++i) {
-                    mma_pv(tmem + col_o, tmem + col_p + 64 * i, b + 4 * step * i, d_hi, idesc_pv, i || !first, step);
-                    mma_pv(tmem + col_o, tmem + col_p + 64 * i + 16, b + 4 * step * i, d_hi, idesc_pv, 1, step);
-                }
+                const uint32_t b = v_lo + ((slot * L::kTileBytes) >> 4) + 4 * step * half;
+                mma_pv(tmem + col_o, tmem + col_p + 64 * half, b, d_hi, idesc_pv, !first, step);
+                mma_pv(tmem + col_o, tmem + col_p + 64 * half + 16, b, d_hi, idesc_pv, 1, step);
             };
             bool ok = true;
             // tile t of the run: K in ring position 2 t, V in 2 t + 1
@@ -475,8 +470,8 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                     if (!wait_full(2 * s)) return false;
                     tc::fence_after_sync();
-                    issue_s((s & 1) * 128, sn & 1, (int)(2 * s % L::kSlots), 0);
-                    tc::mma_commit(&sm.sfull[0][s & 1]);
+                    issue_s((s & 1) * 128, sn & 1, (int)(2 * s % L::kSlots));
+                    tc::mma_commit(&sm.sfull[s & 1]);
                     tc::mma_commit(&sm.empty[2 * s % L::kSlots]);
                     --s_left;
                     ++s;
@@ -496,6 +491,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                     tc::fence_after_sync();
                     issue_pv(kColO0 + 128 * (n & 1), (t & 1) * 128, slot, 0, first);
+                    issue_pv(kColO0 + 128 * (n & 1), (t & 1) * 128, slot, 1, false);
                     tc::mma_commit(&sm.empty[slot]);
                     tc::mma_commit(&sm.odone[0][t & 1]);
                     ++t;
@@ -506,58 +502,57 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                 }
             } else {
-                // A thread per row tile; S(u + 1) is issued before PV(u) is, S(u + 2) behind it.
+                // A thread per row tile; the product of the first half of a tile's weights begins
+                // while the other half is weighed.
                 const int x = warp - L::kMmaWarp;
-                unsigned t = 0, u = 0;       // key tiles of the run so far; score tiles of the row tile
-                unsigned dirty = 0;          // score tiles of the run so far that reached into a tree
+                unsigned t = 0, u = 0;       // key tiles of the run so far, and of the row tile
+                unsigned dirty = 0;          // key tiles of the run so far that reached into a tree
                 int worked = 0;              // pieces of the row tile
                 for (int n = 0; ok; ++n) {
                     if (!(ok = mbar_wait<TW>(&sm.qfull[0], n & 1, p.err))) break;
                     const Piece pc = sm.piece[0];
-                    const int tiles = pc.t1 - pc.t0, all = 2 * tiles;
+                    const int tiles = pc.t1 - pc.t0;
                     if (tiles == 0) break;
                     const Rows r(p, pc);
-                    const int clean = max(0, (r.before - pc.t0 * kTile) / L::kKeys);  // score tiles before the tree's
+                    const int clean = max(0, r.before / kTile - pc.t0);  // key tiles before the tree's
                     if (x == 1 && r.nodes <= p.plan.tile_nodes) {
                         mbar_arrive(&sm.qempty[0]);
-                        for (int i = 0; i < all; ++i) {
+                        for (int i = 0; i < 2 * tiles; ++i) {
                             if (!(ok = wait_full(2 * t + i))) break;
                             mbar_arrive(&sm.empty[(2 * t + i) % L::kSlots]);
                         }
                         t += tiles;
-                        dirty += max(0, all - clean);
+                        dirty += max(0, tiles - clean);
                         continue;
                     }
-                    auto next_s = [&](int j, unsigned s) {  // score tile j of the piece, s of the row tile
-                        const int slot = (int)((2 * (t + (j >> 1))) % L::kSlots);
-                        issue_s(128 * x + 64 * (s & 1), x, slot, j & 1);
-                        tc::mma_commit(&sm.sfull[x][s & 1]);
-                        if (j & 1) tc::mma_commit(&sm.empty[slot]);
-                        if (j + 1 == all) tc::mma_commit(&sm.qempty[0]);
+                    auto next_s = [&](int j) {  // tile j of the piece
+                        const int slot = (int)(2 * (t + j) % L::kSlots);
+                        issue_s(128 * x, x, slot);
+                        tc::mma_commit(&sm.sfull[x]);
+                        tc::mma_commit(&sm.empty[slot]);
+                        if (j + 1 == tiles) tc::mma_commit(&sm.qempty[0]);
                     };
                     if (!(ok = wait_full(2 * t))) break;
                     tc::fence_after_sync();
-                    next_s(0, u);
-                    next_s(1, u + 1);
-                    for (int j = 0; j < all; ++j, ++u) {
+                    next_s(0);
+                    for (int j = 0; j < tiles; ++j, ++u) {
                         // (the weights last: between their arrival and their product nothing is left to do)
-                        const int slot = (int)((2 * (t + (j >> 1)) + 1) % L::kSlots);
-                        if ((j & 1) == 0)
-                            ok = wait_full(2 * (t + (j >> 1)) + 1) && (j + 2 >= all || wait_full(2 * (t + (j >> 1)) + 2)) &&
-                                 (j > 0 || worked == 0 || mbar_wait<TW>(&sm.oempty[x], (worked - 1) & 1, p.err));
+                        const int slot = (int)((2 * (t + j) + 1) % L::kSlots);
+                        ok = wait_full(2 * (t + j) + 1) && (j + 1 == tiles || wait_full(2 * (t + j) + 2)) &&
+                             (j > 0 || worked == 0 || mbar_wait<TW>(&sm.oempty[x], (worked - 1) & 1, p.err));
                         if (ok && j >= clean) {
                             ok = mbar_wait<TW>(&sm.vclean[dirty & 7], (dirty >> 3) & 1, p.err);
                             ++dirty;
                         }
-                        if (!ok || !mbar_wait<TW>(&sm.pfull[x][u & 1], (u >> 1) & 1, p.err)) {
-                            ok = false;
-                            break;
+                        for (int half = 0; ok && half < 2; ++half) {
+                            if (!(ok = mbar_wait<TW>(&sm.pfull[x][half], u & 1, p.err))) break;
+                            tc::fence_after_sync();
+                            issue_pv(kColO0 + 128 * x, 128 * x, slot, half, j == 0 && half == 0);
                         }
-                        tc::fence_after_sync();
-                        issue_pv(kColO0 + 128 * x, 128 * x + 64 * (u & 1), slot, j & 1, j == 0);
+                        if (!ok) break;
+                        if (j + 1 < tiles) next_s(j + 1);
                         tc::mma_commit(&sm.odone[x][u & 1]);
-                        if (j & 1) tc::mma_commit(&sm.empty[slot]);
-                        if (j + 2 < all) next_s(j + 2, u + 2);
+                        tc::mma_commit(&sm.empty[slot]);
                     }
                     t += tiles;
                     ++worked;
@@ -577,10 +572,10 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         const int copy = MT == 1 ? lane_row / per_copy : 0;
         const int row = lane_row - copy * per_copy;
         const int row_node = row / p.g, row_head = row - row_node * p.g;
-        const int chunks = L::kKeys / 32 / p.copies, c0 = copy * chunks, c1 = c0 + chunks;  // of 32 keys, this copy's
-        unsigned t = 0;      // score tiles of this row tile so far
+        const int chunks = 4 / p.copies, c0 = copy * chunks, c1 = c0 + chunks;  // of 32 keys, this copy's
+        unsigned t = 0;      // key tiles of this row tile so far
         unsigned run_t = 0;  // key tiles of the run so far
-        unsigned dirty = 0;  // MT = 2: score tiles of the run so far that reached into a tree
+        unsigned dirty = 0;  // MT = 2: key tiles of the run so far that reached into a tree
         int n = 0;           // pieces
         bool ok = true;
         while (true) {
@@ -610,22 +605,61 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             Ancestors anc;
             if (!idle && pc.t1 * kTile > r.before) anc.walk(parents, node);
             float m_used = -INFINITY, l_sum = 0.f;
-            for (int j = 0; j < tiles * MT; ++j, ++t, run_t += MT == 1 || (j & 1) == 0) {
-                const int buf = (int)(t & 1);
+            for (int j = 0; j < tiles; ++j, ++t, ++run_t) {
+                const int buf = MT == 1 ? (int)(t & 1) : x;
                 bool bad = *abort_flag != 0;
-                if (!bad) bad = !mbar_wait<TW>(&sm.sfull[x][buf], (t >> 1) & 1, p.err);
+                if (!bad) bad = !mbar_wait<TW>(&sm.sfull[buf], (MT == 1 ? t >> 1 : t) & 1, p.err);
                 if (__any_sync(0xffffffffu, bad)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
-                const int half = MT == 1 ? 0 : j & 1;
-                const int key0 = pc.t0 * kTile + j * L::kKeys;
-                const bool tail = key0 + L::kKeys > r.before;
-                const uint32_t gone = (sm.gone[run_t & 7] >> (4 * half)) & (MT == 1 ? 255u : 15u);
-                const uint32_t scol = tmem + lane_base + 128 * x + L::kKeys * buf;
+                const int key0 = (pc.t0 + j) * kTile;
+                const bool tail = key0 + kTile > r.before;
+                const uint32_t gone = sm.gone[run_t & 7];
+                const uint32_t scol = tmem + lane_base + 128 * buf;
                 bool rescale = false;
                 float alpha = 1.f;
+                auto arrive = [&](int which) {  // the weights are there
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.pfull[x][which]);
+                };
+                if (tail && x == 0) {
+                    // the rows of V that lie in the tree or behind it
+                    const unsigned pos = 2 * run_t + 1;
+                    if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1, p.err))) {
+                        ok = false;
+                        break;
+                    }
+                    char *vt = ring + (int)(pos % L::kSlots) * L::kTileBytes;
+                    const int row0 = max(0, r.before - key0);
+                    constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
+#pragma unroll 2
+                    for (int i = row0 * (D / 8) + tid; i < 128 * (D / 8); i += 128) {
+                        const int at_row = i / (D / 8);
+                        uint4 *at4 = reinterpret_cast<uint4 *>(vt + tile_offset<D>(at_row, i % (D / 8)));
+                        const uint4 v = *at4;
+                        uint32_t y[4] = {v.x, v.y, v.z, v.w};
+                        bool here = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((y[k] & top) == top) y[k] &= 0xffff0000u, here = true;
+                            if ((y[k] >> 16 & top) == top) y[k] &= 0x0000ffffu, here = true;
+                        }
+                        if (key0 + at_row >= pc.seq.len)
+                            *at4 = make_uint4(0u, 0u, 0u, 0u);
+                        else if (here)
+                            *at4 = make_uint4(y[0], y[1], y[2], y[3]), sm.nonfinite[n & 1] = n;
+                    }
+                    tc::fence_proxy_async_smem();  // before the tensor core reads them
+                    if constexpr (MT == 2) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.vclean[dirty & 7]);
+                        ++dirty;
+                    }
+                }
                 if (!idle) {
                     // Loops over chunks of 32 keys are not unrolled, and scores are read twice:
                     // the code of a tile has to stay in the instruction caches.
@@ -648,11 +682,9 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     // Scores are read twice, for the maximum (which tensor memory finds) and for the weights,
                     // 32 at a time: all of them in registers at once would unroll into more code than
                     // the instruction caches next to the schedulers hold.
-                    float mrow = MT == 1 && chunks == 1 ? tmem_max<32>(scol + 32 * c0) : tmem_max<64>(scol + 32 * c0);
-                    if (MT == 1 && chunks == 4) mrow = fmaxf(mrow, tmem_max<64>(scol + 64));
+                    float mrow = chunks == 1 ? tmem_max<32>(scol + 32 * c0) : tmem_max<64>(scol + 32 * c0);
+                    if (chunks == 4) mrow = fmaxf(mrow, tmem_max<64>(scol + 64));
                     mrow *= p.scale_log2;  // scale > 0
-                    uint32_t va[32], vb[32];
-                    tc::tmem_ld32(scol + 32 * c0, va);
                     if (m_used == -INFINITY) {
                         m_used = mrow;
                     } else if (mrow > m_used + kRenew) {
@@ -661,6 +693,26 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         l_sum *= alpha;
                         rescale = true;
                     }
+                    if (__any_sync(0xffffffffu, rescale)) {
+                        // O holds the products up to the tile before once that one's are done
+                        if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.odone[x][(t - 1) & 1], ((t - 1) >> 1) & 1, p.err))) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+                        const uint32_t ocol = tmem + lane_base + kColO0 + 128 * (MT == 1 ? n & 1 : x);
+#pragma unroll 1
+                        for (int i = 0; i < D / 16; ++i) {
+                            uint32_t v[16];
+                            tc::tmem_ld16(ocol + 16 * i, v);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                            tc::tmem_st16(ocol + 16 * i, v);
+                        }
+                    }
+                    uint32_t va[32], vb[32];
+                    tc::tmem_ld32(scol + 32 * c0, va);
                     const float ref = m_used == -INFINITY ? 0.f : m_used;
                     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-ref, -ref);
                     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -686,6 +738,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         if (c + 2 < c1) tc::tmem_ld32(scol + 32 * (c + 2), va);
                         weigh(vb, c + 1);
                         tc::tmem_wait_ld();
+                        if constexpr (MT == 2) arrive(c >> 1);
                     }
                     l_sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
                     if (MT == 1 && chunks < 4) {  // the other copies' keys
@@ -696,63 +749,13 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         for (int c = 0; c < 4; ++c)
                             if (c < c0 || c >= c1) tc::tmem_st32(scol + 32 * c, zero);
                     }
-                    if (__any_sync(0xffffffffu, rescale)) {
-                        // O holds the products up to the tile before once that one's are done
-                        if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.odone[x][buf ^ 1], ((t - 1) >> 1) & 1, p.err))) {
-                            ok = false;
-                            break;
-                        }
-                        tc::fence_after_sync();
-                        const uint32_t ocol = tmem + lane_base + kColO0 + 128 * (MT == 1 ? n & 1 : x);
-#pragma unroll 1
-                        for (int i = 0; i < D / 16; ++i) {
-                            uint32_t v[16];
-                            tc::tmem_ld16(ocol + 16 * i, v);
-                            tc::tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-                            tc::tmem_st16(ocol + 16 * i, v);
-                        }
-                    }
                 }
-                if (tail && x == 0) {
-                    // the rows of V that lie in the tree or behind it
-                    const unsigned pos = 2 * run_t + 1;
-                    if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1, p.err))) {
-                        ok = false;
-                        break;
-                    }
-                    char *vt = ring + (int)(pos % L::kSlots) * L::kTileBytes;
-                    const int row0 = 64 * half + max(0, r.before - key0);
-                    constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
-#pragma unroll 2
-                    for (int i = row0 * (D / 8) + tid; i < (64 * half + L::kKeys) * (D / 8); i += 128) {
-                        const int at_row = i / (D / 8);
-                        uint4 *at4 = reinterpret_cast<uint4 *>(vt + tile_offset<D>(at_row, i % (D / 8)));
-                        const uint4 v = *at4;
-                        uint32_t y[4] = {v.x, v.y, v.z, v.w};
-                        bool here = false;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if ((y[k] & top) == top) y[k] &= 0xffff0000u, here = true;
-                            if ((y[k] >> 16 & top) == top) y[k] &= 0x0000ffffu, here = true;
-                        }
-                        if (key0 - 64 * half + at_row >= pc.seq.len)
-                            *at4 = make_uint4(0u, 0u, 0u, 0u);
-                        else if (here)
-                            *at4 = make_uint4(y[0], y[1], y[2], y[3]), sm.nonfinite[n & 1] = n;
-                    }
-                    tc::fence_proxy_async_smem();  // before the tensor core reads them
-                    if constexpr (MT == 2) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.vclean[dirty & 7]);
-                        ++dirty;
-                    }
+                if constexpr (MT == 1) {
+                    arrive(buf);
+                } else if (idle) {
+                    arrive(0);
+                    arrive(1);
                 }
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.pfull[x][buf]);
             }
             // ---- the piece's end
             if (ok && tiles > 0) {
