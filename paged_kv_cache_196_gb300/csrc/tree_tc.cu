@@ -79,6 +79,7 @@ struct Shared {
     uint64_t odone[MT][2];         // of a row tile, by tile in turn: the product of its weights and V is done
     uint64_t oempty[2];            // MT = 1: by piece in turn; MT = 2: of a row tile
     uint64_t vclean[8];            // MT = 2: by key tile that reaches into the tree, in turn
+    uint64_t turn[2];              // MT = 2: a row tile's turn to end a key tile, by key tile of the run
     uint64_t done;
     uint32_t tmem;
     int abort;
@@ -296,6 +297,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 mbar_init(&sm.odone[x][s], 1);
             }
             mbar_init(&sm.sfull[s], 1);
+            mbar_init(&sm.turn[s], 1);
             mbar_init(&sm.oempty[s], 4);
             sm.nonfinite[s] = -1;
         }
@@ -503,7 +505,9 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 }
             } else {
                 // A thread per row tile; the product of the first half of a tile's weights begins
-                // while the other half is weighed.
+                // while the other half is weighed.  The rest of a tile's products and the next
+                // scores are issued in turn: products of both row tiles side by side would
+                // end together, and then neither's softmax would run beside the other's products.
                 const int x = warp - L::kMmaWarp;
                 unsigned t = 0, u = 0;       // key tiles of the run so far, and of the row tile
                 unsigned dirty = 0;          // key tiles of the run so far that reached into a tree
@@ -520,6 +524,10 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         for (int i = 0; i < 2 * tiles; ++i) {
                             if (!(ok = wait_full(2 * t + i))) break;
                             mbar_arrive(&sm.empty[(2 * t + i) % L::kSlots]);
+                            if (i & 1) {
+                                if (!(ok = mbar_wait<TW>(&sm.turn[1], (t + (i >> 1)) & 1, p.err))) break;
+                                mbar_arrive(&sm.turn[0]);
+                            }
                         }
                         t += tiles;
                         dirty += max(0, tiles - clean);
@@ -546,11 +554,15 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         }
                         for (int half = 0; ok && half < 2; ++half) {
                             if (!(ok = mbar_wait<TW>(&sm.pfull[x][half], u & 1, p.err))) break;
+                            if (half && (x == 1 || t + j > 0) &&
+                                !(ok = mbar_wait<TW>(&sm.turn[x], (t + j + (x == 0)) & 1, p.err)))
+                                break;
                             tc::fence_after_sync();
                             issue_pv(kColO0 + 128 * x, 128 * x, slot, half, j == 0 && half == 0);
                         }
                         if (!ok) break;
                         if (j + 1 < tiles) next_s(j + 1);
+                        mbar_arrive(&sm.turn[x ^ 1]);
                         tc::mma_commit(&sm.odone[x][u & 1]);
                         tc::mma_commit(&sm.empty[slot]);
                     }
