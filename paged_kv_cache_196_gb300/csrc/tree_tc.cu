@@ -112,6 +112,13 @@ KV_DEVICE void tma_load_4d(void *dst, const CUtensorMap *map, int group, uint64_
         : "memory");
 }
 
+// One lane of a warp, the same every time.
+KV_DEVICE bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // 32 bytes in one store where they are a sector.
 KV_DEVICE void store_sector(void *dst, const uint32_t (&y)[8], bool aligned) {
     if (aligned) {
@@ -426,7 +433,22 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         if (!ok && lane == 0) *abort_flag = 1;
     } else if (warp >= L::kMmaWarp) {
         // ================================================== products
-        if (lane == 0) {
+        // The whole warp runs this and one lane of it issues: the operands of a product lie in
+        // registers that all lanes share, and values of a single lane's branch have to be
+        // moved there one by one (90 clocks a product beside busy softmax warps, 65 this way).
+        {
+            const bool one = elect_one();
+            auto same = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };  // (tells the compiler)
+            auto commit = [&](uint64_t *bar) {
+                if (one) tc::mma_commit(bar);
+            };
+            auto arrive = [&](uint64_t *bar) {
+                __syncwarp();
+                if (one) mbar_arrive(bar);
+            };
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, mbar_wait<TW>(bar, parity, p.err));
+            };
             constexpr uint32_t idesc_qk = F16 ? tc::idesc_f16_f32(128, 128, false, false)
                                               : tc::idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t idesc_pv = F16 ? tc::idesc_f16_f32(128, D, false, true)
@@ -437,21 +459,26 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             const uint32_t k_lo = tc::smem_desc_sw128_lo(smem_addr(ring), 16);
             const uint32_t v_lo = tc::smem_desc_sw128_lo(smem_addr(ring), 1024);  // (the other 64 dimensions)
             auto issue_s = [&](uint32_t col, int q_tile, int slot) {
-                const uint32_t a = q_lo + ((q_tile * L::kTileBytes) >> 4), b = k_lo + ((slot * L::kTileBytes) >> 4);
+                const uint32_t a = same(q_lo + ((q_tile * L::kTileBytes) >> 4)), b = same(k_lo + ((slot * L::kTileBytes) >> 4));
+                const uint32_t d = same(tmem + col);
+                if (one) {
 #pragma unroll
-                for (int h = 0; h < L::kHalves; ++h)
-                    mma_ss_k64(tmem + col, a + 1024 * h, q_hi, b + 64 * h, d_hi, idesc_qk, h);
+                    for (int h = 0; h < L::kHalves; ++h) mma_ss_k64(d, a + 1024 * h, q_hi, b + 64 * h, d_hi, idesc_qk, h);
+                }
             };
             auto issue_pv = [&](uint32_t col_o, uint32_t col_p, int slot, int half, bool first) {  // 64 keys
                 constexpr uint32_t step = 2 * L::kGroupBytes / 16;
-                const uint32_t b = v_lo + ((slot * L::kTileBytes) >> 4) + 4 * step * half;
-                mma_pv(tmem + col_o, tmem + col_p + 64 * half, b, d_hi, idesc_pv, !first, step);
-                mma_pv(tmem + col_o, tmem + col_p + 64 * half + 16, b, d_hi, idesc_pv, 1, step);
+                const uint32_t b = same(v_lo + ((slot * L::kTileBytes) >> 4) + 4 * step * half);
+                const uint32_t d = same(tmem + col_o), w = same(tmem + col_p + 64 * half);
+                if (one) {
+                    mma_pv(d, w, b, d_hi, idesc_pv, !first, step);
+                    mma_pv(d, w + 16, b, d_hi, idesc_pv, 1, step);
+                }
             };
             bool ok = true;
             // tile t of the run: K in ring position 2 t, V in 2 t + 1
             auto wait_full = [&](unsigned pos) {
-                return mbar_wait<TW>(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1, p.err);
+                return wait(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1);
             };
             if constexpr (MT == 1) {
                 // S(t + 1) is issued before PV(t), across pieces too.
@@ -466,15 +493,15 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     if (s_left == 0) {
                         if (!more) return true;
                         ++sn;
-                        if (!mbar_wait<TW>(&sm.qfull[sn & 1], (sn >> 1) & 1, p.err)) return false;
+                        if (!wait(&sm.qfull[sn & 1], (sn >> 1) & 1)) return false;
                         s_left = len[sn & 1] = sm.piece[sn & 1].t1 - sm.piece[sn & 1].t0;
                         if (!(more = s_left > 0)) return true;
                     }
                     if (!wait_full(2 * s)) return false;
                     tc::fence_after_sync();
                     issue_s((s & 1) * 128, sn & 1, (int)(2 * s % L::kSlots));
-                    tc::mma_commit(&sm.sfull[s & 1]);
-                    tc::mma_commit(&sm.empty[2 * s % L::kSlots]);
+                    commit(&sm.sfull[s & 1]);
+                    commit(&sm.empty[2 * s % L::kSlots]);
                     --s_left;
                     ++s;
                     return true;
@@ -486,16 +513,16 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     if (!(ok = next_s())) break;
                     // (the weights last: between their arrival and their product nothing is left to do)
                     const int slot = (int)((2 * t + 1) % L::kSlots);
-                    if ((first && n >= 2 && !mbar_wait<TW>(&sm.oempty[n & 1], ((n >> 1) - 1) & 1, p.err)) ||
-                        !wait_full(2 * t + 1) || !mbar_wait<TW>(&sm.pfull[0][t & 1], (t >> 1) & 1, p.err)) {
+                    if ((first && n >= 2 && !wait(&sm.oempty[n & 1], ((n >> 1) - 1) & 1)) ||
+                        !wait_full(2 * t + 1) || !wait(&sm.pfull[0][t & 1], (t >> 1) & 1)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
                     issue_pv(kColO0 + 128 * (n & 1), (t & 1) * 128, slot, 0, first);
                     issue_pv(kColO0 + 128 * (n & 1), (t & 1) * 128, slot, 1, false);
-                    tc::mma_commit(&sm.empty[slot]);
-                    tc::mma_commit(&sm.odone[0][t & 1]);
+                    commit(&sm.empty[slot]);
+                    commit(&sm.odone[0][t & 1]);
                     ++t;
                     first = --t_left == 0;
                     if (first) {
@@ -513,20 +540,20 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 unsigned dirty = 0;          // key tiles of the run so far that reached into a tree
                 int worked = 0;              // pieces of the row tile
                 for (int n = 0; ok; ++n) {
-                    if (!(ok = mbar_wait<TW>(&sm.qfull[0], n & 1, p.err))) break;
+                    if (!(ok = wait(&sm.qfull[0], n & 1))) break;
                     const Piece pc = sm.piece[0];
                     const int tiles = pc.t1 - pc.t0;
                     if (tiles == 0) break;
                     const Rows r(p, pc);
                     const int clean = max(0, r.before / kTile - pc.t0);  // key tiles before the tree's
                     if (x == 1 && r.nodes <= p.plan.tile_nodes) {
-                        mbar_arrive(&sm.qempty[0]);
+                        arrive(&sm.qempty[0]);
                         for (int i = 0; i < 2 * tiles; ++i) {
                             if (!(ok = wait_full(2 * t + i))) break;
-                            mbar_arrive(&sm.empty[(2 * t + i) % L::kSlots]);
+                            arrive(&sm.empty[(2 * t + i) % L::kSlots]);
                             if (i & 1) {
-                                if (!(ok = mbar_wait<TW>(&sm.turn[1], (t + (i >> 1)) & 1, p.err))) break;
-                                mbar_arrive(&sm.turn[0]);
+                                if (!(ok = wait(&sm.turn[1], (t + (i >> 1)) & 1))) break;
+                                arrive(&sm.turn[0]);
                             }
                         }
                         t += tiles;
@@ -536,9 +563,9 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     auto next_s = [&](int j) {  // tile j of the piece
                         const int slot = (int)(2 * (t + j) % L::kSlots);
                         issue_s(128 * x, x, slot);
-                        tc::mma_commit(&sm.sfull[x]);
-                        tc::mma_commit(&sm.empty[slot]);
-                        if (j + 1 == tiles) tc::mma_commit(&sm.qempty[0]);
+                        commit(&sm.sfull[x]);
+                        commit(&sm.empty[slot]);
+                        if (j + 1 == tiles) commit(&sm.qempty[0]);
                     };
                     if (!(ok = wait_full(2 * t))) break;
                     tc::fence_after_sync();
@@ -547,30 +574,30 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         // (the weights last: between their arrival and their product nothing is left to do)
                         const int slot = (int)((2 * (t + j) + 1) % L::kSlots);
                         ok = wait_full(2 * (t + j) + 1) && (j + 1 == tiles || wait_full(2 * (t + j) + 2)) &&
-                             (j > 0 || worked == 0 || mbar_wait<TW>(&sm.oempty[x], (worked - 1) & 1, p.err));
+                             (j > 0 || worked == 0 || wait(&sm.oempty[x], (worked - 1) & 1));
                         if (ok && j >= clean) {
-                            ok = mbar_wait<TW>(&sm.vclean[dirty & 7], (dirty >> 3) & 1, p.err);
+                            ok = wait(&sm.vclean[dirty & 7], (dirty >> 3) & 1);
                             ++dirty;
                         }
                         for (int half = 0; ok && half < 2; ++half) {
-                            if (!(ok = mbar_wait<TW>(&sm.pfull[x][half], u & 1, p.err))) break;
+                            if (!(ok = wait(&sm.pfull[x][half], u & 1))) break;
                             if (half && (x == 1 || t + j > 0) &&
-                                !(ok = mbar_wait<TW>(&sm.turn[x], (t + j + (x == 0)) & 1, p.err)))
+                                !(ok = wait(&sm.turn[x], (t + j + (x == 0)) & 1)))
                                 break;
                             tc::fence_after_sync();
                             issue_pv(kColO0 + 128 * x, 128 * x, slot, half, j == 0 && half == 0);
                         }
                         if (!ok) break;
                         if (j + 1 < tiles) next_s(j + 1);
-                        mbar_arrive(&sm.turn[x ^ 1]);
-                        tc::mma_commit(&sm.odone[x][u & 1]);
-                        tc::mma_commit(&sm.empty[slot]);
+                        arrive(&sm.turn[x ^ 1]);
+                        commit(&sm.odone[x][u & 1]);
+                        commit(&sm.empty[slot]);
                     }
                     t += tiles;
                     ++worked;
                 }
             }
-            tc::mma_commit(&sm.done);
+            commit(&sm.done);
             if (!ok) *abort_flag = 1;
             // no product may still write tensor memory when it is freed
             mbar_wait_drain(&sm.done, 0, p.err);
