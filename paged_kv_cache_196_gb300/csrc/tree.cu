@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
     const int tid = threadIdx.x, ty = tid / 8, tx = tid % 8;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this kernel's end
     const Place at = place(p.plan, blockIdx.x, sm.scratch, blockIdx.x == 0 ? p.err : nullptr);
+    if (tid == 0) p.cuts[blockIdx.x] = cut_of(p.plan, at, blockIdx.x, p.g);
     Pieces pieces;
     pieces.start(p.plan, at, blockIdx.x);
     Piece pc;
@@ -191,29 +192,20 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
 // CTA x looks at the end of run x: if it lies among the tiles of a pair, the pair is cut,
 // and this CTA (with those of other y) takes one share of its rows, one share per cut.  A
 // warp takes 8 rows of 16 dimensions, so that it reads lines and writes sectors whole.
-// Launched while the attention kernel runs, so that finding the place costs nothing.
-constexpr int kMergeThreads = 256, kMergeShares = 8, kMergeAhead = 4;
+constexpr int kMergeThreads = 256, kMergeAhead = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p, int slot_rows) {
-    __shared__ PlaceScratch<kMergeThreads> scratch;
-    const int r = blockIdx.x + 1;
-    const Place at = place(p.plan, r, scratch, nullptr);
-    if (at.b >= p.plan.batch) return;
-    const Seq seq = at.seq;
-    const int cost = seq.tiles + kTreePairCost;
-    const int r0 = (int)((at.first + kTreePairCost) / at.per);  // the run that has the pair's first tile
-    const int r1 = (int)((at.first + cost - 1) / at.per);       // and the last
-    if (r <= r0 || r > r1) return;
-    const int h = at.pair / seq.groups, node0 = (at.pair - h * seq.groups) * p.plan.group_nodes;
-    const int rows = min(p.plan.group_nodes, seq.nodes - node0) * p.g;
-    const int shares = (r1 - r0) * kMergeShares, share = (r - r0 - 1) * kMergeShares + blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Cut cut = p.cuts[blockIdx.x + 1];
+    if (cut.rows == 0) return;
+    const int r0 = cut.r0, r1 = cut.r1, slot0 = cut.slot0, rows = cut.rows;
+    const int shares = (r1 - r0) * (int)gridDim.y, share = (cut.r - r0 - 1) * (int)gridDim.y + (int)blockIdx.y;
     const int row0 = (int)((long long)rows * share / shares), row1 = (int)((long long)rows * (share + 1) / shares);
     const size_t step = (size_t)slot_rows * (D + 2);
-    const int slot0 = 2 * r0 + (at.first < r0 * at.per ? 0 : 1);
     const int lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kWide = D / 16;  // warps' worth of dimensions
+#pragma unroll 2
     for (int w = threadIdx.x >> 5; w < (row1 - row0 + 7) / 8 * kWide; w += kMergeThreads / 32) {
         const int row = row0 + w / kWide * 8 + (lane & 7), dq = w % kWide * 4 + (lane >> 3);
         if (row >= row1) continue;
@@ -253,7 +245,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
         }
         const bool seen = den != 0.f;
         const float inv = seen ? 1.f / den : 0.f;
-        const size_t orow = (size_t)(seq.q0 + node0 + node) * p.hq + h * p.g + row - node * p.g;
+        const size_t orow = (size_t)(cut.q0 + cut.node0 + node) * p.hq + cut.h * p.g + row - node * p.g;
         store_out4(p.out, orow * D + 4 * dq, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), p.out_type);
         if (p.lse && dq == 0) p.lse[orow] = seen ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
     }
@@ -263,7 +255,7 @@ namespace {
 
 constexpr int kSimplePerSm = 3;  // CTAs
 
-size_t slot_bytes(int rows, int d) { return (size_t)rows * (d + 2) * sizeof(float); }
+
 
 kv_status launch_simple(const TreeParams &pp, int d, cudaStream_t stream) {
     auto fn = d == 64 ? tree_simple_kernel<64> : tree_simple_kernel<128>;
@@ -276,7 +268,7 @@ kv_status launch_simple(const TreeParams &pp, int d, cudaStream_t stream) {
 
 kv_status launch_merge(const TreeParams &pp, int d, int slot_rows, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)pp.plan.runs - 1, kMergeShares);
+    cfg.gridDim = dim3((unsigned)pp.plan.runs - 1, slot_rows / 32);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -308,6 +300,10 @@ Shape shape_of(const kv_pool *p, int g, int max_q_len) {
     return s;
 }
 
+// Two slots and a cut for each run.
+size_t slots_bytes(const Shape &s, int d) { return 2 * (size_t)s.runs * s.slot_rows * (d + 2) * sizeof(float); }
+size_t workspace_bytes_of(const Shape &s, int d) { return slots_bytes(s, d) + s.runs * sizeof(Cut); }
+
 // Arguments that the query and the call refuse alike.
 kv_status check(kv_pool_t p, int batch, int num_q_heads, int max_blocks, int max_q_len) {
     if (!p || batch < 0 || max_q_len < 0 || max_blocks < 0 || num_q_heads <= 0) return KV_ERR_ARG;
@@ -335,7 +331,7 @@ kv_status kv_tree_workspace_size(kv_pool_t p, int batch, int num_q_heads, int ma
     *bytes = 0;
     if (batch == 0 || max_q_len == 0) return KV_OK;
     const tree::Shape s = tree::shape_of(p, num_q_heads / p->num_kv_heads, max_q_len);
-    *bytes = 2 * (size_t)s.runs * tree::slot_bytes(s.slot_rows, p->head_dim);
+    *bytes = tree::workspace_bytes_of(s, p->head_dim);
     return KV_OK;
 }
 
@@ -354,7 +350,7 @@ kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, 
         return KV_ERR_ARG;
     const int g = num_q_heads / p->num_kv_heads;
     const tree::Shape s = tree::shape_of(p, g, max_q_len);
-    if (workspace_bytes < 2 * (size_t)s.runs * tree::slot_bytes(s.slot_rows, p->head_dim)) return KV_ERR_ARG;
+    if (workspace_bytes < tree::workspace_bytes_of(s, p->head_dim)) return KV_ERR_ARG;
     tree::TreeParams pp{};
     pp.plan = {cu_q, seq_lens, batch, total_q, max_q_len, max_blocks, p->num_kv_heads, s.group_nodes,
                s.tile_nodes, s.runs, s.min_run, 0};
@@ -373,6 +369,7 @@ kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, 
     pp.out_type = out_dtype;
     pp.lse = lse_out;
     pp.partial = static_cast<float *>(workspace);
+    pp.cuts = reinterpret_cast<tree::Cut *>(static_cast<char *>(workspace) + tree::slots_bytes(s, p->head_dim));
     pp.err = p->err;
     if (p->dtype == KV_F32) {
         if (kv_status st = tree::launch_simple(pp, p->head_dim, as_stream(stream))) return st;

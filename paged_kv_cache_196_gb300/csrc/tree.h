@@ -25,6 +25,7 @@ struct TreeParams {
     int out_type;
     float *lse;
     float *partial;          // slots of [D / 4][rows] float4 and [rows] (reference, sum)
+    Cut *cuts;               // [runs]
     int *err;
 };
 

@@ -39,9 +39,17 @@ struct Seq {
     KV_DEVICE long long pair_units() const { return tiles + kTreePairCost; }
 };
 
-// Sequence b; without nodes where there are none or what describes it is out of range.
-KV_DEVICE Seq load_seq(const Plan &p, int b, int *err) {
-    const long long q0 = __ldg(p.cu_q + b), t = __ldg(p.cu_q + b + 1) - q0, len = __ldg(p.seq_lens + b);
+// What describes a sequence, as it lies in memory.
+struct RawSeq {
+    int q0, q1, len;
+};
+KV_DEVICE RawSeq load_raw(const Plan &p, int b) {
+    return RawSeq{__ldg(p.cu_q + b), __ldg(p.cu_q + b + 1), __ldg(p.seq_lens + b)};
+}
+
+// A sequence; without nodes where there are none or what describes it is out of range.
+KV_DEVICE Seq make_seq(const Plan &p, const RawSeq &raw, int *err) {
+    const long long q0 = raw.q0, t = raw.q1 - q0, len = raw.len;
     Seq s{0, 0, 0, 0, 0};
     if (t == 0) return s;
     if (t < 0 || t > p.max_q_len || q0 < 0 || q0 + t > p.total_q || len < t || len > (long long)p.max_blocks * 16) {
@@ -55,6 +63,8 @@ KV_DEVICE Seq load_seq(const Plan &p, int b, int *err) {
     s.groups = (s.nodes + p.group_nodes - 1) / p.group_nodes;
     return s;
 }
+
+KV_DEVICE Seq load_seq(const Plan &p, int b, int *err) { return make_seq(p, load_raw(p, b), err); }
 
 KV_DEVICE long long seq_units(const Plan &p, const Seq &s) {
     return s.nodes ? (long long)p.hkv * s.groups * s.pair_units() : 0;
@@ -128,7 +138,8 @@ struct Piece {
 struct Pieces {
     long long unit, end, first;  // first: of the pair
     int b, pair, run;
-    Seq seq, ahead;  // of sequences b and b + 1
+    Seq seq;
+    RawSeq ahead;  // of sequence b + 1: looked at when it is reached, so that nothing waits for it before
 
     KV_DEVICE void start(const Plan &p, const Place &at, int r) {
         run = r;
@@ -141,15 +152,15 @@ struct Pieces {
         if (unit < end) load_ahead(p);
     }
     KV_DEVICE void load_ahead(const Plan &p) {
-        ahead = Seq{0, 0, 0, 0, 0};
-        if (b + 1 < p.batch) ahead = load_seq(p, b + 1, nullptr);
+        ahead = RawSeq{0, 0, 0};
+        if (b + 1 < p.batch) ahead = load_raw(p, b + 1);
     }
     KV_DEVICE bool next(const Plan &p, Piece &out) {
         while (unit < end) {
             if (pair == p.hkv * seq.groups) {  // (a sequence without nodes has no pairs)
                 pair = 0;
                 ++b;
-                seq = ahead;
+                seq = make_seq(p, ahead, nullptr);
                 load_ahead(p);
                 continue;
             }
@@ -173,6 +184,29 @@ struct Pieces {
         return false;
     }
 };
+
+// ---------------------------------------------------------------- cut pairs
+// What the kernel that adds up cut pairs has to know of the end of a run: the pair that lies
+// across it.
+struct Cut {
+    int q0, node0, rows, h;  // rows of the group; 0: no pair is cut here
+    int r0, r1, slot0, r;    // the runs that hold its first and last tile, r0's slot, the run that begins here
+};
+
+KV_DEVICE Cut cut_of(const Plan &p, const Place &at, int r, int g) {
+    Cut c{0, 0, 0, 0, 0, 0, 0, r};
+    if (at.b >= p.batch || p.whole) return c;
+    const int cost = at.seq.tiles + kTreePairCost;
+    c.r0 = (int)((at.first + kTreePairCost) / at.per);
+    c.r1 = (int)((at.first + cost - 1) / at.per);
+    if (r <= c.r0 || r > c.r1) return c;
+    c.slot0 = 2 * c.r0 + (at.first < c.r0 * at.per ? 0 : 1);
+    c.h = at.pair / at.seq.groups;
+    c.node0 = (at.pair - c.h * at.seq.groups) * p.group_nodes;
+    c.rows = min(p.group_nodes, at.seq.nodes - c.node0) * g;
+    c.q0 = at.seq.q0;
+    return c;
+}
 
 // ---------------------------------------------------------------- the tree
 // Ancestors of the nodes, 32 of them a word.

@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             mbar_init(&sm.empty[s], MT);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&sm.qfull[s], 1);
+            mbar_init(&sm.qfull[s], 2);  // the copies, and what the piece is
             // MT = 2: each row tile's last S, and each softmax warp once it has read what the piece is
             mbar_init(&sm.qempty[s], MT == 1 ? 4 : 2 + 8);
             for (int x = 0; x < MT; ++x) {
@@ -386,6 +386,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         // heads of tile_nodes nodes; rows past the group's last hold anything (no row
         // reaches another one).
         if (lane == 0) tc::prefetch_tensormap(&tm_q);
+        bool told = false;  // what lies across the run's beginning
         int copied = 0;  // pieces whose queries were asked for
         Pieces pieces;
         pieces.start(p.plan, at, blockIdx.x);
@@ -399,31 +400,31 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                      (n < L::kQBufs || mbar_wait<TW>(&sm.qempty[buf], (n / L::kQBufs - 1) & 1, p.err));
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
+            if (!more) pc.t0 = pc.t1 = 0;
+            if (lane == 0 && more) {
+                const Rows r(p, pc);
+                const int per_copy = 128 / p.copies;
+                const int boxes = MT == 2 ? (r.nodes > p.plan.tile_nodes ? 2 : 1) : p.copies;
+                mbar_arrive_expect_tx(&sm.qfull[buf], boxes * L::kHalves * p.plan.tile_nodes * p.g * 128);
+                for (int i = 0; i < boxes; ++i) {
+                    char *dst = sQ + buf * L::kTileBytes + (MT == 2 ? i * L::kTileBytes : i * per_copy * 128);
+                    const int y = pc.seq.q0 + r.node0 + (MT == 2 ? i * p.plan.tile_nodes : 0);
+#pragma unroll
+                    for (int h = 0; h < L::kHalves; ++h)
+                        tc::tma_load_3d(dst + h * (128 * 128), &tm_q, 64 * h, pc.h * p.g, y, &sm.qfull[buf]);
+                }
+                ++copied;
+            }
             if (more)
                 sm.parents[buf][lane] = Ancestors::pack(p.parents ? p.parents + pc.seq.q0 : nullptr, pc.seq.nodes, p.err);
-            else
-                pc.t0 = pc.t1 = 0;
+            if (lane == 0) sm.piece[buf] = pc;
             __syncwarp();
             if (lane == 0) {
-                sm.piece[buf] = pc;
-                if (more) {
-                    const Rows r(p, pc);
-                    const int per_copy = 128 / p.copies;
-                    const int boxes = MT == 2 ? (r.nodes > p.plan.tile_nodes ? 2 : 1) : p.copies;
-                    mbar_arrive_expect_tx(&sm.qfull[buf], boxes * L::kHalves * p.plan.tile_nodes * p.g * 128);
-                    for (int i = 0; i < boxes; ++i) {
-                        char *dst = sQ + buf * L::kTileBytes + (MT == 2 ? i * L::kTileBytes : i * per_copy * 128);
-                        const int y = pc.seq.q0 + r.node0 + (MT == 2 ? i * p.plan.tile_nodes : 0);
-#pragma unroll
-                        for (int h = 0; h < L::kHalves; ++h)
-                            tc::tma_load_3d(dst + h * (128 * 128), &tm_q, 64 * h, pc.h * p.g, y, &sm.qfull[buf]);
-                    }
-                    ++copied;
-                } else {
-                    mbar_arrive(&sm.qfull[buf]);
-                }
+                mbar_arrive(&sm.qfull[buf]);
+                if (!more) mbar_arrive(&sm.qfull[buf]);  // (in place of the copies')
+                if (!told) p.cuts[blockIdx.x] = cut_of(p.plan, at, blockIdx.x, p.g);
             }
-            __syncwarp();
+            told = true;
         }
         // No copy may be in flight when the CTA ends.  (A buffer that was given anew had its
         // queries read; the end, once told, is in the one after the last piece's.)
