@@ -733,8 +733,9 @@ kv_status paged_prefill_attention(kv_pool_t p, const void *q, const int32_t *cu_
  *   max_q_len   host: the most nodes of a tree, at most 256;
  *   scale       positive and finite;
  *   lse_out     device fp32[total_q][num_q_heads] or NULL;
- *   workspace   16-byte aligned, kv_tree_workspace_size bytes for the same sizes.  Nothing in
- *               it has to start at zero; calls that may run at the same time need one each.
+ *   workspace   16-byte aligned, kv_tree_workspace_size bytes for the same sizes (NULL if that is
+ *               0: tables of few blocks).  Nothing in it has to start at zero; calls that may
+ *               run at the same time need one each.
  * Other arguments as paged_prefill_attention; pools of KV_F32, KV_BF16 and KV_F16, head_dim
  * 64 and 128.  Sums and softmax statistics are fp32.  fp32 pools: products in fp32.  16-bit
  * pools: products on the tensor cores, softmax weights in two parts of the pool's type (16

@@ -4,10 +4,9 @@
 // A sequence of L tokens and T nodes is kv heads x groups pairs: a group is as many
 // whole nodes as the kernel takes query rows (all heads of a kv head, row = node *
 // g + head within a row tile), so a pair is what one pass over the keys of a kv head serves.
-// A pair counts kTreePairCost units (its queries and its end) and one per key tile of
-// 128.  The units of all pairs are laid end to end, sequence by sequence, and cut into
+// A pair counts pair_cost units (its queries and its end) and one per key tile of 128.  The units of all pairs are laid end to end, sequence by sequence, and cut into
 // equal runs, one per CTA.  What a run holds of a pair is a piece: a range of its key
-// tiles, empty where the run's end falls among the pair's first kTreePairCost units.
+// tiles, empty where the run's end falls among the pair's first pair_cost units.
 // A pair of more than one piece leaves partial results: a run that begins inside a pair
 // has its piece of it in slot 2 run, the one that it begins and does not end in slot
 // 2 run + 1.
@@ -22,7 +21,6 @@ namespace pkv {
 namespace tree {
 
 constexpr int kTile = 128;  // keys
-constexpr int kTreePairCost = 1;
 
 struct Plan {
     const int32_t *cu_q, *seq_lens;
@@ -30,13 +28,13 @@ struct Plan {
     int hkv, group_nodes;  // kv heads; nodes of a group
     int tile_nodes;        // of a row tile: row of the group = node / tile_nodes * 128 + node % tile_nodes * g + head
     int runs;              // CTAs
+    int pair_cost;         // units
     int min_run;           // units of the shortest run
     int whole;             // a run takes the pairs that begin in it whole: none is cut
 };
 
 struct Seq {
     int q0, nodes, len, tiles, groups;
-    KV_DEVICE long long pair_units() const { return tiles + kTreePairCost; }
 };
 
 // What describes a sequence, as it lies in memory.
@@ -67,7 +65,7 @@ KV_DEVICE Seq make_seq(const Plan &p, const RawSeq &raw, int *err) {
 KV_DEVICE Seq load_seq(const Plan &p, int b, int *err) { return make_seq(p, load_raw(p, b), err); }
 
 KV_DEVICE long long seq_units(const Plan &p, const Seq &s) {
-    return s.nodes ? (long long)p.hkv * s.groups * s.pair_units() : 0;
+    return s.nodes ? (long long)p.hkv * s.groups * (s.tiles + p.pair_cost) : 0;
 }
 
 // What a CTA knows after place(): units of a run, all units, and of the unit it asked for
@@ -116,8 +114,8 @@ KV_DEVICE Place place(const Plan &p, int run, PlaceScratch<kThreads> &s, int *er
             const Seq q = load_seq(p, b, nullptr);
             const long long n = seq_units(p, q);
             if (unit < base + n) {
-                const int pair = (int)((unit - base) / q.pair_units());
-                s.at = Place{per, total, base + pair * q.pair_units(), b, pair, q};
+                const int cost = q.tiles + p.pair_cost, pair = (int)((unit - base) / cost);
+                s.at = Place{per, total, base + (long long)pair * cost, b, pair, q};
                 break;
             }
             base += n;
@@ -164,15 +162,15 @@ struct Pieces {
                 load_ahead(p);
                 continue;
             }
-            const int cost = seq.tiles + kTreePairCost;
+            const int cost = seq.tiles + p.pair_cost;
             const int from = (int)(unit - first);
             const int to = p.whole ? cost : (int)min(end - first, (long long)cost);
             const int now = pair++;
             first += cost;
             unit = first;
             if (p.whole && from > 0) continue;  // the run before has it
-            out.t0 = max(0, from - kTreePairCost);
-            out.t1 = max(0, to - kTreePairCost);
+            out.t0 = max(0, from - p.pair_cost);
+            out.t1 = max(0, to - p.pair_cost);
             if (out.t0 >= out.t1) continue;
             out.b = b;
             out.h = seq.groups == 1 ? now : now / seq.groups;
@@ -196,8 +194,8 @@ struct Cut {
 KV_DEVICE Cut cut_of(const Plan &p, const Place &at, int r, int g) {
     Cut c{0, 0, 0, 0, 0, 0, 0, r};
     if (at.b >= p.batch || p.whole) return c;
-    const int cost = at.seq.tiles + kTreePairCost;
-    c.r0 = (int)((at.first + kTreePairCost) / at.per);
+    const int cost = at.seq.tiles + p.pair_cost;
+    c.r0 = (int)((at.first + p.pair_cost) / at.per);
     c.r1 = (int)((at.first + cost - 1) / at.per);
     if (r <= c.r0 || r > c.r1) return c;
     c.slot0 = 2 * c.r0 + (at.first < c.r0 * at.per ? 0 : 1);

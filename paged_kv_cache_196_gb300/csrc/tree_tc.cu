@@ -386,7 +386,6 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         // heads of tile_nodes nodes; rows past the group's last hold anything (no row
         // reaches another one).
         if (lane == 0) tc::prefetch_tensormap(&tm_q);
-        bool told = false;  // what lies across the run's beginning
         int copied = 0;  // pieces whose queries were asked for
         Pieces pieces;
         pieces.start(p.plan, at, blockIdx.x);
@@ -422,10 +421,9 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             if (lane == 0) {
                 mbar_arrive(&sm.qfull[buf]);
                 if (!more) mbar_arrive(&sm.qfull[buf]);  // (in place of the copies')
-                if (!told) p.cuts[blockIdx.x] = cut_of(p.plan, at, blockIdx.x, p.g);
             }
-            told = true;
         }
+        if (lane == 0 && p.cuts) p.cuts[blockIdx.x] = cut_of(p.plan, at, blockIdx.x, p.g);
         // No copy may be in flight when the CTA ends.  (A buffer that was given anew had its
         // queries read; the end, once told, is in the one after the last piece's.)
         if (lane == 0)
@@ -674,10 +672,11 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         break;
                     }
                     char *vt = ring + (int)(pos % L::kSlots) * L::kTileBytes;
-                    const int row0 = max(0, r.before - key0);
+                    // (as far as their last block: copies of blocks that are not there are zeros)
+                    const int row0 = max(0, r.before - key0), row1 = min(128, (pc.seq.len - key0 + 15) & ~15);
                     constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
 #pragma unroll 2
-                    for (int i = row0 * (D / 8) + tid; i < 128 * (D / 8); i += 128) {
+                    for (int i = row0 * (D / 8) + tid; i < row1 * (D / 8); i += 128) {
                         const int at_row = i / (D / 8);
                         uint4 *at4 = reinterpret_cast<uint4 *>(vt + tile_offset<D>(at_row, i % (D / 8)));
                         const uint4 v = *at4;
@@ -706,6 +705,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     if (tail || gone) {
 #pragma unroll 1
                         for (int c = c0; c < c1; ++c) {
+                            if (!gone && key0 + 32 * c + 32 <= r.before) continue;
                             uint32_t bits = tail ? anc.keys(key0 + 32 * c - r.before) : 0xffffffffu;
                             if (gone >> (2 * c) & 1) bits &= 0xffff0000u;
                             if (gone >> (2 * c + 1) & 1) bits &= 0x0000ffffu;
@@ -857,14 +857,17 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             };
             if (MT == 2 || p.copies == 1) {
 #pragma unroll 1
-                for (int i = 0; i < D / 16; ++i) {
-                    uint32_t v[16];
-                    tc::tmem_ld16(ocol + 16 * i, v);
+                for (int i = 0; i < D / 16; i += 2) {
+                    uint32_t v[32];
+                    tc::tmem_ld32(ocol + 16 * i, v);
                     tc::tmem_wait_ld();
-                    float o[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = __uint_as_float(v[k]) * factor;
-                    if (valid) store(i, o);
+                    for (int h = 0; h < 2; ++h) {
+                        float o[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __uint_as_float(v[16 * h + k]) * factor;
+                        if (valid) store(i + h, o);
+                    }
                 }
             } else {
                 // Half of the columns at a time, in strips of 16: copy c sums and stores every

@@ -9,11 +9,18 @@
 // chosen (q null) count as drawn from a q that is one at x: W loses its entry at x.
 //
 // A draw from 10^5 tokens lies next to a border between two of them: sums that depend on
-// their order would return another token now and then.  So weights are integers, p and q in
-// steps of 2^-E with E = 62 - ceil(log2(vocab)): no sum passes 2^62 whatever the rows
-// hold, sums are exact in any order, and a step is at most 2^-42 (2^-45 for 128000 tokens),
-// 2^21 times finer than the rounding of an fp32 near one.  Single comparisons (u q(x) against
-// p(x)) are in fp64, where the product of two fp32 numbers is exact.
+// their order would return another token now and then.  So weights are integers, p and q
+// rounded to steps of 2^-E with E = 45, less for more than 2^17 tokens (42 for 2^20): no sum
+// passes 2^62 whatever the rows hold, sums are exact in any order, and their roundings, at random,
+// add up to about sqrt(vocab) 2^-47: 3e-12 for 128000 tokens, so that a draw meets another
+// token than the real numbers' about once in 3 million times.  (Cut off instead of rounded they
+// would add up to 2^-30.)  Single comparisons (u q(x) against p(x)) are in fp64, where the
+// product of two fp32 numbers is exact.
+//
+// A probability becomes an integer in two parts, 22 bits and E - 22: adding 2^23 to a number
+// below 2^22 leaves its whole part in the mantissa, what that leaves is exact, and both parts
+// sum up in 32 bits over a lane's 16 tokens: six full-rate operations where a conversion to 64
+// bits takes the time of sixteen.
 //
 // A walk down a tree needs p(x) and q(x) of each draft, which are loaded at once for all
 // nodes before it begins; only a rejection and the draw at the end read whole rows, so the
@@ -38,7 +45,7 @@ namespace tree {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVerifyThreads = 256;
+constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kChunk = 512;           // tokens
 constexpr int kMaxVocab = 1 << 20;
@@ -129,8 +136,20 @@ KV_DEVICE void load_chunk(const void *row, int first, int vocab, bool wide, floa
     }
 }
 
-// p as a whole number of steps 2^-E (towards zero; a power of two scales exactly).
-KV_DEVICE unsigned long long fixed(float x, float step_inv) { return __float2ull_rz(prob(x) * step_inv); }
+// A probability in steps of 2^-E: hi 2^(E - 22) + lo.
+struct Parts {
+    uint32_t hi, lo;
+};
+KV_DEVICE Parts parts(float x, float lo_scale) {  // x of prob(), lo_scale = 2^(E - 22)
+    const float y = x * 0x1p22f;
+    const float t = __fadd_rd(y, 0x1p23f);
+    const float rest = y - (t - 0x1p23f);  // exact
+    return Parts{__float_as_uint(t) & 0x7fffffu, __float_as_uint(__fadd_rn(rest * lo_scale, 0x1p23f)) - 0x4b000000u};
+}
+KV_DEVICE unsigned long long fixed(float x, int e) {
+    const Parts a = parts(prob(x), __uint_as_float((uint32_t)(127 + e - 22) << 23));
+    return ((unsigned long long)a.hi << (e - 22)) + a.lo;
+}
 
 // floor(a b / 2^shift)
 KV_DEVICE unsigned long long mul_shift(unsigned long long a, unsigned long long b, int shift) {
@@ -169,23 +188,30 @@ KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const
     const char *p = static_cast<const char *>(a.p) + row * a.p_stride * kElem<T>;
     const char *q = static_cast<const char *>(a.q) + row * a.q_stride * kElem<T>;
     const bool p_wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0, q_wide = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
-    const float unit = exp2f((float)a.scale_exp);
+    const float lo_scale = __uint_as_float((uint32_t)(127 + a.scale_exp - 22) << 23);
+    const int shift = a.scale_exp - 22;
     for (int c = warp; c < chunks; c += kVerifyWarps) {
         const long long first = ((long long)rank * chunks + c) * kChunk;
         unsigned long long sum = 0;
         if (first < a.vocab) {
             const bool full = first + kChunk <= a.vocab;
             float x[16], y[16];
-            if (k == 0) {
-                load_chunk<T>(p, (int)first, a.vocab, full && p_wide, x);
+            load_chunk<T>(p, (int)first, a.vocab, full && p_wide && (k == 0 || q_wide), x);
+            if (k) load_chunk<T>(q, (int)first, a.vocab, full && p_wide && q_wide, y);
+            if (k <= 1) {
+                // max(p - q, 0) part by part, where p > q (a part may be below q's; the sum is not)
+                uint32_t hi = 0, lo = 0;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sum += fixed(x[i], unit);
+                for (int i = 0; i < 16; ++i) {
+                    const float px = prob(x[i]), qx = k ? prob(y[i]) : 0.f;
+                    const Parts u = parts(px, lo_scale), v = parts(qx, lo_scale);
+                    if (px > qx) hi += u.hi - v.hi, lo += u.lo - v.lo;
+                }
+                sum = ((unsigned long long)hi << shift) + (long long)(int32_t)lo;
             } else {
-                const bool wide = full && p_wide && q_wide;
-                load_chunk<T>(p, (int)first, a.vocab, wide, x);
-                load_chunk<T>(q, (int)first, a.vocab, wide, y);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sum += residual(fixed(x[i], unit), fixed(y[i], unit), k, sm.left, a.scale_exp);
+                for (int i = 0; i < 16; ++i)
+                    sum += residual(fixed(x[i], a.scale_exp), fixed(y[i], a.scale_exp), k, sm.left, a.scale_exp);
             }
         }
         sum = warp_sum(sum);
@@ -196,7 +222,7 @@ KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const
         if (lane == 0)
             for (int i = 0; i < gone; ++i) {
                 const int at = sm.token[sm.gone[i]] / kChunk - rank * chunks;
-                if (at >= 0 && at < chunks) sm.chunk[at] -= fixed(sm.p[sm.gone[i]], unit);
+                if (at >= 0 && at < chunks) sm.chunk[at] -= fixed(sm.p[sm.gone[i]], a.scale_exp);
             }
         __syncwarp();
         unsigned long long sum = 0;
@@ -236,13 +262,12 @@ KV_DEVICE int find(const VerifyParams &a, const VerifyShared &sm, int chunks, in
     }
     const char *p = static_cast<const char *>(a.p) + row * a.p_stride * kElem<T>;
     const char *q = static_cast<const char *>(a.q) + row * a.q_stride * kElem<T>;
-    const float unit = exp2f((float)a.scale_exp);
     const int first = (rank * chunks + c) * kChunk + 16 * lane;
     auto weight = [&](int x) -> unsigned long long {
         if (x >= a.vocab) return 0;
         for (int i = 0; i < gone; ++i)
             if (sm.token[sm.gone[i]] == x) return 0;
-        return residual(fixed(one<T>(p, x), unit), k ? fixed(one<T>(q, x), unit) : 0, k, sm.left, a.scale_exp);
+        return residual(fixed(one<T>(p, x), a.scale_exp), k ? fixed(one<T>(q, x), a.scale_exp) : 0, k, sm.left, a.scale_exp);
     };
     unsigned long long w[16], mine = 0;
 #pragma unroll
@@ -265,7 +290,7 @@ KV_DEVICE int find(const VerifyParams &a, const VerifyShared &sm, int chunks, in
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams a) {
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyParams a) {
     __shared__ VerifyShared sm;
     const cg::cluster_group cluster = cg::this_cluster();
     const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -526,8 +551,8 @@ kv_status kv_verify_tree(kv_pool_t p, const void *target_probs, int64_t target_s
     a.p_stride = target_stride ? target_stride : vocab;
     a.q_stride = draft_stride ? draft_stride : vocab;
     a.vocab = vocab;
-    a.scale_exp = 62;
-    while ((1 << (62 - a.scale_exp)) < vocab) --a.scale_exp;
+    a.scale_exp = 45;
+    while ((1ll << (62 - a.scale_exp)) < vocab) --a.scale_exp;
     a.cu_q = cu_q;
     a.total_q = total_q;
     a.max_q_len = max_q_len;

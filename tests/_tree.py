@@ -89,6 +89,11 @@ class TreeCase:
             if n:
                 self.write(b)
 
+    def widen(self, width):
+        """Tables of that many columns."""
+        self.tables = np.concatenate([self.tables, np.full((self.batch, width - self.width), -1, np.int32)], 1)
+        self.width = width
+
     def slots(self, b, n=None):
         j = np.arange(self.lens[b] if n is None else n)
         return self.tables[b, j // 16].astype(np.int64) * 16 + j % 16

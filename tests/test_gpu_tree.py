@@ -18,11 +18,16 @@ def _cuda():
 
 
 def run(case, out_dtype=None, err=0, gone=(), **kw):
+    """The call, under a table of few blocks (no sequence is cut) also under a wider one (they may be)."""
     try:
         a = case.args(out_dtype, **kw)
         case.call(a)
         case.check(a, err=err, gone=gone)
-        return a
+        if case.width <= 32:
+            case.widen(33)
+            a = case.args(out_dtype, **kw)
+            case.call(a)
+            case.check(a, err=err, gone=gone)
     finally:
         case.close()
 
@@ -81,8 +86,9 @@ def test_table_wider_than_the_sequences():
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-def test_masked_keys_reach_nobody(dtype, d, bad):
-    case = TreeCase(dtype, d, 2, 4, [100, 250], [20, 11], kind="star", seed=9, garbage=bad)
+@pytest.mark.parametrize("width,g", [(0, 4), (33, 4), (33, 1), (33, 8)])
+def test_masked_keys_reach_nobody(dtype, d, bad, width, g):
+    case = TreeCase(dtype, d, 2, g, [100, 250], [20, 11], kind="star", seed=9, garbage=bad, width=width)
     case.k[0][100 + 7] = bad   # node 7 of the first tree: only its own rows see it
     case.v[0][100 + 9] = bad   # node 9
     case.v[1][250 + 4, :, 5] = bad
@@ -102,8 +108,9 @@ def test_masked_keys_reach_nobody(dtype, d, bad):
         case.close()
 
 
-def test_nan_in_a_cached_key_reaches_every_row():
-    case = TreeCase("bf16", 128, 1, 4, [300], [12], seed=2)
+@pytest.mark.parametrize("width", [0, 33])
+def test_nan_in_a_cached_key_reaches_every_row(width):
+    case = TreeCase("bf16", 128, 1, 4, [300], [12], seed=2, width=width)
     case.k[0][17] = math.nan
     case.write(0)
     try:
@@ -116,8 +123,9 @@ def test_nan_in_a_cached_key_reaches_every_row():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-def test_blocks_out_of_range(dtype):
-    case = TreeCase(dtype, 128, 2, 2, [200, 0], [9, 4], seed=4)
+@pytest.mark.parametrize("width", [0, 33])
+def test_blocks_out_of_range(dtype, width):
+    case = TreeCase(dtype, 128, 2, 2, [200, 0], [9, 4], seed=4, width=width)
     case.tables[0, 3] = case.blocks
     case.tables[0, 12] = -5      # the tree's own block: tokens 192 .. 207
     case.tables[1, 0] = 1 << 30  # all that the second sequence has
@@ -302,6 +310,18 @@ def test_offsets_past_32_bits():
             pk.kv_pool_destroy(pool)
 
 
+def test_no_workspace_under_few_blocks():
+    case = TreeCase("f16", 128, 2, 4, [300, 0, 77], [6, 33, 1], width=32)
+    try:
+        a = case.args("f32")
+        assert a["ws_bytes"] == 0 and pk.kv_tree_workspace_size(case.pool, 3, case.hq, 33, 33) > 0
+        a["ws"] = None
+        case.call(a)
+        case.check(a)
+    finally:
+        case.close()
+
+
 def test_nothing_to_do():
     case = TreeCase("bf16", 128, 1, 1, [5], [0])
     try:
@@ -315,7 +335,7 @@ def test_nothing_to_do():
 
 
 def test_refusals():
-    case = TreeCase("bf16", 128, 2, 2, [20], [4])
+    case = TreeCase("bf16", 128, 2, 2, [20], [4], width=33)
     i4 = pk.kv_pool_create(4, 16, 2, 128, pk.KV_I4)
     try:
         a = case.args("f32")
