@@ -76,6 +76,8 @@ struct VerifyShared {
     int16_t parent[kMaxNodes];                  // -1: none, or no draft
     int16_t gone[kMaxNodes];                    // rejected nodes whose tokens were chosen
     int16_t path[kMaxNodes];
+    unsigned long long weight[kChunk + kChunk / 16];  // of the chunk that holds the draw, 16 and a gap
+    int node, count, rejected, gone_count, end;  // where the walk stands; end: nothing is left to try
 };
 
 // A probability: not below 0 (nor NaN), not above 1.
@@ -101,6 +103,14 @@ template <typename T>
 constexpr int kElem = 2;
 template <>
 constexpr int kElem<float> = 4;
+
+// Which token of its chunk a lane's i-th is.
+template <typename T>
+KV_DEVICE int chunk_index(int i, bool wide) {
+    const int lane = threadIdx.x & 31;
+    constexpr int kVec = 16 / kElem<T>;
+    return wide ? i / kVec * (32 * kVec) + lane * kVec + i % kVec : 32 * i + lane;
+}
 
 // A lane's 16 tokens of the chunk at `first`: in 16-byte loads where `wide`, else every 32nd.
 template <typename T>
@@ -177,11 +187,15 @@ KV_DEVICE unsigned long long warp_sum(unsigned long long x) {
     return x;
 }
 
+// The cluster's barrier in two halves: arrived at when a CTA begins, waited for where it matters.
+KV_DEVICE void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+KV_DEVICE void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 // One pass over the node's row: sums of W_k by chunk, and of all of it over the cluster.
 // `gone`: nodes whose tokens have lost their weight.  The whole cluster calls it.
 template <typename T>
 KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const cg::cluster_group &cluster, long long row,
-                                  int k, int gone, int turn) {
+                                  int k, int gone, int turn, bool first_pass) {
     const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int chunks = ((a.vocab + kChunk - 1) / kChunk + ctas - 1) / ctas;  // a CTA's share
@@ -228,8 +242,10 @@ KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const
         unsigned long long sum = 0;
         for (int c = lane; c < chunks; c += 32) sum += sm.chunk[c];
         sum = warp_sum(sum);
+        if (first_pass) cluster_wait();  // the other CTAs run: their shared memory may be written
         if (lane < ctas) *cluster.map_shared_rank(&sm.totals[turn][rank], lane) = sum;
     }
+    if (first_pass && warp != 0) cluster_wait();
     cluster.sync();
     unsigned long long total = 0;
     for (int i = 0; i < ctas; ++i) total += sm.totals[turn][i];
@@ -239,7 +255,7 @@ KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const
 // The first token whose running sum of W_k passes `point`, counted from this CTA's share on
 // (one warp; the share holds it).
 template <typename T>
-KV_DEVICE int find(const VerifyParams &a, const VerifyShared &sm, int chunks, int rank, long long row, int k, int gone,
+KV_DEVICE int find(const VerifyParams &a, VerifyShared &sm, int chunks, int rank, long long row, int k, int gone,
                    unsigned long long point) {
     const int lane = threadIdx.x & 31;
     int c = 0;
@@ -262,16 +278,27 @@ KV_DEVICE int find(const VerifyParams &a, const VerifyShared &sm, int chunks, in
     }
     const char *p = static_cast<const char *>(a.p) + row * a.p_stride * kElem<T>;
     const char *q = static_cast<const char *>(a.q) + row * a.q_stride * kElem<T>;
-    const int first = (rank * chunks + c) * kChunk + 16 * lane;
-    auto weight = [&](int x) -> unsigned long long {
-        if (x >= a.vocab) return 0;
-        for (int i = 0; i < gone; ++i)
-            if (sm.token[sm.gone[i]] == x) return 0;
-        return residual(fixed(one<T>(p, x), a.scale_exp), k ? fixed(one<T>(q, x), a.scale_exp) : 0, k, sm.left, a.scale_exp);
-    };
-    unsigned long long w[16], mine = 0;
+    const int first = (rank * chunks + c) * kChunk;
+    const bool wide = first + kChunk <= a.vocab && (reinterpret_cast<uintptr_t>(p) & 15) == 0 &&
+                      (k == 0 || (reinterpret_cast<uintptr_t>(q) & 15) == 0);
+    float x[16], y[16];
+    load_chunk<T>(p, first, a.vocab, wide, x);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) mine += w[i] = weight(first + i);
+    for (int i = 0; i < 16; ++i) y[i] = 0.f;
+    if (k) load_chunk<T>(q, first, a.vocab, wide, y);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int at = chunk_index<T>(i, wide);
+        sm.weight[at + at / 16] = residual(fixed(x[i], a.scale_exp), fixed(y[i], a.scale_exp), k, sm.left, a.scale_exp);
+    }
+    __syncwarp();
+    for (int i = lane; i < gone; i += 32) {
+        const int at = sm.token[sm.gone[i]] - first;
+        if (at >= 0 && at < kChunk) sm.weight[at + at / 16] = 0;
+    }
+    __syncwarp();
+    unsigned long long mine = 0;
+    for (int i = 0; i < 16; ++i) mine += sm.weight[17 * lane + i];
     unsigned long long upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -281,10 +308,9 @@ KV_DEVICE int find(const VerifyParams &a, const VerifyShared &sm, int chunks, in
     const uint32_t past = __ballot_sync(0xffffffffu, upto > point);
     unsigned long long sum = upto - mine;
     int found = -1;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        sum += w[i];
-        if (found < 0 && sum > point) found = first + i;
+    for (int i = 0; i < 16 && found < 0; ++i) {
+        sum += sm.weight[17 * lane + i];
+        if (sum > point) found = first + 16 * lane + i;
     }
     return past ? __shfl_sync(0xffffffffu, found, __ffs(past) - 1) : -1;
 }
@@ -297,6 +323,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
     const int b = blockIdx.x / ctas;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool drawn = a.q != nullptr;
+    cluster_arrive();
 
     const long long q0 = __ldg(a.cu_q + b);
     long long nodes = __ldg(a.cu_q + b + 1) - q0;
@@ -323,68 +350,82 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
             sm.u[i] = __ldg(a.accept_u + q0 + i);
         }
     }
-    cluster.sync();  // (the other CTAs run: their shared memory may be written)
+    __syncthreads();
 
-    const double unit = exp2((double)-a.scale_exp);
+    const double unit = __longlong_as_double((long long)(1023 - a.scale_exp) << 52);
     const int chunks = ((a.vocab + kChunk - 1) / kChunk + ctas - 1) / ctas;
+    unsigned long long total = 0;  // of the pass over W_k, once there was one
     int node = 0, count = 0, turn = 0;
-    int k = 0, gone = 0;            // rejections at the node
-    unsigned long long total = 0;   // of the pass over W_k, once there was one
-    bool summed = false;
-    while (T > 0 && count < a.max_path) {
-        double left = 1.0;
-        int last = node, taken = -1;
-        k = gone = 0;
-        summed = false;
-        while (taken < 0 && left > 0.0) {
-            int child = T;
-            for (int base = (last + 1) & ~31; base < T && child == T; base += 32) {
-                const int i = base + lane;
-                const uint32_t is = __ballot_sync(0xffffffffu, i > last && i < T && sm.parent[i] == node);
-                if (is) child = base + __ffs(is) - 1;
+    int k = 0, gone = 0;           // rejections at the node
+    int last = 0;                  // its child that was tried last
+    double left = 1.0;             // S_k
+    bool summed = false, first_pass = true;
+    while (T > 0) {
+        // Warp 0 of every CTA walks (64-bit floating point is slow: once is enough) until a rejection asks
+        // for a pass over the row, or the walk ends.
+        if (warp == 0) {
+            int end = 0;
+            while (true) {
+                int child = T;
+                if (count < a.max_path && left > 0.0)
+                    for (int base = (last + 1) & ~31; base < T && child == T; base += 32) {
+                        const int i = base + lane;
+                        const uint32_t is = __ballot_sync(0xffffffffu, i > last && i < T && sm.parent[i] == node);
+                        if (is) child = base + __ffs(is) - 1;
+                    }
+                if (child == T) {
+                    end = 1;
+                    break;
+                }
+                last = child;
+                double w = sm.p[child];
+                if (drawn) {
+                    for (int i = 0; i < k; ++i) w = fmax(w - (i ? (double)sm.left[i] * unit : 1.0) * sm.q[child], 0.0);
+                } else {
+                    for (int i = 0; i < gone; ++i)
+                        if (sm.token[sm.gone[i]] == sm.token[child]) w = 0.0;
+                }
+                if ((double)sm.u[child] * sm.q[child] * left < w) {
+                    if (lane == 0) sm.path[count] = (int16_t)child;
+                    ++count;
+                    node = last = child;
+                    k = gone = 0;
+                    left = 1.0;
+                    summed = false;
+                } else if (drawn) {
+                    ++k;
+                    break;
+                } else if (w > 0.0) {
+                    left -= w;
+                    __syncwarp();
+                    if (lane == 0) sm.gone[gone] = (int16_t)child;
+                    ++gone;
+                    __syncwarp();
+                }
             }
-            if (child == T) break;
-            last = child;
-            double w = sm.p[child];
-            if (drawn) {
-                for (int i = 0; i < k; ++i) w = fmax(w - (i ? (double)sm.left[i] * unit : 1.0) * sm.q[child], 0.0);
-            } else {
-                for (int i = 0; i < gone; ++i)
-                    if (sm.token[sm.gone[i]] == sm.token[child]) w = 0.0;
-            }
-            if ((double)sm.u[child] * sm.q[child] * left < w) {
-                taken = child;
-            } else if (drawn) {
-                total = pass<E>(a, sm, cluster, q0 + node, ++k, 0, turn);
-                turn ^= 1;
-                summed = true;
-                left = (double)total * unit;
-                if (tid == 0 && k < kMaxNodes) sm.left[k] = total;
-                __syncthreads();
-            } else if (w > 0.0) {
-                left -= w;
-                __syncthreads();  // every thread has read the list
-                if (tid == 0) sm.gone[gone] = (int16_t)child;
-                ++gone;
-                __syncthreads();
-            }
+            if (lane == 0) sm.node = node, sm.count = count, sm.rejected = k, sm.gone_count = gone, sm.end = end;
         }
-        if (taken < 0) break;
-        if (tid == 0) sm.path[count] = (int16_t)taken;
-        ++count;
-        node = taken;
-        k = gone = 0;
-        summed = false;
+        __syncthreads();
+        if (sm.node != node) summed = false;
+        node = sm.node, count = sm.count, k = sm.rejected, gone = sm.gone_count;
+        if (sm.end) break;
+        total = pass<E>(a, sm, cluster, q0 + node, k, 0, turn, first_pass);
+        turn ^= 1;
+        summed = true;
+        first_pass = false;
+        if (warp == 0) left = (double)total * unit;
+        if (tid == 0) sm.left[k] = total;
     }
     int token = -1;
     if (T > 0) {
         if (!summed) {
-            total = pass<E>(a, sm, cluster, q0 + node, 0, gone, turn);
+            total = pass<E>(a, sm, cluster, q0 + node, 0, gone, turn, first_pass);
             turn ^= 1;
+            first_pass = false;
         }
         if (total == 0 && (k > 0 || gone > 0)) {  // nothing is left: p itself
             k = gone = 0;
-            total = pass<E>(a, sm, cluster, q0 + node, 0, 0, turn);
+            total = pass<E>(a, sm, cluster, q0 + node, 0, 0, turn, first_pass);
             turn ^= 1;
         }
         // floor(u total): u is a whole number of 2^-shift
@@ -401,6 +442,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
             if (lane == 0) a.out_tokens[(long long)b * (a.max_path + 1) + count] = token;
         }
     }
+    if (first_pass) cluster_wait();  // (no pass: no nodes)
     if (rank == 0) {
         __syncthreads();
         if (tid == 0) a.num_accepted[b] = count;
