@@ -15,7 +15,8 @@
 // add up to about sqrt(vocab) 2^-47: 3e-12 for 128000 tokens, so that a draw meets another
 // token than the real numbers' about once in 3 million times.  (Cut off instead of rounded they
 // would add up to 2^-30.)  Single comparisons (u q(x) against p(x)) are in fp64, where the
-// product of two fp32 numbers is exact.
+// product of two fp32 numbers is exact (in the first test of a node in fp32, by the product and
+// what a fused multiply-add says it leaves).
 //
 // A probability becomes an integer in two parts, 22 bits and E - 22: adding 2^23 to a number
 // below 2^22 leaves its whole part in the mantissa, what that leaves is exact, and both parts
@@ -169,16 +170,23 @@ KV_DEVICE unsigned long long mul_shift(unsigned long long a, unsigned long long 
     return shift ? (lo >> shift) | (hi << (64 - shift)) : lo;
 }
 
-// W_k of a token from its p and q: `left` holds S_1 .. S_{k-1} from its second entry on.
-KV_DEVICE unsigned long long residual(unsigned long long p, unsigned long long q, int k,
-                                      const unsigned long long *left, int e) {
-    if (k == 0) return p;
-    unsigned long long w = p > q ? p - q : 0;
+// W_k of a token from its W_1 and q, k > 1: `left` holds S_1 .. S_{k-1} from its second entry on.
+// (A function of its own: in line, sixteen times over, it is more code than the rest of a pass,
+// and a launch begins with empty instruction caches.)
+__device__ __noinline__ unsigned long long residual(unsigned long long w, float q, int k, const unsigned long long *left,
+                                                    int e) {
+    const unsigned long long steps = fixed(q, e);
     for (int i = 1; i < k; ++i) {
-        const unsigned long long x = mul_shift(left[i], q, e);
+        const unsigned long long x = mul_shift(left[i], steps, e);
         w = w > x ? w - x : 0;
     }
     return w;
+}
+
+// W_1 of a token, W_0 where k is 0.
+KV_DEVICE unsigned long long first_residual(float p, float q, int k, int e) {
+    const unsigned long long a = fixed(p, e), b = k ? fixed(q, e) : 0;
+    return a > b ? a - b : 0;
 }
 
 KV_DEVICE unsigned long long warp_sum(unsigned long long x) {
@@ -225,7 +233,7 @@ KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const
             } else {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    sum += residual(fixed(x[i], a.scale_exp), fixed(y[i], a.scale_exp), k, sm.left, a.scale_exp);
+                    sum += residual(first_residual(x[i], y[i], 1, a.scale_exp), y[i], k, sm.left, a.scale_exp);
             }
         }
         sum = warp_sum(sum);
@@ -289,7 +297,9 @@ KV_DEVICE int find(const VerifyParams &a, VerifyShared &sm, int chunks, int rank
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int at = chunk_index<T>(i, wide);
-        sm.weight[at + at / 16] = residual(fixed(x[i], a.scale_exp), fixed(y[i], a.scale_exp), k, sm.left, a.scale_exp);
+        unsigned long long w = first_residual(x[i], y[i], k, a.scale_exp);
+        if (k > 1) w = residual(w, y[i], k, sm.left, a.scale_exp);
+        sm.weight[at + at / 16] = w;
     }
     __syncwarp();
     for (int i = lane; i < gone; i += 32) {
@@ -378,14 +388,23 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
                     break;
                 }
                 last = child;
-                double w = sm.p[child];
-                if (drawn) {
-                    for (int i = 0; i < k; ++i) w = fmax(w - (i ? (double)sm.left[i] * unit : 1.0) * sm.q[child], 0.0);
+                bool takes;
+                double w = 0.0;
+                if (k == 0 && gone == 0) {
+                    // u q against p in fp32 and what its product leaves: exact, without 64 bits
+                    const float hi = sm.u[child] * sm.q[child], lo = fmaf(sm.u[child], sm.q[child], -hi);
+                    takes = hi < sm.p[child] || (hi == sm.p[child] && lo < 0.f);
                 } else {
-                    for (int i = 0; i < gone; ++i)
-                        if (sm.token[sm.gone[i]] == sm.token[child]) w = 0.0;
+                    w = sm.p[child];
+                    if (drawn) {
+                        for (int i = 0; i < k; ++i) w = fmax(w - (i ? (double)sm.left[i] * unit : 1.0) * sm.q[child], 0.0);
+                    } else {
+                        for (int i = 0; i < gone; ++i)
+                            if (sm.token[sm.gone[i]] == sm.token[child]) w = 0.0;
+                    }
+                    takes = (double)sm.u[child] * sm.q[child] * left < w;
                 }
-                if ((double)sm.u[child] * sm.q[child] * left < w) {
+                if (takes) {
                     if (lane == 0) sm.path[count] = (int16_t)child;
                     ++count;
                     node = last = child;
@@ -395,8 +414,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
                 } else if (drawn) {
                     ++k;
                     break;
-                } else if (w > 0.0) {
-                    left -= w;
+                } else if (gone == 0 ? sm.p[child] > 0.f : w > 0.0) {
+                    left -= gone == 0 ? (double)sm.p[child] : w;
                     __syncwarp();
                     if (lane == 0) sm.gone[gone] = (int16_t)child;
                     ++gone;
