@@ -51,9 +51,7 @@ constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kChunk = 512;           // tokens
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kMaxCluster = 8;
-// Chunks of a CTA: a cluster that could be larger has fewer than 2 kVerifyWarps a CTA.
-constexpr int kCtaChunks = kMaxVocab / kChunk / kMaxCluster;
-static_assert(kCtaChunks >= 2 * kVerifyWarps, "chunk sums of a CTA");
+constexpr int kCtaChunks = kMaxVocab / kChunk;  // of a cluster of one
 
 struct VerifyParams {
     const void *p, *q;  // rows of the vocabulary; q null: drafts were chosen
@@ -557,17 +555,21 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
 
 namespace {
 
-// CTAs of a sequence's cluster: as many as leave each of its warps a chunk or more.
-int cluster_size(int vocab) {
+// CTAs of a sequence's cluster: as many as leave a chunk for each of its warps while the batch
+// stays within a third more than one wave of two CTAs per SM.  Trees, which pass over rows again
+// and again, gain by large clusters, chains by one wave: 16 trees over 128000 tokens 70.5 us in
+// clusters of 8, 118 of 4; 100 trees over 50000 90 us of 4, 137 of 2; 64 chains over 128000 22.1 us
+// of 4, 26.8 of 8; 200 chains over 32000 21.4 us alone, 24.9 in clusters of 2, 30.6 of 4.
+int cluster_size(int vocab, int batch) {
     const int chunks = (vocab + kChunk - 1) / kChunk;
     int n = 1;
-    while (n < kMaxCluster && 2 * n * kVerifyWarps <= chunks) n *= 2;
+    while (n < kMaxCluster && n * kVerifyWarps < chunks && 2ll * n * batch * 3 <= 8ll * sm_count()) n *= 2;
     return n;
 }
 
 template <typename E>
 kv_status launch_verify(const VerifyParams &a, cudaStream_t stream) {
-    const int n = cluster_size(a.vocab);
+    const int n = cluster_size(a.vocab, a.batch);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.batch * (unsigned)n);
     cfg.blockDim = dim3(kVerifyThreads);
