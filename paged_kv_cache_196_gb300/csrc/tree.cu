@@ -34,19 +34,25 @@ KV_DEVICE float ex2(float x) {
 }
 
 // ---------------------------------------------------------------- fp32 arithmetic
-// 32 rows of a pair against 32 keys at a time, products by fp32 multiply-adds: thread
+// 32 rows of a pair against 32 keys at a time, the next 32 copied meanwhile, products by fp32
+// multiply-adds: thread
 // (ty, tx) holds rows 2 ty, 2 ty + 1, scores keys tx + 8 j and sums dimensions
 // 4 tx + 32 i.  A warp owns eight rows, so their statistics and weights need no barrier.
 constexpr int kSimpleRows = 32, kSimpleKeys = 32, kSimpleThreads = 128;
 
 template <int D>
 struct SimpleShared {
-    float q[kSimpleRows][D + 4], k[kSimpleKeys][D + 4], v[kSimpleKeys][D + 4];
+    float q[kSimpleRows][D + 4], k[2][kSimpleKeys][D + 4], v[2][kSimpleKeys][D + 4];
     float p[kSimpleRows][kSimpleKeys + 1];
     uint32_t anc[kSimpleRows][kMaxNodes / 32];
-    uint32_t there;  // bit j: key j of the tile is in the pool
     PlaceScratch<kSimpleThreads> scratch;
 };
+
+// 16 bytes into shared memory, zeros if they are not there.
+KV_DEVICE void copy16(void *dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeParams p) {
@@ -83,29 +89,40 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) o[0][i] = o[1][i] = make_float4(0.f, 0.f, 0.f, 0.f);
         const int key1 = min(pc.t1 * kTile, pc.seq.len);
-        for (int key0 = pc.t0 * kTile; key0 < key1; key0 += kSimpleKeys) {
-            __syncthreads();
-            if (tid < kSimpleKeys) {
-                const int key = key0 + tid;
-                const int id = key < key1 ? __ldg(table + key / 16) : 0;
-                const bool in = id >= 0 && id < p.num_blocks;
-                if (!in) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
-                const uint32_t there = __ballot_sync(0xffffffffu, in && key < key1);
-                if (tid == 0) sm.there = there;
-            }
-            for (int i = tid; i < kSimpleKeys * D / 4; i += kSimpleThreads) {
-                const int r = i / (D / 4), d = i % (D / 4) * 4, key = key0 + r;
-                const int id = key < key1 ? __ldg(table + key / 16) : -1;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-                if (id >= 0 && id < p.num_blocks) {
-                    const size_t at0 = (((size_t)id * p.plan.hkv + pc.h) * 16 + key % 16) * D + d;
-                    x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.k) + at0));
-                    y = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.v) + at0));
+        // Keys key0 .. key0 + 31 (two blocks) into one of two buffers, zeros where there are none;
+        // the bits of those that are there.
+        auto fetch = [&](int key0, int buf) {
+            int id[2];
+            uint32_t there = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                id[i] = key0 + 16 * i < key1 ? __ldg(table + key0 / 16 + i) : -1;
+                if (key0 + 16 * i >= key1) continue;
+                if (id[i] < 0 || id[i] >= p.num_blocks) {
+                    id[i] = -1;
+                    if (tid == 0) atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
+                } else {
+                    there |= (0xffffu >> max(0, key0 + 16 * i + 16 - key1)) << (16 * i);
                 }
-                *reinterpret_cast<float4 *>(&sm.k[r][d]) = x;
-                *reinterpret_cast<float4 *>(&sm.v[r][d]) = y;
             }
-            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kSimpleKeys * D / 4 / kSimpleThreads; ++j) {
+                const int i = tid + j * kSimpleThreads, r = i / (D / 4), d = i % (D / 4) * 4;
+                const bool here = there >> r & 1;
+                const size_t at0 = (((size_t)max(id[r >> 4], 0) * p.plan.hkv + pc.h) * 16 + r % 16) * D + d;
+                copy16(&sm.k[buf][r][d], static_cast<const float *>(p.k) + at0, here);
+                copy16(&sm.v[buf][r][d], static_cast<const float *>(p.v) + at0, here);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            return there;
+        };
+        uint32_t there_next = fetch(pc.t0 * kTile, 0);
+        int buf = 0;
+        for (int key0 = pc.t0 * kTile; key0 < key1; key0 += kSimpleKeys, buf ^= 1) {
+            const uint32_t there = there_next;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();  // this tile is there, and every thread is done with the one before
+            if (key0 + kSimpleKeys < key1) there_next = fetch(key0 + kSimpleKeys, buf ^ 1);
             float s[2][4] = {};
 #pragma unroll 4
             for (int d = 0; d < D; d += 4) {
@@ -113,7 +130,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
                 const float4 c = *reinterpret_cast<const float4 *>(&sm.q[2 * ty + 1][d]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float4 b = *reinterpret_cast<const float4 *>(&sm.k[tx + 8 * j][d]);
+                    const float4 b = *reinterpret_cast<const float4 *>(&sm.k[buf][tx + 8 * j][d]);
                     s[0][j] += a.x * b.x, s[0][j] += a.y * b.y, s[0][j] += a.z * b.z, s[0][j] += a.w * b.w;
                     s[1][j] += c.x * b.x, s[1][j] += c.y * b.y, s[1][j] += c.z * b.z, s[1][j] += c.w * b.w;
                 }
@@ -121,7 +138,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = 2 * ty + i;
-                const uint32_t bits = key_bits(sm.anc[row], key0 - before) & sm.there;
+                const uint32_t bits = key_bits(sm.anc[row], key0 - before) & there;
                 float mx = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -155,7 +172,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
                 const float e0 = sm.p[2 * ty][j], e1 = sm.p[2 * ty + 1][j];
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) {
-                    const float4 v = *reinterpret_cast<const float4 *>(&sm.v[j][4 * tx + 32 * k]);
+                    const float4 v = *reinterpret_cast<const float4 *>(&sm.v[buf][j][4 * tx + 32 * k]);
                     if (e0 != 0.f)
                         o[0][k].x += e0 * v.x, o[0][k].y += e0 * v.y, o[0][k].z += e0 * v.z, o[0][k].w += e0 * v.w;
                     if (e1 != 0.f)
@@ -253,7 +270,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const Tree
 
 namespace {
 
-constexpr int kSimplePerSm = 3;  // CTAs
+constexpr int kSimplePerSm = 2;  // CTAs
 // Tables of up to this many blocks (four key tiles): no pair is cut, and no second kernel runs.  Two
 // sequences of 44 to 408 tokens: 13.1 us whole, 14.7 cut.
 constexpr int kWholeBlocks = 32;
