@@ -531,9 +531,10 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 }
             } else {
                 // A thread per row tile; the product of the first half of a tile's weights begins
-                // while the other half is weighed.  The rest of a tile's products and the next
-                // scores are issued in turn: products of both row tiles side by side would
-                // end together, and then neither's softmax would run beside the other's products.
+                // while the other half is weighed.  Row tiles issue a key tile's products (and the
+                // next scores) in turn: products of both side by side would end together, and then
+                // neither's softmax would run beside the other's products (four long contexts: 156
+                // us in turn, 186 side by side).
                 const int x = warp - L::kMmaWarp;
                 unsigned t = 0, u = 0;       // key tiles of the run so far, and of the row tile
                 unsigned dirty = 0;          // key tiles of the run so far that reached into a tree
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         }
                         for (int half = 0; ok && half < 2; ++half) {
                             if (!(ok = wait(&sm.pfull[x][half], u & 1))) break;
-                            if (half && (x == 1 || t + j > 0) &&
+                            if (half == 0 && (x == 1 || t + j > 0) &&
                                 !(ok = wait(&sm.turn[x], (t + j + (x == 0)) & 1)))
                                 break;
                             tc::fence_after_sync();
