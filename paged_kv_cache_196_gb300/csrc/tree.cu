@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
 // CTA x looks at the end of run x: if it lies among the tiles of a pair, the pair is cut,
 // and this CTA (with those of other y) takes one share of its rows, one share per cut.  A
 // warp takes 8 rows of 16 dimensions, so that it reads lines and writes sectors whole.
-constexpr int kMergeThreads = 256, kMergeAhead = 2;
+constexpr int kMergeThreads = 256, kMergeAhead = 3;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const TreeParams p, int slot_rows) {
@@ -222,49 +222,90 @@ __global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const Tree
     const size_t step = (size_t)slot_rows * (D + 2);
     const int lane = threadIdx.x & 31;
     constexpr int kWide = D / 16;  // warps' worth of dimensions
-#pragma unroll 4
-    for (int w = threadIdx.x >> 5; w < (row1 - row0 + 7) / 8 * kWide; w += kMergeThreads / 32) {
-        const int row = row0 + w / kWide * 8 + (lane & 7), dq = w % kWide * 4 + (lane >> 3);
-        if (row >= row1) continue;
+    const int items = (row1 - row0 + 7) / 8 * kWide;
+    // The place of item w's values in a slot; false if this lane has none.
+    auto locate = [&](int w, int &row, int &dq, int &at_row) {
+        row = row0 + w / kWide * 8 + (lane & 7);
+        dq = w % kWide * 4 + (lane >> 3);
         const int node = row / p.g, x = node / p.plan.tile_nodes;
-        const int at_row = x * 128 + row - x * p.plan.tile_nodes * p.g;  // of the slot
-        float M = -INFINITY, den = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s0 = r0; s0 <= r1; s0 += kMergeAhead) {
-            float2 ml[kMergeAhead];
-            float4 v[kMergeAhead];
-#pragma unroll
-            for (int i = 0; i < kMergeAhead; ++i) {
-                const int s = s0 + i;
-                ml[i] = make_float2(-INFINITY, 0.f);
-                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (s <= r1) {
-                    const float *part = p.partial + (s == r0 ? slot0 : 2 * s) * step;
-                    ml[i] = reinterpret_cast<const float2 *>(part + (size_t)slot_rows * D)[at_row];
-                    v[i] = reinterpret_cast<const float4 *>(part)[(size_t)dq * slot_rows + at_row];
-                }
-            }
-            float up = M;
-#pragma unroll
-            for (int i = 0; i < kMergeAhead; ++i) up = fmaxf(up, ml[i].x);
-            const float ref = up == -INFINITY ? 0.f : up;
-            const float alpha = ex2(M - ref);
-            M = up;
-            den *= alpha;
-            a.x *= alpha, a.y *= alpha, a.z *= alpha, a.w *= alpha;
-#pragma unroll
-            for (int i = 0; i < kMergeAhead; ++i) {
-                if (ml[i].y == 0.f) continue;  // a piece without a key of the row has nothing to add
-                const float e = ex2(ml[i].x - ref);
-                den += e * ml[i].y;
-                a.x += e * v[i].x, a.y += e * v[i].y, a.z += e * v[i].z, a.w += e * v[i].w;
-            }
-        }
+        at_row = x * 128 + row - x * p.plan.tile_nodes * p.g;
+        return w < items && row < row1;
+    };
+    auto finish = [&](int row, int dq, float4 a, float M, float den) {
         const bool seen = den != 0.f;
         const float inv = seen ? 1.f / den : 0.f;
+        const int node = row / p.g;
         const size_t orow = (size_t)(cut.q0 + cut.node0 + node) * p.hq + cut.h * p.g + row - node * p.g;
         store_out4(p.out, orow * D + 4 * dq, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), p.out_type);
         if (p.lse && dq == 0) p.lse[orow] = seen ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+    };
+    // Pieces s0 .. s0 + kMergeAhead - 1 of the pair: their values, nothing past the last.
+    auto load = [&](int s0, int dq, int at_row, bool on, float2 (&ml)[kMergeAhead], float4 (&v)[kMergeAhead]) {
+#pragma unroll
+        for (int i = 0; i < kMergeAhead; ++i) {
+            const int s = s0 + i;
+            ml[i] = make_float2(-INFINITY, 0.f);
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (on && s <= r1) {
+                const float *part = p.partial + (s == r0 ? slot0 : 2 * s) * step;
+                ml[i] = reinterpret_cast<const float2 *>(part + (size_t)slot_rows * D)[at_row];
+                v[i] = reinterpret_cast<const float4 *>(part)[(size_t)dq * slot_rows + at_row];
+            }
+        }
+    };
+    // (a piece without a key of the row has nothing to add, whatever its reference)
+    auto add = [&](const float2 (&ml)[kMergeAhead], const float4 (&v)[kMergeAhead], float &M, float &den, float4 &a) {
+        float up = M;
+#pragma unroll
+        for (int i = 0; i < kMergeAhead; ++i) up = fmaxf(up, ml[i].x);
+        const float ref = up == -INFINITY ? 0.f : up;
+        const float alpha = ex2(M - ref);
+        M = up;
+        den *= alpha;
+        a.x *= alpha, a.y *= alpha, a.z *= alpha, a.w *= alpha;
+#pragma unroll
+        for (int i = 0; i < kMergeAhead; ++i) {
+            if (ml[i].y == 0.f) continue;
+            const float e = ex2(ml[i].x - ref);
+            den += e * ml[i].y;
+            a.x += e * v[i].x, a.y += e * v[i].y, a.z += e * v[i].z, a.w += e * v[i].w;
+        }
+    };
+    constexpr int kStep = kMergeThreads / 32;
+    if (r1 - r0 < kMergeAhead) {  // most pairs: all their pieces at once, two items at a time
+        for (int w = threadIdx.x >> 5; w < items; w += 2 * kStep) {
+            int row[2], dq[2], at_row[2];
+            bool on[2];
+            float2 ml[2][kMergeAhead];
+            float4 v[2][kMergeAhead];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                on[j] = locate(w + j * kStep, row[j], dq[j], at_row[j]);
+                load(r0, dq[j], at_row[j], on[j], ml[j], v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float M = -INFINITY, den = 0.f;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                add(ml[j], v[j], M, den, a);
+                if (on[j]) finish(row[j], dq[j], a, M, den);
+            }
+        }
+        return;
+    }
+    for (int w = threadIdx.x >> 5; w < items; w += kStep) {
+        int row, dq, at_row;
+        const bool on = locate(w, row, dq, at_row);
+        float M = -INFINITY, den = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int s = r0; s <= r1; s += kMergeAhead) {
+            float2 ml[kMergeAhead];
+            float4 v[kMergeAhead];
+            load(s, dq, at_row, on, ml, v);
+            add(ml, v, M, den, a);
+        }
+        if (on) finish(row, dq, a, M, den);
     }
 }
 
@@ -288,7 +329,7 @@ kv_status launch_simple(const TreeParams &pp, int d, cudaStream_t stream) {
 
 kv_status launch_merge(const TreeParams &pp, int d, int slot_rows, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)pp.plan.runs - 1, slot_rows / 64 > 0 ? slot_rows / 64 : 1);
+    cfg.gridDim = dim3((unsigned)pp.plan.runs - 1, slot_rows / 32);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -104,11 +104,11 @@ KV_DEVICE float max3(float a, float b, float c) {
 }
 
 // A block's rows: all of the first three dimensions, two groups of 8 rows from `group` on.
-KV_DEVICE void tma_load_4d(void *dst, const CUtensorMap *map, int group, uint64_t *bar) {
+KV_DEVICE void tma_load_4d(void *dst, const CUtensorMap *map, int group, uint64_t *bar, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(smem_addr(dst)),
-        "l"(map), "r"(0), "r"(group), "r"(smem_addr(bar))
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %2, %2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(0), "r"(group), "r"(smem_addr(bar)), "l"(policy)
         : "memory");
 }
 
@@ -326,6 +326,8 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             tc::prefetch_tensormap(&tm_k);
             tc::prefetch_tensormap(&tm_v);
         }
+        // (read once, but for a tree's other groups: partial results stay in L2 instead)
+        const uint64_t policy = l2_evict_first_policy();
         int slot = 0, phase = 0, turn = 0;
         unsigned issued = 0;
         bool stop = false;
@@ -361,7 +363,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                     __syncwarp();
                     if (lane < 8)
-                        tma_load_4d(dst + lane * 2 * L::kGroupBytes, is_v ? &tm_v : &tm_k, y, &sm.full[slot]);
+                        tma_load_4d(dst + lane * 2 * L::kGroupBytes, is_v ? &tm_v : &tm_k, y, &sm.full[slot], policy);
                     ++issued;
                     if (++slot == L::kSlots) slot = 0, phase ^= 1;
                 }
