@@ -313,6 +313,11 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         sm.abort = 0;
         mbar_init_fence();
     }
+    if (tid == L::kQWarp * 32) {
+        tc::prefetch_tensormap(&tm_q);
+        tc::prefetch_tensormap(&tm_k);
+        tc::prefetch_tensormap(&tm_v);
+    }
     const Place at = place(p.plan, blockIdx.x, sm.scratch, blockIdx.x == 0 ? p.err : nullptr);
     tc::fence_before_sync();
     __syncthreads();
@@ -322,10 +327,6 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
 
     if (warp == L::kCopyWarp) {
         // ================================================== K and V tiles
-        if (lane == 0) {
-            tc::prefetch_tensormap(&tm_k);
-            tc::prefetch_tensormap(&tm_v);
-        }
         // (read once, but for a tree's other groups: partial results stay in L2 instead)
         const uint64_t policy = l2_evict_first_policy();
         int slot = 0, phase = 0, turn = 0;
@@ -387,7 +388,6 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         // round trips to memory at every piece's beginning.  A box holds 64 dimensions of all
         // heads of tile_nodes nodes; rows past the group's last hold anything (no row
         // reaches another one).
-        if (lane == 0) tc::prefetch_tensormap(&tm_q);
         int copied = 0;  // pieces whose queries were asked for
         Pieces pieces;
         pieces.start(p.plan, at, blockIdx.x);
