@@ -803,6 +803,8 @@ kv_status kv_verify_tree(kv_pool_t p, const void *target_probs, int64_t target_s
  * (device int32[batch], not overlapping seq_lens) becomes seq_lens[b] - T_b + 1 +
  * num_accepted[b]: what the next append goes on from.  (Blocks behind it stay in the
  * tables; the host frees or refills them.)  A sequence without nodes keeps its length.
+ * With kv_pool_set_launch_overlap on for any of the pools, the call keeps the next launch
+ * from overlapping it (a decode would read the new lengths early).
  *   pools     host array of num_pools distinct pools of one size, type and device, one per
  *             layer, which share tables and lengths: one launch moves up to 128 of them;
  *   path, num_accepted, max_path  as kv_verify_tree leaves them; a path rises.

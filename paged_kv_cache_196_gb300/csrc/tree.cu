@@ -59,7 +59,6 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
     extern __shared__ __align__(16) char raw[];
     auto &sm = *reinterpret_cast<SimpleShared<D> *>(raw);
     const int tid = threadIdx.x, ty = tid / 8, tx = tid % 8;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this kernel's end
     const Place at = place(p.plan, blockIdx.x, sm.scratch, blockIdx.x == 0 ? p.err : nullptr);
     if (tid == 0 && p.cuts) p.cuts[blockIdx.x] = cut_of(p.plan, at, blockIdx.x, p.g);
     Pieces pieces;
@@ -213,7 +212,6 @@ constexpr int kMergeThreads = 256, kMergeAhead = 3;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const TreeParams p, int slot_rows) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const Cut cut = p.cuts[blockIdx.x + 1];
     if (cut.rows == 0) return;
     const int r0 = cut.r0, r1 = cut.r1, slot0 = cut.slot0, rows = cut.rows;
@@ -328,16 +326,12 @@ kv_status launch_simple(const TreeParams &pp, int d, cudaStream_t stream) {
 }
 
 kv_status launch_merge(const TreeParams &pp, int d, int slot_rows, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)pp.plan.runs - 1, slot_rows / 32);
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, d == 64 ? tree_merge_kernel<64> : tree_merge_kernel<128>, pp, slot_rows));
+    const dim3 grid((unsigned)pp.plan.runs - 1, (unsigned)slot_rows / 32);
+    if (d == 64)
+        tree_merge_kernel<64><<<grid, kMergeThreads, 0, stream>>>(pp, slot_rows);
+    else
+        tree_merge_kernel<128><<<grid, kMergeThreads, 0, stream>>>(pp, slot_rows);
+    return cuda_status(cudaGetLastError());
 }
 
 // How a call runs: what the workspace query and the call have to agree on.

@@ -279,8 +279,6 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                    const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
     using L = Layout<D, MT>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // the kernel that adds up cut pairs may start beside this one; it waits for its end
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) char smem_raw[];
     char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     char *sQ = smem, *ring = smem + L::kRing;

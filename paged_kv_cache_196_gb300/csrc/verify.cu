@@ -679,6 +679,10 @@ kv_status kv_keep_path(const kv_pool_t *pools, int num_pools, const int32_t *cu_
         tree::keep_kernel<<<(unsigned)n * (unsigned)batch, tree::kKeepThreads, 0, as_stream(stream)>>>(a);
         if (kv_status st = cuda_status(cudaGetLastError())) return st;
     }
+    // A decode launched to overlap the kernel before it reads its lengths early, and the new
+    // lengths were just written.  Anything but a kernel between the two ends the overlap.
+    for (int i = 0; i < num_pools; ++i)
+        if (pools[i]->launch_overlap) return cuda_status(cudaMemsetAsync(p->err + 1, 0, sizeof(int), as_stream(stream)));
     return KV_OK;
 }
 

@@ -193,6 +193,42 @@ def test_captured_and_replayed():
         case.close()
 
 
+def test_a_decode_that_overlaps_reads_the_new_lengths():
+    case = KeepCase("bf16", 128, 2, [700, 40, 300], [16, 9, 30], [3, 0, 7], layers=1, seed=4)
+    pool = case.pools[0]
+    try:
+        for x in views(pool, case.blocks, 2, 128, "bf16"):
+            x.copy_(torch.randn(x.shape, generator=torch.Generator().manual_seed(5)).bfloat16())
+        a = case.args()
+        q = torch.randn(3, 8, 128, generator=torch.Generator().manual_seed(6)).bfloat16().cuda()
+        n = pk.kv_decode_workspace_size(3, 8, 2, 128, case.width, 1)
+        ws = torch.empty(max(16, n), dtype=torch.uint8, device="cuda")
+        outs = [torch.zeros(3, 8, 128, device="cuda") for _ in range(2)]
+
+        def decode(lens, out):
+            pk.paged_decode_attention(pool, q, a["tables"], case.width, lens, 3, 8, 1 / math.sqrt(128), out, pk.KV_F32, None, 1,
+                                      ws, n)
+        case.call(a)
+        torch.cuda.synchronize()
+        lens = a["new"][:3].clone()
+        decode(lens, outs[0])
+        torch.cuda.synchronize()
+        a["count"].zero_()  # nothing moves again; the lengths shrink to the roots
+        case.paths = [[], [], []]
+        roots = torch.tensor([701, 41, 301], dtype=torch.int32, device="cuda")
+        decode(roots, outs[0])
+        torch.cuda.synchronize()
+        pk.kv_pool_set_launch_overlap(pool, True)
+        for _ in range(20):
+            a["new"].fill_(1)
+            case.call(a)
+            decode(a["new"], outs[1])
+            torch.cuda.synchronize()
+            assert torch.equal(outs[0], outs[1])
+    finally:
+        case.close()
+
+
 def test_offsets_past_32_bits():
     blocks = 140000
     case = KeepCase("bf16", 128, 8, [40], [9], [3], layers=1, seed=2)

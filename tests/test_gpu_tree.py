@@ -287,6 +287,44 @@ def test_on_a_stream_of_its_own():
         case.close()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_two_calls_at_once(dtype):
+    """One pool, two streams, a workspace each."""
+    case = TreeCase(dtype, 128, 2, 4, [3000, 20, 900], [40, 3, 64], seed=12)
+    try:
+        a, b = case.args("f32"), case.args("f32")
+        torch.cuda.synchronize()
+        s, t = torch.cuda.Stream(), torch.cuda.Stream()
+        for _ in range(8):
+            case.call(a, stream=s)
+            case.call(b, stream=t)
+        torch.cuda.synchronize()
+        case.check(a)
+        case.check(b)
+        assert torch.equal(a["out"], b["out"])
+    finally:
+        case.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_many_sequences_of_few_tokens(dtype):
+    # more than a thread of a CTA has to scan one by one; sequences without nodes in between
+    rng = np.random.default_rng(3)
+    run(TreeCase(dtype, 64, 1, 2, rng.integers(0, 20, 3000), rng.integers(0, 3, 3000), seed=6))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_shapes(seed):
+    rng = np.random.default_rng(1000 + seed)
+    dtype, d = ("f32", "bf16", "f16")[rng.integers(3)], (64, 128)[rng.integers(2)]
+    batch, g, hkv = int(rng.integers(1, 9)), int(rng.integers(1, 9)), int(rng.integers(1, 5))
+    most = int(np.exp(rng.uniform(0, np.log(256))))
+    top = int(np.exp(rng.uniform(0, np.log(4000))))
+    run(TreeCase(dtype, d, hkv, g, rng.integers(0, top + 1, batch), rng.integers(0, most + 1, batch),
+                 kind=("chain", "star", "tree", "forest")[rng.integers(4)], seed=seed, q_size=float(rng.choice([0.3, 1.0, 3.0]))),
+        out_dtype=(dtype, "f32")[rng.integers(2)], rows=int(rng.integers(0, 4)))
+
+
 def test_offsets_past_32_bits():
     # blocks at the far end of pools of more than 2^32 bytes each
     for dtype, d, hkv in (("bf16", 128, 8), ("f32", 64, 8)):
@@ -308,6 +346,26 @@ def test_offsets_past_32_bits():
         finally:
             small.close()
             pk.kv_pool_destroy(pool)
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("nodes", [3, 30, 70])
+def test_output_aligned_to_16_bytes_only(dtype, out_dtype, nodes):
+    case = TreeCase(dtype, 64, 2, 4, [300], [nodes])
+    try:
+        a = case.args(out_dtype)
+        n = 16 // a["out"].element_size()
+        buf = torch.full((a["out"].numel() + n,), 777.0, dtype=a["out"].dtype, device="cuda")
+        a["out"] = buf[n:].view(a["out"].shape)
+        q = torch.zeros(a["q"].numel() + 16 // a["q"].element_size(), dtype=a["q"].dtype, device="cuda")
+        q[16 // q.element_size():] = a["q"].flatten()
+        a["q"] = q[16 // q.element_size():].view(a["q"].shape)
+        assert a["out"].data_ptr() % 32 == 16 and a["q"].data_ptr() % 32 == 16
+        case.call(a)
+        case.check(a)
+        assert (buf[:n] == 777).all()
+    finally:
+        case.close()
 
 
 def test_no_workspace_under_few_blocks():
