@@ -342,7 +342,8 @@ struct Shape {
     int runs, pair_cost, min_run;
     bool whole;                   // no pair is cut
 };
-Shape shape_of(const kv_pool *p, int g, int max_q_len, int max_blocks) {
+// (the query, which does not know the output's type, takes the larger: that of 16-bit output)
+Shape shape_of(const kv_pool *p, int g, int max_q_len, int max_blocks, kv_dtype out_dtype) {
     const bool whole = max_blocks <= kWholeBlocks;
     if (p->dtype == KV_F32)
         return {kSimpleRows, kSimpleRows / g, kSimpleRows / g, 1, kSimplePerSm * sm_count(), 1, 3, whole};
@@ -350,7 +351,7 @@ Shape shape_of(const kv_pool *p, int g, int max_q_len, int max_blocks) {
     if (max_q_len <= 64 / g) {
         s.copies = max_q_len <= 32 / g ? 4 : 2;
         s.tile_nodes = s.group_nodes = 128 / s.copies / g;
-    } else if (max_q_len > s.tile_nodes) {
+    } else if (max_q_len > s.tile_nodes && !(p->dtype == KV_BF16 && out_dtype == KV_F32)) {
         s.slot_rows = 256;
         s.group_nodes = 2 * s.tile_nodes;
         s.pair_cost = 2;
@@ -389,7 +390,7 @@ kv_status kv_tree_workspace_size(kv_pool_t p, int batch, int num_q_heads, int ma
     if (kv_status st = tree::check(p, batch, num_q_heads, max_blocks, max_q_len)) return st;
     *bytes = 0;
     if (batch == 0 || max_q_len == 0) return KV_OK;
-    const tree::Shape s = tree::shape_of(p, num_q_heads / p->num_kv_heads, max_q_len, max_blocks);
+    const tree::Shape s = tree::shape_of(p, num_q_heads / p->num_kv_heads, max_q_len, max_blocks, p->dtype);
     *bytes = tree::workspace_bytes_of(s, p->head_dim);
     return KV_OK;
 }
@@ -408,7 +409,7 @@ kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, 
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(workspace)) & 15)
         return KV_ERR_ARG;
     const int g = num_q_heads / p->num_kv_heads;
-    const tree::Shape s = tree::shape_of(p, g, max_q_len, max_blocks);
+    const tree::Shape s = tree::shape_of(p, g, max_q_len, max_blocks, out_dtype);
     if (!s.whole && (!workspace || workspace_bytes < tree::workspace_bytes_of(s, p->head_dim))) return KV_ERR_ARG;
     tree::TreeParams pp{};
     pp.plan = {cu_q, seq_lens, batch, total_q, max_q_len, max_blocks, p->num_kv_heads, s.group_nodes,

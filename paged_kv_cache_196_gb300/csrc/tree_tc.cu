@@ -9,6 +9,8 @@
 //                  weights keep 16 significant bits with bf16, 22 with fp16 (a bf16
 //                  weight alone would be off by 2^-8 of itself, as much as a bf16 output)
 //   O += P_hi V + P_lo V   (P from tensor memory)
+// THREE: fp32 output of a bf16 pool, where 16 bits of a weight would be what is lost: a third
+// part, in the columns of the second O.
 // Roles: softmax warps (a thread = a row = a tensor-memory lane), a warp that copies K and V
 // tiles into one ring by TMA (each block-table entry becomes one box), a thread per row tile
 // that issues its products, a warp that describes the next piece and copies its queries.  The ring runs on across pieces.
@@ -24,7 +26,7 @@
 // from one wait to the next, and the product of half the weights begins while the other half is made.
 //
 // Tensor memory (512 columns): MT = 1: S at 0 and 128, O at 256 and 384, by tile and by piece
-// in turn; MT = 2: S_A, S_B, O_A, O_B.
+// in turn (THREE: one O, the third parts of both S at 384); MT = 2: S_A, S_B, O_A, O_B.
 //
 // Only tiles that reach into the tree are masked, by the bits of each row's node and of
 // those above it.  Their V rows are looked over before the product: a weight of zero does
@@ -46,7 +48,7 @@ namespace pkv {
 namespace tree {
 
 constexpr float kRenew = 8.0f;  // log2 units by which a maximum passes the reference before sums are scaled
-constexpr uint32_t kColO0 = 256;
+constexpr uint32_t kColO0 = 256, kColThird = 384;
 
 template <int D, int MT>
 struct Layout {
@@ -154,15 +156,19 @@ KV_DEVICE float tmem_max(uint32_t taddr) {
 // step of 2^-8 (bf16) or 2^-11 (fp16) each, what both leave is at most 2^-16 or 2^-22 of a weight.
 // (Cutting bf16 off instead of rounding it takes as long and leaves twice as much.)
 template <bool F16>
-KV_DEVICE void split(float2 e, uint32_t &hi, uint32_t &lo) {
+KV_DEVICE float2 split(float2 e, uint32_t &hi) {  // the rest, exact
     hi = F16 ? tc::pack_f16x2(e.x, e.y) : tc::pack_bf16x2(e.x, e.y);
     const float2 h = F16 ? f16x2_to_float2(hi) : bf16x2_to_float2(hi);
-    const float2 rest = __ffma2_rn(h, make_float2(-1.f, -1.f), e);
-    lo = F16 ? tc::pack_f16x2(rest.x, rest.y) : tc::pack_bf16x2(rest.x, rest.y);
+    return __ffma2_rn(h, make_float2(-1.f, -1.f), e);
+}
+template <bool F16>
+KV_DEVICE uint32_t round2(float2 e) {
+    return F16 ? tc::pack_f16x2(e.x, e.y) : tc::pack_bf16x2(e.x, e.y);
 }
 
 // D (+)= P B over 64 keys: P at p_tmem in steps of 16 keys, 8 columns each, two steps of every
-// 32 columns; B (V, MN-major) advances by `step` 16-byte units per 16 keys.
+// kGap columns; B (V, MN-major) advances by `step` 16-byte units per 16 keys.
+template <int kGap>
 KV_DEVICE void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc_first,
                       uint32_t step) {
     asm volatile(
@@ -172,11 +178,11 @@ KV_DEVICE void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t b_lo, uint32_t 
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t"
         "add.u32 x, %1, 8;\n\tadd.u32 y, %2, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 32;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, %7;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 40;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, %8;\n\tadd.u32 y, y, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t}" ::"r"(d_tmem),
-        "r"(p_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc_first), "r"(step)
+        "r"(p_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc_first), "r"(step), "n"(kGap), "n"(kGap + 8)
         : "memory");
 }
 
@@ -267,7 +273,7 @@ struct Ancestors {
     }
 };
 
-template <int D, bool F16, int MT, bool TW>
+template <int D, bool F16, int MT, bool TW, bool THREE = false>
 __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
@@ -463,9 +469,11 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 constexpr uint32_t step = 2 * L::kGroupBytes / 16;
                 const uint32_t b = same(v_lo + ((slot * L::kTileBytes) >> 4) + 4 * step * half);
                 const uint32_t d = same(tmem + col_o), w = same(tmem + col_p + 64 * half);
+                const uint32_t third = same(tmem + kColThird + col_p / 2 + 32 * half);
                 if (one) {
-                    mma_pv(d, w, b, d_hi, idesc_pv, !first, step);
-                    mma_pv(d, w + 16, b, d_hi, idesc_pv, 1, step);
+                    mma_pv<32>(d, w, b, d_hi, idesc_pv, !first, step);
+                    mma_pv<32>(d, w + 16, b, d_hi, idesc_pv, 1, step);
+                    if constexpr (THREE) mma_pv<16>(d, third, b, d_hi, idesc_pv, 1, step);
                 }
             };
             bool ok = true;
@@ -506,14 +514,16 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     if (!(ok = next_s())) break;
                     // (the weights last: between their arrival and their product nothing is left to do)
                     const int slot = (int)((2 * t + 1) % L::kSlots);
-                    if ((first && n >= 2 && !wait(&sm.oempty[n & 1], ((n >> 1) - 1) & 1)) ||
+                    const int free_at = THREE ? n - 1 : n - 2;  // the piece that had this O before
+                    if ((first && free_at >= 0 && !wait(&sm.oempty[free_at & 1], (free_at >> 1) & 1)) ||
                         !wait_full(2 * t + 1) || !wait(&sm.pfull[0][t & 1], (t >> 1) & 1)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
-                    issue_pv(kColO0 + 128 * (n & 1), (t & 1) * 128, slot, 0, first);
-                    issue_pv(kColO0 + 128 * (n & 1), (t & 1) * 128, slot, 1, false);
+                    const uint32_t col_o = kColO0 + (THREE ? 0 : 128 * (n & 1));
+                    issue_pv(col_o, (t & 1) * 128, slot, 0, first);
+                    issue_pv(col_o, (t & 1) * 128, slot, 1, false);
                     commit(&sm.empty[slot]);
                     commit(&sm.odone[0][t & 1]);
                     ++t;
@@ -650,7 +660,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 const int key0 = (pc.t0 + j) * kTile;
                 const bool tail = key0 + kTile > r.before;
                 const uint32_t gone = sm.gone[run_t & 7];
-                const uint32_t scol = tmem + lane_base + 128 * buf;
+                const uint32_t scol = tmem + lane_base + 128 * buf, third = tmem + lane_base + kColThird + 64 * buf;
                 bool rescale = false;
                 float alpha = 1.f;
                 auto arrive = [&](int which) {  // the weights are there
@@ -735,7 +745,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                             break;
                         }
                         tc::fence_after_sync();
-                        const uint32_t ocol = tmem + lane_base + kColO0 + 128 * (MT == 1 ? n & 1 : x);
+                        const uint32_t ocol = tmem + lane_base + kColO0 + (THREE ? 0 : 128 * (MT == 1 ? n & 1 : x));
 #pragma unroll 1
                         for (int i = 0; i < D / 16; ++i) {
                             uint32_t v[16];
@@ -752,16 +762,21 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-ref, -ref);
                     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     auto weigh = [&](uint32_t (&v)[32], int c) {
-                        uint32_t w[32];
+                        uint32_t w[32], w3[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             const float2 xx = __ffma2_rn(
                                 make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sc2, nm2);
                             const float2 e = make_float2(tc_ex2(xx.x), tc_ex2(xx.y));
                             acc[k & 1] = __fadd2_rn(acc[k & 1], e);
-                            split<F16>(e, w[k], w[16 + k]);
+                            const float2 rest = split<F16>(e, w[k]);
+                            if constexpr (THREE)
+                                w3[k] = round2<F16>(split<F16>(rest, w[16 + k]));
+                            else
+                                w[16 + k] = round2<F16>(rest);
                         }
                         tc::tmem_st32(scol + 32 * c, w);
+                        if constexpr (THREE) tc::tmem_st16(third + 16 * c, w3);
                     };
                     tc::tmem_wait_ld();
 #pragma unroll 1
@@ -782,7 +797,15 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         for (int k = 0; k < 32; ++k) zero[k] = 0;
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c)
-                            if (c < c0 || c >= c1) tc::tmem_st32(scol + 32 * c, zero);
+                            if (c < c0 || c >= c1) {
+                                tc::tmem_st32(scol + 32 * c, zero);
+                                if constexpr (THREE) {
+                                    uint32_t zero16[16];
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) zero16[k] = 0;
+                                    tc::tmem_st16(third + 16 * c, zero16);
+                                }
+                            }
                     }
                 }
                 if constexpr (MT == 1) {
@@ -804,7 +827,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             }
             if (!ok || tiles == 0) break;
             tc::fence_after_sync();
-            const uint32_t ocol = tmem + lane_base + kColO0 + 128 * (MT == 1 ? n & 1 : x);
+            const uint32_t ocol = tmem + lane_base + kColO0 + (THREE ? 0 : 128 * (MT == 1 ? n & 1 : x));
             const bool nonfinite = *reinterpret_cast<volatile int *>(&sm.nonfinite[n & 1]) == n;
             float factor = 1.f;
             if (MT == 1 && p.copies > 1) {
@@ -965,8 +988,13 @@ kv_status launch(const TreeParams &pp, bool f16, const CUtensorMap &tk, const CU
     if (!encode_q_map(&tq, pp.q, pp.total_q, pp.hq, pp.g, pp.plan.tile_nodes, D)) return KV_ERR_CUDA;
     constexpr int smem = L::kBars + (int)sizeof(Shared<D, MT>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    auto fn = test_waits_enabled() ? (f16 ? tree_tc_kernel<D, true, MT, true> : tree_tc_kernel<D, false, MT, true>)
-                                   : (f16 ? tree_tc_kernel<D, true, MT, false> : tree_tc_kernel<D, false, MT, false>);
+    auto pick = [&](auto tw) {
+        constexpr bool TW = decltype(tw)::value;
+        if constexpr (MT == 1)
+            if (!f16 && pp.out_type == KV_F32) return tree_tc_kernel<D, false, 1, TW, true>;
+        return f16 ? tree_tc_kernel<D, true, MT, TW> : tree_tc_kernel<D, false, MT, TW>;
+    };
+    auto fn = test_waits_enabled() ? pick(std::true_type{}) : pick(std::false_type{});
     if (kv_status st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
         return st;
     fn<<<pp.plan.runs, L::kThreads, smem, stream>>>(tq, tk, tv, pp);

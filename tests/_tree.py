@@ -8,10 +8,10 @@ its distance to the reference adds roundings of 2^-24 of the score's and the dis
 log2 units: times log2 e, and back).  So a score is off by
   ds = scale A (D + 2) 2^-24 + 4 |s|max 2^-24,
 with |s|max <= scale A, a weight by the factor exp(ds) and the exponential's own 2^-22, and,
-where it is held in two parts of a 16-bit type of half step h, by h^2.  Sums over n keys, in
+where it is held in two parts of a 16-bit type of half step h, by h^2 (in three, by h^3).  Sums over n keys, in
 any order and piecewise: n 2^-24 of the sum of magnitudes, numerator and denominator; the
 merge of up to n pieces scales each once more (2^-22).  With |o| <= V = max |v|:
-  |error of o| <= V (2 ds + 2 (2^-21 + h^2) + 2 n 2^-24) + half step of the output * |o|
+  |error of o| <= V (2 ds + 2 (2^-21 + h^2 or h^3) + 2 n 2^-24) + half step of the output * |o|
   |error of lse| <= ds + 2^-21 + n 2^-24 + 4 |lse| 2^-24.
 (h^2 once for the numerator; twice leaves room for second order terms.)
 """
@@ -132,13 +132,14 @@ class TreeCase:
                                 self.width, a["lens"], self.batch, self.hq, self.scale, a["out"], KV[a["out_dtype"]],
                                 a["lse"] if lse else None, a["ws"], a["ws_bytes"], stream=stream)
 
-    def reference(self, gone=()):
+    def reference(self, gone=(), out_dtype=None):
         """out, lse in 64 bits and the bounds of their errors; `gone`: (sequence, block index) pairs whose
         keys are left out."""
         out = np.zeros((self.total, self.hq, self.d))
         lse = np.full((self.total, self.hq), -np.inf)
         out_tol, lse_tol = np.zeros(out.shape), np.zeros(lse.shape)
         h = 0.0 if self.dtype == "f32" else HALF[self.dtype]
+        parts = h ** (3 if (self.dtype, out_dtype) == ("bf16", "f32") else 2)
         for b, (n, t) in enumerate(zip(self.lens, self.nodes)):
             if not t:
                 continue
@@ -172,7 +173,7 @@ class TreeCase:
                     a = np.where(seen, np.abs(q[:, hq]) @ np.abs(kh).T * self.scale, 0).max(1)
                 ds = a * (self.d + 6) * 2.0 ** -24
                 big = np.abs(np.where(seen[:, :, None], vh[None], 0)).max((1, 2)) if n else np.zeros(t)
-                out_tol[r0:r0 + t, hq] = (big * (2 * ds + 2 * (2.0 ** -21 + h * h) + 2 * n * 2.0 ** -24))[:, None]
+                out_tol[r0:r0 + t, hq] = (big * (2 * ds + 2 * (2.0 ** -21 + parts) + 2 * n * 2.0 ** -24))[:, None]
                 lse_tol[r0:r0 + t, hq] = ds + 2.0 ** -21 + n * 2.0 ** -24 + 4 * 2.0 ** -24 * np.abs(
                     np.where(np.isfinite(lse[r0:r0 + t, hq]), lse[r0:r0 + t, hq], 0))
         return out, lse, out_tol, lse_tol
@@ -180,7 +181,7 @@ class TreeCase:
     def check(self, a, gone=(), err=0, rows=None):
         torch.cuda.synchronize()
         assert pk.kv_get_device_error(self.pool) == err
-        out, lse, out_tol, lse_tol = self.reference(gone)
+        out, lse, out_tol, lse_tol = self.reference(gone, a["out_dtype"])
         got, got_lse = a["out"].double().cpu().numpy()[:self.total], a["lse"].double().cpu().numpy()[:self.total]
         keep = np.ones(self.total, bool) if rows is None else rows
         with np.errstate(invalid="ignore"):

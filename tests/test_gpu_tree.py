@@ -78,6 +78,18 @@ def test_long_and_short(dtype, q_size):
     run(TreeCase(dtype, 128, 2, 4, [9000, 3, 500, 0], [13, 8, 1, 2], q_size=q_size, seed=5), out_dtype="f32")
 
 
+# the output that shows how the weights are held; many pieces to a CTA and many CTAs to a sequence
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nodes", [3, 16, 40, 90])
+@pytest.mark.parametrize("batch,cached", [(2, 2500), (50, 300)])
+def test_output_in_32_bits(dtype, d, nodes, batch, cached):
+    rng = np.random.default_rng(nodes)
+    run(TreeCase(dtype, d, 4, 4 if batch == 2 else 2, rng.integers(0, cached, batch),
+                 rng.integers(1 if batch == 2 else 0, nodes + 1, batch), width=40, seed=nodes), out_dtype="f32",
+        max_q_len=nodes)
+
+
 def test_table_wider_than_the_sequences():
     run(TreeCase("bf16", 128, 2, 4, [40, 700], [8, 8], width=5000))
 
