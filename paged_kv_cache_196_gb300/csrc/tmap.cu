@@ -81,6 +81,8 @@ kv_status pool_tensor_maps(kv_pool *p) {
 }
 
 kv_status pool_group_maps(kv_pool *p) {
+    static std::mutex making;  // two threads' first calls
+    std::lock_guard<std::mutex> lock(making);
     if (p->gmaps_ready) return KV_OK;
     if (p->dtype == KV_F32 || p->dtype == KV_I4) return KV_ERR_UNSUPPORTED;
     const long long rows = (long long)p->num_blocks * p->num_kv_heads * 16;

@@ -38,6 +38,9 @@ KV_DEVICE float ex2(float x) {
 // multiply-adds: thread
 // (ty, tx) holds rows 2 ty, 2 ty + 1, scores keys tx + 8 j and sums dimensions
 // 4 tx + 32 i.  A warp owns eight rows, so their statistics and weights need no barrier.
+// Bound by latency: two CTAs an SM of four warps each wait for shared memory and for their
+// own sums.  Five ragged trees of 3 to 33 nodes over an fp32 pool (12 heads over 4, head_dim 64, to 1531
+// tokens): 37.7 us where K and V take 1.3 to read; 55 for the first version.
 constexpr int kSimpleRows = 32, kSimpleKeys = 32, kSimpleThreads = 128;
 
 template <int D>
@@ -208,6 +211,10 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
 // CTA x looks at the end of run x: if it lies among the tiles of a pair, the pair is cut,
 // and this CTA (with those of other y) takes one share of its rows, one share per cut.  A
 // warp takes 8 rows of 16 dimensions, so that it reads lines and writes sectors whole.
+// Latency again: 3 to 6 us for slots of 128 rows, 12 for 256 rows (up to 40 MB of them); all pieces
+// of a pair are read at once (three, and most pairs have two), before any is used.  A launch that
+// overlaps the attention's end gains nothing: its CTAs find no room beside one that takes a
+// whole SM.
 constexpr int kMergeThreads = 256, kMergeAhead = 3;
 
 template <int D>
@@ -314,8 +321,6 @@ constexpr int kSimplePerSm = 2;  // CTAs
 // sequences of 44 to 408 tokens: 13.1 us whole, 14.7 cut.
 constexpr int kWholeBlocks = 32;
 
-
-
 kv_status launch_simple(const TreeParams &pp, int d, cudaStream_t stream) {
     auto fn = d == 64 ? tree_simple_kernel<64> : tree_simple_kernel<128>;
     const int smem = d == 64 ? (int)sizeof(SimpleShared<64>) : (int)sizeof(SimpleShared<128>);
@@ -334,7 +339,13 @@ kv_status launch_merge(const TreeParams &pp, int d, int slot_rows, cudaStream_t 
     return cuda_status(cudaGetLastError());
 }
 
-// How a call runs: what the workspace query and the call have to agree on.
+// How a call runs: what the workspace query and the call have to agree on.  pair_cost (tree_plan.cuh)
+// is what a piece's beginning and end take in key tiles' times, measured: 64 ragged sequences 1 to
+// 5 give 131.5, 124.5, 123.1, 124.0 and 125.0 us, 16 trees of two row tiles 111.7, 105.8, 107.2,
+// 108.6 and 110.7.  min_run, the least of a run where a batch leaves CTAs without work: one row tile, a
+// sequence of 3000 tokens (8 heads over 2): 17.9 us with 4, 18.3 with 5, 18.9 with 6, 20.8 with 8 and
+// 24.8 with 12; two, a sequence of 8000 with 64 nodes (16 over 2): 29.8 us with 3, 27.6 with 4, 28.7
+// with 6, 31.6 with 8.
 struct Shape {
     int slot_rows;                // rows of a slot of partial results
     int tile_nodes, group_nodes;  // nodes of a row tile and of a group
@@ -342,12 +353,14 @@ struct Shape {
     int runs, pair_cost, min_run;
     bool whole;                   // no pair is cut
 };
-// (the query, which does not know the output's type, takes the larger: that of 16-bit output)
+// Copies as many as fit, two row tiles where a tree has more rows than one (and they have room: the
+// third part of the weights takes it).  The query, which does not know the output's type, takes the
+// larger workspace: that of 16-bit output.
 Shape shape_of(const kv_pool *p, int g, int max_q_len, int max_blocks, kv_dtype out_dtype) {
     const bool whole = max_blocks <= kWholeBlocks;
     if (p->dtype == KV_F32)
         return {kSimpleRows, kSimpleRows / g, kSimpleRows / g, 1, kSimplePerSm * sm_count(), 1, 3, whole};
-    Shape s{128, 128 / g, 128 / g, 1, sm_count(), 3, 5, whole};
+    Shape s{128, 128 / g, 128 / g, 1, sm_count(), 3, 4, whole};
     if (max_q_len <= 64 / g) {
         s.copies = max_q_len <= 32 / g ? 4 : 2;
         s.tile_nodes = s.group_nodes = 128 / s.copies / g;

@@ -6,14 +6,18 @@
 //   S = Q K^T      (M = 128 rows, N = 128 keys, fp32 in tensor memory)
 //   softmax warps  S -> P, written over S: of every 32 keys' columns the first 16 hold
 //                  P_hi = t(P) in the pool's type t, the others P_lo = t(P - P_hi), so the
-//                  weights keep 16 significant bits with bf16, 22 with fp16 (a bf16
-//                  weight alone would be off by 2^-8 of itself, as much as a bf16 output)
+//                  weights keep 16 significant bits with bf16, 22 with fp16.  (A bf16
+//                  weight alone would be off by 2^-8 of itself, as much as a bf16 output.  It
+//                  would take 160 us for the four long contexts below when two parts took 195.)
 //   O += P_hi V + P_lo V   (P from tensor memory)
 // THREE: fp32 output of a bf16 pool, where 16 bits of a weight would be what is lost: a third
-// part, in the columns of the second O.
+// part, in the columns of the second O.  Relative error 1.6e-6 where two parts have 2.3e-6 (the tensor
+// cores' own sums, which are cut off and not rounded, are 1.1e-6 of it); 7% more time for the ragged
+// batch below, 17% and 37% for the trees that take two row tiles otherwise.
 // Roles: softmax warps (a thread = a row = a tensor-memory lane), a warp that copies K and V
-// tiles into one ring by TMA (each block-table entry becomes one box), a thread per row tile
-// that issues its products, a warp that describes the next piece and copies its queries.  The ring runs on across pieces.
+// tiles into one ring by TMA (each block-table entry becomes one box), a warp per row tile
+// that issues its products, a warp that describes the next piece and copies its queries.
+// The ring runs on across pieces.
 //
 // MT = 1: S is double-buffered, so the next tile's scores are computed while the softmax warps
 // work on this one's; Q and O are too, so a piece's end overlaps the next piece's beginning.
@@ -22,8 +26,23 @@
 // each copy's warps take their own keys of the tile and leave zeros as the others' weights,
 // so that all four schedulers share the exponentials; the copies' sums meet at the piece's
 // end.  MT = 2: each row tile has one S and one O, and works while the other's products run; a
-// thread of its own issues each row tile's products, since a thread takes hundreds of cycles
-// from one wait to the next, and the product of half the weights begins while the other half is made.
+// warp of its own issues each row tile's products, since one takes hundreds of cycles
+// from one wait to the next, and the product of half the weights begins while the other half is
+// made.  The row tiles end a key tile in turn: side by side they fall into step, and both wait for
+// the tensor core at once, then it for both (four long contexts 156 us in turn, 186 side by side).
+//
+// What bounds it, measured (times with the kernel that adds up cut pairs, 16-bit output, head_dim
+// 128, a GPU that copies 6.69 TB/s and multiplies 1.96 PFLOP/s).  MT = 1, 64 sequences of 512 to
+// 4096 tokens, 1 to 17 nodes, 32 heads over 8: 114 us; the 92 us of reading K and V at that rate,
+// and what a CTA's start (6 us until the first product), the pieces' ends (3 to 4 us each) and the
+// adding up (3 to 6) do not hide.  MT = 2, 16 sequences of 1000 to 8000 and 64 nodes: 99.5 us where K
+// and V take 47 and one product each of Q K^T and P V 39; four sequences of 32768 to 131072 with
+// 26 nodes, 32 heads over 4: 156 us where they take 92 and 65.  There a key tile of 128 takes
+// 4200 clocks, 3264 of them products (two row tiles, 8 + 2 x 8 instructions of 65 to 70 clocks each);
+// the rest is the chain S, weights, product of one row tile that the other does not cover.
+// Loops over the weights stay rolled: unrolled they pass the instruction cache, and every warp
+// waits for code.  K and V leave L2 first, so that partial results stay: 114 us for the ragged batch,
+// 121 without.
 //
 // Tensor memory (512 columns): MT = 1: S at 0 and 128, O at 256 and 384, by tile and by piece
 // in turn (THREE: one O, the third parts of both S at 384); MT = 2: S_A, S_B, O_A, O_B.
@@ -92,6 +111,26 @@ struct Shared {
     uint2 parents[2][32];          // of the piece's tree, 8 nodes a lane (Ancestors)
     PlaceScratch<Layout<D, MT>::kThreads> scratch;
 };
+
+// A pipeline wait.  Under a limit of zero a poll that does not suspend the thread (a suspending one may
+// last longer than a short run's waits, and none would run out).
+template <bool TW>
+KV_DEVICE bool pipe_wait(uint64_t *bar, uint32_t parity, int *err) {
+    if constexpr (TW)
+        if (g_wait_limit_ns == 0) {
+            uint32_t done;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(done)
+                : "r"(smem_addr(bar)), "r"(parity)
+                : "memory");
+            if (!done) atomicOr(err, KV_DEVERR_TIMEOUT);
+            return done != 0;
+        }
+    return mbar_wait<TW>(bar, parity, err);
+}
 
 KV_DEVICE float tc_ex2(float x) {
     float y;
@@ -352,7 +391,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
 #pragma unroll
                 for (int is_v = 0; is_v < 2; ++is_v) {
                     if (lane == 0)
-                        stop = *abort_flag || (issued >= L::kSlots && !mbar_wait<TW>(&sm.empty[slot], phase ^ 1, p.err));
+                        stop = *abort_flag || (issued >= L::kSlots && !pipe_wait<TW>(&sm.empty[slot], phase ^ 1, p.err));
                     stop = __shfl_sync(0xffffffffu, stop, 0);
                     if (stop) break;
                     char *dst = ring + slot * L::kTileBytes;
@@ -396,7 +435,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             const int buf = n % L::kQBufs;
             if (lane == 0)
                 ok = !*abort_flag &&
-                     (n < L::kQBufs || mbar_wait<TW>(&sm.qempty[buf], (n / L::kQBufs - 1) & 1, p.err));
+                     (n < L::kQBufs || pipe_wait<TW>(&sm.qempty[buf], (n / L::kQBufs - 1) & 1, p.err));
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             if (!more) pc.t0 = pc.t1 = 0;
@@ -446,7 +485,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 if (one) mbar_arrive(bar);
             };
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                return __all_sync(0xffffffffu, mbar_wait<TW>(bar, parity, p.err));
+                return __all_sync(0xffffffffu, pipe_wait<TW>(bar, parity, p.err));
             };
             constexpr uint32_t idesc_qk = F16 ? tc::idesc_f16_f32(128, 128, false, false)
                                               : tc::idesc_bf16_f32(128, 128, false, false);
@@ -622,7 +661,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
         int n = 0;           // pieces
         bool ok = true;
         while (true) {
-            ok = mbar_wait<TW>(&sm.qfull[n % L::kQBufs], (n / L::kQBufs) & 1, p.err);
+            ok = pipe_wait<TW>(&sm.qfull[n % L::kQBufs], (n / L::kQBufs) & 1, p.err);
             ok = !__any_sync(0xffffffffu, !ok);
             Piece pc{};
             uint2 parents = make_uint2(0, 0);
@@ -651,7 +690,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             for (int j = 0; j < tiles; ++j, ++t, ++run_t) {
                 const int buf = MT == 1 ? (int)(t & 1) : x;
                 bool bad = *abort_flag != 0;
-                if (!bad) bad = !mbar_wait<TW>(&sm.sfull[buf], (MT == 1 ? t >> 1 : t) & 1, p.err);
+                if (!bad) bad = !pipe_wait<TW>(&sm.sfull[buf], (MT == 1 ? t >> 1 : t) & 1, p.err);
                 if (__any_sync(0xffffffffu, bad)) {
                     ok = false;
                     break;
@@ -672,7 +711,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 if (tail && x == 0) {
                     // the rows of V that lie in the tree or behind it
                     const unsigned pos = 2 * run_t + 1;
-                    if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1, p.err))) {
+                    if (__any_sync(0xffffffffu, !pipe_wait<TW>(&sm.full[pos % L::kSlots], (pos / L::kSlots) & 1, p.err))) {
                         ok = false;
                         break;
                     }
@@ -740,7 +779,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                     if (__any_sync(0xffffffffu, rescale)) {
                         // O holds the products up to the tile before once that one's are done
-                        if (__any_sync(0xffffffffu, !mbar_wait<TW>(&sm.odone[x][(t - 1) & 1], ((t - 1) >> 1) & 1, p.err))) {
+                        if (__any_sync(0xffffffffu, !pipe_wait<TW>(&sm.odone[x][(t - 1) & 1], ((t - 1) >> 1) & 1, p.err))) {
                             ok = false;
                             break;
                         }
@@ -817,7 +856,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
             }
             // ---- the piece's end
             if (ok && tiles > 0) {
-                const bool bad = !mbar_wait<TW>(&sm.odone[x][(t - 1) & 1], ((t - 1) >> 1) & 1, p.err);
+                const bool bad = !pipe_wait<TW>(&sm.odone[x][(t - 1) & 1], ((t - 1) >> 1) & 1, p.err);
                 ok = !__any_sync(0xffffffffu, bad);
             }
             // MT = 1: all warps stay or leave together; they meet once for every piece and for the end

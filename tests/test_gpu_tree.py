@@ -1,5 +1,7 @@
 """Attention of a tree of drafted tokens over the paged cache against the formula in 64 bits."""
 import math
+import threading
+from concurrent.futures import ThreadPoolExecutor
 
 import numpy as np
 import pytest
@@ -314,6 +316,28 @@ def test_two_calls_at_once(dtype):
         case.check(a)
         case.check(b)
         assert torch.equal(a["out"], b["out"])
+    finally:
+        case.close()
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_first_calls_of_two_host_threads(seed):
+    """They make what the pool keeps for its calls (its tensor maps) together."""
+    case = TreeCase("bf16", 128, 2, 4, [700, 20], [9, 3], seed=seed, width=40)
+    try:
+        a = [case.args("f32") for _ in range(2)]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        start = threading.Barrier(2)
+
+        def one(i):
+            start.wait(timeout=30)
+            case.call(a[i], stream=streams[i])
+        with ThreadPoolExecutor(2) as pool:
+            list(pool.map(one, range(2)))
+        torch.cuda.synchronize()
+        case.check(a[0])
+        case.check(a[1])
     finally:
         case.close()
 
