@@ -53,7 +53,7 @@ namespace tree {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 512, kVerifyMost = 1024;  // of a CTA (verify_threads)
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kChunk = 512;           // tokens
 constexpr int kMaxVocab = 1 << 20;
@@ -217,7 +217,7 @@ KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const
     const bool p_wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0, q_wide = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
     const float lo_scale = __uint_as_float((uint32_t)(127 + a.scale_exp - 22) << 23);
     const int shift = a.scale_exp - 22;
-    for (int c = warp; c < chunks; c += kVerifyWarps) {
+    for (int c = warp; c < chunks; c += (int)blockDim.x / 32) {
         const long long first = ((long long)rank * chunks + c) * kChunk;
         unsigned long long sum = 0;
         if (first < a.vocab) {
@@ -331,7 +331,7 @@ KV_DEVICE int find(const VerifyParams &a, VerifyShared &sm, int chunks, int rank
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyParams a) {
+__global__ void __launch_bounds__(kVerifyMost, 1) verify_kernel(const VerifyParams a) {
     __shared__ VerifyShared sm;
     const cg::cluster_group cluster = cg::this_cluster();
     const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
         nodes = 0;
     }
     const int T = (int)nodes;
-    for (int i = tid; i < T; i += kVerifyThreads) {
+    for (int i = tid; i < T; i += (int)blockDim.x) {
         int up = i == 0 ? -1 : a.parents ? __ldg(a.parents + q0 + i) : i - 1;
         const int x = __ldg(a.tokens + q0 + i);
         if (i > 0) {
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
     if (rank == 0) {
         __syncthreads();
         if (tid == 0) a.num_accepted[b] = count;
-        for (int i = tid; i <= a.max_path; i += kVerifyThreads) {
+        for (int i = tid; i <= a.max_path; i += (int)blockDim.x) {
             const int at = i < count ? sm.path[i] : -1;
             if (i < a.max_path) a.path[(long long)b * a.max_path + i] = at;
             if (i != count || total == 0) a.out_tokens[(long long)b * (a.max_path + 1) + i] = at < 0 ? -1 : sm.token[at];
@@ -575,12 +575,18 @@ int cluster_size(int vocab, int batch) {
     return n;
 }
 
+// Threads of a CTA: as many as an SM takes where clusters leave one CTA to an SM and chunks to every warp.
+int verify_threads(int vocab, int batch, int cluster) {
+    const int chunks = ((vocab + kChunk - 1) / kChunk + cluster - 1) / cluster;
+    return chunks > kVerifyWarps && (long long)cluster * batch <= sm_count() ? kVerifyMost : kVerifyThreads;
+}
+
 template <typename E>
 kv_status launch_verify(const VerifyParams &a, cudaStream_t stream) {
     const int n = cluster_size(a.vocab, a.batch);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.batch * (unsigned)n);
-    cfg.blockDim = dim3(kVerifyThreads);
+    cfg.blockDim = dim3((unsigned)verify_threads(a.vocab, a.batch, n));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
