@@ -4,7 +4,8 @@
 // children were drawn from.  A child with token x is accepted if u q(x) < p(x); after a
 // rejection the next child, and in the end the draw of the next token, meet the residual
 // max(p - q, 0) / sum.  Without the division: with W_0 = p, S_0 = 1,
-//   W_{k+1} = max(W_k - S_k q, 0),  S_{k+1} = sum W_{k+1},  accept iff u q(x) S_k < W_k(x),
+//   W_{k+1} = max(W_k - S_k q, 0),  S_{k+1} = sum W_{k+1},  accept iff u q(x) S_k < W_k(x);
+// nothing that went to zero returns, so W_k = max(p - (S_0 + .. + S_{k-1}) q, 0) at once,
 // and the draw is the first index whose running sum of W_k passes u S_k.  Drafts that were
 // chosen (q null) count as drawn from a q that is one at x: W loses its entry at x.
 //
@@ -76,7 +77,6 @@ struct VerifyParams {
 struct VerifyShared {
     unsigned long long chunk[kCtaChunks];
     unsigned long long totals[2][kMaxCluster];  // of the cluster's CTAs, for passes in turn
-    unsigned long long left[kMaxNodes];         // S_k of the node
     float p[kMaxNodes], q[kMaxNodes], u[kMaxNodes];  // of each node's token, in its parent's rows
     int32_t token[kMaxNodes];
     int16_t parent[kMaxNodes];                  // -1: none, or no draft
@@ -175,17 +175,26 @@ KV_DEVICE unsigned long long mul_shift(unsigned long long a, unsigned long long 
     return shift ? (lo >> shift) | (hi << (64 - shift)) : lo;
 }
 
-// W_k of a token from its W_1 and q, k > 1: `left` holds S_1 .. S_{k-1} from its second entry on.
-// (A function of its own: in line, sixteen times over, it is more code than the rest of a pass,
-// and a launch begins with empty instruction caches.)
-__device__ __noinline__ unsigned long long residual(unsigned long long w, float q, int k, const unsigned long long *left,
-                                                    int e) {
-    const unsigned long long steps = fixed(q, e);
-    for (int i = 1; i < k; ++i) {
-        const unsigned long long x = mul_shift(left[i], steps, e);
-        w = w > x ? w - x : 0;
+// S_1 + .. + S_{k-1}, as the factor of a product whose upper half is floor(of it times q / 2^E): shifted to
+// the left as far as it goes (it is below 2^63), q the rest of the 64 - E places.
+struct Taken {
+    unsigned long long s;
+    int q_shift, e;
+    KV_DEVICE Taken(unsigned long long sum, int scale_exp) : e(scale_exp) {
+        const int a = min(__clzll((long long)sum), 64 - e);
+        s = sum << a;
+        q_shift = 64 - e - a;
     }
-    return w;
+    // W_k, k > 1
+    KV_DEVICE unsigned long long weight(float p, float q) const {
+        const unsigned long long a = fixed(p, e), b = fixed(q, e), x = b + __umul64hi(s, b << q_shift);
+        return a > x ? a - x : 0;
+    }
+};
+// Of four tokens.  (A function of its own: in line, four times over, it is more code than the rest of
+// a pass, and a launch begins with empty instruction caches.)
+__device__ __noinline__ unsigned long long weights(float4 p, float4 q, const Taken t) {
+    return t.weight(p.x, q.x) + t.weight(p.y, q.y) + t.weight(p.z, q.z) + t.weight(p.w, q.w);
 }
 
 // W_1 of a token, W_0 where k is 0.
@@ -208,7 +217,7 @@ KV_DEVICE void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory
 // `gone`: nodes whose tokens have lost their weight.  The whole cluster calls it.
 template <typename T>
 KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const cg::cluster_group &cluster, long long row,
-                                  int k, int gone, int turn, bool first_pass) {
+                                  int k, unsigned long long taken, int gone, int turn, bool first_pass) {
     const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int chunks = ((a.vocab + kChunk - 1) / kChunk + ctas - 1) / ctas;  // a CTA's share
@@ -217,6 +226,7 @@ KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const
     const bool p_wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0, q_wide = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
     const float lo_scale = __uint_as_float((uint32_t)(127 + a.scale_exp - 22) << 23);
     const int shift = a.scale_exp - 22;
+    const Taken t(taken, a.scale_exp);
     for (int c = warp; c < chunks; c += (int)blockDim.x / 32) {
         const long long first = ((long long)rank * chunks + c) * kChunk;
         unsigned long long sum = 0;
@@ -237,8 +247,9 @@ KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const
                 sum = ((unsigned long long)hi << shift) + (long long)(int32_t)lo;
             } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    sum += residual(first_residual(x[i], y[i], 1, a.scale_exp), y[i], k, sm.left, a.scale_exp);
+                for (int i = 0; i < 16; i += 4)
+                    sum += weights(make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]),
+                                   make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]), t);
             }
         }
         sum = warp_sum(sum);
@@ -268,8 +279,8 @@ KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const
 // The first token whose running sum of W_k passes `point`, counted from this CTA's share on
 // (one warp; the share holds it).
 template <typename T>
-KV_DEVICE int find(const VerifyParams &a, VerifyShared &sm, int chunks, int rank, long long row, int k, int gone,
-                   unsigned long long point) {
+KV_DEVICE int find(const VerifyParams &a, VerifyShared &sm, int chunks, int rank, long long row, int k,
+                   unsigned long long taken, int gone, unsigned long long point) {
     const int lane = threadIdx.x & 31;
     int c = 0;
     for (int base = 0; base < chunks; base += 32) {
@@ -302,9 +313,15 @@ KV_DEVICE int find(const VerifyParams &a, VerifyShared &sm, int chunks, int rank
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int at = chunk_index<T>(i, wide);
-        unsigned long long w = first_residual(x[i], y[i], k, a.scale_exp);
-        if (k > 1) w = residual(w, y[i], k, sm.left, a.scale_exp);
-        sm.weight[at + at / 16] = w;
+        sm.weight[at + at / 16] = first_residual(x[i], y[i], k, a.scale_exp);
+    }
+    if (k > 1) {
+        const Taken t(taken, a.scale_exp);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int at = chunk_index<T>(i, wide);
+            sm.weight[at + at / 16] = weights(make_float4(x[i], 0.f, 0.f, 0.f), make_float4(y[i], 0.f, 0.f, 0.f), t);
+        }
     }
     __syncwarp();
     for (int i = lane; i < gone; i += 32) {
@@ -369,7 +386,8 @@ __global__ void __launch_bounds__(kVerifyMost, 1) verify_kernel(const VerifyPara
 
     const double unit = __longlong_as_double((long long)(1023 - a.scale_exp) << 52);
     const int chunks = ((a.vocab + kChunk - 1) / kChunk + ctas - 1) / ctas;
-    unsigned long long total = 0;  // of the pass over W_k, once there was one
+    unsigned long long total = 0;  // of the pass over W_k, once there was one: S_k
+    unsigned long long taken = 0;  // S_1 + .. + S_{k-1}
     int node = 0, count = 0, turn = 0;
     int k = 0, gone = 0;           // rejections at the node
     int last = 0;                  // its child that was tried last
@@ -402,7 +420,7 @@ __global__ void __launch_bounds__(kVerifyMost, 1) verify_kernel(const VerifyPara
                 } else {
                     w = sm.p[child];
                     if (drawn) {
-                        for (int i = 0; i < k; ++i) w = fmax(w - (i ? (double)sm.left[i] * unit : 1.0) * sm.q[child], 0.0);
+                        w = fmax(w - (1.0 + (double)taken * unit) * sm.q[child], 0.0);
                     } else {
                         for (int i = 0; i < gone; ++i)
                             if (sm.token[sm.gone[i]] == sm.token[child]) w = 0.0;
@@ -433,23 +451,24 @@ __global__ void __launch_bounds__(kVerifyMost, 1) verify_kernel(const VerifyPara
         if (sm.node != node) summed = false;
         node = sm.node, count = sm.count, k = sm.rejected, gone = sm.gone_count;
         if (sm.end) break;
-        total = pass<E>(a, sm, cluster, q0 + node, k, 0, turn, first_pass);
+        // (at the node's k-th rejection the last pass was over W_{k-1}; 2^63 is never reached by rows that sum to one)
+        taken = k < 2 ? 0 : min((k == 2 ? 0 : taken) + total, ~0ull >> 1);
+        total = pass<E>(a, sm, cluster, q0 + node, k, taken, 0, turn, first_pass);
         turn ^= 1;
         summed = true;
         first_pass = false;
         if (warp == 0) left = (double)total * unit;
-        if (tid == 0) sm.left[k] = total;
     }
     int token = -1;
     if (T > 0) {
         if (!summed) {
-            total = pass<E>(a, sm, cluster, q0 + node, 0, gone, turn, first_pass);
+            total = pass<E>(a, sm, cluster, q0 + node, 0, 0, gone, turn, first_pass);
             turn ^= 1;
             first_pass = false;
         }
         if (total == 0 && (k > 0 || gone > 0)) {  // nothing is left: p itself
             k = gone = 0;
-            total = pass<E>(a, sm, cluster, q0 + node, 0, 0, turn, first_pass);
+            total = pass<E>(a, sm, cluster, q0 + node, 0, 0, 0, turn, first_pass);
             turn ^= 1;
         }
         // floor(u total): u is a whole number of 2^-shift
@@ -462,7 +481,7 @@ __global__ void __launch_bounds__(kVerifyMost, 1) verify_kernel(const VerifyPara
         for (int i = 0; i < rank; ++i) before += sm.totals[turn ^ 1][i];
         const unsigned long long mine = sm.totals[turn ^ 1][rank];
         if (warp == 0 && point >= before && point - before < mine) {
-            token = find<E>(a, sm, chunks, rank, q0 + node, k, gone, point - before);
+            token = find<E>(a, sm, chunks, rank, q0 + node, k, taken, gone, point - before);
             if (lane == 0) a.out_tokens[(long long)b * (a.max_path + 1) + count] = token;
         }
     }
