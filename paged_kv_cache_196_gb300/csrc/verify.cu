@@ -54,7 +54,7 @@ namespace tree {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVerifyThreads = 512, kVerifyMost = 1024;  // of a CTA (verify_threads)
+constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kChunk = 512;           // tokens
 constexpr int kMaxVocab = 1 << 20;
@@ -152,6 +152,27 @@ KV_DEVICE void load_chunk(const void *row, int first, int vocab, bool wide, floa
     }
 }
 
+// Four tokens from `at` on: in one load where `wide`.
+template <typename T>
+KV_DEVICE float4 load_four(const void *row, int at, int vocab, bool wide) {
+    if (wide) {
+        if constexpr (kElem<T> == 4) {
+            return __ldg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(row) + at));
+        } else {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(row) + at));
+            const float2 a = std::is_same<T, PB16>::value ? bf16x2_to_float2(x.x) : f16x2_to_float2(x.x);
+            const float2 b = std::is_same<T, PB16>::value ? bf16x2_to_float2(x.y) : f16x2_to_float2(x.y);
+            return make_float4(a.x, a.y, b.x, b.y);
+        }
+    }
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (at < vocab) v.x = one<T>(row, at);
+    if (at + 1 < vocab) v.y = one<T>(row, at + 1);
+    if (at + 2 < vocab) v.z = one<T>(row, at + 2);
+    if (at + 3 < vocab) v.w = one<T>(row, at + 3);
+    return v;
+}
+
 // A probability in steps of 2^-E: hi 2^(E - 22) + lo.
 struct Parts {
     uint32_t hi, lo;
@@ -164,7 +185,7 @@ KV_DEVICE Parts parts(float x, float lo_scale) {  // x of prob(), lo_scale = 2^(
 }
 KV_DEVICE unsigned long long fixed(float x, int e) {
     const Parts a = parts(prob(x), __uint_as_float((uint32_t)(127 + e - 22) << 23));
-    return ((unsigned long long)a.hi << (e - 22)) + a.lo;
+    return (unsigned long long)a.hi * (1u << (e - 22)) + a.lo;  // (one multiply-add)
 }
 
 // floor(a b / 2^shift)
@@ -187,16 +208,13 @@ struct Taken {
     }
     // W_k, k > 1
     KV_DEVICE unsigned long long weight(float p, float q) const {
-        const unsigned long long a = fixed(p, e), b = fixed(q, e), x = b + __umul64hi(s, b << q_shift);
+        const unsigned long long a = fixed(p, e), b = fixed(q, e);
+        const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);  // (q_shift < 32)
+        const unsigned long long y = (unsigned long long)__funnelshift_l(lo, hi, q_shift) << 32 | lo << q_shift;
+        const unsigned long long x = b + __umul64hi(s, y);
         return a > x ? a - x : 0;
     }
 };
-// Of four tokens.  (A function of its own: in line, four times over, it is more code than the rest of
-// a pass, and a launch begins with empty instruction caches.)
-__device__ __noinline__ unsigned long long weights(float4 p, float4 q, const Taken t) {
-    return t.weight(p.x, q.x) + t.weight(p.y, q.y) + t.weight(p.z, q.z) + t.weight(p.w, q.w);
-}
-
 // W_1 of a token, W_0 where k is 0.
 KV_DEVICE unsigned long long first_residual(float p, float q, int k, int e) {
     const unsigned long long a = fixed(p, e), b = k ? fixed(q, e) : 0;
@@ -227,15 +245,15 @@ KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const
     const float lo_scale = __uint_as_float((uint32_t)(127 + a.scale_exp - 22) << 23);
     const int shift = a.scale_exp - 22;
     const Taken t(taken, a.scale_exp);
-    for (int c = warp; c < chunks; c += (int)blockDim.x / 32) {
+    for (int c = warp; c < chunks; c += kVerifyWarps) {
         const long long first = ((long long)rank * chunks + c) * kChunk;
         unsigned long long sum = 0;
         if (first < a.vocab) {
             const bool full = first + kChunk <= a.vocab;
-            float x[16], y[16];
-            load_chunk<T>(p, (int)first, a.vocab, full && p_wide && (k == 0 || q_wide), x);
-            if (k) load_chunk<T>(q, (int)first, a.vocab, full && p_wide && q_wide, y);
             if (k <= 1) {
+                float x[16], y[16];
+                load_chunk<T>(p, (int)first, a.vocab, full && p_wide && (k == 0 || q_wide), x);
+                if (k) load_chunk<T>(q, (int)first, a.vocab, full && p_wide && q_wide, y);
                 // max(p - q, 0) part by part, where p > q (a part may be below q's; the sum is not)
                 uint32_t hi = 0, lo = 0;
 #pragma unroll
@@ -246,10 +264,17 @@ KV_DEVICE unsigned long long pass(const VerifyParams &a, VerifyShared &sm, const
                 }
                 sum = ((unsigned long long)hi << shift) + (long long)(int32_t)lo;
             } else {
-#pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    sum += weights(make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]),
-                                   make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]), t);
+                // (a loop, since all 16 in line are more code than the rest of a pass)
+                const bool wide = full && p_wide && q_wide;
+                int at = (int)first + 4 * lane;
+                float4 x = load_four<T>(p, at, a.vocab, wide), y = load_four<T>(q, at, a.vocab, wide);
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const float4 x0 = x, y0 = y;
+                    at += 128;
+                    if (i < 3) x = load_four<T>(p, at, a.vocab, wide), y = load_four<T>(q, at, a.vocab, wide);
+                    sum += t.weight(x0.x, y0.x) + t.weight(x0.y, y0.y) + t.weight(x0.z, y0.z) + t.weight(x0.w, y0.w);
+                }
             }
         }
         sum = warp_sum(sum);
@@ -320,7 +345,7 @@ KV_DEVICE int find(const VerifyParams &a, VerifyShared &sm, int chunks, int rank
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int at = chunk_index<T>(i, wide);
-            sm.weight[at + at / 16] = weights(make_float4(x[i], 0.f, 0.f, 0.f), make_float4(y[i], 0.f, 0.f, 0.f), t);
+            sm.weight[at + at / 16] = t.weight(x[i], y[i]);
         }
     }
     __syncwarp();
@@ -348,7 +373,7 @@ KV_DEVICE int find(const VerifyParams &a, VerifyShared &sm, int chunks, int rank
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kVerifyMost, 1) verify_kernel(const VerifyParams a) {
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyParams a) {
     __shared__ VerifyShared sm;
     const cg::cluster_group cluster = cg::this_cluster();
     const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -364,7 +389,7 @@ __global__ void __launch_bounds__(kVerifyMost, 1) verify_kernel(const VerifyPara
         nodes = 0;
     }
     const int T = (int)nodes;
-    for (int i = tid; i < T; i += (int)blockDim.x) {
+    for (int i = tid; i < T; i += kVerifyThreads) {
         int up = i == 0 ? -1 : a.parents ? __ldg(a.parents + q0 + i) : i - 1;
         const int x = __ldg(a.tokens + q0 + i);
         if (i > 0) {
@@ -489,7 +514,7 @@ __global__ void __launch_bounds__(kVerifyMost, 1) verify_kernel(const VerifyPara
     if (rank == 0) {
         __syncthreads();
         if (tid == 0) a.num_accepted[b] = count;
-        for (int i = tid; i <= a.max_path; i += (int)blockDim.x) {
+        for (int i = tid; i <= a.max_path; i += kVerifyThreads) {
             const int at = i < count ? sm.path[i] : -1;
             if (i < a.max_path) a.path[(long long)b * a.max_path + i] = at;
             if (i != count || total == 0) a.out_tokens[(long long)b * (a.max_path + 1) + i] = at < 0 ? -1 : sm.token[at];
@@ -594,18 +619,12 @@ int cluster_size(int vocab, int batch) {
     return n;
 }
 
-// Threads of a CTA: as many as an SM takes where clusters leave one CTA to an SM and chunks to every warp.
-int verify_threads(int vocab, int batch, int cluster) {
-    const int chunks = ((vocab + kChunk - 1) / kChunk + cluster - 1) / cluster;
-    return chunks > kVerifyWarps && (long long)cluster * batch <= sm_count() ? kVerifyMost : kVerifyThreads;
-}
-
 template <typename E>
 kv_status launch_verify(const VerifyParams &a, cudaStream_t stream) {
     const int n = cluster_size(a.vocab, a.batch);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.batch * (unsigned)n);
-    cfg.blockDim = dim3((unsigned)verify_threads(a.vocab, a.batch, n));
+    cfg.blockDim = dim3(kVerifyThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
