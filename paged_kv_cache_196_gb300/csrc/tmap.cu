@@ -30,6 +30,9 @@ static EncodeTiledFn encode_fn() {
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<EncodeTiledFn>(f);
     });
+    // Encoding asks for a current context, which a host thread has from its first runtime call that needs one.
+    static thread_local bool bound = false;
+    if (int dev = 0; !bound && cudaGetDevice(&dev) == cudaSuccess) bound = cudaSetDevice(dev) == cudaSuccess;
     return fn;
 }
 

@@ -33,10 +33,12 @@
 // the totals is exchanged.
 //
 // What bounds it: chains read their last node's rows once, 64 of them over 128000 tokens (fp32, p and q)
-// 65 MB and 9.8 us at the copy rate in 22.0 us: the start, the walk (3 us) and the draw are
+// 65 MB and 9.8 us at the copy rate in 21.4 us: the start, the walk and the draw are
 // latencies, and the batch is little more than one wave.  Trees read a row again for every
-// rejection: 16 trees of 64 nodes, about 20 passes one behind the other of 3.5 us each, 71.3 us.  A
-// pass is loads, their conversion, and a barrier of the cluster.  The walk is one warp's: with all warps
+// rejection, one pass behind the other: 16 trees of 64 nodes 40.7 us.  With up to 15 of them, an SM to
+// each CTA, a rejection costs 5 us at first and 8 from the second on; 16 share SMs, 13.  (W_k from W_1
+// in k - 1 steps of 64 bits: 16 rejections 1050 us where one product takes 206.  The product in pairs of
+// fp32 numbers, 180, but the 16 trees 41.0.)  The walk, 1 us, is one warp's: with all warps
 // in it the fp64 unit takes several times as long.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -610,8 +612,8 @@ namespace {
 // CTAs of a sequence's cluster: as many as leave a chunk for each of its warps while the batch
 // stays within a third more than one wave of two CTAs per SM.  Trees, which pass over rows again
 // and again, gain by large clusters, chains by one wave: 16 trees over 128000 tokens 70.5 us in
-// clusters of 8, 118 of 4; 100 trees over 50000 90 us of 4, 137 of 2; 64 chains over 128000 22.1 us
-// of 4, 26.8 of 8; 200 chains over 32000 21.4 us alone, 24.9 in clusters of 2, 30.6 of 4.
+// clusters of 8, 118 of 4 (both with an earlier form of the passes, as are the next); 100 trees over
+// 50000 90 us of 4, 137 of 2; 64 chains over 128000 22.1 us of 4, 26.8 of 8; 200 chains over 32000 21.4 us alone, 24.9 in clusters of 2, 30.6 of 4.
 int cluster_size(int vocab, int batch) {
     const int chunks = (vocab + kChunk - 1) / kChunk;
     int n = 1;
