@@ -1001,6 +1001,8 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 }
             }
             tc::fence_before_sync();
+            // the box's ordinary accesses before the copy that fills the Q buffer anew
+            if (MT == 1 && p.copies > 1) tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sm.oempty[MT == 1 ? n & 1 : x]);
