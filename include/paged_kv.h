@@ -739,7 +739,8 @@ kv_status paged_prefill_attention(kv_pool_t p, const void *q, const int32_t *cu_
  * Other arguments as paged_prefill_attention; pools of KV_F32, KV_BF16 and KV_F16, head_dim
  * 64 and 128.  Sums and softmax statistics are fp32.  fp32 pools: products in fp32.  16-bit
  * pools: products on the tensor cores, softmax weights in two parts of the pool's type (16
- * significant bits with bf16, 22 with fp16), in three (24) for KV_F32 output of a bf16 pool.
+ * significant bits with bf16; 22 with fp16, for weights below 2^-12 of the row's largest steps of 2^-33
+ * of that one), in three (24) for KV_F32 output of a bf16 pool.
  * The kernel cuts the batch by the lengths on the device, so a captured call stays balanced
  * as they change; results depend, within rounding, on the batch's lengths, and are the same
  * from call to call.  A tree that is longer than max_q_len or its sequence, a sequence

@@ -6,7 +6,8 @@
 //   S = Q K^T      (M = 128 rows, N = 128 keys, fp32 in tensor memory)
 //   softmax warps  S -> P, written over S: of every 32 keys' columns the first 16 hold
 //                  P_hi = t(P) in the pool's type t, the others P_lo = t(P - P_hi), so the
-//                  weights keep 16 significant bits with bf16, 22 with fp16.  (A bf16
+//                  weights keep 16 significant bits with bf16, 22 with fp16 (less below 2^-12 of
+//                  the row's largest, kLift).  (A bf16
 //                  weight alone would be off by 2^-8 of itself, as much as a bf16 output.  It
 //                  would take 160 us for the four long contexts below when two parts took 195.)
 //   O += P_hi V + P_lo V   (P from tensor memory)
@@ -66,7 +67,17 @@
 namespace pkv {
 namespace tree {
 
-constexpr float kRenew = 8.0f;  // log2 units by which a maximum passes the reference before sums are scaled
+// A row's reference is its maximum less kLift (log2 units) until a maximum lies kRenew above that
+// one; then sums are scaled.  So weights reach 2^(kLift + kRenew).  bf16 has fp32's exponents and no
+// lift.  fp16's steps end at 2^-24: without a lift weights below 2^-3 of the largest would lose bits, and
+// those below 2^-25, which may be most of a long context under one large score, all of them.  With it a
+// weight is off by 2^-34 of the largest at most.  A higher one has to renew sooner: lifts of 7, 9 and
+// 11 (15 in all) take 113.8, 114.0 and 118.2 us for the ragged batch below, 165, 170 and 177 for
+// the long contexts in fp16.
+template <bool F16>
+constexpr float kLift = F16 ? 9.0f : 0.0f;
+template <bool F16>
+constexpr float kRenew = F16 ? 6.0f : 8.0f;
 constexpr uint32_t kColO0 = 256, kColThird = 384;
 
 template <int D, int MT>
@@ -192,7 +203,8 @@ KV_DEVICE float tmem_max(uint32_t taddr) {
 }
 
 // Two weights as a pair of the 16-bit type and the pair of what that leaves of them: with half a
-// step of 2^-8 (bf16) or 2^-11 (fp16) each, what both leave is at most 2^-16 or 2^-22 of a weight.
+// step of 2^-8 (bf16) or 2^-11 (fp16) each, what both leave is at most 2^-16 or 2^-22 of a weight; in
+// fp16 at least the half step of its smallest numbers, 2^-25 where a row's largest is 2^kLift or more.
 // (Cutting bf16 off instead of rounding it takes as long and leaves twice as much.)
 template <bool F16>
 KV_DEVICE float2 split(float2 e, uint32_t &hi) {  // the rest, exact
@@ -770,10 +782,10 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     if (chunks == 4) mrow = fmaxf(mrow, tmem_max<64>(scol + 64));
                     mrow *= p.scale_log2;  // scale > 0
                     if (m_used == -INFINITY) {
-                        m_used = mrow;
-                    } else if (mrow > m_used + kRenew) {
-                        alpha = tc_ex2(m_used - mrow);
-                        m_used = mrow;
+                        m_used = mrow - kLift<F16>;
+                    } else if (mrow > m_used + (kLift<F16> + kRenew<F16>)) {
+                        alpha = tc_ex2(m_used - (mrow - kLift<F16>));
+                        m_used = mrow - kLift<F16>;
                         l_sum *= alpha;
                         rescale = true;
                     }
