@@ -58,3 +58,89 @@ def test_small_weights_under_a_sink(dtype, out_dtype, nodes, sink, gap):
             assert (np.abs(got[node] - want) <= tol * want).all(), (node, got[node][0, [0, 63]], want[[0, 63]], tol)
     finally:
         case.close()
+
+
+# Keys that are one in a dimension of their own, so that a query's entries are its scores (a product and
+# zeros, exact), and values that let an output show single weights.
+def one_hot_case(dtype, d, g, nodes, keys, cached, width, seed, small):
+    """`keys` rows per dimension at places of `pos`; `small`: the second of a pair, by the
+    first.  A table of 33 blocks or more lets a sequence be cut."""
+    case = TreeCase(dtype, d, 2, g, [cached], [nodes], kind="star", seed=seed, width=width)
+    rng = np.random.default_rng(seed)
+    pos = rng.permutation(cached)[:keys * d].reshape(keys, d)
+    k, v = torch.zeros_like(case.k[0]), torch.zeros_like(case.v[0])
+    for j in range(keys):
+        for i in range(d):
+            k[int(pos[j, i]), :, i] = 8.0 * (small if j else 1.0)
+    q = (torch.from_numpy(rng.uniform(-2.0, 1.5, (nodes, case.hq, d))) * (math.sqrt(d) / 8)).to(DT[dtype])
+    case.k[0], case.q = k, q
+    return case, k, v, pos
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nodes", [4, 13, 30, 70])
+@pytest.mark.parametrize("cached,width", [(140, 0), (140, 33), (1500, 0)])
+def test_every_weight_for_itself(dtype, d, nodes, cached, width):
+    """Value i is one in dimension i alone, so out[i] is key i's share; out[i] / out[0] = exp(s_i - s_0) whatever
+    the sum of weights is.
+
+    Each of the two is off by: its distance to the reference, rounded below 2^4 log2 units, 2^-21 ln 2; the scaled
+    scores, 3 2^-24 of |s_i - s_0| (their common part is the reference's, which cancels); the exponential,
+    2^-22; the weight's parts, 2^-24 (three of bf16), 2^-22 (two of fp16); up to three parts added, 2^-23 each;
+    the joining of pieces, 2^-22 and a product, copies of a row the same, and the division's product: 2^-20.
+    Two parts of bf16 would be off by up to 2^-16, one of fp16 by 2^-11."""
+    case, k, v, pos = one_hot_case(dtype, d, 4, nodes, 1, cached, width, seed=nodes, small=1.0)
+    try:
+        for i in range(d):
+            v[int(pos[0, i]), :, i] = 1.0
+        case.v[0] = v
+        case.write(0)
+        a = case.args("f32")
+        case.call(a)
+        torch.cuda.synchronize()
+        got = a["out"].double().cpu().numpy()[:nodes]
+        s = case.q.double().numpy() * 8.0 * case.scale
+        want = np.exp(s - s[:, :, :1])
+        err = np.abs(got / got[:, :, :1] - want) / want
+        parts = {"bf16": 2.0 ** -24, "f16": 2.0 ** -22, "f32": 0.0}[dtype]
+        tol = 2 * (2.0 ** -21 * math.log(2) + 2.0 ** -22 + parts + 3 * 2.0 ** -23 + 2.0 ** -20) + 3 * 2.0 ** -24 * np.abs(s - s[:, :, :1])
+        assert (err <= tol).all(), (err.max(), tol.min())
+    finally:
+        case.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nodes", [4, 13, 30, 70])
+@pytest.mark.parametrize("cached,width", [(300, 0), (300, 33), (1500, 0)])
+def test_differences_of_weights(dtype, d, nodes, cached, width):
+    """16-bit output: two keys a dimension, 1 / 128 apart in score, with values one and minus one, so that what the
+    output's rounding loses is small beside the weights: out[i] = (w - w') / sum.
+
+    Of (w + w') / sum: 2^-16 (two parts of bf16) or 2^-22 (of fp16) and the terms of the test above, 2^-18 in all; of
+    out: the sum of n weights n 2^-24, and the rounding of the output.  One part of bf16 would be off by 2^-9, of fp16 by 2^-12."""
+    small = 1 - 2.0 ** -7
+    case, k, v, pos = one_hot_case(dtype, d, 4, nodes, 2, cached, width, seed=nodes, small=small)
+    try:
+        for i in range(d):
+            v[int(pos[0, i]), :, i], v[int(pos[1, i]), :, i] = 1.0, -1.0
+        case.v[0] = v
+        case.write(0)
+        a = case.args(dtype)
+        case.call(a)
+        torch.cuda.synchronize()
+        got = a["out"].double().cpu().numpy()[:nodes]
+        s = case.q.double().numpy() * 8.0 * case.scale
+        w, w2 = np.exp(s), np.exp(s * small)
+        own = np.full((nodes, 1), 2.0)   # scores of zero: the node and the one above it, the other keys
+        own[0] = 1.0
+        total = (w + w2).sum(2) + own + cached - 2 * d
+        want = (w - w2) / total[:, :, None]
+        parts = {"bf16": 2.0 ** -16, "f16": 2.0 ** -22}[dtype]
+        tol = (w + w2) / total[:, :, None] * (parts + 2.0 ** -18) + np.abs(want) * (HALF[dtype] + cached * 2.0 ** -24)
+        if dtype == "f16":
+            tol += 2.0 ** -25   # outputs below 2^-14
+        assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
+    finally:
+        case.close()
