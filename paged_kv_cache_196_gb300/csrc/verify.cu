@@ -13,11 +13,14 @@
 // their order would return another token now and then.  So weights are integers, p and q
 // rounded to steps of 2^-E with E = 45, less for more than 2^17 tokens (42 for 2^20): no sum
 // passes 2^62 whatever the rows hold, sums are exact in any order, and their roundings, at random,
-// add up to about sqrt(vocab) 2^-47: 3e-12 for 128000 tokens, so that a draw meets another
-// token than the real numbers' about once in 3 million times.  (Cut off instead of rounded they
-// would add up to 2^-30.)  Single comparisons (u q(x) against p(x)) are in fp64, where the
-// product of two fp32 numbers is exact (in the first test of a node in fp32, by the product and
-// what a fused multiply-add says it leaves).
+// add up to about sqrt(vocab) 2^-47: 3e-12 for 128000 tokens.  A draw meets another token than the
+// real numbers' where it lies between a border and its place here: over all borders of rows of 128000
+// tokens (normal logits of deviation 6, three of them) that is a chance of 7e-7 to 3e-6, from a node's second
+// rejection on, when the rounding of S_1 counts too, of 1e-6 to 5e-5.  (Products cut off instead of rounded
+// 5e-5 to 5e-4; probabilities cut off would add up to 2^-30.)  Single comparisons (u q(x) against
+// p(x)) are in fp64, where the product of two fp32 numbers is exact (in the first test of a node
+// in fp32, by the product and what a fused multiply-add says it leaves); after a rejection, when S_k or
+// S_0 + .. comes in, they are as good as fp64.
 //
 // A probability becomes an integer in two parts, 22 bits and E - 22: adding 2^23 to a number
 // below 2^22 leaves its whole part in the mantissa, what that leaves is exact, and both parts
@@ -35,8 +38,9 @@
 // What bounds it: chains read their last node's rows once, 64 of them over 128000 tokens (fp32, p and q)
 // 65 MB and 9.8 us at the copy rate in 21.4 us: the start, the walk and the draw are
 // latencies, and the batch is little more than one wave.  Trees read a row again for every
-// rejection, one pass behind the other: 16 trees of 64 nodes 40.7 us.  With up to 15 of them, an SM to
-// each CTA, a rejection costs 5 us at first and 8 from the second on; 16 share SMs, 13.  (W_k from W_1
+// rejection, one pass behind the other: 16 trees of 64 nodes 43.1 us (41.0 with products
+// cut off).  With up to 15 of them, an SM to
+// each CTA, a rejection costs 5 us at first and 8 to 9 from the second on; 16 share SMs, 13.  (W_k from W_1
 // in k - 1 steps of 64 bits: 16 rejections 1050 us where one product takes 206.  The product in pairs of
 // fp32 numbers, 180, but the 16 trees 41.0.)  The walk, 1 us, is one warp's: with all warps
 // in it the fp64 unit takes several times as long.
@@ -198,22 +202,23 @@ KV_DEVICE unsigned long long mul_shift(unsigned long long a, unsigned long long 
     return shift ? (lo >> shift) | (hi << (64 - shift)) : lo;
 }
 
-// S_1 + .. + S_{k-1}, as the factor of a product whose upper half is floor(of it times q / 2^E): shifted to
-// the left as far as it goes (it is below 2^63), q the rest of the 64 - E places.
+// S_1 + .. + S_{k-1}, as the factor of a product whose upper half is floor(2 (of it times q) / 2^E), to be
+// rounded: shifted to the left as far as it goes (it is below 2^63), q the rest of the 65 - E places.  (Only a
+// q of one may lose its bit there: nothing of p is left of it anyway.)
 struct Taken {
     unsigned long long s;
     int q_shift, e;
     KV_DEVICE Taken(unsigned long long sum, int scale_exp) : e(scale_exp) {
         const int a = min(__clzll((long long)sum), 64 - e);
         s = sum << a;
-        q_shift = 64 - e - a;
+        q_shift = 65 - e - a;
     }
     // W_k, k > 1
     KV_DEVICE unsigned long long weight(float p, float q) const {
         const unsigned long long a = fixed(p, e), b = fixed(q, e);
         const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);  // (q_shift < 32)
         const unsigned long long y = (unsigned long long)__funnelshift_l(lo, hi, q_shift) << 32 | lo << q_shift;
-        const unsigned long long x = b + __umul64hi(s, y);
+        const unsigned long long x = b + ((__umul64hi(s, y) + 1) >> 1);
         return a > x ? a - x : 0;
     }
 };

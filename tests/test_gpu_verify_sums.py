@@ -1,0 +1,86 @@
+"""Draws of verification next to the borders between tokens, after rejections."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_196_gb300 as pk
+from _gpu import require_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _cuda():
+    require_cuda()
+
+
+@pytest.fixture
+def pool():
+    require_cuda()
+    p = pk.kv_pool_create(1, 16, 1, 64, pk.KV_F32)
+    yield p
+    pk.kv_pool_destroy(p)
+
+
+def ints(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+HEAVY, LIGHT = 64, 65536
+
+
+def two_rejections(seed):
+    """p, q of 131072 tokens in fp32 (whole numbers of 2^-45, so as integers too) whose second residual is half on 64
+    tokens and half on 65536 behind them; the last two tokens, with p = 0, are the drafts."""
+    rng = np.random.default_rng(seed)
+    vocab, s = 131072, 2.0 ** -11
+    q, p = np.zeros(vocab, np.float32), np.zeros(vocab, np.float32)
+    n = HEAVY + LIGHT
+    q[:n] = rng.uniform(2.0 ** -18, 3 * 2.0 ** -18, n)
+    q[:n] *= 0.5 / q[:n].sum(dtype=np.float64)
+    rest = np.where(np.arange(n) < HEAVY, s / 4 / HEAVY, s / 4 / LIGHT) * rng.uniform(0.5, 1.5, n)
+    p[:n] = (1 + s) * q[:n].astype(np.float64) + rest
+    q[-2:] = 2.0 ** -10
+    unit = 2.0 ** 45
+    pi, qi = (x.astype(np.float64) * unit for x in (p, q))
+    assert (pi == np.rint(pi)).all() and (qi == np.rint(qi)).all()
+    return p, q, [int(x) for x in pi], [int(x) for x in qi]
+
+
+def test_borders_after_two_rejections(pool):
+    """W_2 = max(p - (1 + S_1) q, 0), S_1 = sum max(p - q, 0): exact in whole numbers of 2^-90 here.
+
+    The kernel holds W_2 in whole numbers of 2^-45.  Rounded, 65600 weights err by at most half of one each and as often
+    up as down: their sum by 75 (one standard deviation), of 2^33 that S_2 has.  Cut off, all would err by half of
+    one in one direction, and the border between the 64 and the 65536 would lie 16000 below its place.  Numbers are drawn
+    from 2000 to 30000 off the border on both sides: 25 standard deviations and more."""
+    for seed in range(3):
+        p, q, pi, qi = two_rejections(seed)
+        vocab = len(p)
+        s1 = sum(max(a - b, 0) for a, b in zip(pi, qi))
+        w = [max(((a - b) << 45) - s1 * b, 0) for a, b in zip(pi, qi)]
+        total, border = sum(w), sum(w[:HEAVY])
+        assert 2 ** 32 < total >> 45 < 2 ** 34 and abs(border / total - 0.5) < 0.1
+        u = [np.float32((border + off * 2 ** 45) / total) for off in
+             (-30000, -14000, -8000, -5000, -3000, 3000, 5000, 8000, 14000, 30000)]
+        want = []
+        for x in u:
+            # the first token whose running sum passes x * total, with x's exact value
+            num, den = float(x).as_integer_ratio()
+            point, run, at = num * total // den, 0, 0
+            assert abs(point - border) > 2000 * 2 ** 45
+            while run + w[at] <= point:
+                run += w[at]
+                at += 1
+            want.append(at)
+        b = len(u)
+        rows = lambda x: torch.from_numpy(x).cuda().repeat(3 * b, 1)
+        tokens = np.tile([0, vocab - 1, vocab - 2], b)
+        count, path, out = ints(np.full(b, 7)), ints(np.full((b, 1), 7)), ints(np.full((b, 2), 7))
+        pk.kv_verify_tree(pool, rows(p), rows(q), pk.KV_F32, vocab, ints(np.arange(0, 3 * b + 1, 3)), 3 * b, 3,
+                          ints(np.tile([-1, 0, 0], b)), ints(tokens), torch.full((3 * b,), 0.5, device="cuda"),
+                          torch.from_numpy(np.array(u)).cuda(), b, 1, count, path, out)
+        torch.cuda.synchronize()
+        assert pk.kv_get_device_error(pool) == 0
+        assert (count == 0).all() and (path == -1).all() and (out[:, 1] == -1).all()
+        assert out[:, 0].tolist() == want
