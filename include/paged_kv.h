@@ -767,12 +767,14 @@ kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, 
  * accepted if u q(x) < p(x); otherwise p becomes max(p - q, 0), divided by its sum, for the
  * next child.  When no child is accepted, or max_path nodes are, the next token is drawn from
  * what p is by then: the first whose running sum of p passes sample_uniform times the sum
- * of all.  So what is emitted is distributed as the target's own samples.
+ * of all.  So what is emitted is distributed as the target's own samples, if rows sum to one.
  *   target_probs  device [total_q][vocab] of probs_dtype (KV_F32, KV_BF16 or KV_F16), row
  *                 cu_q[b] + i from i * target_stride elements on (0: vocab): after node i;
  *   draft_probs   the same for the distribution that node i's children were drawn from (rows
  *                 of leaves are not read), or NULL: drafts were chosen, not drawn (the
- *                 draft's likeliest tokens, say), and q counts as one at x;
+ *                 draft's likeliest tokens, say), and q counts as one at x.  p then counts as
+ *                 summing to one whatever it sums to: a rejected x loses its p(x), and what is
+ *                 left is divided by 1 less all p(x) so lost (the draw, by its sum);
  *   tokens        device int32[total_q], each node's token (node 0's is not read); a negative
  *                 one is no draft: it is passed over;
  *   accept_uniform, sample_uniform  device fp32 [total_q] and [batch], random numbers of
@@ -783,7 +785,9 @@ kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, 
  *                 them (may be NULL if max_path is 0);
  *   out_tokens    device int32[batch][max_path + 1]: their tokens, the next token, then -1.
  * Rows need not sum to one (a draw divides by their sum, a first acceptance takes p and q
- * as they are); entries that are negative or NaN count as 0, above one as 1.  If nothing of
+ * as they are; without draft_probs all do, so a p that sums to s accepts a later child
+ * (s - lost) / (1 - lost) times as often as p / s would: have rows normalised, 16-bit ones
+ * before they are rounded); entries that are negative or NaN count as 0, above one as 1.  If nothing of
  * p is left after the rejections, the draw is from p as it was before them; a row without any
  * positive entry gives the token -1.  For a sequence that samples greedily p is one at its
  * token.  Sums are exact (whole numbers of 2^-42 or finer), so that a draw does not depend on

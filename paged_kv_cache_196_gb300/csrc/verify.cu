@@ -7,7 +7,8 @@
 //   W_{k+1} = max(W_k - S_k q, 0),  S_{k+1} = sum W_{k+1},  accept iff u q(x) S_k < W_k(x);
 // nothing that went to zero returns, so W_k = max(p - (S_0 + .. + S_{k-1}) q, 0) at once,
 // and the draw is the first index whose running sum of W_k passes u S_k.  Drafts that were
-// chosen (q null) count as drawn from a q that is one at x: W loses its entry at x.
+// chosen (q null) count as drawn from a q that is one at x: W loses its entry at x, and S that
+// entry (from 1, what a row of probabilities sums to: the row itself is read for the draw alone).
 //
 // A draw from 10^5 tokens lies next to a border between two of them: sums that depend on
 // their order would return another token now and then.  So weights are integers, p and q

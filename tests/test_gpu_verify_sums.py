@@ -84,3 +84,42 @@ def test_borders_after_two_rejections(pool):
         assert pk.kv_get_device_error(pool) == 0
         assert (count == 0).all() and (path == -1).all() and (out[:, 1] == -1).all()
         assert out[:, 0].tolist() == want
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("row", [(0.3, 0.1, 0.05, 0.05), (0.5, 0.25, 0.125, 0.125), (0.8, 0.1, 0.3, 0.3),
+                                 (0.9975, 0.002, 0.0005, 0.0), (0.6, 0.2, 0.1, 0.0)])
+def test_chosen_drafts_of_rows_of_any_sum(pool, dtype, row):
+    """Without q a row counts as summing to one: after the draft of token 0 was rejected that of token 1 is
+    accepted below p(1) / (1 - p(0)), then that of token 2 below p(2) / (1 - p(0) - p(1)), whatever the row sums to; the
+    draw divides by what is left.  Numbers lie 2^-10 off each border, the fp64 tests 2^-50."""
+    p = torch.zeros(1, 40, dtype=dtype)
+    p[0, :4] = torch.tensor(row)
+    p0, p1, p2, p3 = p[0, :4].double().tolist()
+    one = 1 - 2.0 ** -24
+    up = lambda x: min(one, x * (1 + 2.0 ** -10))
+    second, third = p1 / (1 - p0), p2 / (1 - p0 - p1) if p0 + p1 < 1 else 2.0
+    cases = [([p0 * (1 - 2.0 ** -10), one, one], 0.5, [0]), ([one, second * (1 - 2.0 ** -10), one], 0.5, [1])]
+    if second < 1:
+        cases.append(([one, up(second), min(one, third * (1 - 2.0 ** -10))], 0.5, [2]))
+        if third < 1:
+            left = p3 if p3 else p0 + p1 + p2   # nothing left: the whole row
+            cases += [([one, up(second), up(third)], u, []) for u in (0.0, 0.25, 0.75, one)]
+    b = len(cases)
+    accept = np.array([[0.5, *c[0]] for c in cases], np.float32)
+    count, path, out = ints(np.full(b, 7)), ints(np.full((b, 1), 7)), ints(np.full((b, 2), 7))
+    pk.kv_verify_tree(pool, p.cuda().repeat(4 * b, 1), None, {4: pk.KV_F32, 2: pk.KV_BF16}[p.element_size()]
+                      if dtype != torch.float16 else pk.KV_F16, 40, ints(np.arange(0, 4 * b + 1, 4)), 4 * b, 4,
+                      ints(np.tile([-1, 0, 0, 0], b)), ints(np.tile([0, 0, 1, 2], b)), torch.from_numpy(accept).cuda().flatten(),
+                      torch.tensor([c[1] for c in cases], dtype=torch.float32, device="cuda"), b, 1, count, path, out)
+    torch.cuda.synchronize()
+    assert pk.kv_get_device_error(pool) == 0
+    assert path[:, 0].tolist() == [c[2][0] + 1 if c[2] else -1 for c in cases]
+    for i, (_, u, way) in enumerate(cases):
+        if way:
+            assert out[i, 0] == way[0]
+        elif p3:
+            assert out[i, 0] == 3
+        else:
+            sums = np.cumsum([p0, p1, p2])
+            assert out[i, 0] == int(np.searchsorted(sums, float(np.float32(u)) * sums[-1], side="right"))
