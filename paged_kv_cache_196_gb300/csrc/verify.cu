@@ -19,8 +19,8 @@
 // tokens (normal logits of deviation 6, three of them) that is a chance of 7e-7 to 3e-6, from a node's second
 // rejection on, when the rounding of S_1 counts too, of 1e-6 to 5e-5.  (Products cut off instead of rounded
 // 5e-5 to 5e-4; probabilities cut off would add up to 2^-30.)  Single comparisons (u q(x) against
-// p(x)) are in fp64, where the product of two fp32 numbers is exact (in the first test of a node
-// in fp32, by the product and what a fused multiply-add says it leaves); after a rejection, when S_k or
+// p(x)) are in fp64, where the product of two fp32 numbers is exact (the first test of a node looks
+// in fp32 first); after a rejection, when S_k or
 // S_0 + .. comes in, they are as good as fp64.
 //
 // A probability becomes an integer in two parts, 22 bits and E - 22: adding 2^23 to a number
@@ -447,9 +447,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
                 bool takes;
                 double w = 0.0;
                 if (k == 0 && gone == 0) {
-                    // u q against p in fp32 and what its product leaves: exact, without 64 bits
-                    const float hi = sm.u[child] * sm.q[child], lo = fmaf(sm.u[child], sm.q[child], -hi);
-                    takes = hi < sm.p[child] || (hi == sm.p[child] && lo < 0.f);
+                    // u q against p: a product rounded to fp32 that differs from p lies on the same side of it;
+                    // one that does not is taken in 64 bits (what it lost may be below fp32's smallest number)
+                    const float prod = sm.u[child] * sm.q[child];
+                    takes = prod < sm.p[child] || (prod == sm.p[child] && (double)sm.u[child] * sm.q[child] < sm.p[child]);
                 } else {
                     w = sm.p[child];
                     if (drawn) {

@@ -123,3 +123,34 @@ def test_chosen_drafts_of_rows_of_any_sum(pool, dtype, row):
         else:
             sums = np.cumsum([p0, p1, p2])
             assert out[i, 0] == int(np.searchsorted(sums, float(np.float32(u)) * sums[-1], side="right"))
+
+
+def test_products_next_to_the_probability(pool):
+    """u q(x) < p(x) decides exactly, where u q rounded to fp32 equals p too, down to numbers whose products lose
+    bits below fp32's smallest: the expected side is that of whole numbers."""
+    rng = np.random.default_rng(0)
+    us, qs, ps = [], [], []
+    for low in (-1, -60, -100, -120, -124, -125, -126, -127, -130, -140):
+        for _ in range(60):
+            u = np.float32(1 - 2.0 ** -24 * rng.integers(1, 2 ** int(rng.integers(1, 12))))
+            q = np.float32(np.ldexp(1 + rng.random(), low - 1))
+            exact = u.astype(np.float64) * q.astype(np.float64)
+            near = exact.astype(np.float32)   # rounded to nearest
+            for p in (near, np.nextafter(near, np.float32(0)), np.nextafter(near, np.float32(1))):
+                us.append(u), qs.append(q), ps.append(p)
+    # the product is below p by 2^-46 of it, which is below 2^-149
+    us.append(np.float32(1 - 2.0 ** -23)), qs.append(np.float32(2.0 ** -126 * (1 + 2.0 ** -23))), ps.append(np.float32(2.0 ** -126))
+    b = len(us)
+    want = [float(u) * float(q) < float(p) for u, q, p in zip(us, qs, ps)]   # 48 bits: exact
+    assert want[-1] and 0 < sum(want) < b
+    assert sum(np.float32(u * q) == p for u, q, p in zip(us, qs, ps)) > 500
+    p, q = torch.zeros(2 * b, 8), torch.zeros(2 * b, 8)
+    p[:, 5], q[:, 5] = torch.from_numpy(np.repeat(ps, 2)), torch.from_numpy(np.repeat(qs, 2))
+    p[:, 0] = 0.5
+    count, path, out = ints(np.full(b, 7)), ints(np.full((b, 1), 7)), ints(np.full((b, 2), 7))
+    pk.kv_verify_tree(pool, p.cuda(), q.cuda(), pk.KV_F32, 8, ints(np.arange(0, 2 * b + 1, 2)), 2 * b, 2, None,
+                      ints(np.tile([0, 5], b)), torch.from_numpy(np.repeat(us, 2)).cuda(), torch.full((b,), 0.5, device="cuda"),
+                      b, 1, count, path, out)
+    torch.cuda.synchronize()
+    assert pk.kv_get_device_error(pool) == 0
+    assert count.bool().tolist() == want
