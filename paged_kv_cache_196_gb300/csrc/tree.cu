@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
             __syncthreads();  // this tile is there, and every thread is done with the one before
             if (key0 + kSimpleKeys < key1) there_next = fetch(key0 + kSimpleKeys, buf ^ 1);
             float s[2][4] = {};
+            uint32_t seen[2];  // keys of the tile that each row attends
 #pragma unroll 4
             for (int d = 0; d < D; d += 4) {
                 const float4 a = *reinterpret_cast<const float4 *>(&sm.q[2 * ty][d]);
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = 2 * ty + i;
-                const uint32_t bits = key_bits(sm.anc[row], key0 - before) & there;
+                const uint32_t bits = seen[i] = key_bits(sm.anc[row], key0 - before) & there;
                 float mx = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -168,16 +169,17 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
                     o[i][k].x *= alpha, o[i][k].y *= alpha, o[i][k].z *= alpha, o[i][k].w *= alpha;
             }
             __syncwarp();
-            // a weight of zero leaves its key out: what lies in a masked one reaches no row
+            // What lies in a masked key reaches no row; what lies in an attended one does, though its weight may
+            // be zero: a NaN or an infinity there is to show.
 #pragma unroll 4
             for (int j = 0; j < kSimpleKeys; ++j) {
                 const float e0 = sm.p[2 * ty][j], e1 = sm.p[2 * ty + 1][j];
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) {
                     const float4 v = *reinterpret_cast<const float4 *>(&sm.v[buf][j][4 * tx + 32 * k]);
-                    if (e0 != 0.f)
+                    if (seen[0] >> j & 1)
                         o[0][k].x += e0 * v.x, o[0][k].y += e0 * v.y, o[0][k].z += e0 * v.z, o[0][k].w += e0 * v.w;
-                    if (e1 != 0.f)
+                    if (seen[1] >> j & 1)
                         o[1][k].x += e1 * v.x, o[1][k].y += e1 * v.y, o[1][k].z += e1 * v.z, o[1][k].w += e1 * v.w;
                 }
             }
