@@ -19,20 +19,29 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_
                                    const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+static void *driver_fn(const char *name) {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPointByVersion(name, &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? f
+               : nullptr;
+}
+
 static EncodeTiledFn encode_fn() {
+    using GetCurrentFn = CUresult (*)(CUcontext *);
     static EncodeTiledFn fn = nullptr;
+    static GetCurrentFn current = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(f);
+        fn = reinterpret_cast<EncodeTiledFn>(driver_fn("cuTensorMapEncodeTiled"));
+        current = reinterpret_cast<GetCurrentFn>(driver_fn("cuCtxGetCurrent"));
     });
-    // Encoding asks for a current context, which a host thread has from its first runtime call that needs one.
-    static thread_local bool bound = false;
-    if (int dev = 0; !bound && cudaGetDevice(&dev) == cudaSuccess) bound = cudaSetDevice(dev) == cudaSuccess;
+    // Encoding asks for a current context.  A host thread without one gets its device's primary context, as its
+    // first runtime call that needs one would give it; one that a thread has, of its own even, stays.
+    CUcontext ctx = nullptr;
+    if (current && (current(&ctx) != CUDA_SUCCESS || !ctx))
+        if (int dev = 0; cudaGetDevice(&dev) == cudaSuccess) cudaSetDevice(dev);
     return fn;
 }
 
