@@ -751,7 +751,7 @@ kv_status paged_prefill_attention(kv_pool_t p, const void *q, const int32_t *cu_
  * that a row does not attend, NaN and infinities too, does not reach the row; a NaN in an
  * attended key, or an infinity in its V, makes it NaN or infinite.
  * KV_ERR_UNSUPPORTED: KV_I4 pools, an out_dtype as above, more than 8 query heads per kv
- * head, max_q_len > 256, max_blocks > 2^27 - 1, 16-bit pools of more than 2^31 - 1 (block,
+ * head, max_q_len > 256, max_blocks > 2^27 - 8, 16-bit pools of more than 2^31 - 1 (block,
  * kv head, token) rows. */
 kv_status kv_tree_workspace_size(kv_pool_t p, int batch, int num_q_heads, int max_blocks, int max_q_len,
                                  size_t *bytes);

@@ -385,7 +385,7 @@ kv_status check(kv_pool_t p, int batch, int num_q_heads, int max_blocks, int max
     if (kv_status st = require_device(p->device)) return st;
     if (p->dtype == KV_I4) return KV_ERR_UNSUPPORTED;
     if (num_q_heads % p->num_kv_heads) return KV_ERR_ARG;
-    if (num_q_heads / p->num_kv_heads > 8 || max_q_len > kMaxNodes || max_blocks > (1 << 27) - 1 ||
+    if (num_q_heads / p->num_kv_heads > 8 || max_q_len > kMaxNodes || max_blocks > kMaxBlocks ||
         (p->dtype != KV_F32 && (long long)p->num_blocks * p->num_kv_heads * 16 > INT32_MAX))
         return KV_ERR_UNSUPPORTED;
     return KV_OK;

@@ -23,6 +23,8 @@ namespace pkv {
 namespace tree {
 
 constexpr int kTile = 128;  // keys
+// Columns of a table: 2^31 - 128 tokens, so that the end of a last key tile is an int too.
+constexpr int kMaxBlocks = (1 << 27) - 8;
 
 struct Plan {
     const int32_t *cu_q, *seq_lens;
