@@ -805,7 +805,7 @@ kv_status kv_verify_tree(kv_pool_t p, const void *target_probs, int64_t target_s
 
 /* Leaves the accepted nodes in the cache: the K and V rows of node path[b][i] move to place
  * seq_lens[b] - T_b + 1 + i, behind node 0, for i < num_accepted[b], and new_seq_lens[b]
- * (device int32[batch], not overlapping seq_lens) becomes seq_lens[b] - T_b + 1 +
+ * (device int32[batch], not overlapping any input) becomes seq_lens[b] - T_b + 1 +
  * num_accepted[b]: what the next append goes on from.  (Blocks behind it stay in the
  * tables; the host frees or refills them.)  A sequence without nodes keeps its length.
  * With kv_pool_set_launch_overlap on for any of the pools, the call keeps the next launch

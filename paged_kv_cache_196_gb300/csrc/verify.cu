@@ -714,8 +714,12 @@ kv_status kv_keep_path(const kv_pool_t *pools, int num_pools, const int32_t *cu_
         return KV_ERR_UNSUPPORTED;
     if (batch == 0) return KV_OK;
     if (!cu_q || !num_accepted || !block_tables || !seq_lens || !new_seq_lens || (max_path && !path)) return KV_ERR_ARG;
-    // other CTAs still read the lengths when one writes the new ones
-    if (new_seq_lens < seq_lens + batch && seq_lens < new_seq_lens + batch) return KV_ERR_ARG;
+    // other CTAs still read their inputs when one writes the new lengths
+    auto overlaps = [&](const int32_t *x, size_t n) { return new_seq_lens < x + n && x < new_seq_lens + batch; };
+    const size_t rows = (size_t)batch;
+    if (overlaps(seq_lens, rows) || overlaps(num_accepted, rows) || overlaps(cu_q, rows + 1) ||
+        (max_path && overlaps(path, rows * max_path)) || overlaps(block_tables, rows * max_blocks))
+        return KV_ERR_ARG;
     tree::KeepParams a{};
     a.cu_q = cu_q;
     a.path = path;

@@ -4,7 +4,8 @@ import torch
 
 import paged_kv_cache_196_gb300 as pk
 from _gpu import require_cuda
-from _tree import TreeCase
+from _tree import TreeCase, views
+from test_gpu_keep import KeepCase
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +50,40 @@ def test_a_sequence_in_a_table_of_the_most_columns():
             case.check(a)
         finally:
             case.close()
+
+
+def test_new_lengths_over_an_input():
+    """A CTA of one layer writes a sequence's new length while those of others still read the call's inputs."""
+    case = KeepCase("bf16", 64, 2, [20, 40, 3], [8, 5, 9], [3, 0, 4])
+    try:
+        a = case.args()
+        held = {x: a[x].clone() for x in ("cu", "path", "count", "tables", "lens")}
+
+        def call(new):
+            pk.kv_keep_path(case.pools, a["cu"], 9, a["path"], case.max_path, a["count"], a["tables"], case.width, a["lens"],
+                            3, new)
+        for x in held:
+            n = a[x].numel()
+            start = a[x].data_ptr()
+            for at in (0, 4 * (n - 1), -8):   # its beginning, its last entry, an array that ends in it
+                with pytest.raises(pk.KVError) as e:
+                    call(start + at)
+                assert e.value.status == -1, (x, at)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[x], held[x]) for x in held)
+        # behind an input, and before one
+        buf = torch.full((9,), 77, dtype=torch.int32, device="cuda")
+        buf[3:6] = a["count"]
+        a["count"] = buf[3:6]
+        for at in (6, 0):
+            call(buf[at:at + 3])
+            if at == 6:
+                a["new"] = torch.cat([buf[6:9], a["new"][3:]])
+                case.check(a)
+                for p, kv in zip(case.pools, case.before):   # the rows as they were, for the other call
+                    for x, y in zip(views(p, case.blocks, 2, 64, "bf16"), kv):
+                        x.view(y.dtype).copy_(y)
+        a["new"] = torch.cat([buf[0:3], a["new"][3:]])
+        case.check(a)
+    finally:
+        case.close()
