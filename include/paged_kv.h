@@ -790,8 +790,10 @@ kv_status paged_tree_attention(kv_pool_t p, const void *q, const int32_t *cu_q, 
  * before they are rounded); entries that are negative or NaN count as 0, above one as 1.  If nothing of
  * p is left after the rejections, the draw is from p as it was before them; a row without any
  * positive entry gives the token -1.  For a sequence that samples greedily p is one at its
- * token.  Sums are exact (whole numbers of 2^-42 or finer), so that a draw does not depend on
- * the order of additions.  Rows of nodes that the walk does not reach are not read, but for
+ * token.  For sums entries are rounded to steps of 2^-45 (vocabularies past 2^17: 2^-44, past 2^18
+ * 2^-43, past 2^19 2^-42), ties to even: one of half a step or less counts as 0 in a draw, and a row
+ * of nothing else as one without any.  Sums are exact, so that a draw does not depend on the order
+ * of additions.  Rows of nodes that the walk does not reach are not read, but for
  * the entries of their drafts.  A sequence without nodes, or whose cu_q is out of
  * range (KV_DEVERR_BLOCK_RANGE), accepts nothing and emits -1; a token past the vocabulary or
  * a parent that does not come before its node sets KV_DEVERR_TREE, the draft is passed over.

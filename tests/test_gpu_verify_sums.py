@@ -154,3 +154,21 @@ def test_products_next_to_the_probability(pool):
     torch.cuda.synchronize()
     assert pk.kv_get_device_error(pool) == 0
     assert count.bool().tolist() == want
+
+
+@pytest.mark.parametrize("vocab,step", [(1000, -45), (1 << 17, -45), ((1 << 17) + 1, -44), (1 << 18, -44), ((1 << 18) + 1, -43),
+                                        (1 << 19, -43), ((1 << 19) + 1, -42), (1 << 20, -42)])
+def test_steps_of_a_draw(pool, vocab, step):
+    """Entries of half a step count as nothing, those just above as one step."""
+    p = torch.zeros(4, vocab)
+    half = 2.0 ** (step - 1)
+    p[0, :] = half                                  # nothing
+    p[1, :], p[1, 77] = half, half * (1 + 2.0 ** -20)   # one step
+    p[2, 3], p[2, 5], p[2, 900] = 2.0 ** step, half, 3 * half   # one, nothing, two (a tie, to even)
+    p[3, 3], p[3, 900] = 2.0 ** step, 3 * half
+    count, out = ints(np.full(4, 7)), ints(np.full((4, 1), 7))
+    pk.kv_verify_tree(pool, p.cuda(), None, pk.KV_F32, vocab, ints(np.arange(5)), 4, 1, None, ints(np.zeros(4)),
+                      torch.zeros(4, device="cuda"), torch.tensor([0.5, 0.9, 0.34, 0.33], device="cuda"), 4, 0, count, None, out)
+    torch.cuda.synchronize()
+    assert pk.kv_get_device_error(pool) == 0
+    assert (count == 0).all() and out[:, 0].tolist() == [-1, 77, 900, 3]
