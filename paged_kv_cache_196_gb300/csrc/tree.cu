@@ -40,7 +40,8 @@ KV_DEVICE float ex2(float x) {
 // 4 tx + 32 i.  A warp owns eight rows, so their statistics and weights need no barrier.
 // Bound by latency: two CTAs an SM of four warps each wait for shared memory and for their
 // own sums.  Five ragged trees of 3 to 33 nodes over an fp32 pool (12 heads over 4, head_dim 64, to 1531
-// tokens): 37.7 us where K and V take 1.3 to read; 55 for the first version.
+// tokens): 23.4 us where K and V take 1.3 to read; 55 for the first version, 37.7 with runs of three units
+// at least.
 constexpr int kSimpleRows = 32, kSimpleKeys = 32, kSimpleThreads = 128;
 
 template <int D>
@@ -319,9 +320,15 @@ __global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const Tree
 namespace {
 
 constexpr int kSimplePerSm = 2;  // CTAs
-// Tables of up to this many blocks (four key tiles): no pair is cut, and no second kernel runs.  Two
-// sequences of 44 to 408 tokens: 13.1 us whole, 14.7 cut.
-constexpr int kWholeBlocks = 32;
+// Tables of up to this many blocks: no pair is cut, and no second kernel runs.  Sequences that fill their
+// tables, 8 nodes each, whole / cut in us.  16-bit pools (four key tiles):
+//   pairs of 16, 2, 240, 512 (d 64, 128, 128, 128)   32 blocks 12.1 / 15.1, 13.4 / 15.0, 23.6 / 31.8, 41.1 / 51.7
+//                                                   64         15.9 / 15.3, 17.4 / 16.0, 33.1 / 40.0, 61.6 / 74.7
+//   (whole wins at 48 too, but there ragged sequences gain from being cut)
+// fp32, whose tiles take several times as long (two key tiles):
+//   pairs of 8, 320, 800 (d 64, 128, 128)   16 blocks 24.7 / 26.3,  98.2 /  90.6, 175 / 173
+//                                           32         44.5 / 37.2, 187.9 / 143.2, 328 / 310
+constexpr int kWholeBlocks = 32, kWholeBlocksF32 = 16;
 
 kv_status launch_simple(const TreeParams &pp, int d, cudaStream_t stream) {
     auto fn = d == 64 ? tree_simple_kernel<64> : tree_simple_kernel<128>;
@@ -344,10 +351,11 @@ kv_status launch_merge(const TreeParams &pp, int d, int slot_rows, cudaStream_t 
 // How a call runs: what the workspace query and the call have to agree on.  pair_cost (tree_plan.cuh)
 // is what a piece's beginning and end take in key tiles' times, measured: 64 ragged sequences 1 to
 // 5 give 131.5, 124.5, 123.1, 124.0 and 125.0 us, 16 trees of two row tiles 111.7, 105.8, 107.2,
-// 108.6 and 110.7.  min_run, the least of a run where a batch leaves CTAs without work: one row tile, a
+// 108.6 and 110.7; fp32, 64 sequences of 300 to 1000 tokens (32 heads over 8, d 64), 1 to 3: 235, 249 and 261 us.  min_run, the least of a run where a batch leaves CTAs without work: one row tile, a
 // sequence of 3000 tokens (8 heads over 2): 17.9 us with 4, 18.3 with 5, 18.9 with 6, 20.8 with 8 and
 // 24.8 with 12; two, a sequence of 8000 with 64 nodes (16 over 2): 29.8 us with 3, 27.6 with 4, 28.7
-// with 6, 31.6 with 8.
+// with 6, 31.6 with 8; fp32, a sequence of 3000 (8 over 2, d 128): 30.3 us with 1, 45.6 with 2, 62.1 with 3, 79.5
+// with 4, and of 20000, which fills the grid with longer runs, 74.4, 74.4, 69.9 and 85.1.
 struct Shape {
     int slot_rows;                // rows of a slot of partial results
     int tile_nodes, group_nodes;  // nodes of a row tile and of a group
@@ -359,10 +367,10 @@ struct Shape {
 // third part of the weights takes it).  The query, which does not know the output's type, takes the
 // larger workspace: that of 16-bit output.
 Shape shape_of(const kv_pool *p, int g, int max_q_len, int max_blocks, kv_dtype out_dtype) {
-    const bool whole = max_blocks <= kWholeBlocks;
     if (p->dtype == KV_F32)
-        return {kSimpleRows, kSimpleRows / g, kSimpleRows / g, 1, kSimplePerSm * sm_count(), 1, 3, whole};
-    Shape s{128, 128 / g, 128 / g, 1, sm_count(), 3, 4, whole};
+        return {kSimpleRows, kSimpleRows / g, kSimpleRows / g, 1, kSimplePerSm * sm_count(), 1, 1,
+                max_blocks <= kWholeBlocksF32};
+    Shape s{128, 128 / g, 128 / g, 1, sm_count(), 3, 4, max_blocks <= kWholeBlocks};
     if (max_q_len <= 64 / g) {
         s.copies = max_q_len <= 32 / g ? 4 : 2;
         s.tile_nodes = s.group_nodes = 128 / s.copies / g;

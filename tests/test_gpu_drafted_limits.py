@@ -87,3 +87,18 @@ def test_new_lengths_over_an_input():
         case.check(a)
     finally:
         case.close()
+
+
+@pytest.mark.parametrize("width", [15, 16, 17, 32, 33])
+@pytest.mark.parametrize("d,g,nodes", [(64, 1, 3), (64, 3, 40), (128, 8, 9)])
+def test_fp32_tables_around_the_limit_of_whole_pairs(width, d, g, nodes):
+    """Whole pairs need no workspace; cut ones, in runs down to a key tile, give what the formula gives."""
+    for lens in ([16 * width - nodes], [16 * width - nodes, 0, 5, 100, 16 * width - nodes - 3]):
+        case = TreeCase("f32", d, 2, g, lens, [nodes] * len(lens), width=width, seed=width)
+        try:
+            a = case.args("f32")
+            assert (a["ws_bytes"] == 0) == (width <= 16)
+            case.call(a)
+            case.check(a)
+        finally:
+            case.close()
