@@ -27,12 +27,6 @@
 namespace pkv {
 namespace tree {
 
-KV_DEVICE float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // ---------------------------------------------------------------- fp32 arithmetic
 // 32 rows of a pair against 32 keys at a time, the next 32 copied meanwhile, products by fp32
 // multiply-adds: thread

@@ -10,6 +10,12 @@
 namespace pkv {
 namespace tree {
 
+KV_DEVICE float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 struct TreeParams {
     Plan plan;
     const void *q;           // rows [total_q][hq][D], the pool's type

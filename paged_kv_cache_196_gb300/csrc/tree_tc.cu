@@ -143,12 +143,6 @@ KV_DEVICE bool pipe_wait(uint64_t *bar, uint32_t parity, int *err) {
     return mbar_wait<TW>(bar, parity, err);
 }
 
-KV_DEVICE float tc_ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 KV_DEVICE float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -585,7 +579,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     }
                 }
             } else {
-                // A thread per row tile; the product of the first half of a tile's weights begins
+                // A warp per row tile; the product of the first half of a tile's weights begins
                 // while the other half is weighed.  Row tiles issue a key tile's products (and the
                 // next scores) in turn: products of both side by side would end together, and then
                 // neither's softmax would run beside the other's products (four long contexts: 156
@@ -784,7 +778,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     if (m_used == -INFINITY) {
                         m_used = mrow - kLift<F16>;
                     } else if (mrow > m_used + (kLift<F16> + kRenew<F16>)) {
-                        alpha = tc_ex2(m_used - (mrow - kLift<F16>));
+                        alpha = ex2(m_used - (mrow - kLift<F16>));
                         m_used = mrow - kLift<F16>;
                         l_sum *= alpha;
                         rescale = true;
@@ -818,7 +812,7 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                         for (int k = 0; k < 16; ++k) {
                             const float2 xx = __ffma2_rn(
                                 make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sc2, nm2);
-                            const float2 e = make_float2(tc_ex2(xx.x), tc_ex2(xx.y));
+                            const float2 e = make_float2(ex2(xx.x), ex2(xx.y));
                             acc[k & 1] = __fadd2_rn(acc[k & 1], e);
                             const float2 rest = split<F16>(e, w[k]);
                             if constexpr (THREE)
@@ -889,9 +883,9 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                 float l = 0.f;
                 for (int c = 0; c < p.copies; ++c) {
                     const float2 ml = sm.ml[row + c * per_copy];
-                    l += tc_ex2(ml.x - ref) * ml.y;
+                    l += ex2(ml.x - ref) * ml.y;
                 }
-                factor = tc_ex2(m_used - ref);
+                factor = ex2(m_used - ref);
                 m_used = M;
                 l_sum = l;
             }

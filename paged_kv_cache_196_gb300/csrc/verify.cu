@@ -37,13 +37,12 @@
 // the totals is exchanged.
 //
 // What bounds it: chains read their last node's rows once, 64 of them over 128000 tokens (fp32, p and q)
-// 65 MB and 9.8 us at the copy rate in 21.4 us: the start, the walk and the draw are
+// 65 MB and 9.8 us at the copy rate in 22 us: the start, the walk and the draw are
 // latencies, and the batch is little more than one wave.  Trees read a row again for every
 // rejection, one pass behind the other: 16 trees of 64 nodes 43.1 us (41.0 with products
 // cut off).  With up to 15 of them, an SM to
-// each CTA, a rejection costs 5 us at first and 8 to 9 from the second on; 16 share SMs, 13.  (W_k from W_1
-// in k - 1 steps of 64 bits: 16 rejections 1050 us where one product takes 206.  The product in pairs of
-// fp32 numbers, 180, but the 16 trees 41.0.)  The walk, 1 us, is one warp's: with all warps
+// each CTA, a rejection costs 5 us at first and 8 to 9 from the second on; 16 share SMs, 14: 16 rejections at each of
+// 16 roots 218 us.  (W_k from W_1 in k - 1 steps of 64 bits took 1050 us for them.)  The walk, 1 us, is one warp's: with all warps
 // in it the fp64 unit takes several times as long.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -535,8 +534,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
 // The rows of path[i] move to place i + 1 behind the root.  path rises, so path[i] >= i + 1,
 // and a place that is written is no later row's source: a thread that takes its 16 bytes of
 // every row in order needs no second buffer.  A CTA works on one sequence of one pool; the
-// pools of all layers go in one launch.  64 sequences of 24 layers, 6 rows of 2 x 8 heads x 128 bf16 values
-// each (38 MB moved): 6.5 us; 5.1 at the copy rate.  Two small pools 2.9 us, a launch.
+// pools of all layers go in one launch.  64 sequences of 24 layers, 0 to 6 accepted nodes each, 129 of whose rows of
+// 2 x 8 heads x 128 bf16 values move in every layer (25 MB read and written): 6.5 us; 3.8 at the copy
+// rate.  Two small pools 2.9 us, a launch.
 constexpr int kKeepThreads = 256, kKeepPools = 128, kKeepAhead = 8;
 
 struct KeepParams {
@@ -618,9 +618,11 @@ namespace {
 
 // CTAs of a sequence's cluster: as many as leave a chunk for each of its warps while the batch
 // stays within a third more than one wave of two CTAs per SM.  Trees, which pass over rows again
-// and again, gain by large clusters, chains by one wave: 16 trees over 128000 tokens 70.5 us in
-// clusters of 8, 118 of 4 (both with an earlier form of the passes, as are the next); 100 trees over
-// 50000 90 us of 4, 137 of 2; 64 chains over 128000 22.1 us of 4, 26.8 of 8; 200 chains over 32000 21.4 us alone, 24.9 in clusters of 2, 30.6 of 4.
+// and again, gain by large clusters, chains by one wave.  In us with clusters of 1, 2, 4 and 8 (* the rule's):
+//   16 trees over 128000 tokens   209, 115, 67.6, 43.2*    64 chains over 128000   38.0, 24.5, 22.2*, 27.6
+//   100 trees over 50000          110, 82.0, 61.0*, 60.9   100 chains over 50000   21.4, 19.9, 23.8*, 29.8
+//   200 trees over 32000          109, 63.8*, 68.7, 91.8   200 chains over 32000   21.9, 26.3*, 31.3, 49.9
+//   150 trees over 32000          82.0, 54.8*, 55.7, 66.7  150 chains over 32000   16.2, 15.9*, 24.3, 38.2
 int cluster_size(int vocab, int batch) {
     const int chunks = (vocab + kChunk - 1) / kChunk;
     int n = 1;
