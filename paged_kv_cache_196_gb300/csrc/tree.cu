@@ -140,19 +140,19 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_simple_kernel(const TreeP
                 float mx = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[i][j] = bits >> (tx + 8 * j) & 1 ? s[i][j] * p.scale_log2 : -INFINITY;
+                    s[i][j] = bits >> (tx + 8 * j) & 1 ? s[i][j] : -INFINITY;
                     mx = fmaxf(mx, s[i][j]);
                 }
 #pragma unroll
                 for (int off = 4; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float up = fmaxf(m[i], mx);
+                const float up = fmaxf(m[i], mx * p.scale_log2);  // scale > 0
                 const float ref = up == -INFINITY ? 0.f : up;
                 const float alpha = ex2(m[i] - ref);
                 m[i] = up;
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float e = ex2(s[i][j] - ref);
+                    const float e = ex2(fmaf(s[i][j], p.scale_log2, -ref));  // one rounding, of the distance
                     sum += e;
                     sm.p[row][tx + 8 * j] = e;
                 }

@@ -144,3 +144,41 @@ def test_differences_of_weights(dtype, d, nodes, cached, width):
         assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
     finally:
         case.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("first,last,step,gap", [(2840, 4096, 2, 4), (2840, 4096, 2, 6), (8192, 16384, 8, 4), (8192, 16384, 8, 8),
+                                                 (16384, 32768, 16, 8), (16384, 32768, 16, 16)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("nodes", [4, 30, 60])
+def test_scores_beyond_the_steps_of_their_maximum(dtype, first, last, step, gap, sign, nodes):
+    """Scores of 2^24 and more (log2 units): fp32 holds their maximum, and what is added to it or taken
+    from it, in steps of 1 to 16 units.  All keys of a row have one score, of exact products in fp32, but one of the
+    second tile's, `gap` above: out = 128 w / (1 + (n - 1) w), w = exp(-gap), for the 128 keys with a value of one.
+
+    A row's keys share their reference, however it is rounded; their distances to it are exact but for one
+    rounding, 2^-20 of the weight; the exponential, the parts (and 2^-34 of the largest weight in fp16), the sums of up
+    to n = 400 keys and the joining of pieces: 2^-22, 2^-16 of bf16, n 2^-23, 2^-20.  gap times the scale is off by
+    2^-23 of itself."""
+    cached, g = 300, 4
+    case = TreeCase(dtype, 64, 1, g, [cached], [nodes], kind="star", seed=1, width=33)
+    try:
+        k, v = torch.zeros_like(case.k[0]), torch.zeros_like(case.v[0])
+        k[:, :, 0], k[200, :, 1] = 32768.0 * sign, gap
+        v[:128] = 1.0
+        q0 = np.random.default_rng(nodes).choice(np.arange(first, last, step), (nodes, g))
+        q = torch.zeros_like(case.q)
+        q[:, :, 0], q[:, :, 1] = torch.from_numpy(q0 // 8 * 8 if dtype != "bf16" else 1 << np.log2(q0).astype(int)), 8.0
+        case.k[0], case.v[0], case.q = k, v, q
+        case.write(0)
+        a = case.args("f32")
+        case.call(a)
+        torch.cuda.synchronize()
+        got, w = a["out"].double().cpu().numpy()[:nodes], math.exp(-gap)
+        for i in range(nodes):
+            n = cached + (1 if i == 0 else 2)
+            want = 128 * w / (1 + (n - 1) * w)
+            tol = 2.0 ** -20 + 2.0 ** -22 + 2.0 ** -16 + n * 2.0 ** -23 + 2.0 ** -20 + gap * 2.0 ** -23 + 2.0 ** -34 / w
+            assert (np.abs(got[i] - want) <= tol * want).all(), (i, q[i, :, 0], got[i][:, 0], want)
+    finally:
+        case.close()
