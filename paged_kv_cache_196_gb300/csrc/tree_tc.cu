@@ -775,11 +775,14 @@ __global__ void __launch_bounds__(Layout<D, MT>::kThreads, 1)
                     float mrow = chunks == 1 ? tmem_max<32>(scol + 32 * c0) : tmem_max<64>(scol + 32 * c0);
                     if (chunks == 4) mrow = fmaxf(mrow, tmem_max<64>(scol + 64));
                     mrow *= p.scale_log2;  // scale > 0
+                    // (a reference rounded up and a difference, which is exact: scores past 2^24 have steps of whole
+                    // units, and a weight that another rounding let pass 2^16 would be an fp16 infinity)
+                    const float lifted = __fadd_ru(mrow, -kLift<F16>);
                     if (m_used == -INFINITY) {
-                        m_used = mrow - kLift<F16>;
-                    } else if (mrow > m_used + (kLift<F16> + kRenew<F16>)) {
-                        alpha = ex2(m_used - (mrow - kLift<F16>));
-                        m_used = mrow - kLift<F16>;
+                        m_used = lifted;
+                    } else if (mrow - m_used > kLift<F16> + kRenew<F16>) {
+                        alpha = ex2(m_used - lifted);
+                        m_used = lifted;
                         l_sum *= alpha;
                         rescale = true;
                     }

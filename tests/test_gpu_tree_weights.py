@@ -146,7 +146,7 @@ def test_differences_of_weights(dtype, d, nodes, cached, width):
         case.close()
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("first,last,step,gap", [(2840, 4096, 2, 4), (2840, 4096, 2, 6), (8192, 16384, 8, 4), (8192, 16384, 8, 8),
                                                  (16384, 32768, 16, 8), (16384, 32768, 16, 16)])
 @pytest.mark.parametrize("sign", [1, -1])
