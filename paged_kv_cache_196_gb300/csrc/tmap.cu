@@ -81,7 +81,11 @@ bool encode_q_map(CUtensorMap *m, const void *q, int rows, int hq, int box_heads
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A pool's maps are made by its first call that needs them, which may be two threads' at once.
+static std::mutex making;
+
 kv_status pool_tensor_maps(kv_pool *p) {
+    std::lock_guard<std::mutex> lock(making);
     if (p->tmaps_ready) return KV_OK;
     if (p->dtype == KV_F32 || p->dtype == KV_I4 || p->head_dim != 128) return KV_ERR_UNSUPPORTED;
     const long long rows = (long long)p->num_blocks * p->num_kv_heads * 16;
@@ -93,7 +97,6 @@ kv_status pool_tensor_maps(kv_pool *p) {
 }
 
 kv_status pool_group_maps(kv_pool *p) {
-    static std::mutex making;  // two threads' first calls
     std::lock_guard<std::mutex> lock(making);
     if (p->gmaps_ready) return KV_OK;
     if (p->dtype == KV_F32 || p->dtype == KV_I4) return KV_ERR_UNSUPPORTED;

@@ -1,5 +1,6 @@
 """Tensor maps are made under the calling thread's context, and leave it as it is."""
 import ctypes
+import threading
 from concurrent.futures import ThreadPoolExecutor
 
 import pytest
@@ -7,6 +8,7 @@ import torch
 
 import paged_kv_cache_196_gb300 as pk
 from _gpu import require_cuda
+from _tree import TreeCase
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +54,32 @@ def test_a_thread_without_a_context_gets_one():
             pool.submit(pk.kv_contig_reserve, c, 0).result()
     finally:
         pk.kv_contig_destroy(c)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_first_prefills_of_two_host_threads(seed):
+    """They make what the pool keeps for its calls (its tensor maps) together."""
+    case = TreeCase("bf16", 128, 2, 4, [700, 20], [9, 3], kind="chain", seed=seed)
+    try:
+        a = [case.args("f32") for _ in range(2)]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        start = threading.Barrier(2)
+
+        def one(i):
+            start.wait(timeout=30)
+            x = a[i]
+            pk.paged_prefill_attention(case.pool, x["q"], x["cu"], x["total"], 9, x["tables"], case.width, x["lens"], 2,
+                                       case.hq, case.scale, x["out"], pk.KV_F32, x["lse"], stream=streams[i])
+        with ThreadPoolExecutor(2) as pool:
+            list(pool.map(one, range(2)))
+        torch.cuda.synchronize()
+        assert pk.kv_get_device_error(case.pool) == 0
+        out, lse, _, _ = case.reference()
+        for x in a:
+            got = x["out"].double().cpu().numpy()[:case.total]
+            # (the prefill weighs in bf16 once: 2^-8 of the largest value)
+            assert (abs(got - out) <= 2.0 ** -7 * abs(case.v[0].double()).max().item()).all()
+        assert torch.equal(a[0]["out"], a[1]["out"])
+    finally:
+        case.close()
